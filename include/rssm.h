@@ -76,13 +76,20 @@ enum rssm_status {
     RSSM_ERR_CUDA = 4         /* the CUDA runtime reported an error at launch */
 };
 
-enum rssm_dtype { RSSM_F32 = 0, RSSM_BF16 = 1 };
+enum rssm_dtype {
+    RSSM_F32 = 0,
+    RSSM_BF16 = 1,
+    RSSM_E4M3 = 2 /* 8-bit float, 4 exponent and 3 significand bits, largest value 448: the
+                     paged cache and the norm's output only, always beside float32 scales */
+};
 
 /* Bits ORed into *dev_err by kernels. */
 enum rssm_dev_error {
     RSSM_DEVERR_SLOT = 1,    /* a row's cache index was >= num_slots; the row was skipped */
     RSSM_DEVERR_CURSOR = 2,  /* a row's write_pos / count was outside the ring; row skipped */
-    RSSM_DEVERR_TIMEOUT = 4  /* a bounded wait on an asynchronous copy expired; kernel stopped */
+    RSSM_DEVERR_TIMEOUT = 4, /* a bounded wait on an asynchronous copy expired; kernel stopped */
+    RSSM_DEVERR_PAGE = 8     /* a page-table entry in use was outside [0, num_pages); its tokens
+                                were skipped */
 };
 
 /* Cursor modes of rssm_advance_cursors. */
@@ -671,6 +678,138 @@ int rssm_gdn_spec_full_state_commit(const rssm_gdn_dims* dims, int32_t T, float*
                                     const float* snapshots, const int32_t* cache_indices,
                                     const int32_t* num_accepted, int32_t* dev_err,
                                     rssm_stream_t stream);
+
+/* ------------------------------------------------------------------------- */
+/* Attention layers of a hybrid model: paged cache, decode, residual norm     */
+/* ------------------------------------------------------------------------- */
+
+/* The models the recurrent kernels serve are hybrids ([M2] 实现拆解: Nemotron-H;
+ * [GDN] 实现拆解 item 2: the hybrid linear-attention backend): attention layers stand
+ * between the recurrent ones and share their slots. These entry points are an
+ * attention layer's part of the same decode step: new keys and values go into a paged
+ * cache (rssm_attn_append), the step's queries attend over it (rssm_attn_decode), and
+ * the slots' lengths advance (rssm_attn_advance). The pages have no counterpart. */
+
+typedef struct rssm_attn_dims {
+    int32_t batch;        /* rows in this call (>= 0) */
+    int32_t q_tokens;     /* T >= 1: query tokens per row (1: decode; more: drafts of a verify) */
+    int32_t num_q_heads;  /* HQ */
+    int32_t num_kv_heads; /* HKV: HQ % HKV == 0; query head h reads key / value head h / (HQ/HKV) */
+    int32_t head_dim;     /* D: 64 or 128 */
+    int32_t page_size;    /* tokens per page: 16, 32, 64, 128 or 256 */
+    int32_t num_pages;    /* pages in the cache */
+    int32_t max_pages;    /* columns of the page table; max_pages * page_size <= 2^30 */
+    int32_t num_slots;
+    int32_t act_dtype;    /* RSSM_F32 | RSSM_BF16: q, k, v */
+    int32_t cache_dtype;  /* RSSM_BF16 | RSSM_E4M3: the cache */
+    int32_t out_dtype;    /* RSSM_F32 | RSSM_BF16: o, and what rssm_attn_read returns */
+} rssm_attn_dims;
+
+/* A layer's cache: HOST struct of device pointers, read during the call only.
+ *   k, v        [num_pages][HKV][page_size][D]  cache_dtype
+ *   k_scale, v_scale [num_pages][HKV][page_size] float32 with an E4M3 cache (a cached
+ *               vector is its 8-bit values times its scale); unused (may be NULL) with bf16
+ *   page_table  [num_slots][max_pages] int32: position p of slot s is token p % page_size
+ *               of page page_table[s][p / page_size]; columns past a slot's tokens are not read
+ *   slot_len    [num_slots] int32: committed tokens of each slot
+ * Slots may share pages (a common prefix); rssm_attn_append must not be given a page
+ * that another slot still reads. Offsets into the cache are 64-bit; num_pages * HKV *
+ * page_size < 2^31. */
+typedef struct rssm_attn_cache {
+    void* k;
+    void* v;
+    float* k_scale;
+    float* v_scale;
+    const int32_t* page_table;
+    int32_t* slot_len;
+} rssm_attn_cache;
+
+/* rssm_attn_append -- write new tokens' keys and values at positions slot_len[s],
+ * slot_len[s] + 1, ... of their rows' slots. The lengths do not move
+ * (rssm_attn_advance), so rejected drafts are simply overwritten by the next append.
+ *   cu_tokens NULL: every row has T tokens, n_tokens = batch * T, token i is row i / T.
+ *   cu_tokens [batch + 1] int32: row b has tokens cu_tokens[b] .. cu_tokens[b+1]-1 (a
+ *     non-decreasing list that starts at 0 and ends at n_tokens; prompts of different lengths).
+ *   k, v: token i's [HKV][D] block starts at element i * k_stride (v_stride); strides in
+ *     elements, >= HKV * D and multiples of 8 (slices of a fused projection need no copy).
+ * bf16 cache: values rounded to nearest even. E4M3 cache: per (token, head) with a =
+ * max(max_d |x_d|, 2^-100): scale = a / 448, stored x_d * (448 / a) rounded to nearest
+ * even; a vector that holds an infinity or a NaN gets scale NaN and reads back as NaN
+ * throughout. A token whose position is beyond max_pages * page_size sets
+ * RSSM_DEVERR_CURSOR, one whose page is outside [0, num_pages) RSSM_DEVERR_PAGE; such a
+ * token is not written. */
+int rssm_attn_append(const rssm_attn_dims* dims, const rssm_attn_cache* cache, int32_t n_tokens,
+                     const int32_t* cu_tokens, const void* k, int64_t k_stride, const void* v,
+                     int64_t v_stride, const int32_t* cache_indices, int32_t* dev_err,
+                     rssm_stream_t stream);
+
+/* rssm_attn_read -- read committed tokens back, dense: row b's positions first[b],
+ * first[b] + 1, ... (first NULL: from 0), cu_tokens[b+1] - cu_tokens[b] of them
+ * (cu_tokens as in rssm_attn_append; NULL: T per row), into k_out, v_out [n_tokens][HKV][D]
+ * out_dtype (the stored value times its scale, rounded to nearest even). A position
+ * outside [0, slot_len[s]) sets RSSM_DEVERR_CURSOR, a page outside [0, num_pages)
+ * RSSM_DEVERR_PAGE; the token's outputs are left untouched. */
+int rssm_attn_read(const rssm_attn_dims* dims, const rssm_attn_cache* cache, int32_t n_tokens,
+                   const int32_t* cu_tokens, const int32_t* first, const int32_t* cache_indices,
+                   void* k_out, void* v_out, int32_t* dev_err, rssm_stream_t stream);
+
+/* Bytes of device workspace rssm_attn_decode needs (partial results of rows whose
+ * tokens several CTAs share, and their arrival counters). It must be zero-filled before
+ * its first use; every call leaves its counters at zero. One stream at a time.
+ * 0 for an invalid dims. */
+size_t rssm_attn_workspace_size(const rssm_attn_dims* dims);
+
+/* rssm_attn_decode -- attention of T query tokens per row over the row's cached tokens.
+ * For query token j, head h, n_j = slot_len[s] + (appended ? j + 1 : 0):
+ *   s_p = scale * (q . k_p),  p in [max(0, n_j - window), n_j)   (window 0: from 0)
+ *   o = sum_p exp(s_p - m) v_p / sum_p exp(s_p - m),  m = max_p s_p,  lse = m + log sum_p ...
+ * appended != 0: the queries' own tokens are in the cache (rssm_attn_append ran, the
+ * lengths have not advanced), and draft j sees drafts 0..j. appended == 0: every query
+ * sees the committed tokens. Tokens that a query does not see contribute nothing, whatever
+ * the cache holds there (NaN included). A query that sees no token, or only scores of
+ * -infinity, gets o = 0 and lse = -infinity.
+ *   q: token i = b T + j's [HQ][D] block at element i * q_stride (>= HQ * D, a multiple of 8)
+ *   o [batch][T][HQ][D] out_dtype; lse [batch][T][HQ] float32 (nullable)
+ * Limits: T * (HQ / HKV) <= 64. Scores, softmax sums and outputs accumulate in float32.
+ * A slot_len outside [0, max_pages * page_size - (appended ? T : 0)] skips the row and
+ * sets RSSM_DEVERR_CURSOR; a page outside [0, num_pages) hides its tokens and sets
+ * RSSM_DEVERR_PAGE. Rows may share a slot (the cache is only read). The work is divided
+ * on the device from the slots' lengths, so a captured call serves any lengths; the order
+ * of every sum is fixed by them, and repeated calls give identical bits. */
+int rssm_attn_decode(const rssm_attn_dims* dims, const rssm_attn_cache* cache, int appended,
+                     float scale, int32_t window, const void* q, int64_t q_stride,
+                     const int32_t* cache_indices, void* workspace, size_t workspace_bytes,
+                     void* o, float* lse, int32_t* dev_err, rssm_stream_t stream);
+
+/* rssm_attn_advance -- commit appended tokens: slot_len[s] += num_accepted[b] when given
+ * (0 <= num_accepted[b] <= the row's appended tokens), else all of the row's tokens
+ * (cu_tokens as in rssm_attn_append). A count or a new length out of range sets
+ * RSSM_DEVERR_CURSOR and leaves the slot. Lengths go back to 0 through
+ * RSSM_CURSOR_RESET of rssm_advance_cursors, with slot_len as its slot_wp. */
+int rssm_attn_advance(const rssm_attn_dims* dims, const rssm_attn_cache* cache,
+                      const int32_t* cu_tokens, const int32_t* num_accepted,
+                      const int32_t* cache_indices, int32_t* dev_err, rssm_stream_t stream);
+
+typedef struct rssm_norm_dims {
+    int32_t rows;        /* >= 0 */
+    int32_t cols;        /* 1 .. 32768 */
+    int32_t scale_group; /* E4M3 output: columns per scale, 0 (one scale per row) or 128 */
+    int32_t act_dtype;   /* RSSM_F32 | RSSM_BF16: x, residual, residual_out */
+    int32_t out_dtype;   /* RSSM_F32 | RSSM_BF16 | RSSM_E4M3: y */
+} rssm_norm_dims;
+
+/* rssm_add_rmsnorm -- r = x + residual; residual_out = r; y = r / sqrt(mean(r^2) + eps) * weight.
+ * x, residual, residual_out [rows][cols] act_dtype; weight [cols] float32; y [rows][cols].
+ * residual NULL: r = x. residual_out NULL: r is not stored; residual_out may be residual or
+ * x (in place). The norm uses the float32 sum r, not its stored rounding. E4M3 output:
+ * y_scale [rows][scale_group ? cols / scale_group : 1] float32, the scale rule of
+ * rssm_attn_append over each group (a group with an infinity or a NaN gets scale NaN); the
+ * represented value is y * y_scale. Unused (may be NULL) for the other types.
+ * Errors: RSSM_ERR_UNSUPPORTED for cols > 32768 or a scale_group other than 0 and 128,
+ * RSSM_ERR_CONFIG for cols % scale_group != 0. */
+int rssm_add_rmsnorm(const rssm_norm_dims* dims, const void* x, const void* residual,
+                     const float* weight, float eps, void* residual_out, void* y, float* y_scale,
+                     rssm_stream_t stream);
 
 /* ------------------------------------------------------------------------- */
 

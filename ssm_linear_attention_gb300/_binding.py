@@ -11,8 +11,8 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "librssm.so")
 
 RSSM_OK, RSSM_ERR_INVALID_ARG, RSSM_ERR_UNSUPPORTED, RSSM_ERR_CONFIG, RSSM_ERR_CUDA = range(5)
-RSSM_F32, RSSM_BF16 = 0, 1
-RSSM_DEVERR_SLOT, RSSM_DEVERR_CURSOR, RSSM_DEVERR_TIMEOUT = 1, 2, 4
+RSSM_F32, RSSM_BF16, RSSM_E4M3 = 0, 1, 2
+RSSM_DEVERR_SLOT, RSSM_DEVERR_CURSOR, RSSM_DEVERR_TIMEOUT, RSSM_DEVERR_PAGE = 1, 2, 4, 8
 RSSM_CURSOR_STANDARD, RSSM_CURSOR_SPEC_COMMIT, RSSM_CURSOR_RESET = 0, 1, 2
 RSSM_NOALLOC_WORKSPACE_BYTES = 16 << 20
 RSSM_MAX_SLOT_BUFFERS = 12
@@ -34,6 +34,8 @@ EXPORTS = (
     "rssm_gdn_spec_full_state_snapshot_bytes", "rssm_gdn_spec_full_state_verify",
     "rssm_gdn_spec_full_state_commit", "rssm_kda_workspace_size", "rssm_kda_prepare",
     "rssm_kda_output", "rssm_kda_step", "rssm_kda_full_state_decode",
+    "rssm_attn_append", "rssm_attn_read", "rssm_attn_workspace_size", "rssm_attn_decode",
+    "rssm_attn_advance", "rssm_add_rmsnorm",
     "rssm_debug_pipeline_copy", "rssm_debug_umma_fold",
 )
 
@@ -61,6 +63,23 @@ class GDNDims(ctypes.Structure):
         "num_slots", "act_dtype", "out_dtype")]
 
 
+class AttnDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "batch", "q_tokens", "num_q_heads", "num_kv_heads", "head_dim", "page_size", "num_pages",
+        "max_pages", "num_slots", "act_dtype", "cache_dtype", "out_dtype")]
+
+
+class AttnCache(ctypes.Structure):
+    """A layer's paged cache as device addresses (attn_cache() fills it from tensors)."""
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "k", "v", "k_scale", "v_scale", "page_table", "slot_len")]
+
+
+class NormDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "rows", "cols", "scale_group", "act_dtype", "out_dtype")]
+
+
 _lib = None
 _VP = ctypes.c_void_p
 _I = ctypes.c_int
@@ -71,6 +90,10 @@ _SZ = ctypes.c_size_t
 def _declare(L):
     m2 = ctypes.POINTER(Mamba2Dims)
     gd = ctypes.POINTER(GDNDims)
+    ad = ctypes.POINTER(AttnDims)
+    ac = ctypes.POINTER(AttnCache)
+    i64 = ctypes.c_int64
+    f32 = ctypes.c_float
     sig = {
         "rssm_status_string": (ctypes.c_char_p, [_I]),
         "rssm_abi_version": (_I, []),
@@ -137,6 +160,14 @@ def _declare(L):
                                             _VP]),
         "rssm_gdn_spec_verify": (_I, [gd, _I32, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP,
                                       _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP, _VP, _VP]),
+        "rssm_attn_append": (_I, [ad, ac, _I32, _VP, _VP, i64, _VP, i64, _VP, _VP, _VP]),
+        "rssm_attn_read": (_I, [ad, ac, _I32, _VP, _VP, _VP, _VP, _VP, _VP, _VP]),
+        "rssm_attn_workspace_size": (_SZ, [ad]),
+        "rssm_attn_decode": (_I, [ad, ac, _I, f32, _I32, _VP, i64, _VP, _VP, _SZ, _VP, _VP, _VP,
+                                  _VP]),
+        "rssm_attn_advance": (_I, [ad, ac, _VP, _VP, _VP, _VP, _VP]),
+        "rssm_add_rmsnorm": (_I, [ctypes.POINTER(NormDims), _VP, _VP, _VP, f32, _VP, _VP, _VP,
+                                  _VP]),
         "rssm_debug_pipeline_copy": (_I, [_VP, _VP, _I, _I, _I, _VP, _VP]),
         "rssm_debug_umma_fold": (_I, [_VP, _VP, _I, _I, _VP, _VP, _VP]),
     }
@@ -483,3 +514,45 @@ def rssm_mamba2_spec_verify(dims, T, state, x, dt_raw, dt_bias, dt_softplus, A, 
           _ptr(z), _ptr(ring_x), _ptr(ring_dt), _ptr(ring_B), _ptr(cache_indices), _ptr(slot_cnt),
           _ptr(slot_base), _ptr(slot_flush), _ptr(workspace), workspace_bytes, _ptr(y),
           _ptr(dev_err), _stream(stream))
+
+
+def attn_cache(k, v, k_scale, v_scale, page_table, slot_len):
+    """The rssm_attn_cache of these tensors (they must stay alive while it is used)."""
+    return AttnCache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(page_table),
+                     _ptr(slot_len))
+
+
+def rssm_attn_append(dims, cache, n_tokens, cu_tokens, k, k_stride, v, v_stride, cache_indices,
+                     dev_err=None, stream=None):
+    _call("rssm_attn_append", ctypes.byref(dims), ctypes.byref(cache), n_tokens, _ptr(cu_tokens),
+          _ptr(k), k_stride, _ptr(v), v_stride, _ptr(cache_indices), _ptr(dev_err),
+          _stream(stream))
+
+
+def rssm_attn_read(dims, cache, n_tokens, cu_tokens, first, cache_indices, k_out, v_out,
+                   dev_err=None, stream=None):
+    _call("rssm_attn_read", ctypes.byref(dims), ctypes.byref(cache), n_tokens, _ptr(cu_tokens),
+          _ptr(first), _ptr(cache_indices), _ptr(k_out), _ptr(v_out), _ptr(dev_err),
+          _stream(stream))
+
+
+def rssm_attn_workspace_size(dims):
+    return lib().rssm_attn_workspace_size(ctypes.byref(dims))
+
+
+def rssm_attn_decode(dims, cache, appended, scale, window, q, q_stride, cache_indices, workspace,
+                     workspace_bytes, o, lse=None, dev_err=None, stream=None):
+    _call("rssm_attn_decode", ctypes.byref(dims), ctypes.byref(cache), int(appended), scale,
+          window, _ptr(q), q_stride, _ptr(cache_indices), _ptr(workspace), workspace_bytes,
+          _ptr(o), _ptr(lse), _ptr(dev_err), _stream(stream))
+
+
+def rssm_attn_advance(dims, cache, cu_tokens, num_accepted, cache_indices, dev_err=None,
+                      stream=None):
+    _call("rssm_attn_advance", ctypes.byref(dims), ctypes.byref(cache), _ptr(cu_tokens),
+          _ptr(num_accepted), _ptr(cache_indices), _ptr(dev_err), _stream(stream))
+
+
+def rssm_add_rmsnorm(dims, x, residual, weight, eps, residual_out, y, y_scale=None, stream=None):
+    _call("rssm_add_rmsnorm", ctypes.byref(dims), _ptr(x), _ptr(residual), _ptr(weight), eps,
+          _ptr(residual_out), _ptr(y), _ptr(y_scale), _stream(stream))

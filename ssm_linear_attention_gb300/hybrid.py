@@ -1,0 +1,200 @@
+"""Runners for what stands between the recurrent layers of a hybrid model: attention over
+a paged key-value cache, and the residual add with its RMS norm.
+
+As the runners in decoder.py, each owns the device buffers of one layer (or uses tensors
+that the caller hands in), a step is a sequence of librssm calls in stream order, and no
+call synchronises, so a step can be captured in a CUDA graph:
+
+  attention:  rssm_attn_append -> rssm_attn_decode -> rssm_attn_advance
+              (T > 1 drafts: append and decode, then advance by the accepted counts)
+  norm:       rssm_add_rmsnorm
+"""
+import torch
+
+from . import _binding as B
+from .decoder import torch_dtype_code
+
+__all__ = ["PagedAttentionDecoder", "AddRMSNorm"]
+
+
+def _code(dt):
+    return B.RSSM_E4M3 if dt == torch.float8_e4m3fn else torch_dtype_code(dt)
+
+
+def _check(name, t, shape, dtype, device):
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or \
+            not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor %s on %s" % (name, dtype, tuple(shape),
+                                                                         device))
+    return t
+
+
+class PagedAttentionDecoder:
+    """Attention decode for one layer over a paged cache.
+
+    Buffers: k_cache, v_cache [num_pages, HKV, page_size, D] (cache_dtype: bfloat16 or
+    float8_e4m3fn), k_scale, v_scale [num_pages, HKV, page_size] float32 (8-bit cache
+    only), page_table [num_slots, max_pages] int32 (-1: no page yet; the caller assigns
+    pages), slot_len [num_slots] int32, and workspace / o / lse for up to max_batch rows of
+    T query tokens. Any of the caches, the scales, page_table and slot_len can be the
+    caller's tensors (page_table and slot_len are commonly shared by a model's layers)."""
+
+    def __init__(self, num_q_heads, num_kv_heads, head_dim, page_size, num_pages, num_slots,
+                 max_pages, max_batch, T=1, act_dtype=torch.bfloat16, cache_dtype=torch.bfloat16,
+                 out_dtype=torch.bfloat16, window=0, scale=None, device=None, k_cache=None,
+                 v_cache=None, k_scale=None, v_scale=None, page_table=None, slot_len=None):
+        dev = torch.device("cuda", torch.cuda.current_device()) if device is None \
+            else torch.device(device)
+        self.HQ, self.HKV, self.D, self.T = num_q_heads, num_kv_heads, head_dim, T
+        self.page_size, self.num_pages, self.max_pages = page_size, num_pages, max_pages
+        self.num_slots, self.max_batch, self.window = num_slots, max_batch, window
+        self.scale = head_dim ** -0.5 if scale is None else scale
+        self.act_dtype, self.cache_dtype, self.out_dtype = act_dtype, cache_dtype, out_dtype
+        self.device = dev
+
+        def buf(name, given, shape, dtype, fill=0):
+            if given is None:
+                # 8-bit caches are filled through their bytes
+                raw = torch.uint8 if dtype == torch.float8_e4m3fn else dtype
+                return torch.full(shape, fill, device=dev, dtype=raw).view(dtype)
+            return _check(name, given, shape, dtype, dev)
+        pages = (num_pages, num_kv_heads, page_size)
+        self.k_cache = buf("k_cache", k_cache, pages + (head_dim,), cache_dtype)
+        self.v_cache = buf("v_cache", v_cache, pages + (head_dim,), cache_dtype)
+        if cache_dtype == torch.float8_e4m3fn:
+            self.k_scale = buf("k_scale", k_scale, pages, torch.float32)
+            self.v_scale = buf("v_scale", v_scale, pages, torch.float32)
+        else:
+            self.k_scale = self.v_scale = None
+        self.page_table = buf("page_table", page_table, (num_slots, max_pages), torch.int32, -1)
+        self.slot_len = buf("slot_len", slot_len, (num_slots,), torch.int32)
+        self.dev_err = torch.zeros(4, device=dev, dtype=torch.int32)
+        self.cache = B.attn_cache(self.k_cache, self.v_cache, self.k_scale, self.v_scale,
+                                  self.page_table, self.slot_len)
+        self._dims = {}
+        self.ws_bytes = B.rssm_attn_workspace_size(self.dims(max_batch))
+        # zero-filled: the decode call keeps its arrival counters here
+        self.workspace = torch.zeros(max(self.ws_bytes, 16), device=dev, dtype=torch.uint8)
+        self.o = torch.empty(max_batch, T, num_q_heads, head_dim, device=dev, dtype=out_dtype)
+        self.lse = torch.empty(max_batch, T, num_q_heads, device=dev, dtype=torch.float32)
+
+    def dims(self, batch):
+        d = self._dims.get(batch)
+        if d is None:
+            d = self._dims[batch] = B.AttnDims(
+                batch, self.T, self.HQ, self.HKV, self.D, self.page_size, self.num_pages,
+                self.max_pages, self.num_slots, torch_dtype_code(self.act_dtype),
+                _code(self.cache_dtype), torch_dtype_code(self.out_dtype))
+        return d
+
+    def _stride(self, name, t, heads):
+        """Element distance between consecutive tokens of t [tokens, heads, D] or
+        [rows, T, heads, D]."""
+        s, n = t.stride(), t.shape
+        if t.dtype != self.act_dtype or n[-2:] != (heads, self.D) or s[-1] != 1 or \
+                (s[-2] != self.D and heads > 1) or \
+                (len(n) == 4 and n[0] > 1 and n[1] > 1 and s[0] != n[1] * s[1]) or len(n) > 4:
+            raise ValueError("%s: tokens of dense [%d, %d] %s blocks, evenly spaced, are wanted"
+                             % (name, heads, self.D, self.act_dtype))
+        return s[0] if len(n) == 3 or n[1] == 1 else s[1]
+
+    def append(self, k, v, cache_indices, cu_tokens=None, stream=None):
+        """Write new tokens' k, v [n, HKV, D] (or [b, T, HKV, D]) after the rows' committed
+        tokens; cu_tokens [b + 1] int32 for rows of different token counts (else T each)."""
+        n = k.numel() // (self.HKV * self.D)
+        if v.shape != k.shape:
+            raise ValueError("k and v must have one shape")
+        B.rssm_attn_append(self.dims(cache_indices.shape[0]), self.cache, n, cu_tokens, k,
+                           self._stride("k", k, self.HKV), v, self._stride("v", v, self.HKV),
+                           cache_indices, self.dev_err, stream)
+
+    def decode(self, q, cache_indices, appended=True, o=None, lse=None, with_lse=False,
+               stream=None):
+        """Attention of q [b, T, HQ, D] over the rows' tokens. appended: the queries' own
+        tokens are in the cache and visible (see rssm_attn_decode). Returns o [b, T, HQ, D],
+        with with_lse also lse [b, T, HQ]."""
+        b = cache_indices.shape[0]
+        if b > self.max_batch or q.numel() != b * self.T * self.HQ * self.D:
+            raise ValueError("q must be [b, %d, %d, %d], b = len(cache_indices) <= %d"
+                             % (self.T, self.HQ, self.D, self.max_batch))
+        o = self.o[:b] if o is None else o
+        if lse is None and with_lse:
+            lse = self.lse[:b]
+        B.rssm_attn_decode(self.dims(b), self.cache, appended, self.scale, self.window, q,
+                           self._stride("q", q, self.HQ), cache_indices, self.workspace,
+                           self.ws_bytes, o, lse, self.dev_err, stream)
+        return (o, lse) if with_lse else o
+
+    def advance(self, cache_indices, num_accepted=None, cu_tokens=None, stream=None):
+        """Commit the appended tokens (of T drafts: the first num_accepted[b])."""
+        B.rssm_attn_advance(self.dims(cache_indices.shape[0]), self.cache, cu_tokens, num_accepted,
+                            cache_indices, self.dev_err, stream)
+
+    def step(self, q, k, v, cache_indices, o=None, stream=None):
+        """One decode step for rows cache_indices (padding rows: -1): append, decode,
+        advance. Returns o [b, T, HQ, D]."""
+        self.append(k, v, cache_indices, stream=stream)
+        o = self.decode(q, cache_indices, o=o, stream=stream)
+        self.advance(cache_indices, stream=stream)
+        return o
+
+    def read(self, cache_indices, cu_tokens, n_tokens, first=None, k=None, v=None, stream=None):
+        """Committed tokens back, dense: k, v [n_tokens, HKV, D] (out_dtype)."""
+        if k is None:
+            k = torch.empty(n_tokens, self.HKV, self.D, device=self.device, dtype=self.out_dtype)
+        if v is None:
+            v = torch.empty_like(k)
+        B.rssm_attn_read(self.dims(cache_indices.shape[0]), self.cache, n_tokens, cu_tokens, first,
+                         cache_indices, k, v, self.dev_err, stream)
+        return k, v
+
+    def reset_slots(self, slots, stream=None):
+        """Lengths back to 0 (the page table is the caller's)."""
+        B.rssm_advance_cursors(B.RSSM_CURSOR_RESET, self.slot_len, None, None, slots, None, None,
+                               slots.shape[0], self.num_slots, 1, 0, None, None, self.dev_err,
+                               stream)
+
+
+class AddRMSNorm:
+    """Residual add and RMS norm for one place in a model: r = x + residual, y = r /
+    sqrt(mean(r^2) + eps) * weight, for up to max_rows rows. With out_dtype float8_e4m3fn y
+    comes with float32 scales [rows, cols / scale_group] ([rows, 1] for scale_group 0)."""
+
+    def __init__(self, weight, eps, max_rows, act_dtype=torch.bfloat16, out_dtype=torch.bfloat16,
+                 scale_group=0, device=None):
+        dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+        self.weight = torch.as_tensor(weight, device=dev, dtype=torch.float32).contiguous()
+        self.cols, self.eps, self.max_rows = self.weight.shape[0], eps, max_rows
+        self.act_dtype, self.out_dtype, self.scale_group = act_dtype, out_dtype, scale_group
+        self.y = torch.empty(max_rows, self.cols, device=dev, dtype=out_dtype)
+        self.scale = None
+        if out_dtype == torch.float8_e4m3fn:
+            groups = self.cols // scale_group if scale_group else 1
+            self.scale = torch.empty(max_rows, groups, device=dev, dtype=torch.float32)
+        self._dims = {}
+
+    def dims(self, rows):
+        d = self._dims.get(rows)
+        if d is None:
+            d = self._dims[rows] = B.NormDims(rows, self.cols, self.scale_group,
+                                              torch_dtype_code(self.act_dtype),
+                                              _code(self.out_dtype))
+        return d
+
+    def __call__(self, x, residual=None, residual_out=None, y=None, scale=None, stream=None):
+        """Returns (y, scale) (scale None unless y is 8-bit). residual_out None: the sum
+        replaces residual (without a residual it is not stored)."""
+        rows = x.numel() // self.cols
+        if rows * self.cols != x.numel() or (y is None and rows > self.max_rows):
+            raise ValueError("x must be [rows, %d], rows <= %d" % (self.cols, self.max_rows))
+        for t in (x, residual, residual_out):
+            if t is not None and (t.dtype != self.act_dtype or t.numel() != x.numel() or
+                                  not t.is_contiguous()):
+                raise ValueError("x and the residuals: dense [rows, %d] %s" % (self.cols,
+                                                                               self.act_dtype))
+        y = self.y[:rows] if y is None else y
+        if scale is None and self.scale is not None:
+            scale = self.scale[:rows]
+        B.rssm_add_rmsnorm(self.dims(rows), x, residual, self.weight, self.eps,
+                           residual if residual_out is None else residual_out, y, scale, stream)
+        return y, scale

@@ -1,0 +1,126 @@
+"""The attention and norm entry points reject bad arguments on the host before any launch
+(no GPU needed)."""
+import ctypes
+
+import pytest
+
+import ssm_linear_attention_gb300 as ssm
+from ssm_linear_attention_gb300 import _binding as B
+from ssm_linear_attention_gb300 import build as rbuild
+
+INV, UNS, CFG = B.RSSM_ERR_INVALID_ARG, B.RSSM_ERR_UNSUPPORTED, B.RSSM_ERR_CONFIG
+FAKE = 0x10000  # aligned non-null address; never dereferenced (validation fails first)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    rbuild.build()
+    return ssm.lib()
+
+
+def _dims(**kw):
+    d = dict(batch=4, q_tokens=1, num_q_heads=8, num_kv_heads=2, head_dim=128, page_size=16,
+             num_pages=64, max_pages=8, num_slots=8, act_dtype=B.RSSM_BF16,
+             cache_dtype=B.RSSM_E4M3, out_dtype=B.RSSM_BF16)
+    d.update(kw)
+    return B.AttnDims(**d)
+
+
+def _cache(**kw):
+    c = dict(k=FAKE, v=FAKE, k_scale=FAKE, v_scale=FAKE, page_table=FAKE, slot_len=FAKE)
+    c.update(kw)
+    return B.AttnCache(**c)
+
+
+def _decode(d, c=None, window=0, q=FAKE, q_stride=1024, ci=FAKE, ws=FAKE, wsb=1 << 40, o=FAKE,
+            lse=None):
+    c = _cache() if c is None else c
+    return ssm.lib().rssm_attn_decode(ctypes.byref(d), ctypes.byref(c), 1, 1.0, window, q, q_stride,
+                                      ci, ws, wsb, o, lse, None, None)
+
+
+def _append(d, c=None, n=4, cu=None, k=FAKE, ks=256, v=FAKE, vs=256, ci=FAKE):
+    c = _cache() if c is None else c
+    return ssm.lib().rssm_attn_append(ctypes.byref(d), ctypes.byref(c), n, cu, k, ks, v, vs, ci,
+                                      None, None)
+
+
+def _read(d, c=None, n=4, cu=None, first=None, ci=FAKE, k=FAKE, v=FAKE):
+    c = _cache() if c is None else c
+    return ssm.lib().rssm_attn_read(ctypes.byref(d), ctypes.byref(c), n, cu, first, ci, k, v, None,
+                                    None)
+
+
+def _advance(d, c=None, cu=None, acc=None, ci=FAKE):
+    c = _cache() if c is None else c
+    return ssm.lib().rssm_attn_advance(ctypes.byref(d), ctypes.byref(c), cu, acc, ci, None, None)
+
+
+BAD_DIMS = [
+    (dict(batch=-1), INV), (dict(q_tokens=0), INV), (dict(num_q_heads=0), INV),
+    (dict(num_kv_heads=0), INV), (dict(num_pages=0), INV), (dict(max_pages=0), INV),
+    (dict(num_slots=0), INV), (dict(act_dtype=B.RSSM_E4M3), INV), (dict(act_dtype=9), INV),
+    (dict(cache_dtype=B.RSSM_F32), INV), (dict(out_dtype=B.RSSM_E4M3), INV),
+    (dict(num_q_heads=9), CFG), (dict(head_dim=96), UNS), (dict(page_size=8), UNS),
+    (dict(page_size=48), UNS), (dict(page_size=512), UNS),
+    (dict(max_pages=1 << 27), UNS),                    # positions past 2^30
+    (dict(num_pages=1 << 27), UNS),                    # cache rows past 2^31
+]
+
+
+@pytest.mark.parametrize("bad,code", BAD_DIMS)
+def test_dims(lib, bad, code):
+    d = _dims(**bad)
+    assert _decode(d) == code
+    assert _append(d) == code
+    assert _read(d) == code
+    assert _advance(d) == code
+    assert B.rssm_attn_workspace_size(d) == 0
+
+
+def test_decode_arguments(lib):
+    d = _dims()
+    assert B.rssm_attn_workspace_size(d) > 0
+    for kw in (dict(q=None), dict(q=FAKE + 2), dict(q_stride=1020), dict(q_stride=1016 - 8),
+               dict(ci=None), dict(ws=None), dict(ws=FAKE + 8), dict(o=None), dict(o=FAKE + 8),
+               dict(lse=FAKE + 4), dict(window=-1), dict(c=_cache(k=None)),
+               dict(c=_cache(v=FAKE + 8)), dict(c=_cache(k_scale=None)),
+               dict(c=_cache(page_table=None)), dict(c=_cache(slot_len=None)),
+               dict(wsb=B.rssm_attn_workspace_size(d) - 1)):
+        assert _decode(d, **kw) == INV, kw
+    # 65 queries to a key head
+    assert _decode(_dims(num_q_heads=26, q_tokens=5), q_stride=26 * 128) == UNS
+    assert _decode(_dims(batch=0), q=None) == B.RSSM_OK
+
+
+def test_append_read_and_advance_arguments(lib):
+    d = _dims()
+    for kw in (dict(n=-1), dict(n=5), dict(k=None), dict(v=FAKE + 8), dict(ks=248), dict(vs=260),
+               dict(ci=None), dict(cu=FAKE + 4), dict(c=_cache(v_scale=None)), dict(c=_cache(k=None))):
+        assert _append(d, **kw) == INV, kw
+    assert _append(d, n=0, cu=FAKE, k=None) == B.RSSM_OK
+    assert _append(_dims(batch=0), n=0, k=None) == B.RSSM_OK
+    assert _append(_dims(batch=0), n=3, cu=FAKE) == INV
+    for kw in (dict(n=-1), dict(n=5), dict(k=None), dict(v=FAKE + 8), dict(first=FAKE + 4),
+               dict(ci=None), dict(c=_cache(page_table=None))):
+        assert _read(d, **kw) == INV, kw
+    assert _read(d, n=0, cu=FAKE, k=None) == B.RSSM_OK
+    for kw in (dict(c=_cache(slot_len=None)), dict(ci=None), dict(acc=FAKE + 4), dict(cu=FAKE + 4)):
+        assert _advance(d, **kw) == INV, kw
+    assert _advance(_dims(batch=0), ci=None) == B.RSSM_OK
+
+
+def test_norm_arguments(lib):
+    def call(x=FAKE, res=None, w=FAKE, out=None, y=FAKE, scale=FAKE, **kw):
+        n = dict(rows=4, cols=256, scale_group=0, act_dtype=B.RSSM_BF16, out_dtype=B.RSSM_E4M3)
+        n.update(kw)
+        return ssm.lib().rssm_add_rmsnorm(ctypes.byref(B.NormDims(**n)), x, res, w, 1e-5, out, y,
+                                          scale, None)
+    for kw, code in ((dict(rows=-1), INV), (dict(cols=0), INV), (dict(cols=32769), UNS),
+                     (dict(scale_group=64), UNS), (dict(scale_group=128, cols=200), CFG),
+                     (dict(act_dtype=B.RSSM_E4M3), INV), (dict(out_dtype=3), INV),
+                     (dict(x=None), INV), (dict(x=FAKE + 8), INV), (dict(res=FAKE + 2), INV),
+                     (dict(w=None), INV), (dict(out=FAKE + 4), INV), (dict(y=FAKE + 1), INV),
+                     (dict(scale=None), INV), (dict(scale=FAKE + 4), INV)):
+        assert call(**kw) == code, kw
+    assert call(rows=0, x=None) == B.RSSM_OK
