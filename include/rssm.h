@@ -734,8 +734,8 @@ typedef struct rssm_attn_cache {
  *     elements, >= HKV * D and multiples of 8 (slices of a fused projection need no copy).
  * bf16 cache: values rounded to nearest even. E4M3 cache: per (token, head) with a =
  * max(max_d |x_d|, 2^-100): scale = a / 448, stored x_d * (448 / a) rounded to nearest
- * even; a vector that holds an infinity or a NaN gets scale NaN and reads back as NaN
- * throughout. A token whose position is beyond max_pages * page_size sets
+ * even; a vector that holds an infinity or a NaN is stored as zeros with scale NaN and
+ * reads back as NaN throughout (the 8-bit NaN codes are not used; scales are >= 0). A token whose position is beyond max_pages * page_size sets
  * RSSM_DEVERR_CURSOR, one whose page is outside [0, num_pages) RSSM_DEVERR_PAGE; such a
  * token is not written. */
 int rssm_attn_append(const rssm_attn_dims* dims, const rssm_attn_cache* cache, int32_t n_tokens,
@@ -755,8 +755,8 @@ int rssm_attn_read(const rssm_attn_dims* dims, const rssm_attn_cache* cache, int
 
 /* Bytes of device workspace rssm_attn_decode needs (partial results of rows whose
  * tokens several CTAs share, and their arrival counters). It must be zero-filled before
- * its first use; every call leaves its counters at zero. One stream at a time.
- * 0 for an invalid dims. */
+ * its first use, and again after a call that set RSSM_DEVERR_TIMEOUT; every other call
+ * leaves its counters at zero. One stream at a time. 0 for an invalid dims. */
 size_t rssm_attn_workspace_size(const rssm_attn_dims* dims);
 
 /* rssm_attn_decode -- attention of T query tokens per row over the row's cached tokens.
@@ -770,7 +770,7 @@ size_t rssm_attn_workspace_size(const rssm_attn_dims* dims);
  * -infinity, gets o = 0 and lse = -infinity.
  *   q: token i = b T + j's [HQ][D] block at element i * q_stride (>= HQ * D, a multiple of 8)
  *   o [batch][T][HQ][D] out_dtype; lse [batch][T][HQ] float32 (nullable)
- * Limits: T * (HQ / HKV) <= 64. Scores, softmax sums and outputs accumulate in float32.
+ * Limits: T * (HQ / HKV) <= 64, max_pages * (page_size / 16) * HKV < 2^31. Scores, softmax sums and outputs accumulate in float32.
  * A slot_len outside [0, max_pages * page_size - (appended ? T : 0)] skips the row and
  * sets RSSM_DEVERR_CURSOR; a page outside [0, num_pages) hides its tokens and sets
  * RSSM_DEVERR_PAGE. Rows may share a slot (the cache is only read). The work is divided

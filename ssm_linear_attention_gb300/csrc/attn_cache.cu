@@ -143,9 +143,10 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const MoveArgs a) {
         for (int o = LPV / 2; o >= 1; o >>= 1) m = max(m, __shfl_xor_sync(mask, m, o));
         const bool finite = m < 0x7f800000u;
         const float amax = fmaxf(__uint_as_float(m), kAmaxFloor);
+        // a vector that is not finite is marked by its scale; its values are stored as zeros
         const float inv = __fdiv_rn(kE4M3Max, amax);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] *= inv;
+        for (int j = 0; j < 8; ++j) x[j] = finite ? x[j] * inv : 0.f;
         *reinterpret_cast<uint2*>(static_cast<char*>(a.dst[w]) + vec * D + lane * 8) = pack8_e4m3(x);
         if (lane == 0)
             a.scale[w][vec] = finite ? __fdiv_rn(amax, kE4M3Max) : __uint_as_float(0x7fc00000u);

@@ -1,44 +1,51 @@
 // attn_decode.cu -- attention of a few new tokens per row over the paged cache.
 //
 // For a row's T query tokens and the G = HQ / HKV query heads of one key / value head, the
-// T G queries read the same cached tokens, so they form one operand of M = T G rows and
-// every cached vector is read once:
-//     S = Q K^T (M x tokens),  P = exp2(S - running row maximum),  O += P V,
-// with the softmax's maximum m and sum l kept per row while the tokens stream by and O, l
-// rescaled when m grows. Two such partial results (m, l, O) over different tokens join as
-// O = O_1 2^(m_1 - m) + O_2 2^(m_2 - m), l likewise, m = max(m_1, m_2); that makes the
-// token axis free to split.
+// M = T G queries read the same cached tokens, so every cached vector is read once for all
+// of them:
+//     S^T = K Q^T (tokens x M),  P = exp2(S - running maximum),  O^T += V^T P^T,
+// with the softmax's maximum m and sum l kept per query while the tokens stream by and O, l
+// rescaled when a score passes m by more than 8 (weights up to 2^8 lose nothing in float32
+// sums or bf16 / f16 operands, and most tiles then need no maximum across lanes). Two
+// partial results (m, l, O) over different tokens join as O = O_1 2^(m_1 - m) +
+// O_2 2^(m_2 - m), l likewise, m = max(m_1, m_2); that makes the token axis free to split.
 //
-// Bound: the cached bytes, M flops per byte and two bytes per value at most -- HBM. The
-// contractions are far too small for a tcgen05 tile of 128 rows (M is 1 to 64, mostly 4
-// to 8), and a warp-level mma.sync m16n8k16 whose rows are the queries keeps S, P and O in
-// the registers of one warp, with no tensor-memory round trips between the two products.
+// Bound: the cached bytes, M flops per byte at most -- HBM. The contractions are far too
+// small for a tcgen05 tile of 128 rows (M is 1 to 64, mostly 4 to 8). A warp-level mma.sync
+// m16n8k16 takes 16 cached tokens (then 16 value columns) as its rows and 8 queries as its
+// columns, and keeps S, P and O in one warp's registers; with the queries as rows (16 of
+// them) half of every product and of the softmax was padding at M <= 8.
 //
 // Work: 16 cached tokens of one (row, key head) are a tile, all tiles of the call form one
 // list (row, head, tokens in order), and the list is cut into equal contiguous ranges,
-// one per group of warps (a group: ceil(M / 16) warps that take 16 queries each over the
-// same tiles). Lengths are read on the device: no length reaches the host, ragged batches
-// balance to a tile, a single long row fills the machine. A group streams its tiles with
-// TMA boxes of 128-byte swizzled row segments into a ring of stages of its own (conflict-
-// free ldmatrix), and never meets another group before its range ends. A (row, head) that
-// lies inside one range is written out by its group. One that is cut leaves partial
-// results; the groups of a CTA join theirs through shared memory, and the last CTA of a
-// (row, head) to arrive at a counter joins the CTAs' results, in an order that the
+// one per group of warps (a group: ceil(M / 16) warps that take up to 16 queries each over
+// the same tiles). Lengths are read on the device: no length reaches the host, ragged
+// batches balance to a tile, a single long row fills the machine. A group streams its
+// tiles with TMA boxes of 128-byte swizzled row segments into a ring of stages of its own
+// (conflict-free ldmatrix), and never meets another group before its range ends. A (row,
+// head) that lies inside one range is written out by its group. One that is cut leaves
+// partial results; the groups of a CTA join theirs through shared memory, and the last CTA
+// of a (row, head) to arrive at a counter joins the CTAs' results, in an order that the
 // lengths alone fix.
+#include <cuda_fp16.h>
+
 #include "attn.cuh"
 
 namespace rssm {
 namespace attn {
 
 constexpr int kTok = 16;       // tokens per tile: the smallest page
-constexpr int kWarps = 8;
-constexpr int kDecThreads = kWarps * 32;
+constexpr int kMaxWarps = 16;   // per CTA
 constexpr int kMaxRows = 1024;  // rows per launch (prefix sums in shared memory)
+constexpr int kCumBytes = 5120;  // kMaxRows + 1 of them, up to the stages' alignment
 constexpr int kMaxStages = 8;   // per group
 // A range shorter than this is not cut further: the partial results of a cut cost about as
 // much as these tiles.
 constexpr int kMinTiles = 4;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+// m follows the largest score once it is this far behind (log2 units)
+constexpr float kSlack = 8.f;
 
 struct DecArgs {
     const void* q;
@@ -56,7 +63,7 @@ struct DecArgs {
     int32_t* counters; // [CTAs]
     float qscale;      // scale * log2 e
     int batch, T, G, hq, hkv, ps_log2, num_pages, max_pages, num_slots, window, appended;
-    int M, MT;         // queries per key head, warps per group
+    int M, MT;         // queries per key head, warps per group (each 8 NQ queries)
     int stages;        // per group
     int obf;
 };
@@ -75,32 +82,45 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t* r) {
                  : "r"(addr)
                  : "memory");
 }
+template <bool F16>
 __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    if (F16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+            "{%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+            "{%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// 8 x 8 transpose of 16-bit values, a row's pair per lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+__device__ __forceinline__ float log2_fast(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 
-// Four e4m3 codes w as bf16 pairs: lo = codes 0 and 2, hi = codes 1 and 3, each its value
-// times 2^-120. An e4m3 code has its exponent and significand in the bits below its sign;
-// moved under a bf16 sign, four bits further down, they read as the same number with the
-// bf16 bias (127 against 7), subnormal codes included. Exact, and three instructions a
-// pair. The factor is undone in the score scale and the output (kUnscale).
-__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-    hi = (w & 0x80008000u) | ((w >> 4) & 0x07f007f0u);
-    lo = ((w << 8) & 0x80008000u) | ((w << 4) & 0x07f007f0u);
+// The four e4m3 codes of w as f16 pairs (exact): lo = codes 0, 1, hi = codes 2, 3.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
 }
-// Queries and weights are raised by 2^64 against the codes' 2^-120, so that neither the
-// products nor their sums come near float32's subnormal range; 2^56 remains.
-constexpr float kRaise = 18446744073709551616.f;  // 2^64
-constexpr float kUnscale = 72057594037927936.f;   // 2^56
 
 // Byte offset of 16-byte chunk c of token t in a [16 tokens][ROWB bytes] tile as the TMA
 // boxes leave it: 128-byte row segments, chunk j of row r at j ^ (r % 8).
@@ -152,21 +172,19 @@ struct Tile {
     int b, h, pos, y;
 };
 
+// The tile list (fewer than 2^31 tiles) cut into ranges, one per worker (group of warps).
 struct Ranges {
-    long total;
-    int per_cta;  // groups of a CTA that have a range
+    uint32_t total, base, rem;  // a range has base tiles, the first rem of them one more
+    int per_cta;                // workers of a CTA
     int workers;
 };
-// First tile of worker w's range: the remainder of total / workers goes to the first ones.
-__device__ __forceinline__ long range_start(const Ranges& r, long w) {
-    const long base = r.total / r.workers, rem = r.total - base * r.workers;
-    return w * base + (w < rem ? w : rem);
+__device__ __forceinline__ uint32_t range_start(const Ranges& r, uint32_t w) {
+    return w * r.base + min(w, r.rem);
 }
 // The worker whose range holds tile t.
-__device__ __forceinline__ int worker_of(const Ranges& r, long t) {
-    const long base = r.total / r.workers, rem = r.total - base * r.workers;
-    const long cut = rem * (base + 1);
-    return (int)(t < cut ? t / (base + 1) : rem + (t - cut) / base);
+__device__ __forceinline__ uint32_t worker_of(const Ranges& r, uint32_t t) {
+    const uint32_t cut = r.rem * (r.base + 1);
+    return t < cut ? t / (r.base + 1) : r.rem + (t - cut) / r.base;
 }
 
 // The whole warp's bounded wait for phase `parity` of `bar`; false, with the CTA's abort
@@ -184,7 +202,7 @@ __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatil
 }
 
 // Last row b with cum[b] <= i (rows without tiles are passed over).
-__device__ __forceinline__ int find_row(const long* cum, int batch, long i) {
+__device__ __forceinline__ int find_row(const uint32_t* cum, int batch, uint32_t i) {
     int lo = 0, hi = batch - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -194,16 +212,20 @@ __device__ __forceinline__ int find_row(const long* cum, int batch, long i) {
     return lo;
 }
 
-__device__ __forceinline__ Tile locate_tile(const DecArgs& a, const long* cum, long t) {
-    const int b = find_row(cum, a.batch, t / a.hkv);
-    const long nt = cum[b + 1] - cum[b];
-    const long in_row = t - cum[b] * a.hkv;
-    const int s = a.ci[b];
-    const RowSpan sp = row_span(a, a.slot_len[s]);
-    Tile x;
-    x.b = b;
+// Row and head of tile t, and its number among the (row, head)'s tiles.
+__device__ __forceinline__ int find_tile(const DecArgs& a, const uint32_t* cum, uint32_t t, Tile& x) {
+    x.b = find_row(cum, a.batch, t / (uint32_t)a.hkv);
+    const uint32_t nt = cum[x.b + 1] - cum[x.b];
+    const uint32_t in_row = t - cum[x.b] * (uint32_t)a.hkv;
     x.h = (int)(in_row / nt);
-    x.pos = (sp.first + (int)(in_row - x.h * nt)) * kTok;
+    return (int)(in_row - (uint32_t)x.h * nt);
+}
+
+__device__ __noinline__ Tile locate_tile(const DecArgs& a, const uint32_t* cum, uint32_t t) {
+    Tile x;
+    const int i = find_tile(a, cum, t, x);
+    const int s = a.ci[x.b];
+    x.pos = (row_span(a, a.slot_len[s]).first + i) * kTok;
     const int page = a.page_table[(long)s * a.max_pages + (x.pos >> a.ps_log2)];
     if (page < 0 || page >= a.num_pages) {
         set_dev_err(a.dev_err, RSSM_DEVERR_PAGE);
@@ -229,75 +251,105 @@ struct Run {
     int cta0, cta1;  // first and last CTA
 };
 
-// D: head dim, E4M3: 8-bit cache, PARTS: bf16 parts of a query and of a weight (1 and 2
-// for bf16 activations, 3 and 3 for float32 ones, which keeps all 24 bits).
-template <int D, bool E4M3, bool AF32>
+// D: head dim, E4M3: 8-bit cache, AF32: float32 activations. The products' operands:
+//   bf16 cache: bf16, the cached values as they are. A weight in one bf16 part would add
+//     an error as large as the output's own rounding (1.41 times it together), so it takes
+//     two; float32 activations take three parts of each, all 24 bits.
+//   8-bit cache: f16, which holds every e4m3 value. The value scales go into the softmax's
+//     exponent (weights at most 1, whatever the scales), and a query row is divided by the
+//     power of two at its largest element. One part carries all 8 bits of a bf16 query but
+//     11 of a weight, whose error shows in a small output of large terms: two parts, and
+//     two of each for float32 activations.
+template <int D, bool E4M3, bool AF32, int NQ>
 struct Cfg {
+    // Warps of a CTA. The registers of 16 warps (128 each) hold 8 queries' accumulators;
+    // with a bf16 cache 16 rings would leave one stage each.
+    static constexpr int WARPS = 8;
     static constexpr int ROWB = D * (E4M3 ? 1 : 2);  // bytes of a cached vector
     static constexpr int KB = kTok * ROWB;           // K (or V) bytes of a tile
-    static constexpr int QP = AF32 ? 3 : 1;
-    static constexpr int PP = AF32 ? 3 : 2;
-    static constexpr int NB = D / 8;                 // n blocks of O
+    static constexpr int QP = AF32 ? (E4M3 ? 2 : 3) : 1;
+    static constexpr int PP = !E4M3 && AF32 ? 3 : 2;
+    static constexpr int DB = D / 16;                // 16-column blocks of O^T
+    static constexpr int TD = D + 4;                 // row pitch of tails: stores hit all banks
     static constexpr int AUX = E4M3 ? 2 * kTok * 4 : 0;  // scales of a tile
     static constexpr int STAGE = 2 * KB;
+    // O^T column of block c that lane row n holds in its first (half 0) or second register
+    // pair: 8-bit values come as even and odd columns, bf16 ones as the block's two halves.
+    __device__ static __forceinline__ int col(int c, int n, int half) {
+        return 16 * c + (E4M3 ? 2 * n + half : 8 * half + n);
+    }
 };
 
-// Split v into bf16 parts: part i the rounding of what the parts before it leave.
-template <int N>
-__device__ __forceinline__ void split2(float v0, float v1, uint32_t (*out)[4], int reg) {
+// Split v0, v1 into bf16 (f16) pairs: part i is the rounding of what the parts before it
+// leave.
+template <int N, bool F16>
+__device__ __forceinline__ void split2(float v0, float v1, uint32_t* out) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const uint32_t p = pack_bf16x2(v0, v1);
-        out[i][reg] = p;
-        if (i + 1 < N) {
-            v0 -= bf16_lo(p);
-            v1 -= bf16_hi(p);
+        if (F16) {
+            const __half2 h = __floats2half2_rn(v0, v1);
+            out[i] = *reinterpret_cast<const uint32_t*>(&h);
+            if (i + 1 < N) {
+                v0 -= __low2float(h);
+                v1 -= __high2float(h);
+            }
+        } else {
+            const uint32_t p = pack_bf16x2(v0, v1);
+            out[i] = p;
+            if (i + 1 < N) {
+                v0 -= bf16_lo(p);
+                v1 -= bf16_hi(p);
+            }
         }
     }
 }
 
-template <int D, bool E4M3, bool AF32>
-__global__ void __launch_bounds__(kDecThreads, 1)
+template <int D, bool E4M3, bool AF32, int NQ>
+__global__ void __launch_bounds__((Cfg<D, E4M3, AF32, NQ>::WARPS * 32), 1)
     decode_kernel(const DecArgs a, const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap) {
-    using C = Cfg<D, E4M3, AF32>;
+    using C = Cfg<D, E4M3, AF32, NQ>;
+    constexpr int kWarps = C::WARPS, kDecThreads = kWarps * 32;
     extern __shared__ unsigned char smem_raw[];
     // 128-byte swizzled boxes want their base on 1024 bytes
     unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int ngroups = kWarps / a.MT;
     const int group = warp / a.MT, mt = warp - group * a.MT;
-    const bool in_group = group < ngroups;
+    const int stages = a.stages;
 
-    // shared memory: stages, then scales, tiles, barriers, prefix sums
-    unsigned char* st_kv = smem;
-    const int nst = a.stages * ngroups;
-    float* st_scale = reinterpret_cast<float*>(smem + (size_t)nst * C::STAGE);
-    Tile* st_tile = reinterpret_cast<Tile*>(smem + (size_t)nst * (C::STAGE + C::AUX));
+    // shared memory: prefix sums, stages (at the end the tails lie over them and what
+    // follows), scales, tiles, barriers
+    uint32_t* cum = reinterpret_cast<uint32_t*>(smem);
+    unsigned char* st_kv = smem + kCumBytes;
+    const int nst = stages * ngroups;
+    float* st_scale = reinterpret_cast<float*>(st_kv + (size_t)nst * C::STAGE);
+    int2* st_tile = reinterpret_cast<int2*>(st_kv + (size_t)nst * (C::STAGE + C::AUX));
     uint64_t* full = reinterpret_cast<uint64_t*>(st_tile + nst);
     uint64_t* empty = full + nst;
-    long* cum = reinterpret_cast<long*>(empty + nst);
-    __shared__ long scan[kWarps];
+    __shared__ uint32_t scan[kWarps];
     __shared__ int abort_flag;
     __shared__ int rec_b[2 * kWarps], rec_h[2 * kWarps];  // records; b < 0: none
-    __shared__ Run runs[2 * kWarps + 1];
+    __shared__ Run runs[2 * kWarps];
     __shared__ int nruns, last_flag[2];
-    __shared__ float tail_ml[kWarps * 16][2];
+    __shared__ float tail_ml[kWarps * 8 * NQ][2];
 
+    if (tid < nst) {
+        mbar_init(&full[tid], 1);
+        mbar_init(&empty[tid], a.MT);
+        fence_barrier_init();
+    }
     if (tid == 0) {
         abort_flag = 0;
-        for (int i = 0; i < nst; ++i) {
-            mbar_init(&full[i], 1);
-            mbar_init(&empty[i], a.MT);
-        }
-        fence_barrier_init();
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&kmap) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&vmap) : "memory");
     }
     if (tid < 2 * kWarps) rec_b[tid] = -1;
 
     // ------------------------------------------------------- the call's tile list
     {
         constexpr int R = kMaxRows / kDecThreads;
-        long n[R], sum = 0;
+        uint32_t n[R], sum = 0;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             const int b = tid * R + i;
@@ -305,25 +357,18 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             if (b < a.batch) {
                 const int len = row_len(a, b, blockIdx.x == 0);
                 n[i] = len < 0 ? 0 : row_span(a, len).tiles;
-                // a row that sees nothing has no tiles: its outputs are written here
-                if (len >= 0 && n[i] == 0 && b % gridDim.x == blockIdx.x) {
-                    const long o0 = (long)b * a.T * a.hq, no = (long)a.T * a.hq;
-                    for (long e = 0; e < no * D; ++e) store1(a.o, o0 * D + e, a.obf, 0.f);
-                    if (a.lse)
-                        for (long e = 0; e < no; ++e) a.lse[o0 + e] = -INFINITY;
-                }
             }
             sum += n[i];
         }
-        long inc = sum;
+        uint32_t inc = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long v = __shfl_up_sync(0xffffffffu, inc, o);
+            const uint32_t v = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc += v;
         }
         if (lane == 31) scan[warp] = inc;
         __syncthreads();
-        long before = inc - sum;
+        uint32_t before = inc - sum;
         for (int w = 0; w < warp; ++w) before += scan[w];
 #pragma unroll
         for (int i = 0; i < R; ++i) {
@@ -334,171 +379,201 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         if (tid == kDecThreads - 1 && a.batch == kMaxRows) cum[kMaxRows] = before;
         __syncthreads();
     }
+    // rows that see nothing have no tiles: their outputs are written here
+    for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
+        if (cum[b + 1] != cum[b] || row_len(a, b, false) < 0) continue;
+        const long o0 = (long)b * a.T * a.hq;
+        const int no = a.T * a.hq;
+        for (int e = tid; e < no * D; e += kDecThreads) store1(a.o, o0 * D + e, a.obf, 0.f);
+        if (a.lse)
+            for (int e = tid; e < no; e += kDecThreads) a.lse[o0 + e] = -INFINITY;
+    }
     Ranges rg;
-    rg.total = cum[a.batch] * a.hkv;
+    rg.total = cum[a.batch] * (uint32_t)a.hkv;
     if (rg.total == 0) return;
     {
-        long want = (rg.total + kMinTiles - 1) / kMinTiles;
-        const long ctas = gridDim.x;
-        long k = (want + ctas - 1) / ctas;
-        rg.per_cta = (int)(k < ngroups ? k : ngroups);
-        const long w = ctas * rg.per_cta;
-        rg.workers = (int)(w < want ? w : want);
+        const uint32_t want = (rg.total + kMinTiles - 1) / kMinTiles;
+        const uint32_t k = (want + gridDim.x - 1) / gridDim.x;
+        rg.per_cta = (int)min(k, (uint32_t)ngroups);
+        rg.workers = (int)min(gridDim.x * (uint32_t)rg.per_cta, want);
+        rg.base = rg.total / (uint32_t)rg.workers;
+        rg.rem = rg.total - rg.base * (uint32_t)rg.workers;
     }
     const int w0 = blockIdx.x * rg.per_cta;  // this CTA's first worker
     const int nw = min(rg.per_cta, rg.workers - w0);
     if (nw <= 0) return;
 
     // ------------------------------------------------------- stream the range
-    float o[C::NB][4];
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-    int cb = -1, ch = -1;   // current (row, head)
-    int rec_begin = 0;      // its tiles began before the range
-    const int r0 = mt * 16 + (lane >> 2), r1 = r0 + 8;
-    const int qd = lane & 3;
+    // Lane layout of the products: n = lane / 4 numbers S^T's tokens (n and n + 8) and O^T's
+    // columns, qd = lane % 4 its queries 2 qd and 2 qd + 1 of each block of 8.
+    float o[C::DB][NQ][4];
+    float m[NQ][2], l[NQ][2];
+    const int n8 = lane >> 2, qd = lane & 3;
+    const int q0 = mt * 8 * NQ;  // this warp's first query
 
-    if (in_group && group < nw) {
-        const long t0 = range_start(rg, w0 + group), t1 = range_start(rg, w0 + group + 1);
+    if (group < nw) {
+        const uint32_t t0 = range_start(rg, w0 + group), t1 = range_start(rg, w0 + group + 1);
         const int ntile = (int)(t1 - t0);
         const bool leader = mt == 0;
         const uint64_t pol = policy_evict_first();
-        unsigned char* kv = st_kv + (size_t)group * a.stages * C::STAGE;
-        float* sc = st_scale + group * a.stages * (C::AUX / 4);
-        Tile* tl = st_tile + group * a.stages;
-        uint64_t* fb = full + group * a.stages;
-        uint64_t* eb = empty + group * a.stages;
+        unsigned char* kv = st_kv + (size_t)group * stages * C::STAGE;
+        float* sc = st_scale + group * stages * (C::AUX / 4);
+        int2* tl = st_tile + group * stages;
+        uint64_t* fb = full + group * stages;
+        uint64_t* eb = empty + group * stages;
 
         // tiles 32 w .. 32 w + 31 of the range sit one per lane; the next 32 are looked up
         // while these are issued
         Tile cur{}, nxt{};
-        int win = 0;
-        if (leader) {
-            if (lane < ntile) cur = locate_tile(a, cum, t0 + lane);
-            if (32 + lane < ntile) nxt = locate_tile(a, cum, t0 + 32 + lane);
-        }
-        // issue tile i of the range into its stage (leader warp only)
-        auto issue = [&](int i) {
-            if (i >= ntile) return;
-            if ((i >> 5) != win) {
-                win = i >> 5;
+        int sent = 0, sent_s = 0;  // tiles issued, and the stage of the next
+        // issue the range's next tile into its stage (leader warp only)
+        auto issue = [&]() {
+            if (sent >= ntile) return;
+            if ((sent & 31) == 0) {
+                if (sent == 0 && lane < ntile) nxt = locate_tile(a, cum, t0 + lane);
                 cur = nxt;
-                if (32 * (win + 1) + lane < ntile) nxt = locate_tile(a, cum, t0 + 32 * (win + 1) + lane);
+                if (sent + 32 + lane < ntile) nxt = locate_tile(a, cum, t0 + sent + 32 + lane);
             }
-            if (lane == (i & 31)) {
-                const int s = i % a.stages;
-                unsigned char* dst = kv + (size_t)s * C::STAGE;
-                tl[s] = cur;
+            if (lane == (sent & 31)) {
+                unsigned char* dst = kv + (size_t)sent_s * C::STAGE;
+                tl[sent_s] = make_int2(cur.pos, cur.y);
                 if (cur.y < 0) {
-                    mbar_arrive_plain(&fb[s]);
+                    mbar_arrive_plain(&fb[sent_s]);
                 } else {
-                    mbar_arrive_expect_tx(&fb[s], C::STAGE + C::AUX);
+                    mbar_arrive_expect_tx(&fb[sent_s], C::STAGE + C::AUX);
                     constexpr int EB = E4M3 ? 1 : 2;
                     const int y = C::ROWB >= 128 ? cur.y : cur.y >> 1;
 #pragma unroll
                     for (int x = 0; x < (C::ROWB + 127) / 128; ++x) {
-                        tma_load_2d(dst + x * kTok * 128, &kmap, x * 128 / EB, y, &fb[s], pol);
-                        tma_load_2d(dst + C::KB + x * kTok * 128, &vmap, x * 128 / EB, y, &fb[s], pol);
+                        tma_load_2d(dst + x * kTok * 128, &kmap, x * 128 / EB, y, &fb[sent_s], pol);
+                        tma_load_2d(dst + C::KB + x * kTok * 128, &vmap, x * 128 / EB, y, &fb[sent_s], pol);
                     }
                     if (E4M3) {
-                        bulk_g2s(sc + s * 2 * kTok, a.k_scale + cur.y, kTok * 4, &fb[s]);
-                        bulk_g2s(sc + s * 2 * kTok + kTok, a.v_scale + cur.y, kTok * 4, &fb[s]);
+                        bulk_g2s(sc + sent_s * 2 * kTok, a.k_scale + cur.y, kTok * 4, &fb[sent_s]);
+                        bulk_g2s(sc + sent_s * 2 * kTok + kTok, a.v_scale + cur.y, kTok * 4, &fb[sent_s]);
                     }
                 }
             }
             __syncwarp();
+            ++sent;
+            if (++sent_s == stages) sent_s = 0;
         };
         // A stage is refilled one tile late when several warps read it, so that the
         // leader seldom waits for them.
-        const int lag = a.MT > 1 ? 1 : 0;
         if (leader)
-            for (int i = 0; i < a.stages; ++i) issue(i);
+#pragma unroll 1
+            for (int i = 0; i < stages; ++i) issue();
 
-        uint32_t qf[D / 16][C::QP][4];
-        int end0 = 0, end1 = 0, beg0 = 0, beg1 = 0;  // visible positions of rows r0 and r1
+        uint32_t qf[D / 16][NQ][C::QP][2];  // [k step][query block][part][k half]
+        float rs[NQ][2];                    // score factor of the queries
+        int end[NQ][2], beg[NQ][2];         // the positions they see
         int n_min = 0, n_max = 0, b_min = 0, b_max = 0;
-        const bool works = mt * 16 < a.M;
+        const bool works = q0 < a.M;
+        int cb = 0, ch = 0;      // current (row, head)
+        bool begun = false;      // its tiles began before this range
+        int next = 0;            // tile of the range at which it ends
+        int s = 0, phase = 0;    // stage and phase of tile i
+        int free_s = 0, free_phase = 0;
 
-        // Write the current (row, head)'s result: out when its tiles all lie in this range,
-        // else as a record. `tail`: the range ends with it.
-        auto finish = [&](bool ends, bool tail) {
-            l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-            l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-            l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-            l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-            const float un = E4M3 ? kUnscale : 1.f;
-            if (ends && !rec_begin) {
-                const float i0 = l0 == 0.f ? 0.f : un / l0, i1 = l1 == 0.f ? 0.f : un / l1;
+#pragma unroll 1
+        for (int i = 0;; ++i) {
+            if (i == next || i == ntile) {
+                if (i > 0) {
+                    // The result of the current (row, head): out when all of its tiles lie in this
+                    // range, else a record. The last one stays in registers until the stages are
+                    // free.
+                    const bool whole = i == next && !begun, tail = i == ntile;
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int r = half ? r1 : r0;
-                    if (r >= a.M) continue;
-                    const long row = out_row(a, cb, ch, r);
-                    const float inv = half ? i1 : i0, l = half ? l1 : l0, m = half ? m1 : m0;
+                    for (int q = 0; q < NQ; ++q)
 #pragma unroll
-                    for (int n = 0; n < C::NB; n += 2) {
-                        // bf16: block n has columns 8 n + 2 qd, + 1; e4m3: blocks n, n + 1
-                        // have the even and odd columns of 8 n + 4 qd .. + 3
-                        float v[4] = {o[n][2 * half], E4M3 ? o[n + 1][2 * half] : o[n][2 * half + 1],
-                                      E4M3 ? o[n][2 * half + 1] : o[n + 1][2 * half], o[n + 1][2 * half + 1]};
+                        for (int x = 0; x < 2; ++x)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) v[i] = l == 0.f ? 0.f : v[i] * inv;
-                        const long e0 = row * D + 8 * n + (E4M3 ? 4 * qd : 2 * qd);
-                        const long e1 = E4M3 ? e0 + 2 : e0 + 8;
-                        if (a.obf) {
-                            *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + e0) = pack_bf16x2(v[0], v[1]);
-                            *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + e1) = pack_bf16x2(v[2], v[3]);
-                        } else {
-                            *reinterpret_cast<float2*>(static_cast<float*>(a.o) + e0) = make_float2(v[0], v[1]);
-                            *reinterpret_cast<float2*>(static_cast<float*>(a.o) + e1) = make_float2(v[2], v[3]);
-                        }
+                            for (int w = 4; w < 32; w <<= 1)
+                                l[q][x] += __shfl_xor_sync(0xffffffffu, l[q][x], w);
+                    if (!whole && leader && lane == 0) {
+                        rec_b[2 * group + (tail ? 1 : 0)] = cb;
+                        rec_h[2 * group + (tail ? 1 : 0)] = ch;
                     }
-                    if (a.lse && qd == 0)
-                        a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-                }
-                return;
-            }
-            if (leader && lane == 0) {
-                rec_b[2 * group + (tail ? 1 : 0)] = cb;
-                rec_h[2 * group + (tail ? 1 : 0)] = ch;
-            }
-            if (tail) return;  // stays in registers until the stages are free
-            const long slot = 2L * gridDim.x + w0 + group;
+                    if (whole) {
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int r = half ? r1 : r0;
-                if (r >= a.M) continue;
-                float* dst = a.part + (slot * a.M + r) * D;
+                        for (int q = 0; q < NQ; ++q) {
+                            const float i0 = l[q][0] == 0.f ? 0.f : 1.f / l[q][0];
+                            const float i1 = l[q][1] == 0.f ? 0.f : 1.f / l[q][1];
+                            if (a.obf) {
+                                // transposed, a lane has two columns of query n8
+                                const int r = q0 + 8 * q + n8;
+                                const long row = r < a.M ? out_row(a, cb, ch, r) : 0;
+                                uint16_t* dst = static_cast<uint16_t*>(a.o) + row * D;
 #pragma unroll
-                for (int n = 0; n < C::NB; ++n) {
-                    const int d = E4M3 ? 16 * (n >> 1) + 4 * qd + (n & 1) : 8 * n + 2 * qd;
-                    dst[d] = o[n][2 * half] * un;
-                    dst[d + (E4M3 ? 2 : 1)] = o[n][2 * half + 1] * un;
+                                for (int c = 0; c < C::DB; ++c) {
+                                    float v[4];
+#pragma unroll
+                                    for (int x = 0; x < 4; ++x) {
+                                        const bool none = l[q][x & 1] == 0.f;
+                                        v[x] = none ? 0.f : o[c][q][x] * (x & 1 ? i1 : i0);
+                                    }
+                                    uint32_t lo = transpose8(pack_bf16x2(v[0], v[1]));
+                                    uint32_t hi = transpose8(pack_bf16x2(v[2], v[3]));
+                                    if (r >= a.M) continue;
+                                    if (E4M3) {  // even and odd columns 4 qd .. 4 qd + 3
+                                        *reinterpret_cast<uint2*>(dst + 16 * c + 4 * qd) = make_uint2(
+                                            __byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
+                                    } else {
+                                        *reinterpret_cast<uint32_t*>(dst + 16 * c + 2 * qd) = lo;
+                                        *reinterpret_cast<uint32_t*>(dst + 16 * c + 8 + 2 * qd) = hi;
+                                    }
+                                }
+                            }
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                const int r = q0 + 8 * q + 2 * qd + x;
+                                if (r >= a.M) continue;
+                                const long row = out_row(a, cb, ch, r);
+                                const bool none = l[q][x] == 0.f;
+                                if (!a.obf) {
+                                    float* dst = static_cast<float*>(a.o) + row * D;
+#pragma unroll
+                                    for (int c = 0; c < C::DB; ++c) {
+                                        dst[C::col(c, n8, 0)] = none ? 0.f : o[c][q][x] * (x ? i1 : i0);
+                                        dst[C::col(c, n8, 1)] = none ? 0.f : o[c][q][2 + x] * (x ? i1 : i0);
+                                    }
+                                }
+                                if (a.lse && n8 == 0)
+                                    a.lse[row] = none ? -INFINITY : (m[q][x] + log2f(l[q][x])) * kLn2;
+                            }
+                        }
+                    } else if (!tail) {
+                        const long slot = 2L * gridDim.x + w0 + group;
+#pragma unroll
+                        for (int q = 0; q < NQ; ++q)
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                const int r = q0 + 8 * q + 2 * qd + x;
+                                if (r >= a.M) continue;
+                                float* dst = a.part + (slot * a.M + r) * D;
+#pragma unroll
+                                for (int c = 0; c < C::DB; ++c) {
+                                    dst[C::col(c, n8, 0)] = o[c][q][x];
+                                    dst[C::col(c, n8, 1)] = o[c][q][2 + x];
+                                }
+                                if (n8 == 0) {
+                                    a.part_ml[(slot * a.M + r) * 2] = m[q][x];
+                                    a.part_ml[(slot * a.M + r) * 2 + 1] = l[q][x];
+                                }
+                            }
+                    }
                 }
-                if (qd == 0) {
-                    a.part_ml[(slot * a.M + r) * 2] = half ? m1 : m0;
-                    a.part_ml[(slot * a.M + r) * 2 + 1] = half ? l1 : l0;
-                }
-            }
-        };
+                if (i == ntile) break;
 
-        for (int i = 0; i < ntile; ++i) {
-            const int s = i % a.stages;
-            if (!wait_all(&fb[s], (i / a.stages) & 1, &abort_flag, a.dev_err)) break;
-            const Tile t = tl[s];
-            if (t.b != cb || t.h != ch) {
-                if (cb >= 0) finish(true, false);
-                // the new (row, head): its queries as mma operands
-                rec_begin = 0;
-                if (i == 0) {
-                    const long nt = cum[t.b + 1] - cum[t.b];
-                    rec_begin = t0 > cum[t.b] * a.hkv + t.h * nt;
+                // Start a (row, head): its queries as mma operands, the positions they see.
+                {
+                    Tile x;
+                    const int at = find_tile(a, cum, t0 + i, x);
+                    cb = x.b;
+                    ch = x.h;
+                    begun = at > 0;
+                    next = i + (int)(cum[cb + 1] - cum[cb]) - at;
                 }
-                cb = t.b;
-                ch = t.h;
-                m0 = m1 = -INFINITY;
-                l0 = l1 = 0.f;
-#pragma unroll
-                for (int n = 0; n < C::NB; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
                 const int len = a.slot_len[a.ci[cb]];
                 const int app = a.appended ? 1 : 0;
                 n_min = len + app;
@@ -506,157 +581,221 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 b_min = a.window && n_min > a.window ? n_min - a.window : 0;
                 b_max = a.window && n_max > a.window ? n_max - a.window : 0;
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int r = half ? r1 : r0;
+                for (int c = 0; c < C::DB; ++c)
+#pragma unroll
+                    for (int q = 0; q < NQ; ++q) o[c][q][0] = o[c][q][1] = o[c][q][2] = o[c][q][3] = 0.f;
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) {
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int r = q0 + 8 * q + 2 * qd + x;
+                        const int e = len + (app ? (r < a.M ? r / a.G : 0) + 1 : 0);
+                        end[q][x] = e;
+                        beg[q][x] = a.window && e > a.window ? e - a.window : 0;
+                        m[q][x] = -INFINITY;
+                        l[q][x] = 0.f;
+                        rs[q][x] = a.qscale;
+                    }
+                    const int r = q0 + 8 * q + n8;  // the query whose operand values this lane has
                     const int j = r < a.M ? r / a.G : 0;
-                    const int e = len + (app ? j + 1 : 0);
-                    const int bg = a.window && e > a.window ? e - a.window : 0;
-                    if (half) end1 = e, beg1 = bg;
-                    else end0 = e, beg0 = bg;
                     const long base = ((long)cb * a.T + j) * a.q_stride + (ch * a.G + (r - j * a.G)) * D;
+                    float v[D / 16][4];
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
-                        // columns of the k16 step that this lane's registers 0/1 and 2/3 hold
-                        float v[4];
+                        // columns of a k16 step: pairs at 2 qd and 2 qd + 8; for 8-bit keys, of
+                        // which a lane gets 4 bytes, 4 qd and 4 qd + 2
 #pragma unroll
-                        for (int e2 = 0; e2 < 4; ++e2) {
-                            const int col = E4M3 ? 4 * qd + (e2 & 1) * 2 + (e2 >> 1)
-                                                 : 2 * qd + (e2 & 1) + (e2 >> 1) * 8;
-                            v[e2] = r < a.M ? load1(a.q, base + 16 * kk + col, !AF32) : 0.f;
-                            if (E4M3) v[e2] *= kRaise;
+                        for (int e = 0; e < 4; e += 2) {
+                            const int col = 16 * kk + (E4M3 ? 4 * qd + e : 2 * qd + 4 * e);
+                            v[kk][e] = v[kk][e + 1] = 0.f;
+                            if (r < a.M) {
+                                if (AF32) {
+                                    const float2 f = *reinterpret_cast<const float2*>(
+                                        static_cast<const float*>(a.q) + base + col);
+                                    v[kk][e] = f.x;
+                                    v[kk][e + 1] = f.y;
+                                } else {
+                                    const uint32_t f = *reinterpret_cast<const uint32_t*>(
+                                        static_cast<const uint16_t*>(a.q) + base + col);
+                                    v[kk][e] = bf16_lo(f);
+                                    v[kk][e + 1] = bf16_hi(f);
+                                }
+                            }
                         }
-                        split2<C::QP>(v[0], v[1], qf[kk], half);
-                        split2<C::QP>(v[2], v[3], qf[kk], 2 + half);
+                    }
+                    if (E4M3) {  // into f16's range: divide by the power of two at the largest
+                        float top = 0.f;
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) top = fmaxf(top, fabsf(v[kk][x]));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                        float p2 = __uint_as_float(__float_as_uint(top) & 0x7f800000u);
+                        if (p2 == 0.f || p2 == INFINITY) p2 = 1.f;
+                        const float inv = 1.f / p2;
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) v[kk][x] *= inv;
+                        rs[q][0] = a.qscale * __shfl_sync(0xffffffffu, p2, 8 * qd);
+                        rs[q][1] = a.qscale * __shfl_sync(0xffffffffu, p2, 8 * qd + 4);
+                    }
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        uint32_t lo[C::QP], hi[C::QP];
+                        split2<C::QP, E4M3>(v[kk][0], v[kk][1], lo);
+                        split2<C::QP, E4M3>(v[kk][2], v[kk][3], hi);
+#pragma unroll
+                        for (int p = 0; p < C::QP; ++p) {
+                            qf[kk][q][p][0] = lo[p];
+                            qf[kk][q][p][1] = hi[p];
+                        }
                     }
                 }
             }
+
+            if (!wait_all(&fb[s], phase, &abort_flag, a.dev_err)) break;
+            const int2 t = tl[s];
+            const int pos = t.x;
             if (t.y >= 0 && works) {
+                const unsigned char* vt = kv + (size_t)s * C::STAGE + C::KB;
                 const uint32_t kbase = smem_addr(kv + (size_t)s * C::STAGE), vbase = kbase + C::KB;
-                // ------------------------------------------------ S = Q K^T
-                float sa[2][2][4];
-#pragma unroll
-                for (int x = 0; x < 16; ++x) sa[x >> 3][(x >> 2) & 1][x & 3] = 0.f;
                 const int lr = lane & 7, lm = lane >> 3;
+                // ------------------------------------------------ S^T = K Q^T
+                float sa[2][NQ][4];
+#pragma unroll
+                for (int q = 0; q < NQ; ++q)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) sa[0][q][x] = sa[1][q][x] = 0.f;
                 if (E4M3) {
 #pragma unroll
                     for (int kk = 0; kk < D / 16; kk += 2) {
-                        uint32_t r[4], lo, hi;
+                        uint32_t r[4], f[2][4];
                         ldsm4(kbase + tile_off<C::ROWB>((lm & 1) * 8 + lr, kk + (lm >> 1)), r);
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            e4m3x4_to_bf16(r[x], lo, hi);
+                        for (int x = 0; x < 4; ++x) e4m3x4_to_f16(r[x], f[x >> 1][x & 1], f[x >> 1][2 + (x & 1)]);
 #pragma unroll
-                            for (int p = 0; p < C::QP; ++p)
-                                mma16816(sa[x >> 1][x & 1], qf[kk + (x >> 1)][p], lo, hi);
-                        }
+                        for (int p = 0; p < C::QP; ++p)
+#pragma unroll
+                            for (int q = 0; q < NQ; ++q) {
+                                mma16816<true>(sa[0][q], f[0], qf[kk][q][p][0], qf[kk][q][p][1]);
+                                mma16816<true>(sa[1][q], f[1], qf[kk + 1][q][p][0], qf[kk + 1][q][p][1]);
+                            }
                     }
                 } else {
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         uint32_t r[4];
-                        ldsm4(kbase + tile_off<C::ROWB>((lm >> 1) * 8 + lr, 2 * kk + (lm & 1)), r);
+                        ldsm4(kbase + tile_off<C::ROWB>((lm & 1) * 8 + lr, 2 * kk + (lm >> 1)), r);
 #pragma unroll
-                        for (int p = 0; p < C::QP; ++p) {
-                            mma16816(sa[kk & 1][0], qf[kk][p], r[0], r[1]);
-                            mma16816(sa[kk & 1][1], qf[kk][p], r[2], r[3]);
-                        }
+                        for (int p = 0; p < C::QP; ++p)
+#pragma unroll
+                            for (int q = 0; q < NQ; ++q)
+                                mma16816<false>(sa[kk & 1][q], r, qf[kk][q][p][0], qf[kk][q][p][1]);
                     }
                 }
                 // ------------------------------------------------ softmax
-                float p[2][4];
-                const float* ks = sc + s * 2 * kTok;
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    float f0 = a.qscale, f1 = a.qscale;
-                    if (E4M3) {
-                        const float2 k2 = *reinterpret_cast<const float2*>(ks + n * 8 + 2 * qd);
-                        f0 *= k2.x * kUnscale;
-                        f1 *= k2.y * kUnscale;
-                    }
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        p[n][x] = (sa[0][n][x] + sa[1][n][x]) * (x & 1 ? f1 : f0);
-                }
-                const bool edge = t.pos + kTok > n_min || t.pos < b_max;
-                if (edge) {
-#pragma unroll
-                    for (int n = 0; n < 2; ++n)
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const int tok = t.pos + n * 8 + 2 * qd + (x & 1);
-                            const bool vis = x < 2 ? tok < end0 && tok >= beg0 : tok < end1 && tok >= beg1;
-                            if (!vis) p[n][x] = -INFINITY;
-                        }
-                }
-                float x0 = fmaxf(fmaxf(p[0][0], p[0][1]), fmaxf(p[1][0], p[1][1]));
-                float x1 = fmaxf(fmaxf(p[0][2], p[0][3]), fmaxf(p[1][2], p[1][3]));
-                x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
-                x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
-                x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
-                x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
-                const float nm0 = fmaxf(m0, x0), nm1 = fmaxf(m1, x1);
-                if (__any_sync(0xffffffffu, nm0 != m0 || nm1 != m1)) {
-                    const float f0 = m0 == nm0 ? 1.f : exp2_fast(m0 - nm0);
-                    const float f1 = m1 == nm1 ? 1.f : exp2_fast(m1 - nm1);
-                    l0 *= f0;
-                    l1 *= f1;
-#pragma unroll
-                    for (int n = 0; n < C::NB; ++n) {
-                        o[n][0] *= f0;
-                        o[n][1] *= f0;
-                        o[n][2] *= f1;
-                        o[n][3] *= f1;
-                    }
-                    m0 = nm0;
-                    m1 = nm1;
-                }
-                // a row that has seen only -infinity keeps weights of zero
-                const float c0 = m0 == -INFINITY ? 0.f : m0, c1 = m1 == -INFINITY ? 0.f : m1;
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) p[n][x] = exp2_fast(p[n][x] - (x < 2 ? c0 : c1));
-                    l0 += p[n][0] + p[n][1];
-                    l1 += p[n][2] + p[n][3];
-                }
+                // Scores in log2 units. With an 8-bit cache a token's value scale joins its
+                // weight as log2(scale) in the exponent: m bounds those sums, the weights stay
+                // in f16's range, and l, which wants the scores alone, divides it out again.
+                float p[NQ][4];
+                float ks[2] = {1.f, 1.f}, lv[2] = {0.f, 0.f}, iv[2] = {1.f, 1.f};
                 if (E4M3) {
+                    const float* ts = sc + s * 2 * kTok + n8;
 #pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        const float2 v2 = *reinterpret_cast<const float2*>(ks + kTok + n * 8 + 2 * qd);
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            float w = p[n][x] * ((x & 1 ? v2.y : v2.x) * kRaise);
-                            if (edge) {
-                                const int tok = t.pos + n * 8 + 2 * qd + (x & 1);
-                                const bool vis = x < 2 ? tok < end0 && tok >= beg0 : tok < end1 && tok >= beg1;
-                                if (!vis) w = 0.f;  // whatever the scale there holds
-                            }
-                            p[n][x] = w;
-                        }
+                    for (int x = 0; x < 2; ++x) {
+                        ks[x] = ts[8 * x];
+                        float v = ts[kTok + 8 * x];
+                        if (v < 1.1754944e-38f) v = 1.1754944e-38f;  // (a NaN stays)
+                        lv[x] = log2_fast(v);
+                        iv[x] = exp2_fast(-lv[x]);
                     }
                 }
-                // ------------------------------------------------ O += P V
+                const bool edge = pos + kTok > n_min || pos < b_max;
+                bool grow = false;
+#pragma unroll
+                for (int q = 0; q < NQ; ++q)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        float f = (sa[0][q][x] + sa[1][q][x]) * rs[q][x & 1];
+                        if (E4M3) f = f * ks[x >> 1] + lv[x >> 1];
+                        if (edge) {
+                            const int tok = pos + n8 + 8 * (x >> 1);
+                            // whatever the cache holds there
+                            if (tok >= end[q][x & 1] || tok < beg[q][x & 1]) f = -INFINITY;
+                        }
+                        p[q][x] = f;
+                        grow |= f > m[q][x & 1] + kSlack;
+                    }
+                if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                    for (int q = 0; q < NQ; ++q)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            float t = fmaxf(p[q][x], p[q][2 + x]);
+#pragma unroll
+                            for (int w = 4; w < 32; w <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, w));
+                            t = fmaxf(t, m[q][x]);
+                            const float f = t == m[q][x] ? 1.f : exp2_fast(m[q][x] - t);
+                            m[q][x] = t;
+                            l[q][x] *= f;
+#pragma unroll
+                            for (int c = 0; c < C::DB; ++c) {
+                                o[c][q][x] *= f;
+                                o[c][q][2 + x] *= f;
+                            }
+                        }
+                }
+                uint32_t pf[NQ][C::PP][2];
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) {
+                    // a query that has seen only -infinity keeps weights of zero
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const float c = m[q][x & 1] == -INFINITY ? 0.f : m[q][x & 1];
+                        p[q][x] = exp2_fast(p[q][x] - c);
+                        float w = p[q][x];
+                        if (E4M3) {
+                            w *= iv[x >> 1];
+                            // a hidden token's scale may be anything
+                            if (edge && p[q][x] == 0.f) w = 0.f;
+                        }
+                        l[q][x & 1] += w;
+                    }
+                    uint32_t lo[C::PP], hi[C::PP];
+                    split2<C::PP, E4M3>(p[q][0], p[q][1], lo);
+                    split2<C::PP, E4M3>(p[q][2], p[q][3], hi);
+#pragma unroll
+                    for (int x = 0; x < C::PP; ++x) {
+                        pf[q][x][0] = transpose8(lo[x]);
+                        pf[q][x][1] = transpose8(hi[x]);
+                    }
+                }
+                // ------------------------------------------------ O^T += V^T P^T
                 bool careful = false;
-                if (!E4M3 && edge) {
+                if (edge) {
                     // A weight of zero does not silence an infinity or a NaN in a value. Tokens
                     // that no query sees are cleared; if one that only some see is not finite,
-                    // the tile's products run value by value below.
-                    unsigned char* vt = kv + (size_t)s * C::STAGE + C::KB;
-                    const bool outside = t.pos + kTok > n_max || t.pos < b_min;
-                    if (outside) {
+                    // the tile's products run value by value below (8-bit values are finite:
+                    // what is not is marked in the scale, which a hidden score leaves out).
+                    if (pos + kTok > n_max || pos < b_min) {
+#pragma unroll 1
                         for (int e = lane; e < kTok * (C::ROWB / 16); e += 32) {
                             const int tok = e / (C::ROWB / 16), c = e % (C::ROWB / 16);
-                            if (t.pos + tok >= n_max || t.pos + tok < b_min)
-                                *reinterpret_cast<uint4*>(vt + tile_off<C::ROWB>(tok, c)) = make_uint4(0, 0, 0, 0);
+                            if (pos + tok >= n_max || pos + tok < b_min)
+                                *reinterpret_cast<uint4*>(kv + (size_t)s * C::STAGE + C::KB +
+                                                          tile_off<C::ROWB>(tok, c)) = make_uint4(0, 0, 0, 0);
                         }
                         fence_async_smem();  // the stage's next TMA load comes after these stores
                         __syncwarp();
                     }
-                    if (a.T > 1) {
+                    if (!E4M3 && a.T > 1) {
                         bool odd = false;
+#pragma unroll 1
                         for (int e = lane; e < kTok * (C::ROWB / 16); e += 32) {
-                            const int tok = e / (C::ROWB / 16), c = e % (C::ROWB / 16), pos = t.pos + tok;
-                            if ((pos >= n_min && pos < n_max) || (pos >= b_min && pos < b_max)) {
+                            const int tok = e / (C::ROWB / 16), c = e % (C::ROWB / 16), at = pos + tok;
+                            if ((at >= n_min && at < n_max) || (at >= b_min && at < b_max)) {
                                 const uint4 v = *reinterpret_cast<const uint4*>(vt + tile_off<C::ROWB>(tok, c));
                                 const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -668,78 +807,78 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                     }
                 }
                 if (!careful) {
-                    uint32_t pf[C::PP][4];
-                    split2<C::PP>(p[0][0], p[0][1], pf, 0);
-                    split2<C::PP>(p[0][2], p[0][3], pf, 1);
-                    split2<C::PP>(p[1][0], p[1][1], pf, 2);
-                    split2<C::PP>(p[1][2], p[1][3], pf, 3);
-                    constexpr int CH = C::ROWB / 16;  // 16-byte chunks of a vector
 #pragma unroll
-                    for (int c = 0; c < CH; c += 2) {
-                        uint32_t r[4];
-                        ldsm4_t(vbase + tile_off<C::ROWB>((lm & 1) * 8 + lr, c + (lm >> 1)), r);
+                    for (int c = 0; c < C::DB; ++c) {
+                        uint32_t f[4];
                         if (E4M3) {
-                            uint32_t lo0, hi0, lo1, hi1, lo2, hi2, lo3, hi3;
-                            e4m3x4_to_bf16(r[0], lo0, hi0);
-                            e4m3x4_to_bf16(r[1], lo1, hi1);
-                            e4m3x4_to_bf16(r[2], lo2, hi2);
-                            e4m3x4_to_bf16(r[3], lo3, hi3);
+                            // a register holds two tokens' codes of columns 2 n, 2 n + 1; paired
+                            // by token they are one k pair of the even and of the odd columns
+                            if (c & 1) continue;
+                            uint32_t r[4], g[4];
+                            ldsm4_t(vbase + tile_off<C::ROWB>((lm & 1) * 8 + lr, c + (lm >> 1)), r);
 #pragma unroll
-                            for (int x = 0; x < C::PP; ++x) {
-                                mma16816(o[2 * c], pf[x], lo0, lo1);
-                                mma16816(o[2 * c + 1], pf[x], hi0, hi1);
-                                mma16816(o[2 * c + 2], pf[x], lo2, lo3);
-                                mma16816(o[2 * c + 3], pf[x], hi2, hi3);
+                            for (int x = 0; x < 4; ++x) {
+                                uint32_t lo, hi;
+                                e4m3x4_to_f16(r[x], lo, hi);
+                                uint32_t* d = x < 2 ? f : g;
+                                d[2 * (x & 1)] = __byte_perm(lo, hi, 0x5410);
+                                d[2 * (x & 1) + 1] = __byte_perm(lo, hi, 0x7632);
                             }
+#pragma unroll
+                            for (int x = 0; x < C::PP; ++x)
+#pragma unroll
+                                for (int q = 0; q < NQ; ++q) {
+                                    mma16816<true>(o[c][q], f, pf[q][x][0], pf[q][x][1]);
+                                    mma16816<true>(o[c + 1][q], g, pf[q][x][0], pf[q][x][1]);
+                                }
                         } else {
+                            ldsm4_t(vbase + tile_off<C::ROWB>((lm >> 1) * 8 + lr, 2 * c + (lm & 1)), f);
 #pragma unroll
-                            for (int x = 0; x < C::PP; ++x) {
-                                mma16816(o[c], pf[x], r[0], r[1]);
-                                mma16816(o[c + 1], pf[x], r[2], r[3]);
-                            }
+                            for (int x = 0; x < C::PP; ++x)
+#pragma unroll
+                                for (int q = 0; q < NQ; ++q)
+                                    mma16816<false>(o[c][q], f, pf[q][x][0], pf[q][x][1]);
                         }
                     }
                 } else {
-                    const unsigned char* vt = kv + (size_t)s * C::STAGE + C::KB;
+#pragma unroll 1
                     for (int tok = 0; tok < kTok; ++tok) {
-                        const int src = (lane & ~3) | ((tok & 7) >> 1);
-                        const int n = tok >> 3, x = tok & 1;
-                        const float w0f = n ? (x ? p[1][1] : p[1][0]) : (x ? p[0][1] : p[0][0]);
-                        const float w1f = n ? (x ? p[1][3] : p[1][2]) : (x ? p[0][3] : p[0][2]);
-                        const float w0v = __shfl_sync(0xffffffffu, w0f, src);
-                        const float w1v = __shfl_sync(0xffffffffu, w1f, src);
-                        const int pos = t.pos + tok;
-                        const bool see0 = pos < end0 && pos >= beg0, see1 = pos < end1 && pos >= beg1;
+                        const int src = (tok & 7) * 4 + qd;
 #pragma unroll
-                        for (int nb = 0; nb < C::NB; ++nb) {
-                            const uint32_t v = *reinterpret_cast<const uint32_t*>(
-                                vt + tile_off<C::ROWB>(tok, nb) + 4 * qd);
-                            if (see0) {
-                                o[nb][0] += w0v * bf16_lo(v);
-                                o[nb][1] += w0v * bf16_hi(v);
+                        for (int q = 0; q < NQ; ++q)
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                const float w = __shfl_sync(0xffffffffu, tok < 8 ? p[q][x] : p[q][2 + x], src);
+                                if (pos + tok >= end[q][x] || pos + tok < beg[q][x]) continue;
+#pragma unroll
+                                for (int c = 0; c < C::DB; ++c) {
+                                    const uint16_t* v = reinterpret_cast<const uint16_t*>(
+                                        vt + tile_off<C::ROWB>(tok, 2 * c) + 2 * n8);
+                                    const uint16_t* u = reinterpret_cast<const uint16_t*>(
+                                        vt + tile_off<C::ROWB>(tok, 2 * c + 1) + 2 * n8);
+                                    o[c][q][x] += w * bf16_to_f(*v);
+                                    o[c][q][2 + x] += w * bf16_to_f(*u);
+                                }
                             }
-                            if (see1) {
-                                o[nb][2] += w1v * bf16_lo(v);
-                                o[nb][3] += w1v * bf16_hi(v);
-                            }
-                        }
                     }
                 }
             }
             // ---------------------------------------------------- hand the stage back
             __syncwarp();
-            if (a.MT > 1 && lane == 0) mbar_arrive_plain(&eb[s]);
-            if (leader && i >= lag) {
-                const int done = i - lag;
-                if (a.MT > 1 && done + a.stages < ntile &&
-                    !wait_all(&eb[done % a.stages], (done / a.stages) & 1, &abort_flag, a.dev_err))
-                    break;
-                issue(done + a.stages);
+            if (++s == stages) s = 0, phase ^= 1;
+            if (a.MT == 1) {
+                issue();
+            } else {
+                // the tile before this one: its other readers have had a tile's time
+                if (lane == 0) mbar_arrive_plain(&eb[s == 0 ? stages - 1 : s - 1]);
+                if (leader && i > 0) {
+                    if (sent < ntile &&
+                        !wait_all(&eb[free_s], free_phase, &abort_flag, a.dev_err))
+                        break;
+                    issue();
+                    if (++free_s == stages) free_s = 0, free_phase ^= 1;
+                }
             }
-        }
-        if (cb >= 0) {
-            const long nt = cum[cb + 1] - cum[cb];
-            finish(t1 == cum[cb] * a.hkv + (ch + 1) * nt, true);
         }
     }
     __syncthreads();
@@ -755,25 +894,25 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 
     // ------------------------------------------------------- join the CTA's records
     // Tails into shared memory (the stages are free now).
-    float* tail = reinterpret_cast<float*>(smem);  // [group][M][D]
-    if (in_group && group < nw && rec_b[2 * group + 1] >= 0) {
-        const float un = E4M3 ? kUnscale : 1.f;
+    float* tail = reinterpret_cast<float*>(st_kv);  // [group][M][TD]
+    if (group < nw && rec_b[2 * group + 1] >= 0) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int r = half ? r1 : r0;
-            if (r >= a.M) continue;
-            float* dst = tail + ((long)group * a.M + r) * D;
+        for (int q = 0; q < NQ; ++q)
 #pragma unroll
-            for (int n = 0; n < C::NB; ++n) {
-                const int d = E4M3 ? 16 * (n >> 1) + 4 * qd + (n & 1) : 8 * n + 2 * qd;
-                dst[d] = o[n][2 * half] * un;
-                dst[d + (E4M3 ? 2 : 1)] = o[n][2 * half + 1] * un;
+            for (int x = 0; x < 2; ++x) {
+                const int r = q0 + 8 * q + 2 * qd + x;
+                if (r >= a.M) continue;
+                float* dst = tail + (group * a.M + r) * C::TD;
+#pragma unroll
+                for (int c = 0; c < C::DB; ++c) {
+                    dst[C::col(c, n8, 0)] = o[c][q][x];
+                    dst[C::col(c, n8, 1)] = o[c][q][2 + x];
+                }
+                if (n8 == 0) {
+                    tail_ml[group * a.M + r][0] = m[q][x];
+                    tail_ml[group * a.M + r][1] = l[q][x];
+                }
             }
-            if (qd == 0) {
-                tail_ml[group * a.M + r][0] = half ? m1 : m0;
-                tail_ml[group * a.M + r][1] = half ? l1 : l0;
-            }
-        }
     }
     if (tid == 0) {
         int n = 0;
@@ -784,20 +923,23 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 runs[n - 1].rec1 = i + 1;
                 continue;
             }
-            Run r;
-            r.b = rec_b[i];
-            r.h = rec_h[i];
-            r.rec0 = i;
-            r.rec1 = i + 1;
-            const long nt = cum[r.b + 1] - cum[r.b];
-            const long s0 = cum[r.b] * a.hkv + r.h * nt;
-            r.cta0 = worker_of(rg, s0) / rg.per_cta;
-            r.cta1 = worker_of(rg, s0 + nt - 1) / rg.per_cta;
-            r.whole = r.cta0 == r.cta1;
-            r.slot = 2 * (int)blockIdx.x + (r.cta0 < (int)blockIdx.x ? 0 : 1);
-            runs[n++] = r;
+            runs[n].b = rec_b[i];
+            runs[n].h = rec_h[i];
+            runs[n].rec0 = i;
+            runs[n].rec1 = i + 1;
+            ++n;
         }
         nruns = n;
+    }
+    __syncthreads();
+    if (tid < nruns) {
+        Run& r = runs[tid];
+        const uint32_t nt = cum[r.b + 1] - cum[r.b];
+        const uint32_t s0 = cum[r.b] * (uint32_t)a.hkv + (uint32_t)r.h * nt;
+        r.cta0 = (int)(worker_of(rg, s0) / (uint32_t)rg.per_cta);
+        r.cta1 = (int)(worker_of(rg, s0 + nt - 1) / (uint32_t)rg.per_cta);
+        r.whole = r.cta0 == r.cta1;
+        r.slot = 2 * (int)blockIdx.x + (r.cta0 < (int)blockIdx.x ? 0 : 1);
     }
     __threadfence_block();
     __syncthreads();
@@ -825,7 +967,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 const float* src;
                 if (i & 1) {
                     ml = tail_ml[(i >> 1) * a.M + row];
-                    src = tail + ((long)(i >> 1) * a.M + row) * D + d;
+                    src = tail + ((i >> 1) * a.M + row) * C::TD + d;
                 } else {
                     const long slot = 2L * gridDim.x + w0 + (i >> 1);
                     ml = a.part_ml + (slot * a.M + row) * 2;
@@ -847,7 +989,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 for (int i = 0; i < 4; ++i)
                     store1(a.o, out * D + d + i, a.obf, l == 0.f ? 0.f : y[i] * inv);
                 if (a.lse && d == 0)
-                    a.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+                    a.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
             } else {
                 *reinterpret_cast<float4*>(a.part + ((long)r.slot * a.M + row) * D + d) = acc;
                 if (d == 0) {
@@ -909,7 +1051,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             for (int i = 0; i < 4; ++i)
                 store1(a.o, out * D + d + i, a.obf, l == 0.f ? 0.f : y[i] * inv);
             if (a.lse && d == 0)
-                a.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+                a.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
         }
     }
 }
@@ -925,7 +1067,7 @@ struct Workspace {
 };
 static Workspace workspace_of(const rssm_attn_dims* d) {
     const size_t M = (size_t)d->q_tokens * (d->num_q_heads / d->num_kv_heads);
-    const size_t slots = kMaxCtas * (2 + kWarps);
+    const size_t slots = kMaxCtas * (2 + kMaxWarps);
     Workspace w;
     w.ml = kMaxCtas * sizeof(int32_t);
     w.part = (w.ml + slots * M * 2 * sizeof(float) + 255) / 256 * 256;
@@ -933,21 +1075,23 @@ static Workspace workspace_of(const rssm_attn_dims* d) {
     return w;
 }
 
-template <int D, bool E4M3, bool AF32>
-static int launch(const rssm_attn_dims* d, const rssm_attn_cache* c, DecArgs a, const DeviceInfo& di,
-                  cudaStream_t st) {
-    using C = Cfg<D, E4M3, AF32>;
-    const int ngroups = kWarps / a.MT;
-    const int fixed = (kMaxRows + 1) * 8 + 1024;
-    const int per = C::STAGE + C::AUX + (int)sizeof(Tile) + 16;
-    int stages = (di.max_smem_optin - 2560 - fixed) / (per * ngroups);
+template <int D, bool E4M3, bool AF32, int NQ>
+static int launch_nq(const rssm_attn_dims* d, const rssm_attn_cache* c, DecArgs a, const DeviceInfo& di,
+                     cudaStream_t st) {
+    using C = Cfg<D, E4M3, AF32, NQ>;
+    const int ngroups = C::WARPS / a.MT;
+    const int fixed = kCumBytes + 1024;
+    const int per = C::STAGE + C::AUX + 8 + 16;
+    // what the kernel's static arrays take: the tails' (m, l) and the lists of records
+    const int statics = C::WARPS * 8 * NQ * 8 + C::WARPS * (2 * (int)sizeof(Run) + 20) + 256;
+    int stages = (di.max_smem_optin - statics - fixed) / (per * ngroups);
     if (stages > kMaxStages) stages = kMaxStages;
     if (stages < 2) return RSSM_ERR_UNSUPPORTED;
     a.stages = stages;
     int smem = stages * ngroups * per + fixed;
-    const int tails = kWarps * 16 * D * 4 + 1024;
+    const int tails = C::WARPS * 8 * NQ * C::TD * 4 + fixed;
     if (smem < tails) smem = tails;
-    const void* kern = (const void*)decode_kernel<D, E4M3, AF32>;
+    const void* kern = (const void*)decode_kernel<D, E4M3, AF32, NQ>;
     if (!ensure_smem_limit(kern, smem)) return RSSM_ERR_CUDA;
     // rows of 128 bytes at least: 64-byte vectors go in pairs
     const uint64_t rows = (uint64_t)d->num_pages * d->num_kv_heads * d->page_size;
@@ -957,16 +1101,30 @@ static int launch(const rssm_attn_dims* d, const rssm_attn_cache* c, DecArgs a, 
         !make_tmap_rows128(&vm, c->v, E4M3 ? 1 : 2, pair ? rows / 2 : rows, pair ? 2 * D : D, pair ? kTok / 2 : kTok))
         return RSSM_ERR_CUDA;
     const int grid = di.sm_count < kMaxCtas ? di.sm_count : kMaxCtas;
-    for (int b = 0; b < d->batch; b += kMaxRows) {
+    // rows of a launch: the prefix sums' size, and a tile list of fewer than 2^31
+    const int64_t row_tiles = (int64_t)d->max_pages * (d->page_size / kTok) * a.hkv;
+    int64_t per_launch = (((int64_t)1 << 31) - 1) / row_tiles;
+    if (per_launch < 1) return RSSM_ERR_UNSUPPORTED;
+    if (per_launch > kMaxRows) per_launch = kMaxRows;
+    for (int b = 0; b < d->batch; b += (int)per_launch) {
         DecArgs x = a;
-        x.batch = d->batch - b < kMaxRows ? d->batch - b : kMaxRows;
+        x.batch = d->batch - b < per_launch ? d->batch - b : (int)per_launch;
         x.ci = a.ci + b;
         x.q = static_cast<const char*>(a.q) + (long)b * a.T * a.q_stride * (AF32 ? 4 : 2);
         x.o = static_cast<char*>(a.o) + (long)b * a.T * a.hq * D * (a.obf ? 2 : 4);
         if (a.lse) x.lse = a.lse + (long)b * a.T * a.hq;
-        decode_kernel<D, E4M3, AF32><<<grid, kDecThreads, smem, st>>>(x, km, vm);
+        decode_kernel<D, E4M3, AF32, NQ><<<grid, C::WARPS * 32, smem, st>>>(x, km, vm);
     }
     return launch_status();
+}
+
+// Up to 8 queries fit one block of mma columns; beyond, a warp takes two blocks (one pass
+// over the tile's operands serves both) and a group up to four warps.
+template <int D, bool E4M3, bool AF32>
+static int launch(const rssm_attn_dims* d, const rssm_attn_cache* c, const DecArgs& a,
+                  const DeviceInfo& di, cudaStream_t st) {
+    return a.M <= 8 ? launch_nq<D, E4M3, AF32, 1>(d, c, a, di, st)
+                    : launch_nq<D, E4M3, AF32, 2>(d, c, a, di, st);
 }
 
 }  // namespace attn

@@ -525,3 +525,43 @@ def test_wrapper_refuses_layouts_it_cannot_read():
             dec.decode(q, ci)
     with pytest.raises(ValueError):
         dec.append(good[:, :, :2], good[:1, :, :2], ci)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_every_8_bit_code_counts(d):
+    """Scores and values made of one code each, the subnormal ones included: a key whose
+    first element is the vector's largest (and meets a query element of 0) and whose second
+    is code c scores exactly c * scale; the values' columns run through the codes."""
+    codes = [c for c in range(256) if c & 0x7f != 0x7f]
+    n = len(codes)
+    dec, ci, table, slots, g = make(1, [n], hq=1, hkv=1, d=d, cache=FP8, out=torch.float32, seed=21)
+    val = torch.tensor(codes, dtype=torch.uint8, device="cuda").view(FP8).float()
+    k = torch.zeros(n, 1, d, device="cuda")
+    v = torch.zeros(n, 1, d, device="cuda")
+    k[:, 0, 0] = 448.0
+    k[:, 0, 1] = val
+    v[:, 0, 0] = 448.0
+    for c in range(1, d):
+        v[:, 0, c] = val.roll(c)
+    dec.slot_len.zero_()
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    dec.append(k.bfloat16(), v.bfloat16(), ci, cu_tokens=cu)
+    dec.advance(ci, cu_tokens=cu)
+    p = torch.from_numpy(table[slots[0]][np.arange(n) // 16].astype(np.int64)).cuda()
+    o = torch.arange(n, device="cuda") % 16
+    assert torch.equal(dec.k_cache.view(torch.uint8)[p, 0, o, 1].cpu(), torch.tensor(codes, dtype=torch.uint8))
+    for t in range(n):                                  # one token at a time: its value, exactly
+        if t % 7:
+            continue
+        one = torch.zeros(1, 1, 1, d, device="cuda", dtype=torch.bfloat16)
+        dec.slot_len[slots[0]] = t + 1
+        dec.window = 1
+        out, lse = dec.decode(one, ci, appended=False, with_lse=True)
+        torch.cuda.synchronize()
+        assert float((out[0, 0, 0] - v[t, 0]).abs().max()) <= 2.0 ** -20 * 448
+        assert torch.all(((out[0, 0, 0] - v[t, 0]).abs() <= 2.0 ** -20 * v[t, 0].abs()))
+        one[..., 1] = 1.0                               # its score: c * scale / sqrt(d)
+        out, lse = dec.decode(one, ci, appended=False, with_lse=True)
+        torch.cuda.synchronize()
+        want = float(val[t]) * dec.scale
+        assert abs(float(lse[0, 0, 0]) - want) <= 2.0 ** -19 * abs(want) + 2e-6
