@@ -35,13 +35,17 @@ namespace rssm {
 namespace attn {
 
 constexpr int kTok = 16;       // tokens per tile: the smallest page
-constexpr int kMaxWarps = 16;   // per CTA
+constexpr int kMaxWarps = 8;    // per CTA
+constexpr int kMaxCtas = 256;   // more than the SMs of any machine the library runs on
 constexpr int kMaxRows = 1024;  // rows per launch (prefix sums in shared memory)
-constexpr int kCumBytes = 5120;  // kMaxRows + 1 of them, up to the stages' alignment
+constexpr int kRowBytes = 13312;  // prefix sums, lengths and slots of kMaxRows rows, up to the
+                                  // stages' alignment
 constexpr int kMaxStages = 8;   // per group
-// A range shorter than this is not cut further: the partial results of a cut cost about as
-// much as these tiles.
-constexpr int kMinTiles = 4;
+// Tiles that each group of a CTA gets at least before another CTA joins in.
+constexpr int kMinTiles = 2;
+// Longest (row, head), in tiles, up to which no CTA shares one. Meeting in global memory
+// costs a call some 6 us; an uneven cut costs at most this many tiles over a CTA's groups.
+constexpr int kWholeTiles = 48;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // m follows the largest score once it is this far behind (log2 units)
@@ -59,7 +63,7 @@ struct DecArgs {
     float* lse;
     int32_t* dev_err;
     float* part;       // [2 x CTAs][M][D] partial results of CTAs, then of groups
-    float* part_ml;    // [2 x CTAs + groups][M][2]
+    float* part_ml;    // [2 x CTAs][M][2]
     int32_t* counters; // [CTAs]
     float qscale;      // scale * log2 e
     int batch, T, G, hq, hkv, ps_log2, num_pages, max_pages, num_slots, window, appended;
@@ -149,22 +153,12 @@ __device__ __forceinline__ RowSpan row_span(const DecArgs& a, int len) {
     return s;
 }
 
-// Length of row b's slot, or -1 for a row that is skipped. `flag`: this thread reports.
-__device__ __forceinline__ int row_len(const DecArgs& a, int b, bool flag) {
-    const int s = a.ci[b];
-    if (s < 0) return -1;
-    if (s >= a.num_slots) {
-        if (flag) set_dev_err(a.dev_err, RSSM_DEVERR_SLOT);
-        return -1;
-    }
-    const int len = a.slot_len[s];
-    const long cap = (long)a.max_pages << a.ps_log2;
-    if (len < 0 || (long)len + (a.appended ? a.T : 0) > cap) {
-        if (flag) set_dev_err(a.dev_err, RSSM_DEVERR_CURSOR);
-        return -1;
-    }
-    return len;
-}
+// The call's rows in shared memory.
+struct Rows {
+    uint32_t* cum;  // [batch + 1] tiles of the rows before
+    int* len;       // committed tokens; -1: the row is skipped
+    int* slot;
+};
 
 // Where one tile lies: row, head, first position, row of its first token in the cache
 // matrix (-1: its page is out of range).
@@ -172,25 +166,26 @@ struct Tile {
     int b, h, pos, y;
 };
 
-// The tile list (fewer than 2^31 tiles) cut into ranges, one per worker (group of warps).
-struct Ranges {
-    uint32_t total, base, rem;  // a range has base tiles, the first rem of them one more
-    int per_cta;                // workers of a CTA
-    int workers;
+// The tile list (fewer than 2^31 tiles) cut into the CTAs' ranges. Even cuts share (row,
+// head)s between CTAs, whose results then meet in global memory; where every (row, head)
+// is short, the cuts move up to the next (row, head) instead.
+struct Cuts {
+    uint32_t total, base, rem;  // an even range has base tiles, the first rem of them one more
+    int ctas;                   // that have a range
 };
-__device__ __forceinline__ uint32_t range_start(const Ranges& r, uint32_t w) {
-    return w * r.base + min(w, r.rem);
+__device__ __forceinline__ uint32_t even_cut(const Cuts& r, uint32_t c) {
+    return c * r.base + min(c, r.rem);
 }
-// The worker whose range holds tile t.
-__device__ __forceinline__ uint32_t worker_of(const Ranges& r, uint32_t t) {
+// The CTA whose even range holds tile t.
+__device__ __forceinline__ int cta_of(const Cuts& r, uint32_t t) {
     const uint32_t cut = r.rem * (r.base + 1);
-    return t < cut ? t / (r.base + 1) : r.rem + (t - cut) / r.base;
+    return (int)(t < cut ? t / (r.base + 1) : r.rem + (t - cut) / r.base);
 }
 
 // The whole warp's bounded wait for phase `parity` of `bar`; false, with the CTA's abort
 // flag set, when it ran out on any lane or another warp had given up.
-__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                         int32_t* dev_err) {
+__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                       int32_t* dev_err) {
     const int w = mbar_wait_abortable(bar, parity, RSSM_WAIT_NS, abort);
     if (__all_sync(0xffffffffu, w > 0)) return true;
     if (w == 0) {
@@ -199,6 +194,11 @@ __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatil
     }
     __syncwarp();
     return false;
+}
+__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                         int32_t* dev_err) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return wait_long(bar, parity, abort, dev_err);
 }
 
 // Last row b with cum[b] <= i (rows without tiles are passed over).
@@ -213,20 +213,27 @@ __device__ __forceinline__ int find_row(const uint32_t* cum, int batch, uint32_t
 }
 
 // Row and head of tile t, and its number among the (row, head)'s tiles.
-__device__ __forceinline__ int find_tile(const DecArgs& a, const uint32_t* cum, uint32_t t, Tile& x) {
-    x.b = find_row(cum, a.batch, t / (uint32_t)a.hkv);
+__device__ __noinline__ int find_tile(const DecArgs& a, const uint32_t* cum, uint32_t t, Tile& x) {
+    x.b = a.batch == 1 ? 0 : find_row(cum, a.batch, t / (uint32_t)a.hkv);
     const uint32_t nt = cum[x.b + 1] - cum[x.b];
     const uint32_t in_row = t - cum[x.b] * (uint32_t)a.hkv;
     x.h = (int)(in_row / nt);
     return (int)(in_row - (uint32_t)x.h * nt);
 }
 
-__device__ __noinline__ Tile locate_tile(const DecArgs& a, const uint32_t* cum, uint32_t t) {
+// The first tile from t on that begins a (row, head).
+__device__ __noinline__ uint32_t next_head(const DecArgs& a, const uint32_t* cum, uint32_t t) {
+    if (t >= cum[a.batch] * (uint32_t)a.hkv) return t;
     Tile x;
-    const int i = find_tile(a, cum, t, x);
-    const int s = a.ci[x.b];
-    x.pos = (row_span(a, a.slot_len[s]).first + i) * kTok;
-    const int page = a.page_table[(long)s * a.max_pages + (x.pos >> a.ps_log2)];
+    const uint32_t at = find_tile(a, cum, t, x);
+    return at == 0 ? t : t - at + cum[x.b + 1] - cum[x.b];
+}
+
+__device__ __noinline__ Tile locate_tile(const DecArgs& a, const Rows& rows, uint32_t t) {
+    Tile x;
+    const int i = find_tile(a, rows.cum, t, x);
+    x.pos = (row_span(a, rows.len[x.b]).first + i) * kTok;
+    const int page = __ldg(a.page_table + (long)rows.slot[x.b] * a.max_pages + (x.pos >> a.ps_log2));
     if (page < 0 || page >= a.num_pages) {
         set_dev_err(a.dev_err, RSSM_DEVERR_PAGE);
         x.y = -1;
@@ -237,18 +244,46 @@ __device__ __noinline__ Tile locate_tile(const DecArgs& a, const uint32_t* cum, 
 }
 
 // o and lse of query row r of (b, h): elements d, d + 1.
-__device__ __forceinline__ long out_row(const DecArgs& a, int b, int h, int r) {
+__device__ __noinline__ long out_row(const DecArgs& a, int b, int h, int r) {
     const int j = r / a.G;
     return ((long)b * a.T + j) * a.hq + h * a.G + (r - j * a.G);
 }
 
+// A partial result of one query over four columns: (m, l) and O. Adding one rescales to
+// the larger m; a sum's order is that of the adds.
+struct Partial {
+    float2 ml = make_float2(-INFINITY, 0.f);
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    __device__ __forceinline__ void add(float2 bl, float4 x) {
+        const float top = fmaxf(ml.x, bl.x), base = top == -INFINITY ? 0.f : top;
+        const float f = exp2_fast(ml.x - base), g = exp2_fast(bl.x - base);
+        ml = make_float2(top, ml.y * f + bl.y * g);
+        v.x = v.x * f + x.x * g;
+        v.y = v.y * f + x.y * g;
+        v.z = v.z * f + x.z * g;
+        v.w = v.w * f + x.w * g;
+    }
+    // o at element e: O / l, zeros where nothing was seen; lse of output row r.
+    __device__ __forceinline__ void store(const DecArgs& a, long r, long e, bool with_lse) const {
+        const bool none = ml.y == 0.f;
+        const float inv = none ? 0.f : 1.f / ml.y;
+        const float y[4] = {none ? 0.f : v.x * inv, none ? 0.f : v.y * inv, none ? 0.f : v.z * inv,
+                            none ? 0.f : v.w * inv};
+        if (a.obf)
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + e) =
+                make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+        else
+            *reinterpret_cast<float4*>(static_cast<float*>(a.o) + e) = make_float4(y[0], y[1], y[2], y[3]);
+        if (with_lse && a.lse) a.lse[r] = none ? -INFINITY : (ml.x + log2f(ml.y)) * kLn2;
+    }
+};
+constexpr int kJoin = 8;  // partial results whose loads a thread has in flight
+
 // A run: the consecutive records (partial results of groups) of one (row, head) in a CTA.
 struct Run {
     int b, h;
-    int rec0, rec1;  // records [rec0, rec1): 2 g: group g's head, 2 g + 1: its tail
-    int whole;       // the CTA has all of its tiles
-    int slot;        // else: 2 CTA + (0: began in an earlier CTA, 1: begins here)
-    int cta0, cta1;  // first and last CTA
+    int rec0, rec1;  // its first record and one past its last (2 g: group g's head, 2 g + 1: its tail)
+    int cta0, cta1;  // first and last CTA that has tiles of it
 };
 
 // D: head dim, E4M3: 8-bit cache, AF32: float32 activations. The products' operands:
@@ -260,8 +295,9 @@ struct Run {
 //     power of two at its largest element. One part carries all 8 bits of a bf16 query but
 //     11 of a weight, whose error shows in a small output of large terms: two parts, and
 //     two of each for float32 activations.
-template <int D, bool E4M3, bool AF32, int NQ>
+template <int D, bool E4M3, bool AF32, int NQ, int TILES>
 struct Cfg {
+    static constexpr int TP = TILES;                 // tiles of a step
     // Warps of a CTA. The registers of 16 warps (128 each) hold 8 queries' accumulators;
     // with a bf16 cache 16 rings would leave one stage each.
     static constexpr int WARPS = 8;
@@ -304,11 +340,11 @@ __device__ __forceinline__ void split2(float v0, float v1, uint32_t* out) {
     }
 }
 
-template <int D, bool E4M3, bool AF32, int NQ>
-__global__ void __launch_bounds__((Cfg<D, E4M3, AF32, NQ>::WARPS * 32), 1)
-    decode_kernel(const DecArgs a, const __grid_constant__ CUtensorMap kmap,
+template <int D, bool E4M3, bool AF32, int NQ, int TP>
+__global__ void __launch_bounds__((Cfg<D, E4M3, AF32, NQ, TP>::WARPS * 32), 1)
+    decode_kernel(const __grid_constant__ DecArgs a, const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap) {
-    using C = Cfg<D, E4M3, AF32, NQ>;
+    using C = Cfg<D, E4M3, AF32, NQ, TP>;
     constexpr int kWarps = C::WARPS, kDecThreads = kWarps * 32;
     extern __shared__ unsigned char smem_raw[];
     // 128-byte swizzled boxes want their base on 1024 bytes
@@ -318,21 +354,25 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, NQ>::WARPS * 32), 1)
     const int group = warp / a.MT, mt = warp - group * a.MT;
     const int stages = a.stages;
 
-    // shared memory: prefix sums, stages (at the end the tails lie over them and what
-    // follows), scales, tiles, barriers
-    uint32_t* cum = reinterpret_cast<uint32_t*>(smem);
-    unsigned char* st_kv = smem + kCumBytes;
+    // shared memory: the rows, stages (at the end the tails lie over them and what follows),
+    // scales, tiles, barriers
+    Rows rows;
+    rows.cum = reinterpret_cast<uint32_t*>(smem);
+    rows.len = reinterpret_cast<int*>(smem) + kMaxRows + 4;
+    rows.slot = rows.len + kMaxRows;
+    uint32_t* const cum = rows.cum;
+    unsigned char* st_kv = smem + kRowBytes;
     const int nst = stages * ngroups;
     float* st_scale = reinterpret_cast<float*>(st_kv + (size_t)nst * C::STAGE);
     int2* st_tile = reinterpret_cast<int2*>(st_kv + (size_t)nst * (C::STAGE + C::AUX));
     uint64_t* full = reinterpret_cast<uint64_t*>(st_tile + nst);
     uint64_t* empty = full + nst;
-    __shared__ uint32_t scan[kWarps];
+    __shared__ uint2 scan[kWarps];  // tiles and longest row of the warps' rows
     __shared__ int abort_flag;
     __shared__ int rec_b[2 * kWarps], rec_h[2 * kWarps];  // records; b < 0: none
     __shared__ Run runs[2 * kWarps];
     __shared__ int nruns, last_flag[2];
-    __shared__ float tail_ml[kWarps * 8 * NQ][2];
+    __shared__ float2 rec_ml[2 * kWarps * 8 * NQ];  // [record][M] m and l
 
     if (tid < nst) {
         mbar_init(&full[tid], 1);
@@ -345,31 +385,52 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, NQ>::WARPS * 32), 1)
         asm volatile("prefetch.tensormap [%0];" ::"l"(&vmap) : "memory");
     }
     if (tid < 2 * kWarps) rec_b[tid] = -1;
+    if (tid == 0) runs[0].cta0 = runs[0].cta1 = 0;
 
     // ------------------------------------------------------- the call's tile list
+    uint32_t longest = 0;  // tiles of the longest (row, head)
     {
         constexpr int R = kMaxRows / kDecThreads;
         uint32_t n[R], sum = 0;
+        int slot[R], len[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) slot[i] = tid * R + i < a.batch ? a.ci[tid * R + i] : -1;
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            len[i] = slot[i] >= 0 && slot[i] < a.num_slots ? a.slot_len[slot[i]] : -1;
+        const long cap = ((long)a.max_pages << a.ps_log2) - (a.appended ? a.T : 0);
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            const int b = tid * R + i;
-            n[i] = 0;
-            if (b < a.batch) {
-                const int len = row_len(a, b, blockIdx.x == 0);
-                n[i] = len < 0 ? 0 : row_span(a, len).tiles;
+            if (slot[i] >= a.num_slots) {
+                if (blockIdx.x == 0) set_dev_err(a.dev_err, RSSM_DEVERR_SLOT);
+            } else if (slot[i] >= 0 && (len[i] < 0 || len[i] > cap)) {
+                if (blockIdx.x == 0) set_dev_err(a.dev_err, RSSM_DEVERR_CURSOR);
+                len[i] = -1;
+            }
+            n[i] = len[i] < 0 ? 0 : row_span(a, len[i]).tiles;
+            if (tid * R + i < a.batch) {
+                rows.len[tid * R + i] = len[i];
+                rows.slot[tid * R + i] = slot[i];
             }
             sum += n[i];
         }
-        uint32_t inc = sum;
+        uint32_t inc = sum, top = 0;
+#pragma unroll
+        for (int i = 0; i < R; ++i) top = max(top, n[i]);
+        top = __reduce_max_sync(0xffffffffu, top);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const uint32_t v = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc += v;
         }
-        if (lane == 31) scan[warp] = inc;
+        if (lane == 31) scan[warp] = make_uint2(inc, top);
         __syncthreads();
         uint32_t before = inc - sum;
-        for (int w = 0; w < warp; ++w) before += scan[w];
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) before += scan[w].x;
+            longest = max(longest, scan[w].y);
+        }
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             const int b = tid * R + i;
@@ -380,28 +441,38 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, NQ>::WARPS * 32), 1)
         __syncthreads();
     }
     // rows that see nothing have no tiles: their outputs are written here
+#pragma unroll 1
     for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
-        if (cum[b + 1] != cum[b] || row_len(a, b, false) < 0) continue;
+        if (cum[b + 1] != cum[b] || rows.len[b] < 0) continue;
         const long o0 = (long)b * a.T * a.hq;
         const int no = a.T * a.hq;
+#pragma unroll 1
         for (int e = tid; e < no * D; e += kDecThreads) store1(a.o, o0 * D + e, a.obf, 0.f);
         if (a.lse)
+#pragma unroll 1
             for (int e = tid; e < no; e += kDecThreads) a.lse[o0 + e] = -INFINITY;
     }
-    Ranges rg;
+    Cuts rg;
     rg.total = cum[a.batch] * (uint32_t)a.hkv;
     if (rg.total == 0) return;
+    uint32_t c0, c1;  // this CTA's range
     {
-        const uint32_t want = (rg.total + kMinTiles - 1) / kMinTiles;
-        const uint32_t k = (want + gridDim.x - 1) / gridDim.x;
-        rg.per_cta = (int)min(k, (uint32_t)ngroups);
-        rg.workers = (int)min(gridDim.x * (uint32_t)rg.per_cta, want);
-        rg.base = rg.total / (uint32_t)rg.workers;
-        rg.rem = rg.total - rg.base * (uint32_t)rg.workers;
+        // short (row, head)s: as many CTAs as there may be (row, head)s
+        const uint32_t least = longest <= kWholeTiles ? min((uint32_t)kMinTiles * ngroups, longest)
+                                                      : (uint32_t)kMinTiles * ngroups;
+        rg.ctas = (int)min(gridDim.x, (rg.total + least - 1) / least);
+        rg.base = rg.total / (uint32_t)rg.ctas;
+        rg.rem = rg.total - rg.base * (uint32_t)rg.ctas;
+        if ((int)blockIdx.x >= rg.ctas) return;
+        c0 = even_cut(rg, blockIdx.x);
+        c1 = even_cut(rg, blockIdx.x + 1);
+        if (longest <= kWholeTiles) {
+            c0 = next_head(a, cum, c0);
+            c1 = next_head(a, cum, c1);
+            if (c0 >= c1) return;
+        }
     }
-    const int w0 = blockIdx.x * rg.per_cta;  // this CTA's first worker
-    const int nw = min(rg.per_cta, rg.workers - w0);
-    if (nw <= 0) return;
+    const uint32_t gbase = (c1 - c0) / (uint32_t)ngroups, grem = (c1 - c0) - gbase * (uint32_t)ngroups;
 
     // ------------------------------------------------------- stream the range
     // Lane layout of the products: n = lane / 4 numbers S^T's tokens (n and n + 8) and O^T's
@@ -411,9 +482,9 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, NQ>::WARPS * 32), 1)
     const int n8 = lane >> 2, qd = lane & 3;
     const int q0 = mt * 8 * NQ;  // this warp's first query
 
-    if (group < nw) {
-        const uint32_t t0 = range_start(rg, w0 + group), t1 = range_start(rg, w0 + group + 1);
-        const int ntile = (int)(t1 - t0);
+    const uint32_t t0 = c0 + group * gbase + min((uint32_t)group, grem);
+    const int ntile = group < ngroups ? (int)(gbase + (group < (int)grem ? 1 : 0)) : 0;
+    if (ntile > 0) {
         const bool leader = mt == 0;
         const uint64_t pol = policy_evict_first();
         unsigned char* kv = st_kv + (size_t)group * stages * C::STAGE;
@@ -422,18 +493,13 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, NQ>::WARPS * 32), 1)
         uint64_t* fb = full + group * stages;
         uint64_t* eb = empty + group * stages;
 
-        // tiles 32 w .. 32 w + 31 of the range sit one per lane; the next 32 are looked up
-        // while these are issued
-        Tile cur{}, nxt{};
+        // the next 32 tiles of the range are looked up at once, one per lane
+        Tile cur{};
         int sent = 0, sent_s = 0;  // tiles issued, and the stage of the next
         // issue the range's next tile into its stage (leader warp only)
         auto issue = [&]() {
             if (sent >= ntile) return;
-            if ((sent & 31) == 0) {
-                if (sent == 0 && lane < ntile) nxt = locate_tile(a, cum, t0 + lane);
-                cur = nxt;
-                if (sent + 32 + lane < ntile) nxt = locate_tile(a, cum, t0 + sent + 32 + lane);
-            }
+            if ((sent & 31) == 0 && sent + lane < ntile) cur = locate_tile(a, rows, t0 + sent + lane);
             if (lane == (sent & 31)) {
                 unsigned char* dst = kv + (size_t)sent_s * C::STAGE;
                 tl[sent_s] = make_int2(cur.pos, cur.y);
@@ -458,8 +524,8 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, NQ>::WARPS * 32), 1)
             ++sent;
             if (++sent_s == stages) sent_s = 0;
         };
-        // A stage is refilled one tile late when several warps read it, so that the
-        // leader seldom waits for them.
+        // A stage is refilled a step late when several warps read it, so that the leader
+        // seldom waits for them.
         if (leader)
 #pragma unroll 1
             for (int i = 0; i < stages; ++i) issue();
@@ -473,10 +539,10 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, NQ>::WARPS * 32), 1)
         bool begun = false;      // its tiles began before this range
         int next = 0;            // tile of the range at which it ends
         int s = 0, phase = 0;    // stage and phase of tile i
-        int free_s = 0, free_phase = 0;
+        int hand_s = 0, free_s = 0, free_phase = 0;
 
 #pragma unroll 1
-        for (int i = 0;; ++i) {
+        for (int i = 0;;) {
             if (i == next || i == ntile) {
                 if (i > 0) {
                     // The result of the current (row, head): out when all of its tiles lie in this
@@ -543,7 +609,7 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, NQ>::WARPS * 32), 1)
                             }
                         }
                     } else if (!tail) {
-                        const long slot = 2L * gridDim.x + w0 + group;
+                        const long slot = 2L * gridDim.x + (int)blockIdx.x * kWarps + group;
 #pragma unroll
                         for (int q = 0; q < NQ; ++q)
 #pragma unroll
@@ -556,10 +622,7 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, NQ>::WARPS * 32), 1)
                                     dst[C::col(c, n8, 0)] = o[c][q][x];
                                     dst[C::col(c, n8, 1)] = o[c][q][2 + x];
                                 }
-                                if (n8 == 0) {
-                                    a.part_ml[(slot * a.M + r) * 2] = m[q][x];
-                                    a.part_ml[(slot * a.M + r) * 2 + 1] = l[q][x];
-                                }
+                                if (n8 == 0) rec_ml[2 * group * a.M + r] = make_float2(m[q][x], l[q][x]);
                             }
                     }
                 }
@@ -574,7 +637,7 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, NQ>::WARPS * 32), 1)
                     begun = at > 0;
                     next = i + (int)(cum[cb + 1] - cum[cb]) - at;
                 }
-                const int len = a.slot_len[a.ci[cb]];
+                const int len = rows.len[cb];
                 const int app = a.appended ? 1 : 0;
                 n_min = len + app;
                 n_max = len + (app ? a.T : 0);
@@ -655,90 +718,115 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, NQ>::WARPS * 32), 1)
                 }
             }
 
-            if (!wait_all(&fb[s], phase, &abort_flag, a.dev_err)) break;
-            const int2 t = tl[s];
-            const int pos = t.x;
-            if (t.y >= 0 && works) {
-                const unsigned char* vt = kv + (size_t)s * C::STAGE + C::KB;
-                const uint32_t kbase = smem_addr(kv + (size_t)s * C::STAGE), vbase = kbase + C::KB;
+            // the step's tiles: TP, or what the (row, head) or the range has left
+            const int steps = min(C::TP, min(next, ntile) - i);
+            int2 t[C::TP];
+            int st[C::TP];
+            bool ok = true;
+#pragma unroll
+            for (int u = 0; u < C::TP; ++u) {
+                st[u] = s;
+                t[u] = make_int2(0, -1);
+                if (u < steps) {
+                    ok = ok && wait_all(&fb[s], phase, &abort_flag, a.dev_err);
+                    t[u] = tl[s];
+                    if (++s == stages) s = 0, phase ^= 1;
+                }
+            }
+            if (!ok) break;
+            bool some = t[0].y >= 0;
+            if (C::TP > 1) some = some || t[C::TP - 1].y >= 0;
+            if (some && works) {
                 const int lr = lane & 7, lm = lane >> 3;
                 // ------------------------------------------------ S^T = K Q^T
-                float sa[2][NQ][4];
+                constexpr int SA = C::TP == 1 ? 2 : 1;  // one tile: two chains of sums
+                float sa[C::TP][SA][NQ][4];
 #pragma unroll
-                for (int q = 0; q < NQ; ++q)
+                for (int u = 0; u < C::TP; ++u)
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) sa[0][q][x] = sa[1][q][x] = 0.f;
-                if (E4M3) {
+                    for (int q = 0; q < NQ; ++q)
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; kk += 2) {
-                        uint32_t r[4], f[2][4];
-                        ldsm4(kbase + tile_off<C::ROWB>((lm & 1) * 8 + lr, kk + (lm >> 1)), r);
+                        for (int x = 0; x < 4; ++x) sa[u][0][q][x] = sa[u][SA - 1][q][x] = 0.f;
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) e4m3x4_to_f16(r[x], f[x >> 1][x & 1], f[x >> 1][2 + (x & 1)]);
+                for (int kk = 0; kk < D / 16; kk += E4M3 ? 2 : 1)
 #pragma unroll
-                        for (int p = 0; p < C::QP; ++p)
-#pragma unroll
-                            for (int q = 0; q < NQ; ++q) {
-                                mma16816<true>(sa[0][q], f[0], qf[kk][q][p][0], qf[kk][q][p][1]);
-                                mma16816<true>(sa[1][q], f[1], qf[kk + 1][q][p][0], qf[kk + 1][q][p][1]);
-                            }
-                    }
-                } else {
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
+                    for (int u = 0; u < C::TP; ++u) {
+                        const uint32_t kbase = smem_addr(kv + (size_t)st[u] * C::STAGE);
                         uint32_t r[4];
-                        ldsm4(kbase + tile_off<C::ROWB>((lm & 1) * 8 + lr, 2 * kk + (lm >> 1)), r);
+                        if (E4M3) {
+                            uint32_t f[2][4];
+                            ldsm4(kbase + tile_off<C::ROWB>((lm & 1) * 8 + lr, kk + (lm >> 1)), r);
 #pragma unroll
-                        for (int p = 0; p < C::QP; ++p)
+                            for (int x = 0; x < 4; ++x)
+                                e4m3x4_to_f16(r[x], f[x >> 1][x & 1], f[x >> 1][2 + (x & 1)]);
 #pragma unroll
-                            for (int q = 0; q < NQ; ++q)
-                                mma16816<false>(sa[kk & 1][q], r, qf[kk][q][p][0], qf[kk][q][p][1]);
+                            for (int p = 0; p < C::QP; ++p)
+#pragma unroll
+                                for (int q = 0; q < NQ; ++q) {
+                                    mma16816<true>(sa[u][0][q], f[0], qf[kk][q][p][0], qf[kk][q][p][1]);
+                                    mma16816<true>(sa[u][SA - 1][q], f[1], qf[kk + 1][q][p][0], qf[kk + 1][q][p][1]);
+                                }
+                        } else {
+                            ldsm4(kbase + tile_off<C::ROWB>((lm & 1) * 8 + lr, 2 * kk + (lm >> 1)), r);
+#pragma unroll
+                            for (int p = 0; p < C::QP; ++p)
+#pragma unroll
+                                for (int q = 0; q < NQ; ++q)
+                                    mma16816<false>(sa[u][SA == 2 ? kk & 1 : 0][q], r, qf[kk][q][p][0], qf[kk][q][p][1]);
+                        }
                     }
-                }
                 // ------------------------------------------------ softmax
                 // Scores in log2 units. With an 8-bit cache a token's value scale joins its
                 // weight as log2(scale) in the exponent: m bounds those sums, the weights stay
                 // in f16's range, and l, which wants the scores alone, divides it out again.
-                float p[NQ][4];
-                float ks[2] = {1.f, 1.f}, lv[2] = {0.f, 0.f}, iv[2] = {1.f, 1.f};
-                if (E4M3) {
-                    const float* ts = sc + s * 2 * kTok + n8;
+                float p[C::TP][NQ][4], iv[C::TP][2];
+                bool edge[C::TP], grow = false;
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        ks[x] = ts[8 * x];
-                        float v = ts[kTok + 8 * x];
-                        if (v < 1.1754944e-38f) v = 1.1754944e-38f;  // (a NaN stays)
-                        lv[x] = log2_fast(v);
-                        iv[x] = exp2_fast(-lv[x]);
-                    }
-                }
-                const bool edge = pos + kTok > n_min || pos < b_max;
-                bool grow = false;
+                for (int u = 0; u < C::TP; ++u) {
+                    const int pos = t[u].x;
+                    float ks[2] = {1.f, 1.f}, lv[2] = {0.f, 0.f};
+                    if (E4M3) {
+                        const float* ts = sc + st[u] * 2 * kTok + n8;
 #pragma unroll
-                for (int q = 0; q < NQ; ++q)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        float f = (sa[0][q][x] + sa[1][q][x]) * rs[q][x & 1];
-                        if (E4M3) f = f * ks[x >> 1] + lv[x >> 1];
-                        if (edge) {
-                            const int tok = pos + n8 + 8 * (x >> 1);
-                            // whatever the cache holds there
-                            if (tok >= end[q][x & 1] || tok < beg[q][x & 1]) f = -INFINITY;
+                        for (int x = 0; x < 2; ++x) {
+                            ks[x] = ts[8 * x];
+                            float v = ts[kTok + 8 * x];
+                            if (v < 1.1754944e-38f) v = 1.1754944e-38f;  // (a NaN stays)
+                            lv[x] = log2_fast(v);
+                            iv[u][x] = exp2_fast(-lv[x]);
                         }
-                        p[q][x] = f;
-                        grow |= f > m[q][x & 1] + kSlack;
                     }
+                    // a tile that is not there (or has no page) is all hidden
+                    edge[u] = t[u].y < 0 || pos + kTok > n_min || pos < b_max;
+#pragma unroll
+                    for (int q = 0; q < NQ; ++q)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            float f = SA == 2 ? sa[u][0][q][x] + sa[u][SA - 1][q][x] : sa[u][0][q][x];
+                            f *= rs[q][x & 1];
+                            if (E4M3) f = f * ks[x >> 1] + lv[x >> 1];
+                            if (edge[u]) {
+                                const int tok = pos + n8 + 8 * (x >> 1);
+                                // whatever the cache holds there
+                                if (tok >= end[q][x & 1] || tok < beg[q][x & 1] || t[u].y < 0) f = -INFINITY;
+                            }
+                            p[u][q][x] = f;
+                            grow |= f > m[q][x & 1] + kSlack;
+                        }
+                }
                 if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
                     for (int q = 0; q < NQ; ++q)
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
-                            float t = fmaxf(p[q][x], p[q][2 + x]);
+                            float top = fmaxf(p[0][q][x], p[0][q][2 + x]);
+                            if (C::TP > 1) top = fmaxf(top, fmaxf(p[C::TP - 1][q][x], p[C::TP - 1][q][2 + x]));
 #pragma unroll
-                            for (int w = 4; w < 32; w <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, w));
-                            t = fmaxf(t, m[q][x]);
-                            const float f = t == m[q][x] ? 1.f : exp2_fast(m[q][x] - t);
-                            m[q][x] = t;
+                            for (int w = 4; w < 32; w <<= 1)
+                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+                            top = fmaxf(top, m[q][x]);
+                            const float f = top == m[q][x] ? 1.f : exp2_fast(m[q][x] - top);
+                            m[q][x] = top;
                             l[q][x] *= f;
 #pragma unroll
                             for (int c = 0; c < C::DB; ++c) {
@@ -747,45 +835,56 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, NQ>::WARPS * 32), 1)
                             }
                         }
                 }
-                uint32_t pf[NQ][C::PP][2];
+                uint32_t pf[C::TP][NQ][C::PP][2];
 #pragma unroll
-                for (int q = 0; q < NQ; ++q) {
-                    // a query that has seen only -infinity keeps weights of zero
+                for (int u = 0; u < C::TP; ++u)
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const float c = m[q][x & 1] == -INFINITY ? 0.f : m[q][x & 1];
-                        p[q][x] = exp2_fast(p[q][x] - c);
-                        float w = p[q][x];
-                        if (E4M3) {
-                            w *= iv[x >> 1];
-                            // a hidden token's scale may be anything
-                            if (edge && p[q][x] == 0.f) w = 0.f;
+                    for (int q = 0; q < NQ; ++q) {
+                        // a query that has seen only -infinity keeps weights of zero
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const float c = m[q][x & 1] == -INFINITY ? 0.f : m[q][x & 1];
+                            float w = exp2_fast(p[u][q][x] - c);
+                            p[u][q][x] = w;
+                            if (E4M3) {
+                                w *= iv[u][x >> 1];
+                                // a hidden token's scale may be anything
+                                if (edge[u] && p[u][q][x] == 0.f) w = 0.f;
+                            }
+                            l[q][x & 1] += w;
                         }
-                        l[q][x & 1] += w;
-                    }
-                    uint32_t lo[C::PP], hi[C::PP];
-                    split2<C::PP, E4M3>(p[q][0], p[q][1], lo);
-                    split2<C::PP, E4M3>(p[q][2], p[q][3], hi);
+                        uint32_t lo[C::PP], hi[C::PP];
+                        split2<C::PP, E4M3>(p[u][q][0], p[u][q][1], lo);
+                        split2<C::PP, E4M3>(p[u][q][2], p[u][q][3], hi);
 #pragma unroll
-                    for (int x = 0; x < C::PP; ++x) {
-                        pf[q][x][0] = transpose8(lo[x]);
-                        pf[q][x][1] = transpose8(hi[x]);
+                        for (int x = 0; x < C::PP; ++x) {
+                            pf[u][q][x][0] = transpose8(lo[x]);
+                            pf[u][q][x][1] = transpose8(hi[x]);
+                        }
                     }
-                }
                 // ------------------------------------------------ O^T += V^T P^T
-                bool careful = false;
-                if (edge) {
+                bool careful[C::TP];
+#pragma unroll
+                for (int u = 0; u < C::TP; ++u) {
+                    careful[u] = false;
+                    if (!edge[u]) continue;
                     // A weight of zero does not silence an infinity or a NaN in a value. Tokens
-                    // that no query sees are cleared; if one that only some see is not finite,
-                    // the tile's products run value by value below (8-bit values are finite:
-                    // what is not is marked in the scale, which a hidden score leaves out).
+                    // that no query sees are cleared (a tile that is not there as a whole); if
+                    // one that only some see is not finite, the tile's products run value by
+                    // value below (8-bit values are finite: what is not is marked in the scale,
+                    // which a hidden score leaves out).
+                    const int pos = t[u].x;
+                    unsigned char* vt = kv + (size_t)st[u] * C::STAGE + C::KB;
+                    if (t[u].y < 0) {
+                        careful[u] = true;  // nothing to add
+                        continue;
+                    }
                     if (pos + kTok > n_max || pos < b_min) {
 #pragma unroll 1
                         for (int e = lane; e < kTok * (C::ROWB / 16); e += 32) {
                             const int tok = e / (C::ROWB / 16), c = e % (C::ROWB / 16);
                             if (pos + tok >= n_max || pos + tok < b_min)
-                                *reinterpret_cast<uint4*>(kv + (size_t)s * C::STAGE + C::KB +
-                                                          tile_off<C::ROWB>(tok, c)) = make_uint4(0, 0, 0, 0);
+                                *reinterpret_cast<uint4*>(vt + tile_off<C::ROWB>(tok, c)) = make_uint4(0, 0, 0, 0);
                         }
                         fence_async_smem();  // the stage's next TMA load comes after these stores
                         __syncwarp();
@@ -803,82 +902,94 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, NQ>::WARPS * 32), 1)
                                     odd |= (w[x] & 0x7f80u) == 0x7f80u || (w[x] & 0x7f800000u) == 0x7f800000u;
                             }
                         }
-                        careful = __any_sync(0xffffffffu, odd);
+                        careful[u] = __any_sync(0xffffffffu, odd);
                     }
                 }
-                if (!careful) {
 #pragma unroll
-                    for (int c = 0; c < C::DB; ++c) {
-                        uint32_t f[4];
-                        if (E4M3) {
-                            // a register holds two tokens' codes of columns 2 n, 2 n + 1; paired
-                            // by token they are one k pair of the even and of the odd columns
-                            if (c & 1) continue;
-                            uint32_t r[4], g[4];
-                            ldsm4_t(vbase + tile_off<C::ROWB>((lm & 1) * 8 + lr, c + (lm >> 1)), r);
+                for (int u = 0; u < C::TP; ++u) {
+                    const unsigned char* vt = kv + (size_t)st[u] * C::STAGE + C::KB;
+                    const uint32_t vbase = smem_addr(vt);
+                    if (!careful[u]) {
 #pragma unroll
-                            for (int x = 0; x < 4; ++x) {
-                                uint32_t lo, hi;
-                                e4m3x4_to_f16(r[x], lo, hi);
-                                uint32_t* d = x < 2 ? f : g;
-                                d[2 * (x & 1)] = __byte_perm(lo, hi, 0x5410);
-                                d[2 * (x & 1) + 1] = __byte_perm(lo, hi, 0x7632);
-                            }
+                        for (int c = 0; c < C::DB; ++c) {
+                            uint32_t f[4];
+                            if (E4M3) {
+                                // a register holds two tokens' codes of columns 2 n, 2 n + 1; paired
+                                // by token they are one k pair of the even and of the odd columns
+                                if (c & 1) continue;
+                                uint32_t r[4], g[4];
+                                ldsm4_t(vbase + tile_off<C::ROWB>((lm & 1) * 8 + lr, c + (lm >> 1)), r);
 #pragma unroll
-                            for (int x = 0; x < C::PP; ++x)
-#pragma unroll
-                                for (int q = 0; q < NQ; ++q) {
-                                    mma16816<true>(o[c][q], f, pf[q][x][0], pf[q][x][1]);
-                                    mma16816<true>(o[c + 1][q], g, pf[q][x][0], pf[q][x][1]);
+                                for (int x = 0; x < 4; ++x) {
+                                    uint32_t lo, hi;
+                                    e4m3x4_to_f16(r[x], lo, hi);
+                                    uint32_t* d = x < 2 ? f : g;
+                                    d[2 * (x & 1)] = __byte_perm(lo, hi, 0x5410);
+                                    d[2 * (x & 1) + 1] = __byte_perm(lo, hi, 0x7632);
                                 }
-                        } else {
-                            ldsm4_t(vbase + tile_off<C::ROWB>((lm >> 1) * 8 + lr, 2 * c + (lm & 1)), f);
 #pragma unroll
-                            for (int x = 0; x < C::PP; ++x)
+                                for (int x = 0; x < C::PP; ++x)
 #pragma unroll
-                                for (int q = 0; q < NQ; ++q)
-                                    mma16816<false>(o[c][q], f, pf[q][x][0], pf[q][x][1]);
+                                    for (int q = 0; q < NQ; ++q) {
+                                        mma16816<true>(o[c][q], f, pf[u][q][x][0], pf[u][q][x][1]);
+                                        mma16816<true>(o[c + 1][q], g, pf[u][q][x][0], pf[u][q][x][1]);
+                                    }
+                            } else {
+                                ldsm4_t(vbase + tile_off<C::ROWB>((lm >> 1) * 8 + lr, 2 * c + (lm & 1)), f);
+#pragma unroll
+                                for (int x = 0; x < C::PP; ++x)
+#pragma unroll
+                                    for (int q = 0; q < NQ; ++q)
+                                        mma16816<false>(o[c][q], f, pf[u][q][x][0], pf[u][q][x][1]);
+                            }
                         }
-                    }
-                } else {
+                    } else if (!E4M3 && t[u].y >= 0) {
+                        const int pos = t[u].x;
 #pragma unroll 1
-                    for (int tok = 0; tok < kTok; ++tok) {
-                        const int src = (tok & 7) * 4 + qd;
+                        for (int tok = 0; tok < kTok; ++tok) {
+                            const int src = (tok & 7) * 4 + qd;
 #pragma unroll
-                        for (int q = 0; q < NQ; ++q)
+                            for (int q = 0; q < NQ; ++q)
 #pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                const float w = __shfl_sync(0xffffffffu, tok < 8 ? p[q][x] : p[q][2 + x], src);
-                                if (pos + tok >= end[q][x] || pos + tok < beg[q][x]) continue;
+                                for (int x = 0; x < 2; ++x) {
+                                    const float w = __shfl_sync(0xffffffffu, tok < 8 ? p[u][q][x] : p[u][q][2 + x], src);
+                                    if (pos + tok >= end[q][x] || pos + tok < beg[q][x]) continue;
 #pragma unroll
-                                for (int c = 0; c < C::DB; ++c) {
-                                    const uint16_t* v = reinterpret_cast<const uint16_t*>(
-                                        vt + tile_off<C::ROWB>(tok, 2 * c) + 2 * n8);
-                                    const uint16_t* u = reinterpret_cast<const uint16_t*>(
-                                        vt + tile_off<C::ROWB>(tok, 2 * c + 1) + 2 * n8);
-                                    o[c][q][x] += w * bf16_to_f(*v);
-                                    o[c][q][2 + x] += w * bf16_to_f(*u);
+                                    for (int c = 0; c < C::DB; ++c) {
+                                        const uint16_t* v = reinterpret_cast<const uint16_t*>(
+                                            vt + tile_off<C::ROWB>(tok, 2 * c) + 2 * n8);
+                                        const uint16_t* w2 = reinterpret_cast<const uint16_t*>(
+                                            vt + tile_off<C::ROWB>(tok, 2 * c + 1) + 2 * n8);
+                                        o[c][q][x] += w * bf16_to_f(*v);
+                                        o[c][q][2 + x] += w * bf16_to_f(*w2);
+                                    }
                                 }
-                            }
+                        }
                     }
                 }
             }
-            // ---------------------------------------------------- hand the stage back
+            // ---------------------------------------------------- hand the stages back
             __syncwarp();
-            if (++s == stages) s = 0, phase ^= 1;
-            if (a.MT == 1) {
-                issue();
-            } else {
-                // the tile before this one: its other readers have had a tile's time
-                if (lane == 0) mbar_arrive_plain(&eb[s == 0 ? stages - 1 : s - 1]);
-                if (leader && i > 0) {
-                    if (sent < ntile &&
-                        !wait_all(&eb[free_s], free_phase, &abort_flag, a.dev_err))
+            i += steps;
+#pragma unroll 1
+            for (int u = 0; u < steps; ++u) {
+                if (a.MT == 1) {
+                    issue();
+                    continue;
+                }
+                // of several readers' tiles the one TP before this: they have had a step's time
+                if (lane == 0) mbar_arrive_plain(&eb[hand_s]);
+                if (++hand_s == stages) hand_s = 0;
+                if (leader && i - steps + u >= C::TP) {
+                    if (sent < ntile && !wait_all(&eb[free_s], free_phase, &abort_flag, a.dev_err)) {
+                        ok = false;
                         break;
+                    }
                     issue();
                     if (++free_s == stages) free_s = 0, free_phase ^= 1;
                 }
             }
+            if (!ok) break;
         }
     }
     __syncthreads();
@@ -895,7 +1006,7 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, NQ>::WARPS * 32), 1)
     // ------------------------------------------------------- join the CTA's records
     // Tails into shared memory (the stages are free now).
     float* tail = reinterpret_cast<float*>(st_kv);  // [group][M][TD]
-    if (group < nw && rec_b[2 * group + 1] >= 0) {
+    if (ntile > 0 && rec_b[2 * group + 1] >= 0) {
 #pragma unroll
         for (int q = 0; q < NQ; ++q)
 #pragma unroll
@@ -908,160 +1019,146 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, NQ>::WARPS * 32), 1)
                     dst[C::col(c, n8, 0)] = o[c][q][x];
                     dst[C::col(c, n8, 1)] = o[c][q][2 + x];
                 }
-                if (n8 == 0) {
-                    tail_ml[group * a.M + r][0] = m[q][x];
-                    tail_ml[group * a.M + r][1] = l[q][x];
-                }
+                if (n8 == 0) rec_ml[(2 * group + 1) * a.M + r] = make_float2(m[q][x], l[q][x]);
             }
     }
-    if (tid == 0) {
-        int n = 0;
-        last_flag[0] = last_flag[1] = 0;
-        for (int i = 0; i < 2 * nw; ++i) {
-            if (rec_b[i] < 0) continue;
-            if (n && runs[n - 1].b == rec_b[i] && runs[n - 1].h == rec_h[i]) {
-                runs[n - 1].rec1 = i + 1;
-                continue;
-            }
-            runs[n].b = rec_b[i];
-            runs[n].h = rec_h[i];
-            runs[n].rec0 = i;
-            runs[n].rec1 = i + 1;
-            ++n;
+    // Runs of records: a record whose (row, head) differs from that of the record before it
+    // starts one.
+    if (warp == 0) {
+        const int i = lane;
+        const bool is = i < 2 * ngroups && rec_b[i] >= 0;
+        const unsigned have = __ballot_sync(0xffffffffu, is);
+        const unsigned before = have & ((1u << i) - 1u);
+        const int prev = before ? 31 - __clz(before) : -1;
+        const bool starts = is && (prev < 0 || rec_b[prev] != rec_b[i] || rec_h[prev] != rec_h[i]);
+        const unsigned start = __ballot_sync(0xffffffffu, starts);
+        if (starts) {
+            Run r;
+            r.b = rec_b[i];
+            r.h = rec_h[i];
+            r.rec0 = i;
+            const unsigned later = start & ~((2u << i) - 1u);  // the runs after this one
+            const unsigned mine = have & ~((1u << i) - 1u) & ((later & (0u - later)) - 1u);
+            r.rec1 = 32 - __clz(mine);
+            const uint32_t nt = cum[r.b + 1] - cum[r.b];
+            const uint32_t s0 = cum[r.b] * (uint32_t)a.hkv + (uint32_t)r.h * nt;
+            r.cta0 = r.cta1 = blockIdx.x;
+            if (s0 < c0) r.cta0 = cta_of(rg, s0);
+            if (s0 + nt > c1) r.cta1 = cta_of(rg, s0 + nt - 1);
+            runs[__popc(start & ((1u << i) - 1u))] = r;
         }
-        nruns = n;
+        if (lane == 0) {
+            nruns = __popc(start);
+            last_flag[0] = last_flag[1] = 0;
+        }
     }
-    __syncthreads();
-    if (tid < nruns) {
-        Run& r = runs[tid];
-        const uint32_t nt = cum[r.b + 1] - cum[r.b];
-        const uint32_t s0 = cum[r.b] * (uint32_t)a.hkv + (uint32_t)r.h * nt;
-        r.cta0 = (int)(worker_of(rg, s0) / (uint32_t)rg.per_cta);
-        r.cta1 = (int)(worker_of(rg, s0 + nt - 1) / (uint32_t)rg.per_cta);
-        r.whole = r.cta0 == r.cta1;
-        r.slot = 2 * (int)blockIdx.x + (r.cta0 < (int)blockIdx.x ? 0 : 1);
-    }
-    __threadfence_block();
     __syncthreads();
 
-    // (run, part of its values) pairs over the warps; a lane takes 4 values at a time
-    const int parts = nruns >= kWarps ? 1 : kWarps / max(nruns, 1);
-    for (int item = warp; item < nruns * parts; item += kWarps) {
-        const Run r = runs[item / parts];
-        const int nv = a.M * D / 4, part = item % parts;
-        for (int v = part * 32 + lane; v < nv; v += 32 * parts) {
-            const int row = v / (D / 4), d = (v % (D / 4)) * 4;
-            float m = -INFINITY, l = 0.f;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            // the rows' maxima first, then the weighted sums, in record order
-            for (int i = r.rec0; i < r.rec1; ++i) {
-                if (rec_b[i] < 0) continue;
-                const float* ml = i & 1 ? tail_ml[(i >> 1) * a.M + row]
-                                        : a.part_ml + ((2L * gridDim.x + w0 + (i >> 1)) * a.M + row) * 2;
-                m = fmaxf(m, ml[0]);
-            }
-            const float base = m == -INFINITY ? 0.f : m;
-            for (int i = r.rec0; i < r.rec1; ++i) {
-                if (rec_b[i] < 0) continue;
-                const float* ml;
-                const float* src;
-                if (i & 1) {
-                    ml = tail_ml[(i >> 1) * a.M + row];
-                    src = tail + ((i >> 1) * a.M + row) * C::TD + d;
-                } else {
-                    const long slot = 2L * gridDim.x + w0 + (i >> 1);
-                    ml = a.part_ml + (slot * a.M + row) * 2;
-                    src = a.part + (slot * a.M + row) * D + d;
-                }
-                const float f = exp2_fast(ml[0] - base);
-                const float4 x = *reinterpret_cast<const float4*>(src);
-                l += ml[1] * f;
-                acc.x += x.x * f;
-                acc.y += x.y * f;
-                acc.z += x.z * f;
-                acc.w += x.w * f;
-            }
-            if (r.whole) {
-                const long out = out_row(a, r.b, r.h, row);
-                const float inv = l == 0.f ? 0.f : 1.f / l;
-                float y[4] = {acc.x, acc.y, acc.z, acc.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    store1(a.o, out * D + d + i, a.obf, l == 0.f ? 0.f : y[i] * inv);
-                if (a.lse && d == 0)
-                    a.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-            } else {
-                *reinterpret_cast<float4*>(a.part + ((long)r.slot * a.M + row) * D + d) = acc;
-                if (d == 0) {
-                    a.part_ml[((long)r.slot * a.M + row) * 2] = m;
-                    a.part_ml[((long)r.slot * a.M + row) * 2 + 1] = l;
-                }
-            }
+    // Join each run, 4 columns to a thread. A run is tails (in shared memory) and at most one
+    // head, its last record, in global memory.
+    const int nv = a.M * (D / 4);
+#pragma unroll 1
+    for (int item = tid; item < nruns * nv; item += kDecThreads) {
+        const Run& r = runs[item / nv];
+        const int v = item % nv, row = v / (D / 4), d = (v % (D / 4)) * 4;
+        const int last = r.rec1 - 1;
+        const bool head = !(last & 1);
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (head) {
+            const long slot = 2L * gridDim.x + (int)blockIdx.x * kWarps + (last >> 1);
+            x = *reinterpret_cast<const float4*>(a.part + (slot * a.M + row) * D + d);
+        }
+        Partial acc;
+#pragma unroll 1
+        for (int k = r.rec0 | 1; k < r.rec1; k += 2)
+            if (rec_b[k] >= 0)
+                acc.add(rec_ml[k * a.M + row],
+                        *reinterpret_cast<const float4*>(tail + ((k >> 1) * a.M + row) * C::TD + d));
+        if (head) acc.add(rec_ml[last * a.M + row], x);
+        if (r.cta0 == r.cta1) {
+            const long out = out_row(a, r.b, r.h, row);
+            acc.store(a, out, out * D + d, d == 0);
+        } else {
+            const long slot = 2L * blockIdx.x + (r.cta0 < (int)blockIdx.x ? 0 : 1);
+            *reinterpret_cast<float4*>(a.part + (slot * a.M + row) * D + d) = acc.v;
+            if (d == 0) reinterpret_cast<float2*>(a.part_ml)[slot * a.M + row] = acc.ml;
         }
     }
 
     // ------------------------------------------------------- join the CTAs
+    // Only the first run (begun in an earlier CTA) and the last (which goes on) can be
+    // shared. The counter of a shared (row, head) is its first CTA's.
+    if (runs[0].cta0 == runs[0].cta1 && runs[nruns > 0 ? nruns - 1 : 0].cta0 == runs[nruns > 0 ? nruns - 1 : 0].cta1)
+        return;
     __threadfence();
     __syncthreads();
-    if (tid == 0) {
-        // at most the first run (begun earlier) and the last (goes on) are shared; the
-        // counter is the first CTA's
-        for (int i = 0; i < nruns; ++i) {
-            if (runs[i].whole) continue;
-            const int n = runs[i].cta1 - runs[i].cta0 + 1;
-            if (atomicAdd(&a.counters[runs[i].cta0], 1) == n - 1) {
-                a.counters[runs[i].cta0] = 0;
-                last_flag[i == 0 ? 0 : 1] = i + 1;
-            }
+    if (tid < 2 && (tid == 0 || nruns > 1)) {
+        const Run& r = runs[tid == 0 ? 0 : nruns - 1];
+        if (r.cta0 != r.cta1 && atomicAdd(&a.counters[r.cta0], 1) == r.cta1 - r.cta0) {
+            a.counters[r.cta0] = 0;
+            last_flag[tid] = 1;
         }
         __threadfence();
     }
     __syncthreads();
+    // few values: several threads share one, each a stretch of the partial results
+    const int parts = nv < kDecThreads ? kDecThreads / nv : 1;
+    const int part = parts > 1 ? tid / nv : 0;
+    Partial* jp = reinterpret_cast<Partial*>(st_kv);  // [threads]
 #pragma unroll 1
     for (int f = 0; f < 2; ++f) {
         if (!last_flag[f]) continue;
-        const Run r = runs[last_flag[f] - 1];
-        const int n = r.cta1 - r.cta0 + 1;
-        const int nv = a.M * D / 4;
-        for (int v = tid; v < nv; v += kDecThreads) {
+        const Run r = runs[f == 0 ? 0 : nruns - 1];
+        const int n = r.cta1 - r.cta0 + 1, i0 = n * part / parts, i1 = n * (part + 1) / parts;
+#pragma unroll 1
+        for (int v = parts > 1 ? tid % nv : tid; v < nv && part < parts; v += kDecThreads) {
             const int row = v / (D / 4), d = (v % (D / 4)) * 4;
-            float m = -INFINITY, l = 0.f;
-            for (int i = 0; i < n; ++i) {
-                const long slot = 2L * (r.cta0 + i) + (i == 0 ? 1 : 0);
-                m = fmaxf(m, __ldcg(a.part_ml + (slot * a.M + row) * 2));
-            }
-            const float base = m == -INFINITY ? 0.f : m;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int i = 0; i < n; ++i) {
-                const long slot = 2L * (r.cta0 + i) + (i == 0 ? 1 : 0);
-                const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + slot * a.M + row);
-                const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part + (slot * a.M + row) * D + d));
-                const float w = exp2_fast(ml.x - base);
-                l += ml.y * w;
-                acc.x += x.x * w;
-                acc.y += x.y * w;
-                acc.z += x.z * w;
-                acc.w += x.w * w;
-            }
-            const long out = out_row(a, r.b, r.h, row);
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            float y[4] = {acc.x, acc.y, acc.z, acc.w};
+            Partial acc;
+#pragma unroll 1
+            for (int i = i0; i < i1; i += kJoin) {
+                // the loads of kJoin partial results at once; of the first CTA its last run,
+                // of the others their first
+                float2 ml[kJoin];
+                float4 x[kJoin];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                store1(a.o, out * D + d + i, a.obf, l == 0.f ? 0.f : y[i] * inv);
-            if (a.lse && d == 0)
-                a.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+                for (int k = 0; k < kJoin; ++k) {
+                    ml[k] = make_float2(-INFINITY, 0.f);
+                    x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (i + k < i1) {
+                        const long slot = (2L * (r.cta0 + i + k) + (i + k == 0 ? 1 : 0)) * a.M + row;
+                        ml[k] = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + slot);
+                        x[k] = __ldcg(reinterpret_cast<const float4*>(a.part + slot * D + d));
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < kJoin; ++k) acc.add(ml[k], x[k]);
+            }
+            if (parts > 1) {
+                jp[tid] = acc;
+            } else {
+                const long out = out_row(a, r.b, r.h, row);
+                acc.store(a, out, out * D + d, d == 0);
+            }
+        }
+        if (parts > 1) {
+            __syncthreads();
+            if (tid < nv) {
+                Partial acc = jp[tid];
+#pragma unroll 1
+                for (int i = 1; i < parts; ++i) acc.add(jp[i * nv + tid].ml, jp[i * nv + tid].v);
+                const int row = tid / (D / 4), d = (tid % (D / 4)) * 4;
+                const long out = out_row(a, r.b, r.h, row);
+                acc.store(a, out, out * D + d, d == 0);
+            }
+            __syncthreads();
         }
     }
 }
 
 // ---------------------------------------------------------------- host side
 
-// Workspace: counters (one per CTA), then [2 CTAs + groups] partial results (m, l), then
-// their values. The CTA count is that of the largest machine the library runs on.
-constexpr int kMaxCtas = 256;
-
+// Workspace: counters (one per CTA), then (m, l) of the CTAs' partial results, then the values
+// of these and of the groups' heads.
 struct Workspace {
     size_t ml, part, bytes;
 };
@@ -1075,23 +1172,24 @@ static Workspace workspace_of(const rssm_attn_dims* d) {
     return w;
 }
 
-template <int D, bool E4M3, bool AF32, int NQ>
+template <int D, bool E4M3, bool AF32, int NQ, int TP>
 static int launch_nq(const rssm_attn_dims* d, const rssm_attn_cache* c, DecArgs a, const DeviceInfo& di,
                      cudaStream_t st) {
-    using C = Cfg<D, E4M3, AF32, NQ>;
+    using C = Cfg<D, E4M3, AF32, NQ, TP>;
     const int ngroups = C::WARPS / a.MT;
-    const int fixed = kCumBytes + 1024;
+    const int fixed = kRowBytes + 1024;
     const int per = C::STAGE + C::AUX + 8 + 16;
-    // what the kernel's static arrays take: the tails' (m, l) and the lists of records
-    const int statics = C::WARPS * 8 * NQ * 8 + C::WARPS * (2 * (int)sizeof(Run) + 20) + 256;
+    // what the kernel's static arrays take: (m, l) of records and runs, and their lists
+    const int statics = C::WARPS * 8 * NQ * 16 + C::WARPS * (2 * (int)sizeof(Run) + 20) + 256;
     int stages = (di.max_smem_optin - statics - fixed) / (per * ngroups);
     if (stages > kMaxStages) stages = kMaxStages;
-    if (stages < 2) return RSSM_ERR_UNSUPPORTED;
+    // a step's tiles beside those that wait for their readers
+    if (stages < (a.MT > 1 ? 2 * TP : TP)) return RSSM_ERR_UNSUPPORTED;
     a.stages = stages;
     int smem = stages * ngroups * per + fixed;
     const int tails = C::WARPS * 8 * NQ * C::TD * 4 + fixed;
     if (smem < tails) smem = tails;
-    const void* kern = (const void*)decode_kernel<D, E4M3, AF32, NQ>;
+    const void* kern = (const void*)decode_kernel<D, E4M3, AF32, NQ, TP>;
     if (!ensure_smem_limit(kern, smem)) return RSSM_ERR_CUDA;
     // rows of 128 bytes at least: 64-byte vectors go in pairs
     const uint64_t rows = (uint64_t)d->num_pages * d->num_kv_heads * d->page_size;
@@ -1113,18 +1211,22 @@ static int launch_nq(const rssm_attn_dims* d, const rssm_attn_cache* c, DecArgs 
         x.q = static_cast<const char*>(a.q) + (long)b * a.T * a.q_stride * (AF32 ? 4 : 2);
         x.o = static_cast<char*>(a.o) + (long)b * a.T * a.hq * D * (a.obf ? 2 : 4);
         if (a.lse) x.lse = a.lse + (long)b * a.T * a.hq;
-        decode_kernel<D, E4M3, AF32, NQ><<<grid, C::WARPS * 32, smem, st>>>(x, km, vm);
+        decode_kernel<D, E4M3, AF32, NQ, TP><<<grid, C::WARPS * 32, smem, st>>>(x, km, vm);
     }
     return launch_status();
 }
 
 // Up to 8 queries fit one block of mma columns; beyond, a warp takes two blocks (one pass
-// over the tile's operands serves both) and a group up to four warps.
+// over the tile's operands serves both) and a group up to four warps. A step of two tiles
+// gives a warp independent work between the dependent pieces of one; bf16 tiles of 128
+// columns have rings of three stages unless groups share warps, and take one.
 template <int D, bool E4M3, bool AF32>
 static int launch(const rssm_attn_dims* d, const rssm_attn_cache* c, const DecArgs& a,
                   const DeviceInfo& di, cudaStream_t st) {
-    return a.M <= 8 ? launch_nq<D, E4M3, AF32, 1>(d, c, a, di, st)
-                    : launch_nq<D, E4M3, AF32, 2>(d, c, a, di, st);
+    constexpr bool wide = !E4M3 && D == 128;
+    if (a.M <= 8) return launch_nq<D, E4M3, AF32, 1, wide ? 1 : 2>(d, c, a, di, st);
+    if (wide && a.MT == 1) return launch_nq<D, E4M3, AF32, 2, wide ? 1 : 2>(d, c, a, di, st);
+    return launch_nq<D, E4M3, AF32, 2, 2>(d, c, a, di, st);
 }
 
 }  // namespace attn
