@@ -21,13 +21,14 @@
 // one per group of warps (a group: ceil(M / 16) warps that take up to 16 queries each over
 // the same tiles). Lengths are read on the device: no length reaches the host, ragged
 // batches balance to a tile, a single long row fills the machine. A group streams its
-// tiles with TMA boxes of 128-byte swizzled row segments into a ring of stages of its own
+// tiles into a ring of stages of its own, 16-byte chunks swizzled within 128 bytes
 // (conflict-free ldmatrix), and never meets another group before its range ends. A (row,
-// head) that lies inside one range is written out by its group. One that is cut leaves
-// partial results; the groups of a CTA join theirs through shared memory, and the last CTA
-// of a (row, head) to arrive at a counter joins the CTAs' results, in an order that the
-// lengths alone fix.
+// head) that lies
+// inside one range is written out by its group. One that is cut leaves partial results; the
+// groups of a CTA join theirs through shared memory, and the last CTA of a (row, head) to
+// arrive at a counter joins the CTAs' results, in an order that the lengths alone fix.
 #include <cuda_fp16.h>
+#include <cstring>
 
 #include "attn.cuh"
 
@@ -35,12 +36,12 @@ namespace rssm {
 namespace attn {
 
 constexpr int kTok = 16;       // tokens per tile: the smallest page
-constexpr int kMaxWarps = 8;    // per CTA
+constexpr int kMaxStages = 8;   // per group
+constexpr int kMaxWarps = 16;    // per CTA
 constexpr int kMaxCtas = 256;   // more than the SMs of any machine the library runs on
 constexpr int kMaxRows = 1024;  // rows per launch (prefix sums in shared memory)
 constexpr int kRowBytes = 13312;  // prefix sums, lengths and slots of kMaxRows rows, up to the
                                   // stages' alignment
-constexpr int kMaxStages = 8;   // per group
 // Tiles that each group of a CTA gets at least before another CTA joins in.
 constexpr int kMinTiles = 2;
 // Longest (row, head), in tiles, up to which no CTA shares one. Meeting in global memory
@@ -54,6 +55,8 @@ constexpr float kSlack = 8.f;
 struct DecArgs {
     const void* q;
     long q_stride;
+    const char* k;
+    const char* v;
     const float* k_scale;
     const float* v_scale;
     const int32_t* page_table;
@@ -67,7 +70,7 @@ struct DecArgs {
     int32_t* counters; // [CTAs]
     float qscale;      // scale * log2 e
     int batch, T, G, hq, hkv, ps_log2, num_pages, max_pages, num_slots, window, appended;
-    int M, MT;         // queries per key head, warps per group (each 8 NQ queries)
+    int M, MT;         // queries per key head, warps per group (each 8 queries)
     int stages;        // per group
     int obf;
 };
@@ -86,6 +89,32 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t* r) {
                  : "r"(addr)
                  : "memory");
 }
+// cp.async with an L2 policy, a 4-byte one, and the wait for all but the last N commits.
+__device__ __forceinline__ void cp_async16_hint(uint32_t dst, const void* src, uint64_t policy) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(policy)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_but(int n) {
+    switch (n) {
+        case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+        case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+        case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+        case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+        case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+        case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
+        case 6: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
+        default: asm volatile("cp.async.wait_group 7;" ::: "memory"); break;
+    }
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
+}
+
 template <bool F16>
 __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
     if (F16)
@@ -126,8 +155,8 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t
         : "r"(w));
 }
 
-// Byte offset of 16-byte chunk c of token t in a [16 tokens][ROWB bytes] tile as the TMA
-// boxes leave it: 128-byte row segments, chunk j of row r at j ^ (r % 8).
+// Byte offset of 16-byte chunk c of token t in a [16 tokens][ROWB bytes] tile in shared
+// memory: 128-byte row segments, chunk j of row r at j ^ (r % 8).
 template <int ROWB>
 __device__ __forceinline__ uint32_t tile_off(int t, int c) {
     if (ROWB >= 128) {
@@ -160,10 +189,10 @@ struct Rows {
     int* slot;
 };
 
-// Where one tile lies: row, head, first position, row of its first token in the cache
-// matrix (-1: its page is out of range).
+// Where one tile lies: row, head, number among the (row, head)'s tiles, row of its first
+// token in the cache matrix (-1: its page is out of range).
 struct Tile {
-    int b, h, pos, y;
+    int b, h, at, y;
 };
 
 // The tile list (fewer than 2^31 tiles) cut into the CTAs' ranges. Even cuts share (row,
@@ -195,11 +224,6 @@ __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile 
     __syncwarp();
     return false;
 }
-__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                         int32_t* dev_err) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-    return wait_long(bar, parity, abort, dev_err);
-}
 
 // Last row b with cum[b] <= i (rows without tiles are passed over).
 __device__ __forceinline__ int find_row(const uint32_t* cum, int batch, uint32_t i) {
@@ -213,34 +237,34 @@ __device__ __forceinline__ int find_row(const uint32_t* cum, int batch, uint32_t
 }
 
 // Row and head of tile t, and its number among the (row, head)'s tiles.
-__device__ __noinline__ int find_tile(const DecArgs& a, const uint32_t* cum, uint32_t t, Tile& x) {
+__device__ __noinline__ Tile find_tile(const DecArgs& a, const uint32_t* cum, uint32_t t) {
+    Tile x;
     x.b = a.batch == 1 ? 0 : find_row(cum, a.batch, t / (uint32_t)a.hkv);
     const uint32_t nt = cum[x.b + 1] - cum[x.b];
     const uint32_t in_row = t - cum[x.b] * (uint32_t)a.hkv;
     x.h = (int)(in_row / nt);
-    return (int)(in_row - (uint32_t)x.h * nt);
+    x.at = (int)(in_row - (uint32_t)x.h * nt);
+    x.y = -1;
+    return x;
 }
 
 // The first tile from t on that begins a (row, head).
 __device__ __noinline__ uint32_t next_head(const DecArgs& a, const uint32_t* cum, uint32_t t) {
     if (t >= cum[a.batch] * (uint32_t)a.hkv) return t;
-    Tile x;
-    const uint32_t at = find_tile(a, cum, t, x);
-    return at == 0 ? t : t - at + cum[x.b + 1] - cum[x.b];
+    const Tile x = find_tile(a, cum, t);
+    return x.at == 0 ? t : t - x.at + cum[x.b + 1] - cum[x.b];
 }
 
-__device__ __noinline__ Tile locate_tile(const DecArgs& a, const Rows& rows, uint32_t t) {
-    Tile x;
-    const int i = find_tile(a, rows.cum, t, x);
-    x.pos = (row_span(a, rows.len[x.b]).first + i) * kTok;
-    const int page = __ldg(a.page_table + (long)rows.slot[x.b] * a.max_pages + (x.pos >> a.ps_log2));
+// The same with the tile's place in the cache.
+__device__ __noinline__ int locate_tile(const DecArgs& a, const Rows& rows, uint32_t t) {
+    const Tile x = find_tile(a, rows.cum, t);
+    const int pos = (row_span(a, rows.len[x.b]).first + x.at) * kTok;
+    const int page = __ldg(a.page_table + (long)rows.slot[x.b] * a.max_pages + (pos >> a.ps_log2));
     if (page < 0 || page >= a.num_pages) {
         set_dev_err(a.dev_err, RSSM_DEVERR_PAGE);
-        x.y = -1;
-    } else {
-        x.y = ((page * a.hkv + x.h) << a.ps_log2) + (x.pos & ((1 << a.ps_log2) - 1));
+        return -1;
     }
-    return x;
+    return ((page * a.hkv + x.h) << a.ps_log2) + (pos & ((1 << a.ps_log2) - 1));
 }
 
 // o and lse of query row r of (b, h): elements d, d + 1.
@@ -295,12 +319,15 @@ struct Run {
 //     power of two at its largest element. One part carries all 8 bits of a bf16 query but
 //     11 of a weight, whose error shows in a small output of large terms: two parts, and
 //     two of each for float32 activations.
-template <int D, bool E4M3, bool AF32, int NQ, int TILES>
+template <int D, bool E4M3, bool AF32, bool SHARE>
 struct Cfg {
-    static constexpr int TP = TILES;                 // tiles of a step
-    // Warps of a CTA. The registers of 16 warps (128 each) hold 8 queries' accumulators;
-    // with a bf16 cache 16 rings would leave one stage each.
-    static constexpr int WARPS = 8;
+    static constexpr bool WIDE = !E4M3 && D == 128;
+    static constexpr int TP = WIDE ? 1 : 2;          // tiles of a step
+    static constexpr int WARPS = AF32 || (WIDE && !SHARE) ? 8 : 16;
+    // Wide tiles come by TMA (cp.async keeps fewer bytes in flight: 128 against 154 us on the
+    // 2 x 128k case); for narrow ones the two are level (437 and 431 us on the 256-row 8-bit
+    // case), and where warps share a tile each copies its part.
+    static constexpr bool TMA = WIDE && !SHARE;
     static constexpr int ROWB = D * (E4M3 ? 1 : 2);  // bytes of a cached vector
     static constexpr int KB = kTok * ROWB;           // K (or V) bytes of a tile
     static constexpr int QP = AF32 ? (E4M3 ? 2 : 3) : 1;
@@ -340,49 +367,49 @@ __device__ __forceinline__ void split2(float v0, float v1, uint32_t* out) {
     }
 }
 
-template <int D, bool E4M3, bool AF32, int NQ, int TP>
-__global__ void __launch_bounds__((Cfg<D, E4M3, AF32, NQ, TP>::WARPS * 32), 1)
+template <int D, bool E4M3, bool AF32, bool SHARE>
+__global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
     decode_kernel(const __grid_constant__ DecArgs a, const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap) {
-    using C = Cfg<D, E4M3, AF32, NQ, TP>;
-    constexpr int kWarps = C::WARPS, kDecThreads = kWarps * 32;
+    using C = Cfg<D, E4M3, AF32, SHARE>;
+    constexpr int kWarps = C::WARPS, kDecThreads = kWarps * 32, NQ = 1;
     extern __shared__ unsigned char smem_raw[];
     // 128-byte swizzled boxes want their base on 1024 bytes
     unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int ngroups = kWarps / a.MT;
-    const int group = warp / a.MT, mt = warp - group * a.MT;
+    const int MT = SHARE ? a.MT : 1;
+    const int ngroups = kWarps / MT;
+    const int group = warp / MT, mt = warp - group * MT;
     const int stages = a.stages;
+    const int nst = stages * ngroups;
 
     // shared memory: the rows, stages (at the end the tails lie over them and what follows),
-    // scales, tiles, barriers
+    // scales
     Rows rows;
     rows.cum = reinterpret_cast<uint32_t*>(smem);
     rows.len = reinterpret_cast<int*>(smem) + kMaxRows + 4;
     rows.slot = rows.len + kMaxRows;
     uint32_t* const cum = rows.cum;
     unsigned char* st_kv = smem + kRowBytes;
-    const int nst = stages * ngroups;
     float* st_scale = reinterpret_cast<float*>(st_kv + (size_t)nst * C::STAGE);
-    int2* st_tile = reinterpret_cast<int2*>(st_kv + (size_t)nst * (C::STAGE + C::AUX));
-    uint64_t* full = reinterpret_cast<uint64_t*>(st_tile + nst);
-    uint64_t* empty = full + nst;
-    __shared__ uint2 scan[kWarps];  // tiles and longest row of the warps' rows
+    uint64_t* full = reinterpret_cast<uint64_t*>(st_kv + (size_t)nst * (C::STAGE + C::AUX));
     __shared__ int abort_flag;
+    __shared__ uint2 scan[kWarps];  // tiles and longest row of the warps' rows
     __shared__ int rec_b[2 * kWarps], rec_h[2 * kWarps];  // records; b < 0: none
     __shared__ Run runs[2 * kWarps];
     __shared__ int nruns, last_flag[2];
     __shared__ float2 rec_ml[2 * kWarps * 8 * NQ];  // [record][M] m and l
 
-    if (tid < nst) {
-        mbar_init(&full[tid], 1);
-        mbar_init(&empty[tid], a.MT);
-        fence_barrier_init();
-    }
-    if (tid == 0) {
-        abort_flag = 0;
-        asm volatile("prefetch.tensormap [%0];" ::"l"(&kmap) : "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"(&vmap) : "memory");
+    if (C::TMA) {
+        if (tid < nst) {
+            mbar_init(&full[tid], 1 + (E4M3 ? 32 : 0));
+            fence_barrier_init();
+        }
+        if (tid == 0) {
+            abort_flag = 0;
+            asm volatile("prefetch.tensormap [%0];" ::"l"(&kmap) : "memory");
+            asm volatile("prefetch.tensormap [%0];" ::"l"(&vmap) : "memory");
+        }
     }
     if (tid < 2 * kWarps) rec_b[tid] = -1;
     if (tid == 0) runs[0].cta0 = runs[0].cta1 = 0;
@@ -486,49 +513,70 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, NQ, TP>::WARPS * 32), 1)
     const int ntile = group < ngroups ? (int)(gbase + (group < (int)grem ? 1 : 0)) : 0;
     if (ntile > 0) {
         const bool leader = mt == 0;
-        const uint64_t pol = policy_evict_first();
         unsigned char* kv = st_kv + (size_t)group * stages * C::STAGE;
         float* sc = st_scale + group * stages * (C::AUX / 4);
-        int2* tl = st_tile + group * stages;
-        uint64_t* fb = full + group * stages;
-        uint64_t* eb = empty + group * stages;
+        const uint64_t pol = policy_evict_first();
 
-        // the next 32 tiles of the range are looked up at once, one per lane
-        Tile cur{};
-        int sent = 0, sent_s = 0;  // tiles issued, and the stage of the next
-        // issue the range's next tile into its stage (leader warp only)
+        // The next 32 tiles of the range are looked up at once, one per lane. Tile `sent` goes
+        // into stage sent % stages, each warp of the group copying its share; a commit follows
+        // whether or not there is a tile, so that the waits can count commits.
+        int look = -1;
+        int sent = 0, sent_s = 0;
+        uint32_t bad = 0;  // stages whose tile has no page
+        uint64_t* fb = full + group * stages;
+        uint32_t parity = 0;  // of the stages' barriers, a bit each
         auto issue = [&]() {
-            if (sent >= ntile) return;
-            if ((sent & 31) == 0 && sent + lane < ntile) cur = locate_tile(a, rows, t0 + sent + lane);
-            if (lane == (sent & 31)) {
-                unsigned char* dst = kv + (size_t)sent_s * C::STAGE;
-                tl[sent_s] = make_int2(cur.pos, cur.y);
-                if (cur.y < 0) {
-                    mbar_arrive_plain(&fb[sent_s]);
-                } else {
-                    mbar_arrive_expect_tx(&fb[sent_s], C::STAGE + C::AUX);
-                    constexpr int EB = E4M3 ? 1 : 2;
-                    const int y = C::ROWB >= 128 ? cur.y : cur.y >> 1;
+            if (sent < ntile) {
+                if ((sent & 31) == 0 && sent + lane < ntile) look = locate_tile(a, rows, t0 + sent + lane);
+                const int y = __shfl_sync(0xffffffffu, look, sent & 31);
+                bad = (bad & ~(1u << sent_s)) | (y < 0 ? 1u << sent_s : 0u);
+                if (C::TMA) {
+                    if (leader && y >= 0) {
+                        unsigned char* dst = kv + (size_t)sent_s * C::STAGE;
+                        if (elect_one()) {
+                            constexpr int EB = E4M3 ? 1 : 2;
+                            const int ty = C::ROWB >= 128 ? y : y >> 1;
+                            mbar_arrive_expect_tx(&fb[sent_s], C::STAGE);
 #pragma unroll
-                    for (int x = 0; x < (C::ROWB + 127) / 128; ++x) {
-                        tma_load_2d(dst + x * kTok * 128, &kmap, x * 128 / EB, y, &fb[sent_s], pol);
-                        tma_load_2d(dst + C::KB + x * kTok * 128, &vmap, x * 128 / EB, y, &fb[sent_s], pol);
+                            for (int x = 0; x < (C::ROWB + 127) / 128; ++x) {
+                                tma_load_2d(dst + x * kTok * 128, &kmap, x * 128 / EB, ty, &fb[sent_s], pol);
+                                tma_load_2d(dst + C::KB + x * kTok * 128, &vmap, x * 128 / EB, ty, &fb[sent_s], pol);
+                            }
+                        }
+                        __syncwarp();
+                        if (E4M3) {
+                            cp_async4(smem_addr(sc + sent_s * 2 * kTok + lane),
+                                      (lane < kTok ? a.k_scale : a.v_scale) + y + (lane & (kTok - 1)));
+                            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&fb[sent_s])) : "memory");
+                        }
                     }
-                    if (E4M3) {
-                        bulk_g2s(sc + sent_s * 2 * kTok, a.k_scale + cur.y, kTok * 4, &fb[sent_s]);
-                        bulk_g2s(sc + sent_s * 2 * kTok + kTok, a.v_scale + cur.y, kTok * 4, &fb[sent_s]);
-                    }
-                }
-            }
-            __syncwarp();
-            ++sent;
-            if (++sent_s == stages) sent_s = 0;
-        };
-        // A stage is refilled a step late when several warps read it, so that the leader
-        // seldom waits for them.
-        if (leader)
+                } else if (y >= 0) {
+                    constexpr int LPR = C::ROWB / 16, TPI = 32 / LPR;  // lanes of a token, tokens at once
+                    const uint32_t dst = smem_addr(kv + (size_t)sent_s * C::STAGE);
+                    const long src = ((long)y + lane / LPR) * C::ROWB + (lane % LPR) * 16;
+                    auto copy = [&](int j) {
+                        const uint32_t to = dst + tile_off<C::ROWB>(j * TPI + lane / LPR, lane % LPR);
+                        cp_async16_hint(to, a.k + src + (long)j * TPI * C::ROWB, pol);
+                        cp_async16_hint(to + C::KB, a.v + src + (long)j * TPI * C::ROWB, pol);
+                    };
+                    if (!SHARE) {
+#pragma unroll
+                        for (int j = 0; j < kTok / TPI; ++j) copy(j);
+                    } else {
 #pragma unroll 1
-            for (int i = 0; i < stages; ++i) issue();
+                        for (int j = mt; j < kTok / TPI; j += MT) copy(j);
+                    }
+                    if (E4M3 && leader)
+                        cp_async4(smem_addr(sc + sent_s * 2 * kTok + lane),
+                                  (lane < kTok ? a.k_scale : a.v_scale) + y + (lane & (kTok - 1)));
+                }
+                ++sent;
+                if (++sent_s == stages) sent_s = 0;
+            }
+            if (!C::TMA) cp_async_commit();
+        };
+#pragma unroll 1
+        for (int i = 0; i < stages; ++i) issue();
 
         uint32_t qf[D / 16][NQ][C::QP][2];  // [k step][query block][part][k half]
         float rs[NQ][2];                    // score factor of the queries
@@ -538,8 +586,9 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, NQ, TP>::WARPS * 32), 1)
         int cb = 0, ch = 0;      // current (row, head)
         bool begun = false;      // its tiles began before this range
         int next = 0;            // tile of the range at which it ends
-        int s = 0, phase = 0;    // stage and phase of tile i
-        int hand_s = 0, free_s = 0, free_phase = 0;
+        int s = 0;               // stage of tile i
+        int pos0 = 0;            // position of tile 0 of the range, were all of them this head's
+        int used = 0;            // tiles of the step before
 
 #pragma unroll 1
         for (int i = 0;;) {
@@ -629,15 +678,13 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, NQ, TP>::WARPS * 32), 1)
                 if (i == ntile) break;
 
                 // Start a (row, head): its queries as mma operands, the positions they see.
-                {
-                    Tile x;
-                    const int at = find_tile(a, cum, t0 + i, x);
-                    cb = x.b;
-                    ch = x.h;
-                    begun = at > 0;
-                    next = i + (int)(cum[cb + 1] - cum[cb]) - at;
-                }
+                const Tile x = find_tile(a, cum, t0 + i);
+                cb = x.b;
+                ch = x.h;
+                begun = x.at > 0;
+                next = i + (int)(cum[cb + 1] - cum[cb]) - x.at;
                 const int len = rows.len[cb];
+                pos0 = (row_span(a, len).first + x.at - i) * kTok;
                 const int app = a.appended ? 1 : 0;
                 n_min = len + app;
                 n_max = len + (app ? a.T : 0);
@@ -720,20 +767,40 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, NQ, TP>::WARPS * 32), 1)
 
             // the step's tiles: TP, or what the (row, head) or the range has left
             const int steps = min(C::TP, min(next, ntile) - i);
-            int2 t[C::TP];
+            int2 t[C::TP];  // position, -1 for a tile that is not there or has no page
             int st[C::TP];
             bool ok = true;
+            if (C::TMA) {
+                // every tile of the step that has a page
+#pragma unroll
+                for (int u = 0; u < C::TP; ++u) {
+                    const int z = s + u < stages ? s + u : s + u - stages;
+                    if (u < steps && !(bad >> z & 1)) {
+                        if (!__all_sync(0xffffffffu, mbar_try_wait(&fb[z], parity >> z & 1)))
+                            ok = ok && wait_long(&fb[z], parity >> z & 1, &abort_flag, a.dev_err);
+                        parity ^= 1u << z;
+                    }
+                }
+            }
+            if (!C::TMA) cp_async_wait_but(stages - (SHARE ? 2 : 1) * C::TP);
+            if (!SHARE) {
+                __syncwarp();
+            } else {
+                // the group's copies of this step are here; the stages of the step before are free
+                asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(MT * 32) : "memory");
+#pragma unroll 1
+                for (; used > 0; --used) issue();
+            }
+            if (!ok) break;
 #pragma unroll
             for (int u = 0; u < C::TP; ++u) {
                 st[u] = s;
-                t[u] = make_int2(0, -1);
+                t[u] = make_int2(pos0 + (i + u) * kTok, -1);
                 if (u < steps) {
-                    ok = ok && wait_all(&fb[s], phase, &abort_flag, a.dev_err);
-                    t[u] = tl[s];
-                    if (++s == stages) s = 0, phase ^= 1;
+                    t[u].y = bad >> s & 1 ? -1 : 0;
+                    if (++s == stages) s = 0;
                 }
             }
-            if (!ok) break;
             bool some = t[0].y >= 0;
             if (C::TP > 1) some = some || t[C::TP - 1].y >= 0;
             if (some && works) {
@@ -886,7 +953,7 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, NQ, TP>::WARPS * 32), 1)
                             if (pos + tok >= n_max || pos + tok < b_min)
                                 *reinterpret_cast<uint4*>(vt + tile_off<C::ROWB>(tok, c)) = make_uint4(0, 0, 0, 0);
                         }
-                        fence_async_smem();  // the stage's next TMA load comes after these stores
+                        if (C::TMA) fence_async_smem();  // the stage's next load comes after these stores
                         __syncwarp();
                     }
                     if (!E4M3 && a.T > 1) {
@@ -971,29 +1038,15 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, NQ, TP>::WARPS * 32), 1)
             // ---------------------------------------------------- hand the stages back
             __syncwarp();
             i += steps;
+            used = steps;
+            if (!SHARE)
 #pragma unroll 1
-            for (int u = 0; u < steps; ++u) {
-                if (a.MT == 1) {
-                    issue();
-                    continue;
-                }
-                // of several readers' tiles the one TP before this: they have had a step's time
-                if (lane == 0) mbar_arrive_plain(&eb[hand_s]);
-                if (++hand_s == stages) hand_s = 0;
-                if (leader && i - steps + u >= C::TP) {
-                    if (sent < ntile && !wait_all(&eb[free_s], free_phase, &abort_flag, a.dev_err)) {
-                        ok = false;
-                        break;
-                    }
-                    issue();
-                    if (++free_s == stages) free_s = 0, free_phase ^= 1;
-                }
-            }
-            if (!ok) break;
+                for (; used > 0; --used) issue();
         }
+        cp_async_wait_but(0);
     }
     __syncthreads();
-    if (abort_flag) {
+    if (C::TMA && abort_flag) {
         // A wait ran out: no copy may still be in flight when the CTA ends. Every stage's
         // barrier is watched for a while, whatever its phase.
         if (tid < nst) {
@@ -1172,32 +1225,35 @@ static Workspace workspace_of(const rssm_attn_dims* d) {
     return w;
 }
 
-template <int D, bool E4M3, bool AF32, int NQ, int TP>
-static int launch_nq(const rssm_attn_dims* d, const rssm_attn_cache* c, DecArgs a, const DeviceInfo& di,
-                     cudaStream_t st) {
-    using C = Cfg<D, E4M3, AF32, NQ, TP>;
+template <int D, bool E4M3, bool AF32, bool SHARE>
+static int launch_kernel(const rssm_attn_dims* d, DecArgs a, const DeviceInfo& di, cudaStream_t st) {
+    using C = Cfg<D, E4M3, AF32, SHARE>;
     const int ngroups = C::WARPS / a.MT;
     const int fixed = kRowBytes + 1024;
-    const int per = C::STAGE + C::AUX + 8 + 16;
-    // what the kernel's static arrays take: (m, l) of records and runs, and their lists
-    const int statics = C::WARPS * 8 * NQ * 16 + C::WARPS * (2 * (int)sizeof(Run) + 20) + 256;
+    const int per = C::STAGE + C::AUX + 8;
+    // what the kernel's static arrays take: (m, l) of the records, and the lists
+    const int statics = C::WARPS * (128 + 2 * (int)sizeof(Run) + 24) + 256;
     int stages = (di.max_smem_optin - statics - fixed) / (per * ngroups);
     if (stages > kMaxStages) stages = kMaxStages;
-    // a step's tiles beside those that wait for their readers
-    if (stages < (a.MT > 1 ? 2 * TP : TP)) return RSSM_ERR_UNSUPPORTED;
+    // a step's tiles, beside them those of the step before where warps share
+    if (stages < (SHARE ? 2 : 1) * C::TP) return RSSM_ERR_UNSUPPORTED;
     a.stages = stages;
-    int smem = stages * ngroups * per + fixed;
-    const int tails = C::WARPS * 8 * NQ * C::TD * 4 + fixed;
+    int smem = fixed + stages * ngroups * per;
+    const int tails = fixed + C::WARPS * 8 * C::TD * 4;
     if (smem < tails) smem = tails;
-    const void* kern = (const void*)decode_kernel<D, E4M3, AF32, NQ, TP>;
-    if (!ensure_smem_limit(kern, smem)) return RSSM_ERR_CUDA;
-    // rows of 128 bytes at least: 64-byte vectors go in pairs
-    const uint64_t rows = (uint64_t)d->num_pages * d->num_kv_heads * d->page_size;
-    const bool pair = C::ROWB < 128;
     CUtensorMap km, vm;
-    if (!make_tmap_rows128(&km, c->k, E4M3 ? 1 : 2, pair ? rows / 2 : rows, pair ? 2 * D : D, pair ? kTok / 2 : kTok) ||
-        !make_tmap_rows128(&vm, c->v, E4M3 ? 1 : 2, pair ? rows / 2 : rows, pair ? 2 * D : D, pair ? kTok / 2 : kTok))
-        return RSSM_ERR_CUDA;
+    memset(&km, 0, sizeof km);
+    memset(&vm, 0, sizeof vm);
+    if (C::TMA) {
+        // rows of 128 bytes at least: 64-byte vectors go in pairs
+        const uint64_t nr = (uint64_t)d->num_pages * d->num_kv_heads * d->page_size;
+        const bool pair = C::ROWB < 128;
+        if (!make_tmap_rows128(&km, a.k, E4M3 ? 1 : 2, pair ? nr / 2 : nr, pair ? 2 * D : D, pair ? kTok / 2 : kTok) ||
+            !make_tmap_rows128(&vm, a.v, E4M3 ? 1 : 2, pair ? nr / 2 : nr, pair ? 2 * D : D, pair ? kTok / 2 : kTok))
+            return RSSM_ERR_CUDA;
+    }
+    const void* kern = (const void*)decode_kernel<D, E4M3, AF32, SHARE>;
+    if (!ensure_smem_limit(kern, smem)) return RSSM_ERR_CUDA;
     const int grid = di.sm_count < kMaxCtas ? di.sm_count : kMaxCtas;
     // rows of a launch: the prefix sums' size, and a tile list of fewer than 2^31
     const int64_t row_tiles = (int64_t)d->max_pages * (d->page_size / kTok) * a.hkv;
@@ -1211,22 +1267,15 @@ static int launch_nq(const rssm_attn_dims* d, const rssm_attn_cache* c, DecArgs 
         x.q = static_cast<const char*>(a.q) + (long)b * a.T * a.q_stride * (AF32 ? 4 : 2);
         x.o = static_cast<char*>(a.o) + (long)b * a.T * a.hq * D * (a.obf ? 2 : 4);
         if (a.lse) x.lse = a.lse + (long)b * a.T * a.hq;
-        decode_kernel<D, E4M3, AF32, NQ, TP><<<grid, C::WARPS * 32, smem, st>>>(x, km, vm);
+        decode_kernel<D, E4M3, AF32, SHARE><<<grid, C::WARPS * 32, smem, st>>>(x, km, vm);
     }
     return launch_status();
 }
 
-// Up to 8 queries fit one block of mma columns; beyond, a warp takes two blocks (one pass
-// over the tile's operands serves both) and a group up to four warps. A step of two tiles
-// gives a warp independent work between the dependent pieces of one; bf16 tiles of 128
-// columns have rings of three stages unless groups share warps, and take one.
 template <int D, bool E4M3, bool AF32>
-static int launch(const rssm_attn_dims* d, const rssm_attn_cache* c, const DecArgs& a,
-                  const DeviceInfo& di, cudaStream_t st) {
-    constexpr bool wide = !E4M3 && D == 128;
-    if (a.M <= 8) return launch_nq<D, E4M3, AF32, 1, wide ? 1 : 2>(d, c, a, di, st);
-    if (wide && a.MT == 1) return launch_nq<D, E4M3, AF32, 2, wide ? 1 : 2>(d, c, a, di, st);
-    return launch_nq<D, E4M3, AF32, 2, 2>(d, c, a, di, st);
+static int launch(const rssm_attn_dims* d, const DecArgs& a, const DeviceInfo& di, cudaStream_t st) {
+    return a.MT == 1 ? launch_kernel<D, E4M3, AF32, false>(d, a, di, st)
+                     : launch_kernel<D, E4M3, AF32, true>(d, a, di, st);
 }
 
 }  // namespace attn
@@ -1260,6 +1309,8 @@ extern "C" int rssm_attn_decode(const rssm_attn_dims* d, const rssm_attn_cache* 
     attn::DecArgs a{};
     a.q = q;
     a.q_stride = q_stride;
+    a.k = static_cast<const char*>(c->k);
+    a.v = static_cast<const char*>(c->v);
     a.k_scale = c->k_scale;
     a.v_scale = c->v_scale;
     a.page_table = c->page_table;
@@ -1283,15 +1334,15 @@ extern "C" int rssm_attn_decode(const rssm_attn_dims* d, const rssm_attn_cache* 
     a.window = window;
     a.appended = appended != 0;
     a.M = a.T * G;
-    a.MT = a.M <= 16 ? 1 : a.M <= 32 ? 2 : 4;
+    a.MT = a.M <= 8 ? 1 : a.M <= 16 ? 2 : a.M <= 32 ? 4 : 8;
     a.obf = d->out_dtype == RSSM_BF16;
     const bool q8 = d->cache_dtype == RSSM_E4M3, f32 = d->act_dtype == RSSM_F32;
     const cudaStream_t s = (cudaStream_t)stream;
 #define RSSM_ATTN_D(D_)                                                            \
-    (q8 ? (f32 ? attn::launch<D_, true, true>(d, c, a, di, s)                      \
-               : attn::launch<D_, true, false>(d, c, a, di, s))                    \
-        : (f32 ? attn::launch<D_, false, true>(d, c, a, di, s)                     \
-               : attn::launch<D_, false, false>(d, c, a, di, s)))
+    (q8 ? (f32 ? attn::launch<D_, true, true>(d, a, di, s)                      \
+               : attn::launch<D_, true, false>(d, a, di, s))                    \
+        : (f32 ? attn::launch<D_, false, true>(d, a, di, s)                     \
+               : attn::launch<D_, false, false>(d, a, di, s)))
     return d->head_dim == 64 ? RSSM_ATTN_D(64) : RSSM_ATTN_D(128);
 #undef RSSM_ATTN_D
 }
