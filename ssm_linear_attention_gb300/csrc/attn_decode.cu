@@ -71,6 +71,7 @@ struct DecArgs {
     float qscale;      // scale * log2 e
     int batch, T, G, hq, hkv, ps_log2, num_pages, max_pages, num_slots, window, appended;
     int M, MT;         // queries per key head, warps per group (each 8 queries)
+    int ngroups;       // of a CTA
     int stages;        // per group
     int obf;
 };
@@ -322,7 +323,7 @@ struct Run {
 template <int D, bool E4M3, bool AF32, bool SHARE>
 struct Cfg {
     static constexpr bool WIDE = !E4M3 && D == 128;
-    static constexpr int TP = WIDE ? 1 : 2;          // tiles of a step
+    static constexpr int TP = WIDE && !SHARE ? 1 : 2;  // tiles of a step
     static constexpr int WARPS = AF32 || (WIDE && !SHARE) ? 8 : 16;
     // Wide tiles come by TMA (cp.async keeps fewer bytes in flight: 128 against 154 us on the
     // 2 x 128k case); for narrow ones the two are level (437 and 431 us on the 256-row 8-bit
@@ -378,7 +379,7 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
     unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int MT = SHARE ? a.MT : 1;
-    const int ngroups = kWarps / MT;
+    const int ngroups = a.ngroups;
     const int group = warp / MT, mt = warp - group * MT;
     const int stages = a.stages;
     const int nst = stages * ngroups;
@@ -516,6 +517,11 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
         unsigned char* kv = st_kv + (size_t)group * stages * C::STAGE;
         float* sc = st_scale + group * stages * (C::AUX / 4);
         const uint64_t pol = policy_evict_first();
+        // ldmatrix: lane 8 i + r points at row r of matrix i. Of K, matrices are tokens 0-7 and
+        // 8-15 of one chunk, then of the next; of V as well, chunk and tokens swapped for bf16.
+        const uint32_t kbase = smem_addr(kv);
+        const uint32_t ko = tile_off<C::ROWB>((lane >> 3 & 1) * 8 + (lane & 7), lane >> 4);
+        const uint32_t vo = E4M3 ? ko : tile_off<C::ROWB>((lane >> 4) * 8 + (lane & 7), lane >> 3 & 1);
 
         // The next 32 tiles of the range are looked up at once, one per lane. Tile `sent` goes
         // into stage sent % stages, each warp of the group copying its share; a commit follows
@@ -804,7 +810,6 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
             bool some = t[0].y >= 0;
             if (C::TP > 1) some = some || t[C::TP - 1].y >= 0;
             if (some && works) {
-                const int lr = lane & 7, lm = lane >> 3;
                 // ------------------------------------------------ S^T = K Q^T
                 constexpr int SA = C::TP == 1 ? 2 : 1;  // one tile: two chains of sums
                 float sa[C::TP][SA][NQ][4];
@@ -818,11 +823,13 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
                 for (int kk = 0; kk < D / 16; kk += E4M3 ? 2 : 1)
 #pragma unroll
                     for (int u = 0; u < C::TP; ++u) {
-                        const uint32_t kbase = smem_addr(kv + (size_t)st[u] * C::STAGE);
+                        // chunk 2 kk (8-bit: kk) of the lane's token and half: the swizzle makes a
+                        // step of it an exclusive or
+                        const uint32_t at = (kbase + st[u] * C::STAGE + ko) ^ (uint32_t)((E4M3 ? kk : 2 * kk) % 8 * 16);
                         uint32_t r[4];
                         if (E4M3) {
                             uint32_t f[2][4];
-                            ldsm4(kbase + tile_off<C::ROWB>((lm & 1) * 8 + lr, kk + (lm >> 1)), r);
+                            ldsm4(at, r);
 #pragma unroll
                             for (int x = 0; x < 4; ++x)
                                 e4m3x4_to_f16(r[x], f[x >> 1][x & 1], f[x >> 1][2 + (x & 1)]);
@@ -834,7 +841,7 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
                                     mma16816<true>(sa[u][SA - 1][q], f[1], qf[kk + 1][q][p][0], qf[kk + 1][q][p][1]);
                                 }
                         } else {
-                            ldsm4(kbase + tile_off<C::ROWB>((lm & 1) * 8 + lr, 2 * kk + (lm >> 1)), r);
+                            ldsm4(at + kk / 4 * (kTok * 128), r);
 #pragma unroll
                             for (int p = 0; p < C::QP; ++p)
 #pragma unroll
@@ -975,7 +982,7 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
 #pragma unroll
                 for (int u = 0; u < C::TP; ++u) {
                     const unsigned char* vt = kv + (size_t)st[u] * C::STAGE + C::KB;
-                    const uint32_t vbase = smem_addr(vt);
+                    const uint32_t vbase = kbase + st[u] * C::STAGE + C::KB + vo;
                     if (!careful[u]) {
 #pragma unroll
                         for (int c = 0; c < C::DB; ++c) {
@@ -985,7 +992,7 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
                                 // by token they are one k pair of the even and of the odd columns
                                 if (c & 1) continue;
                                 uint32_t r[4], g[4];
-                                ldsm4_t(vbase + tile_off<C::ROWB>((lm & 1) * 8 + lr, c + (lm >> 1)), r);
+                                ldsm4_t(vbase ^ (uint32_t)(c % 8 * 16), r);
 #pragma unroll
                                 for (int x = 0; x < 4; ++x) {
                                     uint32_t lo, hi;
@@ -1002,7 +1009,7 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
                                         mma16816<true>(o[c + 1][q], g, pf[u][q][x][0], pf[u][q][x][1]);
                                     }
                             } else {
-                                ldsm4_t(vbase + tile_off<C::ROWB>((lm >> 1) * 8 + lr, 2 * c + (lm & 1)), f);
+                                ldsm4_t((vbase ^ (uint32_t)(2 * c % 8 * 16)) + c / 4 * (kTok * 128), f);
 #pragma unroll
                                 for (int x = 0; x < C::PP; ++x)
 #pragma unroll
@@ -1228,17 +1235,19 @@ static Workspace workspace_of(const rssm_attn_dims* d) {
 template <int D, bool E4M3, bool AF32, bool SHARE>
 static int launch_kernel(const rssm_attn_dims* d, DecArgs a, const DeviceInfo& di, cudaStream_t st) {
     using C = Cfg<D, E4M3, AF32, SHARE>;
-    const int ngroups = C::WARPS / a.MT;
     const int fixed = kRowBytes + 1024;
     const int per = C::STAGE + C::AUX + 8;
     // what the kernel's static arrays take: (m, l) of the records, and the lists
     const int statics = C::WARPS * (128 + 2 * (int)sizeof(Run) + 24) + 256;
-    int stages = (di.max_smem_optin - statics - fixed) / (per * ngroups);
-    if (stages > kMaxStages) stages = kMaxStages;
-    // a step's tiles, beside them those of the step before where warps share
-    if (stages < (SHARE ? 2 : 1) * C::TP) return RSSM_ERR_UNSUPPORTED;
-    a.stages = stages;
-    int smem = fixed + stages * ngroups * per;
+    const int budget = di.max_smem_optin - statics - fixed;
+    // a ring holds a step's tiles at least, and those of the step before where warps share them
+    const int least = (SHARE ? 2 : 1) * C::TP;
+    a.ngroups = C::WARPS / a.MT;
+    if (budget / (per * a.ngroups) < least) a.ngroups = budget / (per * least);
+    if (a.ngroups < 1) return RSSM_ERR_UNSUPPORTED;
+    a.stages = budget / (per * a.ngroups);
+    if (a.stages > kMaxStages) a.stages = kMaxStages;
+    int smem = fixed + a.stages * a.ngroups * per;
     const int tails = fixed + C::WARPS * 8 * C::TD * 4;
     if (smem < tails) smem = tails;
     CUtensorMap km, vm;
