@@ -192,24 +192,38 @@ def lib():
 
 
 def _ptr(t):
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or isinstance(t, int):
         return t
     return t.data_ptr()
 
 
+def _current_stream():
+    """The current torch stream of the current device, as a handle."""
+    global _current_stream
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    dev = getattr(torch._C, "_cuda_getDevice", None)
+    if raw is None or dev is None:
+        def _current_stream():
+            return torch.cuda.current_stream().cuda_stream
+    else:  # the same handle without building a Stream object
+        torch.cuda.init()
+
+        def _current_stream():
+            return raw(dev())
+    return _current_stream()
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
 
 
 def _call(name, *args):
-    rc = getattr(lib(), name)(*args)
+    rc = getattr(_lib or lib(), name)(*args)
     if rc != RSSM_OK:
         raise RSSMError(name, rc)
 

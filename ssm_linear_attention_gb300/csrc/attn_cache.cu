@@ -2,12 +2,13 @@
 // tokens written (rounded to bf16, or to e4m3 with a scale per token and head), tokens
 // read back, lengths advanced.
 //
-// All three move bytes and compute next to nothing: a vector of D values is read once and
-// written once, so HBM bounds the large calls and launch latency the small ones. A CTA
-// takes a few consecutive tokens: its first threads look up each token's row, position
-// and page (one dependent chain per token instead of one per vector), then all threads
-// move the tokens' vectors, D / 8 lanes to a vector, 8 values to a lane (one 16-byte load
-// of bf16).
+// All three move bytes: a vector of D values is read once and written once, so HBM bounds
+// the large calls (the 8-bit append comes near the issue rate too: an absolute maximum, a
+// division and a conversion per 8 values) and launch latency the small ones. CTAs loop over
+// blocks of consecutive tokens. One warp looks up row, position and page of the next block's
+// tokens, a chain of dependent loads, while the others move this block's vectors, D / 8
+// lanes to a vector, 8 values to a lane (one 16-byte load of bf16), a vector of each of
+// several tokens at once.
 #include <cuda_fp8.h>
 
 #include "attn.cuh"
@@ -15,8 +16,11 @@
 namespace rssm {
 namespace attn {
 
-constexpr int kThreads = 256;
-constexpr int kTokMax = 16;  // tokens per CTA of a large call
+constexpr int kMovers = 256;          // threads that move vectors
+constexpr int kThreads = kMovers + 32;  // and the warp that looks tokens up
+constexpr int kTokMax = 32;            // tokens of a block: one per lane of that warp
+constexpr int kCtas = 4;               // of an SM
+constexpr int kAhead = 4;              // vectors whose loads a thread has in flight
 
 struct MoveArgs {
     const void* src[2];   // append: k, v; read: the caches
@@ -30,24 +34,33 @@ struct MoveArgs {
     const int32_t* slot_len;
     int32_t* dev_err;
     int n_tokens, batch, T, heads, ps_log2, num_pages, max_pages, num_slots;
-    int tok_per_cta;
+    int block;  // tokens of a block
 };
 
-// Row of token t: t / T, or the row whose [cu[b], cu[b+1]) holds t (the first row b with
-// cu[b+1] > t). -1 when the list does not cover t.
-__device__ __forceinline__ int row_of(const int32_t* cu, int batch, int T, int t, int* in_row) {
-    if (!cu) {
-        *in_row = t % T;
-        return t / T;
+// Row of token t, one token per lane of a warp: t / T, or the row whose [cu[b], cu[b+1])
+// holds t (the first row b with cu[b+1] > t), found among 32 evenly spaced entries held by
+// the lanes and then between two of them. -1 when the list does not cover t.
+__device__ __forceinline__ int row_of(const MoveArgs& a, int t, int* in_row) {
+    if (!a.cu) {
+        *in_row = t % a.T;
+        return t / a.T;
     }
-    int lo = 0, hi = batch;  // first b in [lo, hi) with cu[b + 1] > t
+    const int lane = threadIdx.x & 31, step = (a.batch + 31) / 32;
+    const int mine = a.cu[min((lane + 1) * step, a.batch)];
+    int piece = 0;  // entries that are <= t
+#pragma unroll
+    for (int w = 16; w >= 1; w >>= 1) {
+        const int v = __shfl_sync(0xffffffffu, mine, piece + w - 1);
+        if (v <= t) piece += w;
+    }
+    if (__shfl_sync(0xffffffffu, mine, piece) <= t) return -1;
+    int lo = piece * step, hi = min(lo + step, a.batch) - 1;  // first b in [lo, hi] with cu[b + 1] > t
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
-        if (cu[mid + 1] > t) hi = mid;
+        if (a.cu[mid + 1] > t) hi = mid;
         else lo = mid + 1;
     }
-    if (lo >= batch) return -1;
-    *in_row = t - cu[lo];
+    *in_row = t - a.cu[lo];
     return *in_row < 0 ? -1 : lo;
 }
 
@@ -56,7 +69,8 @@ __device__ __forceinline__ int row_of(const int32_t* cu, int batch, int T, int t
 template <bool READ>
 __device__ __forceinline__ long locate(const MoveArgs& a, int t) {
     int in_row = 0;
-    const int b = row_of(a.cu, a.batch, a.T, t, &in_row);
+    const int b = row_of(a, min(t, a.n_tokens - 1), &in_row);  // the whole warp
+    if (t >= a.n_tokens) return -1;
     if (b < 0) {
         set_dev_err(a.dev_err, RSSM_DEVERR_CURSOR);
         return -1;
@@ -108,81 +122,171 @@ __device__ __forceinline__ void unpack8_e4m3(uint2 v, float* f) {
     }
 }
 
+// Runs over the CTA's blocks of tokens: body(first token, count, where) with where[i] the
+// place of token i.
+template <bool READ, class Body>
+__device__ __forceinline__ void for_blocks(const MoveArgs& a, Body body) {
+    __shared__ long where[2][kTokMax];
+    const int nblk = (a.n_tokens + a.block - 1) / a.block;
+    const bool looks = threadIdx.x >= kMovers;
+    const int lane = threadIdx.x & 31;
+    auto look = [&](int blk, int half) {
+        const int t = blk * a.block + lane;
+        const long w = locate<READ>(a, lane < a.block ? t : a.n_tokens);
+        where[half][lane] = w;
+    };
+    if (looks) look(blockIdx.x, 0);
+    __syncthreads();
+    int half = 0;
+    for (int blk = blockIdx.x; blk < nblk; blk += gridDim.x, half ^= 1) {
+        if (looks) {
+            if (blk + (int)gridDim.x < nblk) look(blk + gridDim.x, half ^ 1);
+        } else {
+            body(blk * a.block, min(a.block, a.n_tokens - blk * a.block), where[half]);
+        }
+        __syncthreads();
+    }
+}
+
+// The vectors of a block: body(w, h, t, dt) for the vectors of k (w 0) or v (w 1), head h, of
+// tokens t, t + dt, ... Groups of D / 8 lanes take one vector of the 2 heads each, and
+// share the tokens where there are more groups than vectors.
+template <int LPV, class Body>
+__device__ __forceinline__ void for_vectors(int heads, Body body) {
+    constexpr int GROUPS = kMovers / LPV;
+    const int g = threadIdx.x / LPV, n = 2 * heads;
+    if (n <= GROUPS) {
+        const int dt = GROUPS / n, t = g / n, j = g - t * n;
+        if (t < dt) body(j >= heads, j >= heads ? j - heads : j, t, dt);
+    } else {
+        for (int j = g; j < n; j += GROUPS) body(j >= heads, j >= heads ? j - heads : j, 0, 1);
+    }
+}
+
+// Largest |x| of 8 loaded values, as the bits of a float32: an infinity or a NaN stays on top.
+__device__ __forceinline__ uint32_t abs_max8(uint4 v) {  // bf16
+    const uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+    return max(m << 16, m & 0xffff0000u);
+}
+
 // D / 8 lanes share a vector; E4M3: the cache is 8-bit; ABF: bf16 activations.
 template <int D, bool E4M3, bool ABF>
 __global__ void __launch_bounds__(kThreads) append_kernel(const MoveArgs a) {
-    __shared__ long where[kTokMax];
     constexpr int LPV = D / 8;
-    const int t0 = blockIdx.x * a.tok_per_cta;
-    const int nt = min(a.tok_per_cta, a.n_tokens - t0);
-    if (threadIdx.x < nt) where[threadIdx.x] = locate<false>(a, t0 + threadIdx.x);
-    __syncthreads();
     const int lane = threadIdx.x % LPV;
-    const int nvec = nt * 2 * a.heads;
-    for (int i = threadIdx.x / LPV; i < nvec; i += kThreads / LPV) {
-        const int h = i % a.heads, r = i / a.heads, w = r & 1, t = r >> 1;
-        const long base = where[t];
-        // the group of lanes that shares a vector takes the same branch
-        if (base < 0) continue;
-        float x[8];
-        load8(static_cast<const char*>(a.src[w]) +
-                  ((long)(t0 + t) * a.stride[w] + h * D + lane * 8) * (ABF ? 2 : 4),
-              ABF, x);
-        const long vec = base + ((long)h << a.ps_log2);
-        if (!E4M3) {
-            store8(static_cast<char*>(a.dst[w]) + (vec * D + lane * 8) * 2, true, x);
-            continue;
-        }
-        // the largest |x| by its bit pattern: an infinity or a NaN stays on top
-        uint32_t m = 0;
+    // the lanes of a vector take every branch together, and exchange among themselves
+    const unsigned group = ((1u << LPV) - 1u) << ((threadIdx.x & 31) / LPV * LPV);
+    for_blocks<false>(a, [&](int t0, int nt, const long* where) {
+        for_vectors<LPV>(a.heads, [&](int w, int h, int t1, int dt) {
+            const char* src = static_cast<const char*>(a.src[w]) +
+                              ((long)t0 * a.stride[w] + h * D + lane * 8) * (ABF ? 2 : 4);
+            char* dst = static_cast<char*>(a.dst[w]);
+            const long head = (long)h << a.ps_log2;
+            for (int t = t1; t < nt; t += kAhead * dt) {
+                uint4 x[kAhead][ABF ? 1 : 2];
+                long vec[kAhead];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(x[j]) & 0x7fffffffu);
-        const unsigned mask = LPV == 32 ? 0xffffffffu
-                                        : ((1u << LPV) - 1u) << ((threadIdx.x & 31) / LPV * LPV);
+                for (int u = 0; u < kAhead; ++u) {
+                    const int tu = t + u * dt;
+                    vec[u] = tu < nt ? where[tu] : -1;
 #pragma unroll
-        for (int o = LPV / 2; o >= 1; o >>= 1) m = max(m, __shfl_xor_sync(mask, m, o));
-        const bool finite = m < 0x7f800000u;
-        const float amax = fmaxf(__uint_as_float(m), kAmaxFloor);
-        // a vector that is not finite is marked by its scale; its values are stored as zeros
-        const float inv = __fdiv_rn(kE4M3Max, amax);
+                    for (int e = 0; e < (ABF ? 1 : 2); ++e) x[u][e] = make_uint4(0, 0, 0, 0);
+                    if (vec[u] >= 0) {
+                        const uint4* p = reinterpret_cast<const uint4*>(src + (long)tu * a.stride[w] * (ABF ? 2 : 4));
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = finite ? x[j] * inv : 0.f;
-        *reinterpret_cast<uint2*>(static_cast<char*>(a.dst[w]) + vec * D + lane * 8) = pack8_e4m3(x);
-        if (lane == 0)
-            a.scale[w][vec] = finite ? __fdiv_rn(amax, kE4M3Max) : __uint_as_float(0x7fc00000u);
-    }
+                        for (int e = 0; e < (ABF ? 1 : 2); ++e) x[u][e] = p[e];
+                    }
+                }
+                float scale = 0.f, inv = 0.f;
+                if (E4M3) {
+                    // Each lane of a vector's group takes one of the kAhead maxima, so that the
+                    // two divisions are made once for all of them.
+                    uint32_t mine = 0;
+#pragma unroll
+                    for (int u = 0; u < kAhead; ++u) {
+                        uint32_t m = 0;
+                        if (ABF) {
+                            m = abs_max8(x[u][0]);
+                        } else {
+                            const uint32_t* f = reinterpret_cast<const uint32_t*>(x[u]);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) m = max(m, f[e] & 0x7fffffffu);
+                        }
+#pragma unroll
+                        for (int o = LPV / 2; o >= 1; o >>= 1) m = max(m, __shfl_xor_sync(group, m, o));
+                        if ((lane & (kAhead - 1)) == u) mine = m;
+                    }
+                    // a vector that is not finite is marked by its scale; its values are stored
+                    // as zeros
+                    const bool finite = mine < 0x7f800000u;
+                    const float amax = fmaxf(__uint_as_float(mine), kAmaxFloor);
+                    scale = finite ? __fdiv_rn(amax, kE4M3Max) : __uint_as_float(0x7fc00000u);
+                    inv = finite ? __fdiv_rn(kE4M3Max, amax) : 0.f;
+                }
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    float f[8];
+                    load8(x[u], ABF, f);
+                    if (E4M3) {
+                        const float by = __shfl_sync(group, inv, u, LPV);
+                        if (vec[u] < 0) continue;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) f[e] = by == 0.f ? 0.f : f[e] * by;
+                        *reinterpret_cast<uint2*>(dst + (vec[u] + head) * D + lane * 8) = pack8_e4m3(f);
+                        if (lane == u) a.scale[w][vec[u] + head] = scale;
+                    } else if (vec[u] >= 0) {
+                        store8(dst + ((vec[u] + head) * D + lane * 8) * 2, true, f);
+                    }
+                }
+            }
+        });
+    });
 }
 
 template <int D, bool E4M3, bool OBF>
 __global__ void __launch_bounds__(kThreads) read_kernel(const MoveArgs a) {
-    __shared__ long where[kTokMax];
     constexpr int LPV = D / 8;
-    const int t0 = blockIdx.x * a.tok_per_cta;
-    const int nt = min(a.tok_per_cta, a.n_tokens - t0);
-    if (threadIdx.x < nt) where[threadIdx.x] = locate<true>(a, t0 + threadIdx.x);
-    __syncthreads();
     const int lane = threadIdx.x % LPV;
-    const int nvec = nt * 2 * a.heads;
-    for (int i = threadIdx.x / LPV; i < nvec; i += kThreads / LPV) {
-        const int h = i % a.heads, r = i / a.heads, w = r & 1, t = r >> 1;
-        const long base = where[t];
-        if (base < 0) continue;
-        const long vec = base + ((long)h << a.ps_log2);
-        float x[8];
-        if (E4M3) {
-            unpack8_e4m3(*reinterpret_cast<const uint2*>(static_cast<const char*>(a.src[w]) +
-                                                         vec * D + lane * 8),
-                         x);
-            const float sc = a.scale[w][vec];
+    for_blocks<true>(a, [&](int t0, int nt, const long* where) {
+        for_vectors<LPV>(a.heads, [&](int w, int h, int t1, int dt) {
+            const char* src = static_cast<const char*>(a.src[w]);
+            char* dst = static_cast<char*>(a.dst[w]) + (((long)t0 * a.heads + h) * D + lane * 8) * (OBF ? 2 : 4);
+            const long head = (long)h << a.ps_log2;
+            for (int t = t1; t < nt; t += kAhead * dt) {
+                uint4 raw[kAhead];  // 8 values: 8 bytes (in x, y) or 16
+                float sc[kAhead];
+                bool have[kAhead];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] *= sc;
-        } else {
-            load8(static_cast<const char*>(a.src[w]) + (vec * D + lane * 8) * 2, true, x);
-        }
-        store8(static_cast<char*>(a.dst[w]) +
-                   (((long)(t0 + t) * a.heads + h) * D + lane * 8) * (OBF ? 2 : 4),
-               OBF, x);
-    }
+                for (int u = 0; u < kAhead; ++u) {
+                    const long vec = t + u * dt < nt ? where[t + u * dt] : -1;
+                    have[u] = vec >= 0;
+                    if (!have[u]) continue;
+                    const char* p = src + ((vec + head) * D + lane * 8) * (E4M3 ? 1 : 2);
+                    if (E4M3) {
+                        const uint2 q = *reinterpret_cast<const uint2*>(p);
+                        raw[u] = make_uint4(q.x, q.y, 0, 0);
+                        sc[u] = a.scale[w][vec + head];
+                    } else {
+                        raw[u] = *reinterpret_cast<const uint4*>(p);
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    if (!have[u]) continue;
+                    float x[8];
+                    if (E4M3) {
+                        unpack8_e4m3(make_uint2(raw[u].x, raw[u].y), x);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) x[j] *= sc[u];
+                    } else {
+                        load8(&raw[u], true, x);
+                    }
+                    store8(dst + (long)(t + u * dt) * a.heads * D * (OBF ? 2 : 4), OBF, x);
+                }
+            }
+        });
+    });
 }
 
 __global__ void advance_kernel(const int32_t* cu, const int32_t* acc, const int32_t* ci,
@@ -206,13 +310,12 @@ __global__ void advance_kernel(const int32_t* cu, const int32_t* acc, const int3
     slot_len[s] = len + add;
 }
 
-// Tokens per CTA: few when the call is small, so that its vectors spread over the SMs;
-// kTokMax when there are enough CTAs all the same (one look-up per token either way).
-static int tokens_per_cta(const rssm_attn_dims* d, int n_tokens, int sm_count) {
-    const int per_pass = kThreads / (d->head_dim / 8);  // vectors a CTA moves at once
+// Tokens of a block: few when the call is small, so that its vectors spread over the SMs,
+// but a vector for every group of lanes; else kTokMax.
+static int block_tokens(const rssm_attn_dims* d, int n_tokens, int sm_count) {
+    const int groups = kMovers / (d->head_dim / 8);
     int tok = kTokMax;
-    while (tok > 1 && (n_tokens + tok - 1) / tok < 4 * sm_count &&
-           tok * 2 * d->num_kv_heads > per_pass)
+    while (tok > 1 && (n_tokens + tok - 1) / tok < 4 * sm_count && tok * 2 * d->num_kv_heads > groups)
         tok >>= 1;
     return tok;
 }
@@ -245,13 +348,13 @@ static MoveArgs move_args(const rssm_attn_dims* d, const rssm_attn_cache* c, int
     a.num_pages = d->num_pages;
     a.max_pages = d->max_pages;
     a.num_slots = d->num_slots;
-    a.tok_per_cta = tokens_per_cta(d, n_tokens, sm_count);
+    a.block = block_tokens(d, n_tokens, sm_count);
     return a;
 }
 
 template <bool READ, int D, bool E4M3>
-static void launch_move(const MoveArgs& a, bool dense_bf16, cudaStream_t st) {
-    const int grid = (a.n_tokens + a.tok_per_cta - 1) / a.tok_per_cta;
+static void launch_move(const MoveArgs& a, bool dense_bf16, int sm_count, cudaStream_t st) {
+    const int grid = min((a.n_tokens + a.block - 1) / a.block, kCtas * sm_count);
     if (READ) {
         if (dense_bf16) read_kernel<D, E4M3, true><<<grid, kThreads, 0, st>>>(a);
         else read_kernel<D, E4M3, false><<<grid, kThreads, 0, st>>>(a);
@@ -262,14 +365,14 @@ static void launch_move(const MoveArgs& a, bool dense_bf16, cudaStream_t st) {
 }
 
 template <bool READ>
-static int run_move(const rssm_attn_dims* d, const MoveArgs& a, int dense_dtype, cudaStream_t st) {
+static int run_move(const rssm_attn_dims* d, const MoveArgs& a, int dense_dtype, int sms, cudaStream_t st) {
     const bool bf = dense_dtype == RSSM_BF16, q = d->cache_dtype == RSSM_E4M3;
     if (d->head_dim == 64) {
-        if (q) launch_move<READ, 64, true>(a, bf, st);
-        else launch_move<READ, 64, false>(a, bf, st);
+        if (q) launch_move<READ, 64, true>(a, bf, sms, st);
+        else launch_move<READ, 64, false>(a, bf, sms, st);
     } else {
-        if (q) launch_move<READ, 128, true>(a, bf, st);
-        else launch_move<READ, 128, false>(a, bf, st);
+        if (q) launch_move<READ, 128, true>(a, bf, sms, st);
+        else launch_move<READ, 128, false>(a, bf, sms, st);
     }
     return launch_status();
 }
@@ -297,7 +400,7 @@ extern "C" int rssm_attn_append(const rssm_attn_dims* d, const rssm_attn_cache* 
     a.dst[1] = c->v;
     a.stride[0] = k_stride;
     a.stride[1] = v_stride;
-    return attn::run_move<false>(d, a, d->act_dtype, (cudaStream_t)stream);
+    return attn::run_move<false>(d, a, d->act_dtype, di.sm_count, (cudaStream_t)stream);
 }
 
 extern "C" int rssm_attn_read(const rssm_attn_dims* d, const rssm_attn_cache* c, int32_t n_tokens,
@@ -315,7 +418,7 @@ extern "C" int rssm_attn_read(const rssm_attn_dims* d, const rssm_attn_cache* c,
     a.dst[0] = k_out;
     a.dst[1] = v_out;
     a.first = first;
-    return attn::run_move<true>(d, a, d->out_dtype, (cudaStream_t)stream);
+    return attn::run_move<true>(d, a, d->out_dtype, di.sm_count, (cudaStream_t)stream);
 }
 
 extern "C" int rssm_attn_advance(const rssm_attn_dims* d, const rssm_attn_cache* c,

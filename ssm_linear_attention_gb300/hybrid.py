@@ -71,7 +71,7 @@ class PagedAttentionDecoder:
         self.dev_err = torch.zeros(4, device=dev, dtype=torch.int32)
         self.cache = B.attn_cache(self.k_cache, self.v_cache, self.k_scale, self.v_scale,
                                   self.page_table, self.slot_len)
-        self._dims = {}
+        self._plans = {}
         self.ws_bytes = B.rssm_attn_workspace_size(self.dims(max_batch))
         # zero-filled: the decode call keeps its arrival counters here
         self.workspace = torch.zeros(max(self.ws_bytes, 16), device=dev, dtype=torch.uint8)
@@ -79,17 +79,25 @@ class PagedAttentionDecoder:
         self.lse = torch.empty(max_batch, T, num_q_heads, device=dev, dtype=torch.float32)
 
     def dims(self, batch):
-        d = self._dims.get(batch)
-        if d is None:
-            d = self._dims[batch] = B.AttnDims(
-                batch, self.T, self.HQ, self.HKV, self.D, self.page_size, self.num_pages,
-                self.max_pages, self.num_slots, torch_dtype_code(self.act_dtype),
-                _code(self.cache_dtype), torch_dtype_code(self.out_dtype))
-        return d
+        return B.AttnDims(batch, self.T, self.HQ, self.HKV, self.D, self.page_size, self.num_pages,
+                          self.max_pages, self.num_slots, torch_dtype_code(self.act_dtype),
+                          _code(self.cache_dtype), torch_dtype_code(self.out_dtype))
+
+    def _plan(self, b):
+        """What calls of b rows share: dims, the shape of q, the outputs. Kept, because a
+        small call's time is the host's."""
+        p = self._plans.get(b)
+        if p is None:
+            p = self._plans[b] = (self.dims(b), torch.Size((b, self.T, self.HQ, self.D)),
+                                  self.o[:b], self.lse[:b])
+        return p
 
     def _stride(self, name, t, heads):
         """Element distance between consecutive tokens of t [tokens, heads, D] or
         [rows, T, heads, D]."""
+        if t.dtype is self.act_dtype and t.is_contiguous() and t.shape[-2] == heads and \
+                t.shape[-1] == self.D:
+            return heads * self.D
         s, n = t.stride(), t.shape
         if t.dtype != self.act_dtype or n[-2:] != (heads, self.D) or s[-1] != 1 or \
                 (s[-2] != self.D and heads > 1) or \
@@ -104,7 +112,7 @@ class PagedAttentionDecoder:
         n = k.numel() // (self.HKV * self.D)
         if v.shape != k.shape:
             raise ValueError("k and v must have one shape")
-        B.rssm_attn_append(self.dims(cache_indices.shape[0]), self.cache, n, cu_tokens, k,
+        B.rssm_attn_append(self._plan(cache_indices.shape[0])[0], self.cache, n, cu_tokens, k,
                            self._stride("k", k, self.HKV), v, self._stride("v", v, self.HKV),
                            cache_indices, self.dev_err, stream)
 
@@ -113,21 +121,22 @@ class PagedAttentionDecoder:
         """Attention of q [b, T, HQ, D] over the rows' tokens. appended: the queries' own
         tokens are in the cache and visible (see rssm_attn_decode). Returns o [b, T, HQ, D],
         with with_lse also lse [b, T, HQ]."""
-        b = cache_indices.shape[0]
-        if b > self.max_batch or q.numel() != b * self.T * self.HQ * self.D:
+        dims, shape, own_o, own_lse = self._plan(cache_indices.shape[0])
+        if dims.batch > self.max_batch or q.numel() != shape.numel():
             raise ValueError("q must be [b, %d, %d, %d], b = len(cache_indices) <= %d"
                              % (self.T, self.HQ, self.D, self.max_batch))
-        o = self.o[:b] if o is None else o
+        if o is None:
+            o = own_o
         if lse is None and with_lse:
-            lse = self.lse[:b]
-        B.rssm_attn_decode(self.dims(b), self.cache, appended, self.scale, self.window, q,
+            lse = own_lse
+        B.rssm_attn_decode(dims, self.cache, appended, self.scale, self.window, q,
                            self._stride("q", q, self.HQ), cache_indices, self.workspace,
                            self.ws_bytes, o, lse, self.dev_err, stream)
         return (o, lse) if with_lse else o
 
     def advance(self, cache_indices, num_accepted=None, cu_tokens=None, stream=None):
         """Commit the appended tokens (of T drafts: the first num_accepted[b])."""
-        B.rssm_attn_advance(self.dims(cache_indices.shape[0]), self.cache, cu_tokens, num_accepted,
+        B.rssm_attn_advance(self._plan(cache_indices.shape[0])[0], self.cache, cu_tokens, num_accepted,
                             cache_indices, self.dev_err, stream)
 
     def step(self, q, k, v, cache_indices, o=None, stream=None):
@@ -144,8 +153,8 @@ class PagedAttentionDecoder:
             k = torch.empty(n_tokens, self.HKV, self.D, device=self.device, dtype=self.out_dtype)
         if v is None:
             v = torch.empty_like(k)
-        B.rssm_attn_read(self.dims(cache_indices.shape[0]), self.cache, n_tokens, cu_tokens, first,
-                         cache_indices, k, v, self.dev_err, stream)
+        B.rssm_attn_read(self._plan(cache_indices.shape[0])[0], self.cache, n_tokens, cu_tokens,
+                         first, cache_indices, k, v, self.dev_err, stream)
         return k, v
 
     def reset_slots(self, slots, stream=None):
@@ -171,30 +180,36 @@ class AddRMSNorm:
         if out_dtype == torch.float8_e4m3fn:
             groups = self.cols // scale_group if scale_group else 1
             self.scale = torch.empty(max_rows, groups, device=dev, dtype=torch.float32)
-        self._dims = {}
+        self._plans = {}
 
     def dims(self, rows):
-        d = self._dims.get(rows)
-        if d is None:
-            d = self._dims[rows] = B.NormDims(rows, self.cols, self.scale_group,
-                                              torch_dtype_code(self.act_dtype),
-                                              _code(self.out_dtype))
-        return d
+        return B.NormDims(rows, self.cols, self.scale_group, torch_dtype_code(self.act_dtype),
+                          _code(self.out_dtype))
+
+    def _plan(self, rows):
+        p = self._plans.get(rows)
+        if p is None:
+            p = self._plans[rows] = (self.dims(rows), self.y[:rows],
+                                     None if self.scale is None else self.scale[:rows])
+        return p
 
     def __call__(self, x, residual=None, residual_out=None, y=None, scale=None, stream=None):
         """Returns (y, scale) (scale None unless y is 8-bit). residual_out None: the sum
         replaces residual (without a residual it is not stored)."""
-        rows = x.numel() // self.cols
-        if rows * self.cols != x.numel() or (y is None and rows > self.max_rows):
+        n = x.numel()
+        rows = n // self.cols
+        if rows * self.cols != n or (y is None and rows > self.max_rows):
             raise ValueError("x must be [rows, %d], rows <= %d" % (self.cols, self.max_rows))
         for t in (x, residual, residual_out):
-            if t is not None and (t.dtype != self.act_dtype or t.numel() != x.numel() or
+            if t is not None and (t.dtype is not self.act_dtype or t.numel() != n or
                                   not t.is_contiguous()):
                 raise ValueError("x and the residuals: dense [rows, %d] %s" % (self.cols,
                                                                                self.act_dtype))
-        y = self.y[:rows] if y is None else y
-        if scale is None and self.scale is not None:
-            scale = self.scale[:rows]
-        B.rssm_add_rmsnorm(self.dims(rows), x, residual, self.weight, self.eps,
+        dims, own_y, own_scale = self._plan(rows)
+        if y is None:
+            y = own_y
+        if scale is None:
+            scale = own_scale
+        B.rssm_add_rmsnorm(dims, x, residual, self.weight, self.eps,
                            residual if residual_out is None else residual_out, y, scale, stream)
         return y, scale
