@@ -19,7 +19,7 @@ namespace attn {
 constexpr int kMovers = 256;          // threads that move vectors
 constexpr int kThreads = kMovers + 32;  // and the warp that looks tokens up
 constexpr int kTokMax = 32;            // tokens of a block: one per lane of that warp
-constexpr int kCtas = 4;               // of an SM
+constexpr int kCtas = 4;               // of an SM: 3 or 5 cost 8 to 27 % on the large cases
 constexpr int kAhead = 4;              // vectors whose loads a thread has in flight
 
 struct MoveArgs {
@@ -172,7 +172,7 @@ __device__ __forceinline__ uint32_t abs_max8(uint4 v) {  // bf16
 
 // D / 8 lanes share a vector; E4M3: the cache is 8-bit; ABF: bf16 activations.
 template <int D, bool E4M3, bool ABF>
-__global__ void __launch_bounds__(kThreads) append_kernel(const MoveArgs a) {
+__global__ void __launch_bounds__(kThreads, kCtas) append_kernel(const MoveArgs a) {
     constexpr int LPV = D / 8;
     const int lane = threadIdx.x % LPV;
     // the lanes of a vector take every branch together, and exchange among themselves
@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const MoveArgs a) {
 }
 
 template <int D, bool E4M3, bool OBF>
-__global__ void __launch_bounds__(kThreads) read_kernel(const MoveArgs a) {
+__global__ void __launch_bounds__(kThreads, kCtas) read_kernel(const MoveArgs a) {
     constexpr int LPV = D / 8;
     const int lane = threadIdx.x % LPV;
     for_blocks<true>(a, [&](int t0, int nt, const long* where) {

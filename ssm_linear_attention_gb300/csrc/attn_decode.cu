@@ -302,6 +302,7 @@ struct Partial {
         if (with_lse && a.lse) a.lse[r] = none ? -INFINITY : (ml.x + log2f(ml.y)) * kLn2;
     }
 };
+constexpr int kItems = 4;  // of a CTA's join that a thread has in flight
 constexpr int kJoin = 8;  // partial results whose loads a thread has in flight
 
 // A run: the consecutive records (partial results of groups) of one (row, head) in a CTA.
@@ -1118,30 +1119,39 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
     // head, its last record, in global memory.
     const int nv = a.M * (D / 4);
 #pragma unroll 1
-    for (int item = tid; item < nruns * nv; item += kDecThreads) {
-        const Run& r = runs[item / nv];
-        const int v = item % nv, row = v / (D / 4), d = (v % (D / 4)) * 4;
-        const int last = r.rec1 - 1;
-        const bool head = !(last & 1);
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (head) {
+    for (int item0 = tid; item0 < nruns * nv; item0 += kItems * kDecThreads) {
+        float4 x[kItems];  // the heads, whose loads start together
+#pragma unroll
+        for (int u = 0; u < kItems; ++u) {
+            const int item = item0 + u * kDecThreads;
+            x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (item >= nruns * nv) continue;
+            const int last = runs[item / nv].rec1 - 1;
             const long slot = 2L * gridDim.x + (int)blockIdx.x * kWarps + (last >> 1);
-            x = *reinterpret_cast<const float4*>(a.part + (slot * a.M + row) * D + d);
+            if (!(last & 1)) x[u] = *reinterpret_cast<const float4*>(a.part + slot * a.M * D + item % nv * 4);
         }
-        Partial acc;
+#pragma unroll
+        for (int u = 0; u < kItems; ++u) {
+            const int item = item0 + u * kDecThreads;
+            if (item >= nruns * nv) continue;
+            const Run& r = runs[item / nv];
+            const int v = item % nv, row = v / (D / 4), d = (v % (D / 4)) * 4;
+            const int last = r.rec1 - 1;
+            Partial acc;
 #pragma unroll 1
-        for (int k = r.rec0 | 1; k < r.rec1; k += 2)
-            if (rec_b[k] >= 0)
-                acc.add(rec_ml[k * a.M + row],
-                        *reinterpret_cast<const float4*>(tail + ((k >> 1) * a.M + row) * C::TD + d));
-        if (head) acc.add(rec_ml[last * a.M + row], x);
-        if (r.cta0 == r.cta1) {
-            const long out = out_row(a, r.b, r.h, row);
-            acc.store(a, out, out * D + d, d == 0);
-        } else {
-            const long slot = 2L * blockIdx.x + (r.cta0 < (int)blockIdx.x ? 0 : 1);
-            *reinterpret_cast<float4*>(a.part + (slot * a.M + row) * D + d) = acc.v;
-            if (d == 0) reinterpret_cast<float2*>(a.part_ml)[slot * a.M + row] = acc.ml;
+            for (int k = r.rec0 | 1; k < r.rec1; k += 2)
+                if (rec_b[k] >= 0)
+                    acc.add(rec_ml[k * a.M + row],
+                            *reinterpret_cast<const float4*>(tail + ((k >> 1) * a.M + row) * C::TD + d));
+            if (!(last & 1)) acc.add(rec_ml[last * a.M + row], x[u]);
+            if (r.cta0 == r.cta1) {
+                const long out = out_row(a, r.b, r.h, row);
+                acc.store(a, out, out * D + d, d == 0);
+            } else {
+                const long slot = 2L * blockIdx.x + (r.cta0 < (int)blockIdx.x ? 0 : 1);
+                *reinterpret_cast<float4*>(a.part + (slot * a.M + row) * D + d) = acc.v;
+                if (d == 0) reinterpret_cast<float2*>(a.part_ml)[slot * a.M + row] = acc.ml;
+            }
         }
     }
 
