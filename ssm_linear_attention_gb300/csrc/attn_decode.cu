@@ -98,18 +98,20 @@ __device__ __forceinline__ void cp_async16_hint(uint32_t dst, const void* src, u
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
+// (or some fewer: 0, 1, 2, 4 and 6 are told apart)
 __device__ __forceinline__ void cp_async_wait_but(int n) {
-    switch (n) {
-        case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
-        case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
-        case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
-        case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
-        case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
-        case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
-        case 6: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
-        default: asm volatile("cp.async.wait_group 7;" ::: "memory"); break;
+    if (n >= 4) {
+        if (n >= 6) asm volatile("cp.async.wait_group 6;" ::: "memory");
+        else asm volatile("cp.async.wait_group 4;" ::: "memory");
+    } else if (n >= 2) {
+        asm volatile("cp.async.wait_group 2;" ::: "memory");
+    } else if (n == 1) {
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+    } else {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
 }
+// True on one lane of the (whole) warp.
 __device__ __forceinline__ bool elect_one() {
     uint32_t ok;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
@@ -145,6 +147,13 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
 __device__ __forceinline__ float log2_fast(float x) {
     float y;
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 1 / x to 1 ulp of float32
+__device__ __forceinline__ float reciprocal(float x) {
+    float y;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 
@@ -268,12 +277,6 @@ __device__ __noinline__ int locate_tile(const DecArgs& a, const Rows& rows, uint
     return ((page * a.hkv + x.h) << a.ps_log2) + (pos & ((1 << a.ps_log2) - 1));
 }
 
-// o and lse of query row r of (b, h): elements d, d + 1.
-__device__ __noinline__ long out_row(const DecArgs& a, int b, int h, int r) {
-    const int j = r / a.G;
-    return ((long)b * a.T + j) * a.hq + h * a.G + (r - j * a.G);
-}
-
 // A partial result of one query over four columns: (m, l) and O. Adding one rescales to
 // the larger m; a sum's order is that of the adds.
 struct Partial {
@@ -288,22 +291,22 @@ struct Partial {
         v.z = v.z * f + x.z * g;
         v.w = v.w * f + x.w * g;
     }
-    // o at element e: O / l, zeros where nothing was seen; lse of output row r.
-    __device__ __forceinline__ void store(const DecArgs& a, long r, long e, bool with_lse) const {
-        const bool none = ml.y == 0.f;
-        const float inv = none ? 0.f : 1.f / ml.y;
-        const float y[4] = {none ? 0.f : v.x * inv, none ? 0.f : v.y * inv, none ? 0.f : v.z * inv,
-                            none ? 0.f : v.w * inv};
-        if (a.obf)
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + e) =
-                make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
-        else
-            *reinterpret_cast<float4*>(static_cast<float*>(a.o) + e) = make_float4(y[0], y[1], y[2], y[3]);
-        if (with_lse && a.lse) a.lse[r] = none ? -INFINITY : (ml.x + log2f(ml.y)) * kLn2;
-    }
 };
-constexpr int kItems = 4;  // of a CTA's join that a thread has in flight
-constexpr int kJoin = 8;  // partial results whose loads a thread has in flight
+// Columns d .. d + 3 of output row r: O / l, zeros where nothing was seen; its lse.
+__device__ __noinline__ void store_partial(const DecArgs& a, const Partial p, long r, int D, int d) {
+    const bool none = p.ml.y == 0.f;
+    const float inv = none ? 0.f : reciprocal(p.ml.y);
+    const float y[4] = {none ? 0.f : p.v.x * inv, none ? 0.f : p.v.y * inv, none ? 0.f : p.v.z * inv,
+                        none ? 0.f : p.v.w * inv};
+    if (a.obf)
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + r * D + d) =
+            make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+    else
+        *reinterpret_cast<float4*>(static_cast<float*>(a.o) + r * D + d) = make_float4(y[0], y[1], y[2], y[3]);
+    if (d == 0 && a.lse) a.lse[r] = none ? -INFINITY : (p.ml.x + log2_fast(p.ml.y)) * kLn2;
+}
+constexpr int kItems = 2;  // of a CTA's join that a thread has in flight
+constexpr int kJoin = 4;  // partial results whose loads a thread has in flight
 
 // A run: the consecutive records (partial results of groups) of one (row, head) in a CTA.
 struct Run {
@@ -396,6 +399,8 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
     float* st_scale = reinterpret_cast<float*>(st_kv + (size_t)nst * C::STAGE);
     uint64_t* full = reinterpret_cast<uint64_t*>(st_kv + (size_t)nst * (C::STAGE + C::AUX));
     __shared__ int abort_flag;
+    __shared__ int q_row[64];  // query r of a key head among its row's T HQ: token * HQ + r % G
+    __shared__ int q_tok[64];  // its token
     __shared__ uint2 scan[kWarps];  // tiles and longest row of the warps' rows
     __shared__ int rec_b[2 * kWarps], rec_h[2 * kWarps];  // records; b < 0: none
     __shared__ Run runs[2 * kWarps];
@@ -414,6 +419,11 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
         }
     }
     if (tid < 2 * kWarps) rec_b[tid] = -1;
+    if (tid < a.M) {
+        const int j = tid / a.G;
+        q_tok[tid] = j;
+        q_row[tid] = j * a.hq + tid - j * a.G;
+    }
     if (tid == 0) runs[0].cta0 = runs[0].cta1 = 0;
 
     // ------------------------------------------------------- the call's tile list
@@ -617,14 +627,15 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
                         rec_h[2 * group + (tail ? 1 : 0)] = ch;
                     }
                     if (whole) {
+                        const long out0 = (long)cb * a.T * a.hq + ch * a.G;
 #pragma unroll
                         for (int q = 0; q < NQ; ++q) {
-                            const float i0 = l[q][0] == 0.f ? 0.f : 1.f / l[q][0];
-                            const float i1 = l[q][1] == 0.f ? 0.f : 1.f / l[q][1];
+                            const float i0 = l[q][0] == 0.f ? 0.f : reciprocal(l[q][0]);
+                            const float i1 = l[q][1] == 0.f ? 0.f : reciprocal(l[q][1]);
                             if (a.obf) {
                                 // transposed, a lane has two columns of query n8
                                 const int r = q0 + 8 * q + n8;
-                                const long row = r < a.M ? out_row(a, cb, ch, r) : 0;
+                                const long row = r < a.M ? out0 + q_row[r] : 0;
                                 uint16_t* dst = static_cast<uint16_t*>(a.o) + row * D;
 #pragma unroll
                                 for (int c = 0; c < C::DB; ++c) {
@@ -650,7 +661,7 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
                             for (int x = 0; x < 2; ++x) {
                                 const int r = q0 + 8 * q + 2 * qd + x;
                                 if (r >= a.M) continue;
-                                const long row = out_row(a, cb, ch, r);
+                                const long row = out0 + q_row[r];
                                 const bool none = l[q][x] == 0.f;
                                 if (!a.obf) {
                                     float* dst = static_cast<float*>(a.o) + row * D;
@@ -661,7 +672,7 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
                                     }
                                 }
                                 if (a.lse && n8 == 0)
-                                    a.lse[row] = none ? -INFINITY : (m[q][x] + log2f(l[q][x])) * kLn2;
+                                    a.lse[row] = none ? -INFINITY : (m[q][x] + log2_fast(l[q][x])) * kLn2;
                             }
                         }
                     } else if (!tail) {
@@ -706,7 +717,7 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         const int r = q0 + 8 * q + 2 * qd + x;
-                        const int e = len + (app ? (r < a.M ? r / a.G : 0) + 1 : 0);
+                        const int e = len + (app ? (r < a.M ? q_tok[r] : 0) + 1 : 0);
                         end[q][x] = e;
                         beg[q][x] = a.window && e > a.window ? e - a.window : 0;
                         m[q][x] = -INFINITY;
@@ -714,7 +725,7 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
                         rs[q][x] = a.qscale;
                     }
                     const int r = q0 + 8 * q + n8;  // the query whose operand values this lane has
-                    const int j = r < a.M ? r / a.G : 0;
+                    const int j = r < a.M ? q_tok[r] : 0;
                     const long base = ((long)cb * a.T + j) * a.q_stride + (ch * a.G + (r - j * a.G)) * D;
                     float v[D / 16][4];
 #pragma unroll
@@ -1119,38 +1130,37 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
     // head, its last record, in global memory.
     const int nv = a.M * (D / 4);
 #pragma unroll 1
-    for (int item0 = tid; item0 < nruns * nv; item0 += kItems * kDecThreads) {
-        float4 x[kItems];  // the heads, whose loads start together
-#pragma unroll
-        for (int u = 0; u < kItems; ++u) {
-            const int item = item0 + u * kDecThreads;
-            x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (item >= nruns * nv) continue;
-            const int last = runs[item / nv].rec1 - 1;
-            const long slot = 2L * gridDim.x + (int)blockIdx.x * kWarps + (last >> 1);
-            if (!(last & 1)) x[u] = *reinterpret_cast<const float4*>(a.part + slot * a.M * D + item % nv * 4);
-        }
-#pragma unroll
-        for (int u = 0; u < kItems; ++u) {
-            const int item = item0 + u * kDecThreads;
-            if (item >= nruns * nv) continue;
-            const Run& r = runs[item / nv];
-            const int v = item % nv, row = v / (D / 4), d = (v % (D / 4)) * 4;
-            const int last = r.rec1 - 1;
-            Partial acc;
+    for (int i = 0; i < nruns; ++i) {
+        const Run r = runs[i];
+        const int last = r.rec1 - 1;
+        const float* head = a.part + (2L * gridDim.x + (int)blockIdx.x * kWarps + (last >> 1)) * a.M * D;
+        const long slot = 2L * blockIdx.x + (r.cta0 < (int)blockIdx.x ? 0 : 1);
 #pragma unroll 1
-            for (int k = r.rec0 | 1; k < r.rec1; k += 2)
-                if (rec_b[k] >= 0)
-                    acc.add(rec_ml[k * a.M + row],
-                            *reinterpret_cast<const float4*>(tail + ((k >> 1) * a.M + row) * C::TD + d));
-            if (!(last & 1)) acc.add(rec_ml[last * a.M + row], x[u]);
-            if (r.cta0 == r.cta1) {
-                const long out = out_row(a, r.b, r.h, row);
-                acc.store(a, out, out * D + d, d == 0);
-            } else {
-                const long slot = 2L * blockIdx.x + (r.cta0 < (int)blockIdx.x ? 0 : 1);
-                *reinterpret_cast<float4*>(a.part + (slot * a.M + row) * D + d) = acc.v;
-                if (d == 0) reinterpret_cast<float2*>(a.part_ml)[slot * a.M + row] = acc.ml;
+        for (int v0 = tid; v0 < nv; v0 += kItems * kDecThreads) {
+            float4 x[kItems];  // the heads, whose loads start together
+#pragma unroll
+            for (int u = 0; u < kItems; ++u) {
+                const int v = v0 + u * kDecThreads;
+                if (v < nv && !(last & 1)) x[u] = *reinterpret_cast<const float4*>(head + v * 4);
+            }
+#pragma unroll
+            for (int u = 0; u < kItems; ++u) {
+                const int v = v0 + u * kDecThreads;
+                if (v >= nv) break;
+                const int row = v / (D / 4), d = (v % (D / 4)) * 4;
+                Partial acc;
+#pragma unroll 1
+                for (int k = r.rec0 | 1; k < r.rec1; k += 2)
+                    if (rec_b[k] >= 0)
+                        acc.add(rec_ml[k * a.M + row],
+                                *reinterpret_cast<const float4*>(tail + ((k >> 1) * a.M + row) * C::TD + d));
+                if (!(last & 1)) acc.add(rec_ml[last * a.M + row], x[u]);
+                if (r.cta0 == r.cta1) {
+                    store_partial(a, acc, (long)r.b * a.T * a.hq + r.h * a.G + q_row[row], D, d);
+                } else {
+                    *reinterpret_cast<float4*>(a.part + slot * a.M * D + v * 4) = acc.v;
+                    if (d == 0) reinterpret_cast<float2*>(a.part_ml)[slot * a.M + row] = acc.ml;
+                }
             }
         }
     }
@@ -1206,8 +1216,7 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
             if (parts > 1) {
                 jp[tid] = acc;
             } else {
-                const long out = out_row(a, r.b, r.h, row);
-                acc.store(a, out, out * D + d, d == 0);
+                store_partial(a, acc, (long)r.b * a.T * a.hq + r.h * a.G + q_row[row], D, d);
             }
         }
         if (parts > 1) {
@@ -1217,8 +1226,7 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
 #pragma unroll 1
                 for (int i = 1; i < parts; ++i) acc.add(jp[i * nv + tid].ml, jp[i * nv + tid].v);
                 const int row = tid / (D / 4), d = (tid % (D / 4)) * 4;
-                const long out = out_row(a, r.b, r.h, row);
-                acc.store(a, out, out * D + d, d == 0);
+                store_partial(a, acc, (long)r.b * a.T * a.hq + r.h * a.G + q_row[row], D, d);
             }
             __syncthreads();
         }
@@ -1248,7 +1256,7 @@ static int launch_kernel(const rssm_attn_dims* d, DecArgs a, const DeviceInfo& d
     const int fixed = kRowBytes + 1024;
     const int per = C::STAGE + C::AUX + 8;
     // what the kernel's static arrays take: (m, l) of the records, and the lists
-    const int statics = C::WARPS * (128 + 2 * (int)sizeof(Run) + 24) + 256;
+    const int statics = C::WARPS * (128 + 2 * (int)sizeof(Run) + 24) + 768;
     const int budget = di.max_smem_optin - statics - fixed;
     // a ring holds a step's tiles at least, and those of the step before where warps share them
     const int least = (SHARE ? 2 : 1) * C::TP;
