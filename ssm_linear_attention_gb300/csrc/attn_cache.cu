@@ -53,7 +53,7 @@ __device__ __forceinline__ int row_of(const MoveArgs& a, int t, int* in_row) {
         const int v = __shfl_sync(0xffffffffu, mine, piece + w - 1);
         if (v <= t) piece += w;
     }
-    if (__shfl_sync(0xffffffffu, mine, piece) <= t) return -1;
+    if (__shfl_sync(0xffffffffu, mine, piece) <= t || piece * step >= a.batch) return -1;
     int lo = piece * step, hi = min(lo + step, a.batch) - 1;  // first b in [lo, hi] with cu[b + 1] > t
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;

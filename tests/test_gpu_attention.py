@@ -164,6 +164,7 @@ CASES = [
     (300, [(91 * i) % 40 for i in range(300)], dict(hkv=4, hq=32, cache=FP8, page=32)),
     (5, [3000, 1, 40, 2999, 16], dict(hq=64, hkv=4, T=4, page=16)),
     (2, [600, 47], dict(out=torch.float32)),
+    (1100, [(53 * i) % 35 for i in range(1100)], dict(hkv=2, hq=2, d=64, cache=FP8)),
 ]
 
 
