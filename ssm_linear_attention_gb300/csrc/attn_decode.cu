@@ -348,6 +348,13 @@ struct Cfg {
     }
 };
 
+// Two float32 as a bf16 pair, one conversion.
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 // Split v0, v1 into bf16 (f16) pairs: part i is the rounding of what the parts before it
 // leave.
 template <int N, bool F16>
@@ -362,7 +369,7 @@ __device__ __forceinline__ void split2(float v0, float v1, uint32_t* out) {
                 v1 -= __high2float(h);
             }
         } else {
-            const uint32_t p = pack_bf16x2(v0, v1);
+            const uint32_t p = pack2(v0, v1);
             out[i] = p;
             if (i + 1 < N) {
                 v0 -= bf16_lo(p);
@@ -542,6 +549,14 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
         uint32_t bad = 0;  // stages whose tile has no page
         uint64_t* fb = full + group * stages;
         uint32_t parity = 0;  // of the stages' barriers, a bit each
+        constexpr int LPR = C::ROWB / 16, TPI = 32 / LPR;  // cp.async: lanes of a token, tokens at once
+        constexpr int INSTR = kTok / TPI;                  // instructions of a tile's k (or v)
+        constexpr int ROWS = C::ROWB >= 128 ? TPI : TPI / 2;  // 128-byte rows of one
+        const int share = !SHARE ? INSTR : INSTR / MT > 0 ? INSTR / MT : mt < INSTR ? 1 : 0;
+        const int tok0 = (mt < INSTR ? mt * share : 0) * TPI + lane / LPR;
+        const char* k_lane = a.k + (long)tok0 * C::ROWB + lane % LPR * 16;
+        const long v_minus_k = a.v - a.k;
+        const uint32_t st_base = smem_addr(kv) + tile_off<C::ROWB>(tok0, lane % LPR);
         auto issue = [&]() {
             if (sent < ntile) {
                 if ((sent & 31) == 0 && sent + lane < ntile) look = locate_tile(a, rows, t0 + sent + lane);
@@ -568,20 +583,16 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
                         }
                     }
                 } else if (y >= 0) {
-                    constexpr int LPR = C::ROWB / 16, TPI = 32 / LPR;  // lanes of a token, tokens at once
-                    const uint32_t dst = smem_addr(kv + (size_t)sent_s * C::STAGE);
-                    const long src = ((long)y + lane / LPR) * C::ROWB + (lane % LPR) * 16;
-                    auto copy = [&](int j) {
-                        const uint32_t to = dst + tile_off<C::ROWB>(j * TPI + lane / LPR, lane % LPR);
-                        cp_async16_hint(to, a.k + src + (long)j * TPI * C::ROWB, pol);
-                        cp_async16_hint(to + C::KB, a.v + src + (long)j * TPI * C::ROWB, pol);
-                    };
-                    if (!SHARE) {
+                    // instruction j copies tokens TPI j .. of k and of v; the swizzle makes a step of j
+                    // an exclusive or of the chunk bits
+                    const uint32_t dst = st_base + sent_s * C::STAGE;
+                    const char* src = k_lane + (long)y * C::ROWB;
 #pragma unroll
-                        for (int j = 0; j < kTok / TPI; ++j) copy(j);
-                    } else {
-#pragma unroll 1
-                        for (int j = mt; j < kTok / TPI; j += MT) copy(j);
+                    for (int j = 0; j < (SHARE ? (INSTR + 1) / 2 : INSTR); ++j) {
+                        if (SHARE && j >= share) break;
+                        const uint32_t to = (dst ^ (uint32_t)(j * ROWS % 8 * 16)) + j * ROWS * 128;
+                        cp_async16_hint(to, src + j * TPI * C::ROWB, pol);
+                        cp_async16_hint(to + C::KB, src + v_minus_k + j * TPI * C::ROWB, pol);
                     }
                     if (E4M3 && leader)
                         cp_async4(smem_addr(sc + sent_s * 2 * kTok + lane),
@@ -645,8 +656,8 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
                                         const bool none = l[q][x & 1] == 0.f;
                                         v[x] = none ? 0.f : o[c][q][x] * (x & 1 ? i1 : i0);
                                     }
-                                    uint32_t lo = transpose8(pack_bf16x2(v[0], v[1]));
-                                    uint32_t hi = transpose8(pack_bf16x2(v[2], v[3]));
+                                    uint32_t lo = transpose8(pack2(v[0], v[1]));
+                                    uint32_t hi = transpose8(pack2(v[2], v[3]));
                                     if (r >= a.M) continue;
                                     if (E4M3) {  // even and odd columns 4 qd .. 4 qd + 3
                                         *reinterpret_cast<uint2*>(dst + 16 * c + 4 * qd) = make_uint2(
