@@ -582,7 +582,7 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
                             asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&fb[sent_s])) : "memory");
                         }
                     }
-                } else if (y >= 0) {
+                } else if (__all_sync(0xffffffffu, y >= 0)) {
                     // instruction j copies tokens TPI j .. of k and of v; the swizzle makes a step of j
                     // an exclusive or of the chunk bits
                     const uint32_t dst = st_base + sent_s * C::STAGE;
@@ -877,10 +877,9 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
                 // weight as log2(scale) in the exponent: m bounds those sums, the weights stay
                 // in f16's range, and l, which wants the scores alone, divides it out again.
                 float p[C::TP][NQ][4], iv[C::TP][2];
-                bool edge[C::TP], grow = false;
+                bool edge[C::TP], edges = false, grow = false;
 #pragma unroll
                 for (int u = 0; u < C::TP; ++u) {
-                    const int pos = t[u].x;
                     float ks[2] = {1.f, 1.f}, lv[2] = {0.f, 0.f};
                     if (E4M3) {
                         const float* ts = sc + st[u] * 2 * kTok + n8;
@@ -894,7 +893,8 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
                         }
                     }
                     // a tile that is not there (or has no page) is all hidden
-                    edge[u] = t[u].y < 0 || pos + kTok > n_min || pos < b_max;
+                    edge[u] = t[u].y < 0 || t[u].x + kTok > n_min || t[u].x < b_max;
+                    edges = edges || edge[u];
 #pragma unroll
                     for (int q = 0; q < NQ; ++q)
 #pragma unroll
@@ -902,15 +902,27 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
                             float f = SA == 2 ? sa[u][0][q][x] + sa[u][SA - 1][q][x] : sa[u][0][q][x];
                             f *= rs[q][x & 1];
                             if (E4M3) f = f * ks[x >> 1] + lv[x >> 1];
-                            if (edge[u]) {
-                                const int tok = pos + n8 + 8 * (x >> 1);
-                                // whatever the cache holds there
-                                if (tok >= end[q][x & 1] || tok < beg[q][x & 1] || t[u].y < 0) f = -INFINITY;
-                            }
                             p[u][q][x] = f;
-                            grow |= f > m[q][x & 1] + kSlack;
                         }
                 }
+                if (__builtin_expect(edges, 0)) {  // hide what a query does not see, whatever it holds
+#pragma unroll
+                    for (int u = 0; u < C::TP; ++u)
+#pragma unroll
+                        for (int q = 0; q < NQ; ++q)
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                const int tok = t[u].x + n8 + 8 * (x >> 1);
+                                if (tok >= end[q][x & 1] || tok < beg[q][x & 1] || t[u].y < 0)
+                                    p[u][q][x] = -INFINITY;
+                            }
+                }
+#pragma unroll
+                for (int u = 0; u < C::TP; ++u)
+#pragma unroll
+                    for (int q = 0; q < NQ; ++q)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) grow |= p[u][q][x] > m[q][x & 1] + kSlack;
                 if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
                     for (int q = 0; q < NQ; ++q)
@@ -941,14 +953,20 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
                             const float c = m[q][x & 1] == -INFINITY ? 0.f : m[q][x & 1];
-                            float w = exp2_fast(p[u][q][x] - c);
-                            p[u][q][x] = w;
-                            if (E4M3) {
-                                w *= iv[u][x >> 1];
-                                // a hidden token's scale may be anything
-                                if (edge[u] && p[u][q][x] == 0.f) w = 0.f;
+                            p[u][q][x] = exp2_fast(p[u][q][x] - c);
+                        }
+                        if (E4M3 && __builtin_expect(edges, 0)) {  // a hidden token's scale may be anything
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                const float w = p[u][q][x] * iv[u][x >> 1];
+                                l[q][x & 1] += p[u][q][x] == 0.f ? 0.f : w;
                             }
-                            l[q][x & 1] += w;
+                        } else {
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                if (E4M3) l[q][x & 1] += p[u][q][x] * iv[u][x >> 1];
+                                else l[q][x & 1] += p[u][q][x];
+                            }
                         }
                         uint32_t lo[C::PP], hi[C::PP];
                         split2<C::PP, E4M3>(p[u][q][0], p[u][q][1], lo);
@@ -964,7 +982,7 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
 #pragma unroll
                 for (int u = 0; u < C::TP; ++u) {
                     careful[u] = false;
-                    if (!edge[u]) continue;
+                    if (__builtin_expect(!edge[u], 1)) continue;
                     // A weight of zero does not silence an infinity or a NaN in a value. Tokens
                     // that no query sees are cleared (a tile that is not there as a whole); if
                     // one that only some see is not finite, the tile's products run value by
