@@ -755,8 +755,8 @@ int rssm_attn_read(const rssm_attn_dims* dims, const rssm_attn_cache* cache, int
 
 /* Bytes of device workspace rssm_attn_decode needs (partial results of rows whose
  * tokens several CTAs share, and their arrival counters). It must be zero-filled before
- * its first use; every call leaves its counters at zero. One stream at a time.
- * 0 for an invalid dims. */
+ * its first use, and again after a call that set RSSM_DEVERR_TIMEOUT; every other call
+ * leaves its counters at zero. One stream at a time. 0 for an invalid dims. */
 size_t rssm_attn_workspace_size(const rssm_attn_dims* dims);
 
 /* rssm_attn_decode -- attention of T query tokens per row over the row's cached tokens.
@@ -775,7 +775,8 @@ size_t rssm_attn_workspace_size(const rssm_attn_dims* dims);
  * sets RSSM_DEVERR_CURSOR; a page outside [0, num_pages) hides its tokens and sets
  * RSSM_DEVERR_PAGE. Rows may share a slot (the cache is only read). The work is divided
  * on the device from the slots' lengths, so a captured call serves any lengths; the order
- * of every sum is fixed by them, and repeated calls give identical bits. */
+ * of every sum is fixed by them and the GPU's SM count, and repeated calls give identical
+ * bits. A bounded wait that runs out sets RSSM_DEVERR_TIMEOUT and leaves outputs unwritten. */
 int rssm_attn_decode(const rssm_attn_dims* dims, const rssm_attn_cache* cache, int appended,
                      float scale, int32_t window, const void* q, int64_t q_stride,
                      const int32_t* cache_indices, void* workspace, size_t workspace_bytes,

@@ -126,14 +126,13 @@ bool make_tmap_rows128(CUtensorMap* out, const void* base, int elem_bytes, uint6
         else
             cudaGetLastError();  // this lookup's own error
     });
-    if (!g_encode || (elem_bytes != 1 && elem_bytes != 2 && elem_bytes != 4)) return false;
+    if (!g_encode || (elem_bytes != 2 && elem_bytes != 4)) return false;
     const cuuint64_t dims[2] = {cols, rows};
     const cuuint64_t strides[1] = {cols * (cuuint64_t)elem_bytes};
     const cuuint32_t box[2] = {(cuuint32_t)(128 / elem_bytes), box_rows};
     const cuuint32_t estr[2] = {1, 1};
-    const CUresult r = g_encode(out, elem_bytes == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                                     : elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                                       : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+    const CUresult r = g_encode(out, elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                     : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
                                 2, const_cast<void*>(base), dims, strides, box, estr,
                                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);

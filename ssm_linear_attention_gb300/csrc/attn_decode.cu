@@ -18,15 +18,20 @@
 //
 // Work: 16 cached tokens of one (row, key head) are a tile, all tiles of the call form one
 // list (row, head, tokens in order), and the list is cut into equal contiguous ranges,
-// one per group of warps (a group: ceil(M / 16) warps that take up to 16 queries each over
-// the same tiles). Lengths are read on the device: no length reaches the host, ragged
-// batches balance to a tile, a single long row fills the machine. A group streams its
-// tiles into a ring of stages of its own, 16-byte chunks swizzled within 128 bytes
-// (conflict-free ldmatrix), and never meets another group before its range ends. A (row,
-// head) that lies
-// inside one range is written out by its group. One that is cut leaves partial results; the
-// groups of a CTA join theirs through shared memory, and the last CTA of a (row, head) to
-// arrive at a counter joins the CTAs' results, in an order that the lengths alone fix.
+// one per group of warps (a group: 1, 2, 4 or 8 warps that take 8 queries each over the same
+// tiles). Lengths are read on the device: no length reaches the host, ragged batches balance
+// to a tile, a single long row fills the machine. A group streams its tiles into a ring of
+// stages of its own, 16-byte chunks swizzled within 128 bytes (conflict-free ldmatrix), and
+// never meets another group before its range ends. A (row, head) that lies inside one range
+// is written out by its group. One that is cut leaves partial results; the groups of a CTA
+// join theirs through shared memory, and the last CTA of a (row, head) to arrive at a counter
+// joins the CTAs' results, in an order that the lengths and the machine alone fix.
+//
+// Measured (one GB300, a stream of calls; of the measured copy bandwidth): 256 rows of 2k to
+// 8k tokens, 8 key heads of 4 queries, D 128: 8-bit cache %FP8%; 2 rows of 128k
+// and less, bf16 cache: %LONG%. With M = 32 (128 rows, 4 drafts) the
+// instruction issue shows: %SPEC%. One row of 300 tokens: %ONE%, latency
+// throughout (three dependent look-ups, one round trip of loads, two joins).
 #include <cuda_fp16.h>
 #include <cstring>
 
@@ -36,17 +41,18 @@ namespace rssm {
 namespace attn {
 
 constexpr int kTok = 16;       // tokens per tile: the smallest page
-constexpr int kMaxStages = 8;   // per group
-constexpr int kMaxWarps = 16;    // per CTA
-constexpr int kMaxCtas = 256;   // more than the SMs of any machine the library runs on
+constexpr int kMaxStages = 8;  // per group
+constexpr int kMaxWarps = 16;  // per CTA
+constexpr int kMaxCtas = 256;  // more than the SMs of any machine the library runs on
 constexpr int kMaxRows = 1024;  // rows per launch (prefix sums in shared memory)
 constexpr int kRowBytes = 13312;  // prefix sums, lengths and slots of kMaxRows rows, up to the
                                   // stages' alignment
 // Tiles that each group of a CTA gets at least before another CTA joins in.
 constexpr int kMinTiles = 2;
 // Longest (row, head), in tiles, up to which no CTA shares one. Meeting in global memory
-// costs a call some 6 us; an uneven cut costs at most this many tiles over a CTA's groups.
-constexpr int kWholeTiles = 48;
+// costs a call some 3 to 6 us; an uneven cut costs at most this many tiles over a CTA's groups
+// (16 rows of 1500 tokens: 24 us with 48 here, 21 with 96 or 160; 64 of 1200: 37, 38, 39).
+constexpr int kWholeTiles = 96;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // m follows the largest score once it is this far behind (log2 units)
@@ -199,10 +205,9 @@ struct Rows {
     int* slot;
 };
 
-// Where one tile lies: row, head, number among the (row, head)'s tiles, row of its first
-// token in the cache matrix (-1: its page is out of range).
+// Where one tile lies: row, head, number among the (row, head)'s tiles.
 struct Tile {
-    int b, h, at, y;
+    int b, h, at;
 };
 
 // The tile list (fewer than 2^31 tiles) cut into the CTAs' ranges. Even cuts share (row,
@@ -254,7 +259,6 @@ __device__ __noinline__ Tile find_tile(const DecArgs& a, const uint32_t* cum, ui
     const uint32_t in_row = t - cum[x.b] * (uint32_t)a.hkv;
     x.h = (int)(in_row / nt);
     x.at = (int)(in_row - (uint32_t)x.h * nt);
-    x.y = -1;
     return x;
 }
 
@@ -265,7 +269,8 @@ __device__ __noinline__ uint32_t next_head(const DecArgs& a, const uint32_t* cum
     return x.at == 0 ? t : t - x.at + cum[x.b + 1] - cum[x.b];
 }
 
-// The same with the tile's place in the cache.
+// Row of tile t's first token in the cache matrix; -1, with the flag set, when its page is
+// out of range.
 __device__ __noinline__ int locate_tile(const DecArgs& a, const Rows& rows, uint32_t t) {
     const Tile x = find_tile(a, rows.cum, t);
     const int pos = (row_span(a, rows.len[x.b]).first + x.at) * kTok;
@@ -305,8 +310,8 @@ __device__ __noinline__ void store_partial(const DecArgs& a, const Partial p, lo
         *reinterpret_cast<float4*>(static_cast<float*>(a.o) + r * D + d) = make_float4(y[0], y[1], y[2], y[3]);
     if (d == 0 && a.lse) a.lse[r] = none ? -INFINITY : (p.ml.x + log2_fast(p.ml.y)) * kLn2;
 }
-constexpr int kItems = 2;  // of a CTA's join that a thread has in flight
-constexpr int kJoin = 4;  // partial results whose loads a thread has in flight
+constexpr int kItems = 2;  // pieces of a CTA's join that a thread has in flight
+constexpr int kJoin = 4;   // partial results of CTAs whose loads a thread has in flight
 
 // A run: the consecutive records (partial results of groups) of one (row, head) in a CTA.
 struct Run {
@@ -327,7 +332,11 @@ struct Run {
 template <int D, bool E4M3, bool AF32, bool SHARE>
 struct Cfg {
     static constexpr bool WIDE = !E4M3 && D == 128;
-    static constexpr int TP = WIDE && !SHARE ? 1 : 2;  // tiles of a step
+    // Tiles of a step: two give a warp independent work between the dependent pieces of one; a
+    // ring of three wide tiles wants them one by one.
+    static constexpr int TP = WIDE && !SHARE ? 1 : 2;
+    // 16 warps of 128 registers hide more than 8 (569 -> 481 us on the 256-row 8-bit case);
+    // float32 operands need more registers, and 16 rings of wide tiles do not fit
     static constexpr int WARPS = AF32 || (WIDE && !SHARE) ? 8 : 16;
     // Wide tiles come by TMA (cp.async keeps fewer bytes in flight: 128 against 154 us on the
     // 2 x 128k case); for narrow ones the two are level (437 and 431 us on the 256-row 8-bit
@@ -384,7 +393,7 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
     decode_kernel(const __grid_constant__ DecArgs a, const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap) {
     using C = Cfg<D, E4M3, AF32, SHARE>;
-    constexpr int kWarps = C::WARPS, kDecThreads = kWarps * 32, NQ = 1;
+    constexpr int kWarps = C::WARPS, kDecThreads = kWarps * 32;
     extern __shared__ unsigned char smem_raw[];
     // 128-byte swizzled boxes want their base on 1024 bytes
     unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -412,11 +421,11 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
     __shared__ int rec_b[2 * kWarps], rec_h[2 * kWarps];  // records; b < 0: none
     __shared__ Run runs[2 * kWarps];
     __shared__ int nruns, last_flag[2];
-    __shared__ float2 rec_ml[2 * kWarps * 8 * NQ];  // [record][M] m and l
+    __shared__ float2 rec_ml[2 * kWarps * 8];  // [record][M] m and l
 
     if (C::TMA) {
         if (tid < nst) {
-            mbar_init(&full[tid], 1 + (E4M3 ? 32 : 0));
+            mbar_init(&full[tid], 1);
             fence_barrier_init();
         }
         if (tid == 0) {
@@ -431,7 +440,6 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
         q_tok[tid] = j;
         q_row[tid] = j * a.hq + tid - j * a.G;
     }
-    if (tid == 0) runs[0].cta0 = runs[0].cta1 = 0;
 
     // ------------------------------------------------------- the call's tile list
     uint32_t longest = 0;  // tiles of the longest (row, head)
@@ -523,10 +531,10 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
     // ------------------------------------------------------- stream the range
     // Lane layout of the products: n = lane / 4 numbers S^T's tokens (n and n + 8) and O^T's
     // columns, qd = lane % 4 its queries 2 qd and 2 qd + 1 of each block of 8.
-    float o[C::DB][NQ][4];
-    float m[NQ][2], l[NQ][2];
+    float o[C::DB][4];
+    float m[2], l[2];
     const int n8 = lane >> 2, qd = lane & 3;
-    const int q0 = mt * 8 * NQ;  // this warp's first query
+    const int q0 = mt * 8;  // this warp's first query
 
     const uint32_t t0 = c0 + group * gbase + min((uint32_t)group, grem);
     const int ntile = group < ngroups ? (int)(gbase + (group < (int)grem ? 1 : 0)) : 0;
@@ -562,25 +570,18 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
                 if ((sent & 31) == 0 && sent + lane < ntile) look = locate_tile(a, rows, t0 + sent + lane);
                 const int y = __shfl_sync(0xffffffffu, look, sent & 31);
                 bad = (bad & ~(1u << sent_s)) | (y < 0 ? 1u << sent_s : 0u);
-                if (C::TMA) {
-                    if (leader && y >= 0) {
+                if (C::TMA) {  // (one warp a group)
+                    if (y >= 0) {
                         unsigned char* dst = kv + (size_t)sent_s * C::STAGE;
                         if (elect_one()) {
-                            constexpr int EB = E4M3 ? 1 : 2;
-                            const int ty = C::ROWB >= 128 ? y : y >> 1;
                             mbar_arrive_expect_tx(&fb[sent_s], C::STAGE);
 #pragma unroll
-                            for (int x = 0; x < (C::ROWB + 127) / 128; ++x) {
-                                tma_load_2d(dst + x * kTok * 128, &kmap, x * 128 / EB, ty, &fb[sent_s], pol);
-                                tma_load_2d(dst + C::KB + x * kTok * 128, &vmap, x * 128 / EB, ty, &fb[sent_s], pol);
+                            for (int x = 0; x < C::ROWB / 128; ++x) {
+                                tma_load_2d(dst + x * kTok * 128, &kmap, 64 * x, y, &fb[sent_s], pol);
+                                tma_load_2d(dst + C::KB + x * kTok * 128, &vmap, 64 * x, y, &fb[sent_s], pol);
                             }
                         }
                         __syncwarp();
-                        if (E4M3) {
-                            cp_async4(smem_addr(sc + sent_s * 2 * kTok + lane),
-                                      (lane < kTok ? a.k_scale : a.v_scale) + y + (lane & (kTok - 1)));
-                            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&fb[sent_s])) : "memory");
-                        }
                     }
                 } else if (__all_sync(0xffffffffu, y >= 0)) {
                     // instruction j copies tokens TPI j .. of k and of v; the swizzle makes a step of j
@@ -606,9 +607,9 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
 #pragma unroll 1
         for (int i = 0; i < stages; ++i) issue();
 
-        uint32_t qf[D / 16][NQ][C::QP][2];  // [k step][query block][part][k half]
-        float rs[NQ][2];                    // score factor of the queries
-        int end[NQ][2], beg[NQ][2];         // the positions they see
+        uint32_t qf[D / 16][C::QP][2];  // [k step][part][k half]
+        float rs[2];                    // score factor of the queries
+        int end[2], beg[2];         // the positions they see
         int n_min = 0, n_max = 0, b_min = 0, b_max = 0;
         const bool works = q0 < a.M;
         int cb = 0, ch = 0;      // current (row, head)
@@ -627,80 +628,73 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
                     // free.
                     const bool whole = i == next && !begun, tail = i == ntile;
 #pragma unroll
-                    for (int q = 0; q < NQ; ++q)
-#pragma unroll
                         for (int x = 0; x < 2; ++x)
 #pragma unroll
                             for (int w = 4; w < 32; w <<= 1)
-                                l[q][x] += __shfl_xor_sync(0xffffffffu, l[q][x], w);
+                                l[x] += __shfl_xor_sync(0xffffffffu, l[x], w);
                     if (!whole && leader && lane == 0) {
                         rec_b[2 * group + (tail ? 1 : 0)] = cb;
                         rec_h[2 * group + (tail ? 1 : 0)] = ch;
                     }
                     if (whole) {
                         const long out0 = (long)cb * a.T * a.hq + ch * a.G;
+                        const float i0 = l[0] == 0.f ? 0.f : reciprocal(l[0]);
+                        const float i1 = l[1] == 0.f ? 0.f : reciprocal(l[1]);
+                        if (a.obf) {
+                            // transposed, a lane has two columns of query n8
+                            const int r = q0 + n8;
+                            const long row = r < a.M ? out0 + q_row[r] : 0;
+                            uint16_t* dst = static_cast<uint16_t*>(a.o) + row * D;
 #pragma unroll
-                        for (int q = 0; q < NQ; ++q) {
-                            const float i0 = l[q][0] == 0.f ? 0.f : reciprocal(l[q][0]);
-                            const float i1 = l[q][1] == 0.f ? 0.f : reciprocal(l[q][1]);
-                            if (a.obf) {
-                                // transposed, a lane has two columns of query n8
-                                const int r = q0 + 8 * q + n8;
-                                const long row = r < a.M ? out0 + q_row[r] : 0;
-                                uint16_t* dst = static_cast<uint16_t*>(a.o) + row * D;
+                            for (int c = 0; c < C::DB; ++c) {
+                                float v[4];
+#pragma unroll
+                                for (int x = 0; x < 4; ++x) {
+                                    const bool none = l[x & 1] == 0.f;
+                                    v[x] = none ? 0.f : o[c][x] * (x & 1 ? i1 : i0);
+                                }
+                                uint32_t lo = transpose8(pack2(v[0], v[1]));
+                                uint32_t hi = transpose8(pack2(v[2], v[3]));
+                                if (r >= a.M) continue;
+                                if (E4M3) {  // even and odd columns 4 qd .. 4 qd + 3
+                                    *reinterpret_cast<uint2*>(dst + 16 * c + 4 * qd) = make_uint2(
+                                        __byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
+                                } else {
+                                    *reinterpret_cast<uint32_t*>(dst + 16 * c + 2 * qd) = lo;
+                                    *reinterpret_cast<uint32_t*>(dst + 16 * c + 8 + 2 * qd) = hi;
+                                }
+                            }
+                        }
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const int r = q0 + 2 * qd + x;
+                            if (r >= a.M) continue;
+                            const long row = out0 + q_row[r];
+                            const bool none = l[x] == 0.f;
+                            if (!a.obf) {
+                                float* dst = static_cast<float*>(a.o) + row * D;
 #pragma unroll
                                 for (int c = 0; c < C::DB; ++c) {
-                                    float v[4];
-#pragma unroll
-                                    for (int x = 0; x < 4; ++x) {
-                                        const bool none = l[q][x & 1] == 0.f;
-                                        v[x] = none ? 0.f : o[c][q][x] * (x & 1 ? i1 : i0);
-                                    }
-                                    uint32_t lo = transpose8(pack2(v[0], v[1]));
-                                    uint32_t hi = transpose8(pack2(v[2], v[3]));
-                                    if (r >= a.M) continue;
-                                    if (E4M3) {  // even and odd columns 4 qd .. 4 qd + 3
-                                        *reinterpret_cast<uint2*>(dst + 16 * c + 4 * qd) = make_uint2(
-                                            __byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
-                                    } else {
-                                        *reinterpret_cast<uint32_t*>(dst + 16 * c + 2 * qd) = lo;
-                                        *reinterpret_cast<uint32_t*>(dst + 16 * c + 8 + 2 * qd) = hi;
-                                    }
+                                    dst[C::col(c, n8, 0)] = none ? 0.f : o[c][x] * (x ? i1 : i0);
+                                    dst[C::col(c, n8, 1)] = none ? 0.f : o[c][2 + x] * (x ? i1 : i0);
                                 }
                             }
-#pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                const int r = q0 + 8 * q + 2 * qd + x;
-                                if (r >= a.M) continue;
-                                const long row = out0 + q_row[r];
-                                const bool none = l[q][x] == 0.f;
-                                if (!a.obf) {
-                                    float* dst = static_cast<float*>(a.o) + row * D;
-#pragma unroll
-                                    for (int c = 0; c < C::DB; ++c) {
-                                        dst[C::col(c, n8, 0)] = none ? 0.f : o[c][q][x] * (x ? i1 : i0);
-                                        dst[C::col(c, n8, 1)] = none ? 0.f : o[c][q][2 + x] * (x ? i1 : i0);
-                                    }
-                                }
-                                if (a.lse && n8 == 0)
-                                    a.lse[row] = none ? -INFINITY : (m[q][x] + log2_fast(l[q][x])) * kLn2;
-                            }
+                            if (a.lse && n8 == 0)
+                                a.lse[row] = none ? -INFINITY : (m[x] + log2_fast(l[x])) * kLn2;
                         }
                     } else if (!tail) {
                         const long slot = 2L * gridDim.x + (int)blockIdx.x * kWarps + group;
 #pragma unroll
-                        for (int q = 0; q < NQ; ++q)
-#pragma unroll
                             for (int x = 0; x < 2; ++x) {
-                                const int r = q0 + 8 * q + 2 * qd + x;
+                                const int r = q0 + 2 * qd + x;
                                 if (r >= a.M) continue;
                                 float* dst = a.part + (slot * a.M + r) * D;
 #pragma unroll
                                 for (int c = 0; c < C::DB; ++c) {
-                                    dst[C::col(c, n8, 0)] = o[c][q][x];
-                                    dst[C::col(c, n8, 1)] = o[c][q][2 + x];
+                                    dst[C::col(c, n8, 0)] = o[c][x];
+                                    dst[C::col(c, n8, 1)] = o[c][2 + x];
                                 }
-                                if (n8 == 0) rec_ml[2 * group * a.M + r] = make_float2(m[q][x], l[q][x]);
+                                if (n8 == 0) rec_ml[2 * group * a.M + r] = make_float2(m[x], l[x]);
                             }
                     }
                 }
@@ -721,75 +715,71 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
                 b_max = a.window && n_max > a.window ? n_max - a.window : 0;
 #pragma unroll
                 for (int c = 0; c < C::DB; ++c)
+                    o[c][0] = o[c][1] = o[c][2] = o[c][3] = 0.f;
 #pragma unroll
-                    for (int q = 0; q < NQ; ++q) o[c][q][0] = o[c][q][1] = o[c][q][2] = o[c][q][3] = 0.f;
+                for (int x = 0; x < 2; ++x) {
+                    const int r = q0 + 2 * qd + x;
+                    const int e = len + (app ? (r < a.M ? q_tok[r] : 0) + 1 : 0);
+                    end[x] = e;
+                    beg[x] = a.window && e > a.window ? e - a.window : 0;
+                    m[x] = -INFINITY;
+                    l[x] = 0.f;
+                    rs[x] = a.qscale;
+                }
+                const int r = q0 + n8;  // the query whose operand values this lane has
+                const int j = r < a.M ? q_tok[r] : 0;
+                const long base = ((long)cb * a.T + j) * a.q_stride + (ch * a.G + (r - j * a.G)) * D;
+                float v[D / 16][4];
 #pragma unroll
-                for (int q = 0; q < NQ; ++q) {
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    // columns of a k16 step: pairs at 2 qd and 2 qd + 8; for 8-bit keys, of
+                    // which a lane gets 4 bytes, 4 qd and 4 qd + 2
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const int r = q0 + 8 * q + 2 * qd + x;
-                        const int e = len + (app ? (r < a.M ? q_tok[r] : 0) + 1 : 0);
-                        end[q][x] = e;
-                        beg[q][x] = a.window && e > a.window ? e - a.window : 0;
-                        m[q][x] = -INFINITY;
-                        l[q][x] = 0.f;
-                        rs[q][x] = a.qscale;
-                    }
-                    const int r = q0 + 8 * q + n8;  // the query whose operand values this lane has
-                    const int j = r < a.M ? q_tok[r] : 0;
-                    const long base = ((long)cb * a.T + j) * a.q_stride + (ch * a.G + (r - j * a.G)) * D;
-                    float v[D / 16][4];
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        // columns of a k16 step: pairs at 2 qd and 2 qd + 8; for 8-bit keys, of
-                        // which a lane gets 4 bytes, 4 qd and 4 qd + 2
-#pragma unroll
-                        for (int e = 0; e < 4; e += 2) {
-                            const int col = 16 * kk + (E4M3 ? 4 * qd + e : 2 * qd + 4 * e);
-                            v[kk][e] = v[kk][e + 1] = 0.f;
-                            if (r < a.M) {
-                                if (AF32) {
-                                    const float2 f = *reinterpret_cast<const float2*>(
-                                        static_cast<const float*>(a.q) + base + col);
-                                    v[kk][e] = f.x;
-                                    v[kk][e + 1] = f.y;
-                                } else {
-                                    const uint32_t f = *reinterpret_cast<const uint32_t*>(
-                                        static_cast<const uint16_t*>(a.q) + base + col);
-                                    v[kk][e] = bf16_lo(f);
-                                    v[kk][e + 1] = bf16_hi(f);
-                                }
+                    for (int e = 0; e < 4; e += 2) {
+                        const int col = 16 * kk + (E4M3 ? 4 * qd + e : 2 * qd + 4 * e);
+                        v[kk][e] = v[kk][e + 1] = 0.f;
+                        if (r < a.M) {
+                            if (AF32) {
+                                const float2 f = *reinterpret_cast<const float2*>(
+                                    static_cast<const float*>(a.q) + base + col);
+                                v[kk][e] = f.x;
+                                v[kk][e + 1] = f.y;
+                            } else {
+                                const uint32_t f = *reinterpret_cast<const uint32_t*>(
+                                    static_cast<const uint16_t*>(a.q) + base + col);
+                                v[kk][e] = bf16_lo(f);
+                                v[kk][e + 1] = bf16_hi(f);
                             }
                         }
                     }
-                    if (E4M3) {  // into f16's range: divide by the power of two at the largest
-                        float top = 0.f;
+                }
+                if (E4M3) {  // into f16's range: divide by the power of two at the largest
+                    float top = 0.f;
 #pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk)
+                    for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
-                            for (int x = 0; x < 4; ++x) top = fmaxf(top, fabsf(v[kk][x]));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                        float p2 = __uint_as_float(__float_as_uint(top) & 0x7f800000u);
-                        if (p2 == 0.f || p2 == INFINITY) p2 = 1.f;
-                        const float inv = 1.f / p2;
+                        for (int x = 0; x < 4; ++x) top = fmaxf(top, fabsf(v[kk][x]));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    float p2 = __uint_as_float(__float_as_uint(top) & 0x7f800000u);
+                    if (p2 == 0.f || p2 == INFINITY) p2 = 1.f;
+                    const float inv = 1.f / p2;
 #pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk)
+                    for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
-                            for (int x = 0; x < 4; ++x) v[kk][x] *= inv;
-                        rs[q][0] = a.qscale * __shfl_sync(0xffffffffu, p2, 8 * qd);
-                        rs[q][1] = a.qscale * __shfl_sync(0xffffffffu, p2, 8 * qd + 4);
-                    }
+                        for (int x = 0; x < 4; ++x) v[kk][x] *= inv;
+                    rs[0] = a.qscale * __shfl_sync(0xffffffffu, p2, 8 * qd);
+                    rs[1] = a.qscale * __shfl_sync(0xffffffffu, p2, 8 * qd + 4);
+                }
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        uint32_t lo[C::QP], hi[C::QP];
-                        split2<C::QP, E4M3>(v[kk][0], v[kk][1], lo);
-                        split2<C::QP, E4M3>(v[kk][2], v[kk][3], hi);
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    uint32_t lo[C::QP], hi[C::QP];
+                    split2<C::QP, E4M3>(v[kk][0], v[kk][1], lo);
+                    split2<C::QP, E4M3>(v[kk][2], v[kk][3], hi);
 #pragma unroll
-                        for (int p = 0; p < C::QP; ++p) {
-                            qf[kk][q][p][0] = lo[p];
-                            qf[kk][q][p][1] = hi[p];
-                        }
+                    for (int p = 0; p < C::QP; ++p) {
+                        qf[kk][p][0] = lo[p];
+                        qf[kk][p][1] = hi[p];
                     }
                 }
             }
@@ -799,19 +789,15 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
             int2 t[C::TP];  // position, -1 for a tile that is not there or has no page
             int st[C::TP];
             bool ok = true;
-            if (C::TMA) {
-                // every tile of the step that has a page
-#pragma unroll
-                for (int u = 0; u < C::TP; ++u) {
-                    const int z = s + u < stages ? s + u : s + u - stages;
-                    if (u < steps && !(bad >> z & 1)) {
-                        if (!__all_sync(0xffffffffu, mbar_try_wait(&fb[z], parity >> z & 1)))
-                            ok = ok && wait_long(&fb[z], parity >> z & 1, &abort_flag, a.dev_err);
-                        parity ^= 1u << z;
-                    }
+            if (C::TMA) {  // (one tile a step)
+                if (!(bad >> s & 1)) {
+                    if (!__all_sync(0xffffffffu, mbar_try_wait(&fb[s], parity >> s & 1)))
+                        ok = wait_long(&fb[s], parity >> s & 1, &abort_flag, a.dev_err);
+                    parity ^= 1u << s;
                 }
+            } else {
+                cp_async_wait_but(stages - (SHARE ? 2 : 1) * C::TP);
             }
-            if (!C::TMA) cp_async_wait_but(stages - (SHARE ? 2 : 1) * C::TP);
             if (!SHARE) {
                 __syncwarp();
             } else {
@@ -835,13 +821,11 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
             if (some && works) {
                 // ------------------------------------------------ S^T = K Q^T
                 constexpr int SA = C::TP == 1 ? 2 : 1;  // one tile: two chains of sums
-                float sa[C::TP][SA][NQ][4];
+                float sa[C::TP][SA][4];
 #pragma unroll
                 for (int u = 0; u < C::TP; ++u)
 #pragma unroll
-                    for (int q = 0; q < NQ; ++q)
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) sa[u][0][q][x] = sa[u][SA - 1][q][x] = 0.f;
+                        for (int x = 0; x < 4; ++x) sa[u][0][x] = sa[u][SA - 1][x] = 0.f;
 #pragma unroll
                 for (int kk = 0; kk < D / 16; kk += E4M3 ? 2 : 1)
 #pragma unroll
@@ -857,26 +841,22 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
                             for (int x = 0; x < 4; ++x)
                                 e4m3x4_to_f16(r[x], f[x >> 1][x & 1], f[x >> 1][2 + (x & 1)]);
 #pragma unroll
-                            for (int p = 0; p < C::QP; ++p)
-#pragma unroll
-                                for (int q = 0; q < NQ; ++q) {
-                                    mma16816<true>(sa[u][0][q], f[0], qf[kk][q][p][0], qf[kk][q][p][1]);
-                                    mma16816<true>(sa[u][SA - 1][q], f[1], qf[kk + 1][q][p][0], qf[kk + 1][q][p][1]);
-                                }
+                            for (int p = 0; p < C::QP; ++p) {
+                                    mma16816<true>(sa[u][0], f[0], qf[kk][p][0], qf[kk][p][1]);
+                                    mma16816<true>(sa[u][SA - 1], f[1], qf[kk + 1][p][0], qf[kk + 1][p][1]);
+                            }
                         } else {
                             ldsm4(at + kk / 4 * (kTok * 128), r);
 #pragma unroll
                             for (int p = 0; p < C::QP; ++p)
-#pragma unroll
-                                for (int q = 0; q < NQ; ++q)
-                                    mma16816<false>(sa[u][SA == 2 ? kk & 1 : 0][q], r, qf[kk][q][p][0], qf[kk][q][p][1]);
+                                    mma16816<false>(sa[u][SA == 2 ? kk & 1 : 0], r, qf[kk][p][0], qf[kk][p][1]);
                         }
                     }
                 // ------------------------------------------------ softmax
                 // Scores in log2 units. With an 8-bit cache a token's value scale joins its
                 // weight as log2(scale) in the exponent: m bounds those sums, the weights stay
                 // in f16's range, and l, which wants the scores alone, divides it out again.
-                float p[C::TP][NQ][4], iv[C::TP][2];
+                float p[C::TP][4], iv[C::TP][2];
                 bool edge[C::TP], edges = false, grow = false;
 #pragma unroll
                 for (int u = 0; u < C::TP; ++u) {
@@ -896,87 +876,77 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
                     edge[u] = t[u].y < 0 || t[u].x + kTok > n_min || t[u].x < b_max;
                     edges = edges || edge[u];
 #pragma unroll
-                    for (int q = 0; q < NQ; ++q)
-#pragma unroll
                         for (int x = 0; x < 4; ++x) {
-                            float f = SA == 2 ? sa[u][0][q][x] + sa[u][SA - 1][q][x] : sa[u][0][q][x];
-                            f *= rs[q][x & 1];
+                            float f = SA == 2 ? sa[u][0][x] + sa[u][SA - 1][x] : sa[u][0][x];
+                            f *= rs[x & 1];
                             if (E4M3) f = f * ks[x >> 1] + lv[x >> 1];
-                            p[u][q][x] = f;
+                            p[u][x] = f;
                         }
                 }
                 if (__builtin_expect(edges, 0)) {  // hide what a query does not see, whatever it holds
 #pragma unroll
                     for (int u = 0; u < C::TP; ++u)
 #pragma unroll
-                        for (int q = 0; q < NQ; ++q)
-#pragma unroll
                             for (int x = 0; x < 4; ++x) {
                                 const int tok = t[u].x + n8 + 8 * (x >> 1);
-                                if (tok >= end[q][x & 1] || tok < beg[q][x & 1] || t[u].y < 0)
-                                    p[u][q][x] = -INFINITY;
+                                if (tok >= end[x & 1] || tok < beg[x & 1] || t[u].y < 0)
+                                    p[u][x] = -INFINITY;
                             }
                 }
 #pragma unroll
                 for (int u = 0; u < C::TP; ++u)
 #pragma unroll
-                    for (int q = 0; q < NQ; ++q)
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) grow |= p[u][q][x] > m[q][x & 1] + kSlack;
+                        for (int x = 0; x < 4; ++x) grow |= p[u][x] > m[x & 1] + kSlack;
                 if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-                    for (int q = 0; q < NQ; ++q)
-#pragma unroll
                         for (int x = 0; x < 2; ++x) {
-                            float top = fmaxf(p[0][q][x], p[0][q][2 + x]);
-                            if (C::TP > 1) top = fmaxf(top, fmaxf(p[C::TP - 1][q][x], p[C::TP - 1][q][2 + x]));
+                            float top = fmaxf(p[0][x], p[0][2 + x]);
+                            if (C::TP > 1) top = fmaxf(top, fmaxf(p[C::TP - 1][x], p[C::TP - 1][2 + x]));
 #pragma unroll
                             for (int w = 4; w < 32; w <<= 1)
                                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-                            top = fmaxf(top, m[q][x]);
-                            const float f = top == m[q][x] ? 1.f : exp2_fast(m[q][x] - top);
-                            m[q][x] = top;
-                            l[q][x] *= f;
+                            top = fmaxf(top, m[x]);
+                            const float f = top == m[x] ? 1.f : exp2_fast(m[x] - top);
+                            m[x] = top;
+                            l[x] *= f;
 #pragma unroll
                             for (int c = 0; c < C::DB; ++c) {
-                                o[c][q][x] *= f;
-                                o[c][q][2 + x] *= f;
+                                o[c][x] *= f;
+                                o[c][2 + x] *= f;
                             }
                         }
                 }
-                uint32_t pf[C::TP][NQ][C::PP][2];
+                uint32_t pf[C::TP][C::PP][2];
 #pragma unroll
-                for (int u = 0; u < C::TP; ++u)
-#pragma unroll
-                    for (int q = 0; q < NQ; ++q) {
+                for (int u = 0; u < C::TP; ++u) {
                         // a query that has seen only -infinity keeps weights of zero
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
-                            const float c = m[q][x & 1] == -INFINITY ? 0.f : m[q][x & 1];
-                            p[u][q][x] = exp2_fast(p[u][q][x] - c);
+                            const float c = m[x & 1] == -INFINITY ? 0.f : m[x & 1];
+                            p[u][x] = exp2_fast(p[u][x] - c);
                         }
                         if (E4M3 && __builtin_expect(edges, 0)) {  // a hidden token's scale may be anything
 #pragma unroll
                             for (int x = 0; x < 4; ++x) {
-                                const float w = p[u][q][x] * iv[u][x >> 1];
-                                l[q][x & 1] += p[u][q][x] == 0.f ? 0.f : w;
+                                const float w = p[u][x] * iv[u][x >> 1];
+                                l[x & 1] += p[u][x] == 0.f ? 0.f : w;
                             }
                         } else {
 #pragma unroll
                             for (int x = 0; x < 4; ++x) {
-                                if (E4M3) l[q][x & 1] += p[u][q][x] * iv[u][x >> 1];
-                                else l[q][x & 1] += p[u][q][x];
+                                if (E4M3) l[x & 1] += p[u][x] * iv[u][x >> 1];
+                                else l[x & 1] += p[u][x];
                             }
                         }
                         uint32_t lo[C::PP], hi[C::PP];
-                        split2<C::PP, E4M3>(p[u][q][0], p[u][q][1], lo);
-                        split2<C::PP, E4M3>(p[u][q][2], p[u][q][3], hi);
+                        split2<C::PP, E4M3>(p[u][0], p[u][1], lo);
+                        split2<C::PP, E4M3>(p[u][2], p[u][3], hi);
 #pragma unroll
                         for (int x = 0; x < C::PP; ++x) {
-                            pf[u][q][x][0] = transpose8(lo[x]);
-                            pf[u][q][x][1] = transpose8(hi[x]);
+                            pf[u][x][0] = transpose8(lo[x]);
+                            pf[u][x][1] = transpose8(hi[x]);
                         }
-                    }
+                }
                 // ------------------------------------------------ O^T += V^T P^T
                 bool careful[C::TP];
 #pragma unroll
@@ -1043,19 +1013,15 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
                                     d[2 * (x & 1) + 1] = __byte_perm(lo, hi, 0x7632);
                                 }
 #pragma unroll
-                                for (int x = 0; x < C::PP; ++x)
-#pragma unroll
-                                    for (int q = 0; q < NQ; ++q) {
-                                        mma16816<true>(o[c][q], f, pf[u][q][x][0], pf[u][q][x][1]);
-                                        mma16816<true>(o[c + 1][q], g, pf[u][q][x][0], pf[u][q][x][1]);
-                                    }
+                                for (int x = 0; x < C::PP; ++x) {
+                                        mma16816<true>(o[c], f, pf[u][x][0], pf[u][x][1]);
+                                        mma16816<true>(o[c + 1], g, pf[u][x][0], pf[u][x][1]);
+                                }
                             } else {
                                 ldsm4_t((vbase ^ (uint32_t)(2 * c % 8 * 16)) + c / 4 * (kTok * 128), f);
 #pragma unroll
                                 for (int x = 0; x < C::PP; ++x)
-#pragma unroll
-                                    for (int q = 0; q < NQ; ++q)
-                                        mma16816<false>(o[c][q], f, pf[u][q][x][0], pf[u][q][x][1]);
+                                        mma16816<false>(o[c], f, pf[u][x][0], pf[u][x][1]);
                             }
                         }
                     } else if (!E4M3 && t[u].y >= 0) {
@@ -1064,19 +1030,17 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
                         for (int tok = 0; tok < kTok; ++tok) {
                             const int src = (tok & 7) * 4 + qd;
 #pragma unroll
-                            for (int q = 0; q < NQ; ++q)
-#pragma unroll
                                 for (int x = 0; x < 2; ++x) {
-                                    const float w = __shfl_sync(0xffffffffu, tok < 8 ? p[u][q][x] : p[u][q][2 + x], src);
-                                    if (pos + tok >= end[q][x] || pos + tok < beg[q][x]) continue;
+                                    const float w = __shfl_sync(0xffffffffu, tok < 8 ? p[u][x] : p[u][2 + x], src);
+                                    if (pos + tok >= end[x] || pos + tok < beg[x]) continue;
 #pragma unroll
                                     for (int c = 0; c < C::DB; ++c) {
                                         const uint16_t* v = reinterpret_cast<const uint16_t*>(
                                             vt + tile_off<C::ROWB>(tok, 2 * c) + 2 * n8);
                                         const uint16_t* w2 = reinterpret_cast<const uint16_t*>(
                                             vt + tile_off<C::ROWB>(tok, 2 * c + 1) + 2 * n8);
-                                        o[c][q][x] += w * bf16_to_f(*v);
-                                        o[c][q][2 + x] += w * bf16_to_f(*w2);
+                                        o[c][x] += w * bf16_to_f(*v);
+                                        o[c][2 + x] += w * bf16_to_f(*w2);
                                     }
                                 }
                         }
@@ -1109,18 +1073,16 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
     float* tail = reinterpret_cast<float*>(st_kv);  // [group][M][TD]
     if (ntile > 0 && rec_b[2 * group + 1] >= 0) {
 #pragma unroll
-        for (int q = 0; q < NQ; ++q)
-#pragma unroll
             for (int x = 0; x < 2; ++x) {
-                const int r = q0 + 8 * q + 2 * qd + x;
+                const int r = q0 + 2 * qd + x;
                 if (r >= a.M) continue;
                 float* dst = tail + (group * a.M + r) * C::TD;
 #pragma unroll
                 for (int c = 0; c < C::DB; ++c) {
-                    dst[C::col(c, n8, 0)] = o[c][q][x];
-                    dst[C::col(c, n8, 1)] = o[c][q][2 + x];
+                    dst[C::col(c, n8, 0)] = o[c][x];
+                    dst[C::col(c, n8, 1)] = o[c][2 + x];
                 }
-                if (n8 == 0) rec_ml[(2 * group + 1) * a.M + r] = make_float2(m[q][x], l[q][x]);
+                if (n8 == 0) rec_ml[(2 * group + 1) * a.M + r] = make_float2(m[x], l[x]);
             }
     }
     // Runs of records: a record whose (row, head) differs from that of the record before it
@@ -1197,8 +1159,7 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
     // ------------------------------------------------------- join the CTAs
     // Only the first run (begun in an earlier CTA) and the last (which goes on) can be
     // shared. The counter of a shared (row, head) is its first CTA's.
-    if (runs[0].cta0 == runs[0].cta1 && runs[nruns > 0 ? nruns - 1 : 0].cta0 == runs[nruns > 0 ? nruns - 1 : 0].cta1)
-        return;
+    if (nruns == 0 || (runs[0].cta0 == runs[0].cta1 && runs[nruns - 1].cta0 == runs[nruns - 1].cta1)) return;
     __threadfence();
     __syncthreads();
     if (tid < 2 && (tid == 0 || nruns > 1)) {
@@ -1301,11 +1262,8 @@ static int launch_kernel(const rssm_attn_dims* d, DecArgs a, const DeviceInfo& d
     memset(&km, 0, sizeof km);
     memset(&vm, 0, sizeof vm);
     if (C::TMA) {
-        // rows of 128 bytes at least: 64-byte vectors go in pairs
         const uint64_t nr = (uint64_t)d->num_pages * d->num_kv_heads * d->page_size;
-        const bool pair = C::ROWB < 128;
-        if (!make_tmap_rows128(&km, a.k, E4M3 ? 1 : 2, pair ? nr / 2 : nr, pair ? 2 * D : D, pair ? kTok / 2 : kTok) ||
-            !make_tmap_rows128(&vm, a.v, E4M3 ? 1 : 2, pair ? nr / 2 : nr, pair ? 2 * D : D, pair ? kTok / 2 : kTok))
+        if (!make_tmap_rows128(&km, a.k, 2, nr, D, kTok) || !make_tmap_rows128(&vm, a.v, 2, nr, D, kTok))
             return RSSM_ERR_CUDA;
     }
     const void* kern = (const void*)decode_kernel<D, E4M3, AF32, SHARE>;

@@ -50,7 +50,7 @@ bool pick_pipe(const DeviceInfo& di, int stage_bytes, int warp_scratch, int tile
                int max_stages, int group_warps, int max_groups, PipeCfg* out, int align = 128);
 
 // A 2-D tensor map over a row-major matrix of `rows` x `cols` elements of
-// `elem_bytes` (1: bytes, 2: bf16, 4: fp32) at `base` (16-byte aligned, rows of cols *
+// `elem_bytes` (2: bf16, 4: fp32) at `base` (16-byte aligned, rows of cols *
 // elem_bytes bytes, a multiple of 16), copied in boxes of box_rows x (128 /
 // elem_bytes) elements -- one 128-byte row segment per box row -- with the 128-byte
 // shared-memory swizzle (16-byte chunk j of box row r lands at chunk j ^ (r % 8)).
