@@ -149,15 +149,16 @@ class PagedAttentionDecoder:
 
     def read(self, cache_indices, cu_tokens, n_tokens, first=None, k=None, v=None, stream=None):
         """Committed tokens back, dense: k, v [n_tokens, HKV, D] (out_dtype; new tensors unless
-        both are given)."""
-        if k is None and v is None:
-            k, v = torch.empty((2, n_tokens, self.HKV, self.D), device=self.device,
-                               dtype=self.out_dtype).unbind(0)
+        given)."""
+        shape = (n_tokens, self.HKV, self.D)
         for t in (k, v):
-            if t.dtype is not self.out_dtype or t.numel() != n_tokens * self.HKV * self.D or \
-                    not t.is_contiguous():
-                raise ValueError("k and v: dense [%d, %d, %d] %s" % (n_tokens, self.HKV, self.D,
-                                                                     self.out_dtype))
+            if t is not None and (t.dtype is not self.out_dtype or t.shape != shape or
+                                  not t.is_contiguous()):
+                raise ValueError("k and v: dense [%d, %d, %d] %s" % (shape + (self.out_dtype,)))
+        if k is None:
+            k = torch.empty(shape, device=self.device, dtype=self.out_dtype)
+        if v is None:
+            v = torch.empty(shape, device=self.device, dtype=self.out_dtype)
         B.rssm_attn_read(self._plan(cache_indices.shape[0])[0], self.cache, n_tokens, cu_tokens,
                          first, cache_indices, k, v, self.dev_err, stream)
         return k, v
