@@ -27,11 +27,12 @@
 // join theirs through shared memory, and the last CTA of a (row, head) to arrive at a counter
 // joins the CTAs' results, in an order that the lengths and the machine alone fix.
 //
-// Measured (one GB300, a stream of calls; of the measured copy bandwidth): 256 rows of 2k to
-// 8k tokens, 8 key heads of 4 queries, D 128: 8-bit cache %FP8%; 2 rows of 128k
-// and less, bf16 cache: %LONG%. With M = 32 (128 rows, 4 drafts) the
-// instruction issue shows: %SPEC%. One row of 300 tokens: %ONE%, latency
-// throughout (three dependent look-ups, one round trip of loads, two joins).
+// Measured (one GB300, GPU time of a call; "of" the measured copy bandwidth): 256 rows of 2k
+// to 8k tokens, 8 key heads of 4 queries, D 128, 8-bit cache: 443 us, 6.4 TB/s, 94 % of it;
+// 2 rows of 128k and 57k tokens, bf16 cache: 127 us, 6.25 TB/s, 92 %. With M = 32 (128 rows, 4 drafts,
+// 8 queries a key head, 8-bit cache) the instruction issue shows: 88 us, 54 %. One row of 300
+// tokens: 9.4 us, latency throughout (three dependent look-ups, one round trip of loads, two
+// joins, and instructions fetched for the first time).
 #include <cuda_fp16.h>
 #include <cstring>
 
@@ -251,13 +252,17 @@ __device__ __forceinline__ int find_row(const uint32_t* cum, int batch, uint32_t
     return lo;
 }
 
-// Row and head of tile t, and its number among the (row, head)'s tiles.
-__device__ __noinline__ Tile find_tile(const DecArgs& a, const uint32_t* cum, uint32_t t) {
+// Row and head of tile t, and its number among the (row, head)'s tiles; `single` says that
+// CTA i has (row, head) i.
+__device__ __noinline__ Tile find_tile(const DecArgs& a, const uint32_t* cum, uint32_t t, bool single) {
     Tile x;
-    x.b = a.batch == 1 ? 0 : find_row(cum, a.batch, t / (uint32_t)a.hkv);
+    if (single)
+        x.b = (int)blockIdx.x / a.hkv;
+    else
+        x.b = a.batch == 1 ? 0 : find_row(cum, a.batch, t / (uint32_t)a.hkv);
     const uint32_t nt = cum[x.b + 1] - cum[x.b];
     const uint32_t in_row = t - cum[x.b] * (uint32_t)a.hkv;
-    x.h = (int)(in_row / nt);
+    x.h = single ? (int)blockIdx.x - x.b * a.hkv : (int)(in_row / nt);
     x.at = (int)(in_row - (uint32_t)x.h * nt);
     return x;
 }
@@ -265,14 +270,14 @@ __device__ __noinline__ Tile find_tile(const DecArgs& a, const uint32_t* cum, ui
 // The first tile from t on that begins a (row, head).
 __device__ __noinline__ uint32_t next_head(const DecArgs& a, const uint32_t* cum, uint32_t t) {
     if (t >= cum[a.batch] * (uint32_t)a.hkv) return t;
-    const Tile x = find_tile(a, cum, t);
+    const Tile x = find_tile(a, cum, t, false);
     return x.at == 0 ? t : t - x.at + cum[x.b + 1] - cum[x.b];
 }
 
 // Row of tile t's first token in the cache matrix; -1, with the flag set, when its page is
 // out of range.
-__device__ __noinline__ int locate_tile(const DecArgs& a, const Rows& rows, uint32_t t) {
-    const Tile x = find_tile(a, rows.cum, t);
+__device__ __noinline__ int locate_tile(const DecArgs& a, const Rows& rows, uint32_t t, bool single) {
+    const Tile x = find_tile(a, rows.cum, t, single);
     const int pos = (row_span(a, rows.len[x.b]).first + x.at) * kTok;
     const int page = __ldg(a.page_table + (long)rows.slot[x.b] * a.max_pages + (pos >> a.ps_log2));
     if (page < 0 || page >= a.num_pages) {
@@ -510,7 +515,16 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
     rg.total = cum[a.batch] * (uint32_t)a.hkv;
     if (rg.total == 0) return;
     uint32_t c0, c1;  // this CTA's range
-    {
+    // Short (row, head)s, and a CTA for each: no cuts at all, and no search for them.
+    const bool single = longest <= kWholeTiles && a.batch * a.hkv <= (int)gridDim.x;
+    if (single) {
+        const int b = (int)blockIdx.x / a.hkv, h = (int)blockIdx.x - b * a.hkv;
+        if (b >= a.batch) return;
+        const uint32_t nt = cum[b + 1] - cum[b];
+        if (nt == 0) return;
+        c0 = cum[b] * (uint32_t)a.hkv + h * nt;
+        c1 = c0 + nt;
+    } else {
         // short (row, head)s: as many CTAs as there may be (row, head)s
         const uint32_t least = longest <= kWholeTiles ? min((uint32_t)kMinTiles * ngroups, longest)
                                                       : (uint32_t)kMinTiles * ngroups;
@@ -567,7 +581,8 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
         const uint32_t st_base = smem_addr(kv) + tile_off<C::ROWB>(tok0, lane % LPR);
         auto issue = [&]() {
             if (sent < ntile) {
-                if ((sent & 31) == 0 && sent + lane < ntile) look = locate_tile(a, rows, t0 + sent + lane);
+                if ((sent & 31) == 0 && sent + lane < ntile)
+                    look = locate_tile(a, rows, t0 + sent + lane, single);
                 const int y = __shfl_sync(0xffffffffu, look, sent & 31);
                 bad = (bad & ~(1u << sent_s)) | (y < 0 ? 1u << sent_s : 0u);
                 if (C::TMA) {  // (one warp a group)
@@ -701,7 +716,7 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
                 if (i == ntile) break;
 
                 // Start a (row, head): its queries as mma operands, the positions they see.
-                const Tile x = find_tile(a, cum, t0 + i);
+                const Tile x = find_tile(a, cum, t0 + i, single);
                 cb = x.b;
                 ch = x.h;
                 begun = x.at > 0;
