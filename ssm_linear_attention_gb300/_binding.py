@@ -228,6 +228,12 @@ def _call(name, *args):
         raise RSSMError(name, rc)
 
 
+def entry(name):
+    """The ctypes function of an entry point, for callers that keep it (pointers as ints, structs
+    by reference; it returns the status)."""
+    return getattr(lib(), name)
+
+
 def rssm_status_string(status):
     return lib().rssm_status_string(status).decode()
 

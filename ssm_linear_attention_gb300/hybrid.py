@@ -9,6 +9,8 @@ call synchronises, so a step can be captured in a CUDA graph:
               (T > 1 drafts: append and decode, then advance by the accepted counts)
   norm:       rssm_add_rmsnorm
 """
+import ctypes
+
 import torch
 
 from . import _binding as B
@@ -77,6 +79,11 @@ class PagedAttentionDecoder:
         self.workspace = torch.zeros(max(self.ws_bytes, 16), device=dev, dtype=torch.uint8)
         self.o = torch.empty(max_batch, T, num_q_heads, head_dim, device=dev, dtype=out_dtype)
         self.lse = torch.empty(max_batch, T, num_q_heads, device=dev, dtype=torch.float32)
+        # what every call passes, made once
+        self._append, self._read = B.entry("rssm_attn_append"), B.entry("rssm_attn_read")
+        self._decode, self._advance = B.entry("rssm_attn_decode"), B.entry("rssm_attn_advance")
+        self._cache = ctypes.byref(self.cache)
+        self._ws, self._err = self.workspace.data_ptr(), self.dev_err.data_ptr()
 
     def dims(self, batch):
         return B.AttnDims(batch, self.T, self.HQ, self.HKV, self.D, self.page_size, self.num_pages,
@@ -84,12 +91,13 @@ class PagedAttentionDecoder:
                           _code(self.cache_dtype), torch_dtype_code(self.out_dtype))
 
     def _plan(self, b):
-        """What calls of b rows share: dims, the shape of q, the outputs. Kept, because a
-        small call's time is the host's."""
+        """What calls of b rows share: a reference to their dims, q's element count, the
+        outputs and their addresses. Kept, because a small call's time is the host's."""
         p = self._plans.get(b)
         if p is None:
-            p = self._plans[b] = (self.dims(b), torch.Size((b, self.T, self.HQ, self.D)),
-                                  self.o[:b], self.lse[:b])
+            o, lse = self.o[:b], self.lse[:b]
+            p = self._plans[b] = (ctypes.byref(self.dims(b)), b * self.T * self.HQ * self.D, o, lse,
+                                  o.data_ptr(), lse.data_ptr())
         return p
 
     def _stride(self, name, t, heads):
@@ -112,32 +120,47 @@ class PagedAttentionDecoder:
         n = k.numel() // (self.HKV * self.D)
         if v.shape != k.shape:
             raise ValueError("k and v must have one shape")
-        B.rssm_attn_append(self._plan(cache_indices.shape[0])[0], self.cache, n, cu_tokens, k,
-                           self._stride("k", k, self.HKV), v, self._stride("v", v, self.HKV),
-                           cache_indices, self.dev_err, stream)
+        rc = self._append(self._plan(cache_indices.shape[0])[0], self._cache, n, B._ptr(cu_tokens),
+                          k.data_ptr(), self._stride("k", k, self.HKV), v.data_ptr(),
+                          self._stride("v", v, self.HKV), cache_indices.data_ptr(), self._err,
+                          B._stream(stream))
+        if rc:
+            raise B.RSSMError("rssm_attn_append", rc)
 
     def decode(self, q, cache_indices, appended=True, o=None, lse=None, with_lse=False,
                stream=None):
         """Attention of q [b, T, HQ, D] over the rows' tokens. appended: the queries' own
         tokens are in the cache and visible (see rssm_attn_decode). Returns o [b, T, HQ, D],
         with with_lse also lse [b, T, HQ]."""
-        dims, shape, own_o, own_lse = self._plan(cache_indices.shape[0])
-        if dims.batch > self.max_batch or q.numel() != shape.numel():
+        b = cache_indices.shape[0]
+        dims, count, own_o, own_lse, o_ptr, lse_ptr = self._plan(b)
+        if b > self.max_batch or q.numel() != count:
             raise ValueError("q must be [b, %d, %d, %d], b = len(cache_indices) <= %d"
                              % (self.T, self.HQ, self.D, self.max_batch))
         if o is None:
             o = own_o
-        if lse is None and with_lse:
+        else:
+            o_ptr = o.data_ptr()
+        if lse is not None:
+            lse_ptr = lse.data_ptr()
+        elif with_lse:
             lse = own_lse
-        B.rssm_attn_decode(dims, self.cache, appended, self.scale, self.window, q,
-                           self._stride("q", q, self.HQ), cache_indices, self.workspace,
-                           self.ws_bytes, o, lse, self.dev_err, stream)
+        else:
+            lse_ptr = None
+        rc = self._decode(dims, self._cache, appended, self.scale, self.window, q.data_ptr(),
+                          self._stride("q", q, self.HQ), cache_indices.data_ptr(), self._ws,
+                          self.ws_bytes, o_ptr, lse_ptr, self._err, B._stream(stream))
+        if rc:
+            raise B.RSSMError("rssm_attn_decode", rc)
         return (o, lse) if with_lse else o
 
     def advance(self, cache_indices, num_accepted=None, cu_tokens=None, stream=None):
         """Commit the appended tokens (of T drafts: the first num_accepted[b])."""
-        B.rssm_attn_advance(self._plan(cache_indices.shape[0])[0], self.cache, cu_tokens, num_accepted,
-                            cache_indices, self.dev_err, stream)
+        rc = self._advance(self._plan(cache_indices.shape[0])[0], self._cache, B._ptr(cu_tokens),
+                           B._ptr(num_accepted), cache_indices.data_ptr(), self._err,
+                           B._stream(stream))
+        if rc:
+            raise B.RSSMError("rssm_attn_advance", rc)
 
     def step(self, q, k, v, cache_indices, o=None, stream=None):
         """One decode step for rows cache_indices (padding rows: -1): append, decode,
@@ -159,8 +182,11 @@ class PagedAttentionDecoder:
             k = torch.empty(shape, device=self.device, dtype=self.out_dtype)
         if v is None:
             v = torch.empty(shape, device=self.device, dtype=self.out_dtype)
-        B.rssm_attn_read(self._plan(cache_indices.shape[0])[0], self.cache, n_tokens, cu_tokens,
-                         first, cache_indices, k, v, self.dev_err, stream)
+        rc = self._read(self._plan(cache_indices.shape[0])[0], self._cache, n_tokens,
+                        B._ptr(cu_tokens), B._ptr(first), cache_indices.data_ptr(), k.data_ptr(),
+                        v.data_ptr(), self._err, B._stream(stream))
+        if rc:
+            raise B.RSSMError("rssm_attn_read", rc)
         return k, v
 
     def reset_slots(self, slots, stream=None):
@@ -187,6 +213,7 @@ class AddRMSNorm:
             groups = self.cols // scale_group if scale_group else 1
             self.scale = torch.empty(max_rows, groups, device=dev, dtype=torch.float32)
         self._plans = {}
+        self._call, self._w = B.entry("rssm_add_rmsnorm"), self.weight.data_ptr()
 
     def dims(self, rows):
         return B.NormDims(rows, self.cols, self.scale_group, torch_dtype_code(self.act_dtype),
@@ -195,8 +222,10 @@ class AddRMSNorm:
     def _plan(self, rows):
         p = self._plans.get(rows)
         if p is None:
-            p = self._plans[rows] = (self.dims(rows), self.y[:rows],
-                                     None if self.scale is None else self.scale[:rows])
+            y = self.y[:rows]
+            scale = None if self.scale is None else self.scale[:rows]
+            p = self._plans[rows] = (ctypes.byref(self.dims(rows)), y, scale, y.data_ptr(),
+                                     B._ptr(scale))
         return p
 
     def __call__(self, x, residual=None, residual_out=None, y=None, scale=None, stream=None):
@@ -211,11 +240,19 @@ class AddRMSNorm:
                                   not t.is_contiguous()):
                 raise ValueError("x and the residuals: dense [rows, %d] %s" % (self.cols,
                                                                                self.act_dtype))
-        dims, own_y, own_scale = self._plan(rows)
+        dims, own_y, own_scale, y_ptr, scale_ptr = self._plan(rows)
         if y is None:
             y = own_y
+        else:
+            y_ptr = y.data_ptr()
         if scale is None:
             scale = own_scale
-        B.rssm_add_rmsnorm(dims, x, residual, self.weight, self.eps,
-                           residual if residual_out is None else residual_out, y, scale, stream)
+        else:
+            scale_ptr = scale.data_ptr()
+        res = None if residual is None else residual.data_ptr()
+        rc = self._call(dims, x.data_ptr(), res, self._w, self.eps,
+                        res if residual_out is None else residual_out.data_ptr(), y_ptr, scale_ptr,
+                        B._stream(stream))
+        if rc:
+            raise B.RSSMError("rssm_add_rmsnorm", rc)
         return y, scale
