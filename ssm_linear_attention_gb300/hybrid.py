@@ -31,7 +31,32 @@ def _check(name, t, shape, dtype, device):
     return t
 
 
-class PagedAttentionDecoder:
+def _check_out(name, t, count, dtype):
+    if t.dtype is not dtype or t.numel() != count or not t.is_contiguous():
+        raise ValueError("%s must be dense, %d %s values" % (name, count, dtype))
+    return t.data_ptr()
+
+
+def _check_list(name, t, count):
+    if t is None:
+        return None
+    if t.dtype is not torch.int32 or t.shape[0] != count or not t.is_contiguous():
+        raise ValueError("%s must be a dense int32 list of %d" % (name, count))
+    return t.data_ptr()
+
+
+class _Fixed:
+    """Calls pass addresses that were taken once, so a runner's tensors and sizes stay the
+    ones it was made with: new values are copied into them."""
+    _free = ()
+
+    def __setattr__(self, name, value):
+        if "_plans" in self.__dict__ and name not in self._free and name[0] != "_":
+            raise AttributeError("%s is fixed when the runner is made; copy into its tensors" % name)
+        object.__setattr__(self, name, value)
+
+
+class PagedAttentionDecoder(_Fixed):
     """Attention decode for one layer over a paged cache.
 
     Buffers: k_cache, v_cache [num_pages, HKV, page_size, D] (cache_dtype: bfloat16 or
@@ -39,7 +64,10 @@ class PagedAttentionDecoder:
     only), page_table [num_slots, max_pages] int32 (-1: no page yet; the caller assigns
     pages), slot_len [num_slots] int32, and workspace / o / lse for up to max_batch rows of
     T query tokens. Any of the caches, the scales, page_table and slot_len can be the
-    caller's tensors (page_table and slot_len are commonly shared by a model's layers)."""
+    caller's tensors (page_table and slot_len are commonly shared by a model's layers). scale
+    and window may be set between calls."""
+
+    _free = ("scale", "window")
 
     def __init__(self, num_q_heads, num_kv_heads, head_dim, page_size, num_pages, num_slots,
                  max_pages, max_batch, T=1, act_dtype=torch.bfloat16, cache_dtype=torch.bfloat16,
@@ -73,7 +101,6 @@ class PagedAttentionDecoder:
         self.dev_err = torch.zeros(4, device=dev, dtype=torch.int32)
         self.cache = B.attn_cache(self.k_cache, self.v_cache, self.k_scale, self.v_scale,
                                   self.page_table, self.slot_len)
-        self._plans = {}
         self.ws_bytes = B.rssm_attn_workspace_size(self.dims(max_batch))
         # zero-filled: the decode call keeps its arrival counters here
         self.workspace = torch.zeros(max(self.ws_bytes, 16), device=dev, dtype=torch.uint8)
@@ -84,15 +111,19 @@ class PagedAttentionDecoder:
         self._decode, self._advance = B.entry("rssm_attn_decode"), B.entry("rssm_attn_advance")
         self._cache = ctypes.byref(self.cache)
         self._ws, self._err = self.workspace.data_ptr(), self.dev_err.data_ptr()
+        self._plans = {}
 
     def dims(self, batch):
         return B.AttnDims(batch, self.T, self.HQ, self.HKV, self.D, self.page_size, self.num_pages,
                           self.max_pages, self.num_slots, torch_dtype_code(self.act_dtype),
                           _code(self.cache_dtype), torch_dtype_code(self.out_dtype))
 
-    def _plan(self, b):
+    def _plan(self, cache_indices):
         """What calls of b rows share: a reference to their dims, q's element count, the
         outputs and their addresses. Kept, because a small call's time is the host's."""
+        b = cache_indices.shape[0]
+        if cache_indices.dtype is not torch.int32 or not cache_indices.is_contiguous():
+            raise ValueError("cache_indices must be a dense int32 list")
         p = self._plans.get(b)
         if p is None:
             o, lse = self.o[:b], self.lse[:b]
@@ -120,7 +151,8 @@ class PagedAttentionDecoder:
         n = k.numel() // (self.HKV * self.D)
         if v.shape != k.shape:
             raise ValueError("k and v must have one shape")
-        rc = self._append(self._plan(cache_indices.shape[0])[0], self._cache, n, B._ptr(cu_tokens),
+        rc = self._append(self._plan(cache_indices)[0], self._cache, n,
+                          _check_list("cu_tokens", cu_tokens, cache_indices.shape[0] + 1),
                           k.data_ptr(), self._stride("k", k, self.HKV), v.data_ptr(),
                           self._stride("v", v, self.HKV), cache_indices.data_ptr(), self._err,
                           B._stream(stream))
@@ -132,17 +164,16 @@ class PagedAttentionDecoder:
         """Attention of q [b, T, HQ, D] over the rows' tokens. appended: the queries' own
         tokens are in the cache and visible (see rssm_attn_decode). Returns o [b, T, HQ, D],
         with with_lse also lse [b, T, HQ]."""
-        b = cache_indices.shape[0]
-        dims, count, own_o, own_lse, o_ptr, lse_ptr = self._plan(b)
-        if b > self.max_batch or q.numel() != count:
+        dims, count, own_o, own_lse, o_ptr, lse_ptr = self._plan(cache_indices)
+        if q.numel() != count or own_lse.shape[0] != cache_indices.shape[0]:
             raise ValueError("q must be [b, %d, %d, %d], b = len(cache_indices) <= %d"
                              % (self.T, self.HQ, self.D, self.max_batch))
         if o is None:
             o = own_o
         else:
-            o_ptr = o.data_ptr()
+            o_ptr = _check_out("o", o, count, self.out_dtype)
         if lse is not None:
-            lse_ptr = lse.data_ptr()
+            lse_ptr = _check_out("lse", lse, count // self.D, torch.float32)
         elif with_lse:
             lse = own_lse
         else:
@@ -156,9 +187,11 @@ class PagedAttentionDecoder:
 
     def advance(self, cache_indices, num_accepted=None, cu_tokens=None, stream=None):
         """Commit the appended tokens (of T drafts: the first num_accepted[b])."""
-        rc = self._advance(self._plan(cache_indices.shape[0])[0], self._cache, B._ptr(cu_tokens),
-                           B._ptr(num_accepted), cache_indices.data_ptr(), self._err,
-                           B._stream(stream))
+        b = cache_indices.shape[0]
+        rc = self._advance(self._plan(cache_indices)[0], self._cache,
+                           _check_list("cu_tokens", cu_tokens, b + 1),
+                           _check_list("num_accepted", num_accepted, b), cache_indices.data_ptr(),
+                           self._err, B._stream(stream))
         if rc:
             raise B.RSSMError("rssm_attn_advance", rc)
 
@@ -182,9 +215,11 @@ class PagedAttentionDecoder:
             k = torch.empty(shape, device=self.device, dtype=self.out_dtype)
         if v is None:
             v = torch.empty(shape, device=self.device, dtype=self.out_dtype)
-        rc = self._read(self._plan(cache_indices.shape[0])[0], self._cache, n_tokens,
-                        B._ptr(cu_tokens), B._ptr(first), cache_indices.data_ptr(), k.data_ptr(),
-                        v.data_ptr(), self._err, B._stream(stream))
+        b = cache_indices.shape[0]
+        rc = self._read(self._plan(cache_indices)[0], self._cache, n_tokens,
+                        _check_list("cu_tokens", cu_tokens, b + 1), _check_list("first", first, b),
+                        cache_indices.data_ptr(), k.data_ptr(), v.data_ptr(), self._err,
+                        B._stream(stream))
         if rc:
             raise B.RSSMError("rssm_attn_read", rc)
         return k, v
@@ -196,10 +231,13 @@ class PagedAttentionDecoder:
                                stream)
 
 
-class AddRMSNorm:
+class AddRMSNorm(_Fixed):
     """Residual add and RMS norm for one place in a model: r = x + residual, y = r /
     sqrt(mean(r^2) + eps) * weight, for up to max_rows rows. With out_dtype float8_e4m3fn y
-    comes with float32 scales [rows, cols / scale_group] ([rows, 1] for scale_group 0)."""
+    comes with float32 scales [rows, cols / scale_group] ([rows, 1] for scale_group 0). eps may
+    be set between calls."""
+
+    _free = ("eps",)
 
     def __init__(self, weight, eps, max_rows, act_dtype=torch.bfloat16, out_dtype=torch.bfloat16,
                  scale_group=0, device=None):
@@ -212,20 +250,25 @@ class AddRMSNorm:
         if out_dtype == torch.float8_e4m3fn:
             groups = self.cols // scale_group if scale_group else 1
             self.scale = torch.empty(max_rows, groups, device=dev, dtype=torch.float32)
-        self._plans = {}
         self._call, self._w = B.entry("rssm_add_rmsnorm"), self.weight.data_ptr()
+        self._plans = {}
 
     def dims(self, rows):
         return B.NormDims(rows, self.cols, self.scale_group, torch_dtype_code(self.act_dtype),
                           _code(self.out_dtype))
 
     def _plan(self, rows):
+        """A reference to the dims of rows rows, the outputs and their addresses (no outputs
+        beyond max_rows)."""
         p = self._plans.get(rows)
         if p is None:
-            y = self.y[:rows]
-            scale = None if self.scale is None else self.scale[:rows]
-            p = self._plans[rows] = (ctypes.byref(self.dims(rows)), y, scale, y.data_ptr(),
-                                     B._ptr(scale))
+            y = scale = None
+            if rows <= self.max_rows:
+                y = self.y[:rows]
+                scale = None if self.scale is None else self.scale[:rows]
+            p = (ctypes.byref(self.dims(rows)), y, scale, B._ptr(y), B._ptr(scale))
+            if rows <= self.max_rows:
+                self._plans[rows] = p
         return p
 
     def __call__(self, x, residual=None, residual_out=None, y=None, scale=None, stream=None):
@@ -233,8 +276,10 @@ class AddRMSNorm:
         replaces residual (without a residual it is not stored)."""
         n = x.numel()
         rows = n // self.cols
-        if rows * self.cols != n or (y is None and rows > self.max_rows):
-            raise ValueError("x must be [rows, %d], rows <= %d" % (self.cols, self.max_rows))
+        if rows * self.cols != n or (rows > self.max_rows and
+                                     (y is None or (scale is None and self.scale is not None))):
+            raise ValueError("x must be [rows, %d], rows <= %d unless the outputs are given"
+                             % (self.cols, self.max_rows))
         for t in (x, residual, residual_out):
             if t is not None and (t.dtype is not self.act_dtype or t.numel() != n or
                                   not t.is_contiguous()):
@@ -244,11 +289,11 @@ class AddRMSNorm:
         if y is None:
             y = own_y
         else:
-            y_ptr = y.data_ptr()
+            y_ptr = _check_out("y", y, n, self.out_dtype)
         if scale is None:
             scale = own_scale
-        else:
-            scale_ptr = scale.data_ptr()
+        elif self.scale is not None:
+            scale_ptr = _check_out("scale", scale, rows * self.scale.shape[1], torch.float32)
         res = None if residual is None else residual.data_ptr()
         rc = self._call(dims, x.data_ptr(), res, self._w, self.eps,
                         res if residual_out is None else residual_out.data_ptr(), y_ptr, scale_ptr,

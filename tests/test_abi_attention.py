@@ -3,6 +3,7 @@
 import ctypes
 
 import pytest
+import torch
 
 import ssm_linear_attention_gb300 as ssm
 from ssm_linear_attention_gb300 import _binding as B
@@ -124,3 +125,44 @@ def test_norm_arguments(lib):
                      (dict(scale=None), INV), (dict(scale=FAKE + 4), INV)):
         assert call(**kw) == code, kw
     assert call(rows=0, x=None) == B.RSSM_OK
+
+
+def test_runner_refusals(lib):
+    """What the runners turn away before a call: lists and outputs of another type or size (the
+    kernels would read or write past them), rows beyond the buffers, replaced buffers."""
+    dec = ssm.PagedAttentionDecoder(8, 2, 64, 16, 4, 4, 2, 3, T=2, device="cpu")
+    i32 = dict(dtype=torch.int32)
+    ci, cu = torch.zeros(3, **i32), torch.zeros(4, **i32)
+    bf = dict(dtype=torch.bfloat16)
+    q, k = torch.zeros(3, 2, 8, 64, **bf), torch.zeros(3, 2, 2, 64, **bf)
+    bad = [lambda: dec.decode(q, ci.long()), lambda: dec.decode(q, torch.zeros(6, **i32)[::2]),
+           lambda: dec.decode(q[:2], ci), lambda: dec.decode(q.float(), ci),
+           lambda: dec.decode(torch.zeros(4, 2, 8, 64, **bf), torch.zeros(4, **i32)),
+           lambda: dec.decode(q, ci, o=torch.zeros(2, 2, 8, 64, **bf)),
+           lambda: dec.decode(q, ci, o=torch.zeros(3, 2, 8, 64)),
+           lambda: dec.decode(q, ci, lse=torch.zeros(3, 2, 7)),
+           lambda: dec.append(k, k[:2], ci), lambda: dec.append(k, k.float(), ci),
+           lambda: dec.append(k, k, ci, cu_tokens=cu[:3]), lambda: dec.append(k, k, ci, cu_tokens=cu.long()),
+           lambda: dec.advance(ci, num_accepted=torch.zeros(2, **i32)),
+           lambda: dec.advance(ci, cu_tokens=cu.long()),
+           lambda: dec.read(ci, cu[:3], 5), lambda: dec.read(ci, cu, 5, first=cu[:2]),
+           lambda: dec.read(ci, cu, 5, k=torch.zeros(4, 2, 64, **bf))]
+    for call in bad:
+        with pytest.raises(ValueError):
+            call()
+    for name in ("page_table", "slot_len", "k_cache", "workspace", "dev_err", "T", "max_batch"):
+        with pytest.raises(AttributeError):
+            setattr(dec, name, getattr(dec, name))
+    dec.window, dec.scale = 7, 0.5
+
+    norm = ssm.AddRMSNorm(torch.ones(128), 1e-5, 2, out_dtype=torch.float8_e4m3fn, device="cpu")
+    x, y = torch.zeros(3, 128, **bf), torch.zeros(3, 128, dtype=torch.float8_e4m3fn)
+    bad = [lambda: norm(x), lambda: norm(x, y=y), lambda: norm(x[:2].float()), lambda: norm(x[:, :64]),
+           lambda: norm(x[:2], y=y), lambda: norm(x[:2], y=y[:2].view(torch.uint8)),
+           lambda: norm(x[:2], x), lambda: norm(x[:2], scale=torch.zeros(1, 1))]
+    for call in bad:
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(AttributeError):
+        norm.weight = torch.zeros(128)
+    norm.eps = 1e-6
