@@ -9,6 +9,12 @@
 // tokens, a chain of dependent loads, while the others move this block's vectors, D / 8
 // lanes to a vector, 8 values to a lane (one 16-byte load of bf16), a vector of each of
 // several tokens at once.
+//
+// Measured (one GB300, GPU time of a call; "of" the measured copy bandwidth; 8 heads, D 128,
+// bf16 against an 8-bit cache): append of 61k tokens 72.5 us, 5.2 TB/s, 77 % of it; read-back
+// of 156k tokens 160 us, 6.1 TB/s, 89 %; append of one token of 512 rows 3.6 us. Loading the
+// next vectors while these are rounded costs more in CTAs (registers) than it hides: append
+// 83 us with 3 CTAs an SM, 88 with 4 and spills.
 #include <cuda_fp8.h>
 
 #include "attn.cuh"

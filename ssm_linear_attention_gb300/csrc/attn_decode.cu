@@ -28,11 +28,11 @@
 // joins the CTAs' results, in an order that the lengths and the machine alone fix.
 //
 // Measured (one GB300, GPU time of a call; "of" the measured copy bandwidth): 256 rows of 2k
-// to 8k tokens, 8 key heads of 4 queries, D 128, 8-bit cache: 443 us, 6.4 TB/s, 94 % of it;
-// 2 rows of 131k and 64k tokens, bf16 cache: 128 us, 6.25 TB/s, 92 %. With M = 32 (128 rows of 500 to
-// 2000 tokens, 4 drafts, 8 queries a key head, bf16 cache) the instruction issue shows: 88 us, 54 %. One row of 300
-// tokens: 9.4 us, latency throughout (three dependent look-ups, one round trip of loads, two
-// joins, and instructions fetched for the first time).
+// to 8k tokens, 8 key heads of 4 queries, D 128, 8-bit cache: 443 us, 6.4 TB/s, 95 % of it;
+// 2 rows of 131k and 64k tokens, bf16 cache: 128 us, 6.25 TB/s, 92 %. With M = 32 (128 rows
+// of 500 to 2000 tokens, 4 drafts, 8 queries a key head, bf16 cache) the instructions show:
+// 88 us, 54 %. One row of 300 tokens: 9.4 us, latency throughout (three dependent look-ups,
+// one round trip of loads, two joins, and instructions fetched for the first time).
 #include <cuda_fp16.h>
 #include <cstring>
 
