@@ -566,3 +566,120 @@ def test_every_8_bit_code_counts(d):
         torch.cuda.synchronize()
         want = float(val[t]) * dec.scale
         assert abs(float(lse[0, 0, 0]) - want) <= 2.0 ** -19 * abs(want) + 2e-6
+
+
+# 9 queries a key head and more: chunks of 128 tokens, query blocks of 16, 32 and 64
+WIDE = [
+    (9, [0, 1, 15, 16, 17, 127, 128, 129, 2500], dict(hq=18, hkv=2, page=16)),
+    (9, [0, 1, 15, 16, 17, 127, 128, 129, 2500], dict(hq=16, hkv=1, d=64, page=64, cache=FP8)),
+    (4, [255, 256, 257, 3], dict(hq=34, hkv=2, page=32, cache=FP8)),
+    (4, [1000, 111, 112, 113], dict(hq=16, hkv=2, T=3, d=64, page=16)),
+    (3, [5, 4000, 300], dict(hq=8, hkv=2, T=8, page=256, out=torch.float32)),
+    (3, [130, 700, 64], dict(hq=22, hkv=2, T=3, page=16, cache=FP8, out=torch.float32)),
+    (2, [640, 1300], dict(hq=21, hkv=1, T=3, d=64, page=128)),
+    (2, [641, 1301], dict(hq=16, hkv=2, T=8, page=64, cache=FP8, d=64)),
+    (1, [70001], dict(hq=32, hkv=1, page=64)),
+    (2, [30000, 77], dict(hq=64, hkv=1, page=32, cache=FP8)),
+    (3, [900, 60, 1025], dict(hq=16, hkv=2, T=4, window=130, page=16)),
+    (3, [900, 60, 1025], dict(hq=16, hkv=2, T=8, window=128, page=64, cache=FP8)),
+    (2, [500, 2], dict(hq=16, hkv=1, T=2, window=1, page=32, d=64)),
+    (1100, [(53 * i) % 35 for i in range(1100)], dict(hkv=1, hq=16, d=64)),
+    (200, [(37 * i) % 301 for i in range(200)], dict(hkv=3, hq=48, T=2, page=32)),
+]
+
+
+@pytest.mark.parametrize("batch,lens,kw", WIDE)
+@pytest.mark.parametrize("appended", [True, False])
+def test_decode_of_many_queries_matches_float64(batch, lens, kw, appended):
+    test_decode_matches_float64(batch, lens, kw, appended)
+
+
+@pytest.mark.parametrize("T,hq", [(2, 16), (4, 16), (8, 16)])
+@pytest.mark.parametrize("cache", [torch.bfloat16, FP8])
+def test_many_queries_and_missing_pages(cache, T, hq):
+    """Pages that are missing at the start (the first chunk is hidden as a whole), inside a
+    chunk, and of a whole row."""
+    import ssm_linear_attention_gb300 as ssm
+    lens = [400, 290, 33]
+    dec, ci, table, slots, g = make(3, lens, hq=hq, hkv=2, T=T, cache=cache, seed=31)
+    fill(dec, ci, table, slots, lens, g)
+    q = torch.randn(3, T, hq, 128, generator=g, device="cuda").to(torch.bfloat16)
+    dec.page_table[slots[0], :9] = -1                      # positions 0..143
+    dec.page_table[slots[1], 3] = dec.num_pages            # 48..63
+    dec.page_table[slots[1], 16] = -5                      # 256..271
+    dec.page_table[slots[2]] = -1
+    o, lse = dec.decode(q, ci, appended=False, with_lse=True)
+    torch.cuda.synchronize()
+    assert int(dec.dev_err[0]) == ssm.RSSM_DEVERR_PAGE
+    for b, hid in ((0, set(range(144))), (1, set(range(48, 64)) | set(range(256, 272)))):
+        ref = reference(dec, q[b:b + 1], table, slots[b:b + 1], lens[b:b + 1], False, hid)
+        check(dec, o[b:b + 1], lse[b:b + 1], ref)
+    assert bool((o[2] == 0).all()) and bool((lse[2] == -math.inf).all())
+
+
+@pytest.mark.parametrize("T,hq", [(4, 8), (8, 8), (16, 8)])
+def test_many_queries_window_and_drafts_nan_included(T, hq):
+    """Values that are not finite at positions that only some drafts see: the last tokens and
+    those at the windows' beginnings."""
+    lens = [300]
+    W = 150
+    dec, ci, table, slots, g = make(1, lens, hq=hq, hkv=2, T=T, window=W, seed=41)
+    fill(dec, ci, table, slots, lens, g)
+    k = torch.randn(1, T, 2, 128, generator=g, device="cuda").bfloat16()
+    v = torch.randn(1, T, 2, 128, generator=g, device="cuda").bfloat16()
+    v[0, T - 1, :, 7] = float("nan")
+    v[0, T - 2, 1, 100] = float("inf")
+    dec.append(k, v, ci)
+    first = lens[0] + 1 - W                                  # draft 0 alone sees this one
+    page, off = int(table[slots[0]][first // 16]), first % 16
+    dec.v_cache[page, 0, off, 64] = float("-inf")
+    q = torch.randn(1, T, hq, 128, generator=g, device="cuda").bfloat16()
+    o, lse = dec.decode(q, ci, with_lse=True)
+    torch.cuda.synchronize()
+    G = hq // 2
+    want = torch.zeros(1, T, hq, 128, dtype=torch.bool, device="cuda")
+    want[0, T - 1, :, 7] = True
+    assert torch.equal(torch.isnan(o), want)
+    inf = torch.zeros_like(want)
+    inf[0, T - 2:, G:, 100] = True
+    inf[0, 0, :G, 64] = True
+    assert torch.equal(torch.isinf(o), inf)
+    assert bool((o[0, T - 2:, G:, 100] > 0).all()) and bool((o[0, 0, :G, 64] < 0).all())
+    ref = reference(dec, q, table, slots, lens, True)
+    clean = [t.clone() for t in ref]
+    bad = want | inf
+    got = o.clone()
+    got[bad] = 0
+    clean[0][bad] = 0
+    clean[2][bad] = 0
+    check(dec, got, lse, clean)
+
+
+@pytest.mark.parametrize("cache", [torch.bfloat16, FP8])
+@pytest.mark.parametrize("T", [4, 8])
+def test_many_queries_whose_maxima_move(cache, T):
+    """Scores that rise through the row (each chunk passes the maximum by far), fall, and rise for
+    some queries alone."""
+    lens = [1500, 700]
+    dec, ci, table, slots, g = make(2, lens, hq=16, hkv=2, T=T, cache=cache, seed=51)
+    n = sum(lens)
+    k = 0.1 * torch.randn(n, 2, 128, generator=g, device="cuda")
+    v = torch.randn(n, 2, 128, generator=g, device="cuda")
+    rise = torch.cat([torch.arange(m, device="cuda") for m in lens])[:, None] / 16.0
+    k[:, :, 0], k[:, :, 1] = rise, -rise
+    keep = dec.slot_len.clone()
+    dec.slot_len.zero_()
+    dec.append(k.bfloat16(), v.bfloat16(), ci,
+               cu_tokens=torch.tensor([0, lens[0], n], dtype=torch.int32, device="cuda"))
+    dec.slot_len.copy_(keep)
+    q = 0.3 * torch.randn(2, T, 16, 128, generator=g, device="cuda")
+    q[:, :, 0::3, 0] = 20.0
+    q[:, :, 1::3, 1] = 20.0
+    o, lse = dec.decode(q.bfloat16(), ci, appended=False, with_lse=True)
+    torch.cuda.synchronize()
+    assert int(dec.dev_err.sum()) == 0
+    o64, lse64, w = reference(dec, q.bfloat16(), table, slots, lens, False)
+    # scores reach the hundreds: float32 leaves 2^-24 of them, which the weights see absolutely
+    bound = 2.0 ** -8 * o64.abs() + (2.0 ** -15 + 2.0 ** -16) * 8 * w + 1e-30
+    assert float(((o.double() - o64).abs() / bound).max()) <= 1.0
+    assert float((lse.double() - lse64).abs().max()) <= 2.0 ** -22 * float(lse64.abs().max()) + 2e-5
