@@ -982,7 +982,7 @@ extern "C" int rssm_attn_decode(const rssm_attn_dims* d, const rssm_attn_cache* 
     a.num_pages = d->num_pages;
     a.max_pages = d->max_pages;
     a.num_slots = d->num_slots;
-    a.window = window;
+    a.window = window < (1 << 30) ? window : 1 << 30;  // (no row is longer: sums with it stay in 32 bits)
     a.appended = appended != 0;
     a.M = a.T * G;
     a.MT = a.M <= 8 ? 1 : a.M <= 16 ? 2 : a.M <= 32 ? 4 : 8;

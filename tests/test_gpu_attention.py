@@ -683,3 +683,18 @@ def test_many_queries_whose_maxima_move(cache, T):
     bound = 2.0 ** -8 * o64.abs() + (2.0 ** -15 + 2.0 ** -16) * 8 * w + 1e-30
     assert float(((o.double() - o64).abs() / bound).max()) <= 1.0
     assert float((lse.double() - lse64).abs().max()) <= 2.0 ** -22 * float(lse64.abs().max()) + 2e-5
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 30, 2 ** 30 - 1])
+@pytest.mark.parametrize("hq", [2, 16])
+def test_a_window_beyond_any_length(window, hq):
+    lens = [130, 20]
+    dec, ci, table, slots, g = make(2, lens, hq=hq, hkv=2, T=4, window=window, seed=61)
+    fill(dec, ci, table, slots, lens, g)
+    k = torch.randn(2, 4, 2, 128, generator=g, device="cuda").bfloat16()
+    dec.append(k, k, ci)
+    q = torch.randn(2, 4, hq, 128, generator=g, device="cuda").bfloat16()
+    o, lse = dec.decode(q, ci, with_lse=True)
+    torch.cuda.synchronize()
+    dec.window = 0
+    check(dec, o, lse, reference(dec, q, table, slots, lens, True))
