@@ -231,12 +231,12 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
     }
 
     // ------------------------------------------------------- the call's tile list
-    const uint32_t longest = list_tiles<kDecThreads, kMaxRows>(a, rows, scan);
+    const uint32_t longest = list_tiles<kDecThreads, kMaxRows, 1>(a, rows, scan);
     write_empty_rows<D, kDecThreads>(a, rows);
     Cuts rg;
     uint32_t c0, c1;  // this CTA's range
     bool single;
-    if (!cut_tiles(a, cum, longest, (uint32_t)kMinTiles * ngroups, rg, c0, c1, single)) return;
+    if (!cut_tiles(a, cum, longest, (uint32_t)kMinTiles * ngroups, kWholeTiles, rg, c0, c1, single)) return;
     const uint32_t gbase = (c1 - c0) / (uint32_t)ngroups, grem = (c1 - c0) - gbase * (uint32_t)ngroups;
 
     // ------------------------------------------------------- stream the range

@@ -226,8 +226,8 @@ struct Run {
 };
 
 // Tiles of the call's rows into `rows`, bad slots and lengths flagged; returns the tiles of the
-// longest row. All THREADS threads of the CTA, ROWS rows at most; scan: a value of shared memory per warp.
-template <int THREADS, int ROWS>
+// longest row. All THREADS threads of the CTA, ROWS rows at most; a list in units of UNIT tiles; scan: a value of shared memory per warp.
+template <int THREADS, int ROWS, int UNIT>
 __device__ __forceinline__ uint32_t list_tiles(const DecArgs& a, const Rows& rows, uint2* scan) {
     constexpr int WARPS = THREADS / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -251,7 +251,7 @@ __device__ __forceinline__ uint32_t list_tiles(const DecArgs& a, const Rows& row
                 if (blockIdx.x == 0) set_dev_err(a.dev_err, RSSM_DEVERR_CURSOR);
                 len[i] = -1;
             }
-            n[i] = len[i] < 0 ? 0 : row_span(a, len[i]).tiles;
+            n[i] = len[i] < 0 ? 0 : (row_span(a, len[i]).tiles + UNIT - 1) / UNIT;
             if (tid * R + i < a.batch) {
                 rows.len[tid * R + i] = len[i];
                 rows.slot[tid * R + i] = slot[i];
@@ -306,14 +306,14 @@ __device__ __forceinline__ void write_empty_rows(const DecArgs& a, const Rows& r
 }
 
 // This CTA's range [c0, c1) of the tile list; false when it has none. least_tiles: a CTA gets at least
-// so many before another joins in. single: every CTA has a (row, head) of its own.
+// so many before another joins in. whole: the longest (row, head) that no CTAs share. single: every CTA has a (row, head) of its own.
 __device__ __forceinline__ bool cut_tiles(const DecArgs& a, const uint32_t* cum, uint32_t longest,
-                                          uint32_t least_tiles, Cuts& rg, uint32_t& c0, uint32_t& c1,
+                                          uint32_t least_tiles, uint32_t whole, Cuts& rg, uint32_t& c0, uint32_t& c1,
                                           bool& single) {
     rg.total = cum[a.batch] * (uint32_t)a.hkv;
     if (rg.total == 0) return false;
     // Short (row, head)s, and a CTA for each: no cuts at all, and no search for them.
-    single = longest <= kWholeTiles && a.batch * a.hkv <= (int)gridDim.x;
+    single = longest <= whole && a.batch * a.hkv <= (int)gridDim.x;
     if (single) {
         const int b = (int)blockIdx.x / a.hkv, h = (int)blockIdx.x - b * a.hkv;
         if (b >= a.batch) return false;
@@ -323,14 +323,14 @@ __device__ __forceinline__ bool cut_tiles(const DecArgs& a, const uint32_t* cum,
         c1 = c0 + nt;
     } else {
         // short (row, head)s: as many CTAs as there may be (row, head)s
-        const uint32_t least = longest <= kWholeTiles ? min(least_tiles, longest) : least_tiles;
+        const uint32_t least = longest <= whole ? min(least_tiles, longest) : least_tiles;
         rg.ctas = (int)min(gridDim.x, (rg.total + least - 1) / least);
         rg.base = rg.total / (uint32_t)rg.ctas;
         rg.rem = rg.total - rg.base * (uint32_t)rg.ctas;
         if ((int)blockIdx.x >= rg.ctas) return false;
         c0 = even_cut(rg, blockIdx.x);
         c1 = even_cut(rg, blockIdx.x + 1);
-        if (longest <= kWholeTiles) {
+        if (longest <= whole) {
             c0 = next_head(a, cum, c0);
             c1 = next_head(a, cum, c1);
             if (c0 >= c1) return false;

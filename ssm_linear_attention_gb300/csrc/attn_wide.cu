@@ -20,15 +20,19 @@
 // one before. The descriptors are made by the whole warp and only stepped by the elected lane:
 // built inside its branch they cost more than the products (1100 against 480 cycles for eight).
 //
+// The list's unit is a chunk here: a cut never leaves two CTAs a part of one each.
+//
 // Measured (one GB300, GPU time of a call; in brackets the warp-level kernel that took these
 // calls before): 128 rows of 500 to 2000 tokens, 4 drafts, 4 key heads of 8 queries, D 128, bf16
-// cache: 67 us, 4.8 TB/s, 71 % of the measured copy bandwidth [88]; 26 rows of 2.8k to 11k tokens,
-// M 32, 8-bit cache: 140 us [183], bound by shared memory (loaded, read, written as f16, read by
-// the products); 147 rows of 500 to 2090 tokens, M 32, D 64, bf16: 117 us [130]; 34 rows of 120
-// to 470, M 32, bf16: 12.7 us [17.4]. Short (row, head)s, several to a CTA, lose: each costs some
-// 4 us beside its chunks (first maxima, the output): 24 rows of 113 tokens, M 64: 24.8 us
-// [22.6]; 55 rows of 100 to 384, M 32, 8-bit, D 64: 33 us [25.6]. Lengths are on the device, so
-// that no rule on the call can tell these from the others.
+// cache: 65.7 us, 4.9 TB/s, 72 % of the measured copy bandwidth [88]; 26 rows of 2.8k to 11k
+// tokens, M 32, 8-bit cache: 131 us, 43 % [183], where the conversions' and the softmax's shared-
+// memory accesses wait on one another; 147 rows of 500 to 2090 tokens, M 32, D 64, bf16: 115 us
+// [130]; 34 rows of 120 to 470, M 32, bf16: 12.8 us [17.4]; 24 rows of 28 to 113, M 64, bf16: 19 us
+// [22.6]. Short (row, head)s over an 8-bit cache, several to a CTA, lose: each costs some 3 us
+// beside its chunks (first maxima, the output): 55 rows of 100 to 384, M 32, D 64: 33 us [25.6].
+// Lengths are on the device, so that no rule on the call can tell these from the others.
+// Tried: 16 softmax warps for 32 queries (level), integer conversions of e4m3 (148 us against
+// 136), conversions by four warps for K and V in turn (140 against 137).
 #include <cstring>
 
 #include "attn_decode.cuh"
@@ -125,17 +129,19 @@ __device__ __forceinline__ float2 unpair16(uint32_t v) {
     return make_float2(bf16_lo(v), bf16_hi(v));
 }
 
-// One (row, head) of a range: tiles t .. end of it, x.at the first one's number in it.
+// One (row, head) of a range: chunks t .. end of the list, x.at the first one's number in it; all of
+// its chunks.
 struct Seg {
     Tile x;
-    uint32_t t, end, tiles;
+    uint32_t t, end, chunks;
 };
-__device__ __forceinline__ Seg first_seg(const DecArgs& a, const uint32_t* cum, uint32_t c0, uint32_t c1, bool single) {
+__device__ __forceinline__ Seg first_seg(const DecArgs& a, const uint32_t* cum, uint32_t c0, uint32_t c1,
+                                         bool single) {
     Seg s;
     s.x = find_tile(a, cum, c0, single);
     s.t = c0;
-    s.tiles = cum[s.x.b + 1] - cum[s.x.b];
-    s.end = min(c1, c0 - s.x.at + s.tiles);
+    s.chunks = cum[s.x.b + 1] - cum[s.x.b];
+    s.end = min(c1, c0 - s.x.at + s.chunks);
     return s;
 }
 // The one after s, where s ends before the range does.
@@ -147,9 +153,9 @@ __device__ __forceinline__ void next_seg(const DecArgs& a, const uint32_t* cum, 
         s.x.h = 0;
         do ++s.x.b;
         while (cum[s.x.b + 1] == cum[s.x.b]);
-        s.tiles = cum[s.x.b + 1] - cum[s.x.b];
+        s.chunks = cum[s.x.b + 1] - cum[s.x.b];
     }
-    s.end = min(c1, s.t + s.tiles);
+    s.end = min(c1, s.t + s.chunks);
 }
 // A ring's slot and the parity of its present use.
 struct Ring {
@@ -228,12 +234,12 @@ __global__ void __launch_bounds__((Wide<D, E4M3, N>::THREADS), 1)
         q_tok[tid] = j;
         q_row[tid] = j * a.hq + tid - j * a.G;
     }
-    const uint32_t longest = list_tiles<C::THREADS, kWideRows>(a, rows, scan);
+    const uint32_t longest = list_tiles<C::THREADS, kWideRows, kChunkTiles>(a, rows, scan);
     write_empty_rows<D, C::THREADS>(a, rows);
     Cuts rg;
     uint32_t c0, c1;  // this CTA's range
     bool single;
-    if (!cut_tiles(a, cum, longest, 2 * kChunkTiles, rg, c0, c1, single)) return;
+    if (!cut_tiles(a, cum, longest, 2, kWholeTiles / kChunkTiles, rg, c0, c1, single)) return;
 
     if (warp == C::W0 + 1) umma::tmem_alloc(&tmem_at, C::COLS);
     umma::fence_before_sync();
@@ -256,7 +262,8 @@ __global__ void __launch_bounds__((Wide<D, E4M3, N>::THREADS), 1)
         for (Seg g = first_seg(a, cum, c0, c1, single); g.t < c1 && !dead; next_seg(a, cum, c1, g), ++seg_no) {
             const uint32_t t = g.t;
             const int len = rows.len[g.x.b];
-            const int pos_t = (row_span(a, len).first + g.x.at) * kTok;
+            const RowSpan span = row_span(a, len);
+            const int pos_t = (span.first + g.x.at * kChunkTiles) * kTok, left = span.tiles - g.x.at * kChunkTiles;
             const int app = a.appended ? 1 : 0;
             const int n_min = len + app, n_max = len + (app ? a.T : 0);
             const int b_min = a.window && n_min > a.window ? n_min - a.window : 0;
@@ -265,9 +272,23 @@ __global__ void __launch_bounds__((Wide<D, E4M3, N>::THREADS), 1)
 #pragma unroll
             for (int q = 0; q < NH; ++q) l[q] = 0.f;
 
-            for (uint32_t u = t; u < g.end; u += kChunkTiles, ++i) {
+            for (uint32_t u = t; u < g.end; ++u, ++i) {
                 const bool first = u == t;
-                const int n = (int)min(g.end - u, (uint32_t)kChunkTiles);
+                const int n = min(left - (int)(u - t) * kChunkTiles, kChunkTiles);
+                dead |= !await(&vfull[vb.slot], vb.parity, stop, a.dev_err);
+                const int pos0 = pos_t + (int)(u - t) * kChunk, pos = pos0 + tok;
+                const uint32_t oks = info_ok[i % kInfo];
+                const bool edge = oks != (1u << kChunkTiles) - 1 || pos0 + kChunk > n_min || pos0 < b_max;
+                float ks = 1.f, lv = 0.f, iv = 1.f;
+                if (E4M3) {
+                    // the value scale joins the weight's exponent; l divides it out again
+                    const float* ts = scales + scb * 2 * kChunk + tok;
+                    ks = ts[0];
+                    float v = ts[kChunk];
+                    if (v < 1.1754944e-38f) v = 1.1754944e-38f;  // (a NaN stays)
+                    lv = log2_fast(v);
+                    iv = exp2_fast(-lv);
+                }
                 dead |= !await(&sfull[sb.slot], sb.parity, stop, a.dev_err);
                 umma::fence_after_sync();
                 float p[NH];
@@ -281,20 +302,7 @@ __global__ void __launch_bounds__((Wide<D, E4M3, N>::THREADS), 1)
                 umma::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_plain(&sfree[sb.slot]);
-                dead |= !await(&vfull[vb.slot], vb.parity, stop, a.dev_err);
-
-                const int pos0 = pos_t + (int)(u - t) * kTok, pos = pos0 + tok;
-                const uint32_t oks = info_ok[i % kInfo];
-                const bool edge = oks != (1u << kChunkTiles) - 1 || pos0 + kChunk > n_min || pos0 < b_max;
-                float iv = 1.f;
                 if (E4M3) {
-                    // the value scale joins the weight's exponent; l divides it out again
-                    const float* ts = scales + scb * 2 * kChunk + tok;
-                    const float ks = ts[0];
-                    float v = ts[kChunk];
-                    if (v < 1.1754944e-38f) v = 1.1754944e-38f;  // (a NaN stays)
-                    const float lv = log2_fast(v);
-                    iv = exp2_fast(-lv);
                     const float* f = rs[seg_no & 3] + q0;
 #pragma unroll
                     for (int q = 0; q < NH; q += 4) {
@@ -313,7 +321,8 @@ __global__ void __launch_bounds__((Wide<D, E4M3, N>::THREADS), 1)
                     const bool ok = oks >> (tok / kTok) & 1;
                     const int past = pos - n_min;
                     const int jlo = app ? max(0, past + 1) : past < 0 ? 0 : a.T;
-                    const int jhi = !a.window ? a.T - 1 : app ? min(a.T - 1, past + a.window) : past + a.window >= 0 ? a.T - 1 : -1;
+                    const int in = past + a.window;
+                    const int jhi = !a.window ? a.T - 1 : app ? min(a.T - 1, in) : in >= 0 ? a.T - 1 : -1;
                     const int from = ok ? jlo * a.G - q0 : NH, to = (jhi + 1) * a.G - q0;
 #pragma unroll
                     for (int q = 0; q < NH; ++q)
@@ -353,16 +362,15 @@ __global__ void __launch_bounds__((Wide<D, E4M3, N>::THREADS), 1)
                 if (!first)
 #pragma unroll
                     for (int q = 0; q < NH; q += 4) {
-                        const float4 m = *reinterpret_cast<const float4*>(ms + q0 + q);
                         const float4 b = *reinterpret_cast<const float4*>(mb + q0 + q);
                         e[q] = p[q] - b.x;
                         e[q + 1] = p[q + 1] - b.y;
                         e[q + 2] = p[q + 2] - b.z;
                         e[q + 3] = p[q + 3] - b.w;
-                        grow |= p[q] > m.x + kSlack;
-                        grow |= p[q + 1] > m.y + kSlack;
-                        grow |= p[q + 2] > m.z + kSlack;
-                        grow |= p[q + 3] > m.w + kSlack;
+                        grow |= e[q] > kSlack;
+                        grow |= e[q + 1] > kSlack;
+                        grow |= e[q + 2] > kSlack;
+                        grow |= e[q + 3] > kSlack;
                     }
                 if (first || any_soft<C::SOFT>(grow || dead)) {
                     // the maxima move: theirs over the chunk, then l and O follow
@@ -377,7 +385,8 @@ __global__ void __launch_bounds__((Wide<D, E4M3, N>::THREADS), 1)
                         const float old = first ? -INFINITY : ms[tid];
                         const float m = fmaxf(fmaxf(fmaxf(red[0][tid], red[1][tid]), fmaxf(red[2][tid], red[3][tid])), old);
                         ms[tid] = m;
-                        mb[tid] = m == -INFINITY ? 0.f : m;  // (seen only -infinity: weights of zero)
+                        // (seen only -infinity: weights of zero, and any score passes it)
+                        mb[tid] = m == -INFINITY ? -1e30f : m;
                         fs[tid] = m == old ? 1.f : exp2_fast(old - m);
                     }
                     any_soft<C::SOFT>(false);
@@ -469,7 +478,7 @@ __global__ void __launch_bounds__((Wide<D, E4M3, N>::THREADS), 1)
             if (lane % (32 / NH) == 0) sums[warp & 3][q0 + lane / (32 / NH)] = l[0];
             dead = any_soft<C::SOFT>(dead);
             if (dead) break;
-            const uint32_t nt = g.tiles, s0 = t - g.x.at;
+            const uint32_t nt = g.chunks, s0 = t - g.x.at;
             const bool whole = s0 >= c0 && s0 + nt <= c1;
             const int cta0 = s0 < c0 ? cta_of(rg, s0) : (int)blockIdx.x;
             const long slot = 2L * blockIdx.x + (cta0 < (int)blockIdx.x ? 0 : 1);
@@ -560,20 +569,22 @@ __global__ void __launch_bounds__((Wide<D, E4M3, N>::THREADS), 1)
         bool ok = true;
         for (Seg g = first_seg(a, cum, c0, c1, single); g.t < c1 && ok; next_seg(a, cum, c1, g)) {
             const uint32_t t = g.t;
-            const int pos_t = (row_span(a, rows.len[g.x.b]).first + g.x.at) * kTok;
+            const RowSpan span = row_span(a, rows.len[g.x.b]);
+            const int pos_t = (span.first + g.x.at * kChunkTiles) * kTok, left = span.tiles - g.x.at * kChunkTiles;
             const int32_t* pages = a.page_table + (long)rows.slot[g.x.b] * a.max_pages;
             int look = -1;  // rows of the next 32 tiles, one a lane
-            for (uint32_t u = t; u < g.end; u += kChunkTiles, ++i) {
-                if (((u - t) & 31) == 0) {
+            for (uint32_t u = t; u < g.end; ++u, ++i) {
+                const int tile = (int)(u - t) * kChunkTiles;
+                if ((tile & 31) == 0) {
                     look = -1;
-                    if (u + lane < g.end) {
-                        const int pos = pos_t + (int)(u - t + lane) * kTok;
+                    if (tile + lane < left) {  // (tiles past this range are looked up in vain)
+                        const int pos = pos_t + (tile + lane) * kTok;
                         const int page = __ldg(pages + (pos >> a.ps_log2));
                         if (page < 0 || page >= a.num_pages) set_dev_err(a.dev_err, RSSM_DEVERR_PAGE);
                         else look = ((page * a.hkv + g.x.h) << a.ps_log2) + (pos & ((1 << a.ps_log2) - 1));
                     }
                 }
-                const int y = __shfl_sync(0xffffffffu, look, (int)((u - t) & 31) + (lane & (kChunkTiles - 1)));
+                const int y = __shfl_sync(0xffffffffu, look, (tile & 31) + (lane & (kChunkTiles - 1)));
                 const bool have = lane < kChunkTiles && y >= 0;
                 const uint32_t oks = __ballot_sync(0xffffffffu, have);
                 const uint32_t count = __popc(oks);
@@ -655,14 +666,15 @@ __global__ void __launch_bounds__((Wide<D, E4M3, N>::THREADS), 1)
         for (Seg g = first_seg(a, cum, c0, c1, single); g.t < c1 && ok; next_seg(a, cum, c1, g)) {
             const uint32_t t = g.t;
             ok = await(&qfull[qb.slot], qb.parity, stop, a.dev_err);
-            for (uint32_t u = t; u < g.end && ok; u += kChunkTiles) {
+            const int left = row_span(a, rows.len[g.x.b]).tiles - g.x.at * kChunkTiles;
+            for (uint32_t u = t; u < g.end && ok; ++u) {
                 ok = await(&kfull[kb.slot], kb.parity, stop, a.dev_err) &&
                      await(&sfree[sb.slot], sb.parity ^ 1, stop, a.dev_err);
                 if (!ok) break;
                 umma::fence_after_sync();
                 const uint64_t kd = umma::smem_desc_swizzle128(sk_at + kb.slot * C::OPER, 16, 1024);
                 const uint64_t qd = umma::smem_desc_kmajor(sq + qb.slot * C::QBYTES, 128, D / 8 * 128);
-                const bool last = u + kChunkTiles >= g.end;
+                const bool last = u + 1 == g.end;
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk)
@@ -677,7 +689,7 @@ __global__ void __launch_bounds__((Wide<D, E4M3, N>::THREADS), 1)
                 kb.next(C::SK);
                 sb.next(2);
                 if (before) ok = add_values();
-                before = (int)min(g.end - u, (uint32_t)kChunkTiles);
+                before = min(left - (int)(u - t) * kChunkTiles, kChunkTiles);
                 before_first = u == t;
             }
             qb.next(C::QB);
@@ -739,7 +751,13 @@ __global__ void __launch_bounds__((Wide<D, E4M3, N>::THREADS), 1)
         // ---------------------------------------------- f16 operands of 8-bit tiles
         const bool w = warp >= C::W0 + 8;  // four warps for K, four for V
         const int ct = (tid - C::SOFT) & 127;
-        constexpr int CPT = D / 16;  // 16-byte pieces of a token
+        // 16-byte pieces of the loaded rows: a thread's are tokens tk, tk + 32, ..., of D = 128 the
+        // halves of each in turn. Eight lanes take pieces that neither meet at a bank when read
+        // nor, as two chunks of a swizzled row, when written.
+        const int hi = ct >> 2 & 1, tk = D == 128 ? (ct >> 3) * 2 + hi : ct >> 2;
+        const int from = tk * D + (ct & 3) * 16 + (D == 128 ? hi * 64 : 0);
+        const int into = tk * 128 + (((ct & 3) * 2 ^ (tk & 7)) << 4) + (D == 128 ? hi * kBlk : 0);
+        const int flip = D == 128 ? (hi ? -kBlk : kBlk) : 0;  // to the other half's block
         const int sn = w ? C::SV : C::SK;
         uint64_t* const full = w ? vfull : kfull;
         uint64_t* const free = w ? vfree : kfree;
@@ -748,35 +766,38 @@ __global__ void __launch_bounds__((Wide<D, E4M3, N>::THREADS), 1)
         uint32_t i = 0;
         bool ok = true;
         for (Seg g = first_seg(a, cum, c0, c1, single); g.t < c1 && ok; next_seg(a, cum, c1, g)) {
-            for (uint32_t u = g.t; u < g.end; u += kChunkTiles, ++i) {
+            for (uint32_t u = g.t; u < g.end; ++u, ++i) {
                 ok = await(&rfull[rb.slot], rb.parity, stop, a.dev_err) &&
                      await(&free[ob.slot], ob.parity ^ 1, stop, a.dev_err);
                 if (!ok) break;
                 const uint32_t oks = info_ok[i % kInfo];
                 const unsigned char* src = raw + rb.slot * C::RAW + (w ? kChunk * D : 0);
                 unsigned char* dst = oper + ob.slot * C::OPER;
-#pragma unroll 1
-                for (int e0 = ct; e0 < kChunk * CPT; e0 += 4 * 128) {
+#pragma unroll
+                for (int x0 = 0; x0 < D / 16; x0 += 4) {
                     uint4 v[4];
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
-                        v[x] = *reinterpret_cast<const uint4*>(src + (e0 + x * 128) * 16);
-                        // (no page: zeros, whatever the stage holds)
-                        if (!(oks >> ((e0 + x * 128) / CPT / kTok) & 1)) v[x] = make_uint4(0, 0, 0, 0);
+                        const int k = D == 128 ? (x0 + x) / 2 : x;  // token tk + 32 k
+                        v[x] = *reinterpret_cast<const uint4*>(src + k * 32 * D + (D == 128 && x % 2 ? from ^ 64 : from));
                     }
+                    if (__builtin_expect(oks != (1u << kChunkTiles) - 1, 0))  // no page: zeros, whatever the stage holds
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const int k = D == 128 ? (x0 + x) / 2 : x;
+                            if (!(oks >> ((tk + 32 * k) / kTok) & 1)) v[x] = make_uint4(0, 0, 0, 0);
+                        }
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
-                        const int e = e0 + x * 128, tk = e / CPT, c = e % CPT;  // columns 16 c .. of token tk
-                        uint4 lo, hi;
-                        e4m3x4_to_f16(v[x].x, lo.x, lo.y);
-                        e4m3x4_to_f16(v[x].y, lo.z, lo.w);
-                        e4m3x4_to_f16(v[x].z, hi.x, hi.y);
-                        e4m3x4_to_f16(v[x].w, hi.z, hi.w);
-                        // (D = 128: odd chunks first in the second half: no two of a token meet at a bank)
-                        unsigned char* row = dst + (c >> 2) * kBlk + tk * 128;
-                        const int j = 2 * (c & 3), s = tk & 7, b = D == 128 ? c >> 2 & 1 : 0;
-                        *reinterpret_cast<uint4*>(row + (((j + b) ^ s) << 4)) = b ? hi : lo;
-                        *reinterpret_cast<uint4*>(row + (((j + 1 - b) ^ s) << 4)) = b ? lo : hi;
+                        const int k = D == 128 ? (x0 + x) / 2 : x;
+                        uint4 y, z;
+                        e4m3x4_to_f16(v[x].x, y.x, y.y);
+                        e4m3x4_to_f16(v[x].y, y.z, y.w);
+                        e4m3x4_to_f16(v[x].z, z.x, z.y);
+                        e4m3x4_to_f16(v[x].w, z.z, z.w);
+                        unsigned char* const at = dst + k * 32 * 128 + (x % 2 ? flip : 0);
+                        *reinterpret_cast<uint4*>(at + into) = y;
+                        *reinterpret_cast<uint4*>(at + (into ^ 16)) = z;
                     }
                 }
                 fence_async_smem();
