@@ -167,11 +167,21 @@ static __device__ __noinline__ Tile find_tile(const DecArgs& a, const uint32_t* 
     return x;
 }
 
-// The first tile from t on that begins a (row, head).
+// The first tile from t (the same on all lanes) on that begins a (row, head). The lanes look for
+// the row together, 32 places at a time.
 static __device__ __noinline__ uint32_t next_head(const DecArgs& a, const uint32_t* cum, uint32_t t) {
     if (t >= cum[a.batch] * (uint32_t)a.hkv) return t;
-    const Tile x = find_tile(a, cum, t, false);
-    return x.at == 0 ? t : t - x.at + cum[x.b + 1] - cum[x.b];
+    const uint32_t i = t / (uint32_t)a.hkv;
+    const int lane = threadIdx.x & 31;
+    int b = 0, n = a.batch;  // the row is one of the n from b on
+    while (n > 1) {
+        const int step = (n + 31) / 32, at = lane * step;
+        const int k = __popc(__ballot_sync(0xffffffffu, at < n && cum[b + min(at, n - 1)] <= i)) - 1;
+        b += k * step;
+        n = min(step, n - k * step);
+    }
+    const uint32_t nt = cum[b + 1] - cum[b], rest = (t - cum[b] * (uint32_t)a.hkv) % nt;
+    return rest == 0 ? t : t - rest + nt;
 }
 
 // Row of tile t's first token in the cache matrix; -1, with the flag set, when its page is
@@ -226,7 +236,8 @@ struct Run {
 };
 
 // Tiles of the call's rows into `rows`, bad slots and lengths flagged; returns the tiles of the
-// longest row. All THREADS threads of the CTA, ROWS rows at most; a list in units of UNIT tiles; scan: a value of shared memory per warp.
+// longest row, all in units of UNIT tiles. All THREADS threads of the CTA, ROWS rows at most;
+// scan: a value of shared memory per warp.
 template <int THREADS, int ROWS, int UNIT>
 __device__ __forceinline__ uint32_t list_tiles(const DecArgs& a, const Rows& rows, uint2* scan) {
     constexpr int WARPS = THREADS / 32;

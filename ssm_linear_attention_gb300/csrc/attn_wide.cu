@@ -24,10 +24,10 @@
 //
 // Measured (one GB300, GPU time of a call; in brackets the warp-level kernel that took these
 // calls before): 128 rows of 500 to 2000 tokens, 4 drafts, 4 key heads of 8 queries, D 128, bf16
-// cache: 65.7 us, 4.9 TB/s, 72 % of the measured copy bandwidth [88]; 26 rows of 2.8k to 11k
+// cache: 65.5 us, 4.9 TB/s, 73 % of the measured copy bandwidth [88]; 26 rows of 2.8k to 11k
 // tokens, M 32, 8-bit cache: 131 us, 43 % [183], where the conversions' and the softmax's shared-
 // memory accesses wait on one another; 147 rows of 500 to 2090 tokens, M 32, D 64, bf16: 115 us
-// [130]; 34 rows of 120 to 470, M 32, bf16: 12.8 us [17.4]; 24 rows of 28 to 113, M 64, bf16: 19 us
+// [130]; 34 rows of 120 to 470, M 32, bf16: 12.5 us [17.4]; 24 rows of 28 to 113, M 64, bf16: 18 us
 // [22.6]. Short (row, head)s over an 8-bit cache, several to a CTA, lose: each costs some 3 us
 // beside its chunks (first maxima, the output): 55 rows of 100 to 384, M 32, D 64: 33 us [25.6].
 // Lengths are on the device, so that no rule on the call can tell these from the others.
