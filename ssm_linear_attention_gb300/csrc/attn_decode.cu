@@ -1,5 +1,6 @@
 // attn_decode.cu -- attention of a few new tokens per row over the paged cache: up to 8 queries a
-// key head, and any number with float32 activations (attn_wide.cu has the others).
+// key head, up to 16 over an 8-bit cache, any number with float32 activations (attn_wide.cu has
+// the others).
 //
 // For a row's T query tokens and the G = HQ / HKV query heads of one key / value head, the
 // M = T G queries read the same cached tokens, so every cached vector is read once for all
@@ -925,8 +926,13 @@ static int launch_kernel(const rssm_attn_dims* d, DecArgs a, const DeviceInfo& d
 template <int D, bool E4M3, bool AF32>
 static int launch(const rssm_attn_dims* d, const DecArgs& a, const DeviceInfo& di, cudaStream_t st) {
     if (a.MT == 1) return launch_kernel<D, E4M3, AF32, false>(d, a, di, st);
-    if constexpr (AF32) return launch_kernel<D, E4M3, AF32, true>(d, a, di, st);
-    return decode_wide(d, a, di, st);
+    // The tensor-memory kernel takes more queries, but for float32 activations, whose operands would
+    // be three parts each, and an 8-bit cache under up to 16 queries, whose conversions cost it more
+    // than it saves (64 rows of 1000 to 4000 tokens, 4 key heads of 16 queries, D 64: 55 us against 40
+    // here; D 128 56 and 55; of 32 queries 59 against 62, 68 against 89).
+    if constexpr (AF32 || E4M3)
+        if (AF32 || a.M <= 16) return launch_kernel<D, E4M3, AF32, true>(d, a, di, st);
+    if constexpr (!AF32) return decode_wide(d, a, di, st);
 }
 
 }  // namespace attn

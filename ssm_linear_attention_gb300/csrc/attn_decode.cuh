@@ -444,7 +444,7 @@ inline int launch_rows(const rssm_attn_dims* d, const DecArgs& a, int most, Laun
     return launch_status();
 }
 
-// attn_wide.cu: calls of 9 queries a key head and more, bf16 activations
+// attn_wide.cu
 int decode_wide(const rssm_attn_dims* d, const DecArgs& a, const DeviceInfo& di, cudaStream_t st);
 
 }  // namespace attn

@@ -1,4 +1,5 @@
-// attn_wide.cu -- paged attention where 9 to 64 queries share a key head (bf16 activations).
+// attn_wide.cu -- paged attention where 9 to 64 queries (8-bit cache: 17 to 64) share a key head,
+// bf16 activations.
 //
 // The mathematics and the tile list are attn_decode.cu's. With so many queries the products and
 // the softmax of a warp-level kernel cost more than the bytes (every warp of 8 queries reads
@@ -28,7 +29,8 @@
 // tokens, M 32, 8-bit cache: 131 us, 43 % [183], where the conversions' and the softmax's shared-
 // memory accesses wait on one another; 147 rows of 500 to 2090 tokens, M 32, D 64, bf16: 115 us
 // [130]; 34 rows of 120 to 470, M 32, bf16: 12.5 us [17.4]; 24 rows of 28 to 113, M 64, bf16: 18 us
-// [22.6]. Short (row, head)s over an 8-bit cache, several to a CTA, lose: each costs some 3 us
+// [22.6]; 64 rows of 1000 to 4000 tokens, M 64, D 128, bf16: 80 us [147], 8-bit: 119 [159].
+// Short (row, head)s over an 8-bit cache, several to a CTA, lose: each costs some 3 us
 // beside its chunks (first maxima, the output): 55 rows of 100 to 384, M 32, D 64: 33 us [25.6].
 // Lengths are on the device, so that no rule on the call can tell these from the others.
 // Tried: 16 softmax warps for 32 queries (level), integer conversions of e4m3 (148 us against
@@ -855,9 +857,9 @@ static int launch_n(const rssm_attn_dims* d, const DecArgs& a, const DeviceInfo&
 
 template <int D, bool E4M3>
 static int launch_wide(const rssm_attn_dims* d, const DecArgs& a, const DeviceInfo& di, cudaStream_t st) {
-    return a.M <= 16   ? launch_n<D, E4M3, 16>(d, a, di, st)
-           : a.M <= 32 ? launch_n<D, E4M3, 32>(d, a, di, st)
-                       : launch_n<D, E4M3, 64>(d, a, di, st);
+    if constexpr (!E4M3)
+        if (a.M <= 16) return launch_n<D, E4M3, 16>(d, a, di, st);
+    return a.M <= 32 ? launch_n<D, E4M3, 32>(d, a, di, st) : launch_n<D, E4M3, 64>(d, a, di, st);
 }
 
 int decode_wide(const rssm_attn_dims* d, const DecArgs& a, const DeviceInfo& di, cudaStream_t st) {
