@@ -232,7 +232,7 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
     }
 
     // ------------------------------------------------------- the call's tile list
-    const uint32_t longest = list_tiles<kDecThreads, kMaxRows, 1>(a, rows, scan);
+    const uint32_t longest = list_tiles<kDecThreads, kMaxRows, 1, 0>(a, rows, scan);
     write_empty_rows<D, kDecThreads>(a, rows);
     Cuts rg;
     uint32_t c0, c1;  // this CTA's range

@@ -236,9 +236,9 @@ struct Run {
 };
 
 // Tiles of the call's rows into `rows`, bad slots and lengths flagged; returns the tiles of the
-// longest row, all in units of UNIT tiles. All THREADS threads of the CTA, ROWS rows at most;
+// longest row, all in units of UNIT tiles, EXTRA more to a row that has any. All THREADS threads of the CTA, ROWS rows at most;
 // scan: a value of shared memory per warp.
-template <int THREADS, int ROWS, int UNIT>
+template <int THREADS, int ROWS, int UNIT, int EXTRA>
 __device__ __forceinline__ uint32_t list_tiles(const DecArgs& a, const Rows& rows, uint2* scan) {
     constexpr int WARPS = THREADS / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -263,6 +263,7 @@ __device__ __forceinline__ uint32_t list_tiles(const DecArgs& a, const Rows& row
                 len[i] = -1;
             }
             n[i] = len[i] < 0 ? 0 : (row_span(a, len[i]).tiles + UNIT - 1) / UNIT;
+            if (EXTRA && n[i]) n[i] += EXTRA;
             if (tid * R + i < a.batch) {
                 rows.len[tid * R + i] = len[i];
                 rows.slot[tid * R + i] = slot[i];

@@ -21,20 +21,19 @@
 // one before. The descriptors are made by the whole warp and only stepped by the elected lane:
 // built inside its branch they cost more than the products (1100 against 480 cycles for eight).
 //
-// The list's unit is a chunk here: a cut never leaves two CTAs a part of one each.
+// The list's unit is a chunk here, and a (row, head) counts for one more (its first maxima, its
+// output): a cut never leaves two CTAs a part of one chunk each.
 //
 // Measured (one GB300, GPU time of a call; in brackets the warp-level kernel that took these
 // calls before): 128 rows of 500 to 2000 tokens, 4 drafts, 4 key heads of 8 queries, D 128, bf16
-// cache: 65.5 us, 4.9 TB/s, 73 % of the measured copy bandwidth [88]; 26 rows of 2.8k to 11k
-// tokens, M 32, 8-bit cache: 131 us, 43 % [183], where the conversions' and the softmax's shared-
-// memory accesses wait on one another; 147 rows of 500 to 2090 tokens, M 32, D 64, bf16: 115 us
-// [130]; 34 rows of 120 to 470, M 32, bf16: 12.5 us [17.4]; 24 rows of 28 to 113, M 64, bf16: 18 us
+// cache: 65 us, 5.0 TB/s, 73 % of the measured copy bandwidth [88]; 26 rows of 2.8k to 11k
+// tokens, M 32, 8-bit cache: 128 us, 44 % [183], where the conversions' and the softmax's shared-
+// memory accesses wait on one another; 147 rows of 500 to 2090 tokens, M 32, D 64, bf16: 104 us
+// [130]; 34 rows of 120 to 470, M 32, bf16: 12.6 us [17.4]; 24 rows of 28 to 113, M 64, bf16: 19 us
 // [22.6]; 64 rows of 1000 to 4000 tokens, M 64, D 128, bf16: 80 us [147], 8-bit: 119 [159].
-// Short (row, head)s over an 8-bit cache, several to a CTA, lose: each costs some 3 us
-// beside its chunks (first maxima, the output): 55 rows of 100 to 384, M 32, D 64: 33 us [25.6].
-// Lengths are on the device, so that no rule on the call can tell these from the others.
-// Tried: 16 softmax warps for 32 queries (level), integer conversions of e4m3 (148 us against
-// 136), conversions by four warps for K and V in turn (140 against 137).
+// Short (row, head)s over an 8-bit cache, several to a CTA, are level: 55 rows of 100 to 384, M 32,
+// D 64: 27 us [25.6]. Tried: 16 softmax warps for 32 queries (level), integer conversions of
+// e4m3 (148 us against 136), conversions by four warps for K and V in turn (140 against 137).
 #include <cstring>
 
 #include "attn_decode.cuh"
@@ -49,6 +48,9 @@ constexpr int kBlk = kChunk * 128;     // bytes of 64 operand columns of a chunk
 constexpr int kWideRows = 512;         // rows of a launch
 constexpr int kWideRowBytes = 7168;    // their facts in shared memory
 constexpr int kInfo = 8;               // chunks whose look-ups are kept
+// What a (row, head) costs beside its chunks, in chunks, where the list is cut: 147 rows, D 64, 116 us with
+// 0, 104 with 1, 100 with 2; 55 rows of 384, 8-bit, 34, 27 and 29; 128 rows of 4 drafts, D 128, level.
+constexpr int kHeadCost = 1;
 
 template <int D, bool E4M3, int N>
 struct Wide {
@@ -131,33 +133,41 @@ __device__ __forceinline__ float2 unpair16(uint32_t v) {
     return make_float2(bf16_lo(v), bf16_hi(v));
 }
 
-// One (row, head) of a range: chunks t .. end of the list, x.at the first one's number in it; all of
-// its chunks.
+// One (row, head) of a range: its chunks are units t .. end of the list, x.at the first one's number;
+// all of its chunks. (Its first kHeadCost units stand for no chunk.)
 struct Seg {
     Tile x;
     uint32_t t, end, chunks;
+    uint32_t after;  // the unit where the next (row, head) begins
 };
-__device__ __forceinline__ Seg first_seg(const DecArgs& a, const uint32_t* cum, uint32_t c0, uint32_t c1,
-                                         bool single) {
-    Seg s;
-    s.x = find_tile(a, cum, c0, single);
-    s.t = c0;
-    s.chunks = cum[s.x.b + 1] - cum[s.x.b];
-    s.end = min(c1, c0 - s.x.at + s.chunks);
-    return s;
+// The (row, head) that begins at unit s0, cut to the range; false when it has no chunk there.
+__device__ __forceinline__ bool clip_seg(const uint32_t* cum, uint32_t s0, uint32_t c0, uint32_t c1, Seg& s) {
+    const uint32_t units = cum[s.x.b + 1] - cum[s.x.b], first = s0 + kHeadCost;
+    s.after = s0 + units;
+    s.chunks = units - kHeadCost;
+    s.t = max(c0, first);
+    s.end = min(c1, s.after);
+    s.x.at = (int)(s.t - first);
+    return s.t < s.end;
 }
-// The one after s, where s ends before the range does.
+// The one after s; t = c1 when there is none.
 __device__ __forceinline__ void next_seg(const DecArgs& a, const uint32_t* cum, uint32_t c1, Seg& s) {
-    s.t = s.end;
-    if (s.t >= c1) return;
-    s.x.at = 0;
+    const uint32_t s0 = s.after;
+    s.t = c1;
+    if (s0 >= c1) return;
     if (++s.x.h == a.hkv) {
         s.x.h = 0;
         do ++s.x.b;
         while (cum[s.x.b + 1] == cum[s.x.b]);
-        s.chunks = cum[s.x.b + 1] - cum[s.x.b];
     }
-    s.end = min(c1, s.t + s.chunks);
+    if (!clip_seg(cum, s0, s0, c1, s)) s.t = c1;
+}
+__device__ __forceinline__ Seg first_seg(const DecArgs& a, const uint32_t* cum, uint32_t c0, uint32_t c1,
+                                         bool single) {
+    Seg s;
+    s.x = find_tile(a, cum, c0, single);
+    if (!clip_seg(cum, c0 - s.x.at, c0, c1, s)) next_seg(a, cum, c1, s);
+    return s;
 }
 // A ring's slot and the parity of its present use.
 struct Ring {
@@ -236,12 +246,12 @@ __global__ void __launch_bounds__((Wide<D, E4M3, N>::THREADS), 1)
         q_tok[tid] = j;
         q_row[tid] = j * a.hq + tid - j * a.G;
     }
-    const uint32_t longest = list_tiles<C::THREADS, kWideRows, kChunkTiles>(a, rows, scan);
+    const uint32_t longest = list_tiles<C::THREADS, kWideRows, kChunkTiles, kHeadCost>(a, rows, scan);
     write_empty_rows<D, C::THREADS>(a, rows);
     Cuts rg;
     uint32_t c0, c1;  // this CTA's range
     bool single;
-    if (!cut_tiles(a, cum, longest, 2, kWholeTiles / kChunkTiles, rg, c0, c1, single)) return;
+    if (!cut_tiles(a, cum, longest, 2 + kHeadCost, kWholeTiles / kChunkTiles + kHeadCost, rg, c0, c1, single)) return;
 
     if (warp == C::W0 + 1) umma::tmem_alloc(&tmem_at, C::COLS);
     umma::fence_before_sync();
