@@ -735,9 +735,9 @@ typedef struct rssm_attn_cache {
  * bf16 cache: values rounded to nearest even. E4M3 cache: per (token, head) with a =
  * max(max_d |x_d|, 2^-100): scale = a / 448, stored x_d * (448 / a) rounded to nearest
  * even; a vector that holds an infinity or a NaN is stored as zeros with scale NaN and
- * reads back as NaN throughout (the 8-bit NaN codes are not used; scales are >= 0). A token whose position is beyond max_pages * page_size sets
- * RSSM_DEVERR_CURSOR, one whose page is outside [0, num_pages) RSSM_DEVERR_PAGE; such a
- * token is not written. */
+ * reads back as NaN throughout (the 8-bit NaN codes are not used; scales are >= 0). A token
+ * whose position is beyond max_pages * page_size sets RSSM_DEVERR_CURSOR, one whose page is
+ * outside [0, num_pages) RSSM_DEVERR_PAGE; such a token is not written. */
 int rssm_attn_append(const rssm_attn_dims* dims, const rssm_attn_cache* cache, int32_t n_tokens,
                      const int32_t* cu_tokens, const void* k, int64_t k_stride, const void* v,
                      int64_t v_stride, const int32_t* cache_indices, int32_t* dev_err,
@@ -770,7 +770,10 @@ size_t rssm_attn_workspace_size(const rssm_attn_dims* dims);
  * -infinity, gets o = 0 and lse = -infinity.
  *   q: token i = b T + j's [HQ][D] block at element i * q_stride (>= HQ * D, a multiple of 8)
  *   o [batch][T][HQ][D] out_dtype; lse [batch][T][HQ] float32 (nullable)
- * Limits: T * (HQ / HKV) <= 64, max_pages * (page_size / 16) * HKV < 2^31. Scores, softmax sums and outputs accumulate in float32.
+ * A value of v that is not finite makes the outputs that see it not finite (an infinity: infinite
+ * or NaN, since a weight enters the product in parts).
+ * Limits: T * (HQ / HKV) <= 64, max_pages * (page_size / 16) * HKV < 2^31. Scores, softmax sums
+ * and outputs accumulate in float32.
  * A slot_len outside [0, max_pages * page_size - (appended ? T : 0)] skips the row and
  * sets RSSM_DEVERR_CURSOR; a page outside [0, num_pages) hides its tokens and sets
  * RSSM_DEVERR_PAGE. Rows may share a slot (the cache is only read). The work is divided
