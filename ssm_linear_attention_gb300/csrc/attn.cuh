@@ -39,6 +39,28 @@ inline bool ok_stride(const rssm_attn_dims* d, int64_t stride, int heads) {
     return stride >= (int64_t)heads * d->head_dim && stride % 8 == 0;
 }
 
+// A kernel launched with launch_early may start while the one before it in the stream still ends
+// (its launch, first instructions and barriers then cost nothing): every thread waits here for
+// that one's completion before it touches memory, and lets the next one start early in turn.
+// Of a stream of calls: 1 row of 300 tokens 10.9 -> 8.8 us, norm of 509 x 8192 8.2 -> 6.9.
+__device__ __forceinline__ void wait_for_stream() {
+    asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
+}
+template <class... P, class... A>
+inline void launch_early(void (*kernel)(P...), int grid, int block, size_t smem, cudaStream_t st, const A&... args) {
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3(grid);
+    c.blockDim = dim3(block);
+    c.dynamicSmemBytes = smem;
+    c.stream = st;
+    c.attrs = at;
+    c.numAttrs = 1;
+    cudaLaunchKernelEx(&c, kernel, static_cast<P>(args)...);
+}
+
 inline int log2_of(int v) {
     int l = 0;
     while ((1 << l) < v) ++l;

@@ -919,7 +919,7 @@ static int launch_kernel(const rssm_attn_dims* d, DecArgs a, const DeviceInfo& d
     if (!ensure_smem_limit(kern, smem)) return RSSM_ERR_CUDA;
     const int grid = di.sm_count < kMaxCtas ? di.sm_count : kMaxCtas;
     return launch_rows(d, a, kMaxRows, [&](const DecArgs& x) {
-        decode_kernel<D, E4M3, AF32, SHARE><<<grid, C::WARPS * 32, smem, st>>>(x, km, vm);
+        launch_early(decode_kernel<D, E4M3, AF32, SHARE>, grid, C::WARPS * 32, smem, st, x, km, vm);
     });
 }
 

@@ -861,7 +861,7 @@ static int launch_n(const rssm_attn_dims* d, const DecArgs& a, const DeviceInfo&
     if (!ensure_smem_limit((const void*)wide_kernel<D, E4M3, N>, smem)) return RSSM_ERR_CUDA;
     const int grid = di.sm_count < kMaxCtas ? di.sm_count : kMaxCtas;
     return launch_rows(d, a, kWideRows, [&](const DecArgs& x) {
-        wide_kernel<D, E4M3, N><<<grid, C::THREADS, smem, st>>>(x, km, vm);
+        launch_early(wide_kernel<D, E4M3, N>, grid, C::THREADS, smem, st, x, km, vm);
     });
 }
 

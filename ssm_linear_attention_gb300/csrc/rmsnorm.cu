@@ -109,6 +109,7 @@ __global__ void __launch_bounds__(max_threads(V), V == 2 ? 2 : 1) vector_kernel(
     __shared__ uint32_t red_m[2][32];
     constexpr bool AHEAD = V <= 4;               // the next row's loads before this row's sums
     constexpr bool WREG = V == 1 || (V == 2 && ABF);  // weights in registers before they are used
+    attn::wait_for_stream();
     const int np = a.cols >> 3;
     Raw<ABF> x[V], r[V];
     long row = blockIdx.x;
@@ -235,7 +236,7 @@ static int launch(const Args& a, const DeviceInfo& di, cudaStream_t st) {
     // as many CTAs as fit the SMs by threads, and 32 of one warp
     const int per_sm = min(max(1, (V <= 2 ? 1024 : 512) / threads), 32);
     const long grid = min((long)a.rows, (long)di.sm_count * per_sm);
-    vector_kernel<ABF, OUT, V><<<(int)grid, threads, 0, st>>>(a);
+    attn::launch_early(vector_kernel<ABF, OUT, V>, (int)grid, threads, 0, st, a);
     return launch_status();
 }
 
