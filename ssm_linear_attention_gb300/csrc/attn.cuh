@@ -41,11 +41,12 @@ inline bool ok_stride(const rssm_attn_dims* d, int64_t stride, int heads) {
 
 // A kernel launched with launch_early may start while the one before it in the stream still ends
 // (its launch, first instructions and barriers then cost nothing): every thread waits here for
-// that one's completion before it touches memory, and lets the next one start early in turn.
-// Of a stream of calls: 1 row of 300 tokens 10.9 -> 8.8 us, norm of 509 x 8192 8.2 -> 6.9.
-__device__ __forceinline__ void wait_for_stream() {
-    asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
-}
+// that one's completion before it touches memory. Of a stream of calls: 1 row of 300 tokens 10.9
+// -> 8.8 us, norm of 509 x 8192 8.2 -> 6.9, append of 61k tokens 75.0 -> 72.4.
+__device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets the next kernel's CTAs in before this one's are gone: where it helps (attention 9.0 -> 8.7 us on 1
+// row; level or worse for the norm and large moves, whose own CTAs want the room).
+__device__ __forceinline__ void let_next_in() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 template <class... P, class... A>
 inline void launch_early(void (*kernel)(P...), int grid, int block, size_t smem, cudaStream_t st, const A&... args) {
     cudaLaunchAttribute at[1];

@@ -130,9 +130,11 @@ __device__ __forceinline__ void unpack8_e4m3(uint2 v, float* f) {
 
 // Runs over the CTA's blocks of tokens: body(first token, count, where) with where[i] the
 // place of token i.
-template <bool READ, class Body>
+template <bool READ, bool SMALL, class Body>
 __device__ __forceinline__ void for_blocks(const MoveArgs& a, Body body) {
     __shared__ long where[2][kTokMax];
+    if (SMALL) let_next_in();  // (a large call's CTAs want the room)
+    wait_for_stream();
     const int nblk = (a.n_tokens + a.block - 1) / a.block;
     const bool looks = threadIdx.x >= kMovers;
     const int lane = threadIdx.x & 31;
@@ -183,7 +185,7 @@ template <int D, bool E4M3, bool ABF, int AHEAD>
 __global__ void __launch_bounds__(kThreads, kCtas) append_kernel(const MoveArgs a) {
     constexpr int LPV = D / 8;
     const int lane = threadIdx.x % LPV;
-    for_blocks<false>(a, [&](int t0, int nt, const long* where) {
+    for_blocks<false, AHEAD == 1>(a, [&](int t0, int nt, const long* where) {
         for_vectors<LPV>(a.heads, [&](bool w, int h, int t1, int dt) {
             constexpr int SA = ABF ? 2 : 4;
             const char* src = static_cast<const char*>(w ? a.src[1] : a.src[0]);
@@ -258,7 +260,7 @@ template <int D, bool E4M3, bool OBF, int AHEAD>
 __global__ void __launch_bounds__(kThreads, kCtas) read_kernel(const MoveArgs a) {
     constexpr int LPV = D / 8;
     const int lane = threadIdx.x % LPV;
-    for_blocks<true>(a, [&](int t0, int nt, const long* where) {
+    for_blocks<true, AHEAD == 1>(a, [&](int t0, int nt, const long* where) {
         for_vectors<LPV>(a.heads, [&](bool w, int h, int t1, int dt) {
             const char* src = static_cast<const char*>(w ? a.src[1] : a.src[0]) + lane * 8 * (E4M3 ? 1 : 2);
             char* dst = static_cast<char*>(w ? a.dst[1] : a.dst[0]) +
@@ -371,10 +373,10 @@ static void launch_move(const MoveArgs& a, int sm_count, cudaStream_t st) {
     // a block with no more vectors than groups of lanes: one each (4.8 -> 3.6 us for one token of
     // 512 rows)
     const bool one = a.block * 2 * a.heads <= kMovers / (D / 8);
-    if (READ && one) read_kernel<D, E4M3, DBF, 1><<<grid, kThreads, 0, st>>>(a);
-    if (READ && !one) read_kernel<D, E4M3, DBF, kAhead><<<grid, kThreads, 0, st>>>(a);
-    if (!READ && one) append_kernel<D, E4M3, DBF, 1><<<grid, kThreads, 0, st>>>(a);
-    if (!READ && !one) append_kernel<D, E4M3, DBF, kAhead><<<grid, kThreads, 0, st>>>(a);
+    if (READ && one) launch_early(read_kernel<D, E4M3, DBF, 1>, grid, kThreads, 0, st, a);
+    if (READ && !one) launch_early(read_kernel<D, E4M3, DBF, kAhead>, grid, kThreads, 0, st, a);
+    if (!READ && one) launch_early(append_kernel<D, E4M3, DBF, 1>, grid, kThreads, 0, st, a);
+    if (!READ && !one) launch_early(append_kernel<D, E4M3, DBF, kAhead>, grid, kThreads, 0, st, a);
 }
 
 template <bool READ>

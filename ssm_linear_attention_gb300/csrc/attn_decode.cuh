@@ -248,6 +248,7 @@ __device__ __forceinline__ uint32_t list_tiles(const DecArgs& a, const Rows& row
         constexpr int R = (ROWS + THREADS - 1) / THREADS;
         uint32_t n[R], sum = 0;
         int slot[R], len[R];
+        let_next_in();
         wait_for_stream();
 #pragma unroll
         for (int i = 0; i < R; ++i) slot[i] = tid * R + i < a.batch ? a.ci[tid * R + i] : -1;
