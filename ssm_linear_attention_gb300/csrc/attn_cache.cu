@@ -11,8 +11,8 @@
 // several tokens at once.
 //
 // Measured (one GB300, GPU time of a call; "of" the measured copy bandwidth; 8 heads, D 128,
-// bf16 against an 8-bit cache): append of 61k tokens 72.5 us, 5.2 TB/s, 77 % of it; read-back
-// of 156k tokens 160 us, 6.1 TB/s, 89 %; append of one token of 512 rows 3.6 us. Loading the
+// bf16 against an 8-bit cache): append of 61k tokens 72.3 us, 5.2 TB/s, 77 % of it; read-back
+// of 156k tokens 159 us, 6.1 TB/s, 90 %; append of one token of 512 rows 3.4 us. Loading the
 // next vectors while these are rounded costs more in CTAs (registers) than it hides: append
 // 83 us with 3 CTAs an SM, 88 with 4 and spills.
 #include <cuda_fp8.h>

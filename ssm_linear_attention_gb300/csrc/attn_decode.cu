@@ -31,8 +31,8 @@
 //
 // Measured (one GB300, GPU time of a call; "of" the measured copy bandwidth): 256 rows of 2k
 // to 8k tokens, 8 key heads of 4 queries, D 128, 8-bit cache: 443 us, 6.4 TB/s, 95 % of it;
-// 2 rows of 131k and 64k tokens, bf16 cache: 128 us, 6.25 TB/s, 92 %. 16 rows in float32 under a
-// window of 1000 tokens: 12.5 us. One row of 300 tokens: 9.3 us, latency throughout (three
+// 2 rows of 131k and 64k tokens, bf16 cache: 127 us, 6.3 TB/s, 93 %. 16 rows in float32 under a
+// window of 1000 tokens: 11.8 us. One row of 300 tokens: 8.7 us, latency throughout (three
 // dependent look-ups, one round trip of loads, two joins, and instructions fetched for the first
 // time).
 #include <cstring>

@@ -8,8 +8,8 @@
 // throughout.
 //
 // Measured (one GB300, GPU time of a call; "of" the measured copy bandwidth): 32768 x 4096 bf16
-// to e4m3 in groups of 128: 147 us, 6.4 TB/s, 95 % of it. 509 x 8192 bf16: 7.2 us, 4.6 TB/s,
-// of which a launch that does nothing much (one row of 4096: 2.4 us) is a third.
+// to e4m3 in groups of 128: 146.5 us, 6.4 TB/s, 95 % of it. 509 x 8192 bf16: 6.8 us, 4.9 TB/s,
+// of which a launch that does nothing much (one row of 4096: 2.1 us) is a third.
 #include <cuda_fp8.h>
 
 #include "attn.cuh"
