@@ -773,7 +773,8 @@ size_t rssm_attn_workspace_size(const rssm_attn_dims* dims);
  * A value of v that is not finite makes the outputs that see it not finite (an infinity: infinite
  * or NaN, since a weight enters the product in parts).
  * Limits: T * (HQ / HKV) <= 64, max_pages * (page_size / 16) * HKV < 2^31. Scores, softmax sums
- * and outputs accumulate in float32.
+ * and outputs accumulate in float32; a weight enters the sum over v with 16 bits (24 with float32
+ * q), however far behind the largest it is.
  * A slot_len outside [0, max_pages * page_size - (appended ? T : 0)] skips the row and
  * sets RSSM_DEVERR_CURSOR; a page outside [0, num_pages) hides its tokens and sets
  * RSSM_DEVERR_PAGE. Rows may share a slot (the cache is only read). The work is divided

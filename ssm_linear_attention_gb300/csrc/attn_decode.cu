@@ -114,11 +114,11 @@ __device__ __forceinline__ uint32_t tile_off(int t, int c) {
 //   bf16 cache: bf16, the cached values as they are. A weight in one bf16 part would add
 //     an error as large as the output's own rounding (1.41 times it together), so it takes
 //     two; float32 activations take three parts of each, all 24 bits.
-//   8-bit cache: f16, which holds every e4m3 value. The value scales go into the softmax's
-//     exponent (weights at most 1, whatever the scales), and a query row is divided by the
-//     power of two at its largest element. One part carries all 8 bits of a bf16 query but
-//     11 of a weight, whose error shows in a small output of large terms: two parts, and
-//     two of each for float32 activations.
+//   8-bit cache: keys and queries f16, which holds every e4m3 value; a query row is divided by
+//     the power of two at its largest element and takes one part, two of float32. The value
+//     scales go into the softmax's exponent. Values and weights are bf16, in as many parts as
+//     with a bf16 cache: f16 has no room below 2^-25 for the weights of a hundred thousand
+//     tokens that stand far behind one, which may add up to all of an output.
 template <int D, bool E4M3, bool AF32, bool SHARE>
 struct Cfg {
     static constexpr bool WIDE = !E4M3 && D == 128;
@@ -135,7 +135,7 @@ struct Cfg {
     static constexpr int ROWB = D * (E4M3 ? 1 : 2);  // bytes of a cached vector
     static constexpr int KB = kTok * ROWB;           // K (or V) bytes of a tile
     static constexpr int QP = AF32 ? (E4M3 ? 2 : 3) : 1;
-    static constexpr int PP = !E4M3 && AF32 ? 3 : 2;
+    static constexpr int PP = AF32 ? 3 : 2;
     static constexpr int DB = D / 16;                // 16-column blocks of O^T
     static constexpr int TD = D + 4;                 // row pitch of tails: stores hit all banks
     static constexpr int AUX = E4M3 ? 2 * kTok * 4 : 0;  // scales of a tile
@@ -652,8 +652,8 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
                             }
                         }
                         uint32_t lo[C::PP], hi[C::PP];
-                        split2<C::PP, E4M3>(p[u][0], p[u][1], lo);
-                        split2<C::PP, E4M3>(p[u][2], p[u][3], hi);
+                        split2<C::PP, false>(p[u][0], p[u][1], lo);
+                        split2<C::PP, false>(p[u][2], p[u][3], hi);
 #pragma unroll
                         for (int x = 0; x < C::PP; ++x) {
                             pf[u][x][0] = transpose8(lo[x]);
@@ -721,14 +721,15 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
                                 for (int x = 0; x < 4; ++x) {
                                     uint32_t lo, hi;
                                     e4m3x4_to_f16(r[x], lo, hi);
+                                    const float2 t0 = f16x2_to_f(lo), t1 = f16x2_to_f(hi);
                                     uint32_t* d = x < 2 ? f : g;
-                                    d[2 * (x & 1)] = __byte_perm(lo, hi, 0x5410);
-                                    d[2 * (x & 1) + 1] = __byte_perm(lo, hi, 0x7632);
+                                    d[2 * (x & 1)] = pack2(t0.x, t1.x);
+                                    d[2 * (x & 1) + 1] = pack2(t0.y, t1.y);
                                 }
 #pragma unroll
                                 for (int x = 0; x < C::PP; ++x) {
-                                        mma16816<true>(o[c], f, pf[u][x][0], pf[u][x][1]);
-                                        mma16816<true>(o[c + 1], g, pf[u][x][0], pf[u][x][1]);
+                                        mma16816<false>(o[c], f, pf[u][x][0], pf[u][x][1]);
+                                        mma16816<false>(o[c + 1], g, pf[u][x][0], pf[u][x][1]);
                                 }
                             } else {
                                 ldsm4_t((vbase ^ (uint32_t)(2 * c % 8 * 16)) + c / 4 * (kTok * 128), f);

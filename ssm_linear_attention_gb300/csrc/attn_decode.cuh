@@ -83,6 +83,9 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t
         : "=r"(lo), "=r"(hi)
         : "r"(w));
 }
+__device__ __forceinline__ float2 f16x2_to_f(uint32_t v) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
 
 // Tiles of a row: tokens from the first one any query sees to the last, in whole tiles.
 struct RowSpan {

@@ -9,7 +9,7 @@
 //     S [128 tokens][N]     = K Q^T     A = K, its rows as the cache has them
 //     O^T [D][2 N]         += V^T P     A = V transposed by its descriptor, P = [hi | lo]
 // with a token a lane of S: a thread makes its token's weights for N / 2 (N / 4) queries without
-// looking at another lane, and writes them as rows of P. The weights are two bf16 (f16) parts,
+// looking at another lane, and writes them as rows of P. The weights are two bf16 parts,
 // side by side in P, so that V is read once for both; their sums meet when a (row, head) ends.
 // As there, O is rescaled only when a score passes the running maximum by 8 (log2 units).
 //
@@ -119,7 +119,7 @@ __device__ __forceinline__ void combine(float (&v)[NH], int lane) {
         }
     }
 }
-// Two float32 as an operand pair (f16 with an 8-bit cache, else bf16).
+// Two float32 as an operand pair.
 template <bool F16>
 __device__ __forceinline__ uint32_t pair16(float lo, float hi) {
     uint32_t r;
@@ -127,12 +127,6 @@ __device__ __forceinline__ uint32_t pair16(float lo, float hi) {
     else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-template <bool F16>
-__device__ __forceinline__ float2 unpair16(uint32_t v) {
-    if (F16) return __half22float2(*reinterpret_cast<const __half2*>(&v));
-    return make_float2(bf16_lo(v), bf16_hi(v));
-}
-
 // One (row, head) of a range: its chunks are units t .. end of the list, x.at the first one's number;
 // all of its chunks. (Its first kHeadCost units stand for no chunk.)
 struct Seg {
@@ -446,9 +440,8 @@ __global__ void __launch_bounds__((Wide<D, E4M3, N>::THREADS), 1)
                     uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
-                        hi[x] = pair16<E4M3>(p[q + 2 * x], p[q + 2 * x + 1]);
-                        const float2 h = unpair16<E4M3>(hi[x]);
-                        lo[x] = pair16<E4M3>(p[q + 2 * x] - h.x, p[q + 2 * x + 1] - h.y);
+                        hi[x] = pair16<false>(p[q + 2 * x], p[q + 2 * x + 1]);
+                        lo[x] = pair16<false>(p[q + 2 * x] - bf16_lo(hi[x]), p[q + 2 * x + 1] - bf16_hi(hi[x]));
                     }
                     *reinterpret_cast<uint4*>(row + q * 16) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     *reinterpret_cast<uint4*>(row + (N + q) * 16) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -648,7 +641,7 @@ __global__ void __launch_bounds__((Wide<D, E4M3, N>::THREADS), 1)
     } else if (warp == C::W0 + 1) {
         // ------------------------------------------------------------ products
         constexpr uint32_t is = umma::idesc_16bit(128, N, !E4M3, false);
-        constexpr uint32_t io = umma::idesc_16bit(128, 2 * N, !E4M3, true);
+        constexpr uint32_t io = umma::idesc_16bit(128, 2 * N, true, true);
         const uint32_t sk_at = smem_addr(sk), sv_at = smem_addr(sv);
         const uint64_t pd = umma::smem_desc_mnmajor(smem_addr(sp), C::PK, 128);
         Ring kb, sb, qb, vb, pb;
@@ -760,7 +753,7 @@ __global__ void __launch_bounds__((Wide<D, E4M3, N>::THREADS), 1)
             qb.next(C::QB);
         }
     } else if (E4M3) {
-        // ---------------------------------------------- f16 operands of 8-bit tiles
+        // ------------------------------------- operands of 8-bit tiles: K in f16, V in bf16
         const bool w = warp >= C::W0 + 8;  // four warps for K, four for V
         const int ct = (tid - C::SOFT) & 127;
         // 16-byte pieces of the loaded rows: a thread's are tokens tk, tk + 32, ..., of D = 128 the
@@ -807,6 +800,14 @@ __global__ void __launch_bounds__((Wide<D, E4M3, N>::THREADS), 1)
                         e4m3x4_to_f16(v[x].y, y.z, y.w);
                         e4m3x4_to_f16(v[x].z, z.x, z.y);
                         e4m3x4_to_f16(v[x].w, z.z, z.w);
+                        if (w) {  // values: on to bf16, exact as well
+                            uint32_t* const pairs[8] = {&y.x, &y.y, &y.z, &y.w, &z.x, &z.y, &z.z, &z.w};
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const float2 f = f16x2_to_f(*pairs[e]);
+                                *pairs[e] = pair16<false>(f.x, f.y);
+                            }
+                        }
                         unsigned char* const at = dst + k * 32 * 128 + (x % 2 ? flip : 0);
                         *reinterpret_cast<uint4*>(at + into) = y;
                         *reinterpret_cast<uint4*>(at + (into ^ 16)) = z;

@@ -1,0 +1,122 @@
+"""Attention over an 8-bit cache whose weights or value scales differ by much: one token far ahead of the rest, as in a long context.
+
+The outputs are float32, and each is compared with float64 in units of the terms' size
+w = sum_p p |v_p| (of the same output). What the arithmetic leaves, for scores of up to some 40
+(log2 units, made by one element of the query) and at most a few thousand additions a sum:
+  * a score: 8 steps of the matrix unit, each cutting at most 2^-23 of some 64: 2^-14 absolute in
+    the worst case, 2^-17 where the steps are not all at the top; a weight sees it times ln 2;
+  * a weight in two bf16 parts: 2^-17; a value scale as a float32 factor: 2^-24;
+  * the matrix unit's sums over a group's or chunk's tokens: 2^-16.
+The weight and the sum of weights both carry the score's part: 2^-13 of w bounds them all."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from tests import test_gpu_attention as A
+
+pytestmark = pytest.mark.gpu
+
+FP8 = torch.float8_e4m3fn
+BOUND = 2.0 ** -13
+
+# Queries a key head that take each of the kernels: one warp a tile, warps that share a tile,
+# the tensor-memory kernel's two query blocks; float32 activations in the first two forms.
+FORMS = [(4, torch.bfloat16), (16, torch.bfloat16), (32, torch.bfloat16), (64, torch.bfloat16),
+         (4, torch.float32), (32, torch.float32)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    assert torch.cuda.is_available(), "the gpu tests need a CUDA device"
+    import ssm_linear_attention_gb300 as ssm
+    ssm.lib()
+
+
+def row(n, M, act, d, seed, cache=FP8, hkv=2):
+    """One row of n committed tokens with random keys and values; the first element of a key
+    scores for itself (q's first element is 16, its others are small)."""
+    import ssm_linear_attention_gb300 as ssm
+    hkv = hkv if M < 64 else 1
+    dec, ci, table, slots, g = A.make(1, [n], hq=hkv * M, hkv=hkv, d=d, page=64, cache=cache,
+                                      act=act, out=torch.float32, seed=seed)
+    k = 0.05 * torch.randn(n, hkv, d, generator=g, device="cuda")
+    k[:, :, 0] = 0
+    v = torch.randn(n, hkv, d, generator=g, device="cuda")
+    q = 0.05 * torch.randn(1, 1, hkv * M, d, generator=g, device="cuda")
+    q[..., 0] = 16.0
+    return dec, ci, table, slots, g, k, v, q.to(act)
+
+
+def append(dec, ci, k, v):
+    n = k.shape[0]
+    dec.slot_len.zero_()
+    dec.append(k.to(dec.act_dtype), v.to(dec.act_dtype), ci,
+               cu_tokens=torch.tensor([0, n], dtype=torch.int32, device="cuda"))
+    dec.slot_len[ci.long()] = n
+
+
+def nats(x, d):
+    """The key element that puts a token x ahead (its query element is 16)."""
+    return x * d ** 0.5 / 16
+
+
+def places(dec, table, slots, pos):
+    pos = np.asarray(pos)
+    return (torch.from_numpy(table[slots[0]][pos // dec.page_size].astype(np.int64)).cuda(),
+            torch.from_numpy(pos % dec.page_size).cuda())
+
+
+def compare(dec, ci, q, table, slots, n):
+    o, lse = dec.decode(q, ci, appended=False, with_lse=True)
+    torch.cuda.synchronize()
+    assert int(dec.dev_err.sum()) == 0
+    ro, rl, w = A.reference(dec, q, table, slots, [n], False)
+    assert bool(torch.isfinite(o).all()) and bool(torch.isfinite(lse).all())
+    worst = float(((o.double() - ro).abs() - BOUND * w).max())
+    assert worst <= 1e-30, (worst, float((o.double() - ro).abs().max()), float(w.max()))
+    # (scores in the tens: 2^-22 of them, and the logarithm's own few 2^-22)
+    assert float((lse.double() - rl).abs().max()) <= 2e-5 + 2.0 ** -20 * float(rl.abs().max())
+
+
+@pytest.mark.parametrize("M,act", FORMS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,ahead", [(131072, 14.0), (131072, 17.0), (131072, 20.0), (20000, 30.0)])
+def test_one_token_far_ahead_of_many(M, act, d, n, ahead):
+    """Half of the leader's value is zero: these columns are the others' alone, with weights of
+    e^-ahead."""
+    dec, ci, table, slots, g, k, v, q = row(n, M, act, d, int(ahead))
+    lead = n // 3
+    k[lead, :, 0] = nats(ahead, d)
+    v = v.abs() + 0.5
+    v[lead, :, ::2] = 0
+    append(dec, ci, k, v)
+    compare(dec, ci, q, table, slots, n)
+
+
+@pytest.mark.parametrize("M,act", FORMS)
+@pytest.mark.parametrize("d", [64, 128])
+def test_values_over_eighty_binades(M, act, d):
+    n = 900
+    dec, ci, table, slots, g, k, v, q = row(n, M, act, d, 3)
+    k[:, :, 0] = nats(1.0, d) * torch.randn(n, 2 if M < 64 else 1, generator=g, device="cuda")
+    v *= 2.0 ** torch.randint(-40, 41, (n, 1, 1), generator=g, device="cuda")
+    append(dec, ci, k, v)
+    compare(dec, ci, q, table, slots, n)
+
+
+@pytest.mark.parametrize("M,act", FORMS)
+def test_8_bit_nan_codes_of_a_caller_s_cache_show(M, act):
+    """append never writes the NaN codes, but a cache may be the caller's."""
+    n = 200
+    dec, ci, table, slots, g, k, v, q = row(n, M, act, 128, 5)
+    append(dec, ci, k, v)
+    p, o = places(dec, table, slots, [77])
+    dec.v_cache.view(torch.uint8)[p, 0, o, 9] = 0x7f
+    dec.v_cache.view(torch.uint8)[p, 0, o, 64] = 0xff
+    out = dec.decode(q, ci, appended=False)
+    torch.cuda.synchronize()
+    bad = torch.zeros_like(out, dtype=torch.bool)
+    bad[:, :, :dec.HQ // dec.HKV, [9, 64]] = True
+    assert torch.equal(torch.isnan(out), bad)
