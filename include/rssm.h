@@ -771,7 +771,7 @@ size_t rssm_attn_workspace_size(const rssm_attn_dims* dims);
  *   q: token i = b T + j's [HQ][D] block at element i * q_stride (>= HQ * D, a multiple of 8)
  *   o [batch][T][HQ][D] out_dtype; lse [batch][T][HQ] float32 (nullable)
  * A value of v that is not finite makes the outputs that see it not finite (an infinity: infinite
- * or NaN, since a weight enters the product in parts).
+ * or NaN, since a weight enters the product in parts); lse is the scores' alone.
  * Limits: T * (HQ / HKV) <= 64, max_pages * (page_size / 16) * HKV < 2^31. Scores, softmax sums
  * and outputs accumulate in float32; a weight enters the sum over v with 16 bits (24 with float32
  * q), however far behind the largest it is.

@@ -115,9 +115,8 @@ __device__ __forceinline__ uint32_t tile_off(int t, int c) {
 //     an error as large as the output's own rounding (1.41 times it together), so it takes
 //     two; float32 activations take three parts of each, all 24 bits.
 //   8-bit cache: keys and queries f16, which holds every e4m3 value; a query row is divided by
-//     the power of two at its largest element and takes one part, two of float32. The value
-//     scales go into the softmax's exponent. Values and weights are bf16, in as many parts as
-//     with a bf16 cache: f16 has no room below 2^-25 for the weights of a hundred thousand
+//     the power of two at its largest element and takes one part, two of float32. Values and
+//     weights (times the value scales) are bf16, in as many parts as with a bf16 cache: f16 has no room below 2^-25 for the weights of a hundred thousand
 //     tokens that stand far behind one, which may add up to all of an output.
 template <int D, bool E4M3, bool AF32, bool SHARE>
 struct Cfg {
@@ -566,23 +565,19 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
                         }
                     }
                 // ------------------------------------------------ softmax
-                // Scores in log2 units. With an 8-bit cache a token's value scale joins its
-                // weight as log2(scale) in the exponent: m bounds those sums, the weights stay
-                // in f16's range, and l, which wants the scores alone, divides it out again.
-                float p[C::TP][4], iv[C::TP][2];
+                // Scores in log2 units. With an 8-bit cache a token's value scale multiplies its
+                // weight where that meets the value: m and l are the scores' alone.
+                float p[C::TP][4], vs[C::TP][2];
                 bool edge[C::TP], edges = false, grow = false;
 #pragma unroll
                 for (int u = 0; u < C::TP; ++u) {
-                    float ks[2] = {1.f, 1.f}, lv[2] = {0.f, 0.f};
+                    float ks[2] = {1.f, 1.f};
                     if (E4M3) {
                         const float* ts = sc + st[u] * 2 * kTok + n8;
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
                             ks[x] = ts[8 * x];
-                            float v = ts[kTok + 8 * x];
-                            if (v < 1.1754944e-38f) v = 1.1754944e-38f;  // (a NaN stays)
-                            lv[x] = log2_fast(v);
-                            iv[u][x] = exp2_fast(-lv[x]);
+                            vs[u][x] = ts[kTok + 8 * x];
                         }
                     }
                     // a tile that is not there (or has no page) is all hidden
@@ -592,7 +587,7 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
                         for (int x = 0; x < 4; ++x) {
                             float f = SA == 2 ? sa[u][0][x] + sa[u][SA - 1][x] : sa[u][0][x];
                             f *= rs[x & 1];
-                            if (E4M3) f = f * ks[x >> 1] + lv[x >> 1];
+                            if (E4M3) f *= ks[x >> 1];
                             p[u][x] = f;
                         }
                 }
@@ -638,18 +633,18 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
                             const float c = m[x & 1] == -INFINITY ? 0.f : m[x & 1];
                             p[u][x] = exp2_fast(p[u][x] - c);
                         }
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) l[x & 1] += p[u][x];
                         if (E4M3 && __builtin_expect(edges, 0)) {  // a hidden token's scale may be anything
 #pragma unroll
                             for (int x = 0; x < 4; ++x) {
-                                const float w = p[u][x] * iv[u][x >> 1];
-                                l[x & 1] += p[u][x] == 0.f ? 0.f : w;
+                                const int tok = t[u].x + n8 + 8 * (x >> 1);
+                                const bool hidden = tok >= end[x & 1] || tok < beg[x & 1] || t[u].y < 0;
+                                p[u][x] = hidden ? 0.f : p[u][x] * vs[u][x >> 1];
                             }
-                        } else {
+                        } else if (E4M3) {
 #pragma unroll
-                            for (int x = 0; x < 4; ++x) {
-                                if (E4M3) l[x & 1] += p[u][x] * iv[u][x >> 1];
-                                else l[x & 1] += p[u][x];
-                            }
+                            for (int x = 0; x < 4; ++x) p[u][x] *= vs[u][x >> 1];
                         }
                         uint32_t lo[C::PP], hi[C::PP];
                         split2<C::PP, false>(p[u][0], p[u][1], lo);

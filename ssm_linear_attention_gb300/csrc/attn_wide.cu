@@ -285,15 +285,13 @@ __global__ void __launch_bounds__((Wide<D, E4M3, N>::THREADS), 1)
                 const int pos0 = pos_t + (int)(u - t) * kChunk, pos = pos0 + tok;
                 const uint32_t oks = info_ok[i % kInfo];
                 const bool edge = oks != (1u << kChunkTiles) - 1 || pos0 + kChunk > n_min || pos0 < b_max;
-                float ks = 1.f, lv = 0.f, iv = 1.f;
+                float ks = 1.f, vs = 1.f;
                 if (E4M3) {
-                    // the value scale joins the weight's exponent; l divides it out again
+                    // (the value scale multiplies the weight where that meets the value: the maxima
+                    // and l are the scores' alone)
                     const float* ts = scales + scb * 2 * kChunk + tok;
                     ks = ts[0];
-                    float v = ts[kChunk];
-                    if (v < 1.1754944e-38f) v = 1.1754944e-38f;  // (a NaN stays)
-                    lv = log2_fast(v);
-                    iv = exp2_fast(-lv);
+                    vs = ts[kChunk];
                 }
                 dead |= !await(&sfull[sb.slot], sb.parity, stop, a.dev_err);
                 umma::fence_after_sync();
@@ -313,15 +311,16 @@ __global__ void __launch_bounds__((Wide<D, E4M3, N>::THREADS), 1)
 #pragma unroll
                     for (int q = 0; q < NH; q += 4) {
                         const float4 r = *reinterpret_cast<const float4*>(f + q);
-                        p[q] = p[q] * r.x * ks + lv;
-                        p[q + 1] = p[q + 1] * r.y * ks + lv;
-                        p[q + 2] = p[q + 2] * r.z * ks + lv;
-                        p[q + 3] = p[q + 3] * r.w * ks + lv;
+                        p[q] *= r.x * ks;
+                        p[q + 1] *= r.y * ks;
+                        p[q + 2] *= r.z * ks;
+                        p[q + 3] *= r.w * ks;
                     }
                 } else {
 #pragma unroll
                     for (int q = 0; q < NH; ++q) p[q] *= a.qscale;
                 }
+                int from = 0, to = NH;  // the queries that see this position
                 if (__builtin_expect(edge, 0)) {  // hide what a query does not see, whatever it holds
                     // queries r of tokens jlo .. jhi see this position: r in [from, to)
                     const bool ok = oks >> (tok / kTok) & 1;
@@ -329,7 +328,7 @@ __global__ void __launch_bounds__((Wide<D, E4M3, N>::THREADS), 1)
                     const int jlo = app ? max(0, past + 1) : past < 0 ? 0 : a.T;
                     const int in = past + a.window;
                     const int jhi = !a.window ? a.T - 1 : app ? min(a.T - 1, in) : in >= 0 ? a.T - 1 : -1;
-                    const int from = ok ? jlo * a.G - q0 : NH, to = (jhi + 1) * a.G - q0;
+                    from = ok ? jlo * a.G - q0 : NH, to = (jhi + 1) * a.G - q0;
 #pragma unroll
                     for (int q = 0; q < NH; ++q)
                         if (q < from || q >= to) p[q] = -INFINITY;
@@ -426,12 +425,14 @@ __global__ void __launch_bounds__((Wide<D, E4M3, N>::THREADS), 1)
                     for (int k = 0; k < 4 * C::PARTS; ++k) careful |= odd[i & 1][k / C::PARTS][k % C::PARTS] != 0;
 #pragma unroll
                 for (int q = 0; q < NH; ++q) p[q] = exp2_fast(e[q]);
+#pragma unroll
+                for (int q = 0; q < NH; ++q) l[q] += p[q];
                 if (E4M3 && __builtin_expect(edge, 0)) {  // a hidden token's scale may be anything
 #pragma unroll
-                    for (int q = 0; q < NH; ++q) l[q] += p[q] == 0.f ? 0.f : p[q] * iv;
-                } else {
+                    for (int q = 0; q < NH; ++q) p[q] = q < from || q >= to ? 0.f : p[q] * vs;
+                } else if (E4M3) {
 #pragma unroll
-                    for (int q = 0; q < NH; ++q) l[q] += E4M3 ? p[q] * iv : p[q];
+                    for (int q = 0; q < NH; ++q) p[q] *= vs;
                 }
                 if (i > 0) dead |= !await(&pfree, pb.parity ^ 1, stop, a.dev_err);  // P is free
                 unsigned char* const row = sp + (tok >> 3) * C::PK + (tok & 7) * 16 + q0 / 8 * 128;

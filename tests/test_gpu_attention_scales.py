@@ -1,4 +1,5 @@
-"""Attention over an 8-bit cache whose weights or value scales differ by much: one token far ahead of the rest, as in a long context.
+"""Attention over an 8-bit cache whose value scales differ by much, or are zero, and whose weights
+do: one token far ahead of the rest, as in a long context.
 
 The outputs are float32, and each is compared with float64 in units of the terms' size
 w = sum_p p |v_p| (of the same output). What the arithmetic leaves, for scores of up to some 40
@@ -97,6 +98,36 @@ def test_one_token_far_ahead_of_many(M, act, d, n, ahead):
 
 @pytest.mark.parametrize("M,act", FORMS)
 @pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("which", ["first", "all", "some", "last"])
+def test_value_scales_of_zero(M, act, d, which):
+    """A token whose value scale is zero has its weight and adds nothing."""
+    n = 700
+    dec, ci, table, slots, g, k, v, q = row(n, M, act, d, 1)
+    append(dec, ci, k, v)
+    pos = {"first": range(40), "all": range(n), "some": range(3, n, 5), "last": range(n - 300, n)}[which]
+    p, o = places(dec, table, slots, list(pos))
+    dec.v_scale[p, :, o] = 0.0
+    compare(dec, ci, q, table, slots, n)
+
+
+@pytest.mark.parametrize("M,act", FORMS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("ahead", [5.5, 10.0, 15.0])
+@pytest.mark.parametrize("zero", [0.0, 2.0 ** -149, 2.0 ** -100])
+def test_scaled_token_ahead_of_many_of_scale_zero(M, act, d, ahead, zero):
+    """Thousands of tokens whose values vanish, behind one whose values do not: their weights
+    are in the sum all the same."""
+    n = 4096
+    dec, ci, table, slots, g, k, v, q = row(n, M, act, d, 2)
+    k[100, :, 0] = nats(ahead, d)
+    append(dec, ci, k, v)
+    p, o = places(dec, table, slots, [i for i in range(n) if i != 100])
+    dec.v_scale[p, :, o] = zero
+    compare(dec, ci, q, table, slots, n)
+
+
+@pytest.mark.parametrize("M,act", FORMS)
+@pytest.mark.parametrize("d", [64, 128])
 def test_values_over_eighty_binades(M, act, d):
     n = 900
     dec, ci, table, slots, g, k, v, q = row(n, M, act, d, 3)
@@ -104,6 +135,23 @@ def test_values_over_eighty_binades(M, act, d):
     v *= 2.0 ** torch.randint(-40, 41, (n, 1, 1), generator=g, device="cuda")
     append(dec, ci, k, v)
     compare(dec, ci, q, table, slots, n)
+
+
+@pytest.mark.parametrize("M,act", FORMS)
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_value_that_is_not_finite_leaves_the_sum_of_weights(M, act, d):
+    """The outputs that see it are NaN; lse, which is the scores', is not."""
+    n = 300
+    dec, ci, table, slots, g, k, v, q = row(n, M, act, d, 4)
+    v[123, 0, 5] = float("nan")
+    append(dec, ci, k, v)
+    o, lse = dec.decode(q, ci, appended=False, with_lse=True)
+    torch.cuda.synchronize()
+    heads = dec.HQ // dec.HKV
+    assert bool(torch.isnan(o[:, :, :heads]).all())
+    assert bool(torch.isfinite(o[:, :, heads:]).all())
+    rl = A.reference(dec, q, table, slots, [n], False)[1]
+    assert float((lse.double() - rl).abs().max()) <= 2e-5
 
 
 @pytest.mark.parametrize("M,act", FORMS)
@@ -120,3 +168,26 @@ def test_8_bit_nan_codes_of_a_caller_s_cache_show(M, act):
     bad = torch.zeros_like(out, dtype=torch.bool)
     bad[:, :, :dec.HQ // dec.HKV, [9, 64]] = True
     assert torch.equal(torch.isnan(out), bad)
+
+
+@pytest.mark.parametrize("T,hq", [(3, 8), (4, 16), (8, 16)])
+def test_drafts_and_scales_that_only_some_see(T, hq):
+    """Infinite and NaN value scales at the drafts' own positions: the drafts before them do not
+    see them, those from them on do."""
+    lens = [61]
+    dec, ci, table, slots, g = A.make(1, lens, hq=hq, hkv=2, T=T, cache=FP8, page=64,
+                                      out=torch.float32, seed=9)
+    A.fill(dec, ci, table, slots, lens, g)
+    k = torch.randn(1, T, 2, 128, generator=g, device="cuda").bfloat16()
+    dec.append(k, k, ci)
+    p, o = places(dec, table, slots, [lens[0] + T - 1])
+    dec.v_scale[p, 0, o] = float("nan")
+    dec.v_scale[p, 1, o] = float("inf")
+    q = torch.randn(1, T, hq, 128, generator=g, device="cuda").bfloat16()
+    out, lse = dec.decode(q, ci, with_lse=True)
+    torch.cuda.synchronize()
+    assert bool(torch.isfinite(out[:, :-1]).all()) and not bool(torch.isfinite(out[:, -1]).any())
+    assert bool(torch.isfinite(lse).all())
+    ro, rl, w = A.reference(dec, q, table, slots, lens, True)
+    assert float(((out.double() - ro).abs() - BOUND * w)[:, :-1].max()) <= 1e-30
+    assert float((lse.double() - rl).abs().max()) <= 2e-5
