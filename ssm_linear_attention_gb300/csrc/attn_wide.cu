@@ -48,6 +48,10 @@ constexpr int kBlk = kChunk * 128;     // bytes of 64 operand columns of a chunk
 constexpr int kWideRows = 512;         // rows of a launch
 constexpr int kWideRowBytes = 7168;    // their facts in shared memory
 constexpr int kInfo = 8;               // chunks whose look-ups are kept
+// (row, head)s whose queries' factors are kept. Those of (row, head) s are written once the products of s - 2
+// are done; these waited for every softmax warp to take the scores of two chunks before, but a warp
+// reads the factors after that: where each (row, head) is one chunk, those of s - 4 may still be read.
+constexpr int kFactors = 8;
 // What a (row, head) costs beside its chunks, in chunks, where the list is cut: 147 rows, D 64, 116 us with
 // 0, 104 with 1, 100 with 2; 55 rows of 384, 8-bit, 34, 27 and 29; 128 rows of 4 drafts, D 128, level.
 constexpr int kHeadCost = 1;
@@ -206,7 +210,7 @@ __global__ void __launch_bounds__((Wide<D, E4M3, N>::THREADS), 1)
     __shared__ int info_y[kInfo][kChunkTiles];  // the tiles' rows in the cache, -1: no page
     __shared__ uint32_t info_ok[kInfo];         // and which have one
     __shared__ uint32_t odd[2][4][C::PARTS];  // cleared tokens to add below, of a warp's 32
-    __shared__ __align__(16) float rs[4][N];                  // score factors of the queries (8-bit cache)
+    __shared__ __align__(16) float rs[kFactors][N];           // score factors of the queries (8-bit cache)
     __shared__ __align__(16) float ms[N], mb[N], fs[N];  // running maxima, finite; the last rescaling
     __shared__ __align__(16) float red[4][N], sums[4][N];
     __shared__ Run runs[2];
@@ -307,7 +311,7 @@ __global__ void __launch_bounds__((Wide<D, E4M3, N>::THREADS), 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive_plain(&sfree[sb.slot]);
                 if (E4M3) {
-                    const float* f = rs[seg_no & 3] + q0;
+                    const float* f = rs[seg_no % kFactors] + q0;
 #pragma unroll
                     for (int q = 0; q < NH; q += 4) {
                         const float4 r = *reinterpret_cast<const float4*>(f + q);
@@ -741,7 +745,7 @@ __global__ void __launch_bounds__((Wide<D, E4M3, N>::THREADS), 1)
                         const float inv = 1.f / p2;
                         x[k] = make_uint4(pair16<true>(v[0] * inv, v[1] * inv), pair16<true>(v[2] * inv, v[3] * inv),
                                           pair16<true>(v[4] * inv, v[5] * inv), pair16<true>(v[6] * inv, v[7] * inv));
-                        if (ql % LPQ == 0) rs[seg_no & 3][r] = a.qscale * p2;
+                        if (ql % LPQ == 0) rs[seg_no % kFactors][r] = a.qscale * p2;
                     }
                     *reinterpret_cast<uint4*>(sq + qb.slot * C::QBYTES + (r >> 3) * (D / 8 * 128) + ql % LPQ * 128 +
                                               (r & 7) * 16) = x[k];

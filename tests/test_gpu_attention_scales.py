@@ -191,3 +191,27 @@ def test_drafts_and_scales_that_only_some_see(T, hq):
     ro, rl, w = A.reference(dec, q, table, slots, lens, True)
     assert float(((out.double() - ro).abs() - BOUND * w)[:, :-1].max()) <= 1e-30
     assert float((lse.double() - rl).abs().max()) <= 2e-5
+
+
+@pytest.mark.parametrize("T,hq", [(2, 32), (4, 32), (8, 16)])
+def test_many_short_rows_whose_queries_differ_in_size(T, hq):
+    """(row, head)s of one chunk each, dozens to a CTA, with queries of sizes 2^-8 to 2^7: each
+    one's score factors are its own, call after call."""
+    B = 700
+    lens = [1 + (61 * i) % 120 for i in range(B)]
+    dec, ci, table, slots, g = A.make(B, lens, hq=hq, hkv=2, d=64, T=T, cache=FP8, page=128,
+                                      out=torch.float32, seed=13)
+    A.fill(dec, ci, table, slots, lens, g)
+    q = torch.randn(B, T, hq, 64, generator=g, device="cuda")
+    q *= 2.0 ** torch.randint(-8, 8, (B, T, hq, 1), generator=g, device="cuda") / 16
+    q = q.bfloat16()
+    o, lse = dec.decode(q, ci, appended=False, with_lse=True)
+    torch.cuda.synchronize()
+    first, first_lse = o.clone(), lse.clone()
+    rows = [0, 1, 2, 350, 351, 697, 698, 699]
+    ro, rl, w = A.reference(dec, q[rows], table, [slots[b] for b in rows], [lens[b] for b in rows], False)
+    assert float(((o[rows].double() - ro).abs() - BOUND * w).max()) <= 1e-30
+    assert float((lse[rows].double() - rl).abs().max()) <= 2e-5 + 2.0 ** -20 * float(rl.abs().max())
+    for _ in range(50):
+        o, lse = dec.decode(q, ci, appended=False, with_lse=True)
+        assert torch.equal(o, first) and torch.equal(lse, first_lse)
