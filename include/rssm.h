@@ -780,7 +780,8 @@ size_t rssm_attn_workspace_size(const rssm_attn_dims* dims);
  * RSSM_DEVERR_PAGE. Rows may share a slot (the cache is only read). The work is divided
  * on the device from the slots' lengths, so a captured call serves any lengths; the order
  * of every sum is fixed by them and the GPU's SM count, and repeated calls give identical
- * bits. A bounded wait that runs out sets RSSM_DEVERR_TIMEOUT and leaves outputs unwritten. */
+ * bits. A bounded wait that runs out sets RSSM_DEVERR_TIMEOUT: (row, head)s that were being
+ * worked on are left unwritten, the others may be written. */
 int rssm_attn_decode(const rssm_attn_dims* dims, const rssm_attn_cache* cache, int appended,
                      float scale, int32_t window, const void* q, int64_t q_stride,
                      const int32_t* cache_indices, void* workspace, size_t workspace_bytes,
@@ -879,6 +880,19 @@ int rssm_debug_umma_fold(const float* A, const uint16_t* B, int w, int N, float*
  * null or misaligned src/dst), RSSM_ERR_CUDA. */
 int rssm_debug_pipeline_copy(const float* src, float* dst, int n_tiles, int stall_tile,
                              int wait_us, int32_t* dev_err, rssm_stream_t stream);
+
+/* rssm_debug_attn_decode -- test / debug: rssm_attn_decode with a wait limit of wait_us
+ * microseconds (1..2000000) in place of 2 s and, for stall_tile >= 0, one stage barrier
+ * armed for 16 bytes more than its copies deliver: that of tile stall_tile of the launch's
+ * tile list (16 tokens of a row and key head; of the kernel of many queries, unit
+ * stall_tile of its list of chunks). The copies land, the wait runs out, and the CTA winds
+ * down as rssm_attn_decode's would. Kernels whose copies no barrier counts (8-bit caches and
+ * head_dim 64 with few queries) ignore stall_tile. The pages have no counterpart. */
+int rssm_debug_attn_decode(const rssm_attn_dims* dims, const rssm_attn_cache* cache, int appended,
+                           float scale, int32_t window, const void* q, int64_t q_stride,
+                           const int32_t* cache_indices, void* workspace, size_t workspace_bytes,
+                           void* o, float* lse, int stall_tile, int wait_us, int32_t* dev_err,
+                           rssm_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -36,7 +36,7 @@ EXPORTS = (
     "rssm_kda_output", "rssm_kda_step", "rssm_kda_full_state_decode",
     "rssm_attn_append", "rssm_attn_read", "rssm_attn_workspace_size", "rssm_attn_decode",
     "rssm_attn_advance", "rssm_add_rmsnorm",
-    "rssm_debug_pipeline_copy", "rssm_debug_umma_fold",
+    "rssm_debug_pipeline_copy", "rssm_debug_umma_fold", "rssm_debug_attn_decode",
 )
 
 
@@ -170,6 +170,8 @@ def _declare(L):
                                   _VP]),
         "rssm_debug_pipeline_copy": (_I, [_VP, _VP, _I, _I, _I, _VP, _VP]),
         "rssm_debug_umma_fold": (_I, [_VP, _VP, _I, _I, _VP, _VP, _VP]),
+        "rssm_debug_attn_decode": (_I, [ad, ac, _I, f32, _I32, _VP, i64, _VP, _VP, _SZ, _VP, _VP,
+                                        _I, _I, _VP, _VP]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -565,6 +567,16 @@ def rssm_attn_decode(dims, cache, appended, scale, window, q, q_stride, cache_in
     _call("rssm_attn_decode", ctypes.byref(dims), ctypes.byref(cache), int(appended), scale,
           window, _ptr(q), q_stride, _ptr(cache_indices), _ptr(workspace), workspace_bytes,
           _ptr(o), _ptr(lse), _ptr(dev_err), _stream(stream))
+
+
+def rssm_debug_attn_decode(dims, cache, appended, scale, window, q, q_stride, cache_indices,
+                           workspace, workspace_bytes, o, lse, stall_tile, wait_us, dev_err=None,
+                           stream=None):
+    """rssm_attn_decode with a wait limit of wait_us; stall_tile >= 0 makes that tile's wait run
+    out (test of the bounded waits)."""
+    _call("rssm_debug_attn_decode", ctypes.byref(dims), ctypes.byref(cache), int(appended), scale,
+          window, _ptr(q), q_stride, _ptr(cache_indices), _ptr(workspace), workspace_bytes,
+          _ptr(o), _ptr(lse), int(stall_tile), int(wait_us), _ptr(dev_err), _stream(stream))
 
 
 def rssm_attn_advance(dims, cache, cu_tokens, num_accepted, cache_indices, dev_err=None,

@@ -286,7 +286,7 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
                     if (y >= 0) {
                         unsigned char* dst = kv + (size_t)sent_s * C::STAGE;
                         if (elect_one()) {
-                            mbar_arrive_expect_tx(&fb[sent_s], C::STAGE);
+                            mbar_arrive_expect_tx(&fb[sent_s], C::STAGE + ((int)t0 + sent == a.stall ? 16 : 0));
 #pragma unroll
                             for (int x = 0; x < C::ROWB / 128; ++x) {
                                 tma_load_2d(dst + x * kTok * 128, &kmap, 64 * x, y, &fb[sent_s], pol);
@@ -504,7 +504,7 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
             if (C::TMA) {  // (one tile a step)
                 if (!(bad >> s & 1)) {
                     if (!__all_sync(0xffffffffu, mbar_try_wait(&fb[s], parity >> s & 1)))
-                        ok = wait_long(&fb[s], parity >> s & 1, &abort_flag, a.dev_err);
+                        ok = wait_long(&fb[s], parity >> s & 1, &abort_flag, a.wait_ns, a.dev_err);
                     parity ^= 1u << s;
                 }
             } else {
@@ -769,12 +769,13 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
     __syncthreads();
     if (C::TMA && abort_flag) {
         // A wait ran out: no copy may still be in flight when the CTA ends. Every stage's
-        // barrier is watched for a while, whatever its phase.
+        // barrier is watched for a while, whatever its phase. The group that gave up left no
+        // record of its tiles: nothing is joined, what the CTA had not written stays unwritten.
         if (tid < nst) {
             mbar_wait_bounded(&full[tid], 0, RSSM_WAIT_NS / 100);
             mbar_wait_bounded(&full[tid], 1, RSSM_WAIT_NS / 100);
         }
-        __syncthreads();
+        return;
     }
 
     // ------------------------------------------------------- join the CTA's records
@@ -941,11 +942,10 @@ extern "C" size_t rssm_attn_workspace_size(const rssm_attn_dims* d) {
     return attn::workspace_of(d).bytes;
 }
 
-extern "C" int rssm_attn_decode(const rssm_attn_dims* d, const rssm_attn_cache* c, int appended,
-                                float scale, int32_t window, const void* q, int64_t q_stride,
-                                const int32_t* cache_indices, void* workspace,
-                                size_t workspace_bytes, void* o, float* lse, int32_t* dev_err,
-                                rssm_stream_t stream) {
+static int decode_call(const rssm_attn_dims* d, const rssm_attn_cache* c, int appended, float scale,
+                       int32_t window, const void* q, int64_t q_stride, const int32_t* cache_indices,
+                       void* workspace, size_t workspace_bytes, void* o, float* lse, int stall,
+                       uint64_t wait_ns, int32_t* dev_err, rssm_stream_t stream) {
     const int st = attn::check_dims(d);
     if (st != RSSM_OK) return st;
     if (window < 0) return RSSM_ERR_INVALID_ARG;
@@ -989,6 +989,8 @@ extern "C" int rssm_attn_decode(const rssm_attn_dims* d, const rssm_attn_cache* 
     a.M = a.T * G;
     a.MT = a.M <= 8 ? 1 : a.M <= 16 ? 2 : a.M <= 32 ? 4 : 8;
     a.obf = d->out_dtype == RSSM_BF16;
+    a.wait_ns = wait_ns;
+    a.stall = stall;
     const bool q8 = d->cache_dtype == RSSM_E4M3, f32 = d->act_dtype == RSSM_F32;
     const cudaStream_t s = (cudaStream_t)stream;
 #define RSSM_ATTN_D(D_)                                                            \
@@ -998,4 +1000,25 @@ extern "C" int rssm_attn_decode(const rssm_attn_dims* d, const rssm_attn_cache* 
                : attn::launch<D_, false, false>(d, a, di, s)))
     return d->head_dim == 64 ? RSSM_ATTN_D(64) : RSSM_ATTN_D(128);
 #undef RSSM_ATTN_D
+}
+
+extern "C" int rssm_attn_decode(const rssm_attn_dims* d, const rssm_attn_cache* c, int appended,
+                                float scale, int32_t window, const void* q, int64_t q_stride,
+                                const int32_t* cache_indices, void* workspace,
+                                size_t workspace_bytes, void* o, float* lse, int32_t* dev_err,
+                                rssm_stream_t stream) {
+    return decode_call(d, c, appended, scale, window, q, q_stride, cache_indices, workspace,
+                       workspace_bytes, o, lse, -1, RSSM_WAIT_NS, dev_err, stream);
+}
+
+extern "C" int rssm_debug_attn_decode(const rssm_attn_dims* d, const rssm_attn_cache* c,
+                                      int appended, float scale, int32_t window, const void* q,
+                                      int64_t q_stride, const int32_t* cache_indices,
+                                      void* workspace, size_t workspace_bytes, void* o, float* lse,
+                                      int stall_tile, int wait_us, int32_t* dev_err,
+                                      rssm_stream_t stream) {
+    if (wait_us < 1 || wait_us > 2000000) return RSSM_ERR_INVALID_ARG;
+    return decode_call(d, c, appended, scale, window, q, q_stride, cache_indices, workspace,
+                       workspace_bytes, o, lse, stall_tile < 0 ? -1 : stall_tile,
+                       (uint64_t)wait_us * 1000ull, dev_err, stream);
 }

@@ -49,6 +49,8 @@ struct DecArgs {
     int ngroups;       // of a CTA
     int stages;        // per group
     int obf;
+    uint64_t wait_ns;  // limit of a wait on a copy or a product
+    int stall;         // test: the tile (many queries: chunk) of the list whose wait runs out; -1: none
 };
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -133,8 +135,8 @@ __device__ __forceinline__ int cta_of(const Cuts& r, uint32_t t) {
 // The whole warp's bounded wait for phase `parity` of `bar`; false, with the CTA's abort
 // flag set, when it ran out on any lane or another warp had given up.
 static __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                       int32_t* dev_err) {
-    const int w = mbar_wait_abortable(bar, parity, RSSM_WAIT_NS, abort);
+                                              uint64_t wait_ns, int32_t* dev_err) {
+    const int w = mbar_wait_abortable(bar, parity, wait_ns, abort);
     if (__all_sync(0xffffffffu, w > 0)) return true;
     if (w == 0) {
         set_dev_err(dev_err, RSSM_DEVERR_TIMEOUT);

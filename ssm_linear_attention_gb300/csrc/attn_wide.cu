@@ -85,9 +85,9 @@ struct Wide {
 };
 
 // The whole warp's bounded wait.
-__device__ __forceinline__ bool await(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* dev_err) {
+__device__ __forceinline__ bool await(uint64_t* bar, uint32_t parity, volatile int* abort, const DecArgs& a) {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-    return wait_long(bar, parity, abort, dev_err);
+    return wait_long(bar, parity, abort, a.wait_ns, a.dev_err);
 }
 // Barrier of the THREADS softmax threads; true where x is on any of them.
 template <int THREADS>
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__((Wide<D, E4M3, N>::THREADS), 1)
             for (uint32_t u = t; u < g.end; ++u, ++i) {
                 const bool first = u == t;
                 const int n = min(left - (int)(u - t) * kChunkTiles, kChunkTiles);
-                dead |= !await(&vfull[vb.slot], vb.parity, stop, a.dev_err);
+                dead |= !await(&vfull[vb.slot], vb.parity, stop, a);
                 const int pos0 = pos_t + (int)(u - t) * kChunk, pos = pos0 + tok;
                 const uint32_t oks = info_ok[i % kInfo];
                 const bool edge = oks != (1u << kChunkTiles) - 1 || pos0 + kChunk > n_min || pos0 < b_max;
@@ -297,7 +297,7 @@ __global__ void __launch_bounds__((Wide<D, E4M3, N>::THREADS), 1)
                     ks = ts[0];
                     vs = ts[kChunk];
                 }
-                dead |= !await(&sfull[sb.slot], sb.parity, stop, a.dev_err);
+                dead |= !await(&sfull[sb.slot], sb.parity, stop, a);
                 umma::fence_after_sync();
                 float p[NH];
                 umma::ld_cols<NH>(lanes + sb.slot * C::SA * N + q0, p);
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__((Wide<D, E4M3, N>::THREADS), 1)
                     }
                     any_soft<C::SOFT>(false);
                     if (!first) {
-                        dead |= !await(&pfree, pb.parity ^ 1, stop, a.dev_err);  // O has the chunk before
+                        dead |= !await(&pfree, pb.parity ^ 1, stop, a);  // O has the chunk before
                         umma::fence_after_sync();
                         float o[NH];
 #pragma unroll
@@ -438,7 +438,7 @@ __global__ void __launch_bounds__((Wide<D, E4M3, N>::THREADS), 1)
 #pragma unroll
                     for (int q = 0; q < NH; ++q) p[q] *= vs;
                 }
-                if (i > 0) dead |= !await(&pfree, pb.parity ^ 1, stop, a.dev_err);  // P is free
+                if (i > 0) dead |= !await(&pfree, pb.parity ^ 1, stop, a);  // P is free
                 unsigned char* const row = sp + (tok >> 3) * C::PK + (tok & 7) * 16 + q0 / 8 * 128;
 #pragma unroll
                 for (int q = 0; q < NH; q += 8) {
@@ -456,7 +456,7 @@ __global__ void __launch_bounds__((Wide<D, E4M3, N>::THREADS), 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive_plain(&pfull);
                 if (__builtin_expect(careful, 0)) {
-                    dead |= !await(&pfree, pb.parity, stop, a.dev_err);
+                    dead |= !await(&pfree, pb.parity, stop, a);
                     umma::fence_after_sync();
                     float o[NH];
                     umma::ld_cols<NH>(ocol, o);
@@ -510,7 +510,7 @@ __global__ void __launch_bounds__((Wide<D, E4M3, N>::THREADS), 1)
                 f[q + 2] = x.z;
                 f[q + 3] = x.w;
             }
-            dead |= !await(&pfree, pb.parity ^ 1, stop, a.dev_err);  // O has the last chunk
+            dead |= !await(&pfree, pb.parity ^ 1, stop, a);  // O has the last chunk
             umma::fence_after_sync();
             // through P's buffer, which is free: rows of D values
             const bool as16 = whole && a.obf;
@@ -602,9 +602,9 @@ __global__ void __launch_bounds__((Wide<D, E4M3, N>::THREADS), 1)
                 if (lane == 0) info_ok[i % kInfo] = oks;
                 __syncwarp();
                 if (!E4M3) {
-                    ok = await(&kfree[kb.slot], kb.parity ^ 1, stop, a.dev_err);
+                    ok = await(&kfree[kb.slot], kb.parity ^ 1, stop, a);
                     if (!ok) break;
-                    if (lane == 0) mbar_arrive_expect_tx(&kfull[kb.slot], count * kTok * D * 2);
+                    if (lane == 0) mbar_arrive_expect_tx(&kfull[kb.slot], count * kTok * D * 2 + ((int)u == a.stall ? 16 : 0));
                     __syncwarp();
                     if (have)
 #pragma unroll
@@ -612,7 +612,7 @@ __global__ void __launch_bounds__((Wide<D, E4M3, N>::THREADS), 1)
                             tma_load_2d(sk + kb.slot * C::OPER + c * kBlk + lane * kTok * 128, &kmap, 64 * c, y,
                                         &kfull[kb.slot], pol);
                     __syncwarp();
-                    ok = await(&vfree[vb.slot], vb.parity ^ 1, stop, a.dev_err);
+                    ok = await(&vfree[vb.slot], vb.parity ^ 1, stop, a);
                     if (!ok) break;
                     if (lane == 0) mbar_arrive_expect_tx(&vfull[vb.slot], count * kTok * D * 2);
                     __syncwarp();
@@ -625,9 +625,9 @@ __global__ void __launch_bounds__((Wide<D, E4M3, N>::THREADS), 1)
                     kb.next(C::SK);
                     vb.next(C::SV);
                 } else {
-                    ok = await(&rfree[rb.slot], rb.parity ^ 1, stop, a.dev_err);
+                    ok = await(&rfree[rb.slot], rb.parity ^ 1, stop, a);
                     if (!ok) break;
-                    if (lane == 0) mbar_arrive_expect_tx(&rfull[rb.slot], count * kTok * (2 * D + 8));
+                    if (lane == 0) mbar_arrive_expect_tx(&rfull[rb.slot], count * kTok * (2 * D + 8) + ((int)u == a.stall ? 16 : 0));
                     __syncwarp();
                     if (have) {
                         unsigned char* dst = raw + rb.slot * C::RAW + lane * kTok * D;
@@ -654,7 +654,7 @@ __global__ void __launch_bounds__((Wide<D, E4M3, N>::THREADS), 1)
         bool before_first = false, ok = true;
         // O^T (+)= V^T P of the chunk before
         auto add_values = [&]() {
-            if (!await(&vfull[vb.slot], vb.parity, stop, a.dev_err) || !await(&pfull, pb.parity, stop, a.dev_err))
+            if (!await(&vfull[vb.slot], vb.parity, stop, a) || !await(&pfull, pb.parity, stop, a))
                 return false;
             umma::fence_after_sync();
             // (D = 64: the second half of the accumulator's rows is not read)
@@ -675,11 +675,11 @@ __global__ void __launch_bounds__((Wide<D, E4M3, N>::THREADS), 1)
         };
         for (Seg g = first_seg(a, cum, c0, c1, single); g.t < c1 && ok; next_seg(a, cum, c1, g)) {
             const uint32_t t = g.t;
-            ok = await(&qfull[qb.slot], qb.parity, stop, a.dev_err);
+            ok = await(&qfull[qb.slot], qb.parity, stop, a);
             const int left = row_span(a, rows.len[g.x.b]).tiles - g.x.at * kChunkTiles;
             for (uint32_t u = t; u < g.end && ok; ++u) {
-                ok = await(&kfull[kb.slot], kb.parity, stop, a.dev_err) &&
-                     await(&sfree[sb.slot], sb.parity ^ 1, stop, a.dev_err);
+                ok = await(&kfull[kb.slot], kb.parity, stop, a) &&
+                     await(&sfree[sb.slot], sb.parity ^ 1, stop, a);
                 if (!ok) break;
                 umma::fence_after_sync();
                 const uint64_t kd = umma::smem_desc_swizzle128(sk_at + kb.slot * C::OPER, 16, 1024);
@@ -728,7 +728,7 @@ __global__ void __launch_bounds__((Wide<D, E4M3, N>::THREADS), 1)
                                                                (long)(g.x.h * a.G + r - j * a.G) * D + ql % LPQ * 8);
                     }
                 }
-                if (k0 == 0) ok = await(&qfree[qb.slot], qb.parity ^ 1, stop, a.dev_err);
+                if (k0 == 0) ok = await(&qfree[qb.slot], qb.parity ^ 1, stop, a);
                 if (!ok) break;
 #pragma unroll
                 for (int k = 0; k < AT; ++k) {
@@ -777,8 +777,8 @@ __global__ void __launch_bounds__((Wide<D, E4M3, N>::THREADS), 1)
         bool ok = true;
         for (Seg g = first_seg(a, cum, c0, c1, single); g.t < c1 && ok; next_seg(a, cum, c1, g)) {
             for (uint32_t u = g.t; u < g.end; ++u, ++i) {
-                ok = await(&rfull[rb.slot], rb.parity, stop, a.dev_err) &&
-                     await(&free[ob.slot], ob.parity ^ 1, stop, a.dev_err);
+                ok = await(&rfull[rb.slot], rb.parity, stop, a) &&
+                     await(&free[ob.slot], ob.parity ^ 1, stop, a);
                 if (!ok) break;
                 const uint32_t oks = info_ok[i % kInfo];
                 const unsigned char* src = raw + rb.slot * C::RAW + (w ? kChunk * D : 0);

@@ -166,3 +166,11 @@ def test_runner_refusals(lib):
     with pytest.raises(AttributeError):
         norm.weight = torch.zeros(128)
     norm.eps = 1e-6
+
+
+def test_debug_decode_arguments(lib):
+    def call(wait_us, q=FAKE):
+        return ssm.lib().rssm_debug_attn_decode(ctypes.byref(_dims()), ctypes.byref(_cache()), 1, 1.0, 0,
+                                                q, 1024, FAKE, FAKE, 1 << 40, FAKE, None, -1, wait_us,
+                                                None, None)
+    assert call(0) == INV and call(2000001) == INV and call(1000, q=None) == INV
