@@ -194,7 +194,9 @@ static __device__ __noinline__ uint32_t next_head(const DecArgs& a, const uint32
 static __device__ __noinline__ int locate_tile(const DecArgs& a, const Rows& rows, uint32_t t, bool single) {
     const Tile x = find_tile(a, rows.cum, t, single);
     const int pos = (row_span(a, rows.len[x.b]).first + x.at) * kTok;
-    const int page = __ldg(a.page_table + (long)rows.slot[x.b] * a.max_pages + (pos >> a.ps_log2));
+    // (a plain load: a kernel that starts early may not take a table for constant that one before
+    // it still writes)
+    const int page = a.page_table[(long)rows.slot[x.b] * a.max_pages + (pos >> a.ps_log2)];
     if (page < 0 || page >= a.num_pages) {
         set_dev_err(a.dev_err, RSSM_DEVERR_PAGE);
         return -1;

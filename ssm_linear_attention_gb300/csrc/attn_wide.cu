@@ -589,7 +589,7 @@ __global__ void __launch_bounds__((Wide<D, E4M3, N>::THREADS), 1)
                     look = -1;
                     if (tile + lane < left) {  // (tiles past this range are looked up in vain)
                         const int pos = pos_t + (tile + lane) * kTok;
-                        const int page = __ldg(pages + (pos >> a.ps_log2));
+                        const int page = pages[pos >> a.ps_log2];
                         if (page < 0 || page >= a.num_pages) set_dev_err(a.dev_err, RSSM_DEVERR_PAGE);
                         else look = ((page * a.hkv + g.x.h) << a.ps_log2) + (pos & ((1 << a.ps_log2) - 1));
                     }

@@ -60,3 +60,32 @@ def test_a_wait_that_runs_out_leaves_the_output_unwritten(hq, cache, act, lens, 
     o2, lse2 = dec.decode(q, ci, appended=False, with_lse=True)
     torch.cuda.synchronize()
     assert torch.equal(o2, o) and torch.equal(lse2, lse)
+
+
+@pytest.mark.parametrize("hq,cache", [(4, torch.bfloat16), (4, FP8), (16, torch.bfloat16), (32, FP8)])
+def test_a_page_table_written_just_before_the_call(hq, cache):
+    """The kernels start while the one before them ends: a table, a length and a page that this one
+    writes are read as it leaves them."""
+    dec, ci, table, slots, g = A.make(3, [500, 70, 900], hq=hq, hkv=1, page=64, cache=cache, seed=5)
+    A.fill(dec, ci, table, slots, [500, 70, 900], g)
+    q = torch.randn(3, 1, hq, 128, generator=g, device="cuda").bfloat16()
+    tables = [dec.page_table.clone(), dec.page_table.clone()]
+    s = torch.from_numpy(slots).cuda()
+    tables[1][s[0], :7] = tables[0][s[2], :7]                  # (full pages)
+    tables[1][s[2], :7] = tables[0][s[0], :7]
+    lens = [dec.slot_len.clone(), dec.slot_len.clone() - dec.slot_len // 3]
+    want = []
+    for t, n in zip(tables, lens):
+        dec.page_table.copy_(t)
+        dec.slot_len.copy_(n)
+        torch.cuda.synchronize()
+        want.append(dec.decode(q, ci, appended=False).clone())
+        torch.cuda.synchronize()
+    assert not torch.equal(*want)
+    got = []
+    for i in range(100):
+        dec.page_table.copy_(tables[i % 2])
+        dec.slot_len.copy_(lens[i % 2])
+        got.append(dec.decode(q, ci, appended=False).clone())
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[i % 2]) for i, o in enumerate(got))
