@@ -31,17 +31,26 @@ def _check(name, t, shape, dtype, device):
     return t
 
 
-def _check_out(name, t, count, dtype):
-    if t.dtype is not dtype or t.numel() != count or not t.is_contiguous():
-        raise ValueError("%s must be dense, %d %s values" % (name, count, dtype))
+def _index(device):
+    """What get_device() says of a tensor on this device."""
+    return device.index if device.type == "cuda" else -1
+
+
+def _check_out(name, t, count, dtype, index):
+    if t.dtype is not dtype or t.numel() != count or not t.is_contiguous() or \
+            t.get_device() != index:
+        raise ValueError("%s must be dense, %d %s values on the runner's device"
+                         % (name, count, dtype))
     return t.data_ptr()
 
 
-def _check_list(name, t, count):
+def _check_list(name, t, count, index):
     if t is None:
         return None
-    if t.dtype is not torch.int32 or t.shape[0] != count or not t.is_contiguous():
-        raise ValueError("%s must be a dense int32 list of %d" % (name, count))
+    if t.dtype is not torch.int32 or t.shape[0] != count or not t.is_contiguous() or \
+            t.get_device() != index:
+        raise ValueError("%s must be a dense int32 list of %d on the runner's device"
+                         % (name, count))
     return t.data_ptr()
 
 
@@ -111,6 +120,7 @@ class PagedAttentionDecoder(_Fixed):
         self._decode, self._advance = B.entry("rssm_attn_decode"), B.entry("rssm_attn_advance")
         self._cache = ctypes.byref(self.cache)
         self._ws, self._err = self.workspace.data_ptr(), self.dev_err.data_ptr()
+        self._index = _index(self.workspace.device)
         self._plans = {}
 
     def dims(self, batch):
@@ -122,8 +132,9 @@ class PagedAttentionDecoder(_Fixed):
         """What calls of b rows share: a reference to their dims, q's element count, the
         outputs and their addresses. Kept, because a small call's time is the host's."""
         b = cache_indices.shape[0]
-        if cache_indices.dtype is not torch.int32 or not cache_indices.is_contiguous():
-            raise ValueError("cache_indices must be a dense int32 list")
+        if cache_indices.dtype is not torch.int32 or not cache_indices.is_contiguous() or \
+                cache_indices.get_device() != self._index:
+            raise ValueError("cache_indices must be a dense int32 list on the runner's device")
         p = self._plans.get(b)
         if p is None:
             o, lse = self.o[:b], self.lse[:b]
@@ -134,6 +145,8 @@ class PagedAttentionDecoder(_Fixed):
     def _stride(self, name, t, heads):
         """Element distance between consecutive tokens of t [tokens, heads, D] or
         [rows, T, heads, D]."""
+        if t.get_device() != self._index:
+            raise ValueError("%s is not on the runner's device" % name)
         if t.dtype is self.act_dtype and t.is_contiguous() and t.shape[-2] == heads and \
                 t.shape[-1] == self.D:
             return heads * self.D
@@ -152,7 +165,8 @@ class PagedAttentionDecoder(_Fixed):
         if v.shape != k.shape:
             raise ValueError("k and v must have one shape")
         rc = self._append(self._plan(cache_indices)[0], self._cache, n,
-                          _check_list("cu_tokens", cu_tokens, cache_indices.shape[0] + 1),
+                          _check_list("cu_tokens", cu_tokens, cache_indices.shape[0] + 1,
+                                      self._index),
                           k.data_ptr(), self._stride("k", k, self.HKV), v.data_ptr(),
                           self._stride("v", v, self.HKV), cache_indices.data_ptr(), self._err,
                           B._stream(stream))
@@ -171,9 +185,9 @@ class PagedAttentionDecoder(_Fixed):
         if o is None:
             o = own_o
         else:
-            o_ptr = _check_out("o", o, count, self.out_dtype)
+            o_ptr = _check_out("o", o, count, self.out_dtype, self._index)
         if lse is not None:
-            lse_ptr = _check_out("lse", lse, count // self.D, torch.float32)
+            lse_ptr = _check_out("lse", lse, count // self.D, torch.float32, self._index)
         elif with_lse:
             lse = own_lse
         else:
@@ -189,9 +203,9 @@ class PagedAttentionDecoder(_Fixed):
         """Commit the appended tokens (of T drafts: the first num_accepted[b])."""
         b = cache_indices.shape[0]
         rc = self._advance(self._plan(cache_indices)[0], self._cache,
-                           _check_list("cu_tokens", cu_tokens, b + 1),
-                           _check_list("num_accepted", num_accepted, b), cache_indices.data_ptr(),
-                           self._err, B._stream(stream))
+                           _check_list("cu_tokens", cu_tokens, b + 1, self._index),
+                           _check_list("num_accepted", num_accepted, b, self._index),
+                           cache_indices.data_ptr(), self._err, B._stream(stream))
         if rc:
             raise B.RSSMError("rssm_attn_advance", rc)
 
@@ -209,17 +223,18 @@ class PagedAttentionDecoder(_Fixed):
         shape = (n_tokens, self.HKV, self.D)
         for t in (k, v):
             if t is not None and (t.dtype is not self.out_dtype or t.shape != shape or
-                                  not t.is_contiguous()):
-                raise ValueError("k and v: dense [%d, %d, %d] %s" % (shape + (self.out_dtype,)))
+                                  not t.is_contiguous() or t.get_device() != self._index):
+                raise ValueError("k and v: dense [%d, %d, %d] %s on the runner's device"
+                                 % (shape + (self.out_dtype,)))
         if k is None:
             k = torch.empty(shape, device=self.device, dtype=self.out_dtype)
         if v is None:
             v = torch.empty(shape, device=self.device, dtype=self.out_dtype)
         b = cache_indices.shape[0]
         rc = self._read(self._plan(cache_indices)[0], self._cache, n_tokens,
-                        _check_list("cu_tokens", cu_tokens, b + 1), _check_list("first", first, b),
-                        cache_indices.data_ptr(), k.data_ptr(), v.data_ptr(), self._err,
-                        B._stream(stream))
+                        _check_list("cu_tokens", cu_tokens, b + 1, self._index),
+                        _check_list("first", first, b, self._index), cache_indices.data_ptr(),
+                        k.data_ptr(), v.data_ptr(), self._err, B._stream(stream))
         if rc:
             raise B.RSSMError("rssm_attn_read", rc)
         return k, v
@@ -251,6 +266,7 @@ class AddRMSNorm(_Fixed):
             groups = self.cols // scale_group if scale_group else 1
             self.scale = torch.empty(max_rows, groups, device=dev, dtype=torch.float32)
         self._call, self._w = B.entry("rssm_add_rmsnorm"), self.weight.data_ptr()
+        self._index = _index(self.weight.device)
         self._plans = {}
 
     def dims(self, rows):
@@ -282,18 +298,19 @@ class AddRMSNorm(_Fixed):
                              % (self.cols, self.max_rows))
         for t in (x, residual, residual_out):
             if t is not None and (t.dtype is not self.act_dtype or t.numel() != n or
-                                  not t.is_contiguous()):
-                raise ValueError("x and the residuals: dense [rows, %d] %s" % (self.cols,
-                                                                               self.act_dtype))
+                                  not t.is_contiguous() or t.get_device() != self._index):
+                raise ValueError("x and the residuals: dense [rows, %d] %s on the runner's device"
+                                 % (self.cols, self.act_dtype))
         dims, own_y, own_scale, y_ptr, scale_ptr = self._plan(rows)
         if y is None:
             y = own_y
         else:
-            y_ptr = _check_out("y", y, n, self.out_dtype)
+            y_ptr = _check_out("y", y, n, self.out_dtype, self._index)
         if scale is None:
             scale = own_scale
         elif self.scale is not None:
-            scale_ptr = _check_out("scale", scale, rows * self.scale.shape[1], torch.float32)
+            scale_ptr = _check_out("scale", scale, rows * self.scale.shape[1], torch.float32,
+                                   self._index)
         res = None if residual is None else residual.data_ptr()
         rc = self._call(dims, x.data_ptr(), res, self._w, self.eps,
                         res if residual_out is None else residual_out.data_ptr(), y_ptr, scale_ptr,

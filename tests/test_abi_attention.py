@@ -174,3 +174,49 @@ def test_debug_decode_arguments(lib):
                                                 q, 1024, FAKE, FAKE, 1 << 40, FAKE, None, -1, wait_us,
                                                 None, None)
     assert call(0) == INV and call(2000001) == INV and call(1000, q=None) == INV
+
+
+def _elsewhere(dec, norm, dev):
+    """Calls of a runner of `dev` that each get one tensor of the CPU."""
+    def there(*a, **kw):
+        return torch.zeros(*a, device=dev, **kw)
+    i32, bf = dict(dtype=torch.int32), dict(dtype=torch.bfloat16)
+    ci, cu = there(3, **i32), there(4, **i32)
+    q, k, kr = there(3, 2, 8, 64, **bf), there(3, 2, 2, 64, **bf), there(5, 2, 64, **bf)
+    x = there(2, 128, **bf)
+    return [lambda: dec.decode(q.cpu(), ci), lambda: dec.decode(q, ci.cpu()),
+            lambda: dec.decode(q, ci, o=q.cpu()), lambda: dec.decode(q, ci, lse=torch.zeros(3, 2, 8)),
+            lambda: dec.append(k.cpu(), k, ci), lambda: dec.append(k, k.cpu(), ci),
+            lambda: dec.append(k, k, ci.cpu()), lambda: dec.append(k, k, ci, cu_tokens=cu.cpu()),
+            lambda: dec.advance(ci.cpu()), lambda: dec.advance(ci, num_accepted=ci.cpu()),
+            lambda: dec.advance(ci, cu_tokens=cu.cpu()), lambda: dec.read(ci.cpu(), cu, 5),
+            lambda: dec.read(ci, cu.cpu(), 5), lambda: dec.read(ci, cu, 5, first=ci.cpu()),
+            lambda: dec.read(ci, cu, 5, k=kr.cpu()), lambda: dec.read(ci, cu, 5, v=kr.cpu()),
+            lambda: norm(x.cpu()), lambda: norm(x, x.cpu()), lambda: norm(x, x, residual_out=x.cpu()),
+            lambda: norm(x, y=torch.zeros(2, 128, dtype=torch.float8_e4m3fn)),
+            lambda: norm(x, scale=torch.zeros(2, 1))]
+
+
+def _refuses(calls):
+    for i, call in enumerate(calls):
+        with pytest.raises(ValueError, match="device"):
+            call()
+
+
+def test_runner_refuses_tensors_of_another_device(lib):
+    """Without a GPU: runners made on the CPU that stand for ones of GPU 0."""
+    dec = ssm.PagedAttentionDecoder(8, 2, 64, 16, 4, 4, 2, 3, T=2, device="cpu")
+    norm = ssm.AddRMSNorm(torch.ones(128), 1e-5, 2, out_dtype=torch.float8_e4m3fn, device="cpu")
+    dec._index = norm._index = 0
+    _refuses(_elsewhere(dec, norm, "cpu"))
+
+
+@pytest.mark.gpu
+def test_gpu_runner_refuses_tensors_of_the_cpu():
+    dec = ssm.PagedAttentionDecoder(8, 2, 64, 16, 4, 4, 2, 3, T=2)
+    norm = ssm.AddRMSNorm(torch.ones(128), 1e-5, 2, out_dtype=torch.float8_e4m3fn)
+    _refuses(_elsewhere(dec, norm, "cuda"))
+    ci = torch.full((3,), -1, dtype=torch.int32, device="cuda")
+    dec.step(*(torch.zeros(3, 2, h, 64, dtype=torch.bfloat16, device="cuda") for h in (8, 2, 2)), ci)
+    norm(torch.zeros(2, 128, dtype=torch.bfloat16, device="cuda"))
+    torch.cuda.synchronize()
