@@ -31,6 +31,14 @@ def _check(name, t, shape, dtype, device):
     return t
 
 
+def _device(device):
+    """The device meant: the current GPU for None and for "cuda" without a number."""
+    dev = torch.device("cuda" if device is None else device)
+    if dev.type == "cuda" and dev.index is None:
+        dev = torch.device("cuda", torch.cuda.current_device())
+    return dev
+
+
 def _index(device):
     """What get_device() says of a tensor on this device."""
     return device.index if device.type == "cuda" else -1
@@ -82,8 +90,7 @@ class PagedAttentionDecoder(_Fixed):
                  max_pages, max_batch, T=1, act_dtype=torch.bfloat16, cache_dtype=torch.bfloat16,
                  out_dtype=torch.bfloat16, window=0, scale=None, device=None, k_cache=None,
                  v_cache=None, k_scale=None, v_scale=None, page_table=None, slot_len=None):
-        dev = torch.device("cuda", torch.cuda.current_device()) if device is None \
-            else torch.device(device)
+        dev = _device(device)
         self.HQ, self.HKV, self.D, self.T = num_q_heads, num_kv_heads, head_dim, T
         self.page_size, self.num_pages, self.max_pages = page_size, num_pages, max_pages
         self.num_slots, self.max_batch, self.window = num_slots, max_batch, window
@@ -256,7 +263,7 @@ class AddRMSNorm(_Fixed):
 
     def __init__(self, weight, eps, max_rows, act_dtype=torch.bfloat16, out_dtype=torch.bfloat16,
                  scale_group=0, device=None):
-        dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+        dev = _device(device)
         self.weight = torch.as_tensor(weight, device=dev, dtype=torch.float32).contiguous()
         self.cols, self.eps, self.max_rows = self.weight.shape[0], eps, max_rows
         self.act_dtype, self.out_dtype, self.scale_group = act_dtype, out_dtype, scale_group

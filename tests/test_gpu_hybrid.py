@@ -99,3 +99,21 @@ def test_hybrid_with_eight_bit_cache_and_norms_runs_and_leaves_padding_alone(exa
     lens = model.pages["slot_len"].tolist()
     assert [n for i, n in enumerate(lens) if i in (5, 2)] == [20, 20] and sum(lens) == 40
     assert bool(torch.isfinite(out[[0, 2]].float()).all())
+
+
+@pytest.mark.parametrize("device", [None, "cuda", 0, torch.device("cuda"), "cuda:0"])
+def test_runners_take_the_device_however_it_is_named(example, device):
+    import ssm_linear_attention_gb300 as ssm
+    cache = torch.zeros(4, 2, 16, 64, device="cuda", dtype=torch.bfloat16)
+    dec = ssm.PagedAttentionDecoder(8, 2, 64, 16, 4, 4, 2, 3, device=device, k_cache=cache,
+                                    v_cache=cache.clone())
+    assert dec.k_cache is cache and dec.device == cache.device
+    dec.page_table.copy_(torch.arange(4)[:, None].expand(4, 2))
+    ci = torch.tensor([2, 0, -1], dtype=torch.int32, device="cuda")
+    x = torch.ones(3, 12, 64, device="cuda", dtype=torch.bfloat16)
+    dec.step(x[:, :8].unsqueeze(1), x[:, 8:10], x[:, 10:], ci)
+    norm = ssm.AddRMSNorm(torch.ones(64), 1e-5, 3, device=device)
+    y, _ = norm(x[:, 0].contiguous())
+    torch.cuda.synchronize()
+    assert dec.slot_len.tolist() == [1, 0, 1, 0] and int(dec.dev_err.sum()) == 0
+    assert bool((dec.o[:2] == 1).all()) and bool((y == 1).all())
