@@ -756,7 +756,8 @@ int rssm_attn_read(const rssm_attn_dims* dims, const rssm_attn_cache* cache, int
 /* Bytes of device workspace rssm_attn_decode needs (partial results of rows whose
  * tokens several CTAs share, and their arrival counters). It must be zero-filled before
  * its first use, and again after a call that set RSSM_DEVERR_TIMEOUT; every other call
- * leaves its counters at zero. One stream at a time. 0 for an invalid dims. */
+ * leaves its counters at zero. One stream at a time. The size goes by a key head's queries,
+ * head_dim, the types and the current device's SMs. 0 for dims that rssm_attn_decode refuses. */
 size_t rssm_attn_workspace_size(const rssm_attn_dims* dims);
 
 /* rssm_attn_decode -- attention of T query tokens per row over the row's cached tokens.

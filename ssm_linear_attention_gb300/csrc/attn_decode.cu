@@ -110,6 +110,13 @@ __device__ __forceinline__ uint32_t tile_off(int t, int c) {
     }
 }
 
+// Warps of a CTA: 16 of 128 registers hide more than 8 (569 -> 481 us on 256 rows over an 8-bit
+// cache when that was measured); float32 operands need more registers, and 16 rings of wide tiles
+// do not fit.
+constexpr int warps_of(int D, bool e4m3, bool af32, bool share) {
+    return af32 || (!e4m3 && D == 128 && !share) ? 8 : 16;
+}
+
 // D: head dim, E4M3: 8-bit cache, AF32: float32 activations. The products' operands:
 //   bf16 cache: bf16, the cached values as they are. A weight in one bf16 part would add
 //     an error as large as the output's own rounding (1.41 times it together), so it takes
@@ -124,9 +131,7 @@ struct Cfg {
     // Tiles of a step: two give a warp independent work between the dependent pieces of one; a
     // ring of three wide tiles wants them one by one.
     static constexpr int TP = WIDE && !SHARE ? 1 : 2;
-    // 16 warps of 128 registers hide more than 8 (569 -> 481 us on the 256-row 8-bit case);
-    // float32 operands need more registers, and 16 rings of wide tiles do not fit
-    static constexpr int WARPS = AF32 || (WIDE && !SHARE) ? 8 : 16;
+    static constexpr int WARPS = warps_of(D, E4M3, AF32, SHARE);
     // Wide tiles come by TMA (cp.async keeps fewer bytes in flight: 128 against 154 us on the
     // 2 x 128k case); for narrow ones the two are level (437 and 431 us on the 256-row 8-bit
     // case), and where warps share a tile each copies its part.
@@ -395,7 +400,7 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
                                 a.lse[row] = none ? -INFINITY : (m[x] + log2_fast(l[x])) * kLn2;
                         }
                     } else if (!tail) {
-                        const long slot = 2L * gridDim.x + (int)blockIdx.x * kWarps + group;
+                        const long slot = 2L * gridDim.x + (int)blockIdx.x * ngroups + group;
 #pragma unroll
                             for (int x = 0; x < 2; ++x) {
                                 const int r = q0 + 2 * qd + x;
@@ -834,7 +839,7 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
     for (int i = 0; i < nruns; ++i) {
         const Run r = runs[i];
         const int last = r.rec1 - 1;
-        const float* head = a.part + (2L * gridDim.x + (int)blockIdx.x * kWarps + (last >> 1)) * a.M * D;
+        const float* head = a.part + (2L * gridDim.x + (int)blockIdx.x * ngroups + (last >> 1)) * a.M * D;
         const long slot = 2L * blockIdx.x + (r.cta0 < (int)blockIdx.x ? 0 : 1);
 #pragma unroll 1
         for (int v0 = tid; v0 < nv; v0 += kItems * kDecThreads) {
@@ -871,18 +876,41 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
 
 // ---------------------------------------------------------------- host side
 
-// Workspace: counters (one per CTA), then (m, l) of the CTAs' partial results, then the values
-// of these and of the groups' heads.
+// The kernel that a call's dims take, and its groups' layout.
+struct Form {
+    int M, MT;    // queries per key head, warps per group (each 8 queries)
+    bool wide;    // attn_wide.cu's
+    int groups;   // of a CTA at most, else
+};
+static Form form_of(const rssm_attn_dims* d) {
+    const bool e4m3 = d->cache_dtype == RSSM_E4M3, af32 = d->act_dtype == RSSM_F32;
+    Form f;
+    f.M = d->q_tokens * (d->num_q_heads / d->num_kv_heads);
+    f.MT = f.M <= 8 ? 1 : f.M <= 16 ? 2 : f.M <= 32 ? 4 : 8;
+    // The tensor-memory kernel takes more than 8 queries, but for float32 activations, whose operands
+    // would be three parts each, and an 8-bit cache under up to 16 queries, whose conversions cost it
+    // more than it saves (64 rows of 1000 to 4000 tokens, 4 key heads of 16 queries, D 64: 55 us
+    // against 40 here; D 128 56 and 55; of 32 queries 59 against 62, 68 against 89).
+    f.wide = f.MT > 1 && !af32 && !(e4m3 && f.M <= 16);
+    f.groups = warps_of(d->head_dim, e4m3, af32, f.MT > 1) / f.MT;
+    return f;
+}
+static bool too_many_queries(const rssm_attn_dims* d) {
+    return (int64_t)d->q_tokens * (d->num_q_heads / d->num_kv_heads) > 64;
+}
+
+// Workspace: counters (one per CTA), then (m, l) of the CTAs' partial results (two each), then the
+// values of these and, of the kernel of few queries, of the groups' heads.
 struct Workspace {
     size_t ml, part, bytes;
 };
-static Workspace workspace_of(const rssm_attn_dims* d) {
-    const size_t M = (size_t)d->q_tokens * (d->num_q_heads / d->num_kv_heads);
-    const size_t slots = kMaxCtas * (2 + kMaxWarps);
+static Workspace workspace_of(const rssm_attn_dims* d, const Form& f) {
+    DeviceInfo di;
+    const size_t ctas = device_info(&di) && di.sm_count < kMaxCtas ? di.sm_count : kMaxCtas;
     Workspace w;
     w.ml = kMaxCtas * sizeof(int32_t);
-    w.part = (w.ml + slots * M * 2 * sizeof(float) + 255) / 256 * 256;
-    w.bytes = w.part + slots * M * d->head_dim * sizeof(float);
+    w.part = (w.ml + ctas * 2 * f.M * 2 * sizeof(float) + 255) / 256 * 256;
+    w.bytes = w.part + ctas * (2 + (f.wide ? 0 : f.groups)) * f.M * d->head_dim * sizeof(float);
     return w;
 }
 
@@ -921,14 +949,10 @@ static int launch_kernel(const rssm_attn_dims* d, DecArgs a, const DeviceInfo& d
 }
 
 template <int D, bool E4M3, bool AF32>
-static int launch(const rssm_attn_dims* d, const DecArgs& a, const DeviceInfo& di, cudaStream_t st) {
+static int launch(const rssm_attn_dims* d, const DecArgs& a, bool wide, const DeviceInfo& di, cudaStream_t st) {
     if (a.MT == 1) return launch_kernel<D, E4M3, AF32, false>(d, a, di, st);
-    // The tensor-memory kernel takes more queries, but for float32 activations, whose operands would
-    // be three parts each, and an 8-bit cache under up to 16 queries, whose conversions cost it more
-    // than it saves (64 rows of 1000 to 4000 tokens, 4 key heads of 16 queries, D 64: 55 us against 40
-    // here; D 128 56 and 55; of 32 queries 59 against 62, 68 against 89).
     if constexpr (AF32 || E4M3)
-        if (AF32 || a.M <= 16) return launch_kernel<D, E4M3, AF32, true>(d, a, di, st);
+        if (!wide) return launch_kernel<D, E4M3, AF32, true>(d, a, di, st);
     if constexpr (!AF32) return decode_wide(d, a, di, st);
 }
 
@@ -938,8 +962,8 @@ static int launch(const rssm_attn_dims* d, const DecArgs& a, const DeviceInfo& d
 using namespace rssm;
 
 extern "C" size_t rssm_attn_workspace_size(const rssm_attn_dims* d) {
-    if (attn::check_dims(d) != RSSM_OK) return 0;
-    return attn::workspace_of(d).bytes;
+    if (attn::check_dims(d) != RSSM_OK || attn::too_many_queries(d)) return 0;
+    return attn::workspace_of(d, attn::form_of(d)).bytes;
 }
 
 static int decode_call(const rssm_attn_dims* d, const rssm_attn_cache* c, int appended, float scale,
@@ -949,10 +973,10 @@ static int decode_call(const rssm_attn_dims* d, const rssm_attn_cache* c, int ap
     const int st = attn::check_dims(d);
     if (st != RSSM_OK) return st;
     if (window < 0) return RSSM_ERR_INVALID_ARG;
-    const int G = d->num_q_heads / d->num_kv_heads;
-    if ((int64_t)d->q_tokens * G > 64) return RSSM_ERR_UNSUPPORTED;
+    if (attn::too_many_queries(d)) return RSSM_ERR_UNSUPPORTED;
     if (d->batch == 0) return RSSM_OK;
-    const attn::Workspace ws = attn::workspace_of(d);
+    const attn::Form form = attn::form_of(d);
+    const attn::Workspace ws = attn::workspace_of(d, form);
     if (!attn::ok_cache(d, c) || !ok_ptr(q) || !attn::ok_stride(d, q_stride, d->num_q_heads) ||
         !ok_ptr(cache_indices) || !ok_ptr(workspace) || workspace_bytes < ws.bytes || !ok_ptr(o) ||
         !ok_opt_ptr(lse))
@@ -977,7 +1001,7 @@ static int decode_call(const rssm_attn_dims* d, const rssm_attn_cache* c, int ap
     a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + ws.part);
     a.qscale = scale * attn::kLog2e;
     a.T = d->q_tokens;
-    a.G = G;
+    a.G = d->num_q_heads / d->num_kv_heads;
     a.hq = d->num_q_heads;
     a.hkv = d->num_kv_heads;
     a.ps_log2 = attn::log2_of(d->page_size);
@@ -986,18 +1010,18 @@ static int decode_call(const rssm_attn_dims* d, const rssm_attn_cache* c, int ap
     a.num_slots = d->num_slots;
     a.window = window < (1 << 30) ? window : 1 << 30;  // (no row is longer: sums with it stay in 32 bits)
     a.appended = appended != 0;
-    a.M = a.T * G;
-    a.MT = a.M <= 8 ? 1 : a.M <= 16 ? 2 : a.M <= 32 ? 4 : 8;
+    a.M = form.M;
+    a.MT = form.MT;
     a.obf = d->out_dtype == RSSM_BF16;
     a.wait_ns = wait_ns;
     a.stall = stall;
     const bool q8 = d->cache_dtype == RSSM_E4M3, f32 = d->act_dtype == RSSM_F32;
     const cudaStream_t s = (cudaStream_t)stream;
 #define RSSM_ATTN_D(D_)                                                            \
-    (q8 ? (f32 ? attn::launch<D_, true, true>(d, a, di, s)                      \
-               : attn::launch<D_, true, false>(d, a, di, s))                    \
-        : (f32 ? attn::launch<D_, false, true>(d, a, di, s)                     \
-               : attn::launch<D_, false, false>(d, a, di, s)))
+    (q8 ? (f32 ? attn::launch<D_, true, true>(d, a, form.wide, di, s)                      \
+               : attn::launch<D_, true, false>(d, a, form.wide, di, s))                    \
+        : (f32 ? attn::launch<D_, false, true>(d, a, form.wide, di, s)                     \
+               : attn::launch<D_, false, false>(d, a, form.wide, di, s)))
     return d->head_dim == 64 ? RSSM_ATTN_D(64) : RSSM_ATTN_D(128);
 #undef RSSM_ATTN_D
 }

@@ -40,7 +40,8 @@ struct DecArgs {
     void* o;
     float* lse;
     int32_t* dev_err;
-    float* part;       // [2 x CTAs][M][D] partial results of CTAs, then of groups
+    float* part;       // [2 x CTAs][M][D] partial results of CTAs, then [CTAs][groups][M][D] of
+                       // the groups' heads (few queries)
     float* part_ml;    // [2 x CTAs][M][2]
     int32_t* counters; // [CTAs]
     float qscale;      // scale * log2 e

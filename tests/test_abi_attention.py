@@ -220,3 +220,27 @@ def test_gpu_runner_refuses_tensors_of_the_cpu():
     dec.step(*(torch.zeros(3, 2, h, 64, dtype=torch.bfloat16, device="cuda") for h in (8, 2, 2)), ci)
     norm(torch.zeros(2, 128, dtype=torch.bfloat16, device="cuda"))
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("kw,records", [
+    (dict(num_q_heads=8, cache_dtype=B.RSSM_BF16), 2 + 8),                    # 8 groups a CTA
+    (dict(num_q_heads=8), 2 + 16),
+    (dict(num_q_heads=32), 2 + 8),                                            # two warps a group
+    (dict(num_q_heads=16, q_tokens=4), 2), (dict(num_q_heads=128), 2),        # many queries: the CTAs'
+    (dict(num_q_heads=32, cache_dtype=B.RSSM_BF16), 2),
+    (dict(num_q_heads=128, act_dtype=B.RSSM_F32, out_dtype=B.RSSM_F32), 2 + 1),
+])
+def test_workspace_is_what_the_call_s_kernel_uses(lib, kw, records):
+    d = _dims(**kw)
+    M = d.q_tokens * d.num_q_heads // d.num_kv_heads
+    size = B.rssm_attn_workspace_size(d)
+    assert 0 < size <= 256 * (4 + records * M * d.head_dim * 4 + 2 * M * 8) + 256
+    assert _decode(d, q_stride=d.num_q_heads * 128, wsb=size - 1) == INV
+
+
+def test_workspace_of_dims_that_only_append(lib):
+    """T of a prompt's length: rssm_attn_decode refuses it, no workspace is asked for."""
+    d = _dims(q_tokens=4096, num_q_heads=16)
+    assert B.rssm_attn_workspace_size(d) == 0 and _decode(d) == UNS
+    dec = ssm.PagedAttentionDecoder(16, 2, 64, 16, 4, 4, 2, 1, T=4096, device="cpu")
+    assert dec.workspace.numel() <= 16

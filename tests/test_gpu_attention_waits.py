@@ -89,3 +89,31 @@ def test_a_page_table_written_just_before_the_call(hq, cache):
         got.append(dec.decode(q, ci, appended=False).clone())
     torch.cuda.synchronize()
     assert all(torch.equal(o, want[i % 2]) for i, o in enumerate(got))
+
+
+@pytest.mark.parametrize("hq,cache,act,d,T", [
+    (4, torch.bfloat16, torch.bfloat16, 128, 1), (4, torch.bfloat16, torch.bfloat16, 64, 2),
+    (4, FP8, torch.bfloat16, 128, 1), (8, FP8, torch.bfloat16, 64, 2), (16, FP8, torch.bfloat16, 128, 1),
+    (4, torch.bfloat16, torch.float32, 128, 1), (3, FP8, torch.float32, 64, 5),
+    (8, torch.bfloat16, torch.float32, 128, 8), (16, torch.bfloat16, torch.bfloat16, 128, 1),
+    (8, FP8, torch.bfloat16, 128, 4), (16, torch.bfloat16, torch.bfloat16, 64, 4),
+])
+def test_a_call_stays_within_its_workspace(hq, cache, act, d, T):
+    """Rows that many CTAs and groups share, in a workspace of just the size asked for: what
+    lies behind it stays."""
+    import ssm_linear_attention_gb300 as ssm
+    lens = [21000, 40, 7777, 1, 900]
+    dec, ci, table, slots, g = A.make(5, lens, hq=hq, hkv=1, d=d, T=T, page=64, cache=cache, act=act, seed=7)
+    A.fill(dec, ci, table, slots, lens, g)
+    q = torch.randn(5, T, hq, d, generator=g, device="cuda").to(act)
+    ws = torch.zeros(dec.ws_bytes + (8 << 20), device="cuda", dtype=torch.uint8)
+    ws[dec.ws_bytes:] = 0xa5
+    o = torch.empty(5, T, hq, d, device="cuda", dtype=act)
+    lse = torch.empty(5, T, hq, device="cuda")
+    for _ in range(2):
+        ssm.rssm_attn_decode(dec.dims(5), dec.cache, False, dec.scale, 0, q, hq * d, ci, ws, dec.ws_bytes,
+                             o, lse, dec.dev_err)
+    torch.cuda.synchronize()
+    assert bool((ws[dec.ws_bytes:] == 0xa5).all()) and int(dec.dev_err.sum()) == 0
+    assert bool((ws[:1024] == 0).all())                  # the counters are back at zero
+    A.check(dec, o, lse, A.reference(dec, q, table, slots, lens, False))
