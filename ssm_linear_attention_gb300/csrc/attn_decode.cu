@@ -6,9 +6,9 @@
 // M = T G queries read the same cached tokens, so every cached vector is read once for all
 // of them:
 //     S^T = K Q^T (tokens x M),  P = exp2(S - running maximum),  O^T += V^T P^T,
-// with the softmax's maximum m and sum l kept per query while the tokens stream by and O, l
-// rescaled when a score passes m by more than 8 (weights up to 2^8 lose nothing in float32
-// sums or bf16 / f16 operands, and most tiles then need no maximum across lanes). Two
+// with the softmax's base m (the largest score and 8) and sum l kept per query while the tokens
+// stream by and O, l rescaled when a score passes m (float32 sums and bf16 operands lose nothing by
+// the 8, and most tiles then need no maximum across lanes). Two
 // partial results (m, l, O) over different tokens join as O = O_1 2^(m_1 - m) +
 // O_2 2^(m_2 - m), l likewise, m = max(m_1, m_2); that makes the token axis free to split.
 //
@@ -609,7 +609,7 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
 #pragma unroll
                 for (int u = 0; u < C::TP; ++u)
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) grow |= p[u][x] > m[x & 1] + kSlack;
+                        for (int x = 0; x < 4; ++x) grow |= p[u][x] > m[x & 1];
                 if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
@@ -618,7 +618,8 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
 #pragma unroll
                             for (int w = 4; w < 32; w <<= 1)
                                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-                            top = fmaxf(top, m[x]);
+                            // (a query whose base holds keeps it)
+                            top = top > m[x] ? top + kSlack : m[x];
                             const float f = top == m[x] ? 1.f : exp2_fast(m[x] - top);
                             m[x] = top;
                             l[x] *= f;

@@ -24,7 +24,9 @@ constexpr int kMinTiles = 2;
 constexpr int kWholeTiles = 96;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-// m follows the largest score once it is this far behind (log2 units)
+// The base m of the weights 2^(s - m) is the largest score and this much (log2 units): it moves when a
+// score passes it, so most tiles need no maximum across lanes, and no weight is above 1 (a sum of
+// weighted values overflows only where one of plain softmax weights would).
 constexpr float kSlack = 8.f;
 
 struct DecArgs {

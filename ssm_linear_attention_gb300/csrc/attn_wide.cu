@@ -11,7 +11,8 @@
 // with a token a lane of S: a thread makes its token's weights for N / 2 (N / 4) queries without
 // looking at another lane, and writes them as rows of P. The weights are two bf16 parts,
 // side by side in P, so that V is read once for both; their sums meet when a (row, head) ends.
-// As there, O is rescaled only when a score passes the running maximum by 8 (log2 units).
+// As there, the weights' base is 8 (log2 units) above the largest score, and O is rescaled only when a
+// score passes it.
 //
 // One CTA per SM, a range of the tile list each. Warps 0 to 7 (or 15): softmax, a quarter of the
 // tensor memory's lanes and half (a quarter) of the queries each. Then a warp for loads
@@ -376,10 +377,10 @@ __global__ void __launch_bounds__((Wide<D, E4M3, N>::THREADS), 1)
                         e[q + 1] = p[q + 1] - b.y;
                         e[q + 2] = p[q + 2] - b.z;
                         e[q + 3] = p[q + 3] - b.w;
-                        grow |= e[q] > kSlack;
-                        grow |= e[q + 1] > kSlack;
-                        grow |= e[q + 2] > kSlack;
-                        grow |= e[q + 3] > kSlack;
+                        grow |= e[q] > 0.f;
+                        grow |= e[q + 1] > 0.f;
+                        grow |= e[q + 2] > 0.f;
+                        grow |= e[q + 3] > 0.f;
                     }
                 if (first || any_soft<C::SOFT>(grow || dead)) {
                     // the maxima move: theirs over the chunk, then l and O follow
@@ -392,7 +393,8 @@ __global__ void __launch_bounds__((Wide<D, E4M3, N>::THREADS), 1)
                     if (dead) break;
                     if (tid < N) {
                         const float old = first ? -INFINITY : ms[tid];
-                        const float m = fmaxf(fmaxf(fmaxf(red[0][tid], red[1][tid]), fmaxf(red[2][tid], red[3][tid])), old);
+                        const float top = fmaxf(fmaxf(red[0][tid], red[1][tid]), fmaxf(red[2][tid], red[3][tid]));
+                        const float m = top > old ? top + kSlack : old;
                         ms[tid] = m;
                         // (seen only -infinity: weights of zero, and any score passes it)
                         mb[tid] = m == -INFINITY ? -1e30f : m;

@@ -215,3 +215,18 @@ def test_many_short_rows_whose_queries_differ_in_size(T, hq):
     for _ in range(50):
         o, lse = dec.decode(q, ci, appended=False, with_lse=True)
         assert torch.equal(o, first) and torch.equal(lse, first_lse)
+
+
+@pytest.mark.parametrize("cache", [torch.bfloat16, FP8])
+@pytest.mark.parametrize("M,act", FORMS)
+@pytest.mark.parametrize("d", [64, 128])
+def test_values_near_the_largest_float(M, act, d, cache):
+    """Scores that rise by 5 nats through the row, values of 2^122: the sum of softmax weights times
+    values stays below float32's largest, and no weight is above 1."""
+    n = 640
+    dec, ci, table, slots, g, k, v, q = row(n, M, act, d, 6, cache=cache)
+    k[:, :, 0] = nats(1.0, d) * torch.linspace(0, 5, n, device="cuda")[:, None]
+    v = (1 + v.abs()) * 2.0 ** 114
+    v[n // 2:] *= 2.0 ** 4
+    append(dec, ci, k, v)
+    compare(dec, ci, q, table, slots, n)
