@@ -537,7 +537,9 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
             if (C::TP > 1) some = some || t[C::TP - 1].y >= 0;
             if (some && works) {
                 // ------------------------------------------------ S^T = K Q^T
-                constexpr int SA = C::TP == 1 ? 2 : 1;  // one tile: two chains of sums
+                // One tile: two chains of sums. Float32 queries: one of the first parts and one of the
+                // rest, which an infinite key (or query) turns into NaN where the first has the sign.
+                constexpr int SA = C::TP == 1 || AF32 ? 2 : 1;
                 float sa[C::TP][SA][4];
 #pragma unroll
                 for (int u = 0; u < C::TP; ++u)
@@ -559,14 +561,14 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
                                 e4m3x4_to_f16(r[x], f[x >> 1][x & 1], f[x >> 1][2 + (x & 1)]);
 #pragma unroll
                             for (int p = 0; p < C::QP; ++p) {
-                                    mma16816<true>(sa[u][0], f[0], qf[kk][p][0], qf[kk][p][1]);
-                                    mma16816<true>(sa[u][SA - 1], f[1], qf[kk + 1][p][0], qf[kk + 1][p][1]);
+                                    mma16816<true>(sa[u][AF32 && p > 0 ? 1 : 0], f[0], qf[kk][p][0], qf[kk][p][1]);
+                                    mma16816<true>(sa[u][AF32 ? p > 0 : SA - 1], f[1], qf[kk + 1][p][0], qf[kk + 1][p][1]);
                             }
                         } else {
                             ldsm4(at + kk / 4 * (kTok * 128), r);
 #pragma unroll
                             for (int p = 0; p < C::QP; ++p)
-                                    mma16816<false>(sa[u][SA == 2 ? kk & 1 : 0], r, qf[kk][p][0], qf[kk][p][1]);
+                                    mma16816<false>(sa[u][AF32 ? p > 0 : SA == 2 ? kk & 1 : 0], r, qf[kk][p][0], qf[kk][p][1]);
                         }
                     }
                 // ------------------------------------------------ softmax
@@ -590,7 +592,8 @@ __global__ void __launch_bounds__((Cfg<D, E4M3, AF32, SHARE>::WARPS * 32), 1)
                     edges = edges || edge[u];
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
-                            float f = SA == 2 ? sa[u][0][x] + sa[u][SA - 1][x] : sa[u][0][x];
+                            float f = sa[u][0][x];
+                            if (SA == 2 && !(AF32 && isinf(f))) f += sa[u][SA - 1][x];
                             f *= rs[x & 1];
                             if (E4M3) f *= ks[x >> 1];
                             p[u][x] = f;

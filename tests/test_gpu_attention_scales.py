@@ -230,3 +230,32 @@ def test_values_near_the_largest_float(M, act, d, cache):
     v[n // 2:] *= 2.0 ** 4
     append(dec, ci, k, v)
     compare(dec, ci, q, table, slots, n)
+
+
+@pytest.mark.parametrize("act", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("hq,d", [(2, 128), (2, 64), (32, 128), (32, 64)])
+def test_infinite_keys_under_queries_of_any_size(act, hq, d):
+    """An infinite element of a key makes its score infinite with the sign of the product, a weight of
+    zero or (+infinity) a NaN, also where the query enters the product in parts."""
+    lens = [300]
+    dec, ci, table, slots, g = A.make(1, lens, hq=hq, hkv=2, d=d, act=act, out=torch.float32, seed=17)
+    A.fill(dec, ci, table, slots, lens, g)
+    q = torch.randn(1, 1, hq, d, generator=g, device="cuda").to(act)
+    q[..., 3] = q[..., 3].abs() + 0.1
+    p, o = places(dec, table, slots, range(300))
+    dec.k_cache[p, :, o, 3] = -math.inf                      # every score -infinity
+    out, lse = dec.decode(q, ci, appended=False, with_lse=True)
+    torch.cuda.synchronize()
+    assert bool((out == 0).all()) and bool((lse == -math.inf).all())
+    dec.k_cache[p[40:44], :, o[40:44], 3] = 0.5              # four tokens left
+    out, lse = dec.decode(q, ci, appended=False, with_lse=True)
+    torch.cuda.synchronize()
+    ro, rl, w = A.reference(dec, q, table, slots, lens, False, hidden=set(range(300)) - {40, 41, 42, 43})
+    assert float(((out.double() - ro).abs() - BOUND * w).max()) <= 1e-30
+    assert float((lse.double() - rl).abs().max()) <= 2e-5
+    dec.k_cache[p[100], 0, o[100], 3] = math.inf
+    out, lse = dec.decode(q, ci, appended=False, with_lse=True)
+    torch.cuda.synchronize()
+    G = hq // 2
+    assert bool(torch.isnan(out[:, :, :G]).all()) and bool(torch.isnan(lse[:, :, :G]).all())
+    assert float(((out.double() - ro).abs() - BOUND * w)[:, :, G:].max()) <= 1e-30
