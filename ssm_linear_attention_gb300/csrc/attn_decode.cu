@@ -5,7 +5,7 @@
 // For a row's T query tokens and the G = HQ / HKV query heads of one key / value head, the
 // M = T G queries read the same cached tokens, so every cached vector is read once for all
 // of them:
-//     S^T = K Q^T (tokens x M),  P = exp2(S - running maximum),  O^T += V^T P^T,
+//     S^T = K Q^T (tokens x M),  P = exp2(S - m),  O^T += V^T P^T,
 // with the softmax's base m (the largest score and 8) and sum l kept per query while the tokens
 // stream by and O, l rescaled when a score passes m (float32 sums and bf16 operands lose nothing by
 // the 8, and most tiles then need no maximum across lanes). Two
@@ -30,11 +30,13 @@
 // joins the CTAs' results, in an order that the lengths and the machine alone fix.
 //
 // Measured (one GB300, GPU time of a call; "of" the measured copy bandwidth): 256 rows of 2k
-// to 8k tokens, 8 key heads of 4 queries, D 128, 8-bit cache: 443 us, 6.4 TB/s, 95 % of it;
-// 2 rows of 131k and 64k tokens, bf16 cache: 127 us, 6.3 TB/s, 93 %. 16 rows in float32 under a
-// window of 1000 tokens: 11.8 us. One row of 300 tokens: 8.7 us, latency throughout (three
-// dependent look-ups, one round trip of loads, two joins, and instructions fetched for the first
-// time).
+// to 8k tokens, 8 key heads of 4 queries, D 128, 8-bit cache: 444 us, 6.4 TB/s, 94 % of it;
+// 2 rows of 131k and 64k tokens, bf16 cache: 129 us, 6.2 TB/s, 91 %. 64 rows of 1000 to 4000 tokens, 4 key
+// heads, D 128, in float32: 67 us with 8 queries (74 %), 137 with 32, 266 with 64, where the products of
+// three parts and a pass over the tile for every 8 queries bind. 16 rows in float32 under a window of
+// 1000 tokens: 11.8 us, 64 (row, head)s on as many of the SMs. One row of 300 tokens: 8.7 us, latency
+// throughout (three dependent look-ups, one round trip of loads, two joins, and instructions fetched
+// for the first time).
 #include <cstring>
 
 #include "attn_decode.cuh"
@@ -123,8 +125,10 @@ constexpr int warps_of(int D, bool e4m3, bool af32, bool share) {
 //     two; float32 activations take three parts of each, all 24 bits.
 //   8-bit cache: keys and queries f16, which holds every e4m3 value; a query row is divided by
 //     the power of two at its largest element and takes one part, two of float32. Values and
-//     weights (times the value scales) are bf16, in as many parts as with a bf16 cache: f16 has no room below 2^-25 for the weights of a hundred thousand
-//     tokens that stand far behind one, which may add up to all of an output.
+//     weights (times the value scales) are bf16, in as many parts as with a bf16 cache: f16
+//     has no room below 2^-25 for the weights of a hundred thousand tokens that stand far behind
+//     one, which may add up to all of an output. (f16 took 443 us of the 256-row case, too; with
+//     float32 activations, 64 rows of 4000 tokens, 72 us against 80 with three parts.)
 template <int D, bool E4M3, bool AF32, bool SHARE>
 struct Cfg {
     static constexpr bool WIDE = !E4M3 && D == 128;
@@ -133,8 +137,8 @@ struct Cfg {
     static constexpr int TP = WIDE && !SHARE ? 1 : 2;
     static constexpr int WARPS = warps_of(D, E4M3, AF32, SHARE);
     // Wide tiles come by TMA (cp.async keeps fewer bytes in flight: 128 against 154 us on the
-    // 2 x 128k case); for narrow ones the two are level (437 and 431 us on the 256-row 8-bit
-    // case), and where warps share a tile each copies its part.
+    // 2 x 128k case when both were built); for narrow ones the two were level (437 and 431 us on
+    // the 256-row 8-bit case), and where warps share a tile each copies its part.
     static constexpr bool TMA = WIDE && !SHARE;
     static constexpr int ROWB = D * (E4M3 ? 1 : 2);  // bytes of a cached vector
     static constexpr int KB = kTok * ROWB;           // K (or V) bytes of a tile
@@ -893,8 +897,8 @@ static Form form_of(const rssm_attn_dims* d) {
     f.MT = f.M <= 8 ? 1 : f.M <= 16 ? 2 : f.M <= 32 ? 4 : 8;
     // The tensor-memory kernel takes more than 8 queries, but for float32 activations, whose operands
     // would be three parts each, and an 8-bit cache under up to 16 queries, whose conversions cost it
-    // more than it saves (64 rows of 1000 to 4000 tokens, 4 key heads of 16 queries, D 64: 55 us
-    // against 40 here; D 128 56 and 55; of 32 queries 59 against 62, 68 against 89).
+    // more than it saves (64 rows of 1000 to 4000 tokens, 4 key heads of 16 queries: D 64 65 us
+    // against 45 here, D 128 70 and 63; of 32 queries 64 against 70, 73 against 104).
     f.wide = f.MT > 1 && !af32 && !(e4m3 && f.M <= 16);
     f.groups = warps_of(d->head_dim, e4m3, af32, f.MT > 1) / f.MT;
     return f;

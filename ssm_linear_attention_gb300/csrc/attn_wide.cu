@@ -17,7 +17,7 @@
 // One CTA per SM, a range of the tile list each. Warps 0 to 7 (or 15): softmax, a quarter of the
 // tensor memory's lanes and half (a quarter) of the queries each. Then a warp for loads
 // (TMA), one for the products, two for the queries of the next (row, head), and with an 8-bit
-// cache eight that turn the loaded tiles into f16 operands (four K, four V). They meet at
+// cache eight that turn the loaded tiles into operands (four K in f16, four V in bf16). They meet at
 // mbarriers; S has two buffers, so that the products of a chunk run beside the softmax of the
 // one before. The descriptors are made by the whole warp and only stepped by the elected lane:
 // built inside its branch they cost more than the products (1100 against 480 cycles for eight).
@@ -28,13 +28,14 @@
 // Measured (one GB300, GPU time of a call; in brackets the warp-level kernel that took these
 // calls before): 128 rows of 500 to 2000 tokens, 4 drafts, 4 key heads of 8 queries, D 128, bf16
 // cache: 65 us, 5.0 TB/s, 73 % of the measured copy bandwidth [88]; 26 rows of 2.8k to 11k
-// tokens, M 32, 8-bit cache: 128 us, 44 % [183], where the conversions' and the softmax's shared-
+// tokens, M 32, 8-bit cache: 136 us, 43 % [203], where the conversions' and the softmax's shared-
 // memory accesses wait on one another; 147 rows of 500 to 2090 tokens, M 32, D 64, bf16: 104 us
 // [130]; 34 rows of 120 to 470, M 32, bf16: 12.6 us [17.4]; 24 rows of 28 to 113, M 64, bf16: 19 us
-// [22.6]; 64 rows of 1000 to 4000 tokens, M 64, D 128, bf16: 80 us [147], 8-bit: 119 [159].
+// [22.6]; 64 rows of 1000 to 4000 tokens, M 64, D 128, bf16: 80 us [147], 8-bit: 125 [159].
 // Short (row, head)s over an 8-bit cache, several to a CTA, are level: 55 rows of 100 to 384, M 32,
-// D 64: 27 us [25.6]. Tried: 16 softmax warps for 32 queries (level), integer conversions of
-// e4m3 (148 us against 136), conversions by four warps for K and V in turn (140 against 137).
+// D 64: 28 us [25.6]. Tried, when values were f16, too: 16 softmax warps for 32 queries (level), integer
+// conversions of e4m3 (148 us against 136), conversions by four warps for K and V in turn (140
+// against 137).
 #include <cstring>
 
 #include "attn_decode.cuh"

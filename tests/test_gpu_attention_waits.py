@@ -1,7 +1,10 @@
-"""The attention kernels' bounded waits: a stage whose barrier is armed for 16 bytes more than
-its copies deliver makes the waiting warp give up after a short limit. The copies have landed, the
-kernel returns with RSSM_DEVERR_TIMEOUT, what it could not finish keeps its outputs, and the next
-call (with a cleared workspace) runs normally. No wait is unbounded."""
+"""The attention kernels' bounded waits, and what a call may touch.
+
+A stage whose barrier is armed for 16 bytes more than its copies deliver makes the waiting warp
+give up after a short limit. The copies have landed, the kernel returns with
+RSSM_DEVERR_TIMEOUT, what it could not finish keeps its outputs, and the next call (with a
+cleared workspace) runs normally. No wait is unbounded. Besides: tables written right before a
+call, and a workspace of just the size asked for."""
 import time
 
 import pytest
