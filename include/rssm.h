@@ -887,8 +887,9 @@ int rssm_debug_pipeline_copy(const float* src, float* dst, int n_tiles, int stal
  * armed for 16 bytes more than its copies deliver: that of tile stall_tile of the launch's
  * tile list (16 tokens of a row and key head; of the kernel of many queries, unit
  * stall_tile of its list of chunks). The copies land, the wait runs out, and the CTA winds
- * down as rssm_attn_decode's would. Kernels whose copies no barrier counts (8-bit caches and
- * head_dim 64 with few queries) ignore stall_tile. The pages have no counterpart. */
+ * down as rssm_attn_decode's would. Kernels whose copies no barrier counts ignore stall_tile (few
+ * queries over an 8-bit cache or of head_dim 64, more than 8 of float32). The pages have no
+ * counterpart. */
 int rssm_debug_attn_decode(const rssm_attn_dims* dims, const rssm_attn_cache* cache, int appended,
                            float scale, int32_t window, const void* q, int64_t q_stride,
                            const int32_t* cache_indices, void* workspace, size_t workspace_bytes,
