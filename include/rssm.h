@@ -819,6 +819,122 @@ int rssm_add_rmsnorm(const rssm_norm_dims* dims, const void* x, const void* resi
                      rssm_stream_t stream);
 
 /* ------------------------------------------------------------------------- */
+/* Linear attention with a decay for each head: prompts and single tokens      */
+/* ------------------------------------------------------------------------- */
+
+/* For head h of a row, with key head h / (H / G) and state S [P][N], S before the row's
+ * first token being zero or the slot's:
+ *   S_t = exp(g_t) S_{t-1} + w_t v_t k_t^T,   o_t = scale S_t q_t
+ * The state pool has the Mamba2 checkpoint's layout, so that a Mamba2 layer's prompt is
+ * this with g = dt A, w = dt, v = x, k = B, q = C and scale 1 (the skip D x and the gate are
+ * the caller's), and its decode steps go on from the pool. The pages give decode steps only
+ * ([M2] 实现拆解: prompts go through the engine's prefill kernels). */
+typedef struct rssm_linattn_dims {
+    int32_t batch;       /* rows in this call (>= 0) */
+    int32_t num_heads;   /* H */
+    int32_t num_k_heads; /* G: H % G == 0 */
+    int32_t key_dim;     /* N: 64 or 128 */
+    int32_t value_dim;   /* P: 64 or 128 */
+    int32_t num_slots;
+    int32_t state_dtype; /* RSSM_F32 | RSSM_BF16: state [num_slots][H][P][N] */
+    int32_t act_dtype;   /* RSSM_F32 | RSSM_BF16: q, k, v */
+    int32_t out_dtype;   /* RSSM_F32 | RSSM_BF16: o */
+} rssm_linattn_dims;
+
+/* A call's tokens: HOST struct of device pointers, read during the call only. Strides in
+ * elements between tokens.
+ *   q, k  token i's [G][N] block at i * q_stride (k_stride), >= G * N, a multiple of 8
+ *   v     token i's [H][P] block at i * v_stride, >= H * P, a multiple of 8
+ *   g     token i's [H] natural logarithms of the decays at i * g_stride, >= H, or 0: one [H]
+ *         for every token. Usually <= 0; -infinity empties the state before the token is added.
+ *   w     token i's [H] factors at i * w_stride (>= H); NULL: 1 */
+typedef struct rssm_linattn_inputs {
+    const void* q;
+    const void* k;
+    const void* v;
+    const float* g;
+    const float* w;
+    int64_t q_stride;
+    int64_t k_stride;
+    int64_t v_stride;
+    int64_t g_stride;
+    int64_t w_stride;
+    float scale;
+} rssm_linattn_inputs;
+
+/* Bytes of device workspace rssm_linattn_prompt needs for n_tokens tokens (states of the
+ * parts of long rows; 0 where rows are not cut). It need not be initialised, and holds nothing
+ * between calls; one stream at a time. The size goes by the dims, n_tokens and the current
+ * device's SMs, and does not shrink as n_tokens grows. 0 for dims that rssm_linattn_prompt
+ * refuses. */
+size_t rssm_linattn_workspace_size(const rssm_linattn_dims* dims, int32_t n_tokens);
+
+/* rssm_linattn_prompt -- a whole list of tokens through the recurrence.
+ *   cu_tokens [batch + 1] int32: row b has tokens cu_tokens[b] .. cu_tokens[b+1]-1 (a
+ *     non-decreasing list, 0 <= cu_tokens[b] <= n_tokens; tokens before the first and after the
+ *     last are not touched). NULL: n_tokens / batch tokens each (RSSM_ERR_CONFIG unless whole).
+ *   resume [batch] uint8 (nullable): where it is not 0 the row goes on from its slot's state,
+ *     elsewhere, and everywhere with NULL, from zero, whatever the slot holds.
+ *   state: row b's slot receives the state after its last token; a row without tokens
+ *     leaves its slot as it is.
+ *   o [n_tokens][H][P] out_dtype.
+ * A row whose part of cu_tokens decreases or leaves [0, n_tokens] is skipped and sets
+ * RSSM_DEVERR_CURSOR. With bf16 activations a chunk of 64 tokens at a time on the tensor
+ * cores: products of bf16 values are exact, sums and states float32, and where a weight, a
+ * state or a decayed value enters a product it has 16 bits. An infinity or a NaN in v (k, g, w)
+ * reaches its head's outputs and state of that value row (all value rows) from its token on, as an
+ * infinity or a NaN, and no earlier ones; one in q reaches that token's outputs. The order of every
+ * sum is fixed by the lengths, n_tokens and the GPU's SM count: repeated calls give identical bits.
+ * A bounded wait that runs out sets RSSM_DEVERR_TIMEOUT; what was not finished is not written. */
+int rssm_linattn_prompt(const rssm_linattn_dims* dims, const rssm_linattn_inputs* in,
+                        int32_t n_tokens, const int32_t* cu_tokens, const uint8_t* resume,
+                        void* state, const int32_t* cache_indices, void* workspace,
+                        size_t workspace_bytes, void* o, int32_t* dev_err, rssm_stream_t stream);
+
+/* rssm_linattn_step -- one token for each row, from and into its slot's state: token b is row
+ * b's, o [batch][H][P]. */
+int rssm_linattn_step(const rssm_linattn_dims* dims, const rssm_linattn_inputs* in, void* state,
+                      const int32_t* cache_indices, void* o, int32_t* dev_err,
+                      rssm_stream_t stream);
+
+/* ------------------------------------------------------------------------- */
+/* Rotary positions                                                           */
+/* ------------------------------------------------------------------------- */
+
+typedef struct rssm_rope_dims {
+    int32_t batch;       /* rows (positions from slots only) */
+    int32_t n_tokens;    /* >= 0 */
+    int32_t num_q_heads; /* HQ >= 1 */
+    int32_t num_k_heads; /* HK >= 0 (0: no k) */
+    int32_t head_dim;    /* D: a multiple of 8, at most 512 */
+    int32_t rot_dim;     /* R: even, 2 .. D: the first R values of a head are rotated */
+    int32_t interleaved; /* 0: pairs (i, i + R/2); else (2i, 2i + 1) */
+    int32_t num_slots;   /* (positions from slots only) */
+    int32_t act_dtype;   /* RSSM_F32 | RSSM_BF16 */
+} rssm_rope_dims;
+
+/* rssm_rope -- rotate the queries' and keys' pairs by their token's position:
+ *   (x, y)_i -> mscale (x cos a - y sin a, y cos a + x sin a),  a = 2 pi pos freq[i] / 2^64
+ * freq [R/2] uint64: turns per position in units of 2^-64, so that pos * freq mod 2^64 is the
+ * angle of any int32 position, exactly; the cosine and sine are good to float32. The negative
+ * position turns back.
+ *   positions [n_tokens] int32; or NULL: token j of row b is at slot_len[cache_indices[b]] + j, rows
+ *     of cu_tokens [batch + 1] (NULL: n_tokens / batch each), as rssm_attn_append writes it. Tokens
+ *     of a padding row (negative cache index) and outside of every row are left untouched; a
+ *     cache index >= num_slots sets RSSM_DEVERR_SLOT and leaves its tokens.
+ *   q: token i's [HQ][D] block at i * q_stride, k: [HK][D] at i * k_stride (>= heads * D, multiples of
+ *     8); q_out, k_out alike. q_out may be q with the same stride (in place; then values past R
+ *     are not touched, else they are copied), k_out k; other overlaps are undefined.
+ * Errors: RSSM_ERR_UNSUPPORTED for a head_dim above 512 or no multiple of 8, or n_tokens *
+ * max(HQ, HK) >= 2^30; RSSM_ERR_CONFIG for an odd rot_dim or one outside 2 .. D, and for n_tokens that
+ * batch does not divide where that counts. */
+int rssm_rope(const rssm_rope_dims* dims, const uint64_t* freq, float mscale,
+              const int32_t* positions, const int32_t* cache_indices, const int32_t* slot_len,
+              const int32_t* cu_tokens, const void* q, int64_t q_stride, const void* k,
+              int64_t k_stride, void* q_out, int64_t q_out_stride, void* k_out,
+              int64_t k_out_stride, int32_t* dev_err, rssm_stream_t stream);
+
+/* ------------------------------------------------------------------------- */
 
 /* rssm_mamba2_materialize_state -- test / debug: the current recurrent state of the
  * dims->batch slots listed in slots[] (negative entries skipped), folded from the

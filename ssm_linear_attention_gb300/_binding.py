@@ -36,6 +36,7 @@ EXPORTS = (
     "rssm_kda_output", "rssm_kda_step", "rssm_kda_full_state_decode",
     "rssm_attn_append", "rssm_attn_read", "rssm_attn_workspace_size", "rssm_attn_decode",
     "rssm_attn_advance", "rssm_add_rmsnorm",
+    "rssm_linattn_workspace_size", "rssm_linattn_prompt", "rssm_linattn_step", "rssm_rope",
     "rssm_debug_pipeline_copy", "rssm_debug_umma_fold", "rssm_debug_attn_decode",
 )
 
@@ -80,6 +81,25 @@ class NormDims(ctypes.Structure):
         "rows", "cols", "scale_group", "act_dtype", "out_dtype")]
 
 
+class LinattnDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "batch", "num_heads", "num_k_heads", "key_dim", "value_dim", "num_slots", "state_dtype",
+        "act_dtype", "out_dtype")]
+
+
+class LinattnInputs(ctypes.Structure):
+    """A call's tokens as device addresses and strides (linattn_inputs() fills it from tensors)."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k", "v", "g", "w")] + \
+        [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride", "g_stride", "w_stride")] + \
+        [("scale", ctypes.c_float)]
+
+
+class RopeDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "batch", "n_tokens", "num_q_heads", "num_k_heads", "head_dim", "rot_dim", "interleaved",
+        "num_slots", "act_dtype")]
+
+
 _lib = None
 _VP = ctypes.c_void_p
 _I = ctypes.c_int
@@ -92,9 +112,15 @@ def _declare(L):
     gd = ctypes.POINTER(GDNDims)
     ad = ctypes.POINTER(AttnDims)
     ac = ctypes.POINTER(AttnCache)
+    ld, li = ctypes.POINTER(LinattnDims), ctypes.POINTER(LinattnInputs)
     i64 = ctypes.c_int64
     f32 = ctypes.c_float
     sig = {
+        "rssm_linattn_workspace_size": (_SZ, [ld, _I32]),
+        "rssm_linattn_prompt": (_I, [ld, li, _I32, _VP, _VP, _VP, _VP, _VP, _SZ, _VP, _VP, _VP]),
+        "rssm_linattn_step": (_I, [ld, li, _VP, _VP, _VP, _VP, _VP]),
+        "rssm_rope": (_I, [ctypes.POINTER(RopeDims), _VP, f32, _VP, _VP, _VP, _VP, _VP, i64, _VP, i64,
+                           _VP, i64, _VP, i64, _VP, _VP]),
         "rssm_status_string": (ctypes.c_char_p, [_I]),
         "rssm_abi_version": (_I, []),
         "rssm_advance_cursors": (_I, [_I, _VP, _VP, _VP, _VP, _VP, _VP, _I32, _I32, _I32, _I32,
@@ -588,3 +614,36 @@ def rssm_attn_advance(dims, cache, cu_tokens, num_accepted, cache_indices, dev_e
 def rssm_add_rmsnorm(dims, x, residual, weight, eps, residual_out, y, y_scale=None, stream=None):
     _call("rssm_add_rmsnorm", ctypes.byref(dims), _ptr(x), _ptr(residual), _ptr(weight), eps,
           _ptr(residual_out), _ptr(y), _ptr(y_scale), _stream(stream))
+
+
+def linattn_inputs(q, k, v, g, w=None, scale=1.0, q_stride=None, k_stride=None, v_stride=None,
+                   g_stride=None, w_stride=None):
+    """The rssm_linattn_inputs of these tensors (they must stay alive while it is used). Strides in
+    elements between tokens; None: dense [tokens][heads][dim] blocks, and of g [H] 0."""
+    def of(t, s):
+        return 0 if t is None or t.dim() == 1 else t.stride(0) if s is None else s
+    return LinattnInputs(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(w), of(q, q_stride), of(k, k_stride),
+                         of(v, v_stride), of(g, g_stride), of(w, w_stride), scale)
+
+
+def rssm_linattn_workspace_size(dims, n_tokens):
+    return lib().rssm_linattn_workspace_size(ctypes.byref(dims), n_tokens)
+
+
+def rssm_linattn_prompt(dims, inputs, n_tokens, cu_tokens, resume, state, cache_indices, workspace,
+                        workspace_bytes, o, dev_err=None, stream=None):
+    _call("rssm_linattn_prompt", ctypes.byref(dims), ctypes.byref(inputs), n_tokens,
+          _ptr(cu_tokens), _ptr(resume), _ptr(state), _ptr(cache_indices), _ptr(workspace),
+          workspace_bytes, _ptr(o), _ptr(dev_err), _stream(stream))
+
+
+def rssm_linattn_step(dims, inputs, state, cache_indices, o, dev_err=None, stream=None):
+    _call("rssm_linattn_step", ctypes.byref(dims), ctypes.byref(inputs), _ptr(state),
+          _ptr(cache_indices), _ptr(o), _ptr(dev_err), _stream(stream))
+
+
+def rssm_rope(dims, freq, mscale, positions, cache_indices, slot_len, cu_tokens, q, q_stride, k,
+              k_stride, q_out, q_out_stride, k_out, k_out_stride, dev_err=None, stream=None):
+    _call("rssm_rope", ctypes.byref(dims), _ptr(freq), mscale, _ptr(positions),
+          _ptr(cache_indices), _ptr(slot_len), _ptr(cu_tokens), _ptr(q), q_stride, _ptr(k), k_stride,
+          _ptr(q_out), q_out_stride, _ptr(k_out), k_out_stride, _ptr(dev_err), _stream(stream))

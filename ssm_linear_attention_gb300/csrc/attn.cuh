@@ -48,13 +48,13 @@ __device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol
 // row; level or worse for the norm and large moves, whose own CTAs want the room).
 __device__ __forceinline__ void let_next_in() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 template <class... P, class... A>
-inline void launch_early(void (*kernel)(P...), int grid, int block, size_t smem, cudaStream_t st, const A&... args) {
+inline void launch_early(void (*kernel)(P...), int grid, dim3 block, size_t smem, cudaStream_t st, const A&... args) {
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t c{};
     c.gridDim = dim3(grid);
-    c.blockDim = dim3(block);
+    c.blockDim = block;
     c.dynamicSmemBytes = smem;
     c.stream = st;
     c.attrs = at;

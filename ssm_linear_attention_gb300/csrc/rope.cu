@@ -1,0 +1,229 @@
+// rope.cu -- rotary positions of queries and keys.
+//
+//   (x, y) -> m (x cos a - y sin a, y cos a + x sin a),   a = 2 pi pos f
+//
+// f is kept in turns per position as a 64-bit binary fraction, so that the product pos f modulo
+// one turn is an integer multiplication that drops the whole turns exactly, for any int32 position: no
+// table of cosines, no limit of length, and no loss at far positions (a float32 angle at position
+// 10^6 is off by up to 0.03). Its top 32 bits, as half turns, go to sincospif.
+//
+// Bytes bound it: a thread keeps the cosines and sines of its pairs and takes them through several
+// heads of a token (one head where tokens are few and latency counts).
+#include "attn.cuh"
+
+namespace rssm {
+namespace rope {
+
+struct Args {
+    const uint64_t* freq;
+    const int32_t* pos;
+    const int32_t* slots;
+    const int32_t* len;
+    const int32_t* cu;
+    const char* q;
+    const char* k;
+    char* q_out;
+    char* k_out;
+    long q_stride, k_stride, qo_stride, ko_stride;
+    int32_t* dev_err;
+    float m;
+    int batch, tokens, each, hq, hk, D, R, num_slots;
+    int units;  // threads of a head: pairs W at a time, then copied values
+    int hg, hpt;  // heads: hg groups of threads a token, hpt heads of each
+    bool q_in, k_in;  // in place: values past R stay
+};
+
+template <bool BF, int W>
+struct Vec {
+    float f[W];
+    __device__ __forceinline__ void load(const char* base, long i) {
+        if constexpr (W % 8 == 0) {
+#pragma unroll
+            for (int e = 0; e < W; e += 8) load8(base + (i + e) * (BF ? 2 : 4), BF, f + e);
+        } else if constexpr (W == 4) {
+            load4(base + i * (BF ? 2 : 4), 0, BF, f);
+        } else {
+#pragma unroll
+            for (int e = 0; e < W; ++e) f[e] = load1(base, i + e, BF);
+        }
+    }
+    __device__ __forceinline__ void store(char* base, long i) const {
+        if constexpr (W % 8 == 0) {
+#pragma unroll
+            for (int e = 0; e < W; e += 8) store8(base + (i + e) * (BF ? 2 : 4), BF, f + e);
+        } else if constexpr (W == 4) {
+            if (BF) *reinterpret_cast<uint2*>(base + i * 2) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+            else *reinterpret_cast<float4*>(base + i * 4) = make_float4(f[0], f[1], f[2], f[3]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < W; ++e) store1(base, i + e, BF, f[e]);
+        }
+    }
+};
+
+// Token i's position; false when it is left alone.
+__device__ __forceinline__ bool position(const Args& a, int i, bool report, int& pos) {
+    if (a.pos) {
+        pos = a.pos[i];
+        return true;
+    }
+    int b, first;
+    if (a.cu) {
+        // the last row that begins at or before i
+        int lo = 0, hi = a.batch;  // cu[lo] <= i < cu[hi] where the list is in order
+        if (i < a.cu[0] || i >= a.cu[a.batch]) return false;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (a.cu[mid] <= i) lo = mid;
+            else hi = mid;
+        }
+        b = lo;
+        first = a.cu[lo];
+    } else {
+        b = i / a.each;
+        first = b * a.each;
+    }
+    const int s = a.slots[b];
+    if (s < 0) return false;
+    if (s >= a.num_slots) {
+        if (report) set_dev_err(a.dev_err, RSSM_DEVERR_SLOT);
+        return false;
+    }
+    pos = (int)((uint32_t)a.len[s] + (uint32_t)(i - first));
+    return true;
+}
+
+// W values of a piece. HALF: a thread has W pairs (c, c + R / 2); else W / 2 pairs of neighbours.
+template <bool BF, int W, bool HALF>
+__global__ void __launch_bounds__(512) rope_kernel(const Args a) {
+    constexpr int PAIRS = HALF ? W : W / 2;
+    attn::wait_for_stream();
+    const unsigned group = blockIdx.x * blockDim.y + threadIdx.y;
+    const int i = group / a.hg, h0 = group % a.hg, u = threadIdx.x;
+    if (i >= a.tokens) return;
+    int pos;
+    if (!position(a, i, u == 0 && h0 == 0, pos)) return;
+    const int turning = a.R / 2 / PAIRS;  // units that rotate; those after them copy
+    const int heads = a.hq + a.hk;
+    if (u >= turning) {
+        const int c = a.R + (u - turning) * W;
+        for (int h = h0; h < heads; h += a.hg) {
+            const bool k = h >= a.hq;
+            if (k ? a.k_in : a.q_in) continue;
+            const int hh = k ? h - a.hq : h;
+            Vec<BF, W> x;
+            x.load(k ? a.k : a.q, (k ? i * a.k_stride : i * a.q_stride) + (long)hh * a.D + c);
+            x.store(k ? a.k_out : a.q_out, (k ? i * a.ko_stride : i * a.qo_stride) + (long)hh * a.D + c);
+        }
+        return;
+    }
+    float co[PAIRS], si[PAIRS];
+#pragma unroll
+    for (int e = 0; e < PAIRS; ++e) {
+        const uint64_t turns = (uint64_t)(int64_t)pos * a.freq[u * PAIRS + e];
+        sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &si[e], &co[e]);
+        co[e] *= a.m;
+        si[e] *= a.m;
+    }
+    const int c = u * W, c2 = c + a.R / 2;
+#pragma unroll 2
+    for (int h = h0; h < heads; h += a.hg) {
+        const bool k = h >= a.hq;
+        const int hh = k ? h - a.hq : h;
+        const char* from = k ? a.k : a.q;
+        char* to = k ? a.k_out : a.q_out;
+        const long at = (k ? i * a.k_stride : i * a.q_stride) + (long)hh * a.D;
+        const long into = (k ? i * a.ko_stride : i * a.qo_stride) + (long)hh * a.D;
+        if constexpr (HALF) {
+            Vec<BF, W> x, y, v, z;
+            x.load(from, at + c);
+            y.load(from, at + c2);
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                v.f[e] = x.f[e] * co[e] - y.f[e] * si[e];
+                z.f[e] = y.f[e] * co[e] + x.f[e] * si[e];
+            }
+            v.store(to, into + c);
+            z.store(to, into + c2);
+        } else {
+            Vec<BF, W> x, v;
+            x.load(from, at + c);
+#pragma unroll
+            for (int e = 0; e < PAIRS; ++e) {
+                v.f[2 * e] = x.f[2 * e] * co[e] - x.f[2 * e + 1] * si[e];
+                v.f[2 * e + 1] = x.f[2 * e + 1] * co[e] + x.f[2 * e] * si[e];
+            }
+            v.store(to, into + c);
+        }
+    }
+}
+
+template <bool BF, int W, bool HALF>
+static int launch(Args a, const DeviceInfo& di, cudaStream_t st) {
+    constexpr int PAIRS = HALF ? W : W / 2;
+    a.units = a.R / 2 / PAIRS + (a.q_in && a.k_in ? 0 : (a.D - a.R) / W);
+    const int heads = a.hq + a.hk;
+    // one head a thread until the GPU is full several times over, then up to five
+    const long threads = (long)a.tokens * heads * a.units;
+    const long full = (long)di.sm_count * 2048 * 4;
+    a.hpt = (int)min(5L, 1 + threads / full);
+    a.hg = (heads + a.hpt - 1) / a.hpt;
+    const int y = max(1, 256 / a.units);
+    const long groups = (long)a.tokens * a.hg;
+    attn::launch_early(rope_kernel<BF, W, HALF>, (int)((groups + y - 1) / y), dim3(a.units, y), 0, st, a);
+    return launch_status();
+}
+
+template <bool BF>
+static int launch_all(const Args& a, bool interleaved, const DeviceInfo& di, cudaStream_t st) {
+    // the widest pieces that divide what is rotated (and with it what is copied)
+    if (interleaved) return a.R % 8 == 0 ? launch<BF, 8, false>(a, di, st) : launch<BF, 2, false>(a, di, st);
+    return a.R % 16 == 0 ? launch<BF, 8, true>(a, di, st)
+           : a.R % 8 == 0 ? launch<BF, 4, true>(a, di, st)
+                          : launch<BF, 1, true>(a, di, st);
+}
+
+}  // namespace rope
+}  // namespace rssm
+
+using namespace rssm;
+
+extern "C" int rssm_rope(const rssm_rope_dims* d, const uint64_t* freq, float mscale, const int32_t* positions,
+                         const int32_t* cache_indices, const int32_t* slot_len, const int32_t* cu_tokens, const void* q,
+                         int64_t q_stride, const void* k, int64_t k_stride, void* q_out, int64_t q_out_stride,
+                         void* k_out, int64_t k_out_stride, int32_t* dev_err, rssm_stream_t stream) {
+    if (!d || d->n_tokens < 0 || d->num_q_heads < 1 || d->num_k_heads < 0 || d->head_dim < 1 || !ok_dtype(d->act_dtype))
+        return RSSM_ERR_INVALID_ARG;
+    if (!positions && (d->batch < 0 || d->num_slots < 1)) return RSSM_ERR_INVALID_ARG;
+    if (d->head_dim % 8 || d->head_dim > 512) return RSSM_ERR_UNSUPPORTED;
+    const int most = d->num_q_heads > d->num_k_heads ? d->num_q_heads : d->num_k_heads;
+    if ((int64_t)d->n_tokens * most >= (1 << 30)) return RSSM_ERR_UNSUPPORTED;
+    if (d->rot_dim < 2 || d->rot_dim > d->head_dim || d->rot_dim % 2) return RSSM_ERR_CONFIG;
+    if (!positions && !cu_tokens && d->batch && d->n_tokens % d->batch) return RSSM_ERR_CONFIG;
+    if (d->n_tokens == 0 || (!positions && d->batch == 0)) return RSSM_OK;
+    auto ok = [&](int heads, const void* x, int64_t xs, const void* y, int64_t ys) {
+        if (heads == 0) return true;
+        const int64_t w = (int64_t)heads * d->head_dim, top = (int64_t)1 << 36;
+        return ok_ptr(x) && ok_ptr(y) && xs >= w && xs % 8 == 0 && ys >= w && ys % 8 == 0 && xs < top && ys < top &&
+               (x != y || xs == ys);
+    };
+    if (!ok_ptr(freq) || !ok(d->num_q_heads, q, q_stride, q_out, q_out_stride) ||
+        !ok(d->num_k_heads, k, k_stride, k_out, k_out_stride))
+        return RSSM_ERR_INVALID_ARG;
+    if (positions ? !ok_ptr(positions) : !ok_ptr(cache_indices) || !ok_ptr(slot_len) || !ok_opt_ptr(cu_tokens))
+        return RSSM_ERR_INVALID_ARG;
+    DeviceInfo di;
+    if (!device_info(&di)) return RSSM_ERR_CUDA;
+    rope::Args a{};
+    a.freq = freq; a.pos = positions; a.slots = cache_indices; a.len = slot_len; a.cu = cu_tokens;
+    a.q = static_cast<const char*>(q); a.k = static_cast<const char*>(k);
+    a.q_out = static_cast<char*>(q_out); a.k_out = static_cast<char*>(k_out);
+    a.q_stride = q_stride; a.k_stride = k_stride; a.qo_stride = q_out_stride; a.ko_stride = k_out_stride;
+    a.dev_err = dev_err; a.m = mscale;
+    a.batch = d->batch; a.tokens = d->n_tokens; a.each = positions || d->batch == 0 ? 1 : d->n_tokens / d->batch;
+    a.hq = d->num_q_heads; a.hk = d->num_k_heads; a.D = d->head_dim; a.R = d->rot_dim; a.num_slots = d->num_slots;
+    a.q_in = q == q_out; a.k_in = a.hk == 0 || k == k_out;
+    const cudaStream_t st = (cudaStream_t)stream;
+    return d->act_dtype == RSSM_BF16 ? rope::launch_all<true>(a, d->interleaved != 0, di, st)
+                                     : rope::launch_all<false>(a, d->interleaved != 0, di, st);
+}

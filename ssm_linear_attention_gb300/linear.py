@@ -1,0 +1,308 @@
+"""Runners for linear attention with a decay for each head, and for rotary positions.
+
+As the runners in hybrid.py, each owns the device buffers of one layer (or uses tensors that the
+caller hands in), and no call synchronises, so calls can be captured in a CUDA graph:
+
+  linear attention:  rssm_linattn_prompt (a list of tokens), rssm_linattn_step (one token of each row)
+  positions:         rssm_rope, before a layer's queries and keys are used
+"""
+import ctypes
+import fractions
+import math
+
+import torch
+
+from . import _binding as B
+from .decoder import torch_dtype_code
+from .hybrid import _check, _check_list, _check_out, _device, _Fixed, _index
+
+__all__ = ["LinearAttention", "Rotary"]
+
+
+def _on_current(index):
+    """The calls launch on the current device: a runner of another one is refused."""
+    if index < 0 or index != torch.cuda.current_device():
+        raise ValueError("the runner's device is not the current one")
+
+
+def _blocks(name, t, heads, dim, dtype, index):
+    """Token count and element distance between consecutive tokens of t [tokens, heads, dim] (or
+    [rows, T, heads, dim])."""
+    if t.dtype is not dtype or t.get_device() != index or t.dim() not in (3, 4) or \
+            t.shape[-2] != heads or t.shape[-1] != dim:
+        raise ValueError("%s: %s tokens of [%d, %d] on the runner's device are wanted"
+                         % (name, dtype, heads, dim))
+    n = t.numel() // (heads * dim)
+    if t.is_contiguous():
+        return n, heads * dim
+    s, m = t.stride(), t.shape
+    if s[-1] != 1 or (s[-2] != dim and heads > 1) or \
+            (len(m) == 4 and m[0] > 1 and m[1] > 1 and s[0] != m[1] * s[1]):
+        raise ValueError("%s: dense [%d, %d] blocks, evenly spaced, are wanted" % (name, heads, dim))
+    if n <= 1:
+        return n, heads * dim
+    return n, s[0] if len(m) == 3 or m[1] == 1 else s[1]
+
+
+class LinearAttention(_Fixed):
+    """Linear attention with a decay for each head, for one layer:
+    S <- exp(g) S + w v k^T, o = scale S q, S [value_dim, key_dim] for each of num_heads heads;
+    query and key head h / (num_heads / num_k_heads).
+
+    Buffers: state [num_slots, H, P, N] (state_dtype; or the caller's, e.g. a Mamba2 decoder's),
+    o for up to max_tokens tokens and a workspace for as many. Slots are not cleared when they
+    are given to another row: prompt() begins from zero unless told to resume. scale may be set
+    between calls."""
+
+    _free = ("scale",)
+
+    def __init__(self, num_heads, num_k_heads, key_dim, value_dim, num_slots, max_batch,
+                 max_tokens=None, scale=None, state_dtype=torch.float32, act_dtype=torch.bfloat16,
+                 out_dtype=torch.bfloat16, device=None, state=None):
+        dev = _device(device)
+        self.H, self.G, self.N, self.P = num_heads, num_k_heads, key_dim, value_dim
+        self.num_slots, self.max_batch = num_slots, max_batch
+        self.max_tokens = max_batch if max_tokens is None else max(max_tokens, max_batch)
+        self.scale = key_dim ** -0.5 if scale is None else scale
+        self.state_dtype, self.act_dtype, self.out_dtype = state_dtype, act_dtype, out_dtype
+        self.device = dev
+        shape = (num_slots, num_heads, value_dim, key_dim)
+        self.state = torch.zeros(shape, device=dev, dtype=state_dtype) if state is None else \
+            _check("state", state, shape, state_dtype, dev)
+        self.o = torch.empty(self.max_tokens, num_heads, value_dim, device=dev, dtype=out_dtype)
+        self.dev_err = torch.zeros(4, device=dev, dtype=torch.int32)
+        self.ws_bytes = B.rssm_linattn_workspace_size(self.dims(max_batch), self.max_tokens)
+        self.workspace = torch.empty(max(self.ws_bytes, 16), device=dev, dtype=torch.uint8)
+        self._prompt, self._step = B.entry("rssm_linattn_prompt"), B.entry("rssm_linattn_step")
+        self._addr = (self.state.data_ptr(), self.workspace.data_ptr(), self.dev_err.data_ptr(), self.o.data_ptr())
+        self._index = _index(self.state.device)
+        self._plans = {}
+
+    def dims(self, batch):
+        return B.LinattnDims(batch, self.H, self.G, self.N, self.P, self.num_slots,
+                             torch_dtype_code(self.state_dtype), torch_dtype_code(self.act_dtype),
+                             torch_dtype_code(self.out_dtype))
+
+    def _rows(self, cache_indices):
+        if cache_indices.dtype is not torch.int32 or not cache_indices.is_contiguous() or \
+                cache_indices.get_device() != self._index or cache_indices.dim() != 1:
+            raise ValueError("cache_indices must be a dense int32 list on the runner's device")
+        _on_current(self._index)
+        b = cache_indices.shape[0]
+        if b > self.max_batch:
+            raise ValueError("%d rows: the runner is made for %d" % (b, self.max_batch))
+        d = self._plans.get(b)
+        if d is None:
+            d = self._plans[b] = ctypes.byref(self.dims(b))
+        return b, d
+
+    def _gate(self, name, t, n):
+        """Token stride of the factors t [n, H] (0 for the constants [H])."""
+        if t.dtype is not torch.float32 or t.get_device() != self._index or t.shape[-1] != self.H or \
+                t.numel() not in (self.H, n * self.H) or (t.dim() == 1 and name == "w"):
+            raise ValueError("%s must be float32 [%d, %d]%s on the runner's device"
+                             % (name, n, self.H, "" if name == "w" else " or [%d]" % self.H))
+        if t.dim() == 1:
+            if t.stride(0) != 1 and self.H > 1:
+                raise ValueError("%s must be dense" % name)
+            return 0
+        if t.numel() != n * self.H:
+            raise ValueError("%s must be float32 [%d, %d]" % (name, n, self.H))
+        if t.is_contiguous() or n <= 1 and (t.stride(-1) == 1 or self.H == 1):
+            return self.H
+        if t.dim() != 2 or (t.stride(1) != 1 and self.H > 1) or t.stride(0) < self.H:
+            raise ValueError("%s: dense rows, evenly spaced, are wanted" % name)
+        return t.stride(0)
+
+    def _inputs(self, q, k, v, g, w):
+        i = self._index
+        n, qs = _blocks("q", q, self.G, self.N, self.act_dtype, i)
+        nk, ks = _blocks("k", k, self.G, self.N, self.act_dtype, i)
+        nv, vs = _blocks("v", v, self.H, self.P, self.act_dtype, i)
+        if nk != n or nv != n:
+            raise ValueError("q, k and v must hold the same tokens")
+        gs = self._gate("g", g, n)
+        ws = 0 if w is None else self._gate("w", w, n)
+        return n, B.LinattnInputs(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+                                  None if w is None else w.data_ptr(), qs, ks, vs, gs, ws, self.scale)
+
+    def _out(self, o, n):
+        if o is not None:
+            return o, _check_out("o", o, n * self.H * self.P, self.out_dtype, self._index)
+        if n > self.max_tokens:
+            raise ValueError("%d tokens: the runner is made for %d" % (n, self.max_tokens))
+        return self.o[:n], self._addr[3]
+
+    def prompt(self, q, k, v, g, cache_indices, cu_tokens=None, w=None, resume=None, o=None, stream=None):
+        """Tokens q, k [n, G, N], v [n, H, P] with decays g [n, H] (or [H]) and factors w [n, H]
+        through the rows' states; cu_tokens [b + 1] int32 (None: n / b tokens a row). resume [b]
+        uint8 or bool: rows that go on from their slot's state (None: every row begins from
+        zero; True: none does). Returns o [n, H, P]."""
+        b, dims = self._rows(cache_indices)
+        n, inputs = self._inputs(q, k, v, g, w)
+        if n > self.max_tokens:
+            raise ValueError("%d tokens: the runner is made for %d" % (n, self.max_tokens))
+        if cu_tokens is None and (n % b if b else n):
+            raise ValueError("%d tokens of %d rows: cu_tokens is wanted" % (n, b))
+        o, o_ptr = self._out(o, n)
+        if resume is True:
+            resume = torch.ones(b, device=self.device, dtype=torch.uint8)
+        elif resume is False:
+            resume = None
+        if resume is not None and (resume.dtype not in (torch.uint8, torch.bool) or resume.shape != (b,) or
+                                   not resume.is_contiguous() or resume.get_device() != self._index):
+            raise ValueError("resume must be a dense uint8 or bool list of %d on the runner's device" % b)
+        state, ws, err, _ = self._addr
+        rc = self._prompt(dims, ctypes.byref(inputs), n, _check_list("cu_tokens", cu_tokens, b + 1, self._index),
+                          None if resume is None else resume.data_ptr(), state, cache_indices.data_ptr(), ws,
+                          self.ws_bytes, o_ptr, err, B._stream(stream))
+        if rc:
+            raise B.RSSMError("rssm_linattn_prompt", rc)
+        return o
+
+    def step(self, q, k, v, g, cache_indices, w=None, o=None, stream=None):
+        """One token of each row: q, k [b, G, N], v [b, H, P], g [b, H] (or [H]), w [b, H]. Padding
+        rows: cache index -1. Returns o [b, H, P]."""
+        b, dims = self._rows(cache_indices)
+        n, inputs = self._inputs(q, k, v, g, w)
+        if n != b:
+            raise ValueError("a step takes one token of each row: %d tokens, %d rows" % (n, b))
+        o, o_ptr = self._out(o, n)
+        rc = self._step(dims, ctypes.byref(inputs), self._addr[0], cache_indices.data_ptr(), o_ptr, self._addr[2],
+                        B._stream(stream))
+        if rc:
+            raise B.RSSMError("rssm_linattn_step", rc)
+        return o
+
+
+def rotary_frequencies(rot_dim, base=10000.0, scaling=None):
+    """Angles per position of the rot_dim / 2 pairs (a list of floats) and the factor of the rotated
+    values: base^(-2 i / rot_dim), stretched for long contexts by scaling, a dict with "type" and
+    "factor":
+      linear  every frequency divided by the factor
+      base    the base multiplied by factor^(rot_dim / (rot_dim - 2)), so that the slowest pair is stretched
+              by the factor and the fastest keeps its frequency
+      yarn    pairs that turn more than "fast" (32) times over "original" positions keep their
+              frequency, those that turn less than "slow" (1) times are divided by the factor, a
+              ramp over the pairs between; values times 0.1 log(factor) + 1 ("mscale")
+      bands   the same by wavelength: from "fast" (4) turns kept, up to "slow" (1) divided, linear in the
+              turns between
+    """
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError("rot_dim must be even")
+    s = dict(scaling or {})
+    kind, factor = s.pop("type", "none"), float(s.pop("factor", 1.0))
+    if kind not in ("none", "linear", "base", "yarn", "bands") or not factor > 0 or not base > 0:
+        raise ValueError("scaling: a type of none, linear, base, yarn, bands, a positive factor and base")
+    original = float(s.pop("original", 0) or 0)
+    fast, slow = float(s.pop("fast", 32 if kind == "yarn" else 4)), float(s.pop("slow", 1))
+    mscale = float(s.pop("mscale", 0.1 * math.log(factor) + 1 if kind == "yarn" else 1.0))
+    if s:
+        raise ValueError("scaling: unknown %s" % ", ".join(sorted(s)))
+    if kind in ("yarn", "bands") and not (original > 0 and fast > slow > 0):
+        raise ValueError("scaling: %s wants original > 0 and fast > slow > 0" % kind)
+    if kind == "yarn" and base == 1:
+        raise ValueError("scaling: yarn wants a base other than 1")
+    if kind == "base" and rot_dim > 2:
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    freq = [base ** (-2 * i / rot_dim) for i in range(rot_dim // 2)]
+    if kind == "linear":
+        freq = [f / factor for f in freq]
+    elif kind == "yarn":
+        lo, hi = (rot_dim * math.log(original / (2 * math.pi * t)) / (2 * math.log(base)) for t in (fast, slow))
+        lo, hi = max(math.floor(lo), 0), min(math.ceil(hi), rot_dim - 1)
+        ramp = [min(max((i - lo) / max(hi - lo, 0.001), 0.0), 1.0) for i in range(rot_dim // 2)]
+        freq = [f * (1 - r) + f / factor * r for f, r in zip(freq, ramp)]
+    elif kind == "bands":
+        turns = [original * f / (2 * math.pi) for f in freq]
+        keep = [min(max((t - slow) / (fast - slow), 0.0), 1.0) for t in turns]
+        freq = [f * r + f / factor * (1 - r) for f, r in zip(freq, keep)]
+    return freq, mscale
+
+
+class Rotary(_Fixed):
+    """Rotary positions of queries [n, num_q_heads, head_dim] and keys [n, num_k_heads, head_dim]: the first
+    rot_dim (None: all) values of each head, as pairs (i, i + rot_dim / 2) or, interleaved, (2 i, 2 i + 1).
+    base and scaling as rotary_frequencies(); frequencies, angles per position of the pairs, in their place, with mscale.
+    Any int32 position is exact; there is no table to outgrow. One Rotary serves a model's layers."""
+
+    def __init__(self, num_q_heads, num_k_heads, head_dim, rot_dim=None, interleaved=False, base=10000.0,
+                 scaling=None, act_dtype=torch.bfloat16, device=None, frequencies=None, mscale=1.0):
+        dev = _device(device)
+        self.HQ, self.HK, self.D = num_q_heads, num_k_heads, head_dim
+        self.R = head_dim if rot_dim is None else rot_dim
+        self.interleaved, self.act_dtype, self.device = bool(interleaved), act_dtype, dev
+        if frequencies is None:
+            frequencies, mscale = rotary_frequencies(self.R, base, scaling)
+        frequencies = [float(f) for f in frequencies]
+        if 2 * len(frequencies) != self.R or not all(math.isfinite(f) for f in frequencies):
+            raise ValueError("%d finite frequencies are wanted" % (self.R // 2))
+        self.frequencies, self.mscale = frequencies, float(mscale)
+        # turns per position as 64-bit fractions (of a turn: whole turns per position drop out)
+        two_pi = fractions.Fraction("6.283185307179586476925286766559005768")
+        turns = [round(fractions.Fraction(f) / two_pi * 2 ** 64) % 2 ** 64 for f in frequencies]
+        self.freq = torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns], dtype=torch.int64).to(dev)
+        self.dev_err = torch.zeros(4, device=dev, dtype=torch.int32)
+        self._call = B.entry("rssm_rope")
+        self._index = _index(self.freq.device)
+        self._plans = {}
+
+    def dims(self, batch, n_tokens, num_slots):
+        return B.RopeDims(batch, n_tokens, self.HQ, self.HK, self.D, self.R, self.interleaved, num_slots,
+                          torch_dtype_code(self.act_dtype))
+
+    def _list(self, name, t, count=None):
+        if t.dtype is not torch.int32 or not t.is_contiguous() or t.get_device() != self._index or \
+                (count is not None and t.numel() != count):
+            raise ValueError("%s must be a dense int32 list%s on the runner's device"
+                             % (name, "" if count is None else " of %d" % count))
+        return t.data_ptr()
+
+    def __call__(self, q, k=None, positions=None, cache_indices=None, slot_len=None, cu_tokens=None, q_out=None,
+                 k_out=None, stream=None):
+        """Rotates q and k (k None for num_k_heads 0) at positions [n] int32, or where rssm_attn_append puts
+        the tokens: row b's from slot_len[cache_indices[b]] on, rows of cu_tokens [b + 1] (None: n / b tokens each). In
+        place unless q_out, k_out are given. Slices of a fused projection need no copy. Returns (q, k)
+        as rotated."""
+        _on_current(self._index)
+        n, qs = _blocks("q", q, self.HQ, self.D, self.act_dtype, self._index)
+        q_out = q if q_out is None else q_out
+        no, qos = _blocks("q_out", q_out, self.HQ, self.D, self.act_dtype, self._index)
+        ks = kos = 0
+        nk = nko = n
+        if self.HK:
+            if k is None:
+                raise ValueError("k is wanted")
+            nk, ks = _blocks("k", k, self.HK, self.D, self.act_dtype, self._index)
+            k_out = k if k_out is None else k_out
+            nko, kos = _blocks("k_out", k_out, self.HK, self.D, self.act_dtype, self._index)
+        elif k is not None or k_out is not None:
+            raise ValueError("the runner has no key heads")
+        if not n == no == nk == nko:
+            raise ValueError("q, k and the outputs must hold the same tokens")
+        if (positions is None) == (cache_indices is None) or (cache_indices is None) != (slot_len is None) or \
+                (positions is not None and cu_tokens is not None):
+            raise ValueError("positions, or cache_indices and slot_len (and cu_tokens), are wanted")
+        pos = rows = lens = cu = None
+        b = slots = 0
+        if positions is not None:
+            pos = self._list("positions", positions, n)
+        else:
+            b, slots = cache_indices.numel(), slot_len.numel()
+            rows, lens = self._list("cache_indices", cache_indices), self._list("slot_len", slot_len)
+            if cu_tokens is not None:
+                cu = self._list("cu_tokens", cu_tokens, b + 1)
+            elif n % b if b else n:
+                raise ValueError("%d tokens of %d rows: cu_tokens is wanted" % (n, b))
+        key = (b, n, slots)
+        dims = self._plans.get(key)
+        if dims is None:
+            if len(self._plans) >= 256:  # prompts come in any number of tokens
+                self._plans.clear()
+            dims = self._plans[key] = ctypes.byref(self.dims(b, n, slots))
+        rc = self._call(dims, self.freq.data_ptr(), self.mscale, pos, rows, lens, cu, q.data_ptr(), qs,
+                        k.data_ptr() if self.HK else None, ks, q_out.data_ptr(), qos,
+                        k_out.data_ptr() if self.HK else None, kos, self.dev_err.data_ptr(), B._stream(stream))
+        if rc:
+            raise B.RSSMError("rssm_rope", rc)
+        return q_out, k_out
