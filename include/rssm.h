@@ -879,7 +879,7 @@ size_t rssm_linattn_workspace_size(const rssm_linattn_dims* dims, int32_t n_toke
  *     leaves its slot as it is.
  *   o [n_tokens][H][P] out_dtype.
  * A row whose part of cu_tokens decreases or leaves [0, n_tokens] is skipped and sets
- * RSSM_DEVERR_CURSOR. With bf16 activations a chunk of 64 tokens at a time on the tensor
+ * RSSM_DEVERR_CURSOR; which rows beside it in such a list are taken is not defined. With bf16 activations a chunk of 64 tokens at a time on the tensor
  * cores: products of bf16 values are exact, sums and states float32, and where a weight, a
  * state or a decayed value enters a product it has 16 bits. An infinity or a NaN in v (k, g, w)
  * reaches its head's outputs and state of that value row (all value rows) from its token on, as an

@@ -115,7 +115,7 @@ EncodeTiledFn g_encode = nullptr;
 }  // namespace
 
 bool make_tmap_rows128(CUtensorMap* out, const void* base, int elem_bytes, uint64_t rows,
-                       uint64_t cols, uint32_t box_rows) {
+                       uint64_t cols, uint32_t box_rows, uint64_t row_elems) {
     std::call_once(g_encode_once, []() {
         void* f = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -128,7 +128,7 @@ bool make_tmap_rows128(CUtensorMap* out, const void* base, int elem_bytes, uint6
     });
     if (!g_encode || (elem_bytes != 2 && elem_bytes != 4)) return false;
     const cuuint64_t dims[2] = {cols, rows};
-    const cuuint64_t strides[1] = {cols * (cuuint64_t)elem_bytes};
+    const cuuint64_t strides[1] = {(row_elems ? row_elems : cols) * (cuuint64_t)elem_bytes};
     const cuuint32_t box[2] = {(cuuint32_t)(128 / elem_bytes), box_rows};
     const cuuint32_t estr[2] = {1, 1};
     const CUresult r = g_encode(out, elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16

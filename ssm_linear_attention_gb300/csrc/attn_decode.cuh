@@ -5,6 +5,7 @@
 #include <cuda_fp16.h>
 
 #include "attn.cuh"
+#include "warps.cuh"
 
 namespace rssm {
 namespace attn {
@@ -56,11 +57,6 @@ struct DecArgs {
     int stall;         // test: the tile (many queries: chunk) of the list whose wait runs out; -1: none
 };
 
-__device__ __forceinline__ float exp2_fast(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ float log2_fast(float x) {
     float y;
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -72,13 +68,6 @@ __device__ __forceinline__ float reciprocal(float x) {
     float y;
     asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
-}
-
-// True on one lane of the (whole) warp.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
-    return ok != 0;
 }
 
 // The four e4m3 codes of w as f16 pairs (exact): lo = codes 0, 1, hi = codes 2, 3.
@@ -133,20 +122,6 @@ __device__ __forceinline__ uint32_t even_cut(const Cuts& r, uint32_t c) {
 __device__ __forceinline__ int cta_of(const Cuts& r, uint32_t t) {
     const uint32_t cut = r.rem * (r.base + 1);
     return (int)(t < cut ? t / (r.base + 1) : r.rem + (t - cut) / r.base);
-}
-
-// The whole warp's bounded wait for phase `parity` of `bar`; false, with the CTA's abort
-// flag set, when it ran out on any lane or another warp had given up.
-static __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                              uint64_t wait_ns, int32_t* dev_err) {
-    const int w = mbar_wait_abortable(bar, parity, wait_ns, abort);
-    if (__all_sync(0xffffffffu, w > 0)) return true;
-    if (w == 0) {
-        set_dev_err(dev_err, RSSM_DEVERR_TIMEOUT);
-        *abort = 1;
-    }
-    __syncwarp();
-    return false;
 }
 
 // Last row b with cum[b] <= i (rows without tiles are passed over).

@@ -169,18 +169,6 @@ __device__ __forceinline__ Seg first_seg(const DecArgs& a, const uint32_t* cum, 
     if (!clip_seg(cum, c0 - s.x.at, c0, c1, s)) next_seg(a, cum, c1, s);
     return s;
 }
-// A ring's slot and the parity of its present use.
-struct Ring {
-    int slot = 0;
-    uint32_t parity = 0;
-    __device__ __forceinline__ void next(int n) {
-        if (++slot == n) {
-            slot = 0;
-            parity ^= 1;
-        }
-    }
-};
-
 template <int D, bool E4M3, int N>
 __global__ void __launch_bounds__((Wide<D, E4M3, N>::THREADS), 1)
     wide_kernel(const __grid_constant__ DecArgs a, const __grid_constant__ CUtensorMap kmap,

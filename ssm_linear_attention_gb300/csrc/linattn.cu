@@ -205,7 +205,8 @@ static int launch_recurrence(const Args& a, int N, int P, cudaStream_t st) {
 using namespace rssm;
 
 extern "C" size_t rssm_linattn_workspace_size(const rssm_linattn_dims* d, int32_t n_tokens) {
-    return 0;
+    if (linattn::check_dims(d) != RSSM_OK || n_tokens < 0 || d->act_dtype != RSSM_BF16) return 0;
+    return linattn::chunk_workspace(d, n_tokens);
 }
 
 extern "C" int rssm_linattn_prompt(const rssm_linattn_dims* d, const rssm_linattn_inputs* in, int32_t n_tokens,
@@ -225,8 +226,12 @@ extern "C" int rssm_linattn_prompt(const rssm_linattn_dims* d, const rssm_linatt
     a.tokens = n_tokens;
     a.each = n_tokens / d->batch;
     const cudaStream_t st = (cudaStream_t)stream;
-    return d->act_dtype == RSSM_BF16 ? linattn::launch_recurrence<true>(a, d->key_dim, d->value_dim, st)
-                                     : linattn::launch_recurrence<false>(a, d->key_dim, d->value_dim, st);
+    if (d->act_dtype == RSSM_BF16) {
+        const size_t need = linattn::chunk_workspace(d, n_tokens);
+        if (need && (!ok_ptr(workspace) || workspace_bytes < need)) return RSSM_ERR_INVALID_ARG;
+        return linattn::prompt_chunks(d, a, workspace, RSSM_WAIT_NS, st);
+    }
+    return linattn::launch_recurrence<false>(a, d->key_dim, d->value_dim, st);
 }
 
 extern "C" int rssm_linattn_step(const rssm_linattn_dims* d, const rssm_linattn_inputs* in, void* state,

@@ -77,5 +77,9 @@ __device__ __forceinline__ bool row_of(const Args& a, int b, bool report, int& b
     return end > begin;
 }
 
+// bf16 activations (linattn_chunk.cu).
+size_t chunk_workspace(const rssm_linattn_dims* d, int n_tokens);
+int prompt_chunks(const rssm_linattn_dims* d, const Args& a, void* workspace, uint64_t wait_ns, cudaStream_t st);
+
 }  // namespace linattn
 }  // namespace rssm

@@ -1,0 +1,1012 @@
+// linattn_chunk.cu -- linear attention over prompts, bf16 activations: chunks of 64 tokens on the tensor cores.
+//
+// Inside a chunk, with G_i the sum of the logarithms of the decays up to token i and S_0 [P][N] the state before it,
+//     o_i = scale (exp(G_i) S_0 q_i + sum_{j<=i} W_ij v_j),   W_ij = exp(G_i - G_j) w_j (q_i . k_j)
+//     S   = exp(G_end) S_0 + sum_j V'_j k_j^T,                V'_j = exp(G_end - G_j) w_j v_j
+// which are four products, all with a row of P (128 values: a head of 128 or two of 64) as the tensor memory's lane:
+//     scores [tokens i][tokens j] = Q K^T                     (lanes: tokens)
+//     inter  [P][tokens] = S_0 Q^T     A = S_0 in the tensor memory, written there from the registers that hold it
+//     intra  [P][tokens] = V^T W^T     A = V, transposed by its descriptor
+//     dS     [P][N]      = V'^T K      A = V', B = K, both transposed by their descriptors
+// The state stays in float32 in the registers of eight warps: a chunk's dS is summed from zero in the tensor memory and
+// added there, S = exp(G_end) S_0 + dS, the decay as a float32 and its remainder (a rounded decay would be wrong in the
+// same direction in every chunk: 2e-6 of a state that remembers 50 chunks). Q, K and V are exact; S_0 and W
+// enter as two bf16 parts (16 bits), V' as two for a bf16 state and three (24 bits) for a float32 one.
+// The logarithms are summed as 64-bit fixed point in units of 2^-40, so that differences of sums are exact.
+//
+// A long row is cut into segments where rows and heads alone do not fill the GPU: one launch makes the
+// segments' own states (dS alone), one carries them on, and the main one begins each segment from its state.
+//
+// One CTA per SM takes units (segment, head or pair of heads). Warps have roles and meet at mbarriers:
+//   0-15 state, 16, 17, 20, 21 weights, 18, 19, 22, 23 decayed values, 24-27 output, 28 loads (TMA) and the list,
+//   29 products, 30 decays.
+// What they issue (some 1600 cycles a chunk of 128 x 128) comes near what the chunk's bytes take, so float32 arithmetic is
+// in pairs (f32x2); and the roles' loops are kept short, since what streams through the instruction cache
+// instead of staying in it waits for it (waits inline and loops unrolled, 133 KB of code: 9000 cycles a chunk).
+#include <cstring>
+
+#include "linattn.cuh"
+#include "umma.cuh"
+#include "warps.cuh"
+
+namespace rssm {
+namespace linattn {
+
+constexpr int kC = 64;             // tokens of a chunk
+constexpr int kBox = kC * 128;     // bytes of 64 columns of a chunk
+constexpr int kGates = 3;          // chunks whose decays are kept
+constexpr int kUnits = 4;          // units looked up ahead
+constexpr int kThreads = 1024;
+constexpr float kFix = 0x1p-40f;   // unit of the summed logarithms
+
+struct ChunkArgs {
+    Args a;
+    float* parts;      // states of the rows' segments [index][H][P][N]
+    float2* part_decay;  // and their decays [index][H]
+    int kept;          // of either; behind them the states that cut rows began with, at first token / seg
+    int seg;           // tokens of a segment, a multiple of 64; 0: rows are not cut
+    int blocks;        // units of a segment: heads, or pairs of them
+    int units;         // upper limit of the rows' segments
+    uint64_t wait_ns;
+};
+
+enum { kZero = 0, kSlot = 1, kPart = 2 };
+// A segment of a row, for one head (or pair).
+struct Unit {
+    int tok, n;     // first token, tokens (-1: the list ends)
+    int head;
+    int slot;
+    int part;       // where its state is kept before (kPart) or after it
+    int from, to;   // kZero / kSlot / kPart
+};
+
+template <int N, int P, bool PAIR, int SP, bool OUT>
+struct Chunk {
+    static_assert(!PAIR || P == 64, "pairs are of 64");
+    static constexpr int VH = PAIR ? 2 : 1;             // heads of a unit
+    static constexpr int VL = P * VH;                   // value lanes in use
+    static constexpr int QB = N / 64 * kBox, VB = VL / 64 * kBox;
+    static constexpr int STAGE = 2 * QB + VB;
+    static constexpr int WB = OUT ? VH * kBox : 0;      // one part of W
+    static constexpr int REST = SP * VB + 2 * WB;
+    static constexpr int ST = REST + 3 * STAGE <= 216 * 1024 ? 3 : 2;
+    static constexpr int SMEM = ST * STAGE + REST + (VL == 64 ? 1024 : 0) + 1024;
+    // tensor memory columns
+    static constexpr uint32_t SCORE = 0, STATE = 64, DS = STATE + N, INTER = DS + N, INTRA = INTER + 64;
+    static constexpr int CONS = (OUT ? 8 : 0) + 4 + 16;  // warps that read the decays
+    static constexpr int UCONS = CONS + 2;              // and the list
+};
+
+// Two float32 in a register pair.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 two(float x, float y) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 one_by_one(f2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack2(f2 v) {
+    const float2 f = one_by_one(v);
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(f.y), "f"(f.x));
+    return r;
+}
+// v's next bf16 part; v becomes the (exact) rest.
+__device__ __forceinline__ uint32_t split2(f2& v) {
+    const uint32_t h = pack2(v);
+    v = fma2(two(bf16_lo(h), bf16_hi(h)), two(-1.f, -1.f), v);
+    return h;
+}
+
+// 2^x as a float32 and its remainder, x in units of 2^-40, to some 2^-30 of itself: a table of 2^(i / 32) and a
+// polynomial of what is left (Tang, "Table-driven implementation of the exponential function", 1989).
+__constant__ float2 kPow2[32] = {
+    {0x1.0000000000000p+0f, 0x0.0p+0f}, {0x1.059b0e0000000p+0f, -0x1.9d4f520000000p-25f}, {0x1.0b55860000000p+0f, 0x1.9f31220000000p-25f}, {0x1.11301e0000000p+0f, -0x1.fdb4960000000p-25f},
+    {0x1.172b840000000p+0f, -0x1.c157420000000p-27f}, {0x1.1d48740000000p+0f, -0x1.d2e8ca0000000p-25f}, {0x1.2387a60000000p+0f, 0x1.ceac480000000p-25f}, {0x1.29e9e00000000p+0f, -0x1.5c04240000000p-25f},
+    {0x1.306fe00000000p+0f, 0x1.4636e20000000p-25f}, {0x1.371a740000000p+0f, -0x1.18aac60000000p-25f}, {0x1.3dea640000000p+0f, 0x1.8246840000000p-25f}, {0x1.44e0860000000p+0f, 0x1.8624b40000000p-30f},
+    {0x1.4bfdae0000000p+0f, -0x1.593abc0000000p-25f}, {0x1.5342b60000000p+0f, -0x1.2c56100000000p-25f}, {0x1.5ab07e0000000p+0f, -0x1.5bd5ec0000000p-27f}, {0x1.6247ec0000000p+0f, -0x1.f8b5500000000p-25f},
+    {0x1.6a09e60000000p+0f, 0x1.9fcef40000000p-26f}, {0x1.71f75e0000000p+0f, 0x1.1d8bee0000000p-25f}, {0x1.7a11480000000p+0f, -0x1.829fd00000000p-25f}, {0x1.82589a0000000p+0f, -0x1.accc7c0000000p-26f},
+    {0x1.8ace540000000p+0f, 0x1.15506e0000000p-27f}, {0x1.93737c0000000p+0f, -0x1.e647440000000p-25f}, {0x1.9c49180000000p+0f, 0x1.51f8480000000p-27f}, {0x1.a5503c0000000p+0f, -0x1.b83b540000000p-25f},
+    {0x1.ae89fa0000000p+0f, -0x1.a94b140000000p-26f}, {0x1.b7f7700000000p+0f, -0x1.a094380000000p-25f}, {0x1.c199be0000000p+0f, -0x1.3d56b20000000p-27f}, {0x1.cb720e0000000p+0f, -0x1.8837cc0000000p-27f},
+    {0x1.d5818e0000000p+0f, -0x1.822dbc0000000p-27f}, {0x1.dfc9740000000p+0f, -0x1.908c940000000p-25f}, {0x1.ea4afa0000000p+0f, 0x1.52486c0000000p-27f}, {0x1.f507660000000p+0f, -0x1.246eb00000000p-26f}
+};
+__device__ __forceinline__ float2 exp2_pair(long long x) {
+    const long long whole = x >> 40;
+    if (whole < -160) return make_float2(0.f, 0.f);
+    if (whole > 127) return make_float2(INFINITY, 0.f);
+    const uint64_t frac = (uint64_t)x & ((1ull << 40) - 1);
+    const float2 t = kPow2[frac >> 35];
+    const float r = (float)(frac & ((1ull << 35) - 1)) * (kFix * 0.693147180559945f);
+    const float e = r + r * r * (0.5f + r * (1.f / 6.f + r * (1.f / 24.f)));
+    const float y = fmaf(t.x, e, t.y);
+    const float hi = t.x + y, lo = y - (hi - t.x);
+    return make_float2(ldexpf(hi, (int)whole), ldexpf(lo, (int)whole));
+}
+// log2(exp(g)) in units of 2^-40; +-2^14 for what is beyond (an infinity among it).
+__device__ __forceinline__ long long log2_fixed(float g) {
+    const float top = 11356.5f;  // 2^14 ln 2, nearly
+    g = fminf(fmaxf(g, -top), top);
+    const float L = 1.44269502162933349609375f, l = 1.925963e-8f;  // log2(e) = L + l
+    const float hi = g * L, lo = fmaf(g, l, fmaf(g, L, -hi));
+    return __float2ll_rn(hi * 0x1p40f) + __float2ll_rn(lo * 0x1p40f);
+}
+
+// The segments of a row of n tokens.
+__device__ __forceinline__ int segments(const ChunkArgs& c, int n) { return c.seg ? (n + c.seg - 1) / c.seg : 1; }
+
+template <int N, int P, bool PAIR, int SP, bool OUT>
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_kernel(const __grid_constant__ ChunkArgs c, const __grid_constant__ CUtensorMap qmap,
+                 const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+    using C = Chunk<N, P, PAIR, SP, OUT>;
+    constexpr int VH = C::VH, ST = C::ST;
+    const Args& a = c.a;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* const smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    unsigned char* const vp = smem + ST * C::STAGE;  // V', its parts
+    unsigned char* const sw = vp + SP * C::VB;       // W, two parts
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    __shared__ uint64_t full[3], empty[3], gready[kGates], gfree[kGates], ufull[kUnits], ufree[kUnits];
+    __shared__ uint64_t sc_full, sc_free, w_ready, w_free, vp_ready, vp_free, ds_full, ds_free, s0_ready, s0_free,
+        o_full, o_free, drain;
+    __shared__ uint32_t tmem_at;
+    __shared__ int abort_flag;
+    __shared__ Unit units[kUnits];
+    __shared__ __align__(16) float4 gw[kGates][VH][kC];  // G (log2): whole part, rest; scale w
+    __shared__ __align__(16) float ge[kGates][VH][kC];   // scale exp(G)
+    // a weight of a token of the second half on one of the first: exp(G_i - G_31) times scale exp(G_31 - G_j) w_j
+    __shared__ __align__(16) float gcol[kGates][VH][kC / 2], grow[kGates][VH][kC / 2];
+    __shared__ float gd[kGates][VH][kC];                 // exp(G_end - G) w
+    __shared__ float2 gam[kGates][VH];                   // exp(G_end) and its remainder
+    // of each value row, chunk and 63 - first token whose value is not finite (of older chunks: behind its time)
+    __shared__ unsigned odd[4][C::VL];
+    __shared__ int any_odd[4][4];
+
+    if (tid == 0) {
+        for (int i = 0; i < 3; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < kGates; ++i) {
+            mbar_init(&gready[i], 1);
+            mbar_init(&gfree[i], C::CONS);
+        }
+        for (int i = 0; i < kUnits; ++i) {
+            mbar_init(&ufull[i], 1);
+            mbar_init(&ufree[i], C::UCONS);
+        }
+        mbar_init(&sc_full, 1);
+        mbar_init(&sc_free, 4);
+        mbar_init(&w_ready, 4);
+        mbar_init(&w_free, 1);
+        mbar_init(&vp_ready, 4);
+        mbar_init(&vp_free, 1);
+        mbar_init(&ds_full, 1);
+        mbar_init(&ds_free, 16);
+        mbar_init(&s0_ready, 16);
+        mbar_init(&s0_free, 1);
+        mbar_init(&o_full, 1);
+        mbar_init(&o_free, 4);
+        mbar_init(&drain, 1);
+        fence_barrier_init();
+        abort_flag = 0;
+    }
+    if (OUT)
+        for (int i = tid; i < 4 * C::VL; i += kThreads) odd[i / C::VL][i % C::VL] = 0;
+    if (warp == 29) umma::tmem_alloc(&tmem_at, 512);
+    umma::fence_before_sync();
+    __syncthreads();
+    umma::fence_after_sync();
+    const uint32_t tmem = tmem_at;
+    volatile int* const stop = &abort_flag;
+    auto await = [&](uint64_t* bar, uint32_t parity) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        return wait_long(bar, parity, stop, c.wait_ns, a.dev_err);
+    };
+    // one arrival of the warp
+    auto arrive = [&](uint64_t* bar) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive_plain(bar);
+    };
+    attn::wait_for_stream();
+
+    if (warp < 16) {
+        // --------------------------------------------------------------- state
+        constexpr int NS = N / 4;  // keys of a thread
+        const int p = (warp & 3) * 32 + lane, n0 = (warp >> 2) * NS;
+        const bool mine = p < C::VL;
+        const uint32_t at = tmem + ((uint32_t)(warp & 3) << 21);
+        const int vh = PAIR ? p >> 6 : 0;
+        Ring ur, gr, one, s0;
+        for (;;) {
+            if (!await(&ufull[ur.slot], ur.parity)) break;
+            const Unit u = units[ur.slot];
+            if (u.n < 0) break;
+            f2 s[NS / 2];
+            const long row = ((long)u.head * P + p) * N + n0, all = (long)a.H * P * N;
+#pragma unroll
+            for (int i = 0; i < NS / 2; ++i) s[i] = 0;
+            if (mine && u.from == kSlot) {
+                const char* from = static_cast<const char*>(a.state) + (u.slot * all + row) * (a.sbf ? 2 : 4);
+#pragma unroll
+                for (int i = 0; i < NS; i += 8) {
+                    float x[8];
+                    load8(from + i * (a.sbf ? 2 : 4), a.sbf, x);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[i / 2 + e] = two(x[2 * e], x[2 * e + 1]);
+                }
+            } else if (mine && u.from == kPart) {
+                const float* from = c.parts + u.part * all + row;
+#pragma unroll
+                for (int i = 0; i < NS; i += 4) {
+                    const float4 x = __ldcg(reinterpret_cast<const float4*>(from + i));
+                    s[i / 2] = two(x.x, x.y);
+                    s[i / 2 + 1] = two(x.z, x.w);
+                }
+            }
+            bool ok = true;
+            for (int t = 0; t < u.n; t += kC) {
+                if (OUT) {
+                    ok = await(&s0_free, s0.parity ^ 1);
+                    if (!ok) break;
+                    umma::fence_after_sync();
+                    float hi[NS / 2], lo[NS / 2];
+#pragma unroll
+                    for (int x = 0; x < NS / 2; ++x) {
+                        f2 r = s[x];
+                        hi[x] = __uint_as_float(split2(r));
+                        lo[x] = __uint_as_float(pack2(r));
+                    }
+                    umma::st_cols<NS / 2>(at + C::STATE + n0 / 2, hi);
+                    umma::st_cols<NS / 2>(at + C::STATE + N / 2 + n0 / 2, lo);
+                    umma::wait_st();
+                    umma::fence_before_sync();
+                    arrive(&s0_ready);
+                    s0.next(1);
+                }
+                ok = await(&gready[gr.slot], gr.parity) && await(&ds_full, one.parity);
+                if (!ok) break;
+                const float2 f = gam[gr.slot][vh];
+                const f2 fx = two(f.x, f.x), fy = two(f.y, f.y);
+                umma::fence_after_sync();
+#pragma unroll
+                for (int i = 0; i < NS / 2; i += 8) {
+                    float d[16];
+                    umma::ld_cols<16>(at + C::DS + n0 + 2 * i, d);
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)
+                        s[i + x] = fma2(fx, s[i + x], fma2(fy, s[i + x], two(d[2 * x], d[2 * x + 1])));
+                }
+                umma::fence_before_sync();
+                arrive(&ds_free);
+                if (lane == 0) mbar_arrive_plain(&gfree[gr.slot]);
+                one.next(1);
+                gr.next(kGates);
+            }
+            if (!ok) break;
+            if (mine && u.to != kZero) {
+                const bool sbf = u.to == kSlot && a.sbf;
+                char* to = u.to == kSlot ? static_cast<char*>(a.state) + (u.slot * all + row) * (a.sbf ? 2 : 4)
+                                         : reinterpret_cast<char*>(c.parts + u.part * all + row);
+#pragma unroll
+                for (int i = 0; i < NS; i += 8) {
+                    float x[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 y = one_by_one(s[i / 2 + e]);
+                        x[2 * e] = y.x;
+                        x[2 * e + 1] = y.y;
+                    }
+                    store8(to + i * (sbf ? 2 : 4), sbf, x);
+                }
+            }
+            arrive(&ufree[ur.slot]);
+            ur.next(kUnits);
+        }
+    } else if (warp < 24 && (warp & 2) == 0) {
+        // ------------------------------------------------------------- weights
+        if (OUT) {
+            // a token a thread, its row of W and its lane of the scores, in two warps: each has 16 of every 32 columns
+            const int q = warp & 1, i = q * 32 + lane, half = (warp >> 2) & 1;
+            const uint32_t at = tmem + ((uint32_t)q << 21) + C::SCORE;
+            Ring ur, gr, one;
+            for (;;) {
+                if (!await(&ufull[ur.slot], ur.parity)) break;
+                const int n = units[ur.slot].n;
+                if (n < 0) break;
+                bool ok = true;
+                for (int t = 0; t < n; t += kC) {
+                    ok = await(&gready[gr.slot], gr.parity) && await(&sc_full, one.parity) && await(&w_free, one.parity ^ 1);
+                    if (!ok) break;
+                    umma::fence_after_sync();
+                    const bool tail = t + kC > n;
+#pragma unroll 1
+                    for (int h = 0; h < VH; ++h) {
+                        unsigned char* const row = sw + h * kBox + i * 128;
+                        auto put = [&](int j0, const uint32_t (&hi)[8], const uint32_t (&lo)[8]) {
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                unsigned char* const to = row + (((j0 / 8 + x) ^ (i & 7)) << 4);
+                                *reinterpret_cast<uint4*>(to) = make_uint4(hi[4 * x], hi[4 * x + 1], hi[4 * x + 2], hi[4 * x + 3]);
+                                *reinterpret_cast<uint4*>(to + C::WB) = make_uint4(lo[4 * x], lo[4 * x + 1], lo[4 * x + 2], lo[4 * x + 3]);
+                            }
+                        };
+                        uint32_t hi[8], lo[8];
+                        float s[16];
+                        // the other half's columns: all of them earlier, or all later, tokens
+                        const int j1 = (q ? 0 : 32) + half * 16;
+                        if (q) {
+                            umma::ld_cols<16>(at + j1, s);
+                            const float rr = grow[gr.slot][h][lane];
+                            const f2 r = two(rr, rr);
+#pragma unroll
+                            for (int x = 0; x < 16; x += 4) {
+                                const float4 cj = *reinterpret_cast<const float4*>(&gcol[gr.slot][h][half * 16 + x]);
+                                f2 y = mul2(mul2(r, two(cj.x, cj.y)), two(s[x], s[x + 1]));
+                                f2 z = mul2(mul2(r, two(cj.z, cj.w)), two(s[x + 2], s[x + 3]));
+                                hi[x / 2] = split2(y);
+                                lo[x / 2] = pack2(y);
+                                hi[x / 2 + 1] = split2(z);
+                                lo[x / 2 + 1] = pack2(z);
+                            }
+                            if (tail) {
+#pragma unroll
+                                for (int x = 0; x < 8; ++x) {
+                                    const uint32_t keep = t + j1 + 2 * x + 1 < n ? ~0u : t + j1 + 2 * x < n ? 0xffffu : 0u;
+                                    hi[x] &= keep;
+                                    lo[x] &= keep;
+                                }
+                            }
+                        } else {
+#pragma unroll
+                            for (int x = 0; x < 8; ++x) hi[x] = lo[x] = 0;
+                        }
+                        put(j1, hi, lo);
+                        // the same half's: up to the token itself
+                        const int j0 = q * 32 + half * 16;
+                        const float4 gi = gw[gr.slot][h][i];
+                        umma::ld_cols<16>(at + j0, s);
+                        const int upto = tail ? min(i, n - 1 - t) : i;
+#pragma unroll
+                        for (int x = 0; x < 16; x += 2) {
+                            const float4 g = gw[gr.slot][h][j0 + x], g2 = gw[gr.slot][h][j0 + x + 1];
+                            f2 y = two(exp2_fast((gi.x - g.x) + (gi.y - g.y)), exp2_fast((gi.x - g2.x) + (gi.y - g2.y)));
+                            y = mul2(mul2(y, two(g.z, g2.z)), two(s[x], s[x + 1]));
+                            const uint32_t keep = j0 + x + 1 <= upto ? ~0u : j0 + x <= upto ? 0xffffu : 0u;
+                            hi[x / 2] = split2(y) & keep;
+                            lo[x / 2] = pack2(y) & keep;
+                        }
+                        put(j0, hi, lo);
+                    }
+                    umma::fence_before_sync();
+                    fence_async_smem();
+                    arrive(&w_ready);
+                    if (lane == 0) {
+                        mbar_arrive_plain(&sc_free);
+                        mbar_arrive_plain(&gfree[gr.slot]);
+                    }
+                    one.next(1);
+                    gr.next(kGates);
+                }
+                if (!ok) break;
+                arrive(&ufree[ur.slot]);
+                ur.next(kUnits);
+            }
+        }
+    } else if (warp < 24) {
+        // ------------------------------------------------------ decayed values
+        const int me = (warp & 1) + (warp >> 2 & 1) * 2, vt = me * 32 + lane;
+        Ring ur, gr, st, one;
+        uint32_t k = 0;
+        for (;;) {
+            if (!await(&ufull[ur.slot], ur.parity)) break;
+            const int n = units[ur.slot].n;
+            if (n < 0) break;
+            bool ok = true;
+            for (int t = 0; t < n; t += kC, ++k) {
+                ok = await(&gready[gr.slot], gr.parity) && await(&full[st.slot], st.parity) && await(&vp_free, one.parity ^ 1);
+                if (!ok) break;
+                unsigned char* const sv = smem + st.slot * C::STAGE + 2 * C::QB;
+                const int cnt = n - t;
+                f2 probe = 0;  // becomes NaN where a value is not finite
+#pragma unroll 1
+                for (int e = vt; e < C::VB / 16; e += 128) {
+                    const int j = (e >> 3) & 63, h = PAIR ? e >> 9 : 0;
+                    const uint4 x = *reinterpret_cast<const uint4*>(sv + e * 16);
+                    const float d = gd[gr.slot][h][j];
+                    const f2 dd = two(d, d);
+                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                    uint32_t y[SP][4];
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        const f2 v = two(bf16_lo(w[b]), bf16_hi(w[b]));
+                        if (OUT) probe = fma2(v, 0, probe);
+                        f2 r = mul2(v, dd);
+#pragma unroll
+                        for (int z = 0; z + 1 < SP; ++z) y[z][b] = split2(r);
+                        y[SP - 1][b] = pack2(r);
+                    }
+                    const bool in = j < cnt;
+#pragma unroll
+                    for (int z = 0; z < SP; ++z)
+                        *reinterpret_cast<uint4*>(vp + z * C::VB + e * 16) =
+                            in ? make_uint4(y[z][0], y[z][1], y[z][2], y[z][3]) : make_uint4(0, 0, 0, 0);
+                }
+                if (cnt < kC) {  // rows behind the last token may hold anything, and zero times that is not zero
+                    for (int e = vt; e < C::VB / 16; e += 128)
+                        if (((e >> 3) & 63) >= cnt) *reinterpret_cast<uint4*>(sv + e * 16) = make_uint4(0, 0, 0, 0);
+                    unsigned char* const sk = sv - C::QB;
+                    for (int e = vt; e < C::QB / 16; e += 128)
+                        if (((e >> 3) & 63) >= cnt) *reinterpret_cast<uint4*>(sk + e * 16) = make_uint4(0, 0, 0, 0);
+                }
+                if (OUT) {
+                    // A value that is not finite must not meet the zero weights of the tokens before it: it is
+                    // cleared, and the output makes NaN of its row from its token on.
+                    const float2 pr = one_by_one(probe);
+                    const bool bad = __any_sync(0xffffffffu, pr.x + pr.y != 0.f);
+                    if (__builtin_expect(bad, 0)) {
+                        for (int e = vt; e < C::VB / 16; e += 128) {
+                            const int j = (e >> 3) & 63, col = (e >> 9) * 64 + ((e & 7) ^ (j & 7)) * 8;
+                            if (j >= cnt) continue;
+                            uint16_t* const v = reinterpret_cast<uint16_t*>(sv + e * 16);
+                            for (int x = 0; x < 8; ++x)
+                                if ((v[x] & 0x7f80) == 0x7f80) {
+                                    atomicMax(&odd[k & 3][col + x], ((k + 1) << 6) | (63 - j));
+                                    v[x] = 0;
+                                }
+                        }
+                    }
+                    if (lane == 0) any_odd[k & 3][me] = bad;
+                }
+                fence_async_smem();
+                arrive(&vp_ready);
+                if (lane == 0) mbar_arrive_plain(&gfree[gr.slot]);
+                one.next(1);
+                gr.next(kGates);
+                st.next(ST);
+            }
+            if (!ok) break;
+            arrive(&ufree[ur.slot]);
+            ur.next(kUnits);
+        }
+    } else if (warp < 28) {
+        // -------------------------------------------------------------- output
+        if (OUT) {
+            const int p = (warp & 3) * 32 + lane, odd_lane = lane & 1;
+            const uint32_t at = tmem + ((uint32_t)(warp & 3) << 21);
+            const int vh = PAIR ? p >> 6 : 0;
+            const int size = a.obf ? 2 : 4;
+            const uint32_t step = (uint32_t)(a.H * P * size);  // bytes of a token (64 of them: less than 2^32)
+            Ring ur, gr, one;
+            uint32_t k = 0;
+            for (;;) {
+                if (!await(&ufull[ur.slot], ur.parity)) break;
+                const Unit u = units[ur.slot];
+                if (u.n < 0) break;
+                bool ok = true;
+                for (int t = 0; t < u.n; t += kC, ++k) {
+                    ok = await(&gready[gr.slot], gr.parity) && await(&o_full, one.parity);
+                    if (!ok) break;
+                    umma::fence_after_sync();
+                    const int cnt = p < C::VL ? min(kC, u.n - t) : 0;
+                    int bad = kC;
+                    if (__builtin_expect(any_odd[k & 3][0] | any_odd[k & 3][1] | any_odd[k & 3][2] | any_odd[k & 3][3], 0) && p < C::VL) {
+                        const unsigned x = odd[k & 3][p];
+                        if (x >> 6 == (k + 1) % (1u << 26)) bad = 63 - (x & 63);
+                    }
+                    char* const out = static_cast<char*>(a.o) + (long)(u.tok + t) * step + ((long)u.head * P + p) * size;
+#pragma unroll 1
+                    for (int i0 = 0; i0 < kC; i0 += 16) {
+                        float x[16], y[16];
+                        umma::ld_cols<16>(at + C::INTER + i0, x);
+                        umma::ld_cols<16>(at + C::INTRA + vh * 64 + i0, y);
+                        f2 o[8];
+#pragma unroll
+                        for (int i = 0; i < 16; i += 4) {
+                            const float4 e = *reinterpret_cast<const float4*>(&ge[gr.slot][vh][i0 + i]);
+                            o[i / 2] = fma2(two(e.x, e.y), two(x[i], x[i + 1]), two(y[i], y[i + 1]));
+                            o[i / 2 + 1] = fma2(two(e.z, e.w), two(x[i + 2], x[i + 3]), two(y[i + 2], y[i + 3]));
+                        }
+                        if (__builtin_expect(bad < kC, 0)) {
+#pragma unroll
+                            for (int i = 0; i < 16; i += 2) {
+                                const float nan = __uint_as_float(0x7fc00000u);
+                                const float2 f = one_by_one(o[i / 2]);
+                                o[i / 2] = two(i0 + i >= bad ? nan : f.x, i0 + i + 1 >= bad ? nan : f.y);
+                            }
+                        }
+                        if (a.obf) {
+                            // two tokens of a lane for one token of two lanes: a lane stores 4 bytes
+#pragma unroll
+                            for (int i = 0; i < 16; i += 2) {
+                                const uint32_t w = pack2(o[i / 2]), v = __shfl_xor_sync(0xffffffffu, w, 1);
+                                const uint32_t both = odd_lane ? __byte_perm(v, w, 0x7632) : __byte_perm(w, v, 0x5410);
+                                if (i0 + i + odd_lane < cnt)
+                                    *reinterpret_cast<uint32_t*>(out + (uint32_t)(i0 + i) * step + (odd_lane ? (long)step - 2 : 0)) = both;
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 16; i += 2) {
+                                const float2 f = one_by_one(o[i / 2]);
+                                if (i0 + i < cnt) *reinterpret_cast<float*>(out + (uint32_t)(i0 + i) * step) = f.x;
+                                if (i0 + i + 1 < cnt) *reinterpret_cast<float*>(out + (uint32_t)(i0 + i + 1) * step) = f.y;
+                            }
+                        }
+                    }
+                    umma::fence_before_sync();
+                    arrive(&o_free);
+                    if (lane == 0) mbar_arrive_plain(&gfree[gr.slot]);
+                    one.next(1);
+                    gr.next(kGates);
+                }
+                if (!ok) break;
+                arrive(&ufree[ur.slot]);
+                ur.next(kUnits);
+            }
+        }
+    } else if (warp == 28) {
+        // ------------------------------------------------- the list, and loads
+        const uint64_t pol = policy_evict_first();
+        Ring ur, st;
+        bool ok = true;
+        auto take = [&](const Unit& u) {  // (u: the same on every lane)
+            if (!await(&ufree[ur.slot], ur.parity ^ 1)) return false;
+            if (lane == 0) units[ur.slot] = u;
+            arrive(&ufull[ur.slot]);
+            ur.next(kUnits);
+            const int kh = u.head / (a.H / a.G);
+            for (int t = 0; t < u.n; t += kC) {
+                if (!await(&empty[st.slot], st.parity ^ 1)) return false;
+                unsigned char* const to = smem + st.slot * C::STAGE;
+                if (elect_one()) {
+                    uint64_t* const bar = &full[st.slot];
+                    mbar_arrive_expect_tx(bar, (OUT ? 2 : 1) * C::QB + C::VB);
+#pragma unroll
+                    for (int x = 0; x < N / 64; ++x) {
+                        tma_load_2d(to + C::QB + x * kBox, &kmap, kh * N + 64 * x, u.tok + t, bar, pol);
+                        if (OUT) tma_load_2d(to + x * kBox, &qmap, kh * N + 64 * x, u.tok + t, bar, pol);
+                    }
+#pragma unroll
+                    for (int x = 0; x < C::VL / 64; ++x)
+                        tma_load_2d(to + 2 * C::QB + x * kBox, &vmap, u.head * P + 64 * x, u.tok + t, bar, pol);
+                }
+                __syncwarp();
+                st.next(ST);
+            }
+            return true;
+        };
+        if (OUT) {
+            // a lane looks up one unit of the next 32
+            const unsigned items = (unsigned)c.units * c.blocks;  // (below 2^28)
+            for (unsigned i0 = blockIdx.x; i0 < items && ok; i0 += 32 * gridDim.x) {
+                const unsigned i = i0 + lane * gridDim.x;
+                Unit u;
+                u.n = 0;
+                u.tok = u.head = u.slot = u.part = u.from = u.to = 0;
+                if (i < items) {
+                    const int x = i / (unsigned)c.blocks;
+                    u.head = (int)(i - x * c.blocks) * VH;
+                    int b = x, s = 0;
+                    if (c.seg) {
+                        // row b's segments have the numbers begin / seg + b and on: the last row with that <= x
+                        int lo = 0, hi = a.batch - 1;
+                        while (lo < hi) {
+                            const int mid = (lo + hi + 1) >> 1;
+                            const int begin = a.cu ? a.cu[mid] : mid * a.each;
+                            if (begin / c.seg + mid <= x) lo = mid;
+                            else hi = mid - 1;
+                        }
+                        b = lo;
+                        s = x - ((a.cu ? a.cu[b] : b * a.each) / c.seg + b);
+                    }
+                    int begin, end;
+                    if (row_of(a, b, u.head == 0, begin, end, u.slot) && s >= 0 && s < segments(c, end - begin)) {
+                        const int last = segments(c, end - begin) - 1;
+                        u.tok = begin + s * c.seg;
+                        u.n = s == last ? end - u.tok : c.seg;
+                        u.part = s > 0 ? begin / c.seg + s - 1 : last > 0 ? c.kept + begin / c.seg : 0;
+                        u.from = s > 0 ? kPart : !a.resume || !a.resume[b] ? kZero : last > 0 ? kPart : kSlot;
+                        u.to = s == last ? kSlot : kZero;
+                    }
+                }
+                for (uint32_t m = __ballot_sync(0xffffffffu, u.n > 0); m && ok; m &= m - 1) {
+                    const int l = __ffs(m) - 1;
+                    Unit x;
+                    x.tok = __shfl_sync(0xffffffffu, u.tok, l);
+                    x.n = __shfl_sync(0xffffffffu, u.n, l);
+                    x.head = __shfl_sync(0xffffffffu, u.head, l);
+                    x.slot = __shfl_sync(0xffffffffu, u.slot, l);
+                    x.part = __shfl_sync(0xffffffffu, u.part, l);
+                    x.from = __shfl_sync(0xffffffffu, u.from, l);
+                    x.to = __shfl_sync(0xffffffffu, u.to, l);
+                    ok = take(x);
+                }
+            }
+        } else {
+            // the segments before the last one of each long row
+            unsigned next = blockIdx.x;  // this CTA's next item, counted from the row's first
+            for (int b0 = 0; b0 < a.batch && ok; b0 += 32) {
+                int begin = 0, end = 0, slot = 0, count = 0;
+                if (b0 + lane < a.batch && row_of(a, b0 + lane, false, begin, end, slot)) count = segments(c, end - begin) - 1;
+                for (uint32_t m = __ballot_sync(0xffffffffu, count > 0); m && ok; m &= m - 1) {
+                    const int l = __ffs(m) - 1;
+                    const int first = __shfl_sync(0xffffffffu, begin, l);
+                    const unsigned more = (unsigned)__shfl_sync(0xffffffffu, count, l) * c.blocks;
+                    for (; next < more && ok; next += gridDim.x) {
+                        const int s = next / (unsigned)c.blocks;
+                        Unit u;
+                        u.tok = first + s * c.seg;
+                        u.n = c.seg;
+                        u.head = (int)(next - s * c.blocks) * VH;
+                        u.slot = 0;
+                        u.part = first / c.seg + s;
+                        u.from = kZero;
+                        u.to = kPart;
+                        ok = take(u);
+                    }
+                    next -= more;
+                }
+            }
+        }
+        if (ok && await(&ufree[ur.slot], ur.parity ^ 1)) {
+            if (lane == 0) units[ur.slot].n = -1;
+            arrive(&ufull[ur.slot]);
+        }
+    } else if (warp == 29) {
+        // ------------------------------------------------------------ products
+        constexpr uint32_t i_score = umma::idesc_16bit(128, kC, true, false, false);
+        constexpr uint32_t i_ds = umma::idesc_16bit(128, N, true, true, true);
+        constexpr uint32_t i_inter = umma::idesc_16bit(128, kC, true, false, false);
+        constexpr uint32_t i_intra = umma::idesc_16bit(128, kC * VH, true, true, false);
+        constexpr uint32_t lbo = C::VL == 128 ? kBox : 1024;  // (64 lanes: what the others hold is not read)
+        const uint32_t at = smem_addr(smem), vp_at = smem_addr(vp);
+        const uint64_t wd = umma::smem_desc_swizzle128(smem_addr(sw), 16, 1024);
+        const uint64_t vpd = umma::smem_desc_swizzle128(vp_at, lbo, 1024);
+        Ring ur, st, ahead, sc, v1, s1, w1;
+        // scores of the chunk whose loads are in stage `ahead`
+        auto scores = [&]() {
+            if (!await(&full[ahead.slot], ahead.parity) || !await(&sc_free, sc.parity ^ 1)) return false;
+            umma::fence_after_sync();
+            const uint64_t qd = umma::smem_desc_swizzle128(at + ahead.slot * C::STAGE, 16, 1024);
+            const uint64_t kd = umma::smem_desc_swizzle128(at + ahead.slot * C::STAGE + C::QB, 16, 1024);
+            if (elect_one()) {
+#pragma unroll
+                for (int x = 0; x < N / 16; ++x) {
+                    const int off = (x / 4 * kBox + x % 4 * 32) >> 4;
+                    umma::mma_bf16(tmem + C::SCORE, qd + off, kd + off, i_score, x > 0);
+                }
+                umma::commit_to(&sc_full);
+            }
+            __syncwarp();
+            sc.next(1);
+            ahead.next(ST);
+            return true;
+        };
+        for (;;) {
+            if (!await(&ufull[ur.slot], ur.parity)) break;
+            const int n = units[ur.slot].n;
+            if (n < 0) break;
+            bool ok = !OUT || scores();
+            for (int t = 0; t < n && ok; t += kC) {
+                const uint32_t stage = at + st.slot * C::STAGE;
+                ok = await(&vp_ready, v1.parity) && await(&ds_free, v1.parity ^ 1);
+                if (!ok) break;
+                umma::fence_after_sync();
+                const uint64_t kt = umma::smem_desc_swizzle128(stage + C::QB, kBox, 1024);
+                if (elect_one()) {
+#pragma unroll
+                    for (int z = 0; z < SP; ++z)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            umma::mma_bf16(tmem + C::DS, vpd + ((z * C::VB + x * 2048) >> 4), kt + (x * 2048 >> 4), i_ds,
+                                           z + x > 0);
+                    umma::commit_to(&ds_full);
+                    umma::commit_to(&vp_free);
+                    if (!OUT) umma::commit_to(&empty[st.slot]);
+                }
+                __syncwarp();
+                v1.next(1);
+                if (OUT) {
+                    if (t + kC < n) ok = scores();
+                    ok = ok && await(&s0_ready, s1.parity) && await(&o_free, s1.parity ^ 1);
+                    if (!ok) break;
+                    umma::fence_after_sync();
+                    const uint64_t qd = umma::smem_desc_swizzle128(stage, 16, 1024);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int z = 0; z < 2; ++z)
+#pragma unroll
+                            for (int x = 0; x < N / 16; ++x)
+                                umma::mma_bf16_tmem(tmem + C::INTER, tmem + C::STATE + z * N / 2 + x * 8,
+                                                    qd + ((x / 4 * kBox + x % 4 * 32) >> 4), i_inter, z + x > 0);
+                        umma::commit_to(&s0_free);
+                    }
+                    __syncwarp();
+                    s1.next(1);
+                    ok = await(&w_ready, w1.parity);
+                    if (!ok) break;
+                    umma::fence_after_sync();
+                    const uint64_t vd = umma::smem_desc_swizzle128(stage + 2 * C::QB, lbo, 1024);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int z = 0; z < 2; ++z)
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                umma::mma_bf16(tmem + C::INTRA, vd + (x * 2048 >> 4), wd + ((z * C::WB + x * 32) >> 4), i_intra,
+                                               z + x > 0);
+                        umma::commit_to(&o_full);
+                        umma::commit_to(&w_free);
+                        umma::commit_to(&empty[st.slot]);
+                    }
+                    __syncwarp();
+                    w1.next(1);
+                }
+                st.next(ST);
+            }
+            if (!ok) break;
+            arrive(&ufree[ur.slot]);
+            ur.next(kUnits);
+        }
+    } else if (warp == 30) {
+        // -------------------------------------------------------------- decays
+        Ring ur, gr;
+        for (;;) {
+            if (!await(&ufull[ur.slot], ur.parity)) break;
+            const Unit u = units[ur.slot];
+            if (u.n < 0) break;
+            float g[VH][2], w[VH][2];  // of tokens 2 lane, 2 lane + 1
+            long long total[VH];
+            bool total_bad[VH];
+            auto load = [&](int t) {
+#pragma unroll
+                for (int h = 0; h < VH; ++h)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int j = t + 2 * lane + x;
+                        g[h][x] = w[h][x] = 0.f;
+                        if (j < u.n) {
+                            const long row = u.tok + j;
+                            g[h][x] = a.g[row * a.g_stride + u.head + h];
+                            w[h][x] = a.w ? a.w[row * a.w_stride + u.head + h] : 1.f;
+                        }
+                    }
+            };
+#pragma unroll
+            for (int h = 0; h < VH; ++h) {
+                total[h] = 0;
+                total_bad[h] = false;
+            }
+            load(0);
+            bool ok = true;
+            for (int t = 0; t < u.n; t += kC) {
+                long long x0[VH], x1[VH];
+                float w0[VH], w1[VH];
+                uint32_t bad0[VH], bad1[VH];
+#pragma unroll
+                for (int h = 0; h < VH; ++h) {
+                    x0[h] = log2_fixed(g[h][0]);
+                    x1[h] = log2_fixed(g[h][1]);
+                    bad0[h] = __ballot_sync(0xffffffffu, g[h][0] != g[h][0]);
+                    bad1[h] = __ballot_sync(0xffffffffu, g[h][1] != g[h][1]);
+                    w0[h] = w[h][0];
+                    w1[h] = w[h][1];
+                }
+                if (t + kC < u.n) load(t + kC);
+                ok = await(&gfree[gr.slot], gr.parity ^ 1);
+                if (!ok) break;
+#pragma unroll
+                for (int h = 0; h < VH; ++h) {
+                    long long sum = x0[h] + x1[h];
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const long long y = __shfl_up_sync(0xffffffffu, sum, o);
+                        if (lane >= o) sum += y;
+                    }
+                    const long long G1 = sum, G0 = sum - x1[h], end = __shfl_sync(0xffffffffu, sum, 31);
+                    const uint32_t before = (1u << lane) - 1, either = bad0[h] | bad1[h];
+                    const bool nan0 = (either & before) || (bad0[h] >> lane & 1), nan1 = nan0 || (bad1[h] >> lane & 1);
+                    const float nan = __uint_as_float(0x7fc00000u);
+                    // (a difference of two sums must not lose its bits to their size: a reset is 2^14)
+                    const long long whole0 = G0 >> 40, whole1 = G1 >> 40;
+                    const float s0 = w0[h] * a.scale, s1 = w1[h] * a.scale;
+                    gw[gr.slot][h][2 * lane] = make_float4((float)whole0, __ll2float_rn(G0 - (whole0 << 40)) * kFix, s0, 0.f);
+                    gw[gr.slot][h][2 * lane + 1] = make_float4((float)whole1, __ll2float_rn(G1 - (whole1 << 40)) * kFix, s1, 0.f);
+                    *reinterpret_cast<float2*>(&ge[gr.slot][h][2 * lane]) =
+                        make_float2(nan0 ? nan : a.scale * exp2_fast(__ll2float_rn(G0) * kFix),
+                                    nan1 ? nan : a.scale * exp2_fast(__ll2float_rn(G1) * kFix));
+                    gd[gr.slot][h][2 * lane] = exp2_fast(__ll2float_rn(end - G0) * kFix) * w0[h];
+                    gd[gr.slot][h][2 * lane + 1] = exp2_fast(__ll2float_rn(end - G1) * kFix) * w1[h];
+                    const long long mid = __shfl_sync(0xffffffffu, sum, 15);
+                    if (lane < 16)
+                        *reinterpret_cast<float2*>(&gcol[gr.slot][h][2 * lane]) =
+                            make_float2(exp2_fast(__ll2float_rn(mid - G0) * kFix) * s0, exp2_fast(__ll2float_rn(mid - G1) * kFix) * s1);
+                    else
+                        *reinterpret_cast<float2*>(&grow[gr.slot][h][2 * lane - 32]) =
+                            make_float2(exp2_fast(__ll2float_rn(G0 - mid) * kFix), exp2_fast(__ll2float_rn(G1 - mid) * kFix));
+                    total[h] += end;
+                    // (a sum that leaves the range of exponents stays there)
+                    const long long most = 1ll << 61;
+                    total[h] = total[h] < -most ? -most : total[h] > most ? most : total[h];
+                    total_bad[h] |= either != 0;
+                    if (lane == h) gam[gr.slot][h] = either ? make_float2(nan, nan) : exp2_pair(end);
+                }
+                arrive(&gready[gr.slot]);
+                gr.next(kGates);
+            }
+            if (!ok) break;
+            if (!OUT && lane < VH) {
+                const long long sum = VH == 2 && lane ? total[VH - 1] : total[0];
+                const bool bad = VH == 2 && lane ? total_bad[VH - 1] : total_bad[0];
+                const float nan = __uint_as_float(0x7fc00000u);
+                c.part_decay[(long)u.part * a.H + u.head + lane] = bad ? make_float2(nan, nan) : exp2_pair(sum);
+            }
+            arrive(&ufree[ur.slot]);
+            ur.next(kUnits);
+        }
+    }
+    __syncthreads();
+    if (abort_flag) {
+        // A wait ran out: no copy and no product may still be in flight when the CTA ends.
+        if (warp == 29) {
+            if (elect_one()) umma::commit_to(&drain);
+            __syncwarp();
+            mbar_wait_bounded(&drain, 0, RSSM_WAIT_NS / 100);
+        } else if (tid < ST) {
+            mbar_wait_bounded(&full[tid], 0, RSSM_WAIT_NS / 100);
+            mbar_wait_bounded(&full[tid], 1, RSSM_WAIT_NS / 100);
+        }
+        __syncthreads();
+    }
+    if (warp == 29) umma::tmem_dealloc(tmem, 512);
+}
+
+// parts[s] = the state after segment s, from its own state and what came before. A thread has four
+// values, and goes through the long rows and their segments with the next ones' loads in flight.
+__global__ void __launch_bounds__(256) carry_kernel(const ChunkArgs c, long all, int per_head) {
+    attn::wait_for_stream();
+    const Args& a = c.a;
+    const long e = ((long)blockIdx.x * 256 + threadIdx.x) * 4;
+    const int lane = threadIdx.x & 31;
+    const int h = (int)(min(e, all - 4) / per_head);
+    for (int b0 = 0; b0 < a.batch; b0 += 32) {
+        int begin = 0, end = 0, slot = 0, count = 0;
+        if (b0 + lane < a.batch && row_of(a, b0 + lane, false, begin, end, slot)) count = segments(c, end - begin) - 1;
+        for (uint32_t m = __ballot_sync(0xffffffffu, count > 1 || (count == 1 && a.resume && a.resume[b0 + lane])); m; m &= m - 1) {
+            const int l = __ffs(m) - 1, b = b0 + l;
+            const int first = __shfl_sync(0xffffffffu, begin, l) / c.seg, n = __shfl_sync(0xffffffffu, count, l);
+            const int sl = __shfl_sync(0xffffffffu, slot, l);
+            if (e >= all) continue;
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (a.resume && a.resume[b]) {
+                float f[4];
+                load4(static_cast<const char*>(a.state) + (sl * all + e) * (a.sbf ? 2 : 4), 0, a.sbf, f);
+                s = make_float4(f[0], f[1], f[2], f[3]);
+                // (the main launch writes the slot when the row's last segment ends, maybe before its first begins)
+                __stcg(reinterpret_cast<float4*>(c.parts + (c.kept + first) * all + e), s);
+            }
+            float4* const part = reinterpret_cast<float4*>(c.parts + first * all + e);
+            const float2* const decay = c.part_decay + (long)first * a.H + h;
+            constexpr int U = 8;
+            for (int i0 = 0; i0 < n; i0 += U) {
+                float4 x[U];
+                float2 f[U];
+#pragma unroll
+                for (int i = 0; i < U; ++i)
+                    if (i0 + i < n) {
+                        x[i] = __ldcg(part + (i0 + i) * (all / 4));
+                        f[i] = __ldcg(decay + (long)(i0 + i) * a.H);
+                    }
+#pragma unroll
+                for (int i = 0; i < U; ++i)
+                    if (i0 + i < n) {
+                        s.x = fmaf(f[i].x, s.x, fmaf(f[i].y, s.x, x[i].x));
+                        s.y = fmaf(f[i].x, s.y, fmaf(f[i].y, s.y, x[i].y));
+                        s.z = fmaf(f[i].x, s.z, fmaf(f[i].y, s.z, x[i].z));
+                        s.w = fmaf(f[i].x, s.w, fmaf(f[i].y, s.w, x[i].w));
+                        __stcg(part + (i0 + i) * (all / 4), s);
+                    }
+            }
+        }
+    }
+}
+
+// Tokens of a segment (0: rows are not cut): so many that all tokens in one row would give each SM about
+// three units, and no fewer than 512 (a cut reads k and v twice, and keeps a state).
+static int segment_tokens(const rssm_linattn_dims* d, int n_tokens, int blocks, int sms) {
+    long many = 3L * sms / blocks;
+    if (many < 1) many = 1;
+    long seg = (n_tokens + many - 1) / many;
+    if (seg < 512) seg = 512;
+    seg = (seg + kC - 1) / kC * kC;
+    return seg >= n_tokens ? 0 : (int)seg;
+}
+
+static int head_blocks(const rssm_linattn_dims* d) {
+    const bool pair = d->value_dim == 64 && d->num_heads / d->num_k_heads % 2 == 0;
+    return pair ? d->num_heads / 2 : d->num_heads;
+}
+
+size_t chunk_workspace(const rssm_linattn_dims* d, int n_tokens) {
+    DeviceInfo di;
+    if (!device_info(&di)) return 0;
+    // (the largest over every smaller number of tokens: the count of kept states does not fall with it)
+    const int blocks = head_blocks(d);
+    long many = 3L * di.sm_count / blocks;
+    if (many < 1) many = 1;
+    const long kept = n_tokens <= 512 ? 0 : many < n_tokens / 512 ? many : n_tokens / 512;
+    return (size_t)kept * d->num_heads * ((size_t)d->value_dim * d->key_dim * 8 + 8) + (kept ? 256 : 0);
+}
+
+template <int N, int P, bool PAIR, int SP>
+static int launch(const rssm_linattn_dims* d, const ChunkArgs& c, const DeviceInfo& di, cudaStream_t st) {
+    CUtensorMap qm, km, vm;
+    memset(&qm, 0, sizeof qm);
+    const uint64_t rows = c.a.tokens, kw = (uint64_t)d->num_k_heads * N, vw = (uint64_t)d->num_heads * P;
+    if (!make_tmap_rows128(&qm, c.a.q, 2, rows, kw, kC, c.a.q_stride) ||
+        !make_tmap_rows128(&km, c.a.k, 2, rows, kw, kC, c.a.k_stride) ||
+        !make_tmap_rows128(&vm, c.a.v, 2, rows, vw, kC, c.a.v_stride))
+        return RSSM_ERR_CUDA;
+    auto run = [&](auto kernel, int smem) -> int {
+        if (smem > di.max_smem_optin) return RSSM_ERR_UNSUPPORTED;
+        if (!ensure_smem_limit((const void*)kernel, smem)) return RSSM_ERR_CUDA;
+        const long items = (long)c.units * c.blocks;
+        attn::launch_early(kernel, (int)(items < di.sm_count ? items : di.sm_count), dim3(kThreads), smem, st, c, qm, km, vm);
+        return launch_status();
+    };
+    if (c.seg) {
+        if (const int rc = run(chunk_kernel<N, P, PAIR, SP, false>, Chunk<N, P, PAIR, SP, false>::SMEM)) return rc;
+        const long all = (long)d->num_heads * P * N;
+        attn::launch_early(carry_kernel, (int)((all / 4 + 255) / 256), dim3(256), 0, st, c, all, P * N);
+        if (const int rc = launch_status()) return rc;
+    }
+    return run(chunk_kernel<N, P, PAIR, SP, true>, Chunk<N, P, PAIR, SP, true>::SMEM);
+}
+
+template <int N, int SP>
+static int launch_heads(const rssm_linattn_dims* d, const ChunkArgs& c, const DeviceInfo& di, cudaStream_t st) {
+    if (d->value_dim == 128) return launch<N, 128, false, SP>(d, c, di, st);
+    return c.blocks < d->num_heads ? launch<N, 64, true, SP>(d, c, di, st) : launch<N, 64, false, SP>(d, c, di, st);
+}
+
+int prompt_chunks(const rssm_linattn_dims* d, const Args& a, void* workspace, uint64_t wait_ns, cudaStream_t st) {
+    DeviceInfo di;
+    if (!device_info(&di)) return RSSM_ERR_CUDA;
+    ChunkArgs c{};
+    c.a = a;
+    c.blocks = head_blocks(d);
+    c.seg = segment_tokens(d, a.tokens, c.blocks, di.sm_count);
+    c.units = (c.seg ? a.tokens / c.seg : 0) + a.batch;
+    c.wait_ns = wait_ns;
+    if (c.seg) {
+        const size_t kept = a.tokens / c.seg;
+        c.kept = (int)kept;
+        c.part_decay = static_cast<float2*>(workspace);
+        c.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + (kept * a.H * 8 + 255) / 256 * 256);
+    }
+    // (a float32 state keeps 24 bits of a decayed value, a bf16 one 16)
+    if (d->key_dim == 64) return a.sbf ? launch_heads<64, 2>(d, c, di, st) : launch_heads<64, 3>(d, c, di, st);
+    return a.sbf ? launch_heads<128, 2>(d, c, di, st) : launch_heads<128, 3>(d, c, di, st);
+}
+
+}  // namespace linattn
+}  // namespace rssm

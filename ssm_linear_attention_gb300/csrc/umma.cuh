@@ -114,9 +114,12 @@ __device__ __forceinline__ uint64_t smem_desc_mnmajor(uint32_t start, uint32_t l
 }
 
 // kind::f16 with a choice of operand type (f16 or bf16, both the same) and of MN-major operands.
+__host__ __device__ constexpr uint32_t idesc_16bit(int M, int N, bool bf16, bool a_mn_major, bool b_mn_major) {
+    return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (a_mn_major ? 1u << 15 : 0u) |
+           (b_mn_major ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
 __host__ __device__ constexpr uint32_t idesc_16bit(int M, int N, bool bf16, bool mn_major) {
-    return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (mn_major ? (1u << 15) | (1u << 16) : 0u) |
-           ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+    return idesc_16bit(M, N, bf16, mn_major, mn_major);
 }
 
 // ------------------------------------------------------------------ MMA ----
@@ -129,6 +132,17 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint6
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+}
+
+// The same with A in the tensor memory: row m in lane m, two values of K a column.
+__device__ __forceinline__ void mma_bf16_tmem(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                              uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
         : "memory");
 }
 
