@@ -18,8 +18,8 @@
 // segments' own states (dS alone), one carries them on, and the main one begins each segment from its state.
 //
 // One CTA per SM takes units (segment, head or pair of heads). Warps have roles and meet at mbarriers:
-//   0-15 state, 16, 17, 20, 21 weights, 18, 19, 22, 23 decayed values, 24-27 output, 28 loads (TMA) and the list,
-//   29 products, 30 decays.
+//   0-15 state and output, 16, 17, 20, 21 weights, 18, 19, 22, 23 decayed values, 24 loads (TMA) and the list, 25 products,
+//   26, 27 decays.
 // What they issue (some 1600 cycles a chunk of 128 x 128) comes near what the chunk's bytes take, so float32 arithmetic is
 // in pairs (f32x2); and the roles' loops are kept short, since what streams through the instruction cache
 // instead of staying in it waits for it (waits inline and loops unrolled, 133 KB of code: 9000 cycles a chunk).
@@ -36,8 +36,7 @@ constexpr int kC = 64;             // tokens of a chunk
 constexpr int kBox = kC * 128;     // bytes of 64 columns of a chunk
 constexpr int kGates = 3;          // chunks whose decays are kept
 constexpr int kUnits = 4;          // units looked up ahead
-constexpr int kThreads = 1024;
-constexpr float kFix = 0x1p-40f;   // unit of the summed logarithms
+constexpr int kThreads = 896;
 
 struct ChunkArgs {
     Args a;
@@ -47,7 +46,7 @@ struct ChunkArgs {
     int seg;           // tokens of a segment, a multiple of 64; 0: rows are not cut
     int blocks;        // units of a segment: heads, or pairs of them
     int units;         // upper limit of the rows' segments
-    uint64_t wait_ns;
+    uint32_t wait_ns;
 };
 
 enum { kZero = 0, kSlot = 1, kPart = 2 };
@@ -73,8 +72,9 @@ struct Chunk {
     static constexpr int SMEM = ST * STAGE + REST + (VL == 64 ? 1024 : 0) + 1024;
     // tensor memory columns
     static constexpr uint32_t SCORE = 0, STATE = 64, DS = STATE + N, INTER = DS + N, INTRA = INTER + 64;
-    static constexpr int CONS = (OUT ? 8 : 0) + 4 + 16;  // warps that read the decays
-    static constexpr int UCONS = CONS + 2;              // and the list
+    static constexpr int CONS = (OUT ? 4 : 0) + 4 + 16;  // warps that read the decays
+    static constexpr int DECAYS = OUT || PAIR ? 2 : 1;  // warps that make them
+    static constexpr int UCONS = CONS + 1 + DECAYS;      // warps that follow the list
 };
 
 // Two float32 in a register pair.
@@ -110,10 +110,16 @@ __device__ __forceinline__ uint32_t pack2(f2 v) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(f.y), "f"(f.x));
     return r;
 }
-// v's next bf16 part; v becomes the (exact) rest.
-__device__ __forceinline__ uint32_t split2(f2& v) {
+// v's next bf16 part and the (exact) rest: v - h by a multiply-add that takes h's halves as they are.
+__device__ __forceinline__ uint32_t split2(f2 v, f2& rest) {
     const uint32_t h = pack2(v);
-    v = fma2(two(bf16_lo(h), bf16_hi(h)), two(-1.f, -1.f), v);
+    const float2 f = one_by_one(v);
+    float x, y;
+    asm("{\n\t.reg .b16 l, h, m;\n\tmov.b32 {l, h}, %2;\n\tmov.b16 m, 0xBF80;\n\t"
+        "fma.rn.f32.bf16 %0, l, m, %3;\n\tfma.rn.f32.bf16 %1, h, m, %4;\n\t}"
+        : "=f"(x), "=f"(y)
+        : "r"(h), "f"(f.x), "f"(f.y));
+    rest = two(x, y);
     return h;
 }
 
@@ -130,24 +136,94 @@ __constant__ float2 kPow2[32] = {
     {0x1.d5818e0000000p+0f, -0x1.822dbc0000000p-27f}, {0x1.dfc9740000000p+0f, -0x1.908c940000000p-25f}, {0x1.ea4afa0000000p+0f, 0x1.52486c0000000p-27f}, {0x1.f507660000000p+0f, -0x1.246eb00000000p-26f}
 };
 __device__ __forceinline__ float2 exp2_pair(long long x) {
-    const long long whole = x >> 40;
+    const int whole = (int)(x >> 40);
     if (whole < -160) return make_float2(0.f, 0.f);
     if (whole > 127) return make_float2(INFINITY, 0.f);
     const uint64_t frac = (uint64_t)x & ((1ull << 40) - 1);
     const float2 t = kPow2[frac >> 35];
-    const float r = (float)(frac & ((1ull << 35) - 1)) * (kFix * 0.693147180559945f);
+    const float r = (float)((uint32_t)(frac >> 3) & 0xffffffffu) * (0x1p-37f * 0.693147180559945f);
     const float e = r + r * r * (0.5f + r * (1.f / 6.f + r * (1.f / 24.f)));
     const float y = fmaf(t.x, e, t.y);
     const float hi = t.x + y, lo = y - (hi - t.x);
-    return make_float2(ldexpf(hi, (int)whole), ldexpf(lo, (int)whole));
+    const float a = __int_as_float(((whole >> 1) + 127) << 23), b = __int_as_float((whole - (whole >> 1) + 127) << 23);
+    return make_float2(hi * a * b, lo * a * b);
 }
-// log2(exp(g)) in units of 2^-40; +-2^14 for what is beyond (an infinity among it).
+// log2(exp(g)) in units of 2^-40 (2^14 at most, for an infinity too): g's significand times log2(e) as integers.
+// (Conversions between float32 and 64-bit integers go through the FP64 pipe, 64 cycles a warp each.)
 __device__ __forceinline__ long long log2_fixed(float g) {
-    const float top = 11356.5f;  // 2^14 ln 2, nearly
-    g = fminf(fmaxf(g, -top), top);
-    const float L = 1.44269502162933349609375f, l = 1.925963e-8f;  // log2(e) = L + l
-    const float hi = g * L, lo = fmaf(g, l, fmaf(g, L, -hi));
-    return __float2ll_rn(hi * 0x1p40f) + __float2ll_rn(lo * 0x1p40f);
+    g = fminf(fmaxf(g, -11356.5f), 11356.5f);  // (2^14 ln 2, nearly)
+    const uint32_t u = __float_as_uint(g) & 0x7fffffffu, e = u >> 23;
+    const uint32_t m = (u & 0x7fffffu) | 0x800000u;
+    // log2(e) 2^38 = 92 * 2^32 + 1428001966.05
+    const uint64_t P = (uint64_t)m * 1428001966u + ((uint64_t)(m * 92u) << 32);
+    const uint32_t down = 148u - e;  // g = m 2^(e - 150)
+    const long long x = down < 64 ? (long long)((P + (1ull << (down - 1))) >> down) : 0;
+    return g < 0.f ? -x : x;
+}
+__device__ __forceinline__ float fixed_to_float(long long x) {
+    return (float)(int)(x >> 40) + (float)(uint32_t)(x >> 8) * 0x1p-32f;
+}
+
+// Wait for phase `parity` of the barrier at shared address `bar`: false once `limit` ns went by, or another warp has
+// set the flag at `stop`; then the flag is set. try_wait sleeps, so a wait costs few instructions; and it is
+// spelled out, since a call's moves and saves at each of the waits would cost more room than the wait.
+__device__ __forceinline__ bool sleep_until(uint32_t bar, uint32_t parity, uint32_t stop, uint32_t limit) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b32 t0, t1, n;\n\t"
+        "mov.u32 %0, 1;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra DONE;\n\t"
+        "mov.u32 t0, %%globaltimer_lo;\n\t"
+        "AGAIN:\n\t"
+        "mov.u32 n, 64;\n\t"
+        "TRY:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra DONE;\n\t"
+        "sub.u32 n, n, 1;\n\t"
+        "setp.ne.u32 p, n, 0;\n\t"
+        "@p bra TRY;\n\t"
+        "ld.volatile.shared.u32 t1, [%3];\n\t"
+        "setp.ne.u32 p, t1, 0;\n\t"
+        "@p bra GIVE_UP;\n\t"
+        "mov.u32 t1, %%globaltimer_lo;\n\t"
+        "sub.u32 t1, t1, t0;\n\t"
+        "setp.lt.u32 p, t1, %4;\n\t"
+        "@p bra AGAIN;\n\t"
+        "GIVE_UP:\n\t"
+        "mov.u32 %0, 1;\n\t"
+        "st.volatile.shared.u32 [%3], %0;\n\t"
+        "mov.u32 %0, 0;\n\t"
+        "DONE:\n\t}"
+        : "=&r"(ok)
+        : "r"(bar), "r"(parity), "r"(stop), "r"(limit)
+        : "memory");
+    return ok != 0;
+}
+
+// The products and their commits, issued by the thread with leader != 0 and without a branch: what the whole warp knows
+// stays in its uniform registers, where the descriptors are wanted (moved there one by one from inside a branch, a
+// product took 65 cycles to issue).
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add, uint32_t leader) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"(leader)
+        : "memory");
+}
+__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add, uint32_t leader) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"(leader)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar, uint32_t leader) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar)),
+        "r"(leader)
+        : "memory");
 }
 
 // The segments of a row of n tokens.
@@ -164,18 +240,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     unsigned char* const smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     unsigned char* const vp = smem + ST * C::STAGE;  // V', its parts
     unsigned char* const sw = vp + SP * C::VB;       // W, two parts
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31;
+    // (through a shuffle: what depends on it is then known to be the warp's, and goes through the uniform registers)
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
 
     __shared__ uint64_t full[3], empty[3], gready[kGates], gfree[kGates], ufull[kUnits], ufree[kUnits];
-    __shared__ uint64_t sc_full, sc_free, w_ready, w_free, vp_ready, vp_free, ds_full, ds_free, s0_ready, s0_free,
-        o_full, o_free, drain;
+    __shared__ uint64_t sc_full, sc_free, w_ready, w_free, vp_ready[2], vp_free[2], st_full, ds_free, s0_ready, o_full, o_free,
+        drain;
     __shared__ uint32_t tmem_at;
     __shared__ int abort_flag;
     __shared__ Unit units[kUnits];
     __shared__ __align__(16) float4 gw[kGates][VH][kC];  // G (log2): whole part, rest; scale w
     __shared__ __align__(16) float ge[kGates][VH][kC];   // scale exp(G)
-    // a weight of a token of the second half on one of the first: exp(G_i - G_31) times scale exp(G_31 - G_j) w_j
-    __shared__ __align__(16) float gcol[kGates][VH][kC / 2], grow[kGates][VH][kC / 2];
     __shared__ float gd[kGates][VH][kC];                 // exp(G_end - G) w
     __shared__ float2 gam[kGates][VH];                   // exp(G_end) and its remainder
     // of each value row, chunk and 63 - first token whose value is not finite (of older chunks: behind its time)
@@ -188,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < kGates; ++i) {
-            mbar_init(&gready[i], 1);
+            mbar_init(&gready[i], VH);
             mbar_init(&gfree[i], C::CONS);
         }
         for (int i = 0; i < kUnits; ++i) {
@@ -199,29 +275,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&sc_free, 4);
         mbar_init(&w_ready, 4);
         mbar_init(&w_free, 1);
-        mbar_init(&vp_ready, 4);
-        mbar_init(&vp_free, 1);
-        mbar_init(&ds_full, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&vp_ready[i], 4);
+            mbar_init(&vp_free[i], 1);
+        }
+        mbar_init(&st_full, 1);
         mbar_init(&ds_free, 16);
         mbar_init(&s0_ready, 16);
-        mbar_init(&s0_free, 1);
         mbar_init(&o_full, 1);
-        mbar_init(&o_free, 4);
+        mbar_init(&o_free, 16);
         mbar_init(&drain, 1);
         fence_barrier_init();
         abort_flag = 0;
     }
-    if (OUT)
+    if (OUT) {
         for (int i = tid; i < 4 * C::VL; i += kThreads) odd[i / C::VL][i % C::VL] = 0;
-    if (warp == 29) umma::tmem_alloc(&tmem_at, 512);
+        for (int i = tid; i < 2 * C::WB / 16; i += kThreads) reinterpret_cast<uint4*>(sw)[i] = make_uint4(0, 0, 0, 0);
+        fence_async_smem();
+    }
+    if (warp == 25) umma::tmem_alloc(&tmem_at, 512);
     umma::fence_before_sync();
     __syncthreads();
     umma::fence_after_sync();
     const uint32_t tmem = tmem_at;
-    volatile int* const stop = &abort_flag;
+    const uint32_t stop = smem_addr(&abort_flag);
     auto await = [&](uint64_t* bar, uint32_t parity) {
-        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-        return wait_long(bar, parity, stop, c.wait_ns, a.dev_err);
+        return __all_sync(0xffffffffu, sleep_until(smem_addr(bar), parity, stop, c.wait_ns)) != 0;
+    };
+    auto unit_at = [&](int slot) {
+        Unit u = units[slot];
+        u.tok = __shfl_sync(0xffffffffu, u.tok, 0);
+        u.n = __shfl_sync(0xffffffffu, u.n, 0);
+        u.head = __shfl_sync(0xffffffffu, u.head, 0);
+        u.slot = __shfl_sync(0xffffffffu, u.slot, 0);
+        u.part = __shfl_sync(0xffffffffu, u.part, 0);
+        u.from = __shfl_sync(0xffffffffu, u.from, 0);
+        u.to = __shfl_sync(0xffffffffu, u.to, 0);
+        return u;
     };
     // one arrival of the warp
     auto arrive = [&](uint64_t* bar) {
@@ -231,16 +321,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     attn::wait_for_stream();
 
     if (warp < 16) {
-        // --------------------------------------------------------------- state
+        // ---------------------------------------------------- state and output
         constexpr int NS = N / 4;  // keys of a thread
         const int p = (warp & 3) * 32 + lane, n0 = (warp >> 2) * NS;
         const bool mine = p < C::VL;
         const uint32_t at = tmem + ((uint32_t)(warp & 3) << 21);
         const int vh = PAIR ? p >> 6 : 0;
-        Ring ur, gr, one, s0;
+        // of the output: tokens i0 .. i0 + 15 of a chunk; in bf16 two tokens of a lane become one token of two lanes, so
+        // that a lane stores 4 bytes
+        const int i0 = (warp >> 2) * 16, odd_lane = lane & 1, size = a.obf ? 2 : 4;
+        const uint32_t step = (uint32_t)(a.H * P * size);  // bytes of a token (64 of them: less than 2^32)
+        const uint32_t pick = odd_lane ? 0x3276 : 0x5410;
+        const long swap = odd_lane ? (long)step - 2 : 0, step2 = 2 * (long)step, out_step = kC * (long)step;
+        Ring ur, gr, one;
+        uint32_t k = 0;
         for (;;) {
             if (!await(&ufull[ur.slot], ur.parity)) break;
-            const Unit u = units[ur.slot];
+            const Unit u = unit_at(ur.slot);
             if (u.n < 0) break;
             f2 s[NS / 2];
             const long row = ((long)u.head * P + p) * N + n0, all = (long)a.H * P * N;
@@ -265,40 +362,104 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             bool ok = true;
-            for (int t = 0; t < u.n; t += kC) {
-                if (OUT) {
-                    ok = await(&s0_free, s0.parity ^ 1);
-                    if (!ok) break;
-                    umma::fence_after_sync();
-                    float hi[NS / 2], lo[NS / 2];
+            // (products that read the state's parts before have ended: st_full was waited for)
+            auto give_state = [&]() {
 #pragma unroll
-                    for (int x = 0; x < NS / 2; ++x) {
-                        f2 r = s[x];
-                        hi[x] = __uint_as_float(split2(r));
+                for (int i = 0; i < NS / 2; i += 8) {  // (pieces of 8: all of them at once do not fit the registers)
+                    float hi[8], lo[8];
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) {
+                        f2 r;
+                        hi[x] = __uint_as_float(split2(s[i + x], r));
                         lo[x] = __uint_as_float(pack2(r));
                     }
-                    umma::st_cols<NS / 2>(at + C::STATE + n0 / 2, hi);
-                    umma::st_cols<NS / 2>(at + C::STATE + N / 2 + n0 / 2, lo);
-                    umma::wait_st();
-                    umma::fence_before_sync();
-                    arrive(&s0_ready);
-                    s0.next(1);
+                    umma::st_cols<8>(at + C::STATE + n0 / 2 + i, hi);
+                    umma::st_cols<8>(at + C::STATE + N / 2 + n0 / 2 + i, lo);
                 }
-                ok = await(&gready[gr.slot], gr.parity) && await(&ds_full, one.parity);
+                umma::wait_st();
+                umma::fence_before_sync();
+                arrive(&s0_ready);
+            };
+            if (OUT) give_state();
+            char* to = static_cast<char*>(a.o) + (long)(u.tok + i0) * step + ((long)u.head * P + p) * size;
+#pragma unroll 1
+            for (int t = 0; t < u.n; t += kC, ++k) {
+                ok = await(&st_full, one.parity);
                 if (!ok) break;
                 const float2 f = gam[gr.slot][vh];
                 const f2 fx = two(f.x, f.x), fy = two(f.y, f.y);
                 umma::fence_after_sync();
 #pragma unroll
-                for (int i = 0; i < NS / 2; i += 8) {
-                    float d[16];
-                    umma::ld_cols<16>(at + C::DS + n0 + 2 * i, d);
+                for (int i = 0; i < NS / 2; i += 4) {
+                    float d[8];
+                    umma::ld_cols<8>(at + C::DS + n0 + 2 * i, d);
 #pragma unroll
-                    for (int x = 0; x < 8; ++x)
+                    for (int x = 0; x < 4; ++x)
                         s[i + x] = fma2(fx, s[i + x], fma2(fy, s[i + x], two(d[2 * x], d[2 * x + 1])));
                 }
                 umma::fence_before_sync();
                 arrive(&ds_free);
+                if (OUT) {
+                    if (t + kC < u.n) give_state();
+                    ok = await(&o_full, one.parity);
+                    if (!ok) break;
+                    umma::fence_after_sync();
+                    const int left = mine ? u.n - t - i0 : 0;
+                    const float* e = &ge[gr.slot][vh][i0];
+                    if (a.obf) {
+                        char* q = to + swap;
+                        int more = left - odd_lane;
+#pragma unroll 1
+                        for (int i = 0; i < 16; i += 8, more -= 8, e += 8) {
+                            float x[8], y[8];
+                            umma::ld_cols<8>(at + C::INTER + i0 + i, x);
+                            umma::ld_cols<8>(at + C::INTRA + vh * 64 + i0 + i, y);
+                            if (i) {
+                                umma::fence_before_sync();
+                                arrive(&o_free);
+                            }
+#pragma unroll
+                            for (int j = 0; j < 8; j += 4) {
+                                const float4 g = *reinterpret_cast<const float4*>(e + j);
+                                const uint32_t w0 = pack2(fma2(two(g.x, g.y), two(x[j], x[j + 1]), two(y[j], y[j + 1])));
+                                const uint32_t w1 = pack2(fma2(two(g.z, g.w), two(x[j + 2], x[j + 3]), two(y[j + 2], y[j + 3])));
+                                const uint32_t v0 = __shfl_xor_sync(0xffffffffu, w0, 1), v1 = __shfl_xor_sync(0xffffffffu, w1, 1);
+                                if (j < more) *reinterpret_cast<uint32_t*>(q) = __byte_perm(w0, v0, pick);
+                                q += step2;
+                                if (j + 2 < more) *reinterpret_cast<uint32_t*>(q) = __byte_perm(w1, v1, pick);
+                                q += step2;
+                            }
+                        }
+                    } else {
+                        char* q = to;
+#pragma unroll 1
+                        for (int i = 0; i < 16; i += 8) {
+                            float x[8], y[8];
+                            umma::ld_cols<8>(at + C::INTER + i0 + i, x);
+                            umma::ld_cols<8>(at + C::INTRA + vh * 64 + i0 + i, y);
+                            if (i) {
+                                umma::fence_before_sync();
+                                arrive(&o_free);
+                            }
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                if (i + j < left) *reinterpret_cast<float*>(q) = fmaf(e[i + j], x[j], y[j]);
+                                q += step2 >> 1;
+                            }
+                        }
+                    }
+                    if (__builtin_expect(any_odd[k & 3][0] | any_odd[k & 3][1] | any_odd[k & 3][2] | any_odd[k & 3][3], 0)) {
+                        // (values that are not finite were cleared: their rows' outputs from their token on are NaN)
+                        __syncwarp();
+                        const unsigned x = mine ? odd[k & 3][p] : 0;
+                        const int bad = x >> 6 == (k + 1) % (1u << 26) ? 63 - (int)(x & 63) : kC;
+                        const int end = min(16, u.n - t - i0);
+#pragma unroll 1
+                        for (int i = max(0, bad - i0); i < end; ++i) store1(to + (uint32_t)i * step, 0, a.obf, __uint_as_float(0x7fc00000u));
+                    }
+                    to += out_step;
+                    __syncwarp();
+                }
                 if (lane == 0) mbar_arrive_plain(&gfree[gr.slot]);
                 one.next(1);
                 gr.next(kGates);
@@ -332,71 +493,42 @@ __global__ void __launch_bounds__(kThreads, 1)
             Ring ur, gr, one;
             for (;;) {
                 if (!await(&ufull[ur.slot], ur.parity)) break;
-                const int n = units[ur.slot].n;
+                const int n = __shfl_sync(0xffffffffu, units[ur.slot].n, 0);
                 if (n < 0) break;
                 bool ok = true;
                 for (int t = 0; t < n; t += kC) {
                     ok = await(&gready[gr.slot], gr.parity) && await(&sc_full, one.parity) && await(&w_free, one.parity ^ 1);
                     if (!ok) break;
                     umma::fence_after_sync();
-                    const bool tail = t + kC > n;
+                    const int upto = min(i, n - 1 - t);  // (later tokens' weights are zero)
 #pragma unroll 1
                     for (int h = 0; h < VH; ++h) {
                         unsigned char* const row = sw + h * kBox + i * 128;
-                        auto put = [&](int j0, const uint32_t (&hi)[8], const uint32_t (&lo)[8]) {
+                        const float4 gi = gw[gr.slot][h][i];
+                        // (what the first half's tokens have of the second half's stays zero)
+#pragma unroll 1
+                        for (int j0 = half * 16; j0 < q * 32 + 32; j0 += 32) {
+                            float s[16];
+                            uint32_t hi[8], lo[8];
+                            umma::ld_cols<16>(at + j0, s);
+                            const float4* const gj = &gw[gr.slot][h][j0];
+                            const int see = upto - j0;
+#pragma unroll
+                            for (int x = 0; x < 16; x += 2) {
+                                const float4 g = gj[x], g2 = gj[x + 1];
+                                const f2 y = two(exp2_fast((gi.x - g.x) + (gi.y - g.y)), exp2_fast((gi.x - g2.x) + (gi.y - g2.y)));
+                                const uint32_t keep = see > x ? ~0u : see == x ? 0xffffu : 0u;
+                                f2 rest;
+                                hi[x / 2] = split2(mul2(mul2(y, two(g.z, g2.z)), two(s[x], s[x + 1])), rest) & keep;
+                                lo[x / 2] = pack2(rest) & keep;
+                            }
 #pragma unroll
                             for (int x = 0; x < 2; ++x) {
                                 unsigned char* const to = row + (((j0 / 8 + x) ^ (i & 7)) << 4);
                                 *reinterpret_cast<uint4*>(to) = make_uint4(hi[4 * x], hi[4 * x + 1], hi[4 * x + 2], hi[4 * x + 3]);
                                 *reinterpret_cast<uint4*>(to + C::WB) = make_uint4(lo[4 * x], lo[4 * x + 1], lo[4 * x + 2], lo[4 * x + 3]);
                             }
-                        };
-                        uint32_t hi[8], lo[8];
-                        float s[16];
-                        // the other half's columns: all of them earlier, or all later, tokens
-                        const int j1 = (q ? 0 : 32) + half * 16;
-                        if (q) {
-                            umma::ld_cols<16>(at + j1, s);
-                            const float rr = grow[gr.slot][h][lane];
-                            const f2 r = two(rr, rr);
-#pragma unroll
-                            for (int x = 0; x < 16; x += 4) {
-                                const float4 cj = *reinterpret_cast<const float4*>(&gcol[gr.slot][h][half * 16 + x]);
-                                f2 y = mul2(mul2(r, two(cj.x, cj.y)), two(s[x], s[x + 1]));
-                                f2 z = mul2(mul2(r, two(cj.z, cj.w)), two(s[x + 2], s[x + 3]));
-                                hi[x / 2] = split2(y);
-                                lo[x / 2] = pack2(y);
-                                hi[x / 2 + 1] = split2(z);
-                                lo[x / 2 + 1] = pack2(z);
-                            }
-                            if (tail) {
-#pragma unroll
-                                for (int x = 0; x < 8; ++x) {
-                                    const uint32_t keep = t + j1 + 2 * x + 1 < n ? ~0u : t + j1 + 2 * x < n ? 0xffffu : 0u;
-                                    hi[x] &= keep;
-                                    lo[x] &= keep;
-                                }
-                            }
-                        } else {
-#pragma unroll
-                            for (int x = 0; x < 8; ++x) hi[x] = lo[x] = 0;
                         }
-                        put(j1, hi, lo);
-                        // the same half's: up to the token itself
-                        const int j0 = q * 32 + half * 16;
-                        const float4 gi = gw[gr.slot][h][i];
-                        umma::ld_cols<16>(at + j0, s);
-                        const int upto = tail ? min(i, n - 1 - t) : i;
-#pragma unroll
-                        for (int x = 0; x < 16; x += 2) {
-                            const float4 g = gw[gr.slot][h][j0 + x], g2 = gw[gr.slot][h][j0 + x + 1];
-                            f2 y = two(exp2_fast((gi.x - g.x) + (gi.y - g.y)), exp2_fast((gi.x - g2.x) + (gi.y - g2.y)));
-                            y = mul2(mul2(y, two(g.z, g2.z)), two(s[x], s[x + 1]));
-                            const uint32_t keep = j0 + x + 1 <= upto ? ~0u : j0 + x <= upto ? 0xffffu : 0u;
-                            hi[x / 2] = split2(y) & keep;
-                            lo[x / 2] = pack2(y) & keep;
-                        }
-                        put(j0, hi, lo);
                     }
                     umma::fence_before_sync();
                     fence_async_smem();
@@ -420,55 +552,76 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t k = 0;
         for (;;) {
             if (!await(&ufull[ur.slot], ur.parity)) break;
-            const int n = units[ur.slot].n;
+            const int n = __shfl_sync(0xffffffffu, units[ur.slot].n, 0);
             if (n < 0) break;
             bool ok = true;
             for (int t = 0; t < n; t += kC, ++k) {
-                ok = await(&gready[gr.slot], gr.parity) && await(&full[st.slot], st.parity) && await(&vp_free, one.parity ^ 1);
+                ok = await(&gready[gr.slot], gr.parity) && await(&full[st.slot], st.parity);
                 if (!ok) break;
                 unsigned char* const sv = smem + st.slot * C::STAGE + 2 * C::QB;
                 const int cnt = n - t;
                 f2 probe = 0;  // becomes NaN where a value is not finite
+                // in two halves of 32 tokens, each as soon as the products with the chunk before have read it
 #pragma unroll 1
-                for (int e = vt; e < C::VB / 16; e += 128) {
-                    const int j = (e >> 3) & 63, h = PAIR ? e >> 9 : 0;
-                    const uint4 x = *reinterpret_cast<const uint4*>(sv + e * 16);
-                    const float d = gd[gr.slot][h][j];
-                    const f2 dd = two(d, d);
-                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                    uint32_t y[SP][4];
+                for (int half = 0; half < 2; ++half) {
+                    ok = await(&vp_free[half], one.parity ^ 1);
+                    if (!ok) break;
+                    // 16-byte pieces: tokens vt / 8 and + 16 of 64 columns, then of the next 64
+#pragma unroll 1
+                    for (int e = 0; e < C::VB / 4096; ++e) {
+                        const int at = (e >> 1) * kBox + half * 4096 + (e & 1) * 2048 + vt * 16;
+                        const uint4 in = *reinterpret_cast<const uint4*>(sv + at);
+                        const float d = gd[gr.slot][PAIR ? e >> 1 : 0][half * 32 + (e & 1) * 16 + (vt >> 3)];
+                        const f2 dd = two(d, d);
+                        const uint32_t w[4] = {in.x, in.y, in.z, in.w};
+                        uint32_t y[SP][4];
 #pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        const f2 v = two(bf16_lo(w[b]), bf16_hi(w[b]));
-                        if (OUT) probe = fma2(v, 0, probe);
-                        f2 r = mul2(v, dd);
+                        for (int b = 0; b < 4; ++b) {
+                            const f2 v = two(bf16_lo(w[b]), bf16_hi(w[b]));
+                            if (OUT) probe = fma2(v, 0, probe);
+                            f2 r = mul2(v, dd);
 #pragma unroll
-                        for (int z = 0; z + 1 < SP; ++z) y[z][b] = split2(r);
-                        y[SP - 1][b] = pack2(r);
+                            for (int z = 0; z + 1 < SP; ++z) {
+                                f2 rest;
+                                y[z][b] = split2(r, rest);
+                                r = rest;
+                            }
+                            y[SP - 1][b] = pack2(r);
+                        }
+#pragma unroll
+                        for (int z = 0; z < SP; ++z)
+                            *reinterpret_cast<uint4*>(vp + z * C::VB + at) = make_uint4(y[z][0], y[z][1], y[z][2], y[z][3]);
                     }
-                    const bool in = j < cnt;
-#pragma unroll
-                    for (int z = 0; z < SP; ++z)
-                        *reinterpret_cast<uint4*>(vp + z * C::VB + e * 16) =
-                            in ? make_uint4(y[z][0], y[z][1], y[z][2], y[z][3]) : make_uint4(0, 0, 0, 0);
+                    if (cnt < half * 32 + 32) {  // rows behind the last token may hold anything, and zero times that is not zero
+#pragma unroll 1
+                        for (int e = vt; e < (C::VB + C::QB) / 32; e += 128) {
+                            // (K's boxes stand before V's)
+                            unsigned char* const at = sv - C::QB + (e >> 8) * kBox + half * 4096 + (e & 255) * 16;
+                            if (half * 32 + ((e >> 3) & 31) < cnt) continue;
+                            *reinterpret_cast<uint4*>(at) = make_uint4(0, 0, 0, 0);
+                            if (at >= sv)
+                                for (int z = 0; z < SP; ++z)
+                                    *reinterpret_cast<uint4*>(vp + z * C::VB + (at - sv)) = make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                    if (half == 0) {
+                        fence_async_smem();
+                        arrive(&vp_ready[0]);
+                    }
                 }
-                if (cnt < kC) {  // rows behind the last token may hold anything, and zero times that is not zero
-                    for (int e = vt; e < C::VB / 16; e += 128)
-                        if (((e >> 3) & 63) >= cnt) *reinterpret_cast<uint4*>(sv + e * 16) = make_uint4(0, 0, 0, 0);
-                    unsigned char* const sk = sv - C::QB;
-                    for (int e = vt; e < C::QB / 16; e += 128)
-                        if (((e >> 3) & 63) >= cnt) *reinterpret_cast<uint4*>(sk + e * 16) = make_uint4(0, 0, 0, 0);
-                }
+                if (!ok) break;
                 if (OUT) {
                     // A value that is not finite must not meet the zero weights of the tokens before it: it is
                     // cleared, and the output makes NaN of its row from its token on.
                     const float2 pr = one_by_one(probe);
                     const bool bad = __any_sync(0xffffffffu, pr.x + pr.y != 0.f);
                     if (__builtin_expect(bad, 0)) {
+#pragma unroll 1
                         for (int e = vt; e < C::VB / 16; e += 128) {
                             const int j = (e >> 3) & 63, col = (e >> 9) * 64 + ((e & 7) ^ (j & 7)) * 8;
                             if (j >= cnt) continue;
                             uint16_t* const v = reinterpret_cast<uint16_t*>(sv + e * 16);
+#pragma unroll 1
                             for (int x = 0; x < 8; ++x)
                                 if ((v[x] & 0x7f80) == 0x7f80) {
                                     atomicMax(&odd[k & 3][col + x], ((k + 1) << 6) | (63 - j));
@@ -479,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) any_odd[k & 3][me] = bad;
                 }
                 fence_async_smem();
-                arrive(&vp_ready);
+                arrive(&vp_ready[1]);
                 if (lane == 0) mbar_arrive_plain(&gfree[gr.slot]);
                 one.next(1);
                 gr.next(kGates);
@@ -489,82 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             arrive(&ufree[ur.slot]);
             ur.next(kUnits);
         }
-    } else if (warp < 28) {
-        // -------------------------------------------------------------- output
-        if (OUT) {
-            const int p = (warp & 3) * 32 + lane, odd_lane = lane & 1;
-            const uint32_t at = tmem + ((uint32_t)(warp & 3) << 21);
-            const int vh = PAIR ? p >> 6 : 0;
-            const int size = a.obf ? 2 : 4;
-            const uint32_t step = (uint32_t)(a.H * P * size);  // bytes of a token (64 of them: less than 2^32)
-            Ring ur, gr, one;
-            uint32_t k = 0;
-            for (;;) {
-                if (!await(&ufull[ur.slot], ur.parity)) break;
-                const Unit u = units[ur.slot];
-                if (u.n < 0) break;
-                bool ok = true;
-                for (int t = 0; t < u.n; t += kC, ++k) {
-                    ok = await(&gready[gr.slot], gr.parity) && await(&o_full, one.parity);
-                    if (!ok) break;
-                    umma::fence_after_sync();
-                    const int cnt = p < C::VL ? min(kC, u.n - t) : 0;
-                    int bad = kC;
-                    if (__builtin_expect(any_odd[k & 3][0] | any_odd[k & 3][1] | any_odd[k & 3][2] | any_odd[k & 3][3], 0) && p < C::VL) {
-                        const unsigned x = odd[k & 3][p];
-                        if (x >> 6 == (k + 1) % (1u << 26)) bad = 63 - (x & 63);
-                    }
-                    char* const out = static_cast<char*>(a.o) + (long)(u.tok + t) * step + ((long)u.head * P + p) * size;
-#pragma unroll 1
-                    for (int i0 = 0; i0 < kC; i0 += 16) {
-                        float x[16], y[16];
-                        umma::ld_cols<16>(at + C::INTER + i0, x);
-                        umma::ld_cols<16>(at + C::INTRA + vh * 64 + i0, y);
-                        f2 o[8];
-#pragma unroll
-                        for (int i = 0; i < 16; i += 4) {
-                            const float4 e = *reinterpret_cast<const float4*>(&ge[gr.slot][vh][i0 + i]);
-                            o[i / 2] = fma2(two(e.x, e.y), two(x[i], x[i + 1]), two(y[i], y[i + 1]));
-                            o[i / 2 + 1] = fma2(two(e.z, e.w), two(x[i + 2], x[i + 3]), two(y[i + 2], y[i + 3]));
-                        }
-                        if (__builtin_expect(bad < kC, 0)) {
-#pragma unroll
-                            for (int i = 0; i < 16; i += 2) {
-                                const float nan = __uint_as_float(0x7fc00000u);
-                                const float2 f = one_by_one(o[i / 2]);
-                                o[i / 2] = two(i0 + i >= bad ? nan : f.x, i0 + i + 1 >= bad ? nan : f.y);
-                            }
-                        }
-                        if (a.obf) {
-                            // two tokens of a lane for one token of two lanes: a lane stores 4 bytes
-#pragma unroll
-                            for (int i = 0; i < 16; i += 2) {
-                                const uint32_t w = pack2(o[i / 2]), v = __shfl_xor_sync(0xffffffffu, w, 1);
-                                const uint32_t both = odd_lane ? __byte_perm(v, w, 0x7632) : __byte_perm(w, v, 0x5410);
-                                if (i0 + i + odd_lane < cnt)
-                                    *reinterpret_cast<uint32_t*>(out + (uint32_t)(i0 + i) * step + (odd_lane ? (long)step - 2 : 0)) = both;
-                            }
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 16; i += 2) {
-                                const float2 f = one_by_one(o[i / 2]);
-                                if (i0 + i < cnt) *reinterpret_cast<float*>(out + (uint32_t)(i0 + i) * step) = f.x;
-                                if (i0 + i + 1 < cnt) *reinterpret_cast<float*>(out + (uint32_t)(i0 + i + 1) * step) = f.y;
-                            }
-                        }
-                    }
-                    umma::fence_before_sync();
-                    arrive(&o_free);
-                    if (lane == 0) mbar_arrive_plain(&gfree[gr.slot]);
-                    one.next(1);
-                    gr.next(kGates);
-                }
-                if (!ok) break;
-                arrive(&ufree[ur.slot]);
-                ur.next(kUnits);
-            }
-        }
-    } else if (warp == 28) {
+    } else if (warp == 24) {
         // ------------------------------------------------- the list, and loads
         const uint64_t pol = policy_evict_first();
         Ring ur, st;
@@ -672,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) units[ur.slot].n = -1;
             arrive(&ufull[ur.slot]);
         }
-    } else if (warp == 29) {
+    } else if (warp == 25) {
         // ------------------------------------------------------------ products
         constexpr uint32_t i_score = umma::idesc_16bit(128, kC, true, false, false);
         constexpr uint32_t i_ds = umma::idesc_16bit(128, N, true, true, true);
@@ -682,6 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t at = smem_addr(smem), vp_at = smem_addr(vp);
         const uint64_t wd = umma::smem_desc_swizzle128(smem_addr(sw), 16, 1024);
         const uint64_t vpd = umma::smem_desc_swizzle128(vp_at, lbo, 1024);
+        const uint32_t leader = elect_one();
         Ring ur, st, ahead, sc, v1, s1, w1;
         // scores of the chunk whose loads are in stage `ahead`
         auto scores = [&]() {
@@ -689,42 +768,43 @@ __global__ void __launch_bounds__(kThreads, 1)
             umma::fence_after_sync();
             const uint64_t qd = umma::smem_desc_swizzle128(at + ahead.slot * C::STAGE, 16, 1024);
             const uint64_t kd = umma::smem_desc_swizzle128(at + ahead.slot * C::STAGE + C::QB, 16, 1024);
-            if (elect_one()) {
 #pragma unroll
-                for (int x = 0; x < N / 16; ++x) {
-                    const int off = (x / 4 * kBox + x % 4 * 32) >> 4;
-                    umma::mma_bf16(tmem + C::SCORE, qd + off, kd + off, i_score, x > 0);
-                }
-                umma::commit_to(&sc_full);
+            for (int x = 0; x < N / 16; ++x) {
+                const int off = (x / 4 * kBox + x % 4 * 32) >> 4;
+                mma(tmem + C::SCORE, qd + off, kd + off, i_score, x > 0, leader);
             }
-            __syncwarp();
+            commit(&sc_full, leader);
             sc.next(1);
             ahead.next(ST);
             return true;
         };
         for (;;) {
             if (!await(&ufull[ur.slot], ur.parity)) break;
-            const int n = units[ur.slot].n;
+            const int n = __shfl_sync(0xffffffffu, units[ur.slot].n, 0);
             if (n < 0) break;
             bool ok = !OUT || scores();
             for (int t = 0; t < n && ok; t += kC) {
                 const uint32_t stage = at + st.slot * C::STAGE;
-                ok = await(&vp_ready, v1.parity) && await(&ds_free, v1.parity ^ 1);
-                if (!ok) break;
-                umma::fence_after_sync();
+                ok = await(&ds_free, v1.parity ^ 1);
                 const uint64_t kt = umma::smem_desc_swizzle128(stage + C::QB, kBox, 1024);
-                if (elect_one()) {
+#pragma unroll 1
+                for (int half = 0; half < 2 && ok; ++half) {
+                    ok = await(&vp_ready[half], v1.parity);
+                    if (!ok) break;
+                    umma::fence_after_sync();
 #pragma unroll
                     for (int z = 0; z < SP; ++z)
 #pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            umma::mma_bf16(tmem + C::DS, vpd + ((z * C::VB + x * 2048) >> 4), kt + (x * 2048 >> 4), i_ds,
-                                           z + x > 0);
-                    umma::commit_to(&ds_full);
-                    umma::commit_to(&vp_free);
-                    if (!OUT) umma::commit_to(&empty[st.slot]);
+                        for (int x = 0; x < 2; ++x)
+                            mma(tmem + C::DS, vpd + ((z * C::VB + half * 4096 + x * 2048) >> 4),
+                                kt + ((half * 4096 + x * 2048) >> 4), i_ds, half + z + x > 0, leader);
+                    commit(&vp_free[half], leader);
+                    if (!OUT && half) {
+                        commit(&st_full, leader);
+                        commit(&empty[st.slot], leader);
+                    }
                 }
-                __syncwarp();
+                if (!ok) break;
                 v1.next(1);
                 if (OUT) {
                     if (t + kC < n) ok = scores();
@@ -732,33 +812,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     umma::fence_after_sync();
                     const uint64_t qd = umma::smem_desc_swizzle128(stage, 16, 1024);
-                    if (elect_one()) {
 #pragma unroll
-                        for (int z = 0; z < 2; ++z)
+                    for (int z = 0; z < 2; ++z)
 #pragma unroll
-                            for (int x = 0; x < N / 16; ++x)
-                                umma::mma_bf16_tmem(tmem + C::INTER, tmem + C::STATE + z * N / 2 + x * 8,
-                                                    qd + ((x / 4 * kBox + x % 4 * 32) >> 4), i_inter, z + x > 0);
-                        umma::commit_to(&s0_free);
-                    }
-                    __syncwarp();
+                        for (int x = 0; x < N / 16; ++x)
+                            mma_tmem(tmem + C::INTER, tmem + C::STATE + z * N / 2 + x * 8,
+                                     qd + ((x / 4 * kBox + x % 4 * 32) >> 4), i_inter, z + x > 0, leader);
+                    commit(&st_full, leader);  // (of dS as well, which was issued before)
                     s1.next(1);
                     ok = await(&w_ready, w1.parity);
                     if (!ok) break;
                     umma::fence_after_sync();
                     const uint64_t vd = umma::smem_desc_swizzle128(stage + 2 * C::QB, lbo, 1024);
-                    if (elect_one()) {
 #pragma unroll
-                        for (int z = 0; z < 2; ++z)
+                    for (int z = 0; z < 2; ++z)
 #pragma unroll
-                            for (int x = 0; x < 4; ++x)
-                                umma::mma_bf16(tmem + C::INTRA, vd + (x * 2048 >> 4), wd + ((z * C::WB + x * 32) >> 4), i_intra,
-                                               z + x > 0);
-                        umma::commit_to(&o_full);
-                        umma::commit_to(&w_free);
-                        umma::commit_to(&empty[st.slot]);
-                    }
-                    __syncwarp();
+                        for (int x = 0; x < 4; ++x)
+                            mma(tmem + C::INTRA, vd + (x * 2048 >> 4), wd + ((z * C::WB + x * 32) >> 4), i_intra, z + x > 0, leader);
+                    commit(&o_full, leader);
+                    commit(&w_free, leader);
+                    commit(&empty[st.slot], leader);
                     w1.next(1);
                 }
                 st.next(ST);
@@ -767,107 +840,102 @@ __global__ void __launch_bounds__(kThreads, 1)
             arrive(&ufree[ur.slot]);
             ur.next(kUnits);
         }
-    } else if (warp == 30) {
-        // -------------------------------------------------------------- decays
+    } else if (warp < 26 + C::DECAYS) {
+        // ------- decays: a warp for each head of a pair, else two that take chunks in turn (of a segment's own state: one)
+        const int h = PAIR ? warp & 1 : 0, turn = warp & 1;
+        constexpr bool TURNS = OUT && !PAIR;
+        uint32_t k = 0;
         Ring ur, gr;
         for (;;) {
             if (!await(&ufull[ur.slot], ur.parity)) break;
-            const Unit u = units[ur.slot];
+            const Unit u = unit_at(ur.slot);
             if (u.n < 0) break;
-            float g[VH][2], w[VH][2];  // of tokens 2 lane, 2 lane + 1
-            long long total[VH];
-            bool total_bad[VH];
+            // tokens lane and lane + 32 of a chunk, loaded a chunk ahead
+            const float* gp = a.g + ((long)u.tok + lane) * a.g_stride + u.head + h;
+            const float* wp = a.w ? a.w + ((long)u.tok + lane) * a.w_stride + u.head + h : nullptr;
+            float g0, g1, w0, w1;
             auto load = [&](int t) {
-#pragma unroll
-                for (int h = 0; h < VH; ++h)
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const int j = t + 2 * lane + x;
-                        g[h][x] = w[h][x] = 0.f;
-                        if (j < u.n) {
-                            const long row = u.tok + j;
-                            g[h][x] = a.g[row * a.g_stride + u.head + h];
-                            w[h][x] = a.w ? a.w[row * a.w_stride + u.head + h] : 1.f;
-                        }
-                    }
-            };
-#pragma unroll
-            for (int h = 0; h < VH; ++h) {
-                total[h] = 0;
-                total_bad[h] = false;
-            }
-            load(0);
-            bool ok = true;
-            for (int t = 0; t < u.n; t += kC) {
-                long long x0[VH], x1[VH];
-                float w0[VH], w1[VH];
-                uint32_t bad0[VH], bad1[VH];
-#pragma unroll
-                for (int h = 0; h < VH; ++h) {
-                    x0[h] = log2_fixed(g[h][0]);
-                    x1[h] = log2_fixed(g[h][1]);
-                    bad0[h] = __ballot_sync(0xffffffffu, g[h][0] != g[h][0]);
-                    bad1[h] = __ballot_sync(0xffffffffu, g[h][1] != g[h][1]);
-                    w0[h] = w[h][0];
-                    w1[h] = w[h][1];
+                g0 = g1 = w0 = w1 = 0.f;
+                if (t + lane < u.n) {
+                    g0 = gp[t * a.g_stride];
+                    w0 = wp ? wp[t * a.w_stride] : 1.f;
                 }
-                if (t + kC < u.n) load(t + kC);
+                if (t + lane + 32 < u.n) {
+                    g1 = gp[(t + 32) * a.g_stride];
+                    w1 = wp ? wp[(t + 32) * a.w_stride] : 1.f;
+                }
+            };
+            long long total = 0;
+            bool total_bad = false;
+            bool ok = true;
+            int t = 0;
+            if (TURNS && (k & 1) != turn) {
+                t = kC;
+                gr.next(kGates);
+            }
+            k += (u.n + kC - 1) / kC;
+            load(t);
+#pragma unroll 1
+            while (t < u.n) {
+                const float gx[2] = {g0, g1}, wx[2] = {w0, w1};
+                load(t + (TURNS ? 2 * kC : kC));
                 ok = await(&gfree[gr.slot], gr.parity ^ 1);
                 if (!ok) break;
-#pragma unroll
-                for (int h = 0; h < VH; ++h) {
-                    long long sum = x0[h] + x1[h];
+                const float nan = __uint_as_float(0x7fc00000u);
+                long long G0 = 0, end = 0;
+                bool bad = false;
+#pragma unroll 1
+                for (int x = 0; x < 2; ++x) {
+                    const float gv = x ? gx[1] : gx[0], wv = x ? wx[1] : wx[0];
+                    long long sum = log2_fixed(gv);
 #pragma unroll
                     for (int o = 1; o < 32; o <<= 1) {
                         const long long y = __shfl_up_sync(0xffffffffu, sum, o);
                         if (lane >= o) sum += y;
                     }
-                    const long long G1 = sum, G0 = sum - x1[h], end = __shfl_sync(0xffffffffu, sum, 31);
-                    const uint32_t before = (1u << lane) - 1, either = bad0[h] | bad1[h];
-                    const bool nan0 = (either & before) || (bad0[h] >> lane & 1), nan1 = nan0 || (bad1[h] >> lane & 1);
-                    const float nan = __uint_as_float(0x7fc00000u);
-                    // (a difference of two sums must not lose its bits to their size: a reset is 2^14)
-                    const long long whole0 = G0 >> 40, whole1 = G1 >> 40;
-                    const float s0 = w0[h] * a.scale, s1 = w1[h] * a.scale;
-                    gw[gr.slot][h][2 * lane] = make_float4((float)whole0, __ll2float_rn(G0 - (whole0 << 40)) * kFix, s0, 0.f);
-                    gw[gr.slot][h][2 * lane + 1] = make_float4((float)whole1, __ll2float_rn(G1 - (whole1 << 40)) * kFix, s1, 0.f);
-                    *reinterpret_cast<float2*>(&ge[gr.slot][h][2 * lane]) =
-                        make_float2(nan0 ? nan : a.scale * exp2_fast(__ll2float_rn(G0) * kFix),
-                                    nan1 ? nan : a.scale * exp2_fast(__ll2float_rn(G1) * kFix));
-                    gd[gr.slot][h][2 * lane] = exp2_fast(__ll2float_rn(end - G0) * kFix) * w0[h];
-                    gd[gr.slot][h][2 * lane + 1] = exp2_fast(__ll2float_rn(end - G1) * kFix) * w1[h];
-                    const long long mid = __shfl_sync(0xffffffffu, sum, 15);
-                    if (lane < 16)
-                        *reinterpret_cast<float2*>(&gcol[gr.slot][h][2 * lane]) =
-                            make_float2(exp2_fast(__ll2float_rn(mid - G0) * kFix) * s0, exp2_fast(__ll2float_rn(mid - G1) * kFix) * s1);
-                    else
-                        *reinterpret_cast<float2*>(&grow[gr.slot][h][2 * lane - 32]) =
-                            make_float2(exp2_fast(__ll2float_rn(G0 - mid) * kFix), exp2_fast(__ll2float_rn(G1 - mid) * kFix));
-                    total[h] += end;
+                    sum += end;
+                    const uint32_t bads = __ballot_sync(0xffffffffu, gv != gv);
+                    const bool after = bad || (bads & (2u << lane) - 1);  // (a NaN is here or before)
+                    bad |= bads != 0;
+                    // (the whole part apart: a difference of two sums must not lose its bits to their size; a reset is 2^14)
+                    gw[gr.slot][h][x * 32 + lane] = make_float4((float)(int)(sum >> 40), (float)(uint32_t)(sum >> 8) * 0x1p-32f,
+                                                                wv * a.scale, 0.f);
+                    ge[gr.slot][h][x * 32 + lane] = after ? nan : a.scale * exp2_fast(fixed_to_float(sum));
+                    if (x == 0) G0 = sum;
+                    end = __shfl_sync(0xffffffffu, sum, 31);
+                    if (x == 1) {
+                        gd[gr.slot][h][32 + lane] = exp2_fast(fixed_to_float(end - sum)) * wv;
+                        gd[gr.slot][h][lane] = exp2_fast(fixed_to_float(end - G0)) * wx[0];
+                    }
+                }
+                if (lane == 0) gam[gr.slot][h] = bad ? make_float2(nan, nan) : exp2_pair(end);
+                if (!OUT) {
                     // (a sum that leaves the range of exponents stays there)
                     const long long most = 1ll << 61;
-                    total[h] = total[h] < -most ? -most : total[h] > most ? most : total[h];
-                    total_bad[h] |= either != 0;
-                    if (lane == h) gam[gr.slot][h] = either ? make_float2(nan, nan) : exp2_pair(end);
+                    total = max(-most, min(most, total + end));
+                    total_bad |= bad;
                 }
                 arrive(&gready[gr.slot]);
                 gr.next(kGates);
+                t += kC;
+                if (TURNS) {
+                    if (t < u.n) gr.next(kGates);  // (the other warp's)
+                    t += kC;
+                }
             }
             if (!ok) break;
-            if (!OUT && lane < VH) {
-                const long long sum = VH == 2 && lane ? total[VH - 1] : total[0];
-                const bool bad = VH == 2 && lane ? total_bad[VH - 1] : total_bad[0];
-                const float nan = __uint_as_float(0x7fc00000u);
-                c.part_decay[(long)u.part * a.H + u.head + lane] = bad ? make_float2(nan, nan) : exp2_pair(sum);
-            }
+            if (!OUT && lane == 0)
+                c.part_decay[(long)u.part * a.H + u.head + h] =
+                    total_bad ? make_float2(__uint_as_float(0x7fc00000u), __uint_as_float(0x7fc00000u)) : exp2_pair(total);
             arrive(&ufree[ur.slot]);
             ur.next(kUnits);
         }
     }
     __syncthreads();
     if (abort_flag) {
+        if (tid == 0) set_dev_err(a.dev_err, RSSM_DEVERR_TIMEOUT);
         // A wait ran out: no copy and no product may still be in flight when the CTA ends.
-        if (warp == 29) {
+        if (warp == 25) {
             if (elect_one()) umma::commit_to(&drain);
             __syncwarp();
             mbar_wait_bounded(&drain, 0, RSSM_WAIT_NS / 100);
@@ -877,7 +945,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncthreads();
     }
-    if (warp == 29) umma::tmem_dealloc(tmem, 512);
+    if (warp == 25) umma::tmem_dealloc(tmem, 512);
 }
 
 // parts[s] = the state after segment s, from its own state and what came before. A thread has four
@@ -996,7 +1064,7 @@ int prompt_chunks(const rssm_linattn_dims* d, const Args& a, void* workspace, ui
     c.blocks = head_blocks(d);
     c.seg = segment_tokens(d, a.tokens, c.blocks, di.sm_count);
     c.units = (c.seg ? a.tokens / c.seg : 0) + a.batch;
-    c.wait_ns = wait_ns;
+    c.wait_ns = (uint32_t)wait_ns;
     if (c.seg) {
         const size_t kept = a.tokens / c.seg;
         c.kept = (int)kept;
