@@ -201,6 +201,12 @@ __device__ __forceinline__ bool sleep_until(uint32_t bar, uint32_t parity, uint3
     return ok != 0;
 }
 
+// Stores under a predicate instead of a branch (a branch and its reconvergence cost three instructions for each).
+__device__ __forceinline__ void store_if(bool on, char* to, uint32_t v) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %0, 0;\n\t@p st.global.b32 [%1], %2;\n\t}" ::"r"((uint32_t)on), "l"(to), "r"(v)
+                 : "memory");
+}
+
 // The products and their commits, issued by the thread with leader != 0 and without a branch: what the whole warp knows
 // stays in its uniform registers, where the descriptors are wanted (moved there one by one from inside a branch, a
 // product took 65 cycles to issue).
@@ -424,9 +430,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 const uint32_t w0 = pack2(fma2(two(g.x, g.y), two(x[j], x[j + 1]), two(y[j], y[j + 1])));
                                 const uint32_t w1 = pack2(fma2(two(g.z, g.w), two(x[j + 2], x[j + 3]), two(y[j + 2], y[j + 3])));
                                 const uint32_t v0 = __shfl_xor_sync(0xffffffffu, w0, 1), v1 = __shfl_xor_sync(0xffffffffu, w1, 1);
-                                if (j < more) *reinterpret_cast<uint32_t*>(q) = __byte_perm(w0, v0, pick);
+                                store_if(j < more, q, __byte_perm(w0, v0, pick));
                                 q += step2;
-                                if (j + 2 < more) *reinterpret_cast<uint32_t*>(q) = __byte_perm(w1, v1, pick);
+                                store_if(j + 2 < more, q, __byte_perm(w1, v1, pick));
                                 q += step2;
                             }
                         }
@@ -443,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
 #pragma unroll
                             for (int j = 0; j < 8; ++j) {
-                                if (i + j < left) *reinterpret_cast<float*>(q) = fmaf(e[i + j], x[j], y[j]);
+                                store_if(i + j < left, q, __float_as_uint(fmaf(e[i + j], x[j], y[j])));
                                 q += step2 >> 1;
                             }
                         }
@@ -497,20 +503,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (n < 0) break;
                 bool ok = true;
                 for (int t = 0; t < n; t += kC) {
-                    ok = await(&gready[gr.slot], gr.parity) && await(&sc_full, one.parity) && await(&w_free, one.parity ^ 1);
+                    ok = await(&gready[gr.slot], gr.parity) && await(&sc_full, one.parity);
                     if (!ok) break;
                     umma::fence_after_sync();
                     const int upto = min(i, n - 1 - t);  // (later tokens' weights are zero)
+                    // 16 columns of the first 32 tokens', in b = 0, and 16 of the second's (for the first's, they stay zero)
+                    float s[2][16];
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+                        if (b <= q) umma::ld_cols<16>(at + half * 16 + b * 32, s[b]);
+                    umma::fence_before_sync();
+                    arrive(&sc_free);
 #pragma unroll 1
                     for (int h = 0; h < VH; ++h) {
                         unsigned char* const row = sw + h * kBox + i * 128;
                         const float4 gi = gw[gr.slot][h][i];
-                        // (what the first half's tokens have of the second half's stays zero)
-#pragma unroll 1
-                        for (int j0 = half * 16; j0 < q * 32 + 32; j0 += 32) {
-                            float s[16];
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) {
+                            if (b > q) continue;
                             uint32_t hi[8], lo[8];
-                            umma::ld_cols<16>(at + j0, s);
+                            const int j0 = half * 16 + b * 32;
                             const float4* const gj = &gw[gr.slot][h][j0];
                             const int see = upto - j0;
 #pragma unroll
@@ -519,8 +531,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 const f2 y = two(exp2_fast((gi.x - g.x) + (gi.y - g.y)), exp2_fast((gi.x - g2.x) + (gi.y - g2.y)));
                                 const uint32_t keep = see > x ? ~0u : see == x ? 0xffffu : 0u;
                                 f2 rest;
-                                hi[x / 2] = split2(mul2(mul2(y, two(g.z, g2.z)), two(s[x], s[x + 1])), rest) & keep;
+                                hi[x / 2] = split2(mul2(mul2(y, two(g.z, g2.z)), two(s[b][x], s[b][x + 1])), rest) & keep;
                                 lo[x / 2] = pack2(rest) & keep;
+                            }
+                            if (h + b == 0) {
+                                ok = await(&w_free, one.parity ^ 1);
+                                if (!ok) break;
                             }
 #pragma unroll
                             for (int x = 0; x < 2; ++x) {
@@ -529,14 +545,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 *reinterpret_cast<uint4*>(to + C::WB) = make_uint4(lo[4 * x], lo[4 * x + 1], lo[4 * x + 2], lo[4 * x + 3]);
                             }
                         }
+                        if (!ok) break;
                     }
-                    umma::fence_before_sync();
+                    if (!ok) break;
                     fence_async_smem();
                     arrive(&w_ready);
-                    if (lane == 0) {
-                        mbar_arrive_plain(&sc_free);
-                        mbar_arrive_plain(&gfree[gr.slot]);
-                    }
+                    if (lane == 0) mbar_arrive_plain(&gfree[gr.slot]);
                     one.next(1);
                     gr.next(kGates);
                 }
