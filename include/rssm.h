@@ -862,11 +862,11 @@ typedef struct rssm_linattn_inputs {
     float scale;
 } rssm_linattn_inputs;
 
-/* Bytes of device workspace rssm_linattn_prompt needs for n_tokens tokens (states of the
- * parts of long rows; 0 where rows are not cut). It need not be initialised, and holds nothing
- * between calls; one stream at a time. The size goes by the dims, n_tokens and the current
- * device's SMs, and does not shrink as n_tokens grows. 0 for dims that rssm_linattn_prompt
- * refuses. */
+/* Bytes of device workspace rssm_linattn_prompt needs for n_tokens tokens: counters, and states of
+ * the parts of long rows (0 for float32 activations). It must be zero-filled before its first use, and
+ * again after a call that set RSSM_DEVERR_TIMEOUT; every other call leaves its counters at zero. One
+ * stream at a time. The size goes by the dims but the batch, n_tokens and the current device's SMs, and
+ * does not shrink as n_tokens grows. 0 for dims that rssm_linattn_prompt refuses. */
 size_t rssm_linattn_workspace_size(const rssm_linattn_dims* dims, int32_t n_tokens);
 
 /* rssm_linattn_prompt -- a whole list of tokens through the recurrence.

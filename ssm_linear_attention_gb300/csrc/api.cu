@@ -114,8 +114,8 @@ std::once_flag g_encode_once;
 EncodeTiledFn g_encode = nullptr;
 }  // namespace
 
-bool make_tmap_rows128(CUtensorMap* out, const void* base, int elem_bytes, uint64_t rows,
-                       uint64_t cols, uint32_t box_rows, uint64_t row_elems) {
+bool make_tmap_box(CUtensorMap* out, const void* base, int elem_bytes, uint64_t rows, uint64_t cols,
+                   uint64_t row_elems, uint32_t box_rows, uint32_t box_cols, bool swizzle128) {
     std::call_once(g_encode_once, []() {
         void* f = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -128,15 +128,22 @@ bool make_tmap_rows128(CUtensorMap* out, const void* base, int elem_bytes, uint6
     });
     if (!g_encode || (elem_bytes != 2 && elem_bytes != 4)) return false;
     const cuuint64_t dims[2] = {cols, rows};
-    const cuuint64_t strides[1] = {(row_elems ? row_elems : cols) * (cuuint64_t)elem_bytes};
-    const cuuint32_t box[2] = {(cuuint32_t)(128 / elem_bytes), box_rows};
+    const cuuint64_t strides[1] = {row_elems * (cuuint64_t)elem_bytes};
+    const cuuint32_t box[2] = {box_cols, box_rows};
     const cuuint32_t estr[2] = {1, 1};
     const CUresult r = g_encode(out, elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                      : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
                                 2, const_cast<void*>(base), dims, strides, box, estr,
-                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
+}
+
+bool make_tmap_rows128(CUtensorMap* out, const void* base, int elem_bytes, uint64_t rows,
+                       uint64_t cols, uint32_t box_rows, uint64_t row_elems) {
+    return make_tmap_box(out, base, elem_bytes, rows, cols, row_elems ? row_elems : cols, box_rows,
+                         (uint32_t)(128 / elem_bytes), true);
 }
 
 // ----------------------------------------------------------------------------

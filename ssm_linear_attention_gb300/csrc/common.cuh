@@ -145,6 +145,14 @@ __device__ __forceinline__ void tma_store_2d(const void* tmap, int x, int y, con
                  : "memory");
 }
 
+// 1-D bulk copy shared -> global in this thread's bulk group (bytes % 16 == 0, both addresses 16-byte
+// aligned).
+__device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
+                 "r"(smem_addr(src)), "r"(bytes)
+                 : "memory");
+}
+
 __device__ __forceinline__ void bulk_commit() {
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
@@ -152,6 +160,11 @@ __device__ __forceinline__ void bulk_commit() {
 // Wait until this thread's committed bulk stores have finished reading shared memory.
 __device__ __forceinline__ void bulk_wait_read_all() {
     asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+
+// Wait until this thread's committed bulk stores are complete.
+__device__ __forceinline__ void bulk_wait_all() {
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 // Make this thread's generic-proxy shared-memory stores visible to the async proxy

@@ -55,8 +55,11 @@ bool pick_pipe(const DeviceInfo& di, int stage_bytes, int warp_scratch, int tile
 // elem_bytes) elements -- one 128-byte row segment per box row -- with the 128-byte
 // shared-memory swizzle (16-byte chunk j of box row r lands at chunk j ^ (r % 8)).
 // false when the driver offers no encoder or rejects the arguments.
+// (make_tmap_box: boxes of box_rows x box_cols elements, with that swizzle or none.)
 // row_elems: elements between rows (0: cols), times elem_bytes a multiple of 16.
 bool make_tmap_rows128(CUtensorMap* out, const void* base, int elem_bytes, uint64_t rows,
                        uint64_t cols, uint32_t box_rows, uint64_t row_elems = 0);
+bool make_tmap_box(CUtensorMap* out, const void* base, int elem_bytes, uint64_t rows, uint64_t cols,
+                   uint64_t row_elems, uint32_t box_rows, uint32_t box_cols, bool swizzle128);
 
 }  // namespace rssm

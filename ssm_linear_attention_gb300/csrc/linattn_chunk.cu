@@ -17,14 +17,14 @@
 // A long row is cut into segments where rows and heads alone do not fill the GPU: one launch makes the
 // segments' own states (dS alone), one carries them on, and the main one begins each segment from its state.
 //
-// One CTA per SM takes units (segment, head or pair of heads). Warps have roles and meet at mbarriers:
-//   0-15 state and output, 16, 17, 20, 21 weights, 18, 19, 22, 23 decayed values, 24 loads (TMA) and the list, 25 products,
-//   26, 27 decays.
+// One CTA per SM takes units (segment, head or pair of heads). Warps have roles and meet at mbarriers; of a role with
+// several warps one waits there and the others at the role's barrier, since waiting at an mbarrier is a loop (28 warps in
+// it took half of the issue slots):
+//   0-15 state, decayed values and output, 16, 17, 20, 21 weights, 18 products, 19 loads (TMA) and the list, 22, 23 decays.
+//   (Warp w issues from the SM's part w % 4, and the weights' lanes bind them to two of the parts.)
 // What they issue (some 1600 cycles a chunk of 128 x 128) comes near what the chunk's bytes take, so float32 arithmetic is
 // in pairs (f32x2); and the roles' loops are kept short, since what streams through the instruction cache
 // instead of staying in it waits for it (waits inline and loops unrolled, 133 KB of code: 9000 cycles a chunk).
-#include <cstring>
-
 #include "linattn.cuh"
 #include "umma.cuh"
 #include "warps.cuh"
@@ -36,7 +36,7 @@ constexpr int kC = 64;             // tokens of a chunk
 constexpr int kBox = kC * 128;     // bytes of 64 columns of a chunk
 constexpr int kGates = 3;          // chunks whose decays are kept
 constexpr int kUnits = 4;          // units looked up ahead
-constexpr int kThreads = 896;
+constexpr int kThreads = 768;
 
 struct ChunkArgs {
     Args a;
@@ -47,6 +47,7 @@ struct ChunkArgs {
     int blocks;        // units of a segment: heads, or pairs of them
     int units;         // upper limit of the rows' segments
     uint32_t wait_ns;
+    unsigned* claims;  // next item of those not dealt, CTAs that are done
 };
 
 enum { kZero = 0, kSlot = 1, kPart = 2 };
@@ -67,12 +68,13 @@ struct Chunk {
     static constexpr int QB = N / 64 * kBox, VB = VL / 64 * kBox;
     static constexpr int STAGE = 2 * QB + VB;
     static constexpr int WB = OUT ? VH * kBox : 0;      // one part of W
-    static constexpr int REST = SP * VB + 2 * WB;
+    static constexpr int OB = OUT ? 16 * 2048 : 0;      // output: 16 tokens of 32 values for each of 16 warps
+    static constexpr int REST = SP * VB + 2 * WB + OB;
     static constexpr int ST = REST + 3 * STAGE <= 216 * 1024 ? 3 : 2;
     static constexpr int SMEM = ST * STAGE + REST + (VL == 64 ? 1024 : 0) + 1024;
     // tensor memory columns
     static constexpr uint32_t SCORE = 0, STATE = 64, DS = STATE + N, INTER = DS + N, INTRA = INTER + 64;
-    static constexpr int CONS = (OUT ? 4 : 0) + 4 + 16;  // warps that read the decays
+    static constexpr int CONS = (OUT ? 4 : 0) + 16;  // warps that read the decays
     static constexpr int DECAYS = OUT || PAIR ? 2 : 1;  // warps that make them
     static constexpr int UCONS = CONS + 1 + DECAYS;      // warps that follow the list
 };
@@ -201,10 +203,17 @@ __device__ __forceinline__ bool sleep_until(uint32_t bar, uint32_t parity, uint3
     return ok != 0;
 }
 
-// Stores under a predicate instead of a branch (a branch and its reconvergence cost three instructions for each).
-__device__ __forceinline__ void store_if(bool on, char* to, uint32_t v) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %0, 0;\n\t@p st.global.b32 [%1], %2;\n\t}" ::"r"((uint32_t)on), "l"(to), "r"(v)
-                 : "memory");
+// Barrier ID of a role's THREADS threads: true where ok is on all of them.
+template <int ID, int THREADS>
+__device__ __forceinline__ bool all_of(bool ok) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.and.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)ok), "n"(ID), "n"(THREADS)
+        : "memory");
+    return r != 0;
 }
 
 // The products and their commits, issued by the thread with leader != 0 and without a branch: what the whole warp knows
@@ -238,7 +247,8 @@ __device__ __forceinline__ int segments(const ChunkArgs& c, int n) { return c.se
 template <int N, int P, bool PAIR, int SP, bool OUT>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_kernel(const __grid_constant__ ChunkArgs c, const __grid_constant__ CUtensorMap qmap,
-                 const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+                 const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                 const __grid_constant__ CUtensorMap omap) {
     using C = Chunk<N, P, PAIR, SP, OUT>;
     constexpr int VH = C::VH, ST = C::ST;
     const Args& a = c.a;
@@ -246,13 +256,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     unsigned char* const smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     unsigned char* const vp = smem + ST * C::STAGE;  // V', its parts
     unsigned char* const sw = vp + SP * C::VB;       // W, two parts
+    unsigned char* const so = sw + 2 * C::WB;        // output
     const int tid = threadIdx.x, lane = tid & 31;
     // (through a shuffle: what depends on it is then known to be the warp's, and goes through the uniform registers)
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
 
     __shared__ uint64_t full[3], empty[3], gready[kGates], gfree[kGates], ufull[kUnits], ufree[kUnits];
-    __shared__ uint64_t sc_full, sc_free, w_ready, w_free, vp_ready[2], vp_free[2], st_full, ds_free, s0_ready, o_full, o_free,
-        drain;
+    __shared__ uint64_t sc_full, sc_free, w_ready, w_free, vp_ready, st_full, s0_ready, o_full, o_free, drain;
     __shared__ uint32_t tmem_at;
     __shared__ int abort_flag;
     __shared__ Unit units[kUnits];
@@ -262,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ float2 gam[kGates][VH];                   // exp(G_end) and its remainder
     // of each value row, chunk and 63 - first token whose value is not finite (of older chunks: behind its time)
     __shared__ unsigned odd[4][C::VL];
-    __shared__ int any_odd[4][4];
+    __shared__ int any_odd[4];
 
     if (tid == 0) {
         for (int i = 0; i < 3; ++i) {
@@ -281,12 +291,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&sc_free, 4);
         mbar_init(&w_ready, 4);
         mbar_init(&w_free, 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&vp_ready[i], 4);
-            mbar_init(&vp_free[i], 1);
-        }
+        mbar_init(&vp_ready, 16);
         mbar_init(&st_full, 1);
-        mbar_init(&ds_free, 16);
         mbar_init(&s0_ready, 16);
         mbar_init(&o_full, 1);
         mbar_init(&o_free, 16);
@@ -296,10 +302,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (OUT) {
         for (int i = tid; i < 4 * C::VL; i += kThreads) odd[i / C::VL][i % C::VL] = 0;
+        if (tid < 4) any_odd[tid] = 0;
         for (int i = tid; i < 2 * C::WB / 16; i += kThreads) reinterpret_cast<uint4*>(sw)[i] = make_uint4(0, 0, 0, 0);
         fence_async_smem();
     }
-    if (warp == 25) umma::tmem_alloc(&tmem_at, 512);
+    if (warp == 18) umma::tmem_alloc(&tmem_at, 512);
     umma::fence_before_sync();
     __syncthreads();
     umma::fence_after_sync();
@@ -327,22 +334,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     attn::wait_for_stream();
 
     if (warp < 16) {
-        // ---------------------------------------------------- state and output
+        // ------------------------------------ state, decayed values and output
         constexpr int NS = N / 4;  // keys of a thread
         const int p = (warp & 3) * 32 + lane, n0 = (warp >> 2) * NS;
         const bool mine = p < C::VL;
         const uint32_t at = tmem + ((uint32_t)(warp & 3) << 21);
         const int vh = PAIR ? p >> 6 : 0;
-        // of the output: tokens i0 .. i0 + 15 of a chunk; in bf16 two tokens of a lane become one token of two lanes, so
-        // that a lane stores 4 bytes
-        const int i0 = (warp >> 2) * 16, odd_lane = lane & 1, size = a.obf ? 2 : 4;
+        // of the output: tokens i0 .. i0 + 15 of a chunk
+        const int i0 = (warp >> 2) * 16, size = a.obf ? 2 : 4;
         const uint32_t step = (uint32_t)(a.H * P * size);  // bytes of a token (64 of them: less than 2^32)
-        const uint32_t pick = odd_lane ? 0x3276 : 0x5410;
-        const long swap = odd_lane ? (long)step - 2 : 0, step2 = 2 * (long)step, out_step = kC * (long)step;
-        Ring ur, gr, one;
+        unsigned char* const mine_out = so + warp * 2048 + lane * size;
+        Ring ur, gr, one, gv, sv;
         uint32_t k = 0;
         for (;;) {
-            if (!await(&ufull[ur.slot], ur.parity)) break;
+            if (!all_of<1, 512>(warp != 0 || await(&ufull[ur.slot], ur.parity))) break;
             const Unit u = unit_at(ur.slot);
             if (u.n < 0) break;
             f2 s[NS / 2];
@@ -386,11 +391,77 @@ __global__ void __launch_bounds__(kThreads, 1)
                 umma::fence_before_sync();
                 arrive(&s0_ready);
             };
+            // The decayed values of chunk k1 (tokens t on), two pieces of 8 for each thread. (The products with those before
+            // have ended.)
+            auto make_values = [&](int t, uint32_t k1) {
+                unsigned char* const raw = smem + sv.slot * C::STAGE + 2 * C::QB + tid * 16;
+                const int cnt = u.n - t, j = tid >> 3;
+                f2 probe = 0;  // becomes NaN where a value is not finite
+#pragma unroll 1
+                for (int box = 0; box < C::VL / 64; ++box) {
+                    const uint4 in = *reinterpret_cast<const uint4*>(raw + box * kBox);
+                    const float d = gd[gv.slot][PAIR ? box : 0][j];
+                    const f2 dd = two(d, d);
+                    const uint32_t w[4] = {in.x, in.y, in.z, in.w};
+                    uint32_t y[SP][4];
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        const f2 v = two(bf16_lo(w[b]), bf16_hi(w[b]));
+                        if (OUT) probe = fma2(v, 0, probe);
+                        f2 r = mul2(v, dd);
+#pragma unroll
+                        for (int z = 0; z + 1 < SP; ++z) {
+                            f2 rest;
+                            y[z][b] = split2(r, rest);
+                            r = rest;
+                        }
+                        y[SP - 1][b] = pack2(r);
+                    }
+#pragma unroll
+                    for (int z = 0; z < SP; ++z)
+                        *reinterpret_cast<uint4*>(vp + z * C::VB + box * kBox + tid * 16) = make_uint4(y[z][0], y[z][1], y[z][2], y[z][3]);
+                }
+                if (j >= cnt) {  // rows behind the last token may hold anything, and zero times that is not zero
+                    const uint4 none = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+                    for (int box = 0; box < C::VL / 64; ++box) {
+                        *reinterpret_cast<uint4*>(raw + box * kBox) = none;
+                        for (int z = 0; z < SP; ++z) *reinterpret_cast<uint4*>(vp + z * C::VB + box * kBox + tid * 16) = none;
+                    }
+                    for (int box = 0; box < N / 64; ++box) *reinterpret_cast<uint4*>(raw - C::QB + box * kBox) = none;  // (K)
+                } else if (OUT) {
+                    // A value that is not finite must not meet the zero weights of the tokens before it: it is
+                    // cleared, and the output makes NaN of its row from its token on.
+                    const float2 pr = one_by_one(probe);
+                    if (__builtin_expect(pr.x + pr.y != 0.f, 0)) {
+#pragma unroll 1
+                        for (int e = 0; e < C::VL / 8; ++e) {
+                            uint16_t* const v = reinterpret_cast<uint16_t*>(raw + (e >> 3) * kBox) + (e & 7);
+                            if ((*v & 0x7f80) != 0x7f80) continue;
+                            const int col = (e >> 3) * 64 + ((tid & 7) ^ (j & 7)) * 8 + (e & 7);
+                            atomicMax(&odd[k1 & 3][col], ((k1 + 1) << 6) | (63 - j));
+                            *v = 0;
+                            any_odd[k1 & 3] = k1 + 1;
+                        }
+                    }
+                }
+                fence_async_smem();
+                umma::fence_before_sync();
+                arrive(&vp_ready);
+                gv.next(kGates);
+                sv.next(ST);
+            };
+            auto inputs = [&]() { return await(&gready[gv.slot], gv.parity) && await(&full[sv.slot], sv.parity); };
+            ok = all_of<1, 512>(warp != 0 || inputs());
+            if (!ok) break;
+            make_values(0, k);
             if (OUT) give_state();
-            char* to = static_cast<char*>(a.o) + (long)(u.tok + i0) * step + ((long)u.head * P + p) * size;
+            // token i0 + lane's 32 values of this warp
+            char* to = static_cast<char*>(a.o) + (long)(u.tok + i0 + lane) * step + ((long)u.head * P + p - lane) * size;
 #pragma unroll 1
             for (int t = 0; t < u.n; t += kC, ++k) {
-                ok = await(&st_full, one.parity);
+                const bool more = t + kC < u.n;
+                ok = all_of<1, 512>(warp != 0 || (await(&st_full, one.parity) && (!more || inputs())));
                 if (!ok) break;
                 const float2 f = gam[gr.slot][vh];
                 const f2 fx = two(f.x, f.x), fy = two(f.y, f.y);
@@ -403,67 +474,66 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int x = 0; x < 4; ++x)
                         s[i + x] = fma2(fx, s[i + x], fma2(fy, s[i + x], two(d[2 * x], d[2 * x + 1])));
                 }
-                umma::fence_before_sync();
-                arrive(&ds_free);
+                if (more) {
+                    make_values(t + kC, k + 1);
+                    if (OUT) give_state();
+                }
                 if (OUT) {
-                    if (t + kC < u.n) give_state();
-                    ok = await(&o_full, one.parity);
+                    ok = all_of<1, 512>(warp != 0 || await(&o_full, one.parity));
                     if (!ok) break;
                     umma::fence_after_sync();
-                    const int left = mine ? u.n - t - i0 : 0;
                     const float* e = &ge[gr.slot][vh][i0];
-                    if (a.obf) {
-                        char* q = to + swap;
-                        int more = left - odd_lane;
+                    unsigned char* put = mine_out;
+                    bulk_wait_read_all();  // (the chunk before's)
+                    __syncwarp();
 #pragma unroll 1
-                        for (int i = 0; i < 16; i += 8, more -= 8, e += 8) {
-                            float x[8], y[8];
-                            umma::ld_cols<8>(at + C::INTER + i0 + i, x);
-                            umma::ld_cols<8>(at + C::INTRA + vh * 64 + i0 + i, y);
-                            if (i) {
-                                umma::fence_before_sync();
-                                arrive(&o_free);
-                            }
+                    for (int i = 0; i < 16; i += 8, e += 8) {
+                        float x[8], y[8];
+                        umma::ld_cols<8>(at + C::INTER + i0 + i, x);
+                        umma::ld_cols<8>(at + C::INTRA + vh * 64 + i0 + i, y);
+                        if (i) {
+                            umma::fence_before_sync();
+                            arrive(&o_free);
+                        }
+                        if (a.obf) {
 #pragma unroll
                             for (int j = 0; j < 8; j += 4) {
                                 const float4 g = *reinterpret_cast<const float4*>(e + j);
                                 const uint32_t w0 = pack2(fma2(two(g.x, g.y), two(x[j], x[j + 1]), two(y[j], y[j + 1])));
                                 const uint32_t w1 = pack2(fma2(two(g.z, g.w), two(x[j + 2], x[j + 3]), two(y[j + 2], y[j + 3])));
-                                const uint32_t v0 = __shfl_xor_sync(0xffffffffu, w0, 1), v1 = __shfl_xor_sync(0xffffffffu, w1, 1);
-                                store_if(j < more, q, __byte_perm(w0, v0, pick));
-                                q += step2;
-                                store_if(j + 2 < more, q, __byte_perm(w1, v1, pick));
-                                q += step2;
+                                uint16_t* const to16 = reinterpret_cast<uint16_t*>(put + j * 64);
+                                to16[0] = (uint16_t)w0;
+                                to16[32] = (uint16_t)(w0 >> 16);
+                                to16[64] = (uint16_t)w1;
+                                to16[96] = (uint16_t)(w1 >> 16);
                             }
-                        }
-                    } else {
-                        char* q = to;
-#pragma unroll 1
-                        for (int i = 0; i < 16; i += 8) {
-                            float x[8], y[8];
-                            umma::ld_cols<8>(at + C::INTER + i0 + i, x);
-                            umma::ld_cols<8>(at + C::INTRA + vh * 64 + i0 + i, y);
-                            if (i) {
-                                umma::fence_before_sync();
-                                arrive(&o_free);
-                            }
+                            put += 8 * 64;
+                        } else {
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                store_if(i + j < left, q, __float_as_uint(fmaf(e[i + j], x[j], y[j])));
-                                q += step2 >> 1;
-                            }
+                            for (int j = 0; j < 8; ++j) *reinterpret_cast<float*>(put + j * 128) = fmaf(e[j], x[j], y[j]);
+                            put += 8 * 128;
                         }
                     }
-                    if (__builtin_expect(any_odd[k & 3][0] | any_odd[k & 3][1] | any_odd[k & 3][2] | any_odd[k & 3][3], 0)) {
+                    if (__builtin_expect(any_odd[k & 3] == (int)(k + 1), 0)) {
                         // (values that are not finite were cleared: their rows' outputs from their token on are NaN)
-                        __syncwarp();
                         const unsigned x = mine ? odd[k & 3][p] : 0;
                         const int bad = x >> 6 == (k + 1) % (1u << 26) ? 63 - (int)(x & 63) : kC;
-                        const int end = min(16, u.n - t - i0);
 #pragma unroll 1
-                        for (int i = max(0, bad - i0); i < end; ++i) store1(to + (uint32_t)i * step, 0, a.obf, __uint_as_float(0x7fc00000u));
+                        for (int i = max(0, bad - i0); i < 16; ++i) store1(mine_out + i * 32 * size, 0, a.obf, __uint_as_float(0x7fc00000u));
                     }
-                    to += out_step;
+                    // one box of 16 tokens (stores from the registers, with their addresses and exchanges between lanes, are twice
+                    // the instructions); where the row ends inside, its tokens one by one
+                    fence_async_smem();
+                    __syncwarp();
+                    const int left = u.n - t - i0;
+                    if (!mine || left <= 0) {
+                    } else if (left >= 16) {
+                        if (lane == 0) tma_store_2d(&omap, u.head * P + p, u.tok + t + i0, so + warp * 2048);
+                    } else if (lane < left) {
+                        bulk_s2g(to, so + warp * 2048 + lane * 32 * size, 32 * size);
+                    }
+                    bulk_commit();
+                    to += (long)kC * step;
                     __syncwarp();
                 }
                 if (lane == 0) mbar_arrive_plain(&gfree[gr.slot]);
@@ -490,7 +560,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             arrive(&ufree[ur.slot]);
             ur.next(kUnits);
         }
-    } else if (warp < 24 && (warp & 2) == 0) {
+        if (OUT) bulk_wait_all();
+    } else if ((warp & 2) == 0) {
         // ------------------------------------------------------------- weights
         if (OUT) {
             // a token a thread, its row of W and its lane of the scores, in two warps: each has 16 of every 32 columns
@@ -498,12 +569,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t at = tmem + ((uint32_t)q << 21) + C::SCORE;
             Ring ur, gr, one;
             for (;;) {
-                if (!await(&ufull[ur.slot], ur.parity)) break;
+                if (!all_of<2, 128>(warp != 16 || await(&ufull[ur.slot], ur.parity))) break;
                 const int n = __shfl_sync(0xffffffffu, units[ur.slot].n, 0);
                 if (n < 0) break;
                 bool ok = true;
                 for (int t = 0; t < n; t += kC) {
-                    ok = await(&gready[gr.slot], gr.parity) && await(&sc_full, one.parity);
+                    ok = all_of<2, 128>(warp != 16 || (await(&gready[gr.slot], gr.parity) && await(&sc_full, one.parity)));
                     if (!ok) break;
                     umma::fence_after_sync();
                     const int upto = min(i, n - 1 - t);  // (later tokens' weights are zero)
@@ -535,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 lo[x / 2] = pack2(rest) & keep;
                             }
                             if (h + b == 0) {
-                                ok = await(&w_free, one.parity ^ 1);
+                                ok = all_of<2, 128>(warp != 16 || await(&w_free, one.parity ^ 1));
                                 if (!ok) break;
                             }
 #pragma unroll
@@ -559,104 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ur.next(kUnits);
             }
         }
-    } else if (warp < 24) {
-        // ------------------------------------------------------ decayed values
-        const int me = (warp & 1) + (warp >> 2 & 1) * 2, vt = me * 32 + lane;
-        Ring ur, gr, st, one;
-        uint32_t k = 0;
-        for (;;) {
-            if (!await(&ufull[ur.slot], ur.parity)) break;
-            const int n = __shfl_sync(0xffffffffu, units[ur.slot].n, 0);
-            if (n < 0) break;
-            bool ok = true;
-            for (int t = 0; t < n; t += kC, ++k) {
-                ok = await(&gready[gr.slot], gr.parity) && await(&full[st.slot], st.parity);
-                if (!ok) break;
-                unsigned char* const sv = smem + st.slot * C::STAGE + 2 * C::QB;
-                const int cnt = n - t;
-                f2 probe = 0;  // becomes NaN where a value is not finite
-                // in two halves of 32 tokens, each as soon as the products with the chunk before have read it
-#pragma unroll 1
-                for (int half = 0; half < 2; ++half) {
-                    ok = await(&vp_free[half], one.parity ^ 1);
-                    if (!ok) break;
-                    // 16-byte pieces: tokens vt / 8 and + 16 of 64 columns, then of the next 64
-#pragma unroll 1
-                    for (int e = 0; e < C::VB / 4096; ++e) {
-                        const int at = (e >> 1) * kBox + half * 4096 + (e & 1) * 2048 + vt * 16;
-                        const uint4 in = *reinterpret_cast<const uint4*>(sv + at);
-                        const float d = gd[gr.slot][PAIR ? e >> 1 : 0][half * 32 + (e & 1) * 16 + (vt >> 3)];
-                        const f2 dd = two(d, d);
-                        const uint32_t w[4] = {in.x, in.y, in.z, in.w};
-                        uint32_t y[SP][4];
-#pragma unroll
-                        for (int b = 0; b < 4; ++b) {
-                            const f2 v = two(bf16_lo(w[b]), bf16_hi(w[b]));
-                            if (OUT) probe = fma2(v, 0, probe);
-                            f2 r = mul2(v, dd);
-#pragma unroll
-                            for (int z = 0; z + 1 < SP; ++z) {
-                                f2 rest;
-                                y[z][b] = split2(r, rest);
-                                r = rest;
-                            }
-                            y[SP - 1][b] = pack2(r);
-                        }
-#pragma unroll
-                        for (int z = 0; z < SP; ++z)
-                            *reinterpret_cast<uint4*>(vp + z * C::VB + at) = make_uint4(y[z][0], y[z][1], y[z][2], y[z][3]);
-                    }
-                    if (cnt < half * 32 + 32) {  // rows behind the last token may hold anything, and zero times that is not zero
-#pragma unroll 1
-                        for (int e = vt; e < (C::VB + C::QB) / 32; e += 128) {
-                            // (K's boxes stand before V's)
-                            unsigned char* const at = sv - C::QB + (e >> 8) * kBox + half * 4096 + (e & 255) * 16;
-                            if (half * 32 + ((e >> 3) & 31) < cnt) continue;
-                            *reinterpret_cast<uint4*>(at) = make_uint4(0, 0, 0, 0);
-                            if (at >= sv)
-                                for (int z = 0; z < SP; ++z)
-                                    *reinterpret_cast<uint4*>(vp + z * C::VB + (at - sv)) = make_uint4(0, 0, 0, 0);
-                        }
-                    }
-                    if (half == 0) {
-                        fence_async_smem();
-                        arrive(&vp_ready[0]);
-                    }
-                }
-                if (!ok) break;
-                if (OUT) {
-                    // A value that is not finite must not meet the zero weights of the tokens before it: it is
-                    // cleared, and the output makes NaN of its row from its token on.
-                    const float2 pr = one_by_one(probe);
-                    const bool bad = __any_sync(0xffffffffu, pr.x + pr.y != 0.f);
-                    if (__builtin_expect(bad, 0)) {
-#pragma unroll 1
-                        for (int e = vt; e < C::VB / 16; e += 128) {
-                            const int j = (e >> 3) & 63, col = (e >> 9) * 64 + ((e & 7) ^ (j & 7)) * 8;
-                            if (j >= cnt) continue;
-                            uint16_t* const v = reinterpret_cast<uint16_t*>(sv + e * 16);
-#pragma unroll 1
-                            for (int x = 0; x < 8; ++x)
-                                if ((v[x] & 0x7f80) == 0x7f80) {
-                                    atomicMax(&odd[k & 3][col + x], ((k + 1) << 6) | (63 - j));
-                                    v[x] = 0;
-                                }
-                        }
-                    }
-                    if (lane == 0) any_odd[k & 3][me] = bad;
-                }
-                fence_async_smem();
-                arrive(&vp_ready[1]);
-                if (lane == 0) mbar_arrive_plain(&gfree[gr.slot]);
-                one.next(1);
-                gr.next(kGates);
-                st.next(ST);
-            }
-            if (!ok) break;
-            arrive(&ufree[ur.slot]);
-            ur.next(kUnits);
-        }
-    } else if (warp == 24) {
+    } else if (warp == 19) {
         // ------------------------------------------------- the list, and loads
         const uint64_t pol = policy_evict_first();
         Ring ur, st;
@@ -688,39 +662,42 @@ __global__ void __launch_bounds__(kThreads, 1)
             return true;
         };
         if (OUT) {
-            // a lane looks up one unit of the next 32
+            // Half of the items are dealt, item blockIdx.x and every gridDim.x-th on, and looked up 32 at a time, one a lane;
+            // the rest are claimed one by one, since units differ in length (24 rows of 600 to 2500 tokens, all dealt:
+            // twice the time).
             const unsigned items = (unsigned)c.units * c.blocks;  // (below 2^28)
-            for (unsigned i0 = blockIdx.x; i0 < items && ok; i0 += 32 * gridDim.x) {
-                const unsigned i = i0 + lane * gridDim.x;
+            auto look_up = [&](unsigned i) {
                 Unit u;
                 u.n = 0;
                 u.tok = u.head = u.slot = u.part = u.from = u.to = 0;
-                if (i < items) {
-                    const int x = i / (unsigned)c.blocks;
-                    u.head = (int)(i - x * c.blocks) * VH;
-                    int b = x, s = 0;
-                    if (c.seg) {
-                        // row b's segments have the numbers begin / seg + b and on: the last row with that <= x
-                        int lo = 0, hi = a.batch - 1;
-                        while (lo < hi) {
-                            const int mid = (lo + hi + 1) >> 1;
-                            const int begin = a.cu ? a.cu[mid] : mid * a.each;
-                            if (begin / c.seg + mid <= x) lo = mid;
-                            else hi = mid - 1;
-                        }
-                        b = lo;
-                        s = x - ((a.cu ? a.cu[b] : b * a.each) / c.seg + b);
+                if (i >= items) return u;
+                const int x = i / (unsigned)c.blocks;
+                u.head = (int)(i - x * c.blocks) * VH;
+                int b = x, s = 0;
+                if (c.seg) {
+                    // row b's segments have the numbers begin / seg + b and on: the last row with that <= x
+                    int lo = 0, hi = a.batch - 1;
+                    while (lo < hi) {
+                        const int mid = (lo + hi + 1) >> 1;
+                        const int begin = a.cu ? a.cu[mid] : mid * a.each;
+                        if (begin / c.seg + mid <= x) lo = mid;
+                        else hi = mid - 1;
                     }
-                    int begin, end;
-                    if (row_of(a, b, u.head == 0, begin, end, u.slot) && s >= 0 && s < segments(c, end - begin)) {
-                        const int last = segments(c, end - begin) - 1;
-                        u.tok = begin + s * c.seg;
-                        u.n = s == last ? end - u.tok : c.seg;
-                        u.part = s > 0 ? begin / c.seg + s - 1 : last > 0 ? c.kept + begin / c.seg : 0;
-                        u.from = s > 0 ? kPart : !a.resume || !a.resume[b] ? kZero : last > 0 ? kPart : kSlot;
-                        u.to = s == last ? kSlot : kZero;
-                    }
+                    b = lo;
+                    s = x - ((a.cu ? a.cu[b] : b * a.each) / c.seg + b);
                 }
+                int begin, end;
+                if (row_of(a, b, u.head == 0, begin, end, u.slot) && s >= 0 && s < segments(c, end - begin)) {
+                    const int last = segments(c, end - begin) - 1;
+                    u.tok = begin + s * c.seg;
+                    u.n = s == last ? end - u.tok : c.seg;
+                    u.part = s > 0 ? begin / c.seg + s - 1 : last > 0 ? c.kept + begin / c.seg : 0;
+                    u.from = s > 0 ? kPart : !a.resume || !a.resume[b] ? kZero : last > 0 ? kPart : kSlot;
+                    u.to = s == last ? kSlot : kZero;
+                }
+                return u;
+            };
+            auto take_all = [&](const Unit& u) {  // every lane's
                 for (uint32_t m = __ballot_sync(0xffffffffu, u.n > 0); m && ok; m &= m - 1) {
                     const int l = __ffs(m) - 1;
                     Unit x;
@@ -733,6 +710,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                     x.to = __shfl_sync(0xffffffffu, u.to, l);
                     ok = take(x);
                 }
+            };
+            const unsigned dealt = items / 2 / gridDim.x;  // to each CTA
+            for (unsigned k0 = 0; k0 < dealt && ok; k0 += 32)
+                take_all(look_up(k0 + lane < dealt ? blockIdx.x + (k0 + lane) * gridDim.x : items));
+            auto claim = [&]() { return __shfl_sync(0xffffffffu, lane == 0 ? dealt * gridDim.x + atomicAdd(c.claims, 1u) : 0u, 0); };
+            if (ok) {
+                unsigned first = claim();
+                Unit u = look_up(lane == 0 ? first : items);
+                while (ok) {
+                    const unsigned next = claim();
+                    take_all(u);
+                    if (next >= items) break;
+                    u = look_up(lane == 0 ? next : items);
+                }
+            }
+            // the last CTA leaves the counters as they were
+            __syncwarp();
+            if (lane == 0 && atomicAdd(c.claims + 1, 1u) == gridDim.x - 1) {
+                atomicExch(c.claims, 0u);
+                atomicExch(c.claims + 1, 0u);
             }
         } else {
             // the segments before the last one of each long row
@@ -764,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) units[ur.slot].n = -1;
             arrive(&ufull[ur.slot]);
         }
-    } else if (warp == 25) {
+    } else if (warp == 18) {
         // ------------------------------------------------------------ products
         constexpr uint32_t i_score = umma::idesc_16bit(128, kC, true, false, false);
         constexpr uint32_t i_ds = umma::idesc_16bit(128, N, true, true, true);
@@ -799,26 +796,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = !OUT || scores();
             for (int t = 0; t < n && ok; t += kC) {
                 const uint32_t stage = at + st.slot * C::STAGE;
-                ok = await(&ds_free, v1.parity ^ 1);
-                const uint64_t kt = umma::smem_desc_swizzle128(stage + C::QB, kBox, 1024);
-#pragma unroll 1
-                for (int half = 0; half < 2 && ok; ++half) {
-                    ok = await(&vp_ready[half], v1.parity);
-                    if (!ok) break;
-                    umma::fence_after_sync();
-#pragma unroll
-                    for (int z = 0; z < SP; ++z)
-#pragma unroll
-                        for (int x = 0; x < 2; ++x)
-                            mma(tmem + C::DS, vpd + ((z * C::VB + half * 4096 + x * 2048) >> 4),
-                                kt + ((half * 4096 + x * 2048) >> 4), i_ds, half + z + x > 0, leader);
-                    commit(&vp_free[half], leader);
-                    if (!OUT && half) {
-                        commit(&st_full, leader);
-                        commit(&empty[st.slot], leader);
-                    }
-                }
+                ok = await(&vp_ready, v1.parity);  // (and dS has been read)
                 if (!ok) break;
+                umma::fence_after_sync();
+                const uint64_t kt = umma::smem_desc_swizzle128(stage + C::QB, kBox, 1024);
+#pragma unroll
+                for (int z = 0; z < SP; ++z)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        mma(tmem + C::DS, vpd + ((z * C::VB + x * 2048) >> 4), kt + (x * 2048 >> 4), i_ds, z + x > 0, leader);
+                if (!OUT) {
+                    commit(&st_full, leader);
+                    commit(&empty[st.slot], leader);
+                }
                 v1.next(1);
                 if (OUT) {
                     if (t + kC < n) ok = scores();
@@ -854,7 +844,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             arrive(&ufree[ur.slot]);
             ur.next(kUnits);
         }
-    } else if (warp < 26 + C::DECAYS) {
+    } else if (warp == 22 || C::DECAYS == 2) {
         // ------- decays: a warp for each head of a pair, else two that take chunks in turn (of a segment's own state: one)
         const int h = PAIR ? warp & 1 : 0, turn = warp & 1;
         constexpr bool TURNS = OUT && !PAIR;
@@ -865,34 +855,38 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Unit u = unit_at(ur.slot);
             if (u.n < 0) break;
             // tokens lane and lane + 32 of a chunk, loaded a chunk ahead
-            const float* gp = a.g + ((long)u.tok + lane) * a.g_stride + u.head + h;
-            const float* wp = a.w ? a.w + ((long)u.tok + lane) * a.w_stride + u.head + h : nullptr;
+            const bool first = !TURNS || (k & 1) == turn;  // (this warp has the unit's first chunk)
+            const int skip = TURNS ? 2 * kC : kC;
+            int t = first ? 0 : kC;
+            const float* gp = a.g + (long)(u.tok + t + lane) * a.g_stride + u.head + h;
+            const float* wp = a.w ? a.w + (long)(u.tok + t + lane) * a.w_stride + u.head + h : nullptr;
+            const long g32 = 32 * a.g_stride, w32 = 32 * a.w_stride;
+            int rest = u.n - t - lane;  // tokens from the lane's on
             float g0, g1, w0, w1;
-            auto load = [&](int t) {
+            auto load = [&]() {
                 g0 = g1 = w0 = w1 = 0.f;
-                if (t + lane < u.n) {
-                    g0 = gp[t * a.g_stride];
-                    w0 = wp ? wp[t * a.w_stride] : 1.f;
+                if (rest > 0) {
+                    g0 = gp[0];
+                    w0 = wp ? wp[0] : 1.f;
                 }
-                if (t + lane + 32 < u.n) {
-                    g1 = gp[(t + 32) * a.g_stride];
-                    w1 = wp ? wp[(t + 32) * a.w_stride] : 1.f;
+                if (rest > 32) {
+                    g1 = gp[g32];
+                    w1 = wp ? wp[w32] : 1.f;
                 }
+                gp += skip / 32 * g32;
+                if (wp) wp += skip / 32 * w32;
+                rest -= skip;
             };
             long long total = 0;
             bool total_bad = false;
             bool ok = true;
-            int t = 0;
-            if (TURNS && (k & 1) != turn) {
-                t = kC;
-                gr.next(kGates);
-            }
+            if (!first) gr.next(kGates);
             k += (u.n + kC - 1) / kC;
-            load(t);
+            load();
 #pragma unroll 1
             while (t < u.n) {
                 const float gx[2] = {g0, g1}, wx[2] = {w0, w1};
-                load(t + (TURNS ? 2 * kC : kC));
+                load();
                 ok = await(&gfree[gr.slot], gr.parity ^ 1);
                 if (!ok) break;
                 const float nan = __uint_as_float(0x7fc00000u);
@@ -949,7 +943,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (abort_flag) {
         if (tid == 0) set_dev_err(a.dev_err, RSSM_DEVERR_TIMEOUT);
         // A wait ran out: no copy and no product may still be in flight when the CTA ends.
-        if (warp == 25) {
+        if (warp == 18) {
             if (elect_one()) umma::commit_to(&drain);
             __syncwarp();
             mbar_wait_bounded(&drain, 0, RSSM_WAIT_NS / 100);
@@ -959,7 +953,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncthreads();
     }
-    if (warp == 25) umma::tmem_dealloc(tmem, 512);
+    if (warp == 18) umma::tmem_dealloc(tmem, 512);
 }
 
 // parts[s] = the state after segment s, from its own state and what came before. A thread has four
@@ -1036,23 +1030,23 @@ size_t chunk_workspace(const rssm_linattn_dims* d, int n_tokens) {
     long many = 3L * di.sm_count / blocks;
     if (many < 1) many = 1;
     const long kept = n_tokens <= 512 ? 0 : many < n_tokens / 512 ? many : n_tokens / 512;
-    return (size_t)kept * d->num_heads * ((size_t)d->value_dim * d->key_dim * 8 + 8) + (kept ? 256 : 0);
+    return 256 + (size_t)kept * d->num_heads * ((size_t)d->value_dim * d->key_dim * 8 + 8) + (kept ? 256 : 0);
 }
 
 template <int N, int P, bool PAIR, int SP>
 static int launch(const rssm_linattn_dims* d, const ChunkArgs& c, const DeviceInfo& di, cudaStream_t st) {
-    CUtensorMap qm, km, vm;
-    memset(&qm, 0, sizeof qm);
+    CUtensorMap qm, km, vm, om;
     const uint64_t rows = c.a.tokens, kw = (uint64_t)d->num_k_heads * N, vw = (uint64_t)d->num_heads * P;
     if (!make_tmap_rows128(&qm, c.a.q, 2, rows, kw, kC, c.a.q_stride) ||
         !make_tmap_rows128(&km, c.a.k, 2, rows, kw, kC, c.a.k_stride) ||
-        !make_tmap_rows128(&vm, c.a.v, 2, rows, vw, kC, c.a.v_stride))
+        !make_tmap_rows128(&vm, c.a.v, 2, rows, vw, kC, c.a.v_stride) ||
+        !make_tmap_box(&om, c.a.o, c.a.obf ? 2 : 4, rows, vw, vw, 16, 32, false))
         return RSSM_ERR_CUDA;
     auto run = [&](auto kernel, int smem) -> int {
         if (smem > di.max_smem_optin) return RSSM_ERR_UNSUPPORTED;
         if (!ensure_smem_limit((const void*)kernel, smem)) return RSSM_ERR_CUDA;
         const long items = (long)c.units * c.blocks;
-        attn::launch_early(kernel, (int)(items < di.sm_count ? items : di.sm_count), dim3(kThreads), smem, st, c, qm, km, vm);
+        attn::launch_early(kernel, (int)(items < di.sm_count ? items : di.sm_count), dim3(kThreads), smem, st, c, qm, km, vm, om);
         return launch_status();
     };
     if (c.seg) {
@@ -1079,11 +1073,12 @@ int prompt_chunks(const rssm_linattn_dims* d, const Args& a, void* workspace, ui
     c.seg = segment_tokens(d, a.tokens, c.blocks, di.sm_count);
     c.units = (c.seg ? a.tokens / c.seg : 0) + a.batch;
     c.wait_ns = (uint32_t)wait_ns;
+    c.claims = static_cast<unsigned*>(workspace);
     if (c.seg) {
         const size_t kept = a.tokens / c.seg;
         c.kept = (int)kept;
-        c.part_decay = static_cast<float2*>(workspace);
-        c.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + (kept * a.H * 8 + 255) / 256 * 256);
+        c.part_decay = reinterpret_cast<float2*>(static_cast<char*>(workspace) + 256);
+        c.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + 256 + (kept * a.H * 8 + 255) / 256 * 256);
     }
     // (a float32 state keeps 24 bits of a decayed value, a bf16 one 16)
     if (d->key_dim == 64) return a.sbf ? launch_heads<64, 2>(d, c, di, st) : launch_heads<64, 3>(d, c, di, st);

@@ -72,7 +72,8 @@ class LinearAttention(_Fixed):
         self.o = torch.empty(self.max_tokens, num_heads, value_dim, device=dev, dtype=out_dtype)
         self.dev_err = torch.zeros(4, device=dev, dtype=torch.int32)
         self.ws_bytes = B.rssm_linattn_workspace_size(self.dims(max_batch), self.max_tokens)
-        self.workspace = torch.empty(max(self.ws_bytes, 16), device=dev, dtype=torch.uint8)
+        # zero-filled: the prompt call keeps its counters here
+        self.workspace = torch.zeros(max(self.ws_bytes, 16), device=dev, dtype=torch.uint8)
         self._prompt, self._step = B.entry("rssm_linattn_prompt"), B.entry("rssm_linattn_step")
         self._addr = (self.state.data_ptr(), self.workspace.data_ptr(), self.dev_err.data_ptr(), self.o.data_ptr())
         self._index = _index(self.state.device)
