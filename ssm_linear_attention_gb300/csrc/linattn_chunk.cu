@@ -69,11 +69,12 @@ struct Chunk {
     static constexpr int STAGE = 2 * QB + VB;
     static constexpr int WB = OUT ? VH * kBox : 0;      // one part of W
     static constexpr int OB = OUT ? 16 * 2048 : 0;      // output: 16 tokens of 32 values for each of 16 warps
-    static constexpr int REST = SP * VB + 2 * WB + OB;
+    static constexpr int NV = OUT ? 1 : 2;               // buffers of V' (and of dS)
+    static constexpr int REST = NV * SP * VB + 2 * WB + OB;
     static constexpr int ST = REST + 3 * STAGE <= 216 * 1024 ? 3 : 2;
     static constexpr int SMEM = ST * STAGE + REST + (VL == 64 ? 1024 : 0) + 1024;
     // tensor memory columns
-    static constexpr uint32_t SCORE = 0, STATE = 64, DS = STATE + N, INTER = DS + N, INTRA = INTER + 64;
+    static constexpr uint32_t SCORE = 0, STATE = 64, DS = OUT ? STATE + N : 0, INTER = DS + N, INTRA = INTER + 64;
     static constexpr int CONS = (OUT ? 4 : 0) + 16;  // warps that read the decays
     static constexpr int DECAYS = OUT || PAIR ? 2 : 1;  // warps that make them
     static constexpr int UCONS = CONS + 1 + DECAYS;      // warps that follow the list
@@ -255,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ unsigned char smem_raw[];
     unsigned char* const smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     unsigned char* const vp = smem + ST * C::STAGE;  // V', its parts
-    unsigned char* const sw = vp + SP * C::VB;       // W, two parts
+    unsigned char* const sw = vp + C::NV * SP * C::VB;  // W, two parts
     unsigned char* const so = sw + 2 * C::WB;        // output
     const int tid = threadIdx.x, lane = tid & 31;
     // (through a shuffle: what depends on it is then known to be the warp's, and goes through the uniform registers)
@@ -396,8 +397,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto make_values = [&](int t, uint32_t k1) {
                 unsigned char* const raw = smem + sv.slot * C::STAGE + 2 * C::QB + tid * 16;
                 const int cnt = u.n - t, j = tid >> 3;
+                unsigned char* const to = vp + (OUT ? 0 : (k1 & 1) * SP * C::VB) + tid * 16;
                 f2 probe = 0;  // becomes NaN where a value is not finite
-#pragma unroll 1
+#pragma unroll
                 for (int box = 0; box < C::VL / 64; ++box) {
                     const uint4 in = *reinterpret_cast<const uint4*>(raw + box * kBox);
                     const float d = gd[gv.slot][PAIR ? box : 0][j];
@@ -419,14 +421,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
 #pragma unroll
                     for (int z = 0; z < SP; ++z)
-                        *reinterpret_cast<uint4*>(vp + z * C::VB + box * kBox + tid * 16) = make_uint4(y[z][0], y[z][1], y[z][2], y[z][3]);
+                        *reinterpret_cast<uint4*>(to + z * C::VB + box * kBox) = make_uint4(y[z][0], y[z][1], y[z][2], y[z][3]);
                 }
                 if (j >= cnt) {  // rows behind the last token may hold anything, and zero times that is not zero
                     const uint4 none = make_uint4(0, 0, 0, 0);
 #pragma unroll 1
                     for (int box = 0; box < C::VL / 64; ++box) {
                         *reinterpret_cast<uint4*>(raw + box * kBox) = none;
-                        for (int z = 0; z < SP; ++z) *reinterpret_cast<uint4*>(vp + z * C::VB + box * kBox + tid * 16) = none;
+                        for (int z = 0; z < SP; ++z) *reinterpret_cast<uint4*>(to + z * C::VB + box * kBox) = none;
                     }
                     for (int box = 0; box < N / 64; ++box) *reinterpret_cast<uint4*>(raw - C::QB + box * kBox) = none;  // (K)
                 } else if (OUT) {
@@ -461,7 +463,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int t = 0; t < u.n; t += kC, ++k) {
                 const bool more = t + kC < u.n;
-                ok = all_of<1, 512>(warp != 0 || (await(&st_full, one.parity) && (!more || inputs())));
+                if (!OUT && more) {
+                    ok = all_of<1, 512>(warp != 0 || inputs());
+                    if (!ok) break;
+                    make_values(t + kC, k + 1);
+                }
+                ok = all_of<1, 512>(warp != 0 || (await(&st_full, one.parity) && (!OUT || !more || inputs())));
                 if (!ok) break;
                 const float2 f = gam[gr.slot][vh];
                 const f2 fx = two(f.x, f.x), fy = two(f.y, f.y);
@@ -469,14 +476,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < NS / 2; i += 4) {
                     float d[8];
-                    umma::ld_cols<8>(at + C::DS + n0 + 2 * i, d);
+                    umma::ld_cols<8>(at + C::DS + (OUT ? 0 : (k & 1) * N) + n0 + 2 * i, d);
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
                         s[i + x] = fma2(fx, s[i + x], fma2(fy, s[i + x], two(d[2 * x], d[2 * x + 1])));
                 }
-                if (more) {
+                if (OUT && more) {
                     make_values(t + kC, k + 1);
-                    if (OUT) give_state();
+                    give_state();
                 }
                 if (OUT) {
                     ok = all_of<1, 512>(warp != 0 || await(&o_full, one.parity));
@@ -486,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     unsigned char* put = mine_out;
                     bulk_wait_read_all();  // (the chunk before's)
                     __syncwarp();
-#pragma unroll 1
+#pragma unroll
                     for (int i = 0; i < 16; i += 8, e += 8) {
                         float x[8], y[8];
                         umma::ld_cols<8>(at + C::INTER + i0 + i, x);
@@ -773,6 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t vpd = umma::smem_desc_swizzle128(vp_at, lbo, 1024);
         const uint32_t leader = elect_one();
         Ring ur, st, ahead, sc, v1, s1, w1;
+        uint32_t k = 0;
         // scores of the chunk whose loads are in stage `ahead`
         auto scores = [&]() {
             if (!await(&full[ahead.slot], ahead.parity) || !await(&sc_free, sc.parity ^ 1)) return false;
@@ -794,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int n = __shfl_sync(0xffffffffu, units[ur.slot].n, 0);
             if (n < 0) break;
             bool ok = !OUT || scores();
-            for (int t = 0; t < n && ok; t += kC) {
+            for (int t = 0; t < n && ok; t += kC, ++k) {
                 const uint32_t stage = at + st.slot * C::STAGE;
                 ok = await(&vp_ready, v1.parity);  // (and dS has been read)
                 if (!ok) break;
@@ -804,7 +812,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int z = 0; z < SP; ++z)
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
-                        mma(tmem + C::DS, vpd + ((z * C::VB + x * 2048) >> 4), kt + (x * 2048 >> 4), i_ds, z + x > 0, leader);
+                        mma(tmem + C::DS + (OUT ? 0 : (k & 1) * N), vpd + (((OUT ? 0 : (k & 1) * SP * C::VB) + z * C::VB + x * 2048) >> 4), kt + (x * 2048 >> 4), i_ds, z + x > 0, leader);
                 if (!OUT) {
                     commit(&st_full, leader);
                     commit(&empty[st.slot], leader);
