@@ -12,7 +12,7 @@
 // added there, S = exp(G_end) S_0 + dS, the decay as a float32 and its remainder (a rounded decay would be wrong in the
 // same direction in every chunk: 2e-6 of a state that remembers 50 chunks). Q, K and V are exact; S_0 and W
 // enter as two bf16 parts (16 bits), V' as two for a bf16 state and three (24 bits) for a float32 one.
-// The logarithms are summed as 64-bit fixed point in units of 2^-40, so that differences of sums are exact.
+// The logarithms are summed in fixed point, units of 2^-40, so that differences of sums are exact.
 //
 // A long row is cut into segments where rows and heads alone do not fill the GPU: one launch makes the
 // segments' own states (dS alone), one carries them on, and the main one begins each segment from its state.
@@ -41,7 +41,7 @@ constexpr int kThreads = 768;
 struct ChunkArgs {
     Args a;
     float* parts;      // states of the rows' segments [index][H][P][N]
-    float2* part_decay;  // and their decays [index][H]
+    float2* part_decay;  // and their decays, in two factors [index][H][2]
     int kept;          // of either; behind them the states that cut rows began with, at first token / seg
     int seg;           // tokens of a segment, a multiple of 64; 0: rows are not cut
     int blocks;        // units of a segment: heads, or pairs of them
@@ -76,8 +76,7 @@ struct Chunk {
     // tensor memory columns
     static constexpr uint32_t SCORE = 0, STATE = 64, DS = OUT ? STATE + N : 0, INTER = DS + N, INTRA = INTER + 64;
     static constexpr int CONS = (OUT ? 4 : 0) + 16;  // warps that read the decays
-    static constexpr int DECAYS = OUT || PAIR ? 2 : 1;  // warps that make them
-    static constexpr int UCONS = CONS + 1 + DECAYS;      // warps that follow the list
+    static constexpr int UCONS = CONS + 1 + 2;          // warps that follow the list
 };
 
 // Two float32 in a register pair.
@@ -151,21 +150,17 @@ __device__ __forceinline__ float2 exp2_pair(long long x) {
     const float a = __int_as_float(((whole >> 1) + 127) << 23), b = __int_as_float((whole - (whole >> 1) + 127) << 23);
     return make_float2(hi * a * b, lo * a * b);
 }
-// log2(exp(g)) in units of 2^-40 (2^14 at most, for an infinity too): g's significand times log2(e) as integers.
-// (Conversions between float32 and 64-bit integers go through the FP64 pipe, 64 cycles a warp each.)
-__device__ __forceinline__ long long log2_fixed(float g) {
-    g = fminf(fmaxf(g, -11356.5f), 11356.5f);  // (2^14 ln 2, nearly)
-    const uint32_t u = __float_as_uint(g) & 0x7fffffffu, e = u >> 23;
-    const uint32_t m = (u & 0x7fffffu) | 0x800000u;
-    // log2(e) 2^38 = 92 * 2^32 + 1428001966.05
-    const uint64_t P = (uint64_t)m * 1428001966u + ((uint64_t)(m * 92u) << 32);
-    const uint32_t down = 148u - e;  // g = m 2^(e - 150)
-    const long long x = down < 64 ? (long long)((P + (1ull << (down - 1))) >> down) : 0;
-    return g < 0.f ? -x : x;
+// log2(exp(g)) = x 2^-16 + y 2^-40, +-400 for what is beyond (an infinity too; 2^-400 is zero): 64 of them sum without
+// overflow in either part.
+__device__ __forceinline__ int2 log2_parts(float g) {
+    g = fminf(fmaxf(g, -277.f), 277.f);
+    const float L = 1.44269502162933349609375f, l = 1.925963e-8f;  // log2(e) = L + l
+    const float hi = g * L, lo = fmaf(g, l, fmaf(g, L, -hi));
+    const int x = __float2int_rn(hi * 65536.f);
+    const float rest = fmaf((float)x, -0x1p-16f, hi) + lo;
+    return make_int2(x, __float2int_rn(rest * 0x1p40f));
 }
-__device__ __forceinline__ float fixed_to_float(long long x) {
-    return (float)(int)(x >> 40) + (float)(uint32_t)(x >> 8) * 0x1p-32f;
-}
+__device__ __forceinline__ float parts_to_float(int x, int y) { return fmaf((float)x, 0x1p-16f, (float)y * 0x1p-40f); }
 
 // Wait for phase `parity` of the barrier at shared address `bar`: false once `limit` ns went by, or another warp has
 // set the flag at `stop`; then the flag is set. try_wait sleeps, so a wait costs few instructions; and it is
@@ -852,10 +847,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             arrive(&ufree[ur.slot]);
             ur.next(kUnits);
         }
-    } else if (warp == 22 || C::DECAYS == 2) {
-        // ------- decays: a warp for each head of a pair, else two that take chunks in turn (of a segment's own state: one)
+    } else {
+        // ----------------------- decays: a warp for each head of a pair, else two that take chunks in turn
         const int h = PAIR ? warp & 1 : 0, turn = warp & 1;
-        constexpr bool TURNS = OUT && !PAIR;
+        constexpr bool TURNS = !PAIR;
         uint32_t k = 0;
         Ring ur, gr;
         for (;;) {
@@ -893,42 +888,40 @@ __global__ void __launch_bounds__(kThreads, 1)
             load();
 #pragma unroll 1
             while (t < u.n) {
-                const float gx[2] = {g0, g1}, wx[2] = {w0, w1};
+                const float ga = g0, gb = g1, wa = w0, wb = w1;
                 load();
                 ok = await(&gfree[gr.slot], gr.parity ^ 1);
                 if (!ok) break;
                 const float nan = __uint_as_float(0x7fc00000u);
-                long long G0 = 0, end = 0;
-                bool bad = false;
-#pragma unroll 1
-                for (int x = 0; x < 2; ++x) {
-                    const float gv = x ? gx[1] : gx[0], wv = x ? wx[1] : wx[0];
-                    long long sum = log2_fixed(gv);
+                int2 A = log2_parts(ga), B = log2_parts(gb);
 #pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const long long y = __shfl_up_sync(0xffffffffu, sum, o);
-                        if (lane >= o) sum += y;
-                    }
-                    sum += end;
-                    const uint32_t bads = __ballot_sync(0xffffffffu, gv != gv);
-                    const bool after = bad || (bads & (2u << lane) - 1);  // (a NaN is here or before)
-                    bad |= bads != 0;
-                    // (the whole part apart: a difference of two sums must not lose its bits to their size; a reset is 2^14)
-                    gw[gr.slot][h][x * 32 + lane] = make_float4((float)(int)(sum >> 40), (float)(uint32_t)(sum >> 8) * 0x1p-32f,
-                                                                wv * a.scale, 0.f);
-                    ge[gr.slot][h][x * 32 + lane] = after ? nan : a.scale * exp2_fast(fixed_to_float(sum));
-                    if (x == 0) G0 = sum;
-                    end = __shfl_sync(0xffffffffu, sum, 31);
-                    if (x == 1) {
-                        gd[gr.slot][h][32 + lane] = exp2_fast(fixed_to_float(end - sum)) * wv;
-                        gd[gr.slot][h][lane] = exp2_fast(fixed_to_float(end - G0)) * wx[0];
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int ax = __shfl_up_sync(0xffffffffu, A.x, o), ay = __shfl_up_sync(0xffffffffu, A.y, o);
+                    const int bx = __shfl_up_sync(0xffffffffu, B.x, o), by = __shfl_up_sync(0xffffffffu, B.y, o);
+                    if (lane >= o) {
+                        A.x += ax;
+                        A.y += ay;
+                        B.x += bx;
+                        B.y += by;
                     }
                 }
+                B.x += __shfl_sync(0xffffffffu, A.x, 31);
+                B.y += __shfl_sync(0xffffffffu, A.y, 31);
+                const int2 E = make_int2(__shfl_sync(0xffffffffu, B.x, 31), __shfl_sync(0xffffffffu, B.y, 31));
+                const uint32_t bad_a = __ballot_sync(0xffffffffu, ga != ga), bad_b = __ballot_sync(0xffffffffu, gb != gb);
+                const uint32_t upto = (2u << lane) - 1;  // (a NaN is at the token or before)
+                const bool nan_a = bad_a & upto, nan_b = bad_a || (bad_b & upto), bad = bad_a || bad_b;
+                // (the whole part apart: a difference of two sums must not lose its bits to their size)
+                gw[gr.slot][h][lane] = make_float4((float)(A.x >> 16), parts_to_float(A.x & 0xffff, A.y), wa * a.scale, 0.f);
+                gw[gr.slot][h][32 + lane] = make_float4((float)(B.x >> 16), parts_to_float(B.x & 0xffff, B.y), wb * a.scale, 0.f);
+                ge[gr.slot][h][lane] = nan_a ? nan : a.scale * exp2_fast(parts_to_float(A.x, A.y));
+                ge[gr.slot][h][32 + lane] = nan_b ? nan : a.scale * exp2_fast(parts_to_float(B.x, B.y));
+                gd[gr.slot][h][lane] = exp2_fast(parts_to_float(E.x - A.x, E.y - A.y)) * wa;
+                gd[gr.slot][h][32 + lane] = exp2_fast(parts_to_float(E.x - B.x, E.y - B.y)) * wb;
+                const long long end = ((long long)E.x << 24) + E.y;
                 if (lane == 0) gam[gr.slot][h] = bad ? make_float2(nan, nan) : exp2_pair(end);
                 if (!OUT) {
-                    // (a sum that leaves the range of exponents stays there)
-                    const long long most = 1ll << 61;
-                    total = max(-most, min(most, total + end));
+                    total = max(-(1ll << 52), min(1ll << 52, total + end));  // (far beyond float32's exponents)
                     total_bad |= bad;
                 }
                 arrive(&gready[gr.slot]);
@@ -940,9 +933,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (!ok) break;
-            if (!OUT && lane == 0)
-                c.part_decay[(long)u.part * a.H + u.head + h] =
-                    total_bad ? make_float2(__uint_as_float(0x7fc00000u), __uint_as_float(0x7fc00000u)) : exp2_pair(total);
+            if (!OUT && lane == 0) {
+                // (of the two warps that took turns each has a factor)
+                const float nan = __uint_as_float(0x7fc00000u);
+                c.part_decay[((long)u.part * a.H + u.head + h) * 2 + (TURNS ? turn : 0)] = total_bad ? make_float2(nan, nan) : exp2_pair(total);
+                if (!TURNS) c.part_decay[((long)u.part * a.H + u.head + h) * 2 + 1] = make_float2(1.f, 0.f);
+            }
             arrive(&ufree[ur.slot]);
             ur.next(kUnits);
         }
@@ -989,11 +985,11 @@ __global__ void __launch_bounds__(256) carry_kernel(const ChunkArgs c, long all,
                 __stcg(reinterpret_cast<float4*>(c.parts + (c.kept + first) * all + e), s);
             }
             float4* const part = reinterpret_cast<float4*>(c.parts + first * all + e);
-            const float2* const decay = c.part_decay + (long)first * a.H + h;
+            const float4* const decay = reinterpret_cast<const float4*>(c.part_decay) + (long)first * a.H + h;
             constexpr int U = 8;
             for (int i0 = 0; i0 < n; i0 += U) {
                 float4 x[U];
-                float2 f[U];
+                float4 f[U];
 #pragma unroll
                 for (int i = 0; i < U; ++i)
                     if (i0 + i < n) {
@@ -1003,9 +999,13 @@ __global__ void __launch_bounds__(256) carry_kernel(const ChunkArgs c, long all,
 #pragma unroll
                 for (int i = 0; i < U; ++i)
                     if (i0 + i < n) {
+                        s.x = fmaf(f[i].z, s.x, f[i].w * s.x);
                         s.x = fmaf(f[i].x, s.x, fmaf(f[i].y, s.x, x[i].x));
+                        s.y = fmaf(f[i].z, s.y, f[i].w * s.y);
                         s.y = fmaf(f[i].x, s.y, fmaf(f[i].y, s.y, x[i].y));
+                        s.z = fmaf(f[i].z, s.z, f[i].w * s.z);
                         s.z = fmaf(f[i].x, s.z, fmaf(f[i].y, s.z, x[i].z));
+                        s.w = fmaf(f[i].z, s.w, f[i].w * s.w);
                         s.w = fmaf(f[i].x, s.w, fmaf(f[i].y, s.w, x[i].w));
                         __stcg(part + (i0 + i) * (all / 4), s);
                     }
@@ -1038,7 +1038,7 @@ size_t chunk_workspace(const rssm_linattn_dims* d, int n_tokens) {
     long many = 3L * di.sm_count / blocks;
     if (many < 1) many = 1;
     const long kept = n_tokens <= 512 ? 0 : many < n_tokens / 512 ? many : n_tokens / 512;
-    return 256 + (size_t)kept * d->num_heads * ((size_t)d->value_dim * d->key_dim * 8 + 8) + (kept ? 256 : 0);
+    return 256 + (size_t)kept * d->num_heads * ((size_t)d->value_dim * d->key_dim * 8 + 16) + (kept ? 256 : 0);
 }
 
 template <int N, int P, bool PAIR, int SP>
@@ -1086,7 +1086,7 @@ int prompt_chunks(const rssm_linattn_dims* d, const Args& a, void* workspace, ui
         const size_t kept = a.tokens / c.seg;
         c.kept = (int)kept;
         c.part_decay = reinterpret_cast<float2*>(static_cast<char*>(workspace) + 256);
-        c.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + 256 + (kept * a.H * 8 + 255) / 256 * 256);
+        c.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + 256 + (kept * a.H * 16 + 255) / 256 * 256);
     }
     // (a float32 state keeps 24 bits of a decayed value, a bf16 one 16)
     if (d->key_dim == 64) return a.sbf ? launch_heads<64, 2>(d, c, di, st) : launch_heads<64, 3>(d, c, di, st);
