@@ -6,8 +6,8 @@
 // The step reads and writes every state once and is bound by that; a lane has pieces of 16 bytes
 // of one value row, eight lanes a row, so that a sum over N takes three shuffles.
 //
-// The recurrence over a prompt keeps 16 value rows of a head in the registers of a CTA and takes one token
-// after another.
+// The recurrence over a prompt keeps 64 value rows of a head in the registers of a CTA and takes one token
+// after another: float32 activations, cut into segments as the chunks are, and rows of few tokens.
 #include "linattn.cuh"
 
 namespace rssm {
@@ -119,84 +119,296 @@ static int launch_step(const Args& a, int N, int P, cudaStream_t st) {
 
 // ------------------------------------------------ a prompt, token by token ----
 
-constexpr int kRows = 16;  // value rows of a CTA
+// Float32 activations, and rows of few tokens. A CTA has 64 value rows of a head: a lane group of eight has rows
+// r, r + 4, r + 8, r + 12 of its warp's 16 and a lane of it keys 4 l + 32 j .. + 3, all in registers. EXACT: the decays as a
+// float32 and its remainder (rounded decays would be wrong in the same direction at every token of a long memory).
+// OUT false: a segment's own state, from zero.
 constexpr int kTile = 16;  // tokens staged at a time
 
-// Thread t: value row t / 8, keys 4 (t % 8) + 32 j + 0..3.
-template <bool ABF, int N>
-__global__ void __launch_bounds__(128) recurrence_kernel(const Args a, int P) {
+template <bool ABF, int N, bool EXACT, bool OUT>
+__global__ void __launch_bounds__(128) recurrence_kernel(const ChunkArgs c, int P, bool report) {
     constexpr int J = N / 32;
-    __shared__ __align__(16) float sq[kTile][N], sk[kTile][N];
-    __shared__ float sv[kTile][kRows], so[kTile][kRows], sf[kTile], sw[kTile];
+    const Args& a = c.a;
+    __shared__ __align__(16) float sq[OUT ? kTile : 1][N], sk[kTile][N];
+    __shared__ __align__(16) float sv[kTile][64], so[OUT ? kTile : 1][64], sw[kTile];
+    __shared__ float2 sf[kTile];
+    __shared__ long long total;
+    __shared__ int place[8];
     attn::wait_for_stream();
-    const int parts = P / kRows, part = blockIdx.x % parts, bh = blockIdx.x / parts, b = bh / a.H, h = bh - b * a.H;
-    int begin, end, slot;
-    if (!row_of(a, b, threadIdx.x == 0 && part == 0, begin, end, slot)) return;
-    const int t = threadIdx.x, p = t >> 3, l = t & 7;
-    const int kh = h / (a.H / a.G);
-    const long at = (((long)slot * a.H + h) * P + part * kRows + p) * N;
-    float s[J][4];
-    if (a.resume && a.resume[b]) {
-#pragma unroll
-        for (int j = 0; j < J; ++j) load4(static_cast<const char*>(a.state) + (at + 4 * l + 32 * j) * (a.sbf ? 2 : 4), 0, a.sbf, s[j]);
-    } else {
-#pragma unroll
-        for (int j = 0; j < J; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+    const int parts = P / 64, part = blockIdx.x % parts, xh = blockIdx.x / parts, x = xh / a.H, h = xh - x * a.H;
+    const int t = threadIdx.x;
+    if (t == 0) {
+        int b = x, s = 0, begin, end, slot;
+        if (c.seg) {
+            // row b's segments have the numbers begin / seg + b and on: the last row with that <= x
+            int lo = 0, hi = a.batch - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if ((a.cu ? a.cu[mid] : mid * a.each) / c.seg + mid <= x) lo = mid;
+                else hi = mid - 1;
+            }
+            b = lo;
+            s = x - ((a.cu ? a.cu[b] : b * a.each) / c.seg + b);
+        }
+        const bool row = row_of(a, b, report && h == 0 && part == 0, begin, end, slot);
+        const int last = row ? segments(c, end - begin) - 1 : -1;
+        place[0] = row && (!c.brief || end - begin <= c.brief) && s >= 0 && (OUT ? s <= last : s < last);
+        place[1] = begin + s * c.seg;
+        place[2] = s == last ? end : place[1] + c.seg;
+        place[3] = slot;
+        place[4] = s > 0 ? begin / c.seg + s - 1 : last > 0 ? c.kept + begin / c.seg : 0;  // the part it goes on from
+        place[5] = !OUT ? 0 : s > 0 ? 2 : !a.resume || !a.resume[b] ? 0 : last > 0 ? 2 : 1;
+        place[6] = s == last;
+        place[7] = OUT || !c.seg ? 0 : begin / c.seg + s;
+        total = 0;
     }
+    __syncthreads();
+    if (!place[0]) return;
+    const int begin = place[1], end = place[2];
+    const int l = t & 7, p0 = (t >> 5) * 16 + (t >> 3 & 3);  // of 64 rows
+    const int kh = h / (a.H / a.G);
+    const long all = (long)a.H * P * N, at = ((long)h * P + part * 64 + p0) * N + 4 * l;
+    f2 s[4][J][2];
+    const float* const parts_at = c.parts + place[4] * all + at;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            float f[4] = {0.f, 0.f, 0.f, 0.f};
+            if (place[5] == 1) load4(static_cast<const char*>(a.state) + (place[3] * all + at + r * 4 * N + 32 * j) * (a.sbf ? 2 : 4), 0, a.sbf, f);
+            if (place[5] == 2) load4(parts_at + r * 4 * N + 32 * j, 0, false, f);
+            s[r][j][0] = two(f[0], f[1]);
+            s[r][j][1] = two(f[2], f[3]);
+        }
     for (int i0 = begin; i0 < end; i0 += kTile) {
         const int n = min(kTile, end - i0);
+        if (i0 > begin) __syncthreads();
         for (int e = t; e < n * (N / 4); e += 128) {
-            const int i = e / (N / 4), c = e % (N / 4) * 4;
+            const int i = e / (N / 4), col = e % (N / 4) * 4;
             const long row = i0 + i;
-            load4(static_cast<const char*>(a.q) + (row * a.q_stride + kh * N + c) * (ABF ? 2 : 4), 0, ABF, &sq[i][c]);
-            load4(static_cast<const char*>(a.k) + (row * a.k_stride + kh * N + c) * (ABF ? 2 : 4), 0, ABF, &sk[i][c]);
+            if (OUT) load4(static_cast<const char*>(a.q) + (row * a.q_stride + kh * N + col) * (ABF ? 2 : 4), 0, ABF, &sq[i][col]);
+            load4(static_cast<const char*>(a.k) + (row * a.k_stride + kh * N + col) * (ABF ? 2 : 4), 0, ABF, &sk[i][col]);
         }
-        for (int e = t; e < n * kRows; e += 128) {
-            const int i = e / kRows, c = e % kRows;
-            sv[i][c] = load1(a.v, (i0 + i) * a.v_stride + (long)h * P + part * kRows + c, ABF);
+        for (int e = t; e < n * 16; e += 128) {
+            const int i = e / 16, col = e % 16 * 4;
+            load4(static_cast<const char*>(a.v) + ((i0 + i) * a.v_stride + (long)h * P + part * 64 + col) * (ABF ? 2 : 4), 0, ABF, &sv[i][col]);
         }
         if (t < n) {
-            sf[t] = expf(a.g[(i0 + t) * a.g_stride + h]);
+            const float g = a.g[(i0 + t) * a.g_stride + h];
             sw[t] = a.w ? a.w[(i0 + t) * a.w_stride + h] : 1.f;
+            if (EXACT) {
+                const int2 x = log2_parts(g);
+                const long long fixed = ((long long)x.x << 24) + x.y;
+                sf[t] = g != g ? make_float2(g, g) : exp2_pair(fixed);
+                if (!OUT) {
+                    if (g != g) total = 1ll << 62;
+                    atomicAdd(reinterpret_cast<unsigned long long*>(&total), (unsigned long long)fixed);
+                }
+            } else {
+                sf[t] = make_float2(expf(g), 0.f);
+            }
         }
         __syncthreads();
+#pragma unroll 1
         for (int i = 0; i < n; ++i) {
-            const float f = sf[i], u = sw[i] * sv[i][p];
-            float o = 0.f;
+            const f2 fh = two(sf[i].x, sf[i].x), fl = two(sf[i].y, sf[i].y);
+            const float w = sw[i];
+            f2 k[J][2], q[OUT ? J : 1][2];
 #pragma unroll
             for (int j = 0; j < J; ++j) {
-                const float4 k = *reinterpret_cast<const float4*>(&sk[i][4 * l + 32 * j]);
-                const float4 q = *reinterpret_cast<const float4*>(&sq[i][4 * l + 32 * j]);
-                s[j][0] = f * s[j][0] + u * k.x;
-                s[j][1] = f * s[j][1] + u * k.y;
-                s[j][2] = f * s[j][2] + u * k.z;
-                s[j][3] = f * s[j][3] + u * k.w;
-                o += s[j][0] * q.x + s[j][1] * q.y + (s[j][2] * q.z + s[j][3] * q.w);
+                const float4 x = *reinterpret_cast<const float4*>(&sk[i][4 * l + 32 * j]);
+                k[j][0] = two(x.x, x.y);
+                k[j][1] = two(x.z, x.w);
+                if (OUT) {
+                    const float4 y = *reinterpret_cast<const float4*>(&sq[i][4 * l + 32 * j]);
+                    q[j][0] = two(y.x, y.y);
+                    q[j][1] = two(y.z, y.w);
+                }
             }
+            float o[4];
 #pragma unroll
-            for (int m = 4; m >= 1; m >>= 1) o += __shfl_xor_sync(0xffffffffu, o, m);
-            if (l == 0) so[i][p] = o;
+            for (int r = 0; r < 4; ++r) {
+                const float u = w * sv[i][p0 + 4 * r];
+                const f2 uu = two(u, u);
+                f2 sum = 0;
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        f2 y = mul2(uu, k[j][e]);
+                        if (EXACT) y = fma2(fl, s[r][j][e], y);
+                        s[r][j][e] = fma2(fh, s[r][j][e], y);
+                        if (OUT) sum = fma2(s[r][j][e], q[j][e], sum);
+                    }
+                const float2 f = one_by_one(sum);
+                o[r] = f.x + f.y;
+            }
+            if (OUT) {
+                const int r = reduce_scatter<4, 8>(o);
+                if (!(l & 1)) so[i][p0 + 4 * r] = a.scale * o[0];
+            }
         }
-        __syncthreads();
-        for (int e = t; e < n * kRows; e += 128) {
-            const int i = e / kRows, c = e % kRows;
-            store1(a.o, ((long)(i0 + i) * a.H + h) * P + part * kRows + c, a.obf, a.scale * so[i][c]);
+        if (OUT) {
+            __syncthreads();
+            for (int e = t; e < n * 16; e += 128) {
+                const int i = e / 16, col = e % 16 * 4;
+                const float4 f = *reinterpret_cast<const float4*>(&so[i][col]);
+                const long to = ((long)(i0 + i) * a.H + h) * P + part * 64 + col;
+                if (a.obf) *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + to) = make_uint2(pack_bf16x2(f.x, f.y), pack_bf16x2(f.z, f.w));
+                else *reinterpret_cast<float4*>(static_cast<float*>(a.o) + to) = f;
+            }
         }
     }
+    if (!OUT && t == 0 && part == 0) {
+        const float nan = __uint_as_float(0x7fc00000u);
+        float2* const to = c.part_decay + ((long)place[7] * a.H + h) * 2;
+        to[0] = total > (1ll << 61) ? make_float2(nan, nan) : exp2_pair(total);
+        to[1] = make_float2(1.f, 0.f);
+    }
+    if (OUT && !place[6]) return;
+    const bool sbf = OUT && a.sbf;
+    char* const to = OUT ? static_cast<char*>(a.state) + (place[3] * all + at) * (sbf ? 2 : 4)
+                         : reinterpret_cast<char*>(c.parts + place[7] * all + at);
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-        char* const to = static_cast<char*>(a.state) + (at + 4 * l + 32 * j) * (a.sbf ? 2 : 4);
-        if (a.sbf) *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(s[j][0], s[j][1]), pack_bf16x2(s[j][2], s[j][3]));
-        else *reinterpret_cast<float4*>(to) = make_float4(s[j][0], s[j][1], s[j][2], s[j][3]);
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const float2 f = one_by_one(s[r][j][0]), g = one_by_one(s[r][j][1]);
+            char* const q = to + (r * 4 * N + 32 * j) * (sbf ? 2 : 4);
+            if (sbf) *reinterpret_cast<uint2*>(q) = make_uint2(pack_bf16x2(f.x, f.y), pack_bf16x2(g.x, g.y));
+            else *reinterpret_cast<float4*>(q) = make_float4(f.x, f.y, g.x, g.y);
+        }
+}
+
+template <bool ABF, bool EXACT, bool OUT>
+static int launch_recurrence(const ChunkArgs& c, int N, int P, bool report, cudaStream_t st) {
+    const int grid = c.units * c.a.H * (P / 64);
+    if (N == 64) attn::launch_early(recurrence_kernel<ABF, 64, EXACT, OUT>, grid, 128, 0, st, c, P, report);
+    else attn::launch_early(recurrence_kernel<ABF, 128, EXACT, OUT>, grid, 128, 0, st, c, P, report);
+    return launch_status();
+}
+
+// parts[s] = the state after segment s, from its own state and what came before. A thread has four
+// values, and goes through the long rows and their segments with the next ones' loads in flight.
+__global__ void __launch_bounds__(256) carry_kernel(const ChunkArgs c, long all, int per_head) {
+    attn::wait_for_stream();
+    const Args& a = c.a;
+    const long e = ((long)blockIdx.x * 256 + threadIdx.x) * 4;
+    const int lane = threadIdx.x & 31;
+    const int h = (int)(min(e, all - 4) / per_head);
+    for (int b0 = 0; b0 < a.batch; b0 += 32) {
+        int begin = 0, end = 0, slot = 0, count = 0;
+        if (b0 + lane < a.batch && row_of(a, b0 + lane, false, begin, end, slot)) count = segments(c, end - begin) - 1;
+        for (uint32_t m = __ballot_sync(0xffffffffu, count > 1 || (count == 1 && a.resume && a.resume[b0 + lane])); m; m &= m - 1) {
+            const int l = __ffs(m) - 1, b = b0 + l;
+            const int first = __shfl_sync(0xffffffffu, begin, l) / c.seg, n = __shfl_sync(0xffffffffu, count, l);
+            const int sl = __shfl_sync(0xffffffffu, slot, l);
+            if (e >= all) continue;
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (a.resume && a.resume[b]) {
+                float f[4];
+                load4(static_cast<const char*>(a.state) + (sl * all + e) * (a.sbf ? 2 : 4), 0, a.sbf, f);
+                s = make_float4(f[0], f[1], f[2], f[3]);
+                // (the main launch writes the slot when the row's last segment ends, maybe before its first begins)
+                __stcg(reinterpret_cast<float4*>(c.parts + (c.kept + first) * all + e), s);
+            }
+            float4* const part = reinterpret_cast<float4*>(c.parts + first * all + e);
+            const float4* const decay = reinterpret_cast<const float4*>(c.part_decay) + (long)first * a.H + h;
+            constexpr int U = 8;
+            for (int i0 = 0; i0 < n; i0 += U) {
+                float4 x[U];
+                float4 f[U];
+#pragma unroll
+                for (int i = 0; i < U; ++i)
+                    if (i0 + i < n) {
+                        x[i] = __ldcg(part + (i0 + i) * (all / 4));
+                        f[i] = __ldcg(decay + (long)(i0 + i) * a.H);
+                    }
+#pragma unroll
+                for (int i = 0; i < U; ++i)
+                    if (i0 + i < n) {
+                        s.x = fmaf(f[i].z, s.x, f[i].w * s.x);
+                        s.x = fmaf(f[i].x, s.x, fmaf(f[i].y, s.x, x[i].x));
+                        s.y = fmaf(f[i].z, s.y, f[i].w * s.y);
+                        s.y = fmaf(f[i].x, s.y, fmaf(f[i].y, s.y, x[i].y));
+                        s.z = fmaf(f[i].z, s.z, f[i].w * s.z);
+                        s.z = fmaf(f[i].x, s.z, fmaf(f[i].y, s.z, x[i].z));
+                        s.w = fmaf(f[i].z, s.w, f[i].w * s.w);
+                        s.w = fmaf(f[i].x, s.w, fmaf(f[i].y, s.w, x[i].w));
+                        __stcg(part + (i0 + i) * (all / 4), s);
+                    }
+            }
+        }
     }
 }
 
-template <bool ABF>
-static int launch_recurrence(const Args& a, int N, int P, cudaStream_t st) {
-    const int grid = a.batch * a.H * (P / kRows);
-    if (N == 64) attn::launch_early(recurrence_kernel<ABF, 64>, grid, 128, 0, st, a, P);
-    else attn::launch_early(recurrence_kernel<ABF, 128>, grid, 128, 0, st, a, P);
+int carry(const rssm_linattn_dims* d, const ChunkArgs& c, cudaStream_t st) {
+    const int per_head = d->value_dim * d->key_dim;
+    const long all = (long)d->num_heads * per_head;
+    attn::launch_early(carry_kernel, (int)((all / 4 + 255) / 256), dim3(256), 0, st, c, all, per_head);
     return launch_status();
+}
+
+// Tokens of a segment (0: rows are not cut): so many that all tokens in one row would give each SM about
+// `each` units, and no fewer than `least` (a cut reads k and v twice, and keeps a state). kept: states kept at most, for
+// any smaller number of tokens too.
+static int segment_tokens(const rssm_linattn_dims* d, int n_tokens, int sms, long* kept) {
+    const bool chunks = d->act_dtype == RSSM_BF16;
+    const int blocks = chunks ? chunk_blocks(d) : d->num_heads, least = chunks ? 512 : 64;
+    const long each = chunks ? 3 : 4, many = each * sms / blocks < 1 ? 1 : each * sms / blocks;
+    if (kept) *kept = n_tokens <= least ? 0 : many < n_tokens / least ? many : n_tokens / least;
+    long seg = (n_tokens + many - 1) / many;
+    if (seg < least) seg = least;
+    seg = (seg + 63) / 64 * 64;
+    return seg >= n_tokens ? 0 : (int)seg;
+}
+
+static size_t workspace_size(const rssm_linattn_dims* d, int n_tokens) {
+    DeviceInfo di;
+    if (!device_info(&di)) return 0;
+    long kept;
+    segment_tokens(d, n_tokens, di.sm_count, &kept);
+    return 256 + (size_t)kept * d->num_heads * ((size_t)d->value_dim * d->key_dim * 8 + 16) + (kept ? 256 : 0);
+}
+
+// Rows of few tokens: where they are short on the average, those of at most 32 go token by token (a unit of
+// the chunks' kernel costs its state's way through it, some 10 us).
+constexpr int kBrief = 32;
+
+static int prompt(const rssm_linattn_dims* d, const Args& a, void* workspace, cudaStream_t st) {
+    DeviceInfo di;
+    if (!device_info(&di)) return RSSM_ERR_CUDA;
+    const int N = d->key_dim, P = d->value_dim;
+    ChunkArgs c{};
+    c.a = a;
+    c.seg = segment_tokens(d, a.tokens, di.sm_count, nullptr);
+    c.units = (c.seg ? a.tokens / c.seg : 0) + a.batch;
+    c.wait_ns = (uint32_t)RSSM_WAIT_NS;
+    c.claims = static_cast<unsigned*>(workspace);
+    if (c.seg) {
+        const size_t kept = a.tokens / c.seg;
+        c.kept = (int)kept;
+        c.part_decay = reinterpret_cast<float2*>(static_cast<char*>(workspace) + 256);
+        c.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + 256 + (kept * a.H * 16 + 255) / 256 * 256);
+    }
+    if (d->act_dtype == RSSM_BF16) {
+        c.blocks = chunk_blocks(d);
+        if (a.tokens <= (int64_t)kBrief * a.batch) {
+            c.brief = kBrief;
+            ChunkArgs b = c;
+            b.seg = 0;
+            b.units = a.batch;
+            const bool all = a.tokens <= kBrief || !a.cu;  // no row is longer
+            const int rc = launch_recurrence<true, false, true>(b, N, P, all, st);
+            if (rc || all) return rc;
+        }
+        return prompt_chunks(d, c, di, st);
+    }
+    if (c.seg) {
+        if (const int rc = launch_recurrence<false, true, false>(c, N, P, false, st)) return rc;
+        if (const int rc = carry(d, c, st)) return rc;
+    }
+    return launch_recurrence<false, true, true>(c, N, P, true, st);
 }
 
 }  // namespace linattn
@@ -205,8 +417,8 @@ static int launch_recurrence(const Args& a, int N, int P, cudaStream_t st) {
 using namespace rssm;
 
 extern "C" size_t rssm_linattn_workspace_size(const rssm_linattn_dims* d, int32_t n_tokens) {
-    if (linattn::check_dims(d) != RSSM_OK || n_tokens < 0 || d->act_dtype != RSSM_BF16) return 0;
-    return linattn::chunk_workspace(d, n_tokens);
+    if (linattn::check_dims(d) != RSSM_OK || n_tokens < 0) return 0;
+    return linattn::workspace_size(d, n_tokens);
 }
 
 extern "C" int rssm_linattn_prompt(const rssm_linattn_dims* d, const rssm_linattn_inputs* in, int32_t n_tokens,
@@ -225,13 +437,8 @@ extern "C" int rssm_linattn_prompt(const rssm_linattn_dims* d, const rssm_linatt
     a.resume = resume;
     a.tokens = n_tokens;
     a.each = n_tokens / d->batch;
-    const cudaStream_t st = (cudaStream_t)stream;
-    if (d->act_dtype == RSSM_BF16) {
-        const size_t need = linattn::chunk_workspace(d, n_tokens);
-        if (need && (!ok_ptr(workspace) || workspace_bytes < need)) return RSSM_ERR_INVALID_ARG;
-        return linattn::prompt_chunks(d, a, workspace, RSSM_WAIT_NS, st);
-    }
-    return linattn::launch_recurrence<false>(a, d->key_dim, d->value_dim, st);
+    if (!ok_ptr(workspace) || workspace_bytes < linattn::workspace_size(d, n_tokens)) return RSSM_ERR_INVALID_ARG;
+    return linattn::prompt(d, a, workspace, (cudaStream_t)stream);
 }
 
 extern "C" int rssm_linattn_step(const rssm_linattn_dims* d, const rssm_linattn_inputs* in, void* state,

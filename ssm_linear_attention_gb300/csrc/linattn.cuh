@@ -77,9 +77,98 @@ __device__ __forceinline__ bool row_of(const Args& a, int b, bool report, int& b
     return end > begin;
 }
 
-// bf16 activations (linattn_chunk.cu).
-size_t chunk_workspace(const rssm_linattn_dims* d, int n_tokens);
-int prompt_chunks(const rssm_linattn_dims* d, const Args& a, void* workspace, uint64_t wait_ns, cudaStream_t st);
+// A prompt's call: rows cut into segments.
+struct ChunkArgs {
+    Args a;
+    float* parts;      // states of the rows' segments [index][H][P][N]
+    float2* part_decay;  // and their decays, in two factors [index][H][2]
+    int kept;          // of either; behind them the states that cut rows began with, at first token / seg
+    int seg;           // tokens of a segment, a multiple of 64; 0: rows are not cut
+    int blocks;        // units of a segment: heads, or pairs of them
+    int units;         // upper limit of the rows' segments
+    uint32_t wait_ns;
+    int brief;         // rows of at most so many tokens go token by token (bf16 activations)
+    unsigned* claims;  // next item of those not dealt, CTAs that are done
+};
+
+
+// Two float32 in a register pair.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 two(float x, float y) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 one_by_one(f2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack2(f2 v) {
+    const float2 f = one_by_one(v);
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(f.y), "f"(f.x));
+    return r;
+}
+// 2^x as a float32 and its remainder, x in units of 2^-40, to some 2^-30 of itself: a table of 2^(i / 32) and a
+// polynomial of what is left (Tang, "Table-driven implementation of the exponential function", 1989).
+static __constant__ float2 kPow2[32] = {
+    {0x1.0000000000000p+0f, 0x0.0p+0f}, {0x1.059b0e0000000p+0f, -0x1.9d4f520000000p-25f}, {0x1.0b55860000000p+0f, 0x1.9f31220000000p-25f}, {0x1.11301e0000000p+0f, -0x1.fdb4960000000p-25f},
+    {0x1.172b840000000p+0f, -0x1.c157420000000p-27f}, {0x1.1d48740000000p+0f, -0x1.d2e8ca0000000p-25f}, {0x1.2387a60000000p+0f, 0x1.ceac480000000p-25f}, {0x1.29e9e00000000p+0f, -0x1.5c04240000000p-25f},
+    {0x1.306fe00000000p+0f, 0x1.4636e20000000p-25f}, {0x1.371a740000000p+0f, -0x1.18aac60000000p-25f}, {0x1.3dea640000000p+0f, 0x1.8246840000000p-25f}, {0x1.44e0860000000p+0f, 0x1.8624b40000000p-30f},
+    {0x1.4bfdae0000000p+0f, -0x1.593abc0000000p-25f}, {0x1.5342b60000000p+0f, -0x1.2c56100000000p-25f}, {0x1.5ab07e0000000p+0f, -0x1.5bd5ec0000000p-27f}, {0x1.6247ec0000000p+0f, -0x1.f8b5500000000p-25f},
+    {0x1.6a09e60000000p+0f, 0x1.9fcef40000000p-26f}, {0x1.71f75e0000000p+0f, 0x1.1d8bee0000000p-25f}, {0x1.7a11480000000p+0f, -0x1.829fd00000000p-25f}, {0x1.82589a0000000p+0f, -0x1.accc7c0000000p-26f},
+    {0x1.8ace540000000p+0f, 0x1.15506e0000000p-27f}, {0x1.93737c0000000p+0f, -0x1.e647440000000p-25f}, {0x1.9c49180000000p+0f, 0x1.51f8480000000p-27f}, {0x1.a5503c0000000p+0f, -0x1.b83b540000000p-25f},
+    {0x1.ae89fa0000000p+0f, -0x1.a94b140000000p-26f}, {0x1.b7f7700000000p+0f, -0x1.a094380000000p-25f}, {0x1.c199be0000000p+0f, -0x1.3d56b20000000p-27f}, {0x1.cb720e0000000p+0f, -0x1.8837cc0000000p-27f},
+    {0x1.d5818e0000000p+0f, -0x1.822dbc0000000p-27f}, {0x1.dfc9740000000p+0f, -0x1.908c940000000p-25f}, {0x1.ea4afa0000000p+0f, 0x1.52486c0000000p-27f}, {0x1.f507660000000p+0f, -0x1.246eb00000000p-26f}
+};
+__device__ __forceinline__ float2 exp2_pair(long long x) {
+    const int whole = (int)(x >> 40);
+    if (whole < -160) return make_float2(0.f, 0.f);
+    if (whole > 127) return make_float2(INFINITY, 0.f);
+    const uint64_t frac = (uint64_t)x & ((1ull << 40) - 1);
+    const float2 t = kPow2[frac >> 35];
+    const float r = (float)((uint32_t)(frac >> 3) & 0xffffffffu) * (0x1p-37f * 0.693147180559945f);
+    const float e = r + r * r * (0.5f + r * (1.f / 6.f + r * (1.f / 24.f)));
+    const float y = fmaf(t.x, e, t.y);
+    const float hi = t.x + y, lo = y - (hi - t.x);
+    const float a = __int_as_float(((whole >> 1) + 127) << 23), b = __int_as_float((whole - (whole >> 1) + 127) << 23);
+    return make_float2(hi * a * b, lo * a * b);
+}
+// log2(exp(g)) = x 2^-16 + y 2^-40, +-400 for what is beyond (an infinity too; 2^-400 is zero): 64 of them sum without
+// overflow in either part.
+__device__ __forceinline__ int2 log2_parts(float g) {
+    g = fminf(fmaxf(g, -277.f), 277.f);
+    const float L = 1.44269502162933349609375f, l = 1.925963e-8f;  // log2(e) = L + l
+    const float hi = g * L, lo = fmaf(g, l, fmaf(g, L, -hi));
+    const int x = __float2int_rn(hi * 65536.f);
+    const float rest = fmaf((float)x, -0x1p-16f, hi) + lo;
+    return make_int2(x, __float2int_rn(rest * 0x1p40f));
+}
+__device__ __forceinline__ float parts_to_float(int x, int y) { return fmaf((float)x, 0x1p-16f, (float)y * 0x1p-40f); }
+
+// The segments of a row of n tokens.
+__device__ __forceinline__ int segments(const ChunkArgs& c, int n) { return c.seg ? (n + c.seg - 1) / c.seg : 1; }
+
+// States after each segment from the segments' own ones (linattn.cu), and what bf16 activations do (linattn_chunk.cu).
+int carry(const rssm_linattn_dims* d, const ChunkArgs& c, cudaStream_t st);
+int chunk_blocks(const rssm_linattn_dims* d);
+int prompt_chunks(const rssm_linattn_dims* d, const ChunkArgs& c, const DeviceInfo& di, cudaStream_t st);
 
 }  // namespace linattn
 }  // namespace rssm

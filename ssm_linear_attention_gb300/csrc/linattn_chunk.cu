@@ -38,18 +38,6 @@ constexpr int kGates = 3;          // chunks whose decays are kept
 constexpr int kUnits = 4;          // units looked up ahead
 constexpr int kThreads = 768;
 
-struct ChunkArgs {
-    Args a;
-    float* parts;      // states of the rows' segments [index][H][P][N]
-    float2* part_decay;  // and their decays, in two factors [index][H][2]
-    int kept;          // of either; behind them the states that cut rows began with, at first token / seg
-    int seg;           // tokens of a segment, a multiple of 64; 0: rows are not cut
-    int blocks;        // units of a segment: heads, or pairs of them
-    int units;         // upper limit of the rows' segments
-    uint32_t wait_ns;
-    unsigned* claims;  // next item of those not dealt, CTAs that are done
-};
-
 enum { kZero = 0, kSlot = 1, kPart = 2 };
 // A segment of a row, for one head (or pair).
 struct Unit {
@@ -79,39 +67,6 @@ struct Chunk {
     static constexpr int UCONS = CONS + 1 + 2;          // warps that follow the list
 };
 
-// Two float32 in a register pair.
-typedef unsigned long long f2;
-__device__ __forceinline__ f2 two(float x, float y) {
-    f2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-    return r;
-}
-__device__ __forceinline__ float2 one_by_one(f2 v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-    f2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-    f2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-    f2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint32_t pack2(f2 v) {
-    const float2 f = one_by_one(v);
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(f.y), "f"(f.x));
-    return r;
-}
 // v's next bf16 part and the (exact) rest: v - h by a multiply-add that takes h's halves as they are.
 __device__ __forceinline__ uint32_t split2(f2 v, f2& rest) {
     const uint32_t h = pack2(v);
@@ -124,43 +79,6 @@ __device__ __forceinline__ uint32_t split2(f2 v, f2& rest) {
     rest = two(x, y);
     return h;
 }
-
-// 2^x as a float32 and its remainder, x in units of 2^-40, to some 2^-30 of itself: a table of 2^(i / 32) and a
-// polynomial of what is left (Tang, "Table-driven implementation of the exponential function", 1989).
-__constant__ float2 kPow2[32] = {
-    {0x1.0000000000000p+0f, 0x0.0p+0f}, {0x1.059b0e0000000p+0f, -0x1.9d4f520000000p-25f}, {0x1.0b55860000000p+0f, 0x1.9f31220000000p-25f}, {0x1.11301e0000000p+0f, -0x1.fdb4960000000p-25f},
-    {0x1.172b840000000p+0f, -0x1.c157420000000p-27f}, {0x1.1d48740000000p+0f, -0x1.d2e8ca0000000p-25f}, {0x1.2387a60000000p+0f, 0x1.ceac480000000p-25f}, {0x1.29e9e00000000p+0f, -0x1.5c04240000000p-25f},
-    {0x1.306fe00000000p+0f, 0x1.4636e20000000p-25f}, {0x1.371a740000000p+0f, -0x1.18aac60000000p-25f}, {0x1.3dea640000000p+0f, 0x1.8246840000000p-25f}, {0x1.44e0860000000p+0f, 0x1.8624b40000000p-30f},
-    {0x1.4bfdae0000000p+0f, -0x1.593abc0000000p-25f}, {0x1.5342b60000000p+0f, -0x1.2c56100000000p-25f}, {0x1.5ab07e0000000p+0f, -0x1.5bd5ec0000000p-27f}, {0x1.6247ec0000000p+0f, -0x1.f8b5500000000p-25f},
-    {0x1.6a09e60000000p+0f, 0x1.9fcef40000000p-26f}, {0x1.71f75e0000000p+0f, 0x1.1d8bee0000000p-25f}, {0x1.7a11480000000p+0f, -0x1.829fd00000000p-25f}, {0x1.82589a0000000p+0f, -0x1.accc7c0000000p-26f},
-    {0x1.8ace540000000p+0f, 0x1.15506e0000000p-27f}, {0x1.93737c0000000p+0f, -0x1.e647440000000p-25f}, {0x1.9c49180000000p+0f, 0x1.51f8480000000p-27f}, {0x1.a5503c0000000p+0f, -0x1.b83b540000000p-25f},
-    {0x1.ae89fa0000000p+0f, -0x1.a94b140000000p-26f}, {0x1.b7f7700000000p+0f, -0x1.a094380000000p-25f}, {0x1.c199be0000000p+0f, -0x1.3d56b20000000p-27f}, {0x1.cb720e0000000p+0f, -0x1.8837cc0000000p-27f},
-    {0x1.d5818e0000000p+0f, -0x1.822dbc0000000p-27f}, {0x1.dfc9740000000p+0f, -0x1.908c940000000p-25f}, {0x1.ea4afa0000000p+0f, 0x1.52486c0000000p-27f}, {0x1.f507660000000p+0f, -0x1.246eb00000000p-26f}
-};
-__device__ __forceinline__ float2 exp2_pair(long long x) {
-    const int whole = (int)(x >> 40);
-    if (whole < -160) return make_float2(0.f, 0.f);
-    if (whole > 127) return make_float2(INFINITY, 0.f);
-    const uint64_t frac = (uint64_t)x & ((1ull << 40) - 1);
-    const float2 t = kPow2[frac >> 35];
-    const float r = (float)((uint32_t)(frac >> 3) & 0xffffffffu) * (0x1p-37f * 0.693147180559945f);
-    const float e = r + r * r * (0.5f + r * (1.f / 6.f + r * (1.f / 24.f)));
-    const float y = fmaf(t.x, e, t.y);
-    const float hi = t.x + y, lo = y - (hi - t.x);
-    const float a = __int_as_float(((whole >> 1) + 127) << 23), b = __int_as_float((whole - (whole >> 1) + 127) << 23);
-    return make_float2(hi * a * b, lo * a * b);
-}
-// log2(exp(g)) = x 2^-16 + y 2^-40, +-400 for what is beyond (an infinity too; 2^-400 is zero): 64 of them sum without
-// overflow in either part.
-__device__ __forceinline__ int2 log2_parts(float g) {
-    g = fminf(fmaxf(g, -277.f), 277.f);
-    const float L = 1.44269502162933349609375f, l = 1.925963e-8f;  // log2(e) = L + l
-    const float hi = g * L, lo = fmaf(g, l, fmaf(g, L, -hi));
-    const int x = __float2int_rn(hi * 65536.f);
-    const float rest = fmaf((float)x, -0x1p-16f, hi) + lo;
-    return make_int2(x, __float2int_rn(rest * 0x1p40f));
-}
-__device__ __forceinline__ float parts_to_float(int x, int y) { return fmaf((float)x, 0x1p-16f, (float)y * 0x1p-40f); }
 
 // Wait for phase `parity` of the barrier at shared address `bar`: false once `limit` ns went by, or another warp has
 // set the flag at `stop`; then the flag is set. try_wait sleeps, so a wait costs few instructions; and it is
@@ -236,9 +154,6 @@ __device__ __forceinline__ void commit(uint64_t* bar, uint32_t leader) {
         "r"(leader)
         : "memory");
 }
-
-// The segments of a row of n tokens.
-__device__ __forceinline__ int segments(const ChunkArgs& c, int n) { return c.seg ? (n + c.seg - 1) / c.seg : 1; }
 
 template <int N, int P, bool PAIR, int SP, bool OUT>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -689,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     s = x - ((a.cu ? a.cu[b] : b * a.each) / c.seg + b);
                 }
                 int begin, end;
-                if (row_of(a, b, u.head == 0, begin, end, u.slot) && s >= 0 && s < segments(c, end - begin)) {
+                if (row_of(a, b, u.head == 0, begin, end, u.slot) && end - begin > c.brief && s >= 0 && s < segments(c, end - begin)) {
                     const int last = segments(c, end - begin) - 1;
                     u.tok = begin + s * c.seg;
                     u.n = s == last ? end - u.tok : c.seg;
@@ -960,85 +875,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 18) umma::tmem_dealloc(tmem, 512);
 }
 
-// parts[s] = the state after segment s, from its own state and what came before. A thread has four
-// values, and goes through the long rows and their segments with the next ones' loads in flight.
-__global__ void __launch_bounds__(256) carry_kernel(const ChunkArgs c, long all, int per_head) {
-    attn::wait_for_stream();
-    const Args& a = c.a;
-    const long e = ((long)blockIdx.x * 256 + threadIdx.x) * 4;
-    const int lane = threadIdx.x & 31;
-    const int h = (int)(min(e, all - 4) / per_head);
-    for (int b0 = 0; b0 < a.batch; b0 += 32) {
-        int begin = 0, end = 0, slot = 0, count = 0;
-        if (b0 + lane < a.batch && row_of(a, b0 + lane, false, begin, end, slot)) count = segments(c, end - begin) - 1;
-        for (uint32_t m = __ballot_sync(0xffffffffu, count > 1 || (count == 1 && a.resume && a.resume[b0 + lane])); m; m &= m - 1) {
-            const int l = __ffs(m) - 1, b = b0 + l;
-            const int first = __shfl_sync(0xffffffffu, begin, l) / c.seg, n = __shfl_sync(0xffffffffu, count, l);
-            const int sl = __shfl_sync(0xffffffffu, slot, l);
-            if (e >= all) continue;
-            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (a.resume && a.resume[b]) {
-                float f[4];
-                load4(static_cast<const char*>(a.state) + (sl * all + e) * (a.sbf ? 2 : 4), 0, a.sbf, f);
-                s = make_float4(f[0], f[1], f[2], f[3]);
-                // (the main launch writes the slot when the row's last segment ends, maybe before its first begins)
-                __stcg(reinterpret_cast<float4*>(c.parts + (c.kept + first) * all + e), s);
-            }
-            float4* const part = reinterpret_cast<float4*>(c.parts + first * all + e);
-            const float4* const decay = reinterpret_cast<const float4*>(c.part_decay) + (long)first * a.H + h;
-            constexpr int U = 8;
-            for (int i0 = 0; i0 < n; i0 += U) {
-                float4 x[U];
-                float4 f[U];
-#pragma unroll
-                for (int i = 0; i < U; ++i)
-                    if (i0 + i < n) {
-                        x[i] = __ldcg(part + (i0 + i) * (all / 4));
-                        f[i] = __ldcg(decay + (long)(i0 + i) * a.H);
-                    }
-#pragma unroll
-                for (int i = 0; i < U; ++i)
-                    if (i0 + i < n) {
-                        s.x = fmaf(f[i].z, s.x, f[i].w * s.x);
-                        s.x = fmaf(f[i].x, s.x, fmaf(f[i].y, s.x, x[i].x));
-                        s.y = fmaf(f[i].z, s.y, f[i].w * s.y);
-                        s.y = fmaf(f[i].x, s.y, fmaf(f[i].y, s.y, x[i].y));
-                        s.z = fmaf(f[i].z, s.z, f[i].w * s.z);
-                        s.z = fmaf(f[i].x, s.z, fmaf(f[i].y, s.z, x[i].z));
-                        s.w = fmaf(f[i].z, s.w, f[i].w * s.w);
-                        s.w = fmaf(f[i].x, s.w, fmaf(f[i].y, s.w, x[i].w));
-                        __stcg(part + (i0 + i) * (all / 4), s);
-                    }
-            }
-        }
-    }
-}
-
-// Tokens of a segment (0: rows are not cut): so many that all tokens in one row would give each SM about
-// three units, and no fewer than 512 (a cut reads k and v twice, and keeps a state).
-static int segment_tokens(const rssm_linattn_dims* d, int n_tokens, int blocks, int sms) {
-    long many = 3L * sms / blocks;
-    if (many < 1) many = 1;
-    long seg = (n_tokens + many - 1) / many;
-    if (seg < 512) seg = 512;
-    seg = (seg + kC - 1) / kC * kC;
-    return seg >= n_tokens ? 0 : (int)seg;
-}
-
 static int head_blocks(const rssm_linattn_dims* d) {
     const bool pair = d->value_dim == 64 && d->num_heads / d->num_k_heads % 2 == 0;
     return pair ? d->num_heads / 2 : d->num_heads;
-}
-
-size_t chunk_workspace(const rssm_linattn_dims* d, int n_tokens) {
-    DeviceInfo di;
-    if (!device_info(&di)) return 0;
-    // (the largest over every smaller number of tokens: the count of kept states does not fall with it)
-    const int blocks = head_blocks(d);
-    long many = 3L * di.sm_count / blocks;
-    if (many < 1) many = 1;
-    const long kept = n_tokens <= 512 ? 0 : many < n_tokens / 512 ? many : n_tokens / 512;
-    return 256 + (size_t)kept * d->num_heads * ((size_t)d->value_dim * d->key_dim * 8 + 16) + (kept ? 256 : 0);
 }
 
 template <int N, int P, bool PAIR, int SP>
@@ -1059,9 +898,7 @@ static int launch(const rssm_linattn_dims* d, const ChunkArgs& c, const DeviceIn
     };
     if (c.seg) {
         if (const int rc = run(chunk_kernel<N, P, PAIR, SP, false>, Chunk<N, P, PAIR, SP, false>::SMEM)) return rc;
-        const long all = (long)d->num_heads * P * N;
-        attn::launch_early(carry_kernel, (int)((all / 4 + 255) / 256), dim3(256), 0, st, c, all, P * N);
-        if (const int rc = launch_status()) return rc;
+        if (const int rc = carry(d, c, st)) return rc;
     }
     return run(chunk_kernel<N, P, PAIR, SP, true>, Chunk<N, P, PAIR, SP, true>::SMEM);
 }
@@ -1072,25 +909,12 @@ static int launch_heads(const rssm_linattn_dims* d, const ChunkArgs& c, const De
     return c.blocks < d->num_heads ? launch<N, 64, true, SP>(d, c, di, st) : launch<N, 64, false, SP>(d, c, di, st);
 }
 
-int prompt_chunks(const rssm_linattn_dims* d, const Args& a, void* workspace, uint64_t wait_ns, cudaStream_t st) {
-    DeviceInfo di;
-    if (!device_info(&di)) return RSSM_ERR_CUDA;
-    ChunkArgs c{};
-    c.a = a;
-    c.blocks = head_blocks(d);
-    c.seg = segment_tokens(d, a.tokens, c.blocks, di.sm_count);
-    c.units = (c.seg ? a.tokens / c.seg : 0) + a.batch;
-    c.wait_ns = (uint32_t)wait_ns;
-    c.claims = static_cast<unsigned*>(workspace);
-    if (c.seg) {
-        const size_t kept = a.tokens / c.seg;
-        c.kept = (int)kept;
-        c.part_decay = reinterpret_cast<float2*>(static_cast<char*>(workspace) + 256);
-        c.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + 256 + (kept * a.H * 16 + 255) / 256 * 256);
-    }
+int chunk_blocks(const rssm_linattn_dims* d) { return head_blocks(d); }
+
+int prompt_chunks(const rssm_linattn_dims* d, const ChunkArgs& c, const DeviceInfo& di, cudaStream_t st) {
     // (a float32 state keeps 24 bits of a decayed value, a bf16 one 16)
-    if (d->key_dim == 64) return a.sbf ? launch_heads<64, 2>(d, c, di, st) : launch_heads<64, 3>(d, c, di, st);
-    return a.sbf ? launch_heads<128, 2>(d, c, di, st) : launch_heads<128, 3>(d, c, di, st);
+    if (d->key_dim == 64) return c.a.sbf ? launch_heads<64, 2>(d, c, di, st) : launch_heads<64, 3>(d, c, di, st);
+    return c.a.sbf ? launch_heads<128, 2>(d, c, di, st) : launch_heads<128, 3>(d, c, di, st);
 }
 
 }  // namespace linattn
