@@ -68,38 +68,55 @@ __global__ void __launch_bounds__(128) step_kernel(const Args a, int P) {
     const int kh = h / (a.H / a.G);
     const long q0 = b * a.q_stride + kh * N, k0 = b * a.k_stride + kh * N;
     const long v0 = b * a.v_stride + (long)h * P + p0;
-    float q[V][E], k[V][E], v[R];
+    f2 q[V][E / 2], k[V][E / 2];
+    float v[R];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         const int at = (j * 8 + l) * E;
+        const char* const qp = static_cast<const char*>(a.q) + (q0 + at) * (ABF ? 2 : 4);
+        const char* const kp = static_cast<const char*>(a.k) + (k0 + at) * (ABF ? 2 : 4);
+        float x[E], y[E];
         if constexpr (E == 8) {
-            load8(static_cast<const char*>(a.q) + (q0 + at) * (ABF ? 2 : 4), ABF, q[j]);
-            load8(static_cast<const char*>(a.k) + (k0 + at) * (ABF ? 2 : 4), ABF, k[j]);
+            load8(qp, ABF, x);
+            load8(kp, ABF, y);
         } else {
-            load4(static_cast<const char*>(a.q) + (q0 + at) * (ABF ? 2 : 4), 0, ABF, q[j]);
-            load4(static_cast<const char*>(a.k) + (k0 + at) * (ABF ? 2 : 4), 0, ABF, k[j]);
+            load4(qp, 0, ABF, x);
+            load4(kp, 0, ABF, y);
+        }
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) {
+            q[j][e] = two(x[2 * e], x[2 * e + 1]);
+            k[j][e] = two(y[2 * e], y[2 * e + 1]);
         }
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) v[r] = load1(a.v, v0 + r * 4, ABF);
     const float f = expf(a.g[b * a.g_stride + h]);
     const float w = a.w ? a.w[b * a.w_stride + h] : 1.f;
+    const f2 ff = two(f, f);
     float o[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        const float u = w * v[r];
-        o[r] = 0.f;
+        const float u = __fmul_rn(w, v[r]);
+        const f2 uu = two(u, u);
+        f2 sum = 0;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             float y[E];
             unpack16<SBF>(x[r][j], y);
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                y[e] = f * y[e] + u * k[j][e];
-                o[r] += y[e] * q[j][e];
+            for (int e = 0; e < E / 2; ++e) {
+                // (rounded after each operation: a bf16 state then takes the same side of a tie wherever it is computed so)
+                const f2 n = add2(mul2(ff, two(y[2 * e], y[2 * e + 1])), mul2(uu, k[j][e]));
+                sum = fma2(n, q[j][e], sum);
+                const float2 z = one_by_one(n);
+                y[2 * e] = z.x;
+                y[2 * e + 1] = z.y;
             }
             __stcs(s + r * 4 * ROW + j * 8, pack16<SBF>(y));
         }
+        const float2 z = one_by_one(sum);
+        o[r] = z.x + z.y;
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {

@@ -19,15 +19,23 @@ from .hybrid import _check, _check_list, _check_out, _device, _Fixed, _index
 __all__ = ["LinearAttention", "Rotary"]
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _on_current(index):
     """The calls launch on the current device: a runner of another one is refused."""
-    if index < 0 or index != torch.cuda.current_device():
+    if index < 0 or index != _current_device():
         raise ValueError("the runner's device is not the current one")
 
 
 def _blocks(name, t, heads, dim, dtype, index):
     """Token count and element distance between consecutive tokens of t [tokens, heads, dim] (or
     [rows, T, heads, dim])."""
+    m = t.shape
+    if len(m) == 3 and m[1] == heads and m[2] == dim and t.dtype is dtype and t.get_device() == index:
+        s = t.stride()
+        if s[2] == 1 and (s[1] == dim or heads == 1):
+            return m[0], s[0] if m[0] > 1 else heads * dim
     if t.dtype is not dtype or t.get_device() != index or t.dim() not in (3, 4) or \
             t.shape[-2] != heads or t.shape[-1] != dim:
         raise ValueError("%s: %s tokens of [%d, %d] on the runner's device are wanted"
@@ -77,6 +85,7 @@ class LinearAttention(_Fixed):
         self._prompt, self._step = B.entry("rssm_linattn_prompt"), B.entry("rssm_linattn_step")
         self._addr = (self.state.data_ptr(), self.workspace.data_ptr(), self.dev_err.data_ptr(), self.o.data_ptr())
         self._index = _index(self.state.device)
+        self._tokens = {}
         self._plans = {}
 
     def dims(self, batch):
@@ -115,24 +124,50 @@ class LinearAttention(_Fixed):
             raise ValueError("%s: dense rows, evenly spaced, are wanted" % name)
         return t.stride(0)
 
+    def _plan(self, n):
+        """What calls of n tokens share: the shapes of dense inputs, their structure, o and its address. Kept,
+        because a small call's time is the host's."""
+        p = self._tokens.get(n)
+        if p is None:
+            if len(self._tokens) >= 256:  # prompts come in any number of tokens
+                self._tokens.clear()
+            inputs = B.LinattnInputs(None, None, None, None, None, self.G * self.N, self.G * self.N,
+                                     self.H * self.P, self.H, self.H, self.scale)
+            o = self.o[:n] if n <= self.max_tokens else None
+            p = self._tokens[n] = (torch.Size((n, self.G, self.N)), torch.Size((n, self.H, self.P)),
+                                   torch.Size((n, self.H)), inputs, ctypes.byref(inputs), o)
+        return p
+
     def _inputs(self, q, k, v, g, w):
-        i = self._index
-        n, qs = _blocks("q", q, self.G, self.N, self.act_dtype, i)
-        nk, ks = _blocks("k", k, self.G, self.N, self.act_dtype, i)
-        nv, vs = _blocks("v", v, self.H, self.P, self.act_dtype, i)
+        """Token count, a reference to the call's inputs and o. (Structures are read during a call only.)"""
+        n, i, act = q.shape[0], self._index, self.act_dtype
+        qk, vv, gates, inputs, ref, o = self._plan(n)
+        if q.dtype is act and k.dtype is act and v.dtype is act and q.shape == qk and k.shape == qk and v.shape == vv and \
+                g.shape == gates and g.dtype is torch.float32 and (w is None or w.shape == gates and w.dtype is torch.float32) and \
+                q.get_device() == k.get_device() == v.get_device() == g.get_device() == i and \
+                (w is None or w.get_device() == i and w.is_contiguous()) and \
+                q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and g.is_contiguous():
+            inputs.q, inputs.k, inputs.v, inputs.g = q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr()
+            inputs.w = None if w is None else w.data_ptr()
+            inputs.scale = self.scale
+            return n, ref, o
+        n, qs = _blocks("q", q, self.G, self.N, act, i)
+        nk, ks = _blocks("k", k, self.G, self.N, act, i)
+        nv, vs = _blocks("v", v, self.H, self.P, act, i)
         if nk != n or nv != n:
             raise ValueError("q, k and v must hold the same tokens")
         gs = self._gate("g", g, n)
         ws = 0 if w is None else self._gate("w", w, n)
-        return n, B.LinattnInputs(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
-                                  None if w is None else w.data_ptr(), qs, ks, vs, gs, ws, self.scale)
+        inputs = B.LinattnInputs(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+                                 None if w is None else w.data_ptr(), qs, ks, vs, gs, ws, self.scale)
+        return n, ctypes.byref(inputs), self._plan(n)[5]
 
-    def _out(self, o, n):
+    def _out(self, o, own, n):
         if o is not None:
             return o, _check_out("o", o, n * self.H * self.P, self.out_dtype, self._index)
-        if n > self.max_tokens:
+        if own is None:
             raise ValueError("%d tokens: the runner is made for %d" % (n, self.max_tokens))
-        return self.o[:n], self._addr[3]
+        return own, self._addr[3]
 
     def prompt(self, q, k, v, g, cache_indices, cu_tokens=None, w=None, resume=None, o=None, stream=None):
         """Tokens q, k [n, G, N], v [n, H, P] with decays g [n, H] (or [H]) and factors w [n, H]
@@ -140,12 +175,12 @@ class LinearAttention(_Fixed):
         uint8 or bool: rows that go on from their slot's state (None: every row begins from
         zero; True: none does). Returns o [n, H, P]."""
         b, dims = self._rows(cache_indices)
-        n, inputs = self._inputs(q, k, v, g, w)
+        n, inputs, own = self._inputs(q, k, v, g, w)
         if n > self.max_tokens:
             raise ValueError("%d tokens: the runner is made for %d" % (n, self.max_tokens))
         if cu_tokens is None and (n % b if b else n):
             raise ValueError("%d tokens of %d rows: cu_tokens is wanted" % (n, b))
-        o, o_ptr = self._out(o, n)
+        o, o_ptr = self._out(o, own, n)
         if resume is True:
             resume = torch.ones(b, device=self.device, dtype=torch.uint8)
         elif resume is False:
@@ -154,7 +189,7 @@ class LinearAttention(_Fixed):
                                    not resume.is_contiguous() or resume.get_device() != self._index):
             raise ValueError("resume must be a dense uint8 or bool list of %d on the runner's device" % b)
         state, ws, err, _ = self._addr
-        rc = self._prompt(dims, ctypes.byref(inputs), n, _check_list("cu_tokens", cu_tokens, b + 1, self._index),
+        rc = self._prompt(dims, inputs, n, _check_list("cu_tokens", cu_tokens, b + 1, self._index),
                           None if resume is None else resume.data_ptr(), state, cache_indices.data_ptr(), ws,
                           self.ws_bytes, o_ptr, err, B._stream(stream))
         if rc:
@@ -165,11 +200,11 @@ class LinearAttention(_Fixed):
         """One token of each row: q, k [b, G, N], v [b, H, P], g [b, H] (or [H]), w [b, H]. Padding
         rows: cache index -1. Returns o [b, H, P]."""
         b, dims = self._rows(cache_indices)
-        n, inputs = self._inputs(q, k, v, g, w)
+        n, inputs, own = self._inputs(q, k, v, g, w)
         if n != b:
             raise ValueError("a step takes one token of each row: %d tokens, %d rows" % (n, b))
-        o, o_ptr = self._out(o, n)
-        rc = self._step(dims, ctypes.byref(inputs), self._addr[0], cache_indices.data_ptr(), o_ptr, self._addr[2],
+        o, o_ptr = self._out(o, own, n)
+        rc = self._step(dims, inputs, self._addr[0], cache_indices.data_ptr(), o_ptr, self._addr[2],
                         B._stream(stream))
         if rc:
             raise B.RSSMError("rssm_linattn_step", rc)
