@@ -1012,6 +1012,16 @@ int rssm_debug_attn_decode(const rssm_attn_dims* dims, const rssm_attn_cache* ca
                            void* o, float* lse, int stall_tile, int wait_us, int32_t* dev_err,
                            rssm_stream_t stream);
 
+/* rssm_debug_linattn_prompt -- test / debug: rssm_linattn_prompt with a wait limit of wait_us microseconds
+ * (1..2000000) in place of 2 s and, for stall_chunk >= 0, the stage barrier of head 0's chunk that begins at
+ * token 64 * stall_chunk armed for 16 bytes more than its copies deliver (chunks on the tensor cores only). The copies land, the
+ * wait runs out, and the CTA winds down as rssm_linattn_prompt's would. The pages have no counterpart. */
+int rssm_debug_linattn_prompt(const rssm_linattn_dims* dims, const rssm_linattn_inputs* in,
+                              int32_t n_tokens, const int32_t* cu_tokens, const uint8_t* resume,
+                              void* state, const int32_t* cache_indices, void* workspace,
+                              size_t workspace_bytes, void* o, int stall_chunk, int wait_us,
+                              int32_t* dev_err, rssm_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -38,6 +38,7 @@ EXPORTS = (
     "rssm_attn_advance", "rssm_add_rmsnorm",
     "rssm_linattn_workspace_size", "rssm_linattn_prompt", "rssm_linattn_step", "rssm_rope",
     "rssm_debug_pipeline_copy", "rssm_debug_umma_fold", "rssm_debug_attn_decode",
+    "rssm_debug_linattn_prompt",
 )
 
 
@@ -118,6 +119,7 @@ def _declare(L):
     sig = {
         "rssm_linattn_workspace_size": (_SZ, [ld, _I32]),
         "rssm_linattn_prompt": (_I, [ld, li, _I32, _VP, _VP, _VP, _VP, _VP, _SZ, _VP, _VP, _VP]),
+        "rssm_debug_linattn_prompt": (_I, [ld, li, _I32, _VP, _VP, _VP, _VP, _VP, _SZ, _VP, _I, _I, _VP, _VP]),
         "rssm_linattn_step": (_I, [ld, li, _VP, _VP, _VP, _VP, _VP]),
         "rssm_rope": (_I, [ctypes.POINTER(RopeDims), _VP, f32, _VP, _VP, _VP, _VP, _VP, i64, _VP, i64,
                            _VP, i64, _VP, i64, _VP, _VP]),
@@ -635,6 +637,15 @@ def rssm_linattn_prompt(dims, inputs, n_tokens, cu_tokens, resume, state, cache_
     _call("rssm_linattn_prompt", ctypes.byref(dims), ctypes.byref(inputs), n_tokens,
           _ptr(cu_tokens), _ptr(resume), _ptr(state), _ptr(cache_indices), _ptr(workspace),
           workspace_bytes, _ptr(o), _ptr(dev_err), _stream(stream))
+
+
+def rssm_debug_linattn_prompt(dims, inputs, n_tokens, cu_tokens, resume, state, cache_indices, workspace,
+                              workspace_bytes, o, stall_chunk, wait_us, dev_err=None, stream=None):
+    """rssm_linattn_prompt with a wait limit of wait_us; stall_chunk >= 0 makes that chunk's wait run
+    out (test of the bounded waits)."""
+    _call("rssm_debug_linattn_prompt", ctypes.byref(dims), ctypes.byref(inputs), n_tokens,
+          _ptr(cu_tokens), _ptr(resume), _ptr(state), _ptr(cache_indices), _ptr(workspace),
+          workspace_bytes, _ptr(o), int(stall_chunk), int(wait_us), _ptr(dev_err), _stream(stream))
 
 
 def rssm_linattn_step(dims, inputs, state, cache_indices, o, dev_err=None, stream=None):

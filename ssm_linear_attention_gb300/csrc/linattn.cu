@@ -43,7 +43,8 @@ struct Step {
 };
 
 template <bool ABF, bool SBF, int N>
-__global__ void __launch_bounds__(128) step_kernel(const Args a, int P) {
+// (eight CTAs to an SM: 512 rows of 128 x 64 x 128 in bf16 320 us, with the five that fit otherwise 379)
+__global__ void __launch_bounds__(128, 8) step_kernel(const Args a, int P) {
     using C = Step<ABF, SBF, N>;
     constexpr int E = C::E, V = C::V, R = C::R;
     attn::wait_for_stream();
@@ -392,7 +393,7 @@ static size_t workspace_size(const rssm_linattn_dims* d, int n_tokens) {
 // the chunks' kernel costs its state's way through it, some 10 us).
 constexpr int kBrief = 32;
 
-static int prompt(const rssm_linattn_dims* d, const Args& a, void* workspace, cudaStream_t st) {
+static int prompt(const rssm_linattn_dims* d, const Args& a, void* workspace, int stall, uint64_t wait_ns, cudaStream_t st) {
     DeviceInfo di;
     if (!device_info(&di)) return RSSM_ERR_CUDA;
     const int N = d->key_dim, P = d->value_dim;
@@ -400,7 +401,8 @@ static int prompt(const rssm_linattn_dims* d, const Args& a, void* workspace, cu
     c.a = a;
     c.seg = segment_tokens(d, a.tokens, di.sm_count, nullptr);
     c.units = (c.seg ? a.tokens / c.seg : 0) + a.batch;
-    c.wait_ns = (uint32_t)RSSM_WAIT_NS;
+    c.wait_ns = (uint32_t)wait_ns;
+    c.stall = stall;
     c.claims = static_cast<unsigned*>(workspace);
     if (c.seg) {
         const size_t kept = a.tokens / c.seg;
@@ -438,10 +440,10 @@ extern "C" size_t rssm_linattn_workspace_size(const rssm_linattn_dims* d, int32_
     return linattn::workspace_size(d, n_tokens);
 }
 
-extern "C" int rssm_linattn_prompt(const rssm_linattn_dims* d, const rssm_linattn_inputs* in, int32_t n_tokens,
-                                   const int32_t* cu_tokens, const uint8_t* resume, void* state,
-                                   const int32_t* cache_indices, void* workspace, size_t workspace_bytes, void* o,
-                                   int32_t* dev_err, rssm_stream_t stream) {
+static int linattn_prompt(const rssm_linattn_dims* d, const rssm_linattn_inputs* in, int32_t n_tokens,
+                          const int32_t* cu_tokens, const uint8_t* resume, void* state, const int32_t* cache_indices,
+                          void* workspace, size_t workspace_bytes, void* o, int stall, uint64_t wait_ns, int32_t* dev_err,
+                          rssm_stream_t stream) {
     if (const int rc = linattn::check_dims(d)) return rc;
     if (n_tokens < 0) return RSSM_ERR_INVALID_ARG;
     if (!cu_tokens && d->batch && n_tokens % d->batch) return RSSM_ERR_CONFIG;
@@ -455,7 +457,24 @@ extern "C" int rssm_linattn_prompt(const rssm_linattn_dims* d, const rssm_linatt
     a.tokens = n_tokens;
     a.each = n_tokens / d->batch;
     if (!ok_ptr(workspace) || workspace_bytes < linattn::workspace_size(d, n_tokens)) return RSSM_ERR_INVALID_ARG;
-    return linattn::prompt(d, a, workspace, (cudaStream_t)stream);
+    return linattn::prompt(d, a, workspace, stall, wait_ns, (cudaStream_t)stream);
+}
+
+extern "C" int rssm_linattn_prompt(const rssm_linattn_dims* d, const rssm_linattn_inputs* in, int32_t n_tokens,
+                                   const int32_t* cu_tokens, const uint8_t* resume, void* state,
+                                   const int32_t* cache_indices, void* workspace, size_t workspace_bytes, void* o,
+                                   int32_t* dev_err, rssm_stream_t stream) {
+    return linattn_prompt(d, in, n_tokens, cu_tokens, resume, state, cache_indices, workspace, workspace_bytes, o, -1,
+                          RSSM_WAIT_NS, dev_err, stream);
+}
+
+extern "C" int rssm_debug_linattn_prompt(const rssm_linattn_dims* d, const rssm_linattn_inputs* in, int32_t n_tokens,
+                                         const int32_t* cu_tokens, const uint8_t* resume, void* state,
+                                         const int32_t* cache_indices, void* workspace, size_t workspace_bytes, void* o,
+                                         int stall_chunk, int wait_us, int32_t* dev_err, rssm_stream_t stream) {
+    if (wait_us < 1 || wait_us > 2000000) return RSSM_ERR_INVALID_ARG;
+    return linattn_prompt(d, in, n_tokens, cu_tokens, resume, state, cache_indices, workspace, workspace_bytes, o,
+                          stall_chunk < 0 ? -1 : stall_chunk, (uint64_t)wait_us * 1000, dev_err, stream);
 }
 
 extern "C" int rssm_linattn_step(const rssm_linattn_dims* d, const rssm_linattn_inputs* in, void* state,

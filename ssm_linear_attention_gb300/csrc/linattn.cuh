@@ -87,6 +87,7 @@ struct ChunkArgs {
     int blocks;        // units of a segment: heads, or pairs of them
     int units;         // upper limit of the rows' segments
     uint32_t wait_ns;
+    int stall;         // test: the chunk of head 0 that begins at token 64 stall has its loads' wait run out; -1: none
     int brief;         // rows of at most so many tokens go token by token (bf16 activations)
     unsigned* claims;  // next item of those not dealt, CTAs that are done
 };

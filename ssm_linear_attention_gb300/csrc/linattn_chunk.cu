@@ -563,7 +563,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 unsigned char* const to = smem + st.slot * C::STAGE;
                 if (elect_one()) {
                     uint64_t* const bar = &full[st.slot];
-                    mbar_arrive_expect_tx(bar, (OUT ? 2 : 1) * C::QB + C::VB);
+                    const bool stall = OUT && c.stall >= 0 && u.head == 0 && u.tok + t == c.stall * kC;
+                    mbar_arrive_expect_tx(bar, (OUT ? 2 : 1) * C::QB + C::VB + (stall ? 16 : 0));
 #pragma unroll
                     for (int x = 0; x < N / 64; ++x) {
                         tma_load_2d(to + C::QB + x * kBox, &kmap, kh * N + 64 * x, u.tok + t, bar, pol);
