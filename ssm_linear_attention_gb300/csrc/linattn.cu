@@ -171,8 +171,10 @@ __global__ void __launch_bounds__(128) recurrence_kernel(const ChunkArgs c, int 
         const bool row = row_of(a, b, report && h == 0 && part == 0, begin, end, slot);
         const int last = row ? segments(c, end - begin) - 1 : -1;
         place[0] = row && (!c.brief || end - begin <= c.brief) && s >= 0 && (OUT ? s <= last : s < last);
-        place[1] = begin + s * c.seg;
-        place[2] = s == last ? end : place[1] + c.seg;
+        if (place[0]) {
+            place[1] = begin + segment_begin(end - begin, last + 1, s);
+            place[2] = begin + segment_begin(end - begin, last + 1, s + 1);
+        }
         place[3] = slot;
         place[4] = s > 0 ? begin / c.seg + s - 1 : last > 0 ? c.kept + begin / c.seg : 0;  // the part it goes on from
         place[5] = !OUT ? 0 : s > 0 ? 2 : !a.resume || !a.resume[b] ? 0 : last > 0 ? 2 : 1;
@@ -367,18 +369,19 @@ int carry(const rssm_linattn_dims* d, const ChunkArgs& c, cudaStream_t st) {
     return launch_status();
 }
 
-// Tokens of a segment (0: rows are not cut): so many that all tokens in one row would give each SM about
+// Least tokens of a segment (0: rows are not cut): so many that all tokens in one row would give each SM about
 // `each` units, and no fewer than `least` (a cut reads k and v twice, and keeps a state). kept: states kept at most, for
 // any smaller number of tokens too.
 static int segment_tokens(const rssm_linattn_dims* d, int n_tokens, int sms, long* kept) {
     const bool chunks = d->act_dtype == RSSM_BF16;
     const int blocks = chunks ? chunk_blocks(d) : d->num_heads, least = chunks ? 512 : 64;
     const long each = chunks ? 3 : 4, many = each * sms / blocks < 1 ? 1 : each * sms / blocks;
-    if (kept) *kept = n_tokens <= least ? 0 : many < n_tokens / least ? many : n_tokens / least;
-    long seg = (n_tokens + many - 1) / many;
+    // (a segment rounded down to 64 tokens, and at least `least`, is at most an eighth, or half, shorter)
+    const long most = chunks ? many + many / 8 + 1 : 2 * many;
+    if (kept) *kept = n_tokens < 2 * least ? 0 : most < n_tokens / least ? most : n_tokens / least;
+    long seg = n_tokens / many / 64 * 64;
     if (seg < least) seg = least;
-    seg = (seg + 63) / 64 * 64;
-    return seg >= n_tokens ? 0 : (int)seg;
+    return 2 * seg > n_tokens ? 0 : (int)seg;
 }
 
 static size_t workspace_size(const rssm_linattn_dims* d, int n_tokens) {

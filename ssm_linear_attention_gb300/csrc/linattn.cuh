@@ -83,7 +83,7 @@ struct ChunkArgs {
     float* parts;      // states of the rows' segments [index][H][P][N]
     float2* part_decay;  // and their decays, in two factors [index][H][2]
     int kept;          // of either; behind them the states that cut rows began with, at first token / seg
-    int seg;           // tokens of a segment, a multiple of 64; 0: rows are not cut
+    int seg;           // least tokens of a segment; 0: rows are not cut
     int blocks;        // units of a segment: heads, or pairs of them
     int units;         // upper limit of the rows' segments
     uint32_t wait_ns;
@@ -163,8 +163,13 @@ __device__ __forceinline__ int2 log2_parts(float g) {
 }
 __device__ __forceinline__ float parts_to_float(int x, int y) { return fmaf((float)x, 0x1p-16f, (float)y * 0x1p-40f); }
 
-// The segments of a row of n tokens.
-__device__ __forceinline__ int segments(const ChunkArgs& c, int n) { return c.seg ? (n + c.seg - 1) / c.seg : 1; }
+// The segments of a row of n tokens, and the token that segment s of `count` begins with: rows of twice c.seg and more
+// are cut, into parts that differ by 64 tokens at most.
+__device__ __forceinline__ int segments(const ChunkArgs& c, int n) { return c.seg && n >= 2 * c.seg ? n / c.seg : 1; }
+__device__ __forceinline__ int segment_begin(int n, int count, int s) {
+    const int chunks = (n + 63) / 64, each = chunks / count;
+    return min(n, (s * each + min(s, chunks - each * count)) * 64);
+}
 
 // States after each segment from the segments' own ones (linattn.cu), and what bf16 activations do (linattn_chunk.cu).
 int carry(const rssm_linattn_dims* d, const ChunkArgs& c, cudaStream_t st);

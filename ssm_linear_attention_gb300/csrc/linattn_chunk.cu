@@ -363,8 +363,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 gv.next(kGates);
                 sv.next(ST);
             };
-            auto inputs = [&]() { return await(&gready[gv.slot], gv.parity) && await(&full[sv.slot], sv.parity); };
-            ok = all_of<1, 512>(warp != 0 || inputs());
+            // (each barrier has a warp of its own that waits at it)
+            auto inputs = [&]() {
+                return warp == 1 ? await(&gready[gv.slot], gv.parity) : warp != 2 || await(&full[sv.slot], sv.parity);
+            };
+            ok = all_of<1, 512>(inputs());
             if (!ok) break;
             make_values(0, k);
             if (OUT) give_state();
@@ -374,23 +377,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int t = 0; t < u.n; t += kC, ++k) {
                 const bool more = t + kC < u.n;
                 if (!OUT && more) {
-                    ok = all_of<1, 512>(warp != 0 || inputs());
+                    ok = all_of<1, 512>(inputs());
                     if (!ok) break;
                     make_values(t + kC, k + 1);
                 }
-                ok = all_of<1, 512>(warp != 0 || (await(&st_full, one.parity) && (!OUT || !more || inputs())));
+                ok = all_of<1, 512>(warp == 0 ? await(&st_full, one.parity) : !OUT || !more || inputs());
                 if (!ok) break;
                 const float2 f = gam[gr.slot][vh];
                 const f2 fx = two(f.x, f.x), fy = two(f.y, f.y);
                 umma::fence_after_sync();
+                float d[NS];
+                umma::ld_cols<NS>(at + C::DS + (OUT ? 0 : (k & 1) * N) + n0, d);
 #pragma unroll
-                for (int i = 0; i < NS / 2; i += 4) {
-                    float d[8];
-                    umma::ld_cols<8>(at + C::DS + (OUT ? 0 : (k & 1) * N) + n0 + 2 * i, d);
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        s[i + x] = fma2(fx, s[i + x], fma2(fy, s[i + x], two(d[2 * x], d[2 * x + 1])));
-                }
+                for (int x = 0; x < NS / 2; ++x) s[x] = fma2(fx, s[x], fma2(fy, s[x], two(d[2 * x], d[2 * x + 1])));
                 if (OUT && more) {
                     make_values(t + kC, k + 1);
                     give_state();
@@ -399,37 +398,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = all_of<1, 512>(warp != 0 || await(&o_full, one.parity));
                     if (!ok) break;
                     umma::fence_after_sync();
-                    const float* e = &ge[gr.slot][vh][i0];
-                    unsigned char* put = mine_out;
+                    const float* const e = &ge[gr.slot][vh][i0];
+                    float x[16], y[16];
+                    umma::ld_two16(at + C::INTER + i0, x, at + C::INTRA + vh * 64 + i0, y);
+                    umma::fence_before_sync();
+                    arrive(&o_free);
                     bulk_wait_read_all();  // (the chunk before's)
                     __syncwarp();
+                    if (a.obf) {
 #pragma unroll
-                    for (int i = 0; i < 16; i += 8, e += 8) {
-                        float x[8], y[8];
-                        umma::ld_cols<8>(at + C::INTER + i0 + i, x);
-                        umma::ld_cols<8>(at + C::INTRA + vh * 64 + i0 + i, y);
-                        if (i) {
-                            umma::fence_before_sync();
-                            arrive(&o_free);
+                        for (int j = 0; j < 16; j += 4) {
+                            const float4 g = *reinterpret_cast<const float4*>(e + j);
+                            const uint32_t w0 = pack2(fma2(two(g.x, g.y), two(x[j], x[j + 1]), two(y[j], y[j + 1])));
+                            const uint32_t w1 = pack2(fma2(two(g.z, g.w), two(x[j + 2], x[j + 3]), two(y[j + 2], y[j + 3])));
+                            uint16_t* const to16 = reinterpret_cast<uint16_t*>(mine_out + j * 64);
+                            to16[0] = (uint16_t)w0;
+                            to16[32] = (uint16_t)(w0 >> 16);
+                            to16[64] = (uint16_t)w1;
+                            to16[96] = (uint16_t)(w1 >> 16);
                         }
-                        if (a.obf) {
+                    } else {
 #pragma unroll
-                            for (int j = 0; j < 8; j += 4) {
-                                const float4 g = *reinterpret_cast<const float4*>(e + j);
-                                const uint32_t w0 = pack2(fma2(two(g.x, g.y), two(x[j], x[j + 1]), two(y[j], y[j + 1])));
-                                const uint32_t w1 = pack2(fma2(two(g.z, g.w), two(x[j + 2], x[j + 3]), two(y[j + 2], y[j + 3])));
-                                uint16_t* const to16 = reinterpret_cast<uint16_t*>(put + j * 64);
-                                to16[0] = (uint16_t)w0;
-                                to16[32] = (uint16_t)(w0 >> 16);
-                                to16[64] = (uint16_t)w1;
-                                to16[96] = (uint16_t)(w1 >> 16);
-                            }
-                            put += 8 * 64;
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) *reinterpret_cast<float*>(put + j * 128) = fmaf(e[j], x[j], y[j]);
-                            put += 8 * 128;
-                        }
+                        for (int j = 0; j < 16; ++j) *reinterpret_cast<float*>(mine_out + j * 128) = fmaf(e[j], x[j], y[j]);
                     }
                     if (__builtin_expect(any_odd[k & 3] == (int)(k + 1), 0)) {
                         // (values that are not finite were cleared: their rows' outputs from their token on are NaN)
@@ -491,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (n < 0) break;
                 bool ok = true;
                 for (int t = 0; t < n; t += kC) {
-                    ok = all_of<2, 128>(warp != 16 || (await(&gready[gr.slot], gr.parity) && await(&sc_full, one.parity)));
+                    ok = all_of<2, 128>(warp == 16 ? await(&gready[gr.slot], gr.parity) : warp != 17 || await(&sc_full, one.parity));
                     if (!ok) break;
                     umma::fence_after_sync();
                     const int upto = min(i, n - 1 - t);  // (later tokens' weights are zero)
@@ -607,8 +597,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int begin, end;
                 if (row_of(a, b, u.head == 0, begin, end, u.slot) && end - begin > c.brief && s >= 0 && s < segments(c, end - begin)) {
                     const int last = segments(c, end - begin) - 1;
-                    u.tok = begin + s * c.seg;
-                    u.n = s == last ? end - u.tok : c.seg;
+                    u.tok = begin + segment_begin(end - begin, last + 1, s);
+                    u.n = begin + segment_begin(end - begin, last + 1, s + 1) - u.tok;
                     u.part = s > 0 ? begin / c.seg + s - 1 : last > 0 ? c.kept + begin / c.seg : 0;
                     u.from = s > 0 ? kPart : !a.resume || !a.resume[b] ? kZero : last > 0 ? kPart : kSlot;
                     u.to = s == last ? kSlot : kZero;
@@ -658,12 +648,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (uint32_t m = __ballot_sync(0xffffffffu, count > 0); m && ok; m &= m - 1) {
                     const int l = __ffs(m) - 1;
                     const int first = __shfl_sync(0xffffffffu, begin, l);
-                    const unsigned more = (unsigned)__shfl_sync(0xffffffffu, count, l) * c.blocks;
+                    const int n = __shfl_sync(0xffffffffu, end, l) - first, last = __shfl_sync(0xffffffffu, count, l);
+                    const unsigned more = (unsigned)last * c.blocks;
                     for (; next < more && ok; next += gridDim.x) {
                         const int s = next / (unsigned)c.blocks;
                         Unit u;
-                        u.tok = first + s * c.seg;
-                        u.n = c.seg;
+                        const int from = segment_begin(n, last + 1, s);
+                        u.tok = first + from;
+                        u.n = segment_begin(n, last + 1, s + 1) - from;
                         u.head = (int)(next - s * c.blocks) * VH;
                         u.slot = 0;
                         u.part = first / c.seg + s;
@@ -730,8 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 v1.next(1);
                 if (OUT) {
-                    if (t + kC < n) ok = scores();
-                    ok = ok && await(&s0_ready, s1.parity) && await(&o_free, s1.parity ^ 1);
+                    ok = await(&s0_ready, s1.parity) && await(&o_free, s1.parity ^ 1);
                     if (!ok) break;
                     umma::fence_after_sync();
                     const uint64_t qd = umma::smem_desc_swizzle128(stage, 16, 1024);
@@ -743,7 +734,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                      qd + ((x / 4 * kBox + x % 4 * 32) >> 4), i_inter, z + x > 0, leader);
                     commit(&st_full, leader);  // (of dS as well, which was issued before)
                     s1.next(1);
-                    ok = await(&w_ready, w1.parity);
+                    if (t + kC < n) ok = scores();
+                    ok = ok && await(&w_ready, w1.parity);
                     if (!ok) break;
                     umma::fence_after_sync();
                     const uint64_t vd = umma::smem_desc_swizzle128(stage + 2 * C::QB, lbo, 1024);

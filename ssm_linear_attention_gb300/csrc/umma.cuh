@@ -258,6 +258,20 @@ __device__ __forceinline__ void st_cols(uint32_t taddr, const float (&v)[N]) {
         "f"(v[31]) : "memory");
 }
 
+// Two loads of 16 columns, waited for together.
+__device__ __forceinline__ void ld_two16(uint32_t a_taddr, float (&a)[16], uint32_t b_taddr, float (&b)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%32];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+        "%30, %31}, [%33];\n\ttcgen05.wait::ld.sync.aligned;"
+        : "=f"(a[0]), "=f"(a[1]), "=f"(a[2]), "=f"(a[3]), "=f"(a[4]), "=f"(a[5]), "=f"(a[6]), "=f"(a[7]), "=f"(a[8]),
+          "=f"(a[9]), "=f"(a[10]), "=f"(a[11]), "=f"(a[12]), "=f"(a[13]), "=f"(a[14]), "=f"(a[15]), "=f"(b[0]),
+          "=f"(b[1]), "=f"(b[2]), "=f"(b[3]), "=f"(b[4]), "=f"(b[5]), "=f"(b[6]), "=f"(b[7]), "=f"(b[8]), "=f"(b[9]),
+          "=f"(b[10]), "=f"(b[11]), "=f"(b[12]), "=f"(b[13]), "=f"(b[14]), "=f"(b[15])
+        : "r"(a_taddr), "r"(b_taddr));
+}
+
 // ------------------------------------------------------- bf16 splitting ----
 
 // x = hi + mid + lo with each part a bf16 (x's float32 significand, 24 bits, is
