@@ -7,7 +7,7 @@
 // of one value row, eight lanes a row, so that a sum over N takes three shuffles.
 //
 // The recurrence over a prompt keeps 64 value rows of a head in the registers of a CTA and takes one token
-// after another: float32 activations, cut into segments as the chunks are, and rows of few tokens.
+// after another: float32 activations, cut into segments as the chunks are.
 #include "linattn.cuh"
 
 namespace rssm {
@@ -137,13 +137,13 @@ static int launch_step(const Args& a, int N, int P, cudaStream_t st) {
 
 // ------------------------------------------------ a prompt, token by token ----
 
-// Float32 activations, and rows of few tokens. A CTA has 64 value rows of a head: a lane group of eight has rows
-// r, r + 4, r + 8, r + 12 of its warp's 16 and a lane of it keys 4 l + 32 j .. + 3, all in registers. EXACT: the decays as a
-// float32 and its remainder (rounded decays would be wrong in the same direction at every token of a long memory).
+// Float32 activations. A CTA has 64 value rows of a head: a lane group of eight has rows r, r + 4, r + 8, r + 12 of its
+// warp's 16 and a lane of it keys 4 l + 32 j .. + 3, all in registers. The decays are a float32 and its remainder (rounded
+// decays would be wrong in the same direction at every token of a long memory).
 // OUT false: a segment's own state, from zero.
 constexpr int kTile = 16;  // tokens staged at a time
 
-template <bool ABF, int N, bool EXACT, bool OUT>
+template <int N, bool OUT>
 __global__ void __launch_bounds__(128) recurrence_kernel(const ChunkArgs c, int P, bool report) {
     constexpr int J = N / 32;
     const Args& a = c.a;
@@ -170,10 +170,10 @@ __global__ void __launch_bounds__(128) recurrence_kernel(const ChunkArgs c, int 
         }
         const bool row = row_of(a, b, report && h == 0 && part == 0, begin, end, slot);
         const int last = row ? segments(c, end - begin) - 1 : -1;
-        place[0] = row && (!c.brief || end - begin <= c.brief) && s >= 0 && (OUT ? s <= last : s < last);
+        place[0] = row && s >= 0 && (OUT ? s <= last : s < last);
         if (place[0]) {
-            place[1] = begin + segment_begin(end - begin, last + 1, s);
-            place[2] = begin + segment_begin(end - begin, last + 1, s + 1);
+            place[1] = begin + segment_begin(c, end - begin, last + 1, s);
+            place[2] = begin + segment_begin(c, end - begin, last + 1, s + 1);
         }
         place[3] = slot;
         place[4] = s > 0 ? begin / c.seg + s - 1 : last > 0 ? c.kept + begin / c.seg : 0;  // the part it goes on from
@@ -206,29 +206,24 @@ __global__ void __launch_bounds__(128) recurrence_kernel(const ChunkArgs c, int 
         for (int e = t; e < n * (N / 4); e += 128) {
             const int i = e / (N / 4), col = e % (N / 4) * 4;
             const long row = i0 + i;
-            if (OUT) load4(static_cast<const char*>(a.q) + (row * a.q_stride + kh * N + col) * (ABF ? 2 : 4), 0, ABF, &sq[i][col]);
-            load4(static_cast<const char*>(a.k) + (row * a.k_stride + kh * N + col) * (ABF ? 2 : 4), 0, ABF, &sk[i][col]);
+            if (OUT) load4(static_cast<const float*>(a.q) + row * a.q_stride + kh * N + col, 0, false, &sq[i][col]);
+            load4(static_cast<const float*>(a.k) + row * a.k_stride + kh * N + col, 0, false, &sk[i][col]);
         }
         for (int e = t; e < n * 16; e += 128) {
             const int i = e / 16, col = e % 16 * 4;
-            load4(static_cast<const char*>(a.v) + ((i0 + i) * a.v_stride + (long)h * P + part * 64 + col) * (ABF ? 2 : 4), 0, ABF, &sv[i][col]);
+            load4(static_cast<const float*>(a.v) + (i0 + i) * a.v_stride + (long)h * P + part * 64 + col, 0, false, &sv[i][col]);
         }
         if (t < n) {
             const float g = a.g[(i0 + t) * a.g_stride + h];
             sw[t] = a.w ? a.w[(i0 + t) * a.w_stride + h] : 1.f;
-            if (EXACT) {
-                const int2 x = log2_parts(g);
-                const long long fixed = ((long long)x.x << 24) + x.y;
-                sf[t] = g != g ? make_float2(g, g) : exp2_pair(fixed);
-                if (!OUT) {
-                    if (g != g) total = 1ll << 62;
-                    atomicAdd(reinterpret_cast<unsigned long long*>(&total), (unsigned long long)fixed);
-                }
-            } else {
-                sf[t] = make_float2(expf(g), 0.f);
-            }
+            const int2 x = log2_parts(g);
+            const long long fixed = ((long long)x.x << 24) + x.y;
+            sf[t] = g != g ? make_float2(g, g) : exp2_pair(fixed);
+            if (!OUT) atomicAdd(reinterpret_cast<unsigned long long*>(&total), (unsigned long long)fixed);
         }
         __syncthreads();
+        // (kept from overflow: far beyond float32's exponents)
+        if (!OUT && t == 0) total = max(-(1ll << 52), min(1ll << 52, total));
 #pragma unroll 1
         for (int i = 0; i < n; ++i) {
             const f2 fh = two(sf[i].x, sf[i].x), fl = two(sf[i].y, sf[i].y);
@@ -255,9 +250,7 @@ __global__ void __launch_bounds__(128) recurrence_kernel(const ChunkArgs c, int 
                 for (int j = 0; j < J; ++j)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        f2 y = mul2(uu, k[j][e]);
-                        if (EXACT) y = fma2(fl, s[r][j][e], y);
-                        s[r][j][e] = fma2(fh, s[r][j][e], y);
+                        s[r][j][e] = fma2(fh, s[r][j][e], fma2(fl, s[r][j][e], mul2(uu, k[j][e])));
                         if (OUT) sum = fma2(s[r][j][e], q[j][e], sum);
                     }
                 const float2 f = one_by_one(sum);
@@ -280,9 +273,9 @@ __global__ void __launch_bounds__(128) recurrence_kernel(const ChunkArgs c, int 
         }
     }
     if (!OUT && t == 0 && part == 0) {
-        const float nan = __uint_as_float(0x7fc00000u);
+        // (a decay that is NaN shows in the state)
         float2* const to = c.part_decay + ((long)place[7] * a.H + h) * 2;
-        to[0] = total > (1ll << 61) ? make_float2(nan, nan) : exp2_pair(total);
+        to[0] = exp2_pair(total);
         to[1] = make_float2(1.f, 0.f);
     }
     if (OUT && !place[6]) return;
@@ -300,11 +293,11 @@ __global__ void __launch_bounds__(128) recurrence_kernel(const ChunkArgs c, int 
         }
 }
 
-template <bool ABF, bool EXACT, bool OUT>
+template <bool OUT>
 static int launch_recurrence(const ChunkArgs& c, int N, int P, bool report, cudaStream_t st) {
     const int grid = c.units * c.a.H * (P / 64);
-    if (N == 64) attn::launch_early(recurrence_kernel<ABF, 64, EXACT, OUT>, grid, 128, 0, st, c, P, report);
-    else attn::launch_early(recurrence_kernel<ABF, 128, EXACT, OUT>, grid, 128, 0, st, c, P, report);
+    if (N == 64) attn::launch_early(recurrence_kernel<64, OUT>, grid, 128, 0, st, c, P, report);
+    else attn::launch_early(recurrence_kernel<128, OUT>, grid, 128, 0, st, c, P, report);
     return launch_status();
 }
 
@@ -374,12 +367,11 @@ int carry(const rssm_linattn_dims* d, const ChunkArgs& c, cudaStream_t st) {
 // any smaller number of tokens too.
 static int segment_tokens(const rssm_linattn_dims* d, int n_tokens, int sms, long* kept) {
     const bool chunks = d->act_dtype == RSSM_BF16;
-    const int blocks = chunks ? chunk_blocks(d) : d->num_heads, least = chunks ? 512 : 64;
+    const int blocks = chunks ? chunk_blocks(d) : d->num_heads, least = chunks ? 512 : 48, unit = chunks ? 64 : 1;
     const long each = chunks ? 3 : 4, many = each * sms / blocks < 1 ? 1 : each * sms / blocks;
-    // (a segment rounded down to 64 tokens, and at least `least`, is at most an eighth, or half, shorter)
-    const long most = chunks ? many + many / 8 + 1 : 2 * many;
+    const long most = many + many * unit / least + 1;  // (rounded down to a unit, and no shorter than `least`)
     if (kept) *kept = n_tokens < 2 * least ? 0 : most < n_tokens / least ? most : n_tokens / least;
-    long seg = n_tokens / many / 64 * 64;
+    long seg = n_tokens / many / unit * unit;
     if (seg < least) seg = least;
     return 2 * seg > n_tokens ? 0 : (int)seg;
 }
@@ -392,10 +384,6 @@ static size_t workspace_size(const rssm_linattn_dims* d, int n_tokens) {
     return 256 + (size_t)kept * d->num_heads * ((size_t)d->value_dim * d->key_dim * 8 + 16) + (kept ? 256 : 0);
 }
 
-// Rows of few tokens: where they are short on the average, those of at most 32 go token by token (a unit of
-// the chunks' kernel costs its state's way through it, some 10 us).
-constexpr int kBrief = 32;
-
 static int prompt(const rssm_linattn_dims* d, const Args& a, void* workspace, int stall, uint64_t wait_ns, cudaStream_t st) {
     DeviceInfo di;
     if (!device_info(&di)) return RSSM_ERR_CUDA;
@@ -403,6 +391,7 @@ static int prompt(const rssm_linattn_dims* d, const Args& a, void* workspace, in
     ChunkArgs c{};
     c.a = a;
     c.seg = segment_tokens(d, a.tokens, di.sm_count, nullptr);
+    c.unit = d->act_dtype == RSSM_BF16 ? 64 : 1;
     c.units = (c.seg ? a.tokens / c.seg : 0) + a.batch;
     c.wait_ns = (uint32_t)wait_ns;
     c.stall = stall;
@@ -417,20 +406,17 @@ static int prompt(const rssm_linattn_dims* d, const Args& a, void* workspace, in
         c.blocks = chunk_blocks(d);
         if (a.tokens <= (int64_t)kBrief * a.batch) {
             c.brief = kBrief;
-            ChunkArgs b = c;
-            b.seg = 0;
-            b.units = a.batch;
-            const bool all = a.tokens <= kBrief || !a.cu;  // no row is longer
-            const int rc = launch_recurrence<true, false, true>(b, N, P, all, st);
+            const bool all = a.tokens <= kBrief || !a.cu;  // (no row is longer)
+            const int rc = prompt_brief(d, a, all, st);
             if (rc || all) return rc;
         }
         return prompt_chunks(d, c, di, st);
     }
     if (c.seg) {
-        if (const int rc = launch_recurrence<false, true, false>(c, N, P, false, st)) return rc;
+        if (const int rc = launch_recurrence<false>(c, N, P, false, st)) return rc;
         if (const int rc = carry(d, c, st)) return rc;
     }
-    return launch_recurrence<false, true, true>(c, N, P, true, st);
+    return launch_recurrence<true>(c, N, P, true, st);
 }
 
 }  // namespace linattn

@@ -83,12 +83,12 @@ struct ChunkArgs {
     float* parts;      // states of the rows' segments [index][H][P][N]
     float2* part_decay;  // and their decays, in two factors [index][H][2]
     int kept;          // of either; behind them the states that cut rows began with, at first token / seg
-    int seg;           // least tokens of a segment; 0: rows are not cut
+    int seg, unit;     // least tokens of a segment (0: rows are not cut), and what they differ by
     int blocks;        // units of a segment: heads, or pairs of them
     int units;         // upper limit of the rows' segments
     uint32_t wait_ns;
     int stall;         // test: the chunk of head 0 that begins at token 64 stall has its loads' wait run out; -1: none
-    int brief;         // rows of at most so many tokens go token by token (bf16 activations)
+    int brief;         // rows of at most so many tokens are not the chunks' kernel's
     unsigned* claims;  // next item of those not dealt, CTAs that are done
 };
 
@@ -126,6 +126,19 @@ __device__ __forceinline__ uint32_t pack2(f2 v) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(f.y), "f"(f.x));
     return r;
 }
+// v's next bf16 part and the (exact) rest: v - h by a multiply-add that takes h's halves as they are.
+__device__ __forceinline__ uint32_t split2(f2 v, f2& rest) {
+    const uint32_t h = pack2(v);
+    const float2 f = one_by_one(v);
+    float x, y;
+    asm("{\n\t.reg .b16 l, h, m;\n\tmov.b32 {l, h}, %2;\n\tmov.b16 m, 0xBF80;\n\t"
+        "fma.rn.f32.bf16 %0, l, m, %3;\n\tfma.rn.f32.bf16 %1, h, m, %4;\n\t}"
+        : "=f"(x), "=f"(y)
+        : "r"(h), "f"(f.x), "f"(f.y));
+    rest = two(x, y);
+    return h;
+}
+
 // 2^x as a float32 and its remainder, x in units of 2^-40, to some 2^-30 of itself: a table of 2^(i / 32) and a
 // polynomial of what is left (Tang, "Table-driven implementation of the exponential function", 1989).
 static __constant__ float2 kPow2[32] = {
@@ -164,13 +177,18 @@ __device__ __forceinline__ int2 log2_parts(float g) {
 __device__ __forceinline__ float parts_to_float(int x, int y) { return fmaf((float)x, 0x1p-16f, (float)y * 0x1p-40f); }
 
 // The segments of a row of n tokens, and the token that segment s of `count` begins with: rows of twice c.seg and more
-// are cut, into parts that differ by 64 tokens at most.
+// are cut, into parts that differ by c.unit tokens at most.
 __device__ __forceinline__ int segments(const ChunkArgs& c, int n) { return c.seg && n >= 2 * c.seg ? n / c.seg : 1; }
-__device__ __forceinline__ int segment_begin(int n, int count, int s) {
-    const int chunks = (n + 63) / 64, each = chunks / count;
-    return min(n, (s * each + min(s, chunks - each * count)) * 64);
+__device__ __forceinline__ int segment_begin(const ChunkArgs& c, int n, int count, int s) {
+    const int units = (n + c.unit - 1) / c.unit, each = units / count;
+    return min(n, (s * each + min(s, units - each * count)) * c.unit);
 }
 
+// Rows of few tokens, bf16 activations: where they are short on the average, those of at most 32 have a kernel of their own
+// (linattn_brief.cu).
+constexpr int kBrief = 32;
+
+int prompt_brief(const rssm_linattn_dims* d, const Args& a, bool report, cudaStream_t st);
 // States after each segment from the segments' own ones (linattn.cu), and what bf16 activations do (linattn_chunk.cu).
 int carry(const rssm_linattn_dims* d, const ChunkArgs& c, cudaStream_t st);
 int chunk_blocks(const rssm_linattn_dims* d);

@@ -1,0 +1,321 @@
+// linattn_brief.cu -- linear attention over rows of at most 32 tokens, bf16 activations: a row's tokens as one chunk.
+//
+// With the chunk's formulas (G_i the logarithms' sum up to token i, S_0 the state before, tokens i and j of the row):
+//     o_i = scale (exp(G_i) S_0 q_i + sum_{j<=i} W_ij v_j),   W_ij = exp(G_i - G_j) w_j (q_i . k_j)
+//     S   = exp(G_end) S_0 + sum_j V'_j k_j^T,                V'_j = exp(G_end - G_j) w_j v_j
+// What it has to move is the states, each read and written once, so a CTA is small (64 value rows of a head, in registers)
+// and several on an SM hide each other's loads, products and stores; a tile of 128 x 128 of the tensor memory would be a
+// state alone, and its way in and out the time. The products are 16 x 8 x 16 ones between registers: a warp has 16 value
+// rows of the state as the accumulators of 16 x 8 tiles, lane 4 r + c rows r and r + 8 and of each 16 keys the four from
+// 4 c on (one access of 16 bytes). That order of the keys is the products' own, so q and k are stored in shared memory
+// with their pairs in it, and the accumulators are the second operand of o = q S_0^T as they are, in two bf16 parts.
+// W enters as two parts too, V' as two for a bf16 state and three (24 bits) for a float32 one, as for longer rows.
+#include "linattn.cuh"
+#include "warps.cuh"
+
+namespace rssm {
+namespace linattn {
+
+constexpr int kT = kBrief;          // tokens of a row
+constexpr int kVRow = 64 * 2 + 16;  // bytes of a token's 64 values; rows are 16 bytes apart modulo 128: eight of them
+constexpr int kWRow = kT * 2 + 16;  // at one column lie in different banks, 80 bytes too
+
+__device__ __forceinline__ void ldsm(uint32_t at, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm_t(uint32_t at, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
+}
+// d += a (16 x 16) b (16 x 8). Lane 4 r + c: a rows r, r + 8, r, r + 8, columns 2 c (+ 8 in the last two) and on; b rows
+// 2 c, 2 c + 8 and on of column r; d rows r, r, r + 8, r + 8, columns 2 c, 2 c + 1.
+__device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// SP: bf16 parts of a decayed value.
+template <int N, int SP>
+__global__ void __launch_bounds__(128, 4) brief_kernel(const Args a, int P, bool report) {
+    constexpr int K = N / 16, ROW = N * 2 + 16;
+    __shared__ __align__(16) unsigned char sq[kT * ROW], sk[kT * ROW], sv[kT * kVRow], sw[2][kT * kWRow];
+    __shared__ float whole[kT], frac[kT], weight[kT], grown[kT], shrunk[kT];
+    __shared__ float2 gamma;
+    __shared__ int odd_from[64];
+    attn::wait_for_stream();
+    const int parts = P / 64, part = blockIdx.x % parts, bh = blockIdx.x / parts, b = bh / a.H, h = bh - b * a.H;
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31, r0 = lane >> 2, c0 = lane & 3;
+    int begin, end, slot;
+    if (!row_of(a, b, report && h == 0 && part == 0 && t == 0, begin, end, slot) || end - begin > kT) return;
+    const int n = end - begin, steps = (n + 15) / 16;
+    const int kh = h / (a.H / a.G);
+
+    // q, k and v, zero beyond the row
+    constexpr int PIECES = kT * (N / 8) / 128;
+    uint4 x[PIECES], y[PIECES], z[2];
+#pragma unroll
+    for (int u = 0; u < PIECES; ++u) {
+        const int e = u * 128 + t, i = e / (N / 8), col = e % (N / 8);
+        x[u] = y[u] = make_uint4(0, 0, 0, 0);
+        if (i >= n) continue;
+        x[u] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + (begin + i) * a.q_stride + kh * N + col * 8);
+        y[u] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.k) + (begin + i) * a.k_stride + kh * N + col * 8);
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int i = u * 16 + t / 8;
+        z[u] = make_uint4(0, 0, 0, 0);
+        if (i < n) z[u] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.v) + (begin + i) * a.v_stride + (long)h * P + part * 64 + t % 8 * 8);
+    }
+    float g = 0.f, w = 0.f;
+    if (warp == 0 && lane < n) {
+        g = a.g[(begin + lane) * a.g_stride + h];
+        w = a.w ? a.w[(begin + lane) * a.w_stride + h] : 1.f;
+    }
+    // the state: s[k][r][p] has keys 16 k + 4 c0 + 2 p and on of row r0 + 8 r
+    const long at = (((long)slot * a.H + h) * P + part * 64 + warp * 16 + r0) * N + 4 * c0;
+    f2 s[K][2][2];
+    const bool resume = a.resume && a.resume[b];
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            float f[4] = {0.f, 0.f, 0.f, 0.f};
+            const long i = at + r * 8 * N + k * 16;
+            if (resume && a.sbf) {
+                const uint2 w = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.state) + i));
+                f[0] = bf16_lo(w.x); f[1] = bf16_hi(w.x); f[2] = bf16_lo(w.y); f[3] = bf16_hi(w.y);
+            } else if (resume) {
+                const float4 w = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(a.state) + i));
+                f[0] = w.x; f[1] = w.y; f[2] = w.z; f[3] = w.w;
+            }
+            s[k][r][0] = two(f[0], f[1]);
+            s[k][r][1] = two(f[2], f[3]);
+        }
+    // of 16 keys' eight pairs, 2 c goes to c and 2 c + 1 to 4 + c
+#pragma unroll
+    for (int u = 0; u < PIECES; ++u) {
+        const int e = u * 128 + t, i = e / (N / 8), col = e % (N / 8);
+        const int to = i * ROW + (col >> 1) * 32 + (col & 1) * 8;
+        *reinterpret_cast<uint2*>(sq + to) = make_uint2(x[u].x, x[u].z);
+        *reinterpret_cast<uint2*>(sq + to + 16) = make_uint2(x[u].y, x[u].w);
+        *reinterpret_cast<uint2*>(sk + to) = make_uint2(y[u].x, y[u].z);
+        *reinterpret_cast<uint2*>(sk + to + 16) = make_uint2(y[u].y, y[u].w);
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) *reinterpret_cast<uint4*>(sv + (u * 16 + t / 8) * kVRow + t % 8 * 16) = z[u];
+    if (warp == 0) {
+        // decays: lane i has token i
+        const float nan = __uint_as_float(0x7fc00000u);
+        int2 x = log2_parts(g);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int ux = __shfl_up_sync(0xffffffffu, x.x, o), uy = __shfl_up_sync(0xffffffffu, x.y, o);
+            if (lane >= o) {
+                x.x += ux;
+                x.y += uy;
+            }
+        }
+        const int2 all = make_int2(__shfl_sync(0xffffffffu, x.x, 31), __shfl_sync(0xffffffffu, x.y, 31));
+        const uint32_t bad = __ballot_sync(0xffffffffu, g != g);
+        // (the whole part apart: a difference of two sums must not lose its bits to their size)
+        whole[lane] = (float)(x.x >> 16);
+        frac[lane] = parts_to_float(x.x & 0xffff, x.y);
+        weight[lane] = w * a.scale;
+        grown[lane] = bad & ((2u << lane) - 1) ? nan : a.scale * exp2_fast(parts_to_float(x.x, x.y));
+        shrunk[lane] = exp2_fast(parts_to_float(all.x - x.x, all.y - x.y)) * w;
+        if (lane == 0) gamma = bad ? make_float2(nan, nan) : exp2_pair(((long long)all.x << 24) + all.y);
+    }
+    __syncthreads();
+
+    const uint32_t aq = smem_addr(sq), ak = smem_addr(sk), av = smem_addr(sv), aw = smem_addr(sw[0]);
+    // a 16 x 16 tile as the first operand: matrices (rows 0-7, columns 0-7), (8-15, 0-7), (0-7, 8-15), (8-15, 8-15)
+    const int row16 = lane & 15, col16 = (lane >> 4) * 16;
+    // W: a warp has eight columns j of it
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        if (m >= steps || warp > 2 * m + 1) continue;
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < K; k += 2) {
+            uint32_t x[4], y[4], z[4];
+            ldsm(aq + (m * 16 + row16) * ROW + k * 32 + col16, x);
+            ldsm(aq + (m * 16 + row16) * ROW + k * 32 + 32 + col16, y);
+            ldsm(ak + (warp * 8 + (lane & 7)) * ROW + k * 32 + (lane >> 3) * 16, z);
+            mma16(d, x, z[0], z[1]);
+            mma16(d, y, z[2], z[3]);
+        }
+        const int j = warp * 8 + 2 * c0;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int i = m * 16 + r * 8 + r0;
+            const float x = exp2_fast((whole[i] - whole[j]) + (frac[i] - frac[j])) * weight[j] * d[2 * r];
+            const float y = exp2_fast((whole[i] - whole[j + 1]) + (frac[i] - frac[j + 1])) * weight[j + 1] * d[2 * r + 1];
+            const float u = i >= j ? x : 0.f, v = i > j ? y : 0.f;
+            const uint32_t hi = pack2(two(u, v));
+            const int to = i * kWRow + j * 2;
+            *reinterpret_cast<uint32_t*>(sw[0] + to) = hi;
+            *reinterpret_cast<uint32_t*>(sw[1] + to) = pack2(two(u - bf16_lo(hi), v - bf16_hi(hi)));
+        }
+    }
+    // the warp's values, [value row][token] as a first operand
+    uint32_t v[2][4];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+        if (m < steps) ldsm_t(av + (m * 16 + (lane >> 4) * 8 + (lane & 7)) * kVRow + warp * 32 + (lane >> 3 & 1) * 16, v[m]);
+        else v[m][0] = v[m][1] = v[m][2] = v[m][3] = 0;
+    bool odd = false;
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) odd |= (v[m][e] & 0x7f80u) == 0x7f80u || (v[m][e] & 0x7f800000u) == 0x7f800000u;
+    odd = __any_sync(0xffffffffu, odd);
+    int bad[2] = {kT, kT};  // value rows r0 and r0 + 8: the first token whose value is not finite
+    if (__builtin_expect(odd, 0)) {
+        // (cleared, since a weight of zero would not hide it from the tokens before; NaN from that token on)
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = m * 16 + (e >> 1) * 8 + 2 * c0;
+                if ((v[m][e] & 0x7f800000u) == 0x7f800000u) {
+                    v[m][e] &= 0xffffu;
+                    bad[e & 1] = min(bad[e & 1], i + 1);
+                }
+                if ((v[m][e] & 0x7f80u) == 0x7f80u) {
+                    v[m][e] &= 0xffff0000u;
+                    bad[e & 1] = min(bad[e & 1], i);
+                }
+            }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            bad[r] = min(bad[r], __shfl_xor_sync(0xffffffffu, bad[r], 1));
+            bad[r] = min(bad[r], __shfl_xor_sync(0xffffffffu, bad[r], 2));
+            if (c0 == 0) odd_from[warp * 16 + r * 8 + r0] = bad[r];
+        }
+        __syncwarp();
+    }
+    __syncthreads();
+
+    // o: tokens m * 16 + r0 (+ 8), value rows 8 r + 2 c0 and on
+    float o[2][2][4] = {};
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        uint32_t hi[2][2], lo[2][2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                f2 rest;
+                hi[r][p] = split2(s[k][r][p], rest);
+                lo[r][p] = pack2(rest);
+            }
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            if (m >= steps) continue;
+            uint32_t x[4];
+            ldsm(aq + (m * 16 + row16) * ROW + k * 32 + col16, x);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                mma16(o[m][r], x, hi[r][0], hi[r][1]);
+                mma16(o[m][r], x, lo[r][0], lo[r][1]);
+            }
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        if (m >= steps) continue;
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[m][r][e] *= grown[m * 16 + r0 + (e >> 1) * 8];
+#pragma unroll
+        for (int j = 0; j <= m; ++j)
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+                uint32_t x[4];
+                ldsm(aw + z * (kT * kWRow) + (m * 16 + row16) * kWRow + j * 32 + col16, x);
+#pragma unroll
+                for (int r = 0; r < 2; ++r) mma16(o[m][r], x, v[j][r], v[j][2 + r]);
+            }
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int i = m * 16 + r0 + x * 8, p = warp * 16 + r * 8 + 2 * c0;
+                if (i >= n) continue;
+                float y = o[m][r][2 * x], z = o[m][r][2 * x + 1];
+                if (__builtin_expect(odd, 0)) {
+                    const float nan = __uint_as_float(0x7fc00000u);
+                    if (i >= odd_from[p]) y = nan;
+                    if (i >= odd_from[p + 1]) z = nan;
+                }
+                const long to = ((long)(begin + i) * a.H + h) * P + part * 64 + p;
+                if (a.obf) *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + to) = pack2(two(y, z));
+                else *reinterpret_cast<float2*>(static_cast<float*>(a.o) + to) = make_float2(y, z);
+            }
+    }
+
+    // the decayed values in parts, and the state after the row
+    uint32_t vp[2][SP][4];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 d = *reinterpret_cast<const float2*>(&shrunk[m * 16 + (e >> 1) * 8 + 2 * c0]);
+            f2 x = mul2(two(d.x, d.y), two(bf16_lo(v[m][e]), bf16_hi(v[m][e])));
+#pragma unroll
+            for (int z = 0; z < SP - 1; ++z) vp[m][z][e] = split2(x, x);
+            vp[m][SP - 1][e] = pack2(x);
+        }
+    const f2 fx = two(gamma.x, gamma.x), fy = two(gamma.y, gamma.y);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        float d[2][4] = {};
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            if (m >= steps) continue;
+            uint32_t x[4];
+            ldsm_t(ak + (m * 16 + row16) * ROW + k * 32 + col16, x);
+#pragma unroll
+            for (int z = 0; z < SP; ++z) {
+                mma16(d[0], vp[m][z], x[0], x[1]);
+                mma16(d[1], vp[m][z], x[2], x[3]);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            float2 f[2];
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                f[p] = one_by_one(fma2(fx, s[k][r][p], fma2(fy, s[k][r][p], two(d[p][2 * r], d[p][2 * r + 1]))));
+                if (__builtin_expect(odd, 0) && bad[r] < kT) f[p].x = f[p].y = __uint_as_float(0x7fc00000u);
+            }
+            const long i = at + r * 8 * N + k * 16;
+            if (a.sbf) __stcs(reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.state) + i), make_uint2(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y)));
+            else __stcs(reinterpret_cast<float4*>(static_cast<float*>(a.state) + i), make_float4(f[0].x, f[0].y, f[1].x, f[1].y));
+        }
+    }
+}
+
+int prompt_brief(const rssm_linattn_dims* d, const Args& a, bool report, cudaStream_t st) {
+    const int P = d->value_dim, grid = a.batch * a.H * (P / 64);
+    if (d->key_dim == 64) {
+        if (a.sbf) attn::launch_early(brief_kernel<64, 2>, grid, 128, 0, st, a, P, report);
+        else attn::launch_early(brief_kernel<64, 3>, grid, 128, 0, st, a, P, report);
+    } else {
+        if (a.sbf) attn::launch_early(brief_kernel<128, 2>, grid, 128, 0, st, a, P, report);
+        else attn::launch_early(brief_kernel<128, 3>, grid, 128, 0, st, a, P, report);
+    }
+    return launch_status();
+}
+
+}  // namespace linattn
+}  // namespace rssm

@@ -67,19 +67,6 @@ struct Chunk {
     static constexpr int UCONS = CONS + 1 + 2;          // warps that follow the list
 };
 
-// v's next bf16 part and the (exact) rest: v - h by a multiply-add that takes h's halves as they are.
-__device__ __forceinline__ uint32_t split2(f2 v, f2& rest) {
-    const uint32_t h = pack2(v);
-    const float2 f = one_by_one(v);
-    float x, y;
-    asm("{\n\t.reg .b16 l, h, m;\n\tmov.b32 {l, h}, %2;\n\tmov.b16 m, 0xBF80;\n\t"
-        "fma.rn.f32.bf16 %0, l, m, %3;\n\tfma.rn.f32.bf16 %1, h, m, %4;\n\t}"
-        : "=f"(x), "=f"(y)
-        : "r"(h), "f"(f.x), "f"(f.y));
-    rest = two(x, y);
-    return h;
-}
-
 // Wait for phase `parity` of the barrier at shared address `bar`: false once `limit` ns went by, or another warp has
 // set the flag at `stop`; then the flag is set. try_wait sleeps, so a wait costs few instructions; and it is
 // spelled out, since a call's moves and saves at each of the waits would cost more room than the wait.
@@ -572,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (OUT) {
             // Half of the items are dealt, item blockIdx.x and every gridDim.x-th on, and looked up 32 at a time, one a lane;
             // the rest are claimed one by one, since units differ in length (24 rows of 600 to 2500 tokens, all dealt:
-            // twice the time).
+            // twice the time); or 32 at a time where most rows are not this kernel's.
             const unsigned items = (unsigned)c.units * c.blocks;  // (below 2^28)
             auto look_up = [&](unsigned i) {
                 Unit u;
@@ -597,8 +584,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int begin, end;
                 if (row_of(a, b, u.head == 0, begin, end, u.slot) && end - begin > c.brief && s >= 0 && s < segments(c, end - begin)) {
                     const int last = segments(c, end - begin) - 1;
-                    u.tok = begin + segment_begin(end - begin, last + 1, s);
-                    u.n = begin + segment_begin(end - begin, last + 1, s + 1) - u.tok;
+                    u.tok = begin + segment_begin(c, end - begin, last + 1, s);
+                    u.n = begin + segment_begin(c, end - begin, last + 1, s + 1) - u.tok;
                     u.part = s > 0 ? begin / c.seg + s - 1 : last > 0 ? c.kept + begin / c.seg : 0;
                     u.from = s > 0 ? kPart : !a.resume || !a.resume[b] ? kZero : last > 0 ? kPart : kSlot;
                     u.to = s == last ? kSlot : kZero;
@@ -622,15 +609,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             const unsigned dealt = items / 2 / gridDim.x;  // to each CTA
             for (unsigned k0 = 0; k0 < dealt && ok; k0 += 32)
                 take_all(look_up(k0 + lane < dealt ? blockIdx.x + (k0 + lane) * gridDim.x : items));
-            auto claim = [&]() { return __shfl_sync(0xffffffffu, lane == 0 ? dealt * gridDim.x + atomicAdd(c.claims, 1u) : 0u, 0); };
+            const unsigned at_once = c.brief ? 32 : 1;
+            auto claim = [&]() { return __shfl_sync(0xffffffffu, lane == 0 ? dealt * gridDim.x + atomicAdd(c.claims, at_once) : 0u, 0); };
             if (ok) {
                 unsigned first = claim();
-                Unit u = look_up(lane == 0 ? first : items);
+                Unit u = look_up(lane < at_once ? first + lane : items);
                 while (ok) {
                     const unsigned next = claim();
                     take_all(u);
                     if (next >= items) break;
-                    u = look_up(lane == 0 ? next : items);
+                    u = look_up(lane < at_once ? next + lane : items);
                 }
             }
             // the last CTA leaves the counters as they were
@@ -653,9 +641,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (; next < more && ok; next += gridDim.x) {
                         const int s = next / (unsigned)c.blocks;
                         Unit u;
-                        const int from = segment_begin(n, last + 1, s);
+                        const int from = segment_begin(c, n, last + 1, s);
                         u.tok = first + from;
-                        u.n = segment_begin(n, last + 1, s + 1) - from;
+                        u.n = segment_begin(c, n, last + 1, s + 1) - from;
                         u.head = (int)(next - s * c.blocks) * VH;
                         u.slot = 0;
                         u.part = first / c.seg + s;
