@@ -60,7 +60,7 @@ class LinearAttention(_Fixed):
     Buffers: state [num_slots, H, P, N] (state_dtype; or the caller's, e.g. a Mamba2 decoder's),
     o for up to max_tokens tokens and a workspace for as many. Slots are not cleared when they
     are given to another row: prompt() begins from zero unless told to resume. scale may be set
-    between calls."""
+    between calls. Calls may be on any stream, one after another: they share o and the workspace."""
 
     _free = ("scale",)
 
@@ -82,6 +82,9 @@ class LinearAttention(_Fixed):
         self.ws_bytes = B.rssm_linattn_workspace_size(self.dims(max_batch), self.max_tokens)
         # zero-filled: the prompt call keeps its counters here
         self.workspace = torch.zeros(max(self.ws_bytes, 16), device=dev, dtype=torch.uint8)
+        self._all = torch.ones(max(max_batch, 1), device=dev, dtype=torch.uint8)  # every row resumes
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(dev).synchronize()  # calls may be on any stream
         self._prompt, self._step = B.entry("rssm_linattn_prompt"), B.entry("rssm_linattn_step")
         self._addr = (self.state.data_ptr(), self.workspace.data_ptr(), self.dev_err.data_ptr(), self.o.data_ptr())
         self._index = _index(self.state.device)
@@ -182,7 +185,7 @@ class LinearAttention(_Fixed):
             raise ValueError("%d tokens of %d rows: cu_tokens is wanted" % (n, b))
         o, o_ptr = self._out(o, own, n)
         if resume is True:
-            resume = torch.ones(b, device=self.device, dtype=torch.uint8)
+            resume = self._all[:b]
         elif resume is False:
             resume = None
         if resume is not None and (resume.dtype not in (torch.uint8, torch.bool) or resume.shape != (b,) or
