@@ -830,8 +830,8 @@ int rssm_add_rmsnorm(const rssm_norm_dims* dims, const void* x, const void* resi
  * the caller's), and its decode steps go on from the pool. The pages give decode steps only
  * ([M2] 实现拆解: prompts go through the engine's prefill kernels). */
 typedef struct rssm_linattn_dims {
-    int32_t batch;       /* rows in this call (>= 0) */
-    int32_t num_heads;   /* H */
+    int32_t batch;       /* rows in this call (>= 0); batch * H < 2^27 */
+    int32_t num_heads;   /* H <= 8192 */
     int32_t num_k_heads; /* G: H % G == 0 */
     int32_t key_dim;     /* N: 64 or 128 */
     int32_t value_dim;   /* P: 64 or 128 */
@@ -863,7 +863,7 @@ typedef struct rssm_linattn_inputs {
 } rssm_linattn_inputs;
 
 /* Bytes of device workspace rssm_linattn_prompt needs for n_tokens tokens: counters, and states of
- * the parts of long rows (0 for float32 activations). It must be zero-filled before its first use, and
+ * the parts of long rows. It must be zero-filled before its first use, and
  * again after a call that set RSSM_DEVERR_TIMEOUT; every other call leaves its counters at zero. One
  * stream at a time. The size goes by the dims but the batch, n_tokens and the current device's SMs, and
  * does not shrink as n_tokens grows. 0 for dims that rssm_linattn_prompt refuses. */
@@ -879,9 +879,13 @@ size_t rssm_linattn_workspace_size(const rssm_linattn_dims* dims, int32_t n_toke
  *     leaves its slot as it is.
  *   o [n_tokens][H][P] out_dtype.
  * A row whose part of cu_tokens decreases or leaves [0, n_tokens] is skipped and sets
- * RSSM_DEVERR_CURSOR; which rows beside it in such a list are taken is not defined. With bf16 activations a chunk of 64 tokens at a time on the tensor
- * cores: products of bf16 values are exact, sums and states float32, and where a weight, a
- * state or a decayed value enters a product it has 16 bits. An infinity or a NaN in v (k, g, w)
+ * RSSM_DEVERR_CURSOR; which rows beside it in such a list are taken is not defined. A slot >= num_slots
+ * skips its row and sets RSSM_DEVERR_SLOT, a negative one skips it. Rows of one call need slots of their
+ * own, and o may not overlap an input.
+ * bf16 activations go in chunks of tokens on the tensor cores: products of bf16 values are exact, sums and
+ * states float32, and where a weight or a state enters a product it has 16 bits, a decayed value 16 with a bf16
+ * state and 24 with a float32 one. Float32 activations go token by token in float32. A token's decay beyond
+ * exp(+-277) counts as that much. An infinity or a NaN in v (k, g, w)
  * reaches its head's outputs and state of that value row (all value rows) from its token on, as an
  * infinity or a NaN, and no earlier ones; one in q reaches that token's outputs. The order of every
  * sum is fixed by the lengths, n_tokens and the GPU's SM count: repeated calls give identical bits.
@@ -892,7 +896,8 @@ int rssm_linattn_prompt(const rssm_linattn_dims* dims, const rssm_linattn_inputs
                         size_t workspace_bytes, void* o, int32_t* dev_err, rssm_stream_t stream);
 
 /* rssm_linattn_step -- one token for each row, from and into its slot's state: token b is row
- * b's, o [batch][H][P]. */
+ * b's, o [batch][H][P]. A negative slot skips its row, one >= num_slots sets RSSM_DEVERR_SLOT as well; rows
+ * need slots of their own. */
 int rssm_linattn_step(const rssm_linattn_dims* dims, const rssm_linattn_inputs* in, void* state,
                       const int32_t* cache_indices, void* o, int32_t* dev_err,
                       rssm_stream_t stream);

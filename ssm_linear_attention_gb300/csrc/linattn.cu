@@ -4,10 +4,13 @@
 //   S_t = exp(g_t) S_{t-1} + w_t v_t k_t^T,   o_t = scale S_t q_t      (S [P][N] per head)
 //
 // The step reads and writes every state once and is bound by that; a lane has pieces of 16 bytes
-// of one value row, eight lanes a row, so that a sum over N takes three shuffles.
+// of one value row, eight lanes a row, so that a sum over N takes three shuffles. 256 rows of 32 x 128 x 128 in float32:
+// 157 us, 6.8 TB/s; 512 rows of 128 x 64 x 128 in bf16 320 us, 6.7 TB/s (a plain copy: 6.78).
 //
 // The recurrence over a prompt keeps 64 value rows of a head in the registers of a CTA and takes one token
-// after another: float32 activations, cut into segments as the chunks are.
+// after another: float32 activations, cut into segments as the chunks are. Its time is a token's: smem reads, some 100
+// paired multiply-adds and a sum over eight lanes, one after another, so rows are cut down to 48 tokens a CTA where
+// the GPU is not full (3 rows of 700 tokens, 8 heads of 64: 41 us; parts of 64 tokens 50, of 32 40, whole rows 127).
 #include "linattn.cuh"
 
 namespace rssm {

@@ -22,9 +22,13 @@
 // it took half of the issue slots):
 //   0-15 state, decayed values and output, 16, 17, 20, 21 weights, 18 products, 19 loads (TMA) and the list, 22, 23 decays.
 //   (Warp w issues from the SM's part w % 4, and the weights' lanes bind them to two of the parts.)
-// What they issue (some 1600 cycles a chunk of 128 x 128) comes near what the chunk's bytes take, so float32 arithmetic is
-// in pairs (f32x2); and the roles' loops are kept short, since what streams through the instruction cache
-// instead of staying in it waits for it (waits inline and loops unrolled, 133 KB of code: 9000 cycles a chunk).
+// A chunk of 128 x 128 takes some 4400 cycles (24 rows of 600 to 2500 tokens, 32 heads: 425 us, 2.4 TB/s; their bytes at a
+// copy's rate: 151 us): what bounds it is the state warps' chain (the state's update ~540 cycles, decayed values ~1480, the
+// state's parts ~480, output ~1800, most of it waits for the tensor and shared memories) beside 10000 issued instructions
+// (2500 cycles). So float32 arithmetic is in pairs (f32x2); and the roles' loops are kept short, since what streams through
+// the instruction cache instead of staying in it waits for it (waits inline and loops unrolled, 133 KB of code: 9000
+// cycles a chunk). Separate warps for the output or the decayed values were slower (465 to 626 us): the same
+// registers have to hold state, values and output at 768 threads.
 #include "linattn.cuh"
 #include "umma.cuh"
 #include "warps.cuh"
@@ -559,7 +563,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (OUT) {
             // Half of the items are dealt, item blockIdx.x and every gridDim.x-th on, and looked up 32 at a time, one a lane;
             // the rest are claimed one by one, since units differ in length (24 rows of 600 to 2500 tokens, all dealt:
-            // twice the time); or 32 at a time where most rows are not this kernel's.
+            // twice the time); or in some four claims where most rows are not this kernel's (300 rows of 24 tokens, none of them
+            // its own: 77 us one by one, 15 so; 32 at a time held up batches of 47 rows).
             const unsigned items = (unsigned)c.units * c.blocks;  // (below 2^28)
             auto look_up = [&](unsigned i) {
                 Unit u;
@@ -609,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const unsigned dealt = items / 2 / gridDim.x;  // to each CTA
             for (unsigned k0 = 0; k0 < dealt && ok; k0 += 32)
                 take_all(look_up(k0 + lane < dealt ? blockIdx.x + (k0 + lane) * gridDim.x : items));
-            const unsigned at_once = c.brief ? 32 : 1;
+            const unsigned at_once = c.brief ? max(1u, min(32u, items / (8 * gridDim.x))) : 1;
             auto claim = [&]() { return __shfl_sync(0xffffffffu, lane == 0 ? dealt * gridDim.x + atomicAdd(c.claims, at_once) : 0u, 0); };
             if (ok) {
                 unsigned first = claim();
