@@ -63,3 +63,59 @@ def test_a_value_that_is_not_finite_stays_behind_its_token(token, bad):
         oo[token:50, 2, p] = o[token:50, 2, p]
         ss[c.slots[0], 2, p] = s[c.slots[0], 2, p]
         assert torch.equal(oo, o) and torch.equal(ss, s)
+
+
+@pytest.mark.parametrize("each", [1, 24, 32, 33])
+def test_equal_rows_without_a_list(each):
+    import ssm_linear_attention_gb300 as ssm
+    c = Case([each] * 5, resume=0b10110)
+    want, state = (x.clone() for x in c.run(ssm))
+    layer = c.layer(ssm)
+    o = layer.prompt(c.q, c.k, c.v, c.g, c.slots, w=c.w, resume=c.resume)
+    torch.cuda.synchronize()
+    c.check(o, layer.state)
+    assert torch.equal(o, want) and torch.equal(layer.state, state)
+
+
+@pytest.mark.parametrize("lens", [[5, 7, 3], [5, 70, 3, 2, 4, 1, 8]])
+def test_padding_and_bad_rows(lens):
+    import ssm_linear_attention_gb300 as ssm
+    c = Case(lens, resume=0)
+    want, state = (x.clone() for x in c.run(ssm))
+    layer = c.layer(ssm)
+    slots = c.slots.clone()
+    slots[0], slots[2] = -1, len(lens) + 2
+    layer.o.fill_(7)
+    o = layer.prompt(c.q, c.k, c.v, c.g, slots, cu_tokens=c.cu, w=c.w)
+    torch.cuda.synchronize()
+    assert int(layer.dev_err[0]) == ssm.RSSM_DEVERR_SLOT
+    left = torch.zeros(sum(lens), dtype=torch.bool, device="cuda")
+    for b in (0, 2):
+        left[c.starts[b]:c.starts[b + 1]] = True
+    assert bool((o[left] == 7).all()) and torch.equal(o[~left], want[~left])
+    kept = c.slots[[0, 2]].long()
+    assert torch.equal(layer.state[kept], c.state0[kept])
+    others = [b for b in range(len(lens)) if b not in (0, 2)]
+    assert torch.equal(layer.state[c.slots[others].long()], state[c.slots[others].long()])
+
+
+def test_a_captured_call_follows_its_rows_lengths():
+    import ssm_linear_attention_gb300 as ssm
+    cases = [Case(x, resume=0b1010) for x in ([32, 32, 32, 32], [1, 120, 0, 7], [100, 2, 25, 1])]
+    assert len({sum(c.lens) for c in cases}) == 1
+    first = cases[0]
+    q, k, v, g, w = (x.clone() for x in (first.q.contiguous(), first.k.contiguous(), first.v.contiguous(), first.g, first.w))
+    layer, cu, slots = first.layer(ssm), first.cu.clone(), first.slots.clone()
+    layer.prompt(q, k, v, g, slots, cu_tokens=cu, w=w, resume=first.resume)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o = layer.prompt(q, k, v, g, slots, cu_tokens=cu, w=w, resume=first.resume)
+    for _ in range(2):
+        for c in cases:
+            for to, new in ((q, c.q), (k, c.k), (v, c.v), (g, c.g), (w, c.w), (cu, c.cu), (slots, c.slots), (layer.state, c.state0)):
+                to.copy_(new)
+            graph.replay()
+            torch.cuda.synchronize()
+            c.check(o, layer.state)
+    assert int(layer.dev_err.sum()) == 0
