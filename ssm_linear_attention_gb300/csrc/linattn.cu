@@ -309,6 +309,7 @@ static int launch_recurrence(const ChunkArgs& c, int N, int P, bool report, cuda
 __global__ void __launch_bounds__(256) carry_kernel(const ChunkArgs c, long all, int per_head) {
     attn::wait_for_stream();
     const Args& a = c.a;
+    if (!__syncthreads_or(sees_cut_rows(c, threadIdx.x, 256))) return;
     const long e = ((long)blockIdx.x * 256 + threadIdx.x) * 4;
     const int lane = threadIdx.x & 31;
     const int h = (int)(min(e, all - 4) / per_head);

@@ -184,6 +184,16 @@ __device__ __forceinline__ int segment_begin(const ChunkArgs& c, int n, int coun
     return min(n, (s * each + min(s, units - each * count)) * c.unit);
 }
 
+// Whether one of the rows that thread `t` of `threads` looks at (all of its loads in flight) is long enough to be cut.
+__device__ __forceinline__ bool sees_cut_rows(const ChunkArgs& c, int t, int threads) {
+    const int32_t* const cu = c.a.cu;
+    if (!cu) return c.a.each >= 2 * c.seg;
+    bool any = false;
+#pragma unroll 8
+    for (int b = t; b < c.a.batch; b += threads) any |= (int64_t)cu[b + 1] - cu[b] >= 2 * c.seg;
+    return any;
+}
+
 // Rows of few tokens, bf16 activations: where they are short on the average, those of at most 32 have a kernel of their own
 // (linattn_brief.cu).
 constexpr int kBrief = 32;

@@ -635,7 +635,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
             // the segments before the last one of each long row
             unsigned next = blockIdx.x;  // this CTA's next item, counted from the row's first
-            for (int b0 = 0; b0 < a.batch && ok; b0 += 32) {
+            const bool some = __any_sync(0xffffffffu, sees_cut_rows(c, lane, 32));
+            for (int b0 = 0; some && b0 < a.batch && ok; b0 += 32) {
                 int begin = 0, end = 0, slot = 0, count = 0;
                 if (b0 + lane < a.batch && row_of(a, b0 + lane, false, begin, end, slot)) count = segments(c, end - begin) - 1;
                 for (uint32_t m = __ballot_sync(0xffffffffu, count > 0); m && ok; m &= m - 1) {
