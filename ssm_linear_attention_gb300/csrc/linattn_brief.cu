@@ -6,7 +6,7 @@
 // What it has to move is the states, each read and written once, so a CTA is small (64 value rows of a head, in registers)
 // and several on an SM hide each other's loads, products and stores; a tile of 128 x 128 of the tensor memory would be a
 // state alone, and its way in and out the time (672 us for 300 rows of 24 tokens, 32 heads of 128 x 128 float32, token by
-// token 495; here 257 of a call's 284: 79 % of a copy's rate). The products are 16 x 8 x 16 ones between registers: a warp has 16 value
+// token 495; here 257 of a call's 280: 79 % of a copy's rate). The products are 16 x 8 x 16 ones between registers: a warp has 16 value
 // rows of the state as the accumulators of 16 x 8 tiles, lane 4 r + c rows r and r + 8 and of each 16 keys the four from
 // 4 c on (one access of 16 bytes). That order of the keys is the products' own, so q and k are stored in shared memory
 // with their pairs in it, and the accumulators are the second operand of o = q S_0^T as they are, in two bf16 parts.
